@@ -32,7 +32,9 @@ EXPORTED = ("csa_workspace_size", "csa_quantize_keys", "csa_decode_step",
             "csa_status_string", "csa_workspace_layout",
             "csa_profile_enable", "csa_profile_read",
             "csa_dense_decode_static", "csa_decode_step_device",
-            "csa_quantize_keys8", "csa_decode_step_refined")
+            "csa_quantize_keys8", "csa_decode_step_refined",
+            "csa_rope_turns", "csa_qk_norm_rope", "csa_kv4_append",
+            "csa_kv4_unpack", "csa_kv4_workspace_size", "csa_kv4_decode")
 # size of the fixed scratch array behind csa_dense_decode_static
 DENSE_STATIC_SCRATCH_BYTES = 16 << 20
 STATS_FIELDS = 10
@@ -93,6 +95,23 @@ class csa_phase_times(ctypes.Structure):
                 ("launches", ctypes.c_int64)]
 
 
+class csa_strides(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("t", ctypes.c_int64),
+                ("h", ctypes.c_int64)]
+
+
+class csa_norm_rope(ctypes.Structure):
+    _fields_ = [("wq", ctypes.c_void_p), ("wk", ctypes.c_void_p),
+                ("norm_eps", ctypes.c_float), ("rot_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("turns", ctypes.c_void_p)]
+
+
+class csa_kv4(ctypes.Structure):
+    _fields_ = [("K4", ctypes.c_void_p), ("bounds", ctypes.c_void_p),
+                ("V4", ctypes.c_void_p), ("vscale", ctypes.c_void_p),
+                ("Kt", ctypes.c_void_p), ("Vt", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -140,6 +159,26 @@ def load_library(path: str = LIB_PATH):
     lib.csa_dense_decode_static.argtypes = [P(csa_shape), vp, vp, vp,
                                             P(ctypes.c_int64), vp, vp]
     lib.csa_dense_decode_static.restype = ctypes.c_int
+    lib.csa_rope_turns.argtypes = [P(ctypes.c_double), ctypes.c_int,
+                                   P(ctypes.c_uint64)]
+    lib.csa_rope_turns.restype = ctypes.c_int
+    lib.csa_qk_norm_rope.argtypes = [P(csa_shape), ctypes.c_int,
+                                     P(csa_norm_rope), vp, P(csa_strides), vp,
+                                     P(csa_strides), vp, P(csa_strides), vp,
+                                     vp, vp, vp, vp, ctypes.c_int, vp, vp]
+    lib.csa_qk_norm_rope.restype = ctypes.c_int
+    lib.csa_kv4_append.argtypes = [P(csa_shape), P(csa_kv4), ctypes.c_int, vp,
+                                   P(csa_strides), vp, P(csa_strides), vp, vp,
+                                   vp, vp]
+    lib.csa_kv4_append.restype = ctypes.c_int
+    lib.csa_kv4_unpack.argtypes = [P(csa_shape), P(csa_kv4), ctypes.c_int64,
+                                   vp, vp, vp, vp, vp, vp]
+    lib.csa_kv4_unpack.restype = ctypes.c_int
+    lib.csa_kv4_workspace_size.argtypes = [P(csa_shape), ctypes.c_int]
+    lib.csa_kv4_workspace_size.restype = sz
+    lib.csa_kv4_decode.argtypes = [P(csa_shape), P(csa_kv4), ctypes.c_int, vp,
+                                   P(csa_strides), vp, vp, vp, vp, vp, sz, vp]
+    lib.csa_kv4_decode.restype = ctypes.c_int
     lib.csa_check.argtypes = [vp, vp]
     lib.csa_check.restype = ctypes.c_int
     lib.csa_workspace_layout.argtypes = [P(csa_shape), P(csa_params),
@@ -308,6 +347,69 @@ def csa_dense_decode_static(shape, q, K, V, lens, o, stream=None) -> int:
     return load_library().csa_dense_decode_static(
         ctypes.byref(shape), _ptr(q), _ptr(K), _ptr(V), _i64(lens), _ptr(o),
         _stream(stream))
+
+
+def _strides(t) -> Optional[csa_strides]:
+    """The (b, t, h) element strides of a [B][T][heads][d] tensor."""
+    if t is None or isinstance(t, csa_strides):
+        return t
+    st = t.stride()
+    return csa_strides(st[0], st[1], st[2])
+
+
+def _ref(s):
+    return None if s is None else ctypes.byref(s)
+
+
+def csa_rope_turns(inv_freq) -> list:
+    """The table csa_qk_norm_rope reads (host list of ints below 2^64) for
+    the pairs' angles per position, in radians."""
+    n = len(inv_freq)
+    out = (ctypes.c_uint64 * n)()
+    check(load_library().csa_rope_turns(
+        (ctypes.c_double * n)(*[float(f) for f in inv_freq]), n, out),
+        "csa_rope_turns")
+    return list(out)
+
+
+def csa_qk_norm_rope(shape, T, params, q, qs, k, ks, v, vs, lens_dev, n_new,
+                     q_out, K, V, to_cache, status, stream=None) -> int:
+    """params: csa_norm_rope; qs, ks, vs: csa_strides or the strided
+    tensors; lens_dev, n_new: device int64 [B] (n_new None: T each)."""
+    return load_library().csa_qk_norm_rope(
+        ctypes.byref(shape), int(T), ctypes.byref(params), _ptr(q),
+        _ref(_strides(qs)), _ptr(k), _ref(_strides(ks)), _ptr(v),
+        _ref(_strides(vs)), _ptr(lens_dev), _ptr(n_new), _ptr(q_out),
+        _ptr(K), _ptr(V), int(to_cache), _ptr(status), _stream(stream))
+
+
+def csa_kv4_append(shape, cache, T, k, ks, v, vs, lens_dev, n_new, status,
+                   stream=None) -> int:
+    """cache: csa_kv4; the other arguments as csa_qk_norm_rope."""
+    return load_library().csa_kv4_append(
+        ctypes.byref(shape), ctypes.byref(cache), int(T), _ptr(k),
+        _ref(_strides(ks)), _ptr(v), _ref(_strides(vs)), _ptr(lens_dev),
+        _ptr(n_new), _ptr(status), _stream(stream))
+
+
+def csa_kv4_unpack(shape, cache, rows, first, lens_dev, K, V, status,
+                   stream=None) -> int:
+    return load_library().csa_kv4_unpack(
+        ctypes.byref(shape), ctypes.byref(cache), int(rows), _ptr(first),
+        _ptr(lens_dev), _ptr(K), _ptr(V), _ptr(status), _stream(stream))
+
+
+def csa_kv4_workspace_size(shape: csa_shape, T: int = 1) -> int:
+    return int(load_library().csa_kv4_workspace_size(ctypes.byref(shape),
+                                                     int(T)))
+
+
+def csa_kv4_decode(shape, cache, T, q, qs, lens_dev, n_q, o, lse, workspace,
+                   workspace_bytes, stream=None) -> int:
+    return load_library().csa_kv4_decode(
+        ctypes.byref(shape), ctypes.byref(cache), int(T), _ptr(q),
+        _ref(_strides(qs)), _ptr(lens_dev), _ptr(n_q), _ptr(o), _ptr(lse),
+        _ptr(workspace), int(workspace_bytes), _stream(stream))
 
 
 def csa_profile_enable(on: bool) -> int:
@@ -487,4 +589,261 @@ class DenseDecode:
         check_step_inputs(self.shape, q, K, V, None, lens)
         check(csa_dense_decode(self.shape, q, K, V, lens, self.o, self.ws,
                                self.ws_bytes, stream), "csa_dense_decode")
+        return self.o
+
+
+# ------------------------------------- rows before the cache, 4-bit cache
+
+def _device_index(t) -> int:
+    """Index of the GPU a tensor lies on (a host check; -1: not on one)."""
+    if not getattr(t, "is_cuda", False):
+        return -1
+    i = t.get_device() if hasattr(t, "get_device") else 0
+    return i
+
+
+def _same_device(want: int, **tensors) -> None:
+    """Refuse tensors that do not lie on GPU ``want`` (None ones pass)."""
+    for name, t in tensors.items():
+        if t is not None and _device_index(t) != want:
+            raise ValueError(f"{name}: a tensor on CUDA device {want} is "
+                             "required")
+
+
+def _current(want: int) -> None:
+    """The library launches on the current device: refuse another one."""
+    import torch
+    have = torch.cuda.current_device()
+    if have != want:
+        raise ValueError(f"the buffers lie on CUDA device {want}, the "
+                         f"current device is {have}")
+
+
+def _element_type(t, name: str, shape: csa_shape) -> None:
+    """Refuse a tensor of another element type than the shape's."""
+    if str(t.dtype) != ("torch.float32" if shape.dtype == CSA_F32
+                        else "torch.bfloat16"):
+        raise ValueError(f"{name}: {t.dtype}, the shape's element type is "
+                         "required")
+
+
+def _rows(t, name: str, shape: csa_shape, heads: int, T=None) -> int:
+    """Check a strided [B][T][heads][d] operand of the shape's type; its T."""
+    sz = tuple(t.shape)
+    if len(sz) != 4 or sz[0] != shape.B or sz[2] != heads or \
+            sz[3] != shape.d or sz[1] < 1 or (T is not None and sz[1] != T):
+        want = f"[{shape.B}][{'T' if T is None else T}][{heads}][{shape.d}]"
+        raise ValueError(f"{name}: shape {list(sz)}, {want} is required")
+    st = t.stride()
+    esz = 4 if shape.dtype == CSA_F32 else 2
+    _element_type(t, name, shape)
+    if st[3] != 1 or t.data_ptr() % 16 or any(
+            n > 1 and s * esz % 16 for n, s in zip(sz, st[:3])):
+        raise ValueError(f"{name}: channels must be contiguous and rows "
+                         "start at multiples of 16 bytes")
+    return sz[1]
+
+
+def _counts(t, name: str, B: int) -> None:
+    if str(t.dtype) != "torch.int64" or tuple(t.shape) != (B,) or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous int64 tensor [{B}] is "
+                         "required")
+
+
+class QKNormRope:
+    """Per-head norms of queries and keys with the position rotation
+    (csa_qk_norm_rope), for one shape and set of weights.
+
+    wq, wk: norm weights [d] of the shape's type (None: no norm of that
+    side); inv_freq: the rotated pairs' angles per position in radians (2 x
+    their number = the rotated channels, a multiple of 8; None: no
+    rotation); interleaved: pair i is channels (2i, 2i + 1) instead of (i,
+    i + rot_dim / 2).  ``status`` is the device word csa_check reads."""
+
+    def __init__(self, shape: csa_shape, device, wq=None, wk=None,
+                 norm_eps: float = 1e-6, inv_freq=None,
+                 interleaved: bool = False):
+        import torch
+        self.shape = shape
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self.device = _device_index(self.status)
+        table = [] if inv_freq is None else csa_rope_turns(inv_freq)
+        if len(table) * 2 > shape.d or len(table) % 4:
+            raise ValueError(f"inv_freq: {len(table)} pairs; a multiple of 4 "
+                             f"up to {shape.d // 2} is required")
+        self.turns = torch.tensor(
+            [u - (1 << 64) if u >> 63 else u for u in table],
+            dtype=torch.int64, device=device) if table else None
+        _same_device(self.device, wq=wq, wk=wk)
+        for name, w in (("wq", wq), ("wk", wk)):
+            if w is not None:
+                _require(w, name, shape.d * w.element_size())
+                _element_type(w, name, shape)
+                if tuple(w.shape) != (shape.d,) or w.data_ptr() % 16:
+                    raise ValueError(f"{name}: an aligned tensor "
+                                     f"[{shape.d}] is required")
+        self.weights = (wq, wk)
+        self.params = csa_norm_rope(
+            _ptr(wq), _ptr(wk), float(norm_eps), 2 * len(table),
+            1 if interleaved else 0, _ptr(self.turns))
+
+    def __call__(self, q, k, v, K, V, lens_dev, n_new=None,
+                 to_cache: bool = True, q_out=None, stream=None):
+        """q [B][T][Hq][d], k and v [B][T][Hkv][d] (views with any strides
+        of whole 16 bytes; v None: V is left alone); K, V: the cache
+        [B][Hkv][n_max][d], or with to_cache=False rows [B][T][Hkv][d].
+        lens_dev: device int64 [B], the new tokens counted already; n_new:
+        device int64 [B] (None: T each).  Returns q_out [B][T][Hq][d] (made
+        when not given)."""
+        import torch
+        s = self.shape
+        T = _rows(q, "q", s, s.Hq)
+        _rows(k, "k", s, s.Hkv, T)
+        if v is not None:
+            _rows(v, "v", s, s.Hkv, T)
+        elif V is not None:
+            raise ValueError("V: given without v")
+        _counts(lens_dev, "lens_dev", s.B)
+        if n_new is not None:
+            _counts(n_new, "n_new", s.B)
+        rows = s.B * s.Hkv * (s.n_max if to_cache else T) * s.d
+        for name, t in (("K", K), ("V", V)):
+            if t is not None:
+                _element_type(t, name, s)
+                _require(t, name, rows * t.element_size())
+        if v is not None and V is None:
+            raise ValueError("V: missing")
+        if q_out is None:
+            q_out = torch.empty((s.B, T, s.Hq, s.d), dtype=q.dtype,
+                                device=q.device)
+        else:
+            _rows(q_out, "q_out", s, s.Hq, T)
+            _require(q_out, "q_out", 0)
+        _same_device(self.device, q=q, k=k, v=v, K=K, V=V, lens_dev=lens_dev,
+                     n_new=n_new, q_out=q_out)
+        _current(self.device)
+        check(csa_qk_norm_rope(s, T, self.params, q, q, k, k, v, v, lens_dev,
+                               n_new, q_out, K, V, 1 if to_cache else 0,
+                               self.status, stream), "csa_qk_norm_rope")
+        return q_out
+
+
+class KV4Cache:
+    """Device buffers of a K/V cache held in 4 bits (csa_kv4), for one
+    shape: K4, bounds, V4, vscale of the whole blocks of 64 tokens, Kt, Vt
+    the rows of the incomplete last one.  buffers: those six tensors, in
+    that order, instead of new ones.  ``status`` is the device word
+    csa_check reads after append or unpack."""
+
+    def __init__(self, shape: csa_shape, device, buffers=None):
+        import torch
+        self.shape = shape
+        if csa_kv4_workspace_size(shape, 1) == 0:
+            raise CsaError(2, "KV4Cache")
+        B, H, d = shape.B, shape.Hkv, shape.d
+        nblk = (shape.n_max + BLOCK - 1) // BLOCK
+        el = torch.float32 if shape.dtype == CSA_F32 else torch.bfloat16
+        layout = (("K4", (B, H, nblk * BLOCK, d // 2), torch.uint8),
+                  ("bounds", (B, H, nblk, 2, d), torch.float32),
+                  ("V4", (B, H, nblk, d, BLOCK // 2), torch.uint8),
+                  ("vscale", (B, H, nblk * BLOCK, 2), torch.float32),
+                  ("Kt", (B, H, BLOCK, d), el), ("Vt", (B, H, BLOCK, d), el))
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self.device = _device_index(self.status)
+        if buffers is None:
+            buffers = [torch.zeros(size, dtype=dt, device=device)
+                       for _, size, dt in layout]
+        if len(buffers) != len(layout):
+            raise ValueError("buffers: K4, bounds, V4, vscale, Kt and Vt "
+                             "are required")
+        for (name, size, dt), t in zip(layout, buffers):
+            n = 1
+            for x in size:
+                n *= x
+            if t.dtype != dt:
+                raise ValueError(f"{name}: {dt} is required")
+            _require(t, name, n * t.element_size())
+            _same_device(self.device, **{name: t})
+            if t.data_ptr() % 16:
+                raise ValueError(f"{name}: must start at a multiple of 16 "
+                                 "bytes")
+            setattr(self, name, t)
+        self.desc = csa_kv4(*[t.data_ptr() for t in buffers])
+
+    def append(self, k, v, lens_dev, n_new=None, stream=None) -> None:
+        """Append rows k, v [B][T][Hkv][d] (views with any strides of whole
+        16 bytes): n_new[b] <= T of sequence b (None: T each), which
+        lens_dev counts already (device int64 [B])."""
+        s = self.shape
+        T = _rows(k, "k", s, s.Hkv)
+        _rows(v, "v", s, s.Hkv, T)
+        _counts(lens_dev, "lens_dev", s.B)
+        if n_new is not None:
+            _counts(n_new, "n_new", s.B)
+        _same_device(self.device, k=k, v=v, lens_dev=lens_dev, n_new=n_new)
+        _current(self.device)
+        check(csa_kv4_append(s, self.desc, T, k, k, v, v, lens_dev, n_new,
+                             self.status, stream), "csa_kv4_append")
+
+    def unpack(self, K, V, lens_dev, first=None, stream=None):
+        """Read positions first[b] + i (None: from 0) below lens_dev[b] back
+        into row i of K, V (contiguous [B][Hkv][rows][d]); other rows are
+        left as they are.  Returns (K, V)."""
+        s = self.shape
+        sz = tuple(K.shape)
+        if len(sz) != 4 or sz[0] != s.B or sz[1] != s.Hkv or sz[2] < 1 or \
+                sz[3] != s.d or tuple(V.shape) != sz:
+            raise ValueError(f"K, V: [{s.B}][{s.Hkv}][rows][{s.d}] is "
+                             "required")
+        for name, t in (("K", K), ("V", V)):
+            _element_type(t, name, s)
+            _require(t, name, 0)
+        _counts(lens_dev, "lens_dev", s.B)
+        if first is not None:
+            _counts(first, "first", s.B)
+        _same_device(self.device, K=K, V=V, lens_dev=lens_dev, first=first)
+        _current(self.device)
+        check(csa_kv4_unpack(s, self.desc, sz[2], first, lens_dev, K, V,
+                             self.status, stream), "csa_kv4_unpack")
+        return K, V
+
+
+class KV4Decode:
+    """Owns the workspace and outputs of csa_kv4_decode for one shape and up
+    to T query tokens per sequence: o [B][T][Hq][d] (float32) and, with
+    with_lse, lse [B][T][Hq].  One object serves one call at a time."""
+
+    def __init__(self, shape: csa_shape, device, T: int = 1,
+                 with_lse: bool = False):
+        import torch
+        self.shape, self.T = shape, int(T)
+        self.ws_bytes = csa_kv4_workspace_size(shape, self.T)
+        if self.ws_bytes == 0:
+            raise CsaError(2, "csa_kv4_workspace_size")
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+        self.device = _device_index(self.ws)
+        self.o = torch.zeros((shape.B, self.T, shape.Hq, shape.d),
+                             dtype=torch.float32, device=device)
+        self.lse = (torch.zeros((shape.B, self.T, shape.Hq),
+                                dtype=torch.float32, device=device)
+                    if with_lse else None)
+
+    def __call__(self, q, cache: KV4Cache, lens_dev, n_q=None, stream=None):
+        """q [B][T][Hq][d] (a view with strides of whole 16 bytes); lens_dev
+        and n_q: device int64 [B] (n_q None: T each).  Returns o."""
+        s = self.shape
+        c = cache.shape
+        if (c.B, c.Hkv, c.d, c.n_max, c.dtype) != (s.B, s.Hkv, s.d, s.n_max,
+                                                   s.dtype):
+            raise ValueError("cache: made for another shape")
+        _rows(q, "q", s, s.Hq, self.T)
+        _counts(lens_dev, "lens_dev", s.B)
+        if n_q is not None:
+            _counts(n_q, "n_q", s.B)
+        _same_device(self.device, q=q, cache=cache.K4, lens_dev=lens_dev,
+                     n_q=n_q)
+        _current(self.device)
+        check(csa_kv4_decode(s, cache.desc, self.T, q, q, lens_dev, n_q,
+                             self.o, self.lse, self.ws, self.ws_bytes,
+                             stream), "csa_kv4_decode")
         return self.o

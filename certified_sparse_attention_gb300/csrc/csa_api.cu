@@ -26,6 +26,8 @@ int grid_J(int64_t P, int r) {
   return j;
 }
 
+}  // namespace
+
 // Head counts are capped so that no workspace size can overflow size_t
 // (the largest region, B Hkv (J+1) |pool| 8 bytes, stays below 2^60 with
 // B <= 128, Hkv <= 1024, J + 1 <= 256 and n_max <= 2^31).
@@ -41,6 +43,9 @@ csa_status shape_supported(const csa_shape* s) {
   if (s->B > kMaxB) return CSA_ERR_UNSUPPORTED;
   return CSA_OK;
 }
+
+namespace {
+
 bool params_ok(const csa_params* p) {
   return p && p->eps > 0.f && std::isfinite(p->eps) && p->delta > 0.f && p->delta < 1.f && p->r >= 1 &&
          p->r <= 4 && p->measure >= 0 && p->measure <= 3 && p->J_override >= -1 && p->J_override <= kMaxJ &&
@@ -133,6 +138,8 @@ bool make_layout(const csa_shape* s, const csa_params* p, Layout& L) {
   return true;
 }
 
+}  // namespace
+
 int sm_count() {
   static int cached[64] = {0};
   int dev = 0;
@@ -144,6 +151,8 @@ int sm_count() {
   }
   return cached[dev];
 }
+
+namespace {
 
 csa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? CSA_OK : CSA_ERR_CUDA; }
 

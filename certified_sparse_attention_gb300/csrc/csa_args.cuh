@@ -184,6 +184,18 @@ inline void launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 }
 void add_launches(int k);   // adds to the launch count csa_profile_read reports
 
+bool shape_ok(const csa_shape* s);              // sizes and type are valid
+csa_status shape_supported(const csa_shape* s); // ... and built: d, G, B
+int sm_count();                                 // SMs of the current device
+
+inline bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+// strides of a [B][T][heads][d] operand: multiples of `unit` elements (16
+// bytes); the stride of an axis of length one is never used
+inline bool strides_ok(const csa_strides* s, int64_t unit, int B, int T, int heads) {
+  return s && (B == 1 || s->b % unit == 0) && (T == 1 || s->t % unit == 0) && (heads == 1 || s->h % unit == 0);
+}
+bool kv4_cache_ok(const csa_kv4* c);            // arrays present and aligned
+
 // Unique id of the calling thread's current CUDA context (the driver's
 // cuCtxGetId, reached through the runtime's driver entry points, so that the
 // library does not link libcuda).  Returns false when no context is current.

@@ -1,0 +1,272 @@
+// Per-head norms of queries and keys with the position rotation, and the
+// new rows' way into the cache, in one pass (csa_qk_norm_rope).
+//
+// For a row x of d channels at position p:
+//   x <- x (mean x_c^2 + eps)^(-1/2) w_c,
+//   (x_a, x_b) <- (x_a cos - x_b sin, x_a sin + x_b cos) for each pair,
+// float32 throughout, one rounding at the end.  The angle of pair i is
+// p f_i.  The table holds f_i / (2 pi) as a 64-bit fraction of a turn, so
+// p times it modulo 2^64 is the angle's exact fraction of a turn at any
+// position, and one sincospif on it (|argument| <= 1) has no range
+// reduction to lose digits in.
+//
+// Bound by memory: every row is read once and written once.  A row is held
+// by d / 8 lanes as two vectors of four channels each.  With split pairs
+// (i, i + rot / 2) the two vectors of a lane are partners, so the rotation
+// needs no exchange between lanes; with adjacent pairs the partners are in
+// one vector.  The lanes' eight sines and cosines serve every head of the
+// token that the lanes process.
+#include <cmath>
+
+#include "csa_args.cuh"
+
+namespace csa {
+
+struct RopeArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  csa_strides qs, ks, vs;
+  const int64_t* len;
+  const int64_t* n_new;
+  const void* wq;
+  const void* wk;
+  const uint64_t* turns;
+  void* q_out;
+  void* K;
+  void* V;
+  unsigned* status;
+  int64_t n_max;
+  int B, T, Hq, Hkv;
+  int rot, interleaved, to_cache;
+  int heads_per;      // heads of a token that one group of lanes processes
+  int nchunk;         // groups per token
+  float eps;
+};
+
+template <typename E> struct Vec4;
+template <> struct Vec4<float> {
+  typedef float4 Raw;
+  static __device__ __forceinline__ float4 widen(Raw r) { return r; }
+  static __device__ __forceinline__ Raw narrow(float4 f) { return f; }
+};
+template <> struct Vec4<__nv_bfloat16> {
+  typedef uint2 Raw;
+  static __device__ __forceinline__ float4 widen(Raw u) {
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ Raw narrow(float4 f) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(f.x, f.y), b = __floats2bfloat162_rn(f.z, f.w);
+    return make_uint2(*reinterpret_cast<const unsigned*>(&a), *reinterpret_cast<const unsigned*>(&b));
+  }
+};
+
+// (a, b) <- the rotated pair
+__device__ __forceinline__ void turn_pair(float& a, float& b, float cs, float sn) {
+  const float x = a * cs - b * sn;
+  b = a * sn + b * cs;
+  a = x;
+}
+
+// Sequence b's first new position and number of new tokens; false (nothing
+// to do, flagged by the caller) when they are out of range.
+__device__ __forceinline__ bool new_tokens(const int64_t* len, const int64_t* n_new, int b, int T, int64_t cap,
+                                           int64_t& start, int64_t& m) {
+  const int64_t n = len[b];
+  m = n_new ? n_new[b] : (int64_t)T;
+  start = n - m;
+  return m >= 0 && m <= T && start >= 0 && n <= cap;
+}
+
+constexpr int kRopeThreads = 128;
+constexpr int kRopeBatch = 4;     // rows of a group of lanes in flight
+
+template <int D, typename E>
+__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeArgs a) {
+  pdl_entry();
+  constexpr int LPR = D / 8;                 // lanes per row
+  constexpr int RPB = kRopeThreads / LPR;    // groups of lanes per CTA
+  typedef typename Vec4<E>::Raw Raw;
+  const int j = threadIdx.x % LPR;
+  const int64_t cap = a.to_cache ? a.n_max : INT64_MAX;
+  if (a.status && blockIdx.x == 0 && threadIdx.x < 32) {
+    bool bad = false;
+    for (int b = threadIdx.x; b < a.B; b += 32) {
+      int64_t s0, m0;
+      bad |= !new_tokens(a.len, a.n_new, b, a.T, cap, s0, m0);
+    }
+    const unsigned any = __any_sync(0xffffffffu, bad);
+    if (threadIdx.x == 0) *a.status = any ? 8u : 0u;
+  }
+  const int64_t item = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
+  const int64_t tok = item / a.nchunk;
+  const int chunk = (int)(item - tok * a.nchunk);
+  const int b = (int)(tok / a.T), t = (int)(tok - (int64_t)b * a.T);
+  // (lanes of a warp leave together or stay together for the shuffles below:
+  // the mask of a group's shuffles names its own lanes only)
+  int64_t start = 0, m = 0;
+  if (b >= a.B || !new_tokens(a.len, a.n_new, b, a.T, cap, start, m) || t >= m) return;
+  const int64_t pos = start + t;
+
+  const bool turns_here = j < a.rot / 8;
+  int c0, c1, p0, p1;   // first channels of the two vectors, first pairs
+  if (a.interleaved) {
+    c0 = 8 * j; c1 = c0 + 4;
+    p0 = 4 * j; p1 = p0 + 2;
+  } else {
+    c0 = turns_here ? 4 * j : a.rot + 8 * (j - a.rot / 8);
+    c1 = turns_here ? c0 + a.rot / 2 : c0 + 4;
+    p0 = 4 * j; p1 = p0 + 2;
+  }
+  const int h_lo = chunk * a.heads_per, h_hi = min(h_lo + a.heads_per, a.Hq + 2 * a.Hkv);
+  float cs[4], sn[4];
+  if (turns_here && h_lo < a.Hq + a.Hkv) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = i < 2 ? p0 + i : p1 + i - 2;
+      const long long frac = (long long)((unsigned long long)pos * a.turns[p]);   // signed: [-1/2, 1/2) turn
+      sincospif((float)frac * 1.0842021724855044e-19f, &sn[i], &cs[i]);           // 2^-63: in units of pi
+    }
+  }
+  float4 wq0, wq1, wk0, wk1;
+  if (a.wq) {
+    wq0 = Vec4<E>::widen(*reinterpret_cast<const Raw*>(reinterpret_cast<const E*>(a.wq) + c0));
+    wq1 = Vec4<E>::widen(*reinterpret_cast<const Raw*>(reinterpret_cast<const E*>(a.wq) + c1));
+  }
+  if (a.wk) {
+    wk0 = Vec4<E>::widen(*reinterpret_cast<const Raw*>(reinterpret_cast<const E*>(a.wk) + c0));
+    wk1 = Vec4<E>::widen(*reinterpret_cast<const Raw*>(reinterpret_cast<const E*>(a.wk) + c1));
+  }
+  const unsigned group_mask =
+      LPR == 16 ? 0xffffu << (threadIdx.x & 16) : 0xffu << (threadIdx.x & 24);
+  const E* qrow = reinterpret_cast<const E*>(a.q) + b * a.qs.b + t * a.qs.t;
+  const E* krow = reinterpret_cast<const E*>(a.k) + b * a.ks.b + t * a.ks.t;
+  const E* vrow = reinterpret_cast<const E*>(a.v) + b * a.vs.b + t * a.vs.t;
+
+  for (int h0 = h_lo; h0 < h_hi; h0 += kRopeBatch) {
+    Raw r0[kRopeBatch], r1[kRopeBatch];
+#pragma unroll
+    for (int i = 0; i < kRopeBatch; ++i) {
+      const int h = h0 + i;
+      if (h >= h_hi || (h >= a.Hq + a.Hkv && !a.v)) continue;
+      const E* src = h < a.Hq ? qrow + h * a.qs.h
+                   : h < a.Hq + a.Hkv ? krow + (h - a.Hq) * a.ks.h : vrow + (h - a.Hq - a.Hkv) * a.vs.h;
+      r0[i] = *reinterpret_cast<const Raw*>(src + c0);
+      r1[i] = *reinterpret_cast<const Raw*>(src + c1);
+    }
+#pragma unroll
+    for (int i = 0; i < kRopeBatch; ++i) {
+      const int h = h0 + i;
+      if (h >= h_hi || (h >= a.Hq + a.Hkv && !a.v)) continue;
+      E* dst;
+      if (h < a.Hq) {
+        dst = reinterpret_cast<E*>(a.q_out) + (((int64_t)b * a.T + t) * a.Hq + h) * D;
+      } else {
+        const int g = h < a.Hq + a.Hkv ? h - a.Hq : h - a.Hq - a.Hkv;
+        dst = reinterpret_cast<E*>(h < a.Hq + a.Hkv ? a.K : a.V) +
+              (a.to_cache ? (((int64_t)b * a.Hkv + g) * a.n_max + pos) * D
+                          : (((int64_t)b * a.T + t) * a.Hkv + g) * D);
+      }
+      if (h < a.Hq + a.Hkv) {
+        float4 x = Vec4<E>::widen(r0[i]), y = Vec4<E>::widen(r1[i]);
+        if (h < a.Hq ? a.wq != nullptr : a.wk != nullptr) {
+          float ss = ((x.x * x.x + x.y * x.y) + (x.z * x.z + x.w * x.w)) +
+                     ((y.x * y.x + y.y * y.y) + (y.z * y.z + y.w * y.w));
+#pragma unroll
+          for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group_mask, ss, o);
+          const float inv = rsqrtf(ss * (1.0f / D) + a.eps);
+          const float4 w0 = h < a.Hq ? wq0 : wk0, w1 = h < a.Hq ? wq1 : wk1;
+          x.x *= inv * w0.x; x.y *= inv * w0.y; x.z *= inv * w0.z; x.w *= inv * w0.w;
+          y.x *= inv * w1.x; y.y *= inv * w1.y; y.z *= inv * w1.z; y.w *= inv * w1.w;
+        }
+        if (turns_here) {
+          if (a.interleaved) {
+            turn_pair(x.x, x.y, cs[0], sn[0]); turn_pair(x.z, x.w, cs[1], sn[1]);
+            turn_pair(y.x, y.y, cs[2], sn[2]); turn_pair(y.z, y.w, cs[3], sn[3]);
+          } else {
+            turn_pair(x.x, y.x, cs[0], sn[0]); turn_pair(x.y, y.y, cs[1], sn[1]);
+            turn_pair(x.z, y.z, cs[2], sn[2]); turn_pair(x.w, y.w, cs[3], sn[3]);
+          }
+        }
+        r0[i] = Vec4<E>::narrow(x);
+        r1[i] = Vec4<E>::narrow(y);
+      }
+      *reinterpret_cast<Raw*>(dst + c0) = r0[i];
+      *reinterpret_cast<Raw*>(dst + c1) = r1[i];
+    }
+  }
+}
+
+template <int D, typename E>
+void launch_rope(const RopeArgs& a, int64_t blocks, cudaStream_t st) {
+  launch_pdl(qk_norm_rope_kernel<D, E>, dim3((unsigned)blocks), dim3(kRopeThreads), 0, st, a);
+}
+
+}  // namespace csa
+
+using namespace csa;
+
+extern "C" {
+
+csa_status csa_rope_turns(const double* inv_freq, int n, uint64_t* turns) {
+  if (!inv_freq || !turns || n < 0) return CSA_ERR_INVALID_ARG;
+  // 1 / (2 pi) as the sum of two doubles
+  const double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
+  for (int i = 0; i < n; ++i) {
+    const double f = std::fabs(inv_freq[i]);
+    if (!(f <= 1048576.0)) return CSA_ERR_INVALID_ARG;
+    const double p = f * hi;
+    const double e = std::fma(f, hi, -p) + f * lo;      // f / (2 pi) = p + e
+    const double t = std::ldexp(p - std::floor(p), 64);  // exact, below 2^64
+    const uint64_t u = (uint64_t)t;
+    const uint64_t turn = u + (uint64_t)(int64_t)std::nearbyint((t - (double)u) + std::ldexp(e, 64));
+    turns[i] = inv_freq[i] < 0.0 ? 0u - turn : turn;
+  }
+  return CSA_OK;
+}
+
+csa_status csa_qk_norm_rope(const csa_shape* shape, int T, const csa_norm_rope* params, const void* q,
+                            const csa_strides* qs, const void* k, const csa_strides* ks, const void* v,
+                            const csa_strides* vs, const int64_t* len, const int64_t* n_new, void* q_out, void* K,
+                            void* V, int to_cache, uint32_t* status, void* stream) {
+  if (!shape_ok(shape) || !params || T < 1 || !q || !k || !len || !q_out || !K || (v && !V) ||
+      (to_cache != 0 && to_cache != 1))
+    return CSA_ERR_INVALID_ARG;
+  const csa_status su = shape_supported(shape);
+  if (su != CSA_OK) return su;
+  const int d = shape->d;
+  if (params->rot_dim < 0 || params->rot_dim > d || params->rot_dim % 8 != 0 || (params->rot_dim && !params->turns) ||
+      (params->interleaved != 0 && params->interleaved != 1) || !(params->norm_eps >= 0.f) ||
+      !std::isfinite(params->norm_eps))
+    return CSA_ERR_INVALID_ARG;
+  const bool bf16 = shape->dtype == CSA_BF16;
+  const int64_t unit = bf16 ? 8 : 4;
+  if (!strides_ok(qs, unit, shape->B, T, shape->Hq) || !strides_ok(ks, unit, shape->B, T, shape->Hkv) ||
+      (v && !strides_ok(vs, unit, shape->B, T, shape->Hkv)))
+    return CSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(K) || !aligned16(V) ||
+      !aligned16(params->wq) || !aligned16(params->wk))
+    return CSA_ERR_INVALID_ARG;
+  RopeArgs a = {};
+  a.q = q; a.k = k; a.v = v; a.qs = *qs; a.ks = *ks;
+  if (v) a.vs = *vs;
+  a.len = len; a.n_new = n_new; a.wq = params->wq; a.wk = params->wk; a.turns = params->turns;
+  a.q_out = q_out; a.K = K; a.V = V; a.status = status; a.n_max = shape->n_max;
+  a.B = shape->B; a.T = T; a.Hq = shape->Hq; a.Hkv = shape->Hkv;
+  a.rot = params->rot_dim; a.interleaved = params->interleaved; a.to_cache = to_cache; a.eps = params->norm_eps;
+  const int heads = shape->Hq + (v ? 2 : 1) * shape->Hkv;
+  const int64_t tokens = (int64_t)shape->B * T;
+  a.heads_per = 4;
+  a.nchunk = (heads + a.heads_per - 1) / a.heads_per;
+  const int64_t items = tokens * a.nchunk, per_cta = kRopeThreads / (d / 8);
+  const int64_t blocks = (items + per_cta - 1) / per_cta;
+  if (blocks > 0x7fffffff) return CSA_ERR_UNSUPPORTED;
+  add_launches(1);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (d == 128) bf16 ? launch_rope<128, __nv_bfloat16>(a, blocks, st) : launch_rope<128, float>(a, blocks, st);
+  else bf16 ? launch_rope<64, __nv_bfloat16>(a, blocks, st) : launch_rope<64, float>(a, blocks, st);
+  return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+}
+
+}  // extern "C"

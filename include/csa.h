@@ -299,6 +299,154 @@ csa_status csa_dense_decode_static(const csa_shape* shape, const void* q,
                                    const void* K, const void* V,
                                    const int64_t* len, float* o, void* stream);
 
+/* ---- rows before the cache: per-head norms and the position rotation ----
+ *
+ * What a transformer layer does between its projections and the decode
+ * entry points above.  The paper has no counterpart (its caches hold rotated
+ * keys); Llama-shaped models rotate q and k by position, and several
+ * normalise every head first.
+ *
+ * Element strides of a [B][T][heads][d] operand (channel stride 1): element
+ * (b, t, h, c) lies at b * b_stride + t * t_stride + h * h_stride + c.  The
+ * base address is 16-byte aligned and every stride a multiple of 16 bytes. */
+typedef struct {
+  int64_t b, t, h;
+} csa_strides;
+
+typedef struct {
+  const void* wq;          /* device [d], type `dtype`: norm weights of the   */
+  const void* wk;          /* query / key heads; NULL: that side is not normed */
+  float norm_eps;          /* added to the mean square, >= 0                  */
+  int rot_dim;             /* first channels that rotate: a multiple of 8,    */
+                           /* 0 (no rotation) .. d                            */
+  int interleaved;         /* pair i is channels (2i, 2i + 1) with 1, (i,     */
+                           /* i + rot_dim / 2) with 0                         */
+  const uint64_t* turns;   /* device [rot_dim / 2]: rotation of pair i per    */
+                           /* position, in turns times 2^64 (csa_rope_turns)  */
+} csa_norm_rope;
+
+/* turns[i] = the fractional part of inv_freq[i] / (2 pi), times 2^64 (both
+ * host arrays of n, |inv_freq| <= 2^20): a position times it, modulo 2^64, is
+ * the pair's angle with no loss at far positions. */
+csa_status csa_rope_turns(const double* inv_freq, int n, uint64_t* turns);
+
+/* Query and key norms and the rotation of the new tokens, in one pass:
+ *   x <- x * (mean_c x_c^2 + norm_eps)^(-1/2) * w_c        (with weights)
+ *   (x_a, x_b) <- (x_a cos - x_b sin, x_a sin + x_b cos)   (pair a, b of
+ *                 index i; angle = position * inv_freq[i])
+ * in float32, rounded once to `dtype`.  v is copied.  Sequence b's tokens
+ * t < n_new[b] are at positions len[b] - n_new[b] + t: as in
+ * csa_decode_step_device, len counts the tokens just added.
+ *   q, k, v   device [B][T][Hq | Hkv][d] with strides qs, ks, vs; v may be
+ *             NULL (then V is not written)
+ *   len       device [B] int64; n_new device [B] int64, or NULL: T each
+ *   q_out     device [B][T][Hq][d]
+ *   K, V      to_cache = 1: device [B][Hkv][n_max][d], the row of a token is
+ *             its position (the cache of the decode entry points);
+ *             to_cache = 0: device [B][T][Hkv][d] (rows for csa_kv4_append)
+ * Rows of tokens t >= n_new[b] are neither read nor written.  q_out may be q
+ * itself when q has that layout; otherwise outputs must not overlap inputs.
+ *   status    device uint32 the call sets to 0, or to a flag csa_check turns
+ *             into CSA_ERR_INVALID_ARG when a sequence has n_new outside
+ *             [0, T], len < n_new or (to_cache) len > n_max: that sequence's
+ *             rows are then not written.  NULL: no report. */
+csa_status csa_qk_norm_rope(const csa_shape* shape, int T,
+                            const csa_norm_rope* params, const void* q,
+                            const csa_strides* qs, const void* k,
+                            const csa_strides* ks, const void* v,
+                            const csa_strides* vs, const int64_t* len,
+                            const int64_t* n_new, void* q_out, void* K,
+                            void* V, int to_cache, uint32_t* status,
+                            void* stream);
+
+/* ---- a K/V cache held in 4 bits ----
+ *
+ * Whole blocks of 64 tokens (aligned to position 0) are held as 4-bit codes:
+ * keys per block and channel exactly as csa_quantize_keys codes them (picx.dev
+ * "Algorithm Components" 4, the KIVI scheme, whose values are coded per
+ * token), values per token over their d channels: m = min, Delta = fl((max -
+ * min) / 15), code = clamp(rint(fl(fl(v - m) / Delta)), 0, 15), all codes 0
+ * where Delta = 0.  A code stands for fl(fl(code Delta) + m).  The rows of the
+ * incomplete last block are kept as they are, until the block is whole.  A
+ * NaN or infinity in a block makes everything its key channel, or its
+ * value's token, stands for NaN.
+ *
+ *   K4      [B][Hkv][nblk_max * 64][d/2]    as above
+ *   bounds  [B][Hkv][nblk_max][2][d]        as above
+ *   V4      [B][Hkv][nblk_max][d][32]       uint8: a row holds one channel of
+ *           the block's tokens; token t = 32 i + 16 u + 8 v + 2 w + e (i, u,
+ *           v, e bits, w in 0..3) is nibble 16 w + 8 i + 4 e + 2 u + v (even
+ *           nibbles low): a matrix instruction's operand order
+ *   vscale  [B][Hkv][nblk_max * 64][2]      float: each token's m, Delta
+ *   Kt, Vt  [B][Hkv][64][d]                 type `dtype`: row p % 64 of the
+ *           incomplete block holds position p
+ * All device memory, 16-byte aligned.  152 bytes per token and KV head at
+ * d = 128, against 512 in bf16.  Lengths are device arrays read in stream
+ * order, so appending and attending can be captured into one CUDA graph. */
+typedef struct {
+  uint8_t* K4;
+  float* bounds;
+  uint8_t* V4;
+  float* vscale;
+  void* Kt;
+  void* Vt;
+} csa_kv4;
+
+/* Appends n_new[b] <= T tokens to every sequence; len[b] counts them already
+ * (so the cache held len[b] - n_new[b] tokens before).  Blocks that become
+ * whole are coded from the kept rows and the new ones.
+ *   k, v   device [B][T][Hkv][d] with strides ks, vs; rows t >= n_new[b] are
+ *          not read
+ *   len, n_new, status: as in csa_qk_norm_rope (len <= n_max); a sequence
+ *          out of range is left as it was */
+csa_status csa_kv4_append(const csa_shape* shape, const csa_kv4* cache, int T,
+                          const void* k, const csa_strides* ks, const void* v,
+                          const csa_strides* vs, const int64_t* len,
+                          const int64_t* n_new, uint32_t* status,
+                          void* stream);
+
+/* Reads rows back as the values they stand for, rounded to `dtype`: row i of
+ * K, V (device [B][Hkv][rows][d]) is position first[b] + i, for positions
+ * below len[b]; other rows are left as they are.
+ *   first  device [B] int64 >= 0, or NULL: 0
+ *   len    device [B] int64, 0 <= len[b] <= n_max
+ *   status as in csa_qk_norm_rope (set for first < 0 or len out of range;
+ *          that sequence's rows are not written) */
+csa_status csa_kv4_unpack(const csa_shape* shape, const csa_kv4* cache,
+                          int64_t rows, const int64_t* first,
+                          const int64_t* len, void* K, void* V,
+                          uint32_t* status, void* stream);
+
+/* Bytes of workspace csa_kv4_decode needs for up to T query tokens per
+ * sequence on the current device; 0 when the arguments are invalid. */
+size_t csa_kv4_workspace_size(const csa_shape* shape, int T);
+
+/* Decode attention over the 4-bit cache, for the last n_q[b] <= T tokens of
+ * every sequence (T = 1: a decode step; more: drafted tokens or a short
+ * chunk): o = softmax(q K^T / sqrt d) V with K, V the values the cache stands
+ * for; token t of sequence b, at position len[b] - n_q[b] + t, attends to
+ * the positions up to its own.  Softmax statistics and sums in float32.
+ *   q    device [B][T][Hq][d], type `dtype`, strides qs
+ *   len  device [B] int64, 0 <= len[b] <= n_max, its tokens appended already
+ *   n_q  device [B] int64, or NULL: T each
+ *   o    device [B][T][Hq][d] float; rows t >= n_q[b] are left as they are; a
+ *        row with no position to attend to is 0
+ *   lse  device [B][T][Hq] float, or NULL: ln sum exp(s) of each row (-inf
+ *        for a row with nothing to attend to)
+ *   workspace  device, csa_kv4_workspace_size bytes, 256-byte aligned, one
+ *        per call in flight (two captured graphs that share one must not
+ *        replay at the same time); contents on entry do not matter.  It
+ *        begins with the status word csa_check reads (CSA_ERR_INVALID_ARG:
+ *        a length or n_q out of range, which is clamped).
+ * T <= 16 and T * Hq / Hkv <= 64, else CSA_ERR_UNSUPPORTED. */
+#define CSA_KV4_MAX_T 16
+#define CSA_KV4_MAX_ROWS 64
+csa_status csa_kv4_decode(const csa_shape* shape, const csa_kv4* cache, int T,
+                          const void* q, const csa_strides* qs,
+                          const int64_t* len, const int64_t* n_q, float* o,
+                          float* lse, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
 /* Where csa_decode_step keeps its intermediate arrays inside the workspace
  * (byte offsets), for diagnostics and parity tests.  Valid after the step's
  * stream has synchronised, until the workspace is reused.
@@ -357,11 +505,13 @@ csa_status csa_profile_enable(int on);
 csa_status csa_profile_read(csa_phase_times* out);
 
 /* Synchronises `stream`, then returns the device status word recorded in
- * `workspace` by the last csa_decode_step, csa_decode_step_device or
- * csa_dense_decode that used it: CSA_OK, CSA_ERR_NONFINITE,
- * CSA_ERR_WORKSPACE, CSA_ERR_TIMEOUT (a bounded wait of the dense kernel
- * gave up) or CSA_ERR_INVALID_ARG (a device length out of range); or
- * CSA_ERR_CUDA if the stream reports an error. */
+ * `workspace` by the last csa_decode_step, csa_decode_step_device,
+ * csa_dense_decode or csa_kv4_decode that used it, or in the status word of
+ * the last csa_qk_norm_rope, csa_kv4_append or csa_kv4_unpack that was given
+ * this address: CSA_OK, CSA_ERR_NONFINITE, CSA_ERR_WORKSPACE,
+ * CSA_ERR_TIMEOUT (a bounded wait of a kernel gave up) or
+ * CSA_ERR_INVALID_ARG (a device length out of range); or CSA_ERR_CUDA if the
+ * stream reports an error. */
 csa_status csa_check(void* workspace, void* stream);
 
 /* Static English description of a status code. */
