@@ -15,9 +15,34 @@
 // for each item that was cut.
 //
 // The rows of an item are its T * G query vectors (G query heads share the
-// KV head); a warp handles a tile of 8 rows, so with more than 8 rows the
+// KV head).  A warp handles a tile of 4 or 8 rows; with more than 8 rows the
 // warps of a CTA form teams of 2, 4 or 8 that share the blocks.
+//
+// Whole blocks that every row sees in full go through the tensor cores with
+// the codes themselves as one operand.  A key is k_c = m_c + Delta_c n_c, so
+//   q.k = sum_c q_c m_c + sum_c (q_c Delta_c) n_c,
+// and a value row is v = m_t + Delta_t n, so
+//   sum_t p_t v_t = sum_t p_t m_t + sum_t (p_t Delta_t) n_t :
+// no code is ever converted or scaled.  A nibble in a zeroed 16-bit word is
+// already a half-precision number (n 2^-17 in bits 7..10), which matrix
+// instructions multiply exactly: eight key codes cost two shifts and four
+// ANDs.  The instructions line products up by their operands' exponents and
+// count leading zeros as digits, so nibbles stand as high as they can: at
+// bits 0..3 and 4..7 the 128K-token output was off by 2.3e-5, here by 1e-6
+// (values, whose errors weigh more, all at 7..10; half of the keys at 3..6).
+// The other operand, q_c Delta_c or p_t Delta_t, is scaled by a power of two
+// to the top of the half-precision range and split into two halves (22 bits:
+// a single one would leave 2^-12 of every score), and the products are
+// summed in float32.  With up to 4 rows the two parts
+// fill the 8 columns of one instruction (m16n8k16: codes are the 16-row
+// side); with 8 rows each part takes an instruction.  Blocks that some row
+// sees in part, and the incomplete block, take a plain path (kd_step).
+//
+// Blocks come by bulk copies into a ring of shared-memory stages per team,
+// each stage on an mbarrier; the first blocks of the next item are on their
+// way while the current one is merged.
 #include <cmath>
+#include <cuda_fp16.h>
 
 #include "csa_args.cuh"
 
@@ -39,7 +64,22 @@ struct Kv4DecodeArgs {
 };
 
 constexpr int kKdWarps = 8;
-constexpr int kKdTile = 8;        // query rows of a warp
+constexpr int kKdStages = 16;     // blocks in the rings of a CTA, over all teams
+
+// one block in shared memory.  The bounds are copied in eight pieces, 16
+// bytes apart, so that the four channel ranges of a warp's lanes start in
+// different banks (one piece for all would put them in the same ones).
+template <int D>
+struct KdStage {
+  static constexpr int K = 0;
+  static constexpr int V = K + kBlock * D / 2;
+  static constexpr int S = V + kBlock * D / 2;
+  static constexpr int B = S + kBlock * 8;
+  static constexpr int PIECE = D;                       // bytes: D / 4 floats
+  static constexpr int PITCH = PIECE + 16;
+  static constexpr int bytes = B + 8 * PITCH;
+  static constexpr int tx = kBlock * D + kBlock * 8 + 8 * D;
+};
 
 // units of one (sequence, KV head) of n tokens (at least one: somebody has to
 // write the output of an empty sequence)
@@ -100,22 +140,22 @@ __device__ __forceinline__ void kd_store(const Kv4DecodeArgs& a, int b, int g, i
   if (c == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
 }
 
-template <int D>
+template <int D, int RT>
 struct KdState {
-  float m[kKdTile], l[kKdTile], acc[kKdTile][D / 32];
+  float m[RT], l[RT], acc[RT][D / 32];
 };
 
 // one online-softmax step of a warp over eight tokens: lane holds channels
 // [lane * D / 32, ...) of the eight rows; tok(lane & 7) is the position of
 // the token whose score the lane ends up with; row r sees positions below
 // s_end[r]
-template <int D>
-__device__ __forceinline__ void kd_step(KdState<D>& st, const float (&kv)[8][D / 32], const float (&vv)[8][D / 32],
+template <int D, int RT>
+__device__ __forceinline__ void kd_step(KdState<D, RT>& st, const float (&kv)[8][D / 32], const float (&vv)[8][D / 32],
                                         const float* s_q, const int64_t* s_end, int64_t pos, int rows) {
   constexpr int CPL = D / 32;
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int r = 0; r < kKdTile; ++r) {
+  for (int r = 0; r < RT; ++r) {
     if (r >= rows) break;
     float part[8];
 #pragma unroll
@@ -159,24 +199,479 @@ __device__ __forceinline__ void kd_step(KdState<D>& st, const float (&kv)[8][D /
   }
 }
 
-template <int D, typename E>
-__global__ void __launch_bounds__(kKdWarps * 32) kv4_decode_kernel(const Kv4DecodeArgs a) {
+// ------------------------------------------------------- items and blocks
+
+// the part of an item that lies in a CTA's run
+struct KdSeg {
+  int b, g;
+  int64_t bg, n, nq, ub;   // ub: units of the item
+  int64_t blk0, cnt;       // units [blk0, blk0 + cnt) of it are here
+  int64_t nfast;           // of those, the first nfast are seen in full by every row
+};
+__device__ __forceinline__ KdSeg kd_seg(const Kv4DecodeArgs& a, const int64_t* s_pref, int64_t u, int64_t u1) {
+  KdSeg s;
+  s.b = kd_find(s_pref, a.B, u);
+  s.n = kd_len(a, s.b);
+  s.nq = kd_nq(a, s.b);
+  s.ub = kd_units(s.n);
+  const int64_t rem = u - s_pref[s.b];
+  s.g = (int)(rem / s.ub);
+  s.bg = (int64_t)s.b * a.Hkv + s.g;
+  s.blk0 = rem - s.g * s.ub;
+  s.cnt = min(s.ub - s.blk0, u1 - u);
+  // the first row sees positions below n - nq + 1
+  const int64_t full = min(s.n, max(s.n - s.nq + 1, (int64_t)0)) / kBlock;
+  s.nfast = min(max(full - s.blk0, (int64_t)0), s.cnt);
+  return s;
+}
+
+// The order in which a team takes blocks, over all items of the CTA.
+struct KdCursor {
+  int64_t u, u1, x, nfast, at0, cnt;
+  int step, first;
+  __device__ __forceinline__ void open(const Kv4DecodeArgs& a, const int64_t* s_pref) {
+    const KdSeg s = kd_seg(a, s_pref, u, u1);
+    nfast = s.nfast; cnt = s.cnt; at0 = s.bg * a.nblk_max + s.blk0; x = first;
+  }
+  // the next block's index in the cache, or -1
+  __device__ __forceinline__ int64_t next(const Kv4DecodeArgs& a, const int64_t* s_pref) {
+    while (u < u1) {
+      if (x < nfast) {
+        const int64_t at = at0 + x;
+        x += step;
+        return at;
+      }
+      u += cnt;
+      if (u < u1) open(a, s_pref);
+    }
+    return -1;
+  }
+};
+
+__device__ __forceinline__ void bulk_copy(unsigned dst, const void* src, unsigned bytes, unsigned bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+template <int D>
+__device__ __forceinline__ void kd_load(const csa_kv4& c, int64_t at, unsigned stage, unsigned bar) {
+  using St = KdStage<D>;
+  mbar_expect_tx(bar, St::tx);
+  bulk_copy(stage + St::K, c.K4 + at * (kBlock * D / 2), kBlock * D / 2, bar);
+  bulk_copy(stage + St::V, c.V4 + at * (kBlock * D / 2), kBlock * D / 2, bar);
+  bulk_copy(stage + St::S, c.vscale + at * kBlock * 2, kBlock * 8, bar);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    bulk_copy(stage + St::B + i * St::PITCH, c.bounds + at * 2 * D + i * (D / 4), St::PIECE, bar);
+}
+
+// ------------------------------------------------------ tensor-core blocks
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0,
+                                        unsigned b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ unsigned transpose8(unsigned x) {
+  unsigned y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+// two float32 numbers as half-precision parts: hi = the rounded pair (x low,
+// y high), lo = the rounded remainders
+__device__ __forceinline__ unsigned half_pair(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const unsigned*>(&h);
+}
+__device__ __forceinline__ unsigned half_rest(float x, float y, unsigned hi) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  return half_pair(x - f.x, y - f.y);
+}
+// 2^k, |k| <= 126
+__device__ __forceinline__ float pow2i(int k) { return __int_as_float((127 + k) << 23); }
+// exponent of x > 0 (subnormals: -127)
+__device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Nibbles of a half word in bits 3..6 and 7..10: n 2^-21 and n 2^-17 (bit 10
+// is the lowest exponent bit, where the subnormal numbers go on as normal
+// ones of the same spacing)
+constexpr unsigned kNibA = 0x00780078u, kNibB = 0x07800780u;
+constexpr float kKeyUnit = 2097152.0f, kValueUnit = 131072.0f;   // 2^21, 2^17
+
+// The state of a warp over the tensor-core blocks of an item.  Lane (gid =
+// lane / 4, tid = lane % 4) holds in q the D / 4 channels [tid D / 4, ...)
+// of query row gid % RT (RT = 4: lanes with gid >= 4 hold the same rows and
+// supply the low parts), times qsc, a power of two, and times 1/16 for odd
+// channels, whose codes stand 16 times higher in the operand.
+// Softmax state: rows ra, ra + 1 with ra = 2 (tid % (RT / 2)); the sums l are
+// over the lane's own tokens, om too (RT = 4: and those of lane ^ 2).
+template <int D, int RT>
+struct KdFast {
+  float q[D / 4];
+  float qsc;
+  float csA, csB;         // kKeyUnit / qsc of rows ra, ra + 1
+  float mA, mB, lA, lB, omA, omB;
+  float sv;               // scale of p_t Delta_t, a power of two
+  float o[D / 16][4];     // channels 16 i + gid (+ 8) x operand columns 2 tid, 2 tid + 1
+  bool fresh;
+};
+
+template <int D, int RT>
+__device__ __forceinline__ void kd_fast_init(KdFast<D, RT>& f, const float* s_q, int rows) {
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
+  const int r = gid % RT;
+#pragma unroll
+  for (int i = 0; i < D / 4; ++i) f.q[i] = r < rows ? s_q[r * D + tid * (D / 4) + i] * (i & 1 ? 0.0625f : 1.0f) : 0.0f;
+  f.qsc = 1.0f;
+  f.csA = f.csB = kKeyUnit;
+  f.mA = f.mB = -INFINITY;
+  f.lA = f.lB = f.omA = f.omB = 0.0f;
+  f.sv = 1.0f;
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) f.o[i][0] = f.o[i][1] = f.o[i][2] = f.o[i][3] = 0.0f;
+  f.fresh = true;
+}
+
+template <int D, int RT>
+__device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* st) {
+  using St = KdStage<D>;
+  constexpr int NC = D / 4;        // channels of a lane
+  constexpr int NW = D / 32;       // code words of a lane in a key row
+  constexpr int HL = RT == 8 ? 2 : 1;   // instructions per operand (parts in columns with RT = 4)
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
+  const bool upper = RT == 4 && tid >= 2;
+  const int ra = 2 * (tid % (RT / 2));
+
+  // q_c Delta_c, and sum_c q_c m_c
+  const float* sm = reinterpret_cast<const float*>(st + St::B + tid * St::PITCH);
+  const float* sd = reinterpret_cast<const float*>(st + St::B + (4 + tid) * St::PITCH);
+  float x[NC];
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NC; i += 4) {
+    const float4 dl = *reinterpret_cast<const float4*>(sd + i);
+    x[i] = f.q[i] * dl.x; x[i + 1] = f.q[i + 1] * dl.y; x[i + 2] = f.q[i + 2] * dl.z; x[i + 3] = f.q[i + 3] * dl.w;
+    top = fmaxf(fmaxf(top, fmaxf(fabsf(x[i]), fabsf(x[i + 1]))), fmaxf(fabsf(x[i + 2]), fabsf(x[i + 3])));
+  }
+  // keep the largest of a row below 2^15 (the first block sets it to 2^12 ..
+  // 2^13; smaller ones later keep an absolute error that only shrinks)
+  if (__any_sync(0xffffffffu, f.fresh || top >= 32768.0f)) {
+    float t = top < INFINITY ? top : 0.0f;
+    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+    if (t > 0.0f && (f.fresh || t >= 32768.0f)) {
+      const int have = exponent(f.qsc);
+      const int k = min(max(have + 12 - exponent(t), -100), 100) - have;
+      const float up = ldexpf(1.0f, k);
+      f.qsc *= up;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) { f.q[i] *= up; x[i] *= up; }
+    }
+    const float c = kKeyUnit / f.qsc;
+    f.csA = __shfl_sync(0xffffffffu, c, 4 * ra);
+    f.csB = __shfl_sync(0xffffffffu, c, 4 * ra + 4);
+  }
+  float qm = 0.0f, qm1 = 0.0f;
+  // (odd channels carry 1/16)
+#pragma unroll
+  for (int i = 0; i < NC; i += 4) {
+    if (RT == 4 && (i >= NC / 2) != 0) continue;
+    const float4 mn = *reinterpret_cast<const float4*>(sm + (RT == 4 ? (gid >> 2) * (NC / 2) : 0) + i);
+    const float q0 = RT == 4 ? (gid >> 2 ? f.q[i + NC / 2] : f.q[i]) : f.q[i];
+    const float q1 = RT == 4 ? (gid >> 2 ? f.q[i + 1 + NC / 2] : f.q[i + 1]) : f.q[i + 1];
+    const float q2 = RT == 4 ? (gid >> 2 ? f.q[i + 2 + NC / 2] : f.q[i + 2]) : f.q[i + 2];
+    const float q3 = RT == 4 ? (gid >> 2 ? f.q[i + 3 + NC / 2] : f.q[i + 3]) : f.q[i + 3];
+    qm = fmaf(q0, mn.x, qm); qm1 = fmaf(q1, mn.y, qm1);
+    qm = fmaf(q2, mn.z, qm); qm1 = fmaf(q3, mn.w, qm1);
+  }
+  qm = fmaf(qm1, 16.0f, qm) * (1.0f / f.qsc);           // (qsc: a power of two)
+  qm += __shfl_xor_sync(0xffffffffu, qm, 1);
+  qm += __shfl_xor_sync(0xffffffffu, qm, 2);
+  if (RT == 4) qm += __shfl_xor_sync(0xffffffffu, qm, 16);
+  const float qmA = __shfl_sync(0xffffffffu, qm, 4 * ra), qmB = __shfl_sync(0xffffffffu, qm, 4 * ra + 4);
+
+  // the operand: column gid, channel pairs (8 w + 0, 4), (1, 5), (2, 6), (3, 7)
+  unsigned bq[HL][NW][4];
+#pragma unroll
+  for (int w = 0; w < NW; ++w)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float u = x[8 * w + e], v = x[8 * w + e + 4];
+      const unsigned hi = half_pair(u, v);
+      const unsigned lo = half_rest(u, v, hi);
+      if (RT == 8) { bq[0][w][e] = hi; bq[HL - 1][w][e] = lo; }
+      else bq[0][w][e] = gid >= 4 ? lo : hi;
+    }
+
+  // scores of the four tiles of 16 tokens
+  float s[4][4];
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt) {
+    unsigned k0[NW], k1[NW];
+    const uint8_t* kr = st + St::K + (16 * mt + gid) * (D / 2) + tid * (D / 8);
+    if (D == 128) {
+      const uint4 u = *reinterpret_cast<const uint4*>(kr), v = *reinterpret_cast<const uint4*>(kr + 8 * (D / 2));
+      k0[0] = u.x; k0[1] = u.y; k0[NW - 2] = u.z; k0[NW - 1] = u.w;
+      k1[0] = v.x; k1[1] = v.y; k1[NW - 2] = v.z; k1[NW - 1] = v.w;
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2*>(kr), v = *reinterpret_cast<const uint2*>(kr + 8 * (D / 2));
+      k0[0] = u.x; k0[1] = u.y; k1[0] = v.x; k1[1] = v.y;
+    }
+    // (matrix instructions truncate their sums: short chains from zero, the
+    // low parts first, and the rest of the sum in rounded additions)
+    float t[2][4] = {};
+#pragma unroll
+    for (int h = HL - 1; h >= 0; --h)
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const unsigned g0 = k0[w] << 3, g1 = k1[w] << 3, h0 = k0[w] >> 5, h1 = k1[w] >> 5;
+        mma_f16(t[w & 1], g0 & kNibA, g1 & kNibA, g0 & kNibB, g1 & kNibB, bq[h][w][0], bq[h][w][1]);
+        mma_f16(t[w & 1], h0 & kNibA, h1 & kNibA, h0 & kNibB, h1 & kNibB, bq[h][w][2], bq[h][w][3]);
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[mt][i] = t[0][i] + t[1][i];
+  }
+  // RT = 4: add the two parts; afterwards the lane has token 16 mt + gid (+ 8
+  // in the upper lanes), rows ra, ra + 1, in s[mt][0], s[mt][1].
+  // RT = 8: tokens gid and gid + 8 in s[mt][0..1] and s[mt][2..3].
+  constexpr int TK = RT == 8 ? 2 : 1;    // tokens of a tile in a lane
+  float big = -INFINITY;
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt) {
+    if (RT == 4) {
+      const float g0 = __shfl_xor_sync(0xffffffffu, upper ? s[mt][0] : s[mt][2], 2);
+      const float g1 = __shfl_xor_sync(0xffffffffu, upper ? s[mt][1] : s[mt][3], 2);
+      s[mt][0] = fmaf((upper ? s[mt][2] : s[mt][0]) + g0, f.csA, qmA);
+      s[mt][1] = fmaf((upper ? s[mt][3] : s[mt][1]) + g1, f.csB, qmB);
+    } else {
+      s[mt][0] = fmaf(s[mt][0], f.csA, qmA); s[mt][1] = fmaf(s[mt][1], f.csB, qmB);
+      s[mt][2] = fmaf(s[mt][2], f.csA, qmA); s[mt][3] = fmaf(s[mt][3], f.csB, qmB);
+    }
+#pragma unroll
+    for (int k = 0; k < TK; ++k) big = fmaxf(big, fmaxf(s[mt][2 * k] - f.mA, s[mt][2 * k + 1] - f.mB));
+  }
+  // token scales
+  float2 sc[4][TK];
+  float wide = 0.0f;
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+    for (int k = 0; k < TK; ++k) {
+      sc[mt][k] = *reinterpret_cast<const float2*>(st + St::S + (16 * mt + gid + (RT == 8 ? 8 * k : upper ? 8 : 0)) * 8);
+      wide = fmaxf(wide, sc[mt][k].y);
+    }
+  // The running maximum moves only when a score exceeds it by more than one
+  // (then a weight would pass 2), and the value scale only when Delta_t does
+  // not fit: both are rare after the first blocks.
+  if (__any_sync(0xffffffffu, f.fresh || !(big <= 1.0f) || wide * f.sv > 16384.0f)) {
+    float xA = -INFINITY, xB = -INFINITY;
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int k = 0; k < TK; ++k) {
+        xA = fmaxf(xA, s[mt][2 * k]);
+        xB = fmaxf(xB, s[mt][2 * k + 1]);
+      }
+    float t = 0.0f;
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int k = 0; k < TK; ++k) t = fmaxf(t, sc[mt][k].y < INFINITY ? sc[mt][k].y : 0.0f);
+#pragma unroll
+    for (int m = (RT == 4 ? 2 : 4); m < 32; m <<= 1) {
+      xA = fmaxf(xA, __shfl_xor_sync(0xffffffffu, xA, m));
+      xB = fmaxf(xB, __shfl_xor_sync(0xffffffffu, xB, m));
+    }
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, m));
+    const float nA = fmaxf(f.mA, xA), nB = fmaxf(f.mB, xB);
+    float up = 1.0f;
+    if (t > 0.0f && (f.fresh || t * f.sv > 16384.0f)) {
+      const float to = pow2i(min(max(13 - exponent(t), -100), 100));   // Delta sv in [2^13, 2^14)
+      up = f.sv > 0.0f ? to / f.sv : 1.0f;
+      f.sv = to;
+    }
+    const float eA = f.mA > -INFINITY ? ex2(f.mA - nA) : 0.0f, eB = f.mB > -INFINITY ? ex2(f.mB - nB) : 0.0f;
+    if (!f.fresh) {
+      f.lA *= eA; f.lB *= eB;
+      f.omA *= eA; f.omB *= eB;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        f.o[i][0] *= eA * up; f.o[i][1] *= eB * up;
+        f.o[i][2] *= eA * up; f.o[i][3] *= eB * up;
+      }
+    }
+    f.mA = nA; f.mB = nB;
+    f.fresh = false;
+  }
+  const float rA = f.mA > -INFINITY ? f.mA : 0.0f, rB = f.mB > -INFINITY ? f.mB : 0.0f;
+  // Weights and the second operand: column gid, token pairs.  The tokens
+  // gid + 8 of a tile enter as 15 - n with the opposite sign, and
+  // with m + 15 Delta for m: the sums of codes, all positive, would outgrow
+  // the differences that the output consists of (values around zero) and
+  // leave them their rounding errors.
+  float omA = 0.0f, omB = 0.0f;
+  unsigned bp[HL][4][2];
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt) {
+    unsigned hi[TK], lo[TK];
+#pragma unroll
+    for (int k = 0; k < TK; ++k) {
+      const float pA = ex2(s[mt][2 * k] - rA), pB = ex2(s[mt][2 * k + 1] - rB);
+      f.lA += pA; f.lB += pB;
+      const float m = fmaf(sc[mt][k].y, RT == 8 ? (k ? 15.0f : 0.0f) : upper ? 15.0f : 0.0f, sc[mt][k].x);
+      omA = fmaf(pA, m, omA);
+      omB = fmaf(pB, m, omB);
+      const float w = sc[mt][k].y * ((RT == 8 ? k == 1 : upper) ? -f.sv : f.sv);
+      hi[k] = half_pair(pA * w, pB * w);
+      lo[k] = half_rest(pA * w, pB * w, hi[k]);
+    }
+    if (RT == 4) {
+      const unsigned got = __shfl_xor_sync(0xffffffffu, upper ? hi[0] : lo[0], 2);
+      bp[0][mt][0] = transpose8(upper ? got : hi[0]);
+      bp[0][mt][1] = transpose8(upper ? lo[0] : got);
+    } else {
+      bp[0][mt][0] = transpose8(hi[0]);
+      bp[0][mt][1] = transpose8(hi[TK - 1]);
+      bp[HL - 1][mt][0] = transpose8(lo[0]);
+      bp[HL - 1][mt][1] = transpose8(lo[TK - 1]);
+    }
+  }
+  // (the two halves of the tokens cancel: RT = 4 has them in lane pairs)
+  if (RT == 4) {
+    omA += __shfl_xor_sync(0xffffffffu, omA, 2);
+    omB += __shfl_xor_sync(0xffffffffu, omB, 2);
+  }
+  f.omA += omA;
+  f.omB += omB;
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    const uint8_t* vr = st + St::V + (16 * i + gid) * (kBlock / 2) + tid * 8;
+    const uint2 v0 = *reinterpret_cast<const uint2*>(vr), v1 = *reinterpret_cast<const uint2*>(vr + 8 * (kBlock / 2));
+    float t[4] = {};
+#pragma unroll
+    for (int h = HL - 1; h >= 0; --h)
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        const unsigned a = mt < 2 ? v0.x : v0.y, b = mt < 2 ? v1.x : v1.y;
+        if (mt & 1)
+          mma_f16(t, (a >> 1) & kNibB, (b >> 1) & kNibB, ~(a >> 5) & kNibB, ~(b >> 5) & kNibB, bp[h][mt][0], bp[h][mt][1]);
+        else
+          mma_f16(t, (a << 7) & kNibB, (b << 7) & kNibB, ~(a << 3) & kNibB, ~(b << 3) & kNibB, bp[h][mt][0], bp[h][mt][1]);
+      }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f.o[i][e] += t[e];
+  }
+}
+
+// the warp's sums as rows [RT] of m, l and acc[D] in shared memory
+template <int D, int RT>
+__device__ __forceinline__ void kd_fast_store(KdFast<D, RT>& f, float* s_m, float* s_l, float* s_acc) {
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
+  const bool upper = RT == 4 && tid >= 2;
+  const int ra = 2 * (tid % (RT / 2));
+  if (RT == 4) {
+    f.lA += __shfl_xor_sync(0xffffffffu, f.lA, 2);
+    f.lB += __shfl_xor_sync(0xffffffffu, f.lB, 2);
+  }
+#pragma unroll
+  for (int m = 4; m < 32; m <<= 1) {
+    f.lA += __shfl_xor_sync(0xffffffffu, f.lA, m);
+    f.lB += __shfl_xor_sync(0xffffffffu, f.lB, m);
+    f.omA += __shfl_xor_sync(0xffffffffu, f.omA, m);
+    f.omB += __shfl_xor_sync(0xffffffffu, f.omB, m);
+  }
+  if (gid == 0 && !upper) {
+    s_m[ra] = f.mA; s_m[ra + 1] = f.mB;
+    s_l[ra] = f.lA; s_l[ra + 1] = f.lB;
+  }
+  const float back = kValueUnit / f.sv;
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    if (RT == 4) {
+      const float g0 = __shfl_xor_sync(0xffffffffu, upper ? f.o[i][0] : f.o[i][2], 2);
+      const float g1 = __shfl_xor_sync(0xffffffffu, upper ? f.o[i][1] : f.o[i][3], 2);
+      const int c = 16 * i + gid + (upper ? 8 : 0);
+      s_acc[ra * D + c] = fmaf((upper ? f.o[i][2] : f.o[i][0]) + g0, back, f.omA);
+      s_acc[(ra + 1) * D + c] = fmaf((upper ? f.o[i][3] : f.o[i][1]) + g1, back, f.omB);
+    } else {
+      const int c = 16 * i + gid;
+      s_acc[ra * D + c] = fmaf(f.o[i][0], back, f.omA);
+      s_acc[(ra + 1) * D + c] = fmaf(f.o[i][1], back, f.omB);
+      s_acc[ra * D + c + 8] = fmaf(f.o[i][2], back, f.omA);
+      s_acc[(ra + 1) * D + c + 8] = fmaf(f.o[i][3], back, f.omB);
+    }
+  }
+}
+
+// shared memory: rings, mbarriers (full and empty), q rows, warp sums
+template <int D, int RT>
+struct KdLayout {
+  static constexpr int bars = kKdStages * KdStage<D>::bytes;
+  static constexpr int m = bars + 2 * kKdStages * 8;
+  static constexpr int l = m + kKdWarps * RT * 4;
+  static constexpr int acc = l + kKdWarps * RT * 4;
+  static constexpr int q = acc + kKdWarps * RT * D * 4;
+  static int smem(int rows) { return q + (rows + RT - 1) / RT * RT * D * 4; }
+};
+
+template <int D, int RT, typename E>
+__global__ void __launch_bounds__(kKdWarps * 32, 1) kv4_decode_kernel(const Kv4DecodeArgs a) {
   pdl_entry();
+  using St = KdStage<D>;
+  using Lt = KdLayout<D, RT>;
   constexpr int CPL = D / 32;
   __shared__ int64_t s_pref[kMaxB + 1];
   __shared__ int64_t s_end[CSA_KV4_MAX_ROWS];
-  __shared__ float s_m[kKdWarps][kKdTile], s_l[kKdWarps][kKdTile];
-  extern __shared__ __align__(16) float dyn[];
+  extern __shared__ __align__(128) uint8_t kd_sm[];
+  float* s_m = reinterpret_cast<float*>(kd_sm + Lt::m);        // [warps][RT]
+  float* s_l = reinterpret_cast<float*>(kd_sm + Lt::l);
+  float* s_acc = reinterpret_cast<float*>(kd_sm + Lt::acc);    // [warps][RT][D]
+  float* s_q = reinterpret_cast<float*>(kd_sm + Lt::q);        // [rows, padded][D]
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int R = a.T * a.G, Rp = (R + kKdTile - 1) / kKdTile * kKdTile;
-  float* s_q = dyn;                         // [Rp][D]
-  float* s_acc = dyn + Rp * D;              // [warps][8][D]
-  // teams: warps that share a block, one tile of rows each
-  const int ntile = Rp / kKdTile;
+  const int R = a.T * a.G, Rp = (R + RT - 1) / RT * RT;
+  // teams: warps that share a block, one tile of rows each, and a ring of
+  // kKdStages / nteam stages
+  const int ntile = Rp / RT;
   const int team = ntile <= 1 ? 1 : ntile <= 2 ? 2 : ntile <= 4 ? 4 : 8;
   const int nteam = kKdWarps / team, my_team = w / team, tile = w % team;
-  const int rows = min(kKdTile, R - tile * kKdTile);      // <= 0: a warp with no rows
+  const int rows = min(RT, R - tile * RT);                // <= 0: a warp with no rows
+  const int depth = kKdStages / nteam;
+  const unsigned base = smem_u32(kd_sm);
+  const unsigned ring = base + my_team * depth * St::bytes;
+  const unsigned full = base + Lt::bars + my_team * depth * 8, empty = full + kKdStages * 8;
+  if (tid < kKdStages) {
+    mbar_init(base + Lt::bars + 8 * tid, 1);
+    mbar_init(base + Lt::bars + 8 * (kKdStages + tid), team);
+    fence_barrier_init();
+  }
   kd_prefix(a, s_pref);
+  // (each wait below is bounded: one that gives up marks the call and the
+  // warp goes on without waiting or copying)
+  bool dead = false;
+  const int64_t total = s_pref[kMaxB];
+  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t u0 = (int64_t)blockIdx.x * per, u1 = min(total, u0 + per);
+  KdCursor cur;
+  cur.u = u0; cur.u1 = u1; cur.step = nteam; cur.first = my_team;
+  const bool producer = tile == 0 && lane == 0;
+  int issued = 0, used = 0;
+  if (producer && u0 < u1) {
+    cur.open(a, s_pref);
+    for (; issued < depth; ++issued) {
+      const int64_t at = cur.next(a, s_pref);
+      if (at < 0) break;
+      kd_load<D>(a.c, at, ring + issued * St::bytes, full + 8 * issued);
+    }
+  }
   if (blockIdx.x == 0 && tid < 32) {
     bool bad = false;
     for (int b = lane; b < a.B; b += 32) {
@@ -184,48 +679,68 @@ __global__ void __launch_bounds__(kKdWarps * 32) kv4_decode_kernel(const Kv4Deco
       if (a.n_q) bad |= a.n_q[b] < 0 || a.n_q[b] > a.T;
     }
     const unsigned any = __any_sync(0xffffffffu, bad);
+    // (a wait that gives up flags the word two seconds later at the earliest)
     if (lane == 0) *a.status = any ? 8u : 0u;
   }
-  const int64_t total = s_pref[kMaxB];
-  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t u0 = (int64_t)blockIdx.x * per, u1 = min(total, u0 + per);
 
   for (int64_t u = u0; u < u1;) {
-    const int b = kd_find(s_pref, a.B, u);
-    const int64_t n = kd_len(a, b), ub = kd_units(n), rem = u - s_pref[b];
-    const int g = (int)(rem / ub);
-    const int64_t blk0 = rem - (int64_t)g * ub, cnt = min(ub - blk0, u1 - u);
-    const int64_t nfull = n / kBlock, bg = (int64_t)b * a.Hkv + g;
-    const int64_t nq = kd_nq(a, b);
-    __syncthreads();
+    const KdSeg sg = kd_seg(a, s_pref, u, u1);
     for (int i = tid; i < Rp * D; i += kKdWarps * 32) {
       const int r = i / D, c = i - r * D;
       const int t = r / a.G;
       float x = 0.0f;
-      if (t < nq)
-        x = Elem<E>::get(reinterpret_cast<const E*>(a.q) + b * a.qs.b + t * a.qs.t + (int64_t)(g * a.G + r % a.G) * a.qs.h, c) * a.rs;
+      if (t < sg.nq)
+        x = Elem<E>::get(reinterpret_cast<const E*>(a.q) + sg.b * a.qs.b + t * a.qs.t +
+                             (int64_t)(sg.g * a.G + r % a.G) * a.qs.h, c) * a.rs;
       s_q[i] = x;
     }
-    if (tid < Rp) s_end[tid] = tid / a.G < nq ? n - nq + tid / a.G + 1 : 0;
+    if (tid < Rp) s_end[tid] = tid / a.G < sg.nq ? sg.n - sg.nq + tid / a.G + 1 : 0;
     __syncthreads();
-    KdState<D> st;
-#pragma unroll
-    for (int r = 0; r < kKdTile; ++r) {
-      st.m[r] = -INFINITY; st.l[r] = 0.0f;
-#pragma unroll
-      for (int c = 0; c < CPL; ++c) st.acc[r][c] = 0.0f;
+    const float* q = s_q + tile * RT * D;
+    float* my_m = s_m + w * RT;
+    float* my_l = s_l + w * RT;
+    float* my_acc = s_acc + w * RT * D;
+    {
+      KdFast<D, RT> f;
+      kd_fast_init<D, RT>(f, tile * RT < Rp ? q : s_q, rows);
+      for (int64_t x = my_team; x < sg.nfast; x += nteam) {
+        const int slot = used % depth;
+        if (!dead && !mbar_wait(full + 8 * slot, (used / depth) & 1)) dead = true;
+        if (rows > 0) kd_fast_block<D, RT>(f, kd_sm + (ring - base) + slot * St::bytes);
+        ++used;
+        __syncwarp();
+        if (team > 1 && lane == 0) mbar_arrive(empty + 8 * slot);
+        if (producer && !dead) {
+          const int64_t at = cur.next(a, s_pref);
+          if (at >= 0) {
+            if (team > 1 && !mbar_wait(empty + 8 * slot, ((used - 1) / depth) & 1)) dead = true;
+            if (!dead) kd_load<D>(a.c, at, ring + slot * St::bytes, full + 8 * slot);
+            ++issued;
+          }
+        }
+        dead = __any_sync(0xffffffffu, dead);
+      }
+      kd_fast_store<D, RT>(f, my_m, my_l, my_acc);
     }
-    if (rows > 0) {
-      const float* q = s_q + tile * kKdTile * D;
-      const int64_t* end = s_end + tile * kKdTile;
-      // groups of eight tokens, in turn over the teams
-      for (int64_t x = my_team; x < cnt * 8; x += nteam) {
-        const int64_t blk = blk0 + x / 8;
+    if (rows > 0 && sg.nfast < sg.cnt) {
+      // blocks that are seen in part, and the incomplete one, eight tokens
+      // at a time: the state moves on to lanes that hold channels
+      __syncwarp();
+      KdState<D, RT> st;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        st.m[r] = my_m[r]; st.l[r] = my_l[r];
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) st.acc[r][c] = my_acc[r * D + lane * CPL + c];
+      }
+      const int64_t* end = s_end + tile * RT;
+      for (int64_t x = sg.nfast * 8 + my_team; x < sg.cnt * 8; x += nteam) {
+        const int64_t blk = sg.blk0 + x / 8;
         const int grp = (int)(x % 8);
         const int64_t p0 = blk * kBlock;
         float kv[8][CPL], vv[8][CPL];
-        if (blk < nfull) {
-          const int64_t at = bg * a.nblk_max + blk;
+        if (blk < sg.n / kBlock) {
+          const int64_t at = sg.bg * a.nblk_max + blk;
           float mn[CPL], dl[CPL];
           unsigned vw[CPL];
 #pragma unroll
@@ -236,10 +751,10 @@ __global__ void __launch_bounds__(kKdWarps * 32) kv4_decode_kernel(const Kv4Deco
           }
           // word grp of a V4 row: tokens 32 i + 16 u + 8 v + 2 w + e with
           // i = grp & 1, w = grp >> 1, nibble 4 e + 2 u + v
-          const int base = 32 * (grp & 1) + 2 * (grp >> 1);
+          const int first = 32 * (grp & 1) + 2 * (grp >> 1);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int t = base + 16 * ((i >> 1) & 1) + 8 * (i & 1) + (i >> 2);
+            const int t = first + 16 * ((i >> 1) & 1) + 8 * (i & 1) + (i >> 2);
             const float2 sc = reinterpret_cast<const float2*>(a.c.vscale)[at * kBlock + t];
             const uint8_t* kr = a.c.K4 + (at * kBlock + t) * (D / 2) + lane * CPL / 2;
 #pragma unroll
@@ -249,54 +764,62 @@ __global__ void __launch_bounds__(kKdWarps * 32) kv4_decode_kernel(const Kv4Deco
             }
           }
           const int i = lane & 7;
-          kd_step<D>(st, kv, vv, q, end, p0 + base + 16 * ((i >> 1) & 1) + 8 * (i & 1) + (i >> 2), rows);
+          kd_step<D, RT>(st, kv, vv, q, end, p0 + first + 16 * ((i >> 1) & 1) + 8 * (i & 1) + (i >> 2), rows);
         } else {
-          if (p0 + 8 * grp >= n) continue;
+          if (p0 + 8 * grp >= sg.n) continue;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int t = 8 * grp + i;
-            const bool there = p0 + t < n;
-            const E* kr = reinterpret_cast<const E*>(a.c.Kt) + (bg * kBlock + t) * D + lane * CPL;
-            const E* vr = reinterpret_cast<const E*>(a.c.Vt) + (bg * kBlock + t) * D + lane * CPL;
+            const bool there = p0 + t < sg.n;
+            const E* kr = reinterpret_cast<const E*>(a.c.Kt) + (sg.bg * kBlock + t) * D + lane * CPL;
+            const E* vr = reinterpret_cast<const E*>(a.c.Vt) + (sg.bg * kBlock + t) * D + lane * CPL;
 #pragma unroll
             for (int c = 0; c < CPL; ++c) {
               kv[i][c] = there ? Elem<E>::get(kr, c) : 0.0f;
               vv[i][c] = there ? Elem<E>::get(vr, c) : 0.0f;
             }
           }
-          kd_step<D>(st, kv, vv, q, end, p0 + 8 * grp + (lane & 7), rows);
+          kd_step<D, RT>(st, kv, vv, q, end, p0 + 8 * grp + (lane & 7), rows);
         }
       }
-    }
-    // merge the teams
+      __syncwarp();
 #pragma unroll
-    for (int r = 0; r < kKdTile; ++r) {
-      if (lane == 0) { s_m[w][r] = st.m[r]; s_l[w][r] = st.l[r]; }
+      for (int r = 0; r < RT; ++r) {
+        if (lane == 0) { my_m[r] = st.m[r]; my_l[r] = st.l[r]; }
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) s_acc[(w * kKdTile + r) * D + lane * CPL + c] = st.acc[r][c];
+        for (int c = 0; c < CPL; ++c) my_acc[r * D + lane * CPL + c] = st.acc[r][c];
+      }
     }
     __syncthreads();
-    const bool done = cnt == ub;
+    // merge the teams
+    const bool done = sg.cnt == sg.ub;
     float* part = a.part + (2 * (int64_t)blockIdx.x + (u == u0 ? 0 : 1)) * R * (D + 2);
     for (int i = tid; i < R * D; i += kKdWarps * 32) {
       const int r = i / D, c = i - r * D;
+      const int x0 = r / RT * RT + r % RT;       // (tile, row) of team 0's warps
       float M = -INFINITY, l = 0.0f, v = 0.0f;
-      for (int k = 0; k < nteam; ++k) M = fmaxf(M, s_m[k * team + r / kKdTile][r % kKdTile]);
+      for (int k = 0; k < nteam; ++k) M = fmaxf(M, s_m[k * team * RT + x0]);
       for (int k = 0; k < nteam; ++k) {
-        const int x = k * team + r / kKdTile;
-        const float mx = s_m[x][r % kKdTile];
-        const float e = mx > -INFINITY ? exp2f(mx - M) : s_l[x][r % kKdTile] == 0.0f ? 0.0f : 1.0f;
-        l += e * s_l[x][r % kKdTile];
-        v += e * s_acc[(x * kKdTile + r % kKdTile) * D + c];
+        const int x = k * team * RT + x0;
+        const float e = s_m[x] > -INFINITY ? exp2f(s_m[x] - M) : s_l[x] == 0.0f ? 0.0f : 1.0f;
+        l += e * s_l[x];
+        v += e * s_acc[x * D + c];
       }
       if (done) {
-        if (r / a.G < nq) kd_store<D>(a, b, g, r, c, M, l, v);
+        if (r / a.G < sg.nq) kd_store<D>(a, sg.b, sg.g, r, c, M, l, v);
       } else {
         if (c == 0) { part[r * (D + 2)] = M; part[r * (D + 2) + 1] = l; }
         part[r * (D + 2) + 2 + c] = v;
       }
     }
-    u += cnt;
+    __syncthreads();
+    u += sg.cnt;
+  }
+  if (dead) {
+    // copies that are still on their way land before the CTA leaves
+    if (producer)
+      for (int i = max(0, issued - depth); i < issued; ++i) mbar_wait(full + 8 * (i % depth), (i / depth) & 1);
+    if (lane == 0) atomicOr(a.status, 4u);
   }
 }
 
@@ -350,15 +873,19 @@ size_t kd_workspace(const csa_shape* s, int T) {
   return 256 + (size_t)2 * kd_ctas(s) * R * (s->d + 2) * 4;
 }
 
-template <int D, typename E>
-cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, int ncta, cudaStream_t st) {
-  const int Rp = (a.T * a.G + kKdTile - 1) / kKdTile * kKdTile;
-  const int smem = (Rp + kKdWarps * kKdTile) * D * 4;
-  const cudaError_t e = cudaFuncSetAttribute(kv4_decode_kernel<D, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <int D, int RT, typename E>
+cudaError_t launch_kv4_decode_t(const Kv4DecodeArgs& a, int ncta, cudaStream_t st) {
+  const int smem = KdLayout<D, RT>::smem(a.T * a.G);
+  const cudaError_t e =
+      cudaFuncSetAttribute(kv4_decode_kernel<D, RT, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  launch_pdl(kv4_decode_kernel<D, E>, dim3(ncta), dim3(kKdWarps * 32), smem, st, a);
+  launch_pdl(kv4_decode_kernel<D, RT, E>, dim3(ncta), dim3(kKdWarps * 32), smem, st, a);
   if (ncta > 1) launch_pdl(kv4_join_kernel<D>, dim3(ncta - 1), dim3(256), 0, st, a, ncta);
   return cudaGetLastError();
+}
+template <int D, typename E>
+cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, int ncta, cudaStream_t st) {
+  return a.T * a.G <= 4 ? launch_kv4_decode_t<D, 4, E>(a, ncta, st) : launch_kv4_decode_t<D, 8, E>(a, ncta, st);
 }
 
 bool kd_args_ok(const csa_shape* s, int T, csa_status* st) {
