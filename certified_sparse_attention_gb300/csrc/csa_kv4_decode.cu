@@ -60,11 +60,12 @@ struct Kv4DecodeArgs {
   float* part;          // [2 * CTAs][rows][D + 2]: m, l, acc[D]
   int64_t n_max, nblk_max;
   int B, T, Hq, Hkv, G;
+  int stages;           // blocks in the ring
   float rs;             // log2(e) / sqrt(d): scores in units of log 2
 };
 
-constexpr int kKdWarps = 8;
-constexpr int kKdStages = 16;     // blocks in the rings of a CTA, over all teams
+constexpr int kKdWarps = 12;
+constexpr int kKdMaxStages = 24;  // blocks in the ring of a CTA
 
 // one block in shared memory.  The bounds are copied in eight pieces, 16
 // bytes apart, so that the four channel ranges of a warp's lanes start in
@@ -225,45 +226,71 @@ __device__ __forceinline__ KdSeg kd_seg(const Kv4DecodeArgs& a, const int64_t* s
   return s;
 }
 
-// The order in which a team takes blocks, over all items of the CTA.
+// Walks the CTA's tensor-core blocks, numbered 0, 1, ... over all its items.
 struct KdCursor {
-  int64_t u, u1, x, nfast, at0, cnt;
-  int step, first;
+  int64_t u, u1, cnt, at0;
+  int lo, hi;             // numbers [lo, hi) lie in the item at hand
   __device__ __forceinline__ void open(const Kv4DecodeArgs& a, const int64_t* s_pref) {
     const KdSeg s = kd_seg(a, s_pref, u, u1);
-    nfast = s.nfast; cnt = s.cnt; at0 = s.bg * a.nblk_max + s.blk0; x = first;
+    cnt = s.cnt;
+    at0 = s.bg * a.nblk_max + s.blk0;
+    lo = hi;
+    hi += (int)s.nfast;
   }
-  // the next block's index in the cache, or -1
-  __device__ __forceinline__ int64_t next(const Kv4DecodeArgs& a, const int64_t* s_pref) {
-    while (u < u1) {
-      if (x < nfast) {
-        const int64_t at = at0 + x;
-        x += step;
-        return at;
-      }
+  // place of block `i` in the cache (i never decreases), or -1 past the end
+  __device__ __forceinline__ int64_t find(const Kv4DecodeArgs& a, const int64_t* s_pref, int i) {
+    while (u < u1 && i >= hi) {
       u += cnt;
       if (u < u1) open(a, s_pref);
     }
-    return -1;
+    return u < u1 ? at0 + (i - lo) : -1;
   }
 };
 
-__device__ __forceinline__ void bulk_copy(unsigned dst, const void* src, unsigned bytes, unsigned bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
+// The copies that bring a block: one by each of the lanes 0 .. 10.
 template <int D>
-__device__ __forceinline__ void kd_load(const csa_kv4& c, int64_t at, unsigned stage, unsigned bar) {
-  using St = KdStage<D>;
-  mbar_expect_tx(bar, St::tx);
-  bulk_copy(stage + St::K, c.K4 + at * (kBlock * D / 2), kBlock * D / 2, bar);
-  bulk_copy(stage + St::V, c.V4 + at * (kBlock * D / 2), kBlock * D / 2, bar);
-  bulk_copy(stage + St::S, c.vscale + at * kBlock * 2, kBlock * 8, bar);
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    bulk_copy(stage + St::B + i * St::PITCH, c.bounds + at * 2 * D + i * (D / 4), St::PIECE, bar);
+struct KdCopy {
+  const uint8_t* src;
+  unsigned step, dst, bytes;
+  __device__ __forceinline__ KdCopy(const csa_kv4& c, int lane) {
+    using St = KdStage<D>;
+    const int piece = max(0, lane - 3);
+    src = lane == 0 ? c.K4 : lane == 1 ? c.V4
+        : lane == 2 ? reinterpret_cast<const uint8_t*>(c.vscale)
+                    : reinterpret_cast<const uint8_t*>(c.bounds) + piece * St::PIECE;
+    step = lane < 2 ? kBlock * D / 2 : lane == 2 ? kBlock * 8 : 8 * D;
+    dst = lane == 0 ? St::K : lane == 1 ? St::V : lane == 2 ? St::S : St::B + piece * St::PITCH;
+    bytes = lane < 2 ? kBlock * D / 2 : lane == 2 ? kBlock * 8 : St::PIECE;
+  }
+  // sends for block number i, at place `at` of the cache; *sent tells whoever
+  // waits for it that the barrier's phase is the block's own
+  __device__ __forceinline__ void issue(int lane, int i, int64_t at, unsigned stage, unsigned bar, int* sent) const {
+    if (lane == 0) {
+      mbar_expect_tx(bar, KdStage<D>::tx);
+      __threadfence_block();
+      *(volatile int*)sent = i;
+    }
+    __syncwarp();
+    if (lane < 11)
+      asm volatile(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(stage + dst),
+          "l"(src + at * step), "r"(bytes), "r"(bar)
+          : "memory");
+  }
+};
+
+// Waits until block i has been sent for into its slot, then for its bytes.
+// (The barrier alone does not do: its parity repeats every second round, and
+// a team may be two rounds ahead of the one that frees the slot.)  False
+// after kWaitNs.
+__device__ __forceinline__ bool kd_wait(const int* sent, int i, unsigned bar, unsigned parity) {
+  unsigned long long t0 = 0;
+  for (unsigned it = 0; *(const volatile int*)sent != i; ++it) {
+    if (it == 0) t0 = global_ns();
+    else if ((it & 63u) == 0u && global_ns() - t0 > kWaitNs) return false;
+  }
+  __threadfence_block();
+  return mbar_wait(bar, parity);
 }
 
 // ------------------------------------------------------ tensor-core blocks
@@ -296,8 +323,14 @@ __device__ __forceinline__ float pow2i(int k) { return __int_as_float((127 + k) 
 __device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
 __device__ __forceinline__ float ex2(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// the pair (x low, y high) in half precision, truncated
+__device__ __forceinline__ unsigned half_pair_rz(float x, float y) {
+  unsigned r;
+  asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  return r;
 }
 
 // Nibbles of a half word in bits 3..6 and 7..10: n 2^-21 and n 2^-17 (bit 10
@@ -318,7 +351,8 @@ struct KdFast {
   float q[D / 4];
   float qsc;
   float csA, csB;         // kKeyUnit / qsc of rows ra, ra + 1
-  float mA, mB, lA, lB, omA, omB;
+  float rA, rB;           // reference (running maximum, or up to 1 below it)
+  float lA, lB, omA, omB;
   float sv;               // scale of p_t Delta_t, a power of two
   float o[D / 16][4];     // channels 16 i + gid (+ 8) x operand columns 2 tid, 2 tid + 1
   bool fresh;
@@ -332,8 +366,7 @@ __device__ __forceinline__ void kd_fast_init(KdFast<D, RT>& f, const float* s_q,
   for (int i = 0; i < D / 4; ++i) f.q[i] = r < rows ? s_q[r * D + tid * (D / 4) + i] * (i & 1 ? 0.0625f : 1.0f) : 0.0f;
   f.qsc = 1.0f;
   f.csA = f.csB = kKeyUnit;
-  f.mA = f.mB = -INFINITY;
-  f.lA = f.lB = f.omA = f.omB = 0.0f;
+  f.rA = f.rB = f.lA = f.lB = f.omA = f.omB = 0.0f;
   f.sv = 1.0f;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) f.o[i][0] = f.o[i][1] = f.o[i][2] = f.o[i][3] = 0.0f;
@@ -396,19 +429,19 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
   qm += __shfl_xor_sync(0xffffffffu, qm, 1);
   qm += __shfl_xor_sync(0xffffffffu, qm, 2);
   if (RT == 4) qm += __shfl_xor_sync(0xffffffffu, qm, 16);
-  const float qmA = __shfl_sync(0xffffffffu, qm, 4 * ra), qmB = __shfl_sync(0xffffffffu, qm, 4 * ra + 4);
+  const float sA = __shfl_sync(0xffffffffu, qm, 4 * ra) - f.rA, sB = __shfl_sync(0xffffffffu, qm, 4 * ra + 4) - f.rB;
 
-  // the operand: column gid, channel pairs (8 w + 0, 4), (1, 5), (2, 6), (3, 7)
+  // the operand: column gid, channel pairs (8 w + 0, 4), (1, 5), (2, 6), (3,
+  // 7); high part = the leading 11 bits, low part = the rest
   unsigned bq[HL][NW][4];
+  const unsigned cut = RT == 8 || gid >= 4 ? 0xffffe000u : 0u;
 #pragma unroll
   for (int w = 0; w < NW; ++w)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float u = x[8 * w + e], v = x[8 * w + e + 4];
-      const unsigned hi = half_pair(u, v);
-      const unsigned lo = half_rest(u, v, hi);
-      if (RT == 8) { bq[0][w][e] = hi; bq[HL - 1][w][e] = lo; }
-      else bq[0][w][e] = gid >= 4 ? lo : hi;
+      if (RT == 8) bq[0][w][e] = half_pair_rz(u, v);
+      bq[HL - 1][w][e] = half_pair_rz(u - __uint_as_float(__float_as_uint(u) & cut), v - __uint_as_float(__float_as_uint(v) & cut));
     }
 
   // scores of the four tiles of 16 tokens
@@ -425,38 +458,36 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
       const uint2 u = *reinterpret_cast<const uint2*>(kr), v = *reinterpret_cast<const uint2*>(kr + 8 * (D / 2));
       k0[0] = u.x; k0[1] = u.y; k1[0] = v.x; k1[1] = v.y;
     }
-    // (matrix instructions truncate their sums: short chains from zero, the
-    // low parts first, and the rest of the sum in rounded additions)
-    float t[2][4] = {};
+    // (matrix instructions truncate their sums: chains start from zero, with
+    // the low parts, and sum_c q_c m_c is added in float32 afterwards)
+    s[mt][0] = s[mt][1] = s[mt][2] = s[mt][3] = 0.0f;
 #pragma unroll
     for (int h = HL - 1; h >= 0; --h)
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
         const unsigned g0 = k0[w] << 3, g1 = k1[w] << 3, h0 = k0[w] >> 5, h1 = k1[w] >> 5;
-        mma_f16(t[w & 1], g0 & kNibA, g1 & kNibA, g0 & kNibB, g1 & kNibB, bq[h][w][0], bq[h][w][1]);
-        mma_f16(t[w & 1], h0 & kNibA, h1 & kNibA, h0 & kNibB, h1 & kNibB, bq[h][w][2], bq[h][w][3]);
+        mma_f16(s[mt], g0 & kNibA, g1 & kNibA, g0 & kNibB, g1 & kNibB, bq[h][w][0], bq[h][w][1]);
+        mma_f16(s[mt], h0 & kNibA, h1 & kNibA, h0 & kNibB, h1 & kNibB, bq[h][w][2], bq[h][w][3]);
       }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[mt][i] = t[0][i] + t[1][i];
   }
   // RT = 4: add the two parts; afterwards the lane has token 16 mt + gid (+ 8
   // in the upper lanes), rows ra, ra + 1, in s[mt][0], s[mt][1].
   // RT = 8: tokens gid and gid + 8 in s[mt][0..1] and s[mt][2..3].
   constexpr int TK = RT == 8 ? 2 : 1;    // tokens of a tile in a lane
-  float big = -INFINITY;
+  float big = -INFINITY;                 // (scores are relative to rA, rB)
 #pragma unroll
   for (int mt = 0; mt < 4; ++mt) {
     if (RT == 4) {
       const float g0 = __shfl_xor_sync(0xffffffffu, upper ? s[mt][0] : s[mt][2], 2);
       const float g1 = __shfl_xor_sync(0xffffffffu, upper ? s[mt][1] : s[mt][3], 2);
-      s[mt][0] = fmaf((upper ? s[mt][2] : s[mt][0]) + g0, f.csA, qmA);
-      s[mt][1] = fmaf((upper ? s[mt][3] : s[mt][1]) + g1, f.csB, qmB);
+      s[mt][0] = fmaf((upper ? s[mt][2] : s[mt][0]) + g0, f.csA, sA);
+      s[mt][1] = fmaf((upper ? s[mt][3] : s[mt][1]) + g1, f.csB, sB);
     } else {
-      s[mt][0] = fmaf(s[mt][0], f.csA, qmA); s[mt][1] = fmaf(s[mt][1], f.csB, qmB);
-      s[mt][2] = fmaf(s[mt][2], f.csA, qmA); s[mt][3] = fmaf(s[mt][3], f.csB, qmB);
+      s[mt][0] = fmaf(s[mt][0], f.csA, sA); s[mt][1] = fmaf(s[mt][1], f.csB, sB);
+      s[mt][2] = fmaf(s[mt][2], f.csA, sA); s[mt][3] = fmaf(s[mt][3], f.csB, sB);
     }
 #pragma unroll
-    for (int k = 0; k < TK; ++k) big = fmaxf(big, fmaxf(s[mt][2 * k] - f.mA, s[mt][2 * k + 1] - f.mB));
+    for (int k = 0; k < TK; ++k) big = fmaxf(big, fmaxf(s[mt][2 * k], s[mt][2 * k + 1]));
   }
   // token scales
   float2 sc[4][TK];
@@ -492,15 +523,17 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
     }
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, m));
-    const float nA = fmaxf(f.mA, xA), nB = fmaxf(f.mB, xB);
+    // the references move up by dA, dB (the first block: to its maximum)
+    const float dA = f.fresh ? (xA > -INFINITY ? xA : 0.0f) : fmaxf(xA, 0.0f);
+    const float dB = f.fresh ? (xB > -INFINITY ? xB : 0.0f) : fmaxf(xB, 0.0f);
     float up = 1.0f;
     if (t > 0.0f && (f.fresh || t * f.sv > 16384.0f)) {
       const float to = pow2i(min(max(13 - exponent(t), -100), 100));   // Delta sv in [2^13, 2^14)
       up = f.sv > 0.0f ? to / f.sv : 1.0f;
       f.sv = to;
     }
-    const float eA = f.mA > -INFINITY ? ex2(f.mA - nA) : 0.0f, eB = f.mB > -INFINITY ? ex2(f.mB - nB) : 0.0f;
     if (!f.fresh) {
+      const float eA = ex2(-dA), eB = ex2(-dB);
       f.lA *= eA; f.lB *= eB;
       f.omA *= eA; f.omB *= eB;
 #pragma unroll
@@ -509,10 +542,13 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
         f.o[i][2] *= eA * up; f.o[i][3] *= eB * up;
       }
     }
-    f.mA = nA; f.mB = nB;
+    f.rA += dA; f.rB += dB;
     f.fresh = false;
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int k = 0; k < TK; ++k) { s[mt][2 * k] -= dA; s[mt][2 * k + 1] -= dB; }
   }
-  const float rA = f.mA > -INFINITY ? f.mA : 0.0f, rB = f.mB > -INFINITY ? f.mB : 0.0f;
   // Weights and the second operand: column gid, token pairs.  The tokens
   // gid + 8 of a tile enter as 15 - n with the opposite sign, and
   // with m + 15 Delta for m: the sums of codes, all positive, would outgrow
@@ -525,7 +561,7 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
     unsigned hi[TK], lo[TK];
 #pragma unroll
     for (int k = 0; k < TK; ++k) {
-      const float pA = ex2(s[mt][2 * k] - rA), pB = ex2(s[mt][2 * k + 1] - rB);
+      const float pA = ex2(s[mt][2 * k]), pB = ex2(s[mt][2 * k + 1]);
       f.lA += pA; f.lB += pB;
       const float m = fmaf(sc[mt][k].y, RT == 8 ? (k ? 15.0f : 0.0f) : upper ? 15.0f : 0.0f, sc[mt][k].x);
       omA = fmaf(pA, m, omA);
@@ -590,7 +626,7 @@ __device__ __forceinline__ void kd_fast_store(KdFast<D, RT>& f, float* s_m, floa
     f.omB += __shfl_xor_sync(0xffffffffu, f.omB, m);
   }
   if (gid == 0 && !upper) {
-    s_m[ra] = f.mA; s_m[ra + 1] = f.mB;
+    s_m[ra] = f.fresh ? -INFINITY : f.rA; s_m[ra + 1] = f.fresh ? -INFINITY : f.rB;
     s_l[ra] = f.lA; s_l[ra + 1] = f.lB;
   }
   const float back = kValueUnit / f.sv;
@@ -612,15 +648,16 @@ __device__ __forceinline__ void kd_fast_store(KdFast<D, RT>& f, float* s_m, floa
   }
 }
 
-// shared memory: rings, mbarriers (full and empty), q rows, warp sums
+// shared memory: mbarriers (full and empty), warp sums, q rows, the ring
 template <int D, int RT>
 struct KdLayout {
-  static constexpr int bars = kKdStages * KdStage<D>::bytes;
-  static constexpr int m = bars + 2 * kKdStages * 8;
+  static constexpr int bars = 0;
+  static constexpr int sent = 2 * kKdMaxStages * 8;
+  static constexpr int m = sent + kKdMaxStages * 4;
   static constexpr int l = m + kKdWarps * RT * 4;
   static constexpr int acc = l + kKdWarps * RT * 4;
   static constexpr int q = acc + kKdWarps * RT * D * 4;
-  static int smem(int rows) { return q + (rows + RT - 1) / RT * RT * D * 4; }
+  static int ring(int rows) { return q + (rows + RT - 1) / RT * RT * D * 4; }
 };
 
 template <int D, int RT, typename E>
@@ -638,19 +675,20 @@ __global__ void __launch_bounds__(kKdWarps * 32, 1) kv4_decode_kernel(const Kv4D
   float* s_q = reinterpret_cast<float*>(kd_sm + Lt::q);        // [rows, padded][D]
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int R = a.T * a.G, Rp = (R + RT - 1) / RT * RT;
-  // teams: warps that share a block, one tile of rows each, and a ring of
-  // kKdStages / nteam stages
+  // teams: warps that share a block, one tile of rows each; with team = 8
+  // four warps are left over
   const int ntile = Rp / RT;
   const int team = ntile <= 1 ? 1 : ntile <= 2 ? 2 : ntile <= 4 ? 4 : 8;
   const int nteam = kKdWarps / team, my_team = w / team, tile = w % team;
-  const int rows = min(RT, R - tile * RT);                // <= 0: a warp with no rows
-  const int depth = kKdStages / nteam;
-  const unsigned base = smem_u32(kd_sm);
-  const unsigned ring = base + my_team * depth * St::bytes;
-  const unsigned full = base + Lt::bars + my_team * depth * 8, empty = full + kKdStages * 8;
-  if (tid < kKdStages) {
-    mbar_init(base + Lt::bars + 8 * tid, 1);
-    mbar_init(base + Lt::bars + 8 * (kKdStages + tid), team);
+  const bool active = my_team < nteam;
+  const int rows = active ? min(RT, R - tile * RT) : 0;    // <= 0: a warp with no rows
+  const unsigned full = smem_u32(kd_sm) + Lt::bars, empty = full + kKdMaxStages * 8;
+  int* s_sent = reinterpret_cast<int*>(kd_sm + Lt::sent);
+  uint8_t* ring = kd_sm + Lt::q + Rp * D * 4;
+  if (tid < a.stages) {
+    mbar_init(full + 8 * tid, 1);
+    mbar_init(empty + 8 * tid, team);
+    s_sent[tid] = -1;
     fence_barrier_init();
   }
   kd_prefix(a, s_pref);
@@ -660,18 +698,25 @@ __global__ void __launch_bounds__(kKdWarps * 32, 1) kv4_decode_kernel(const Kv4D
   const int64_t total = s_pref[kMaxB];
   const int64_t per = (total + gridDim.x - 1) / gridDim.x;
   const int64_t u0 = (int64_t)blockIdx.x * per, u1 = min(total, u0 + per);
+  // Block i of the CTA sits in slot i % stages of the ring and is taken by
+  // team i % nteam, whose first warp, once the block is used, sends for
+  // block i + stages into the same slot.
+  const bool leader = active && tile == 0;
+  const KdCopy<D> copy(a.c, lane);
   KdCursor cur;
-  cur.u = u0; cur.u1 = u1; cur.step = nteam; cur.first = my_team;
-  const bool producer = tile == 0 && lane == 0;
-  int issued = 0, used = 0;
-  if (producer && u0 < u1) {
+  cur.u = u0; cur.u1 = u1; cur.lo = cur.hi = 0; cur.cnt = 0; cur.at0 = 0;
+  int next = my_team;               // (leaders) number of the next block to send for
+  int last = -1;                    // number of the last block sent for
+  if (leader && u0 < u1) {
     cur.open(a, s_pref);
-    for (; issued < depth; ++issued) {
-      const int64_t at = cur.next(a, s_pref);
+    for (; next < a.stages; next += nteam) {
+      const int64_t at = cur.find(a, s_pref, next);
       if (at < 0) break;
-      kd_load<D>(a.c, at, ring + issued * St::bytes, full + 8 * issued);
+      copy.issue(lane, next, at, smem_u32(ring) + next * St::bytes, full + 8 * next, s_sent + next);
+      last = next;
     }
   }
+  int base = 0;                     // number of the item's first block
   if (blockIdx.x == 0 && tid < 32) {
     bool bad = false;
     for (int b = lane; b < a.B; b += 32) {
@@ -703,25 +748,30 @@ __global__ void __launch_bounds__(kKdWarps * 32, 1) kv4_decode_kernel(const Kv4D
     {
       KdFast<D, RT> f;
       kd_fast_init<D, RT>(f, tile * RT < Rp ? q : s_q, rows);
-      for (int64_t x = my_team; x < sg.nfast; x += nteam) {
-        const int slot = used % depth;
-        if (!dead && !mbar_wait(full + 8 * slot, (used / depth) & 1)) dead = true;
-        if (rows > 0) kd_fast_block<D, RT>(f, kd_sm + (ring - base) + slot * St::bytes);
-        ++used;
+      // (block `i` is the team's own when i % nteam == my_team)
+      const int lead = (my_team + nteam - base % nteam) % nteam;
+      for (int i = base + lead; active && i < base + (int)sg.nfast; i += nteam) {
+        const int slot = i % a.stages, round = i / a.stages;
+        if (!dead && !kd_wait(s_sent + slot, i, full + 8 * slot, round & 1)) dead = true;
+        if (rows > 0) kd_fast_block<D, RT>(f, ring + slot * St::bytes);
         __syncwarp();
         if (team > 1 && lane == 0) mbar_arrive(empty + 8 * slot);
-        if (producer && !dead) {
-          const int64_t at = cur.next(a, s_pref);
+        dead = __any_sync(0xffffffffu, dead);
+        if (leader && !dead) {
+          const int64_t at = cur.find(a, s_pref, i + a.stages);
           if (at >= 0) {
-            if (team > 1 && !mbar_wait(empty + 8 * slot, ((used - 1) / depth) & 1)) dead = true;
-            if (!dead) kd_load<D>(a.c, at, ring + slot * St::bytes, full + 8 * slot);
-            ++issued;
+            if (team > 1 && !mbar_wait(empty + 8 * slot, round & 1)) dead = true;
+            dead = __any_sync(0xffffffffu, dead);
+            if (!dead) {
+              copy.issue(lane, i + a.stages, at, smem_u32(ring) + slot * St::bytes, full + 8 * slot, s_sent + slot);
+              last = i + a.stages;
+            }
           }
         }
-        dead = __any_sync(0xffffffffu, dead);
       }
       kd_fast_store<D, RT>(f, my_m, my_l, my_acc);
     }
+    base += (int)sg.nfast;
     if (rows > 0 && sg.nfast < sg.cnt) {
       // blocks that are seen in part, and the incomplete one, eight tokens
       // at a time: the state moves on to lanes that hold channels
@@ -816,9 +866,10 @@ __global__ void __launch_bounds__(kKdWarps * 32, 1) kv4_decode_kernel(const Kv4D
     u += sg.cnt;
   }
   if (dead) {
-    // copies that are still on their way land before the CTA leaves
-    if (producer)
-      for (int i = max(0, issued - depth); i < issued; ++i) mbar_wait(full + 8 * (i % depth), (i / depth) & 1);
+    // the copies that this warp sent for land before the CTA leaves
+    if (leader)
+      for (int i = max(my_team, last - a.stages / nteam * nteam); i <= last; i += nteam)
+        mbar_wait(full + 8 * (i % a.stages), (i / a.stages) & 1);
     if (lane == 0) atomicOr(a.status, 4u);
   }
 }
@@ -873,9 +924,14 @@ size_t kd_workspace(const csa_shape* s, int T) {
   return 256 + (size_t)2 * kd_ctas(s) * R * (s->d + 2) * 4;
 }
 
+// as many blocks in the ring as shared memory holds beside the rest
+constexpr int kKdSharedBytes = 232448 - 2048;    // (2 KB: static arrays)
 template <int D, int RT, typename E>
-cudaError_t launch_kv4_decode_t(const Kv4DecodeArgs& a, int ncta, cudaStream_t st) {
-  const int smem = KdLayout<D, RT>::smem(a.T * a.G);
+cudaError_t launch_kv4_decode_t(Kv4DecodeArgs a, int ncta, cudaStream_t st) {
+  const int rest = KdLayout<D, RT>::ring(a.T * a.G);
+  a.stages = (kKdSharedBytes - rest) / KdStage<D>::bytes;
+  if (a.stages > kKdMaxStages) a.stages = kKdMaxStages;
+  const int smem = rest + a.stages * KdStage<D>::bytes;
   const cudaError_t e =
       cudaFuncSetAttribute(kv4_decode_kernel<D, RT, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
