@@ -64,7 +64,8 @@ struct Kv4DecodeArgs {
   float rs;             // log2(e) / sqrt(d): scores in units of log 2
 };
 
-constexpr int kKdWarps = 12;
+// warps of a CTA, by the rows of a warp's tile: what the registers allow
+template <int RT> __host__ __device__ constexpr int kd_warps() { return RT == 4 ? 16 : 12; }
 constexpr int kKdMaxStages = 24;  // blocks in the ring of a CTA
 
 // one block in shared memory.  The bounds are copied in eight pieces, 16
@@ -141,6 +142,13 @@ __device__ __forceinline__ void kd_store(const Kv4DecodeArgs& a, int b, int g, i
   if (c == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
 }
 
+// The query rows of an item in shared memory: row r starts at r (D + 16), its
+// channels in four pieces 4 floats apart (bank offsets, as for the bounds).
+// They are log2(e) / sqrt(d) q times a power of two that puts the row's
+// largest at 2^11 .. 2^12 (undone by s_inv[r]), odd channels times 1/16 more:
+// their codes stand 16 times higher in the operand.
+template <int D> __device__ __forceinline__ constexpr int kd_q(int r, int c) { return r * (D + 16) + c + c / (D / 4) * 4; }
+
 template <int D, int RT>
 struct KdState {
   float m[RT], l[RT], acc[RT][D / 32];
@@ -152,18 +160,21 @@ struct KdState {
 // s_end[r]
 template <int D, int RT>
 __device__ __forceinline__ void kd_step(KdState<D, RT>& st, const float (&kv)[8][D / 32], const float (&vv)[8][D / 32],
-                                        const float* s_q, const int64_t* s_end, int64_t pos, int rows) {
+                                        const float* s_q, const float* s_inv, const int64_t* s_end, int64_t pos,
+                                        int rows) {
   constexpr int CPL = D / 32;
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     if (r >= rows) break;
-    float part[8];
+    float part[8], q[CPL];
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) q[c] = s_q[kd_q<D>(r, lane * CPL) + c] * (c & 1 ? 16.0f * s_inv[r] : s_inv[r]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float p[CPL];
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) p[c] = kv[i][c] * s_q[r * D + lane * CPL + c];
+      for (int c = 0; c < CPL; ++c) p[c] = kv[i][c] * q[c];
       part[i] = local_tree<CPL>(p);
     }
     float s = reduce8_rows(part);
@@ -340,18 +351,17 @@ constexpr unsigned kNibA = 0x00780078u, kNibB = 0x07800780u;
 constexpr float kKeyUnit = 2097152.0f, kValueUnit = 131072.0f;   // 2^21, 2^17
 
 // The state of a warp over the tensor-core blocks of an item.  Lane (gid =
-// lane / 4, tid = lane % 4) holds in q the D / 4 channels [tid D / 4, ...)
-// of query row gid % RT (RT = 4: lanes with gid >= 4 hold the same rows and
-// supply the low parts), times qsc, a power of two, and times 1/16 for odd
-// channels, whose codes stand 16 times higher in the operand.
-// Softmax state: rows ra, ra + 1 with ra = 2 (tid % (RT / 2)); the sums l are
-// over the lane's own tokens, om too (RT = 4: and those of lane ^ 2).
+// lane / 4, tid = lane % 4) works on query row gid % RT (RT = 4: lanes with
+// gid >= 4 have the same rows and supply the low parts) and its channels
+// [tid D / 4, (tid + 1) D / 4).  Softmax state: rows ra, ra + 1 with ra = 2
+// (tid % (RT / 2)); the sums l are over the lane's own tokens, om too (RT =
+// 4: and those of lane ^ 2).
 template <int D, int RT>
 struct KdFast {
-  float q[D / 4];
-  float qsc;
-  float csA, csB;         // kKeyUnit / qsc of rows ra, ra + 1
-  float rA, rB;           // reference (running maximum, or up to 1 below it)
+  float qinv;             // undoes the scale of the lane's row
+  float xs, most;         // scale of Delta_c, a power of two; Delta up to which it holds
+  float csA, csB;         // unit of the code sums of rows ra, ra + 1
+  float rA, rB;           // reference (running maximum, or up to 8 below it)
   float lA, lB, omA, omB;
   float sv;               // scale of p_t Delta_t, a power of two
   float o[D / 16][4];     // channels 16 i + gid (+ 8) x operand columns 2 tid, 2 tid + 1
@@ -359,13 +369,12 @@ struct KdFast {
 };
 
 template <int D, int RT>
-__device__ __forceinline__ void kd_fast_init(KdFast<D, RT>& f, const float* s_q, int rows) {
-  const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
-  const int r = gid % RT;
-#pragma unroll
-  for (int i = 0; i < D / 4; ++i) f.q[i] = r < rows ? s_q[r * D + tid * (D / 4) + i] * (i & 1 ? 0.0625f : 1.0f) : 0.0f;
-  f.qsc = 1.0f;
-  f.csA = f.csB = kKeyUnit;
+__device__ __forceinline__ void kd_fast_init(KdFast<D, RT>& f, const float* s_inv) {
+  const int lane = threadIdx.x & 31, gid = lane >> 2;
+  f.qinv = s_inv[gid % RT];
+  f.xs = 1.0f;
+  f.most = 0.0f;
+  f.csA = f.csB = 0.0f;
   f.rA = f.rB = f.lA = f.lB = f.omA = f.omB = 0.0f;
   f.sv = 1.0f;
 #pragma unroll
@@ -374,7 +383,7 @@ __device__ __forceinline__ void kd_fast_init(KdFast<D, RT>& f, const float* s_q,
 }
 
 template <int D, int RT>
-__device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* st) {
+__device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* st, const float* s_q) {
   using St = KdStage<D>;
   constexpr int NC = D / 4;        // channels of a lane
   constexpr int NW = D / 32;       // code words of a lane in a key row
@@ -384,48 +393,55 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
   const int ra = 2 * (tid % (RT / 2));
 
   // q_c Delta_c, and sum_c q_c m_c
+  const float* sq = s_q + kd_q<D>(gid % RT, tid * NC);
   const float* sm = reinterpret_cast<const float*>(st + St::B + tid * St::PITCH);
   const float* sd = reinterpret_cast<const float*>(st + St::B + (4 + tid) * St::PITCH);
-  float x[NC];
-  float top = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NC; i += 4) {
-    const float4 dl = *reinterpret_cast<const float4*>(sd + i);
-    x[i] = f.q[i] * dl.x; x[i + 1] = f.q[i + 1] * dl.y; x[i + 2] = f.q[i + 2] * dl.z; x[i + 3] = f.q[i + 3] * dl.w;
-    top = fmaxf(fmaxf(top, fmaxf(fabsf(x[i]), fabsf(x[i + 1]))), fmaxf(fabsf(x[i + 2]), fabsf(x[i + 3])));
+  // Keep q_c Delta_c (q below 2^12) below 2^15: steps between 2^-8 and 2^3
+  // need no scale of their own.  (Steps that get smaller later keep an
+  // absolute error of the score that only shrinks.)  The lanes check 4 (2)
+  // steps each.
+  float top;
+  if (D == 128) {
+    const float4 dl = *reinterpret_cast<const float4*>(st + St::B + (4 + (lane >> 3)) * St::PITCH + (lane & 7) * 16);
+    top = fmaxf(fmaxf(dl.x, dl.y), fmaxf(dl.z, dl.w));
+  } else {
+    const float2 dl = *reinterpret_cast<const float2*>(st + St::B + (4 + (lane >> 3)) * St::PITCH + (lane & 7) * 8);
+    top = fmaxf(dl.x, dl.y);
   }
-  // keep the largest of a row below 2^15 (the first block sets it to 2^12 ..
-  // 2^13; smaller ones later keep an absolute error that only shrinks)
-  if (__any_sync(0xffffffffu, f.fresh || top >= 32768.0f)) {
+  if (__any_sync(0xffffffffu, f.fresh || top >= f.most)) {
     float t = top < INFINITY ? top : 0.0f;
-    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-    if (t > 0.0f && (f.fresh || t >= 32768.0f)) {
-      const int have = exponent(f.qsc);
-      const int k = min(max(have + 12 - exponent(t), -100), 100) - have;
-      const float up = ldexpf(1.0f, k);
-      f.qsc *= up;
 #pragma unroll
-      for (int i = 0; i < NC; ++i) { f.q[i] *= up; x[i] *= up; }
+    for (int m = 1; m < 32; m <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, m));
+    if (t > 0.0f && (f.fresh || t >= f.most)) {
+      const int e = exponent(t);
+      f.xs = e >= -8 && e < 3 ? 1.0f : pow2i(min(max(-e, -100), 100));
+      f.most = 8.0f / f.xs;
     }
-    const float c = kKeyUnit / f.qsc;
+    const float c = kKeyUnit * f.qinv / f.xs;
     f.csA = __shfl_sync(0xffffffffu, c, 4 * ra);
     f.csB = __shfl_sync(0xffffffffu, c, 4 * ra + 4);
   }
-  float qm = 0.0f, qm1 = 0.0f;
-  // (odd channels carry 1/16)
+  float x[NC];
 #pragma unroll
   for (int i = 0; i < NC; i += 4) {
-    if (RT == 4 && (i >= NC / 2) != 0) continue;
-    const float4 mn = *reinterpret_cast<const float4*>(sm + (RT == 4 ? (gid >> 2) * (NC / 2) : 0) + i);
-    const float q0 = RT == 4 ? (gid >> 2 ? f.q[i + NC / 2] : f.q[i]) : f.q[i];
-    const float q1 = RT == 4 ? (gid >> 2 ? f.q[i + 1 + NC / 2] : f.q[i + 1]) : f.q[i + 1];
-    const float q2 = RT == 4 ? (gid >> 2 ? f.q[i + 2 + NC / 2] : f.q[i + 2]) : f.q[i + 2];
-    const float q3 = RT == 4 ? (gid >> 2 ? f.q[i + 3 + NC / 2] : f.q[i + 3]) : f.q[i + 3];
-    qm = fmaf(q0, mn.x, qm); qm1 = fmaf(q1, mn.y, qm1);
-    qm = fmaf(q2, mn.z, qm); qm1 = fmaf(q3, mn.w, qm1);
+    const float4 q = *reinterpret_cast<const float4*>(sq + i), dl = *reinterpret_cast<const float4*>(sd + i);
+    x[i] = q.x * dl.x; x[i + 1] = q.y * dl.y; x[i + 2] = q.z * dl.z; x[i + 3] = q.w * dl.w;
   }
-  qm = fmaf(qm1, 16.0f, qm) * (1.0f / f.qsc);           // (qsc: a power of two)
+  if (f.xs != 1.0f) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) x[i] *= f.xs;
+  }
+  // (RT = 4: the lanes gid and gid + 4 take half of the channels each)
+  constexpr int QM = RT == 4 ? NC / 2 : NC;
+  const int half = RT == 4 ? (gid >> 2) * QM : 0;
+  float qm = 0.0f, qm1 = 0.0f;
+#pragma unroll
+  for (int i = 0; i < QM; i += 4) {
+    const float4 q = *reinterpret_cast<const float4*>(sq + half + i), mn = *reinterpret_cast<const float4*>(sm + half + i);
+    qm = fmaf(q.x, mn.x, qm); qm1 = fmaf(q.y, mn.y, qm1);
+    qm = fmaf(q.z, mn.z, qm); qm1 = fmaf(q.w, mn.w, qm1);
+  }
+  qm = fmaf(qm1, 16.0f, qm) * f.qinv;
   qm += __shfl_xor_sync(0xffffffffu, qm, 1);
   qm += __shfl_xor_sync(0xffffffffu, qm, 2);
   if (RT == 4) qm += __shfl_xor_sync(0xffffffffu, qm, 16);
@@ -444,31 +460,40 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
       bq[HL - 1][w][e] = half_pair_rz(u - __uint_as_float(__float_as_uint(u) & cut), v - __uint_as_float(__float_as_uint(v) & cut));
     }
 
-  // scores of the four tiles of 16 tokens
+  // scores of the four tiles of 16 tokens, two at a time (matrix instructions
+  // truncate their sums: chains start from zero, each part its own, and sum_c
+  // q_c m_c is added in float32)
   float s[4][4];
 #pragma unroll
-  for (int mt = 0; mt < 4; ++mt) {
-    unsigned k0[NW], k1[NW];
-    const uint8_t* kr = st + St::K + (16 * mt + gid) * (D / 2) + tid * (D / 8);
-    if (D == 128) {
-      const uint4 u = *reinterpret_cast<const uint4*>(kr), v = *reinterpret_cast<const uint4*>(kr + 8 * (D / 2));
-      k0[0] = u.x; k0[1] = u.y; k0[NW - 2] = u.z; k0[NW - 1] = u.w;
-      k1[0] = v.x; k1[1] = v.y; k1[NW - 2] = v.z; k1[NW - 1] = v.w;
-    } else {
-      const uint2 u = *reinterpret_cast<const uint2*>(kr), v = *reinterpret_cast<const uint2*>(kr + 8 * (D / 2));
-      k0[0] = u.x; k0[1] = u.y; k1[0] = v.x; k1[1] = v.y;
-    }
-    // (matrix instructions truncate their sums: chains start from zero, with
-    // the low parts, and sum_c q_c m_c is added in float32 afterwards)
-    s[mt][0] = s[mt][1] = s[mt][2] = s[mt][3] = 0.0f;
+  for (int pr = 0; pr < 2; ++pr) {
+    unsigned k[4][NW];      // rows gid, gid + 8 of tile 2 pr, then of the next
 #pragma unroll
-    for (int h = HL - 1; h >= 0; --h)
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        const unsigned g0 = k0[w] << 3, g1 = k1[w] << 3, h0 = k0[w] >> 5, h1 = k1[w] >> 5;
-        mma_f16(s[mt], g0 & kNibA, g1 & kNibA, g0 & kNibB, g1 & kNibB, bq[h][w][0], bq[h][w][1]);
-        mma_f16(s[mt], h0 & kNibA, h1 & kNibA, h0 & kNibB, h1 & kNibB, bq[h][w][2], bq[h][w][3]);
+    for (int j = 0; j < 4; ++j) {
+      const uint8_t* kr = st + St::K + (32 * pr + 8 * j + gid) * (D / 2) + tid * (D / 8);
+      if (D == 128) {
+        const uint4 u = *reinterpret_cast<const uint4*>(kr);
+        k[j][0] = u.x; k[j][1] = u.y; k[j][NW - 2] = u.z; k[j][NW - 1] = u.w;
+      } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(kr);
+        k[j][0] = u.x; k[j][1] = u.y;
       }
+    }
+    float t[2][HL][4] = {};
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+#pragma unroll
+      for (int z = 0; z < 2; ++z)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const unsigned a = z ? k[2 * y][w] >> 5 : k[2 * y][w] << 3, b = z ? k[2 * y + 1][w] >> 5 : k[2 * y + 1][w] << 3;
+#pragma unroll
+          for (int h = 0; h < HL; ++h)
+            mma_f16(t[y][h], a & kNibA, b & kNibA, a & kNibB, b & kNibB, bq[h][w][2 * z], bq[h][w][2 * z + 1]);
+        }
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[2 * pr + y][e] = RT == 8 ? t[y][0][e] + t[y][HL - 1][e] : t[y][0][e];
   }
   // RT = 4: add the two parts; afterwards the lane has token 16 mt + gid (+ 8
   // in the upper lanes), rows ra, ra + 1, in s[mt][0], s[mt][1].
@@ -499,10 +524,10 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
       sc[mt][k] = *reinterpret_cast<const float2*>(st + St::S + (16 * mt + gid + (RT == 8 ? 8 * k : upper ? 8 : 0)) * 8);
       wide = fmaxf(wide, sc[mt][k].y);
     }
-  // The running maximum moves only when a score exceeds it by more than one
-  // (then a weight would pass 2), and the value scale only when Delta_t does
-  // not fit: both are rare after the first blocks.
-  if (__any_sync(0xffffffffu, f.fresh || !(big <= 1.0f) || wide * f.sv > 16384.0f)) {
+  // The reference moves only when a score exceeds it by more than 8 (weights
+  // up to 2^8), and the value scale only when Delta_t does not fit (Delta_t sv
+  // up to 2^6): both are rare after the first block.
+  if (__any_sync(0xffffffffu, f.fresh || big > 8.0f || wide * f.sv > 64.0f)) {
     float xA = -INFINITY, xB = -INFINITY;
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
@@ -527,8 +552,8 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
     const float dA = f.fresh ? (xA > -INFINITY ? xA : 0.0f) : fmaxf(xA, 0.0f);
     const float dB = f.fresh ? (xB > -INFINITY ? xB : 0.0f) : fmaxf(xB, 0.0f);
     float up = 1.0f;
-    if (t > 0.0f && (f.fresh || t * f.sv > 16384.0f)) {
-      const float to = pow2i(min(max(13 - exponent(t), -100), 100));   // Delta sv in [2^13, 2^14)
+    if (t > 0.0f && (f.fresh || t * f.sv > 64.0f)) {
+      const float to = pow2i(min(max(5 - exponent(t), -100), 100));   // Delta sv in [2^5, 2^6)
       up = f.sv > 0.0f ? to / f.sv : 1.0f;
       f.sv = to;
     }
@@ -589,22 +614,29 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
   f.omA += omA;
   f.omB += omB;
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) {
-    const uint8_t* vr = st + St::V + (16 * i + gid) * (kBlock / 2) + tid * 8;
-    const uint2 v0 = *reinterpret_cast<const uint2*>(vr), v1 = *reinterpret_cast<const uint2*>(vr + 8 * (kBlock / 2));
-    float t[4] = {};
+  for (int i = 0; i < D / 16; i += 2) {
+    uint2 v[4];             // channels gid, gid + 8 of tile i, then of the next
 #pragma unroll
-    for (int h = HL - 1; h >= 0; --h)
+    for (int j = 0; j < 4; ++j)
+      v[j] = *reinterpret_cast<const uint2*>(st + St::V + (16 * i + 8 * j + gid) * (kBlock / 2) + tid * 8);
+    float t[2][HL][4] = {};
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        const unsigned a = mt < 2 ? v0.x : v0.y, b = mt < 2 ? v1.x : v1.y;
-        if (mt & 1)
-          mma_f16(t, (a >> 1) & kNibB, (b >> 1) & kNibB, ~(a >> 5) & kNibB, ~(b >> 5) & kNibB, bp[h][mt][0], bp[h][mt][1]);
-        else
-          mma_f16(t, (a << 7) & kNibB, (b << 7) & kNibB, ~(a << 3) & kNibB, ~(b << 3) & kNibB, bp[h][mt][0], bp[h][mt][1]);
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const unsigned a = mt < 2 ? v[2 * y].x : v[2 * y].y, b = mt < 2 ? v[2 * y + 1].x : v[2 * y + 1].y;
+        const unsigned a0 = (mt & 1 ? a >> 1 : a << 7) & kNibB, b0 = (mt & 1 ? b >> 1 : b << 7) & kNibB;
+        const unsigned a1 = ~(mt & 1 ? a >> 5 : a << 3) & kNibB, b1 = ~(mt & 1 ? b >> 5 : b << 3) & kNibB;
+#pragma unroll
+        for (int h = 0; h < HL; ++h) mma_f16(t[y][h], a0, b0, a1, b1, bp[h][mt][0], bp[h][mt][1]);
       }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) f.o[i][e] += t[e];
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (RT == 8) f.o[i + y][e] += t[y][HL - 1][e];
+        f.o[i + y][e] += t[y][0][e];
+      }
   }
 }
 
@@ -651,40 +683,42 @@ __device__ __forceinline__ void kd_fast_store(KdFast<D, RT>& f, float* s_m, floa
 // shared memory: mbarriers (full and empty), warp sums, q rows, the ring
 template <int D, int RT>
 struct KdLayout {
+  static constexpr int W = kd_warps<RT>();
   static constexpr int bars = 0;
   static constexpr int sent = 2 * kKdMaxStages * 8;
   static constexpr int m = sent + kKdMaxStages * 4;
-  static constexpr int l = m + kKdWarps * RT * 4;
-  static constexpr int acc = l + kKdWarps * RT * 4;
-  static constexpr int q = acc + kKdWarps * RT * D * 4;
-  static int ring(int rows) { return q + (rows + RT - 1) / RT * RT * D * 4; }
+  static constexpr int l = m + W * RT * 4;
+  static constexpr int acc = l + W * RT * 4;
+  static constexpr int q = acc + W * RT * D * 4;
+  static __host__ __device__ int ring(int rows) { return q + (rows + RT - 1) / RT * RT * (D + 16) * 4; }
 };
 
 template <int D, int RT, typename E>
-__global__ void __launch_bounds__(kKdWarps * 32, 1) kv4_decode_kernel(const Kv4DecodeArgs a) {
+__global__ void __launch_bounds__(kd_warps<RT>() * 32, 1) kv4_decode_kernel(const Kv4DecodeArgs a) {
   pdl_entry();
   using St = KdStage<D>;
   using Lt = KdLayout<D, RT>;
-  constexpr int CPL = D / 32;
+  constexpr int CPL = D / 32, W = kd_warps<RT>();
   __shared__ int64_t s_pref[kMaxB + 1];
   __shared__ int64_t s_end[CSA_KV4_MAX_ROWS];
+  __shared__ float s_inv[CSA_KV4_MAX_ROWS];
   extern __shared__ __align__(128) uint8_t kd_sm[];
   float* s_m = reinterpret_cast<float*>(kd_sm + Lt::m);        // [warps][RT]
   float* s_l = reinterpret_cast<float*>(kd_sm + Lt::l);
   float* s_acc = reinterpret_cast<float*>(kd_sm + Lt::acc);    // [warps][RT][D]
-  float* s_q = reinterpret_cast<float*>(kd_sm + Lt::q);        // [rows, padded][D]
+  float* s_q = reinterpret_cast<float*>(kd_sm + Lt::q);        // [rows, padded] (kd_q)
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int R = a.T * a.G, Rp = (R + RT - 1) / RT * RT;
-  // teams: warps that share a block, one tile of rows each; with team = 8
-  // four warps are left over
+  // teams: warps that share a block, one tile of rows each (RT = 8, more than
+  // 32 rows: one team, four warps left over)
   const int ntile = Rp / RT;
   const int team = ntile <= 1 ? 1 : ntile <= 2 ? 2 : ntile <= 4 ? 4 : 8;
-  const int nteam = kKdWarps / team, my_team = w / team, tile = w % team;
+  const int nteam = W / team, my_team = w / team, tile = w % team;
   const bool active = my_team < nteam;
   const int rows = active ? min(RT, R - tile * RT) : 0;    // <= 0: a warp with no rows
   const unsigned full = smem_u32(kd_sm) + Lt::bars, empty = full + kKdMaxStages * 8;
   int* s_sent = reinterpret_cast<int*>(kd_sm + Lt::sent);
-  uint8_t* ring = kd_sm + Lt::q + Rp * D * 4;
+  uint8_t* ring = kd_sm + Lt::ring(R);
   if (tid < a.stages) {
     mbar_init(full + 8 * tid, 1);
     mbar_init(empty + 8 * tid, team);
@@ -717,6 +751,7 @@ __global__ void __launch_bounds__(kKdWarps * 32, 1) kv4_decode_kernel(const Kv4D
     }
   }
   int base = 0;                     // number of the item's first block
+  int i = my_team, slot = my_team, phase = 0;   // the team's next block, its slot and parity
   if (blockIdx.x == 0 && tid < 32) {
     bool bad = false;
     for (int b = lane; b < a.B; b += 32) {
@@ -730,37 +765,57 @@ __global__ void __launch_bounds__(kKdWarps * 32, 1) kv4_decode_kernel(const Kv4D
 
   for (int64_t u = u0; u < u1;) {
     const KdSeg sg = kd_seg(a, s_pref, u, u1);
-    for (int i = tid; i < Rp * D; i += kKdWarps * 32) {
-      const int r = i / D, c = i - r * D;
+    for (int r = w; r < Rp; r += W) {
       const int t = r / a.G;
-      float x = 0.0f;
-      if (t < sg.nq)
-        x = Elem<E>::get(reinterpret_cast<const E*>(a.q) + sg.b * a.qs.b + t * a.qs.t +
-                             (int64_t)(sg.g * a.G + r % a.G) * a.qs.h, c) * a.rs;
-      s_q[i] = x;
+      float x[CPL];
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) x[c] = 0.0f;
+      if (t < sg.nq) {
+        const E* src = reinterpret_cast<const E*>(a.q) + sg.b * a.qs.b + t * a.qs.t +
+                       (int64_t)(sg.g * a.G + r % a.G) * a.qs.h + lane * CPL;
+        if (CPL == 4) {
+          const float4 v = Elem<E>::get4(src);
+          x[0] = v.x; x[1] = v.y; x[CPL - 2] = v.z; x[CPL - 1] = v.w;
+        } else {
+          const float2 v = Elem<E>::get2(src);
+          x[0] = v.x; x[1] = v.y;
+        }
+      }
+      float top = 0.0f;
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) {
+        x[c] *= a.rs;
+        top = fmaxf(top, fabsf(x[c]));
+      }
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+      const int k = top > 0.0f && top < INFINITY ? min(max(11 - exponent(top), -100), 100) : 0;
+      const float up = pow2i(k);
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) s_q[kd_q<D>(r, lane * CPL) + c] = x[c] * (c & 1 ? 0.0625f * up : up);
+      if (lane == 0) s_inv[r] = pow2i(-k);
     }
     if (tid < Rp) s_end[tid] = tid / a.G < sg.nq ? sg.n - sg.nq + tid / a.G + 1 : 0;
     __syncthreads();
-    const float* q = s_q + tile * RT * D;
+    const int r0 = tile * RT < Rp ? tile * RT : 0;      // (tiles past the rows do nothing)
+    const float* q = s_q + kd_q<D>(r0, 0);
     float* my_m = s_m + w * RT;
     float* my_l = s_l + w * RT;
     float* my_acc = s_acc + w * RT * D;
     {
       KdFast<D, RT> f;
-      kd_fast_init<D, RT>(f, tile * RT < Rp ? q : s_q, rows);
-      // (block `i` is the team's own when i % nteam == my_team)
-      const int lead = (my_team + nteam - base % nteam) % nteam;
-      for (int i = base + lead; active && i < base + (int)sg.nfast; i += nteam) {
-        const int slot = i % a.stages, round = i / a.stages;
-        if (!dead && !kd_wait(s_sent + slot, i, full + 8 * slot, round & 1)) dead = true;
-        if (rows > 0) kd_fast_block<D, RT>(f, ring + slot * St::bytes);
+      kd_fast_init<D, RT>(f, s_inv + r0);
+      const int to = base + (int)sg.nfast;
+      while (active && i < to) {
+        if (!dead && !kd_wait(s_sent + slot, i, full + 8 * slot, phase)) dead = true;
+        if (rows > 0) kd_fast_block<D, RT>(f, ring + slot * St::bytes, q);
         __syncwarp();
         if (team > 1 && lane == 0) mbar_arrive(empty + 8 * slot);
         dead = __any_sync(0xffffffffu, dead);
         if (leader && !dead) {
           const int64_t at = cur.find(a, s_pref, i + a.stages);
           if (at >= 0) {
-            if (team > 1 && !mbar_wait(empty + 8 * slot, round & 1)) dead = true;
+            if (team > 1 && !mbar_wait(empty + 8 * slot, phase)) dead = true;
             dead = __any_sync(0xffffffffu, dead);
             if (!dead) {
               copy.issue(lane, i + a.stages, at, smem_u32(ring) + slot * St::bytes, full + 8 * slot, s_sent + slot);
@@ -768,6 +823,9 @@ __global__ void __launch_bounds__(kKdWarps * 32, 1) kv4_decode_kernel(const Kv4D
             }
           }
         }
+        i += nteam;
+        slot += nteam;
+        if (slot >= a.stages) { slot -= a.stages; phase ^= 1; }
       }
       kd_fast_store<D, RT>(f, my_m, my_l, my_acc);
     }
@@ -783,7 +841,8 @@ __global__ void __launch_bounds__(kKdWarps * 32, 1) kv4_decode_kernel(const Kv4D
 #pragma unroll
         for (int c = 0; c < CPL; ++c) st.acc[r][c] = my_acc[r * D + lane * CPL + c];
       }
-      const int64_t* end = s_end + tile * RT;
+      const int64_t* end = s_end + r0;
+      const float* inv = s_inv + r0;
       for (int64_t x = sg.nfast * 8 + my_team; x < sg.cnt * 8; x += nteam) {
         const int64_t blk = sg.blk0 + x / 8;
         const int grp = (int)(x % 8);
@@ -814,7 +873,7 @@ __global__ void __launch_bounds__(kKdWarps * 32, 1) kv4_decode_kernel(const Kv4D
             }
           }
           const int i = lane & 7;
-          kd_step<D, RT>(st, kv, vv, q, end, p0 + first + 16 * ((i >> 1) & 1) + 8 * (i & 1) + (i >> 2), rows);
+          kd_step<D, RT>(st, kv, vv, q, inv, end, p0 + first + 16 * ((i >> 1) & 1) + 8 * (i & 1) + (i >> 2), rows);
         } else {
           if (p0 + 8 * grp >= sg.n) continue;
 #pragma unroll
@@ -829,7 +888,7 @@ __global__ void __launch_bounds__(kKdWarps * 32, 1) kv4_decode_kernel(const Kv4D
               vv[i][c] = there ? Elem<E>::get(vr, c) : 0.0f;
             }
           }
-          kd_step<D, RT>(st, kv, vv, q, end, p0 + 8 * grp + (lane & 7), rows);
+          kd_step<D, RT>(st, kv, vv, q, inv, end, p0 + 8 * grp + (lane & 7), rows);
         }
       }
       __syncwarp();
@@ -844,7 +903,7 @@ __global__ void __launch_bounds__(kKdWarps * 32, 1) kv4_decode_kernel(const Kv4D
     // merge the teams
     const bool done = sg.cnt == sg.ub;
     float* part = a.part + (2 * (int64_t)blockIdx.x + (u == u0 ? 0 : 1)) * R * (D + 2);
-    for (int i = tid; i < R * D; i += kKdWarps * 32) {
+    for (int i = tid; i < R * D; i += W * 32) {
       const int r = i / D, c = i - r * D;
       const int x0 = r / RT * RT + r % RT;       // (tile, row) of team 0's warps
       float M = -INFINITY, l = 0.0f, v = 0.0f;
@@ -935,7 +994,7 @@ cudaError_t launch_kv4_decode_t(Kv4DecodeArgs a, int ncta, cudaStream_t st) {
   const cudaError_t e =
       cudaFuncSetAttribute(kv4_decode_kernel<D, RT, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  launch_pdl(kv4_decode_kernel<D, RT, E>, dim3(ncta), dim3(kKdWarps * 32), smem, st, a);
+  launch_pdl(kv4_decode_kernel<D, RT, E>, dim3(ncta), dim3(kd_warps<RT>() * 32), smem, st, a);
   if (ncta > 1) launch_pdl(kv4_join_kernel<D>, dim3(ncta - 1), dim3(256), 0, st, a, ncta);
   return cudaGetLastError();
 }
