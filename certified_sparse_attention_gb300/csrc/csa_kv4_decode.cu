@@ -60,27 +60,31 @@ struct Kv4DecodeArgs {
   float* part;          // [2 * CTAs][rows][D + 2]: m, l, acc[D]
   int64_t n_max, nblk_max;
   int B, T, Hq, Hkv, G;
-  int stages;           // blocks in the ring
+  int slotsK, slotsV;   // slots of the two rings: multiples of the number of teams
   float rs;             // log2(e) / sqrt(d): scores in units of log 2
 };
 
-// warps of a CTA, by the rows of a warp's tile: what the registers allow
-template <int RT> __host__ __device__ constexpr int kd_warps() { return RT == 4 ? 16 : 12; }
-constexpr int kKdMaxStages = 24;  // blocks in the ring of a CTA
+constexpr int kKdWarps = 12;      // consumer warps of a CTA: three warpgroups; a fourth
+                                  // one's first two warps send for the blocks
+constexpr int kKdThreads = (kKdWarps + 4) * 32;
+// registers: 512 threads start with 128 each; the producers give theirs up
+constexpr int kKdRegsConsumer = 160, kKdRegsProducer = 32;
+static_assert(3 * kKdRegsConsumer + kKdRegsProducer <= 4 * 128, "more registers than the launch has");
+constexpr int kKdMaxStages = 24;  // slots of a ring
 
-// one block in shared memory.  The bounds are copied in eight pieces, 16
+// One block in shared memory: the keys' part (codes, bounds) in one ring, the
+// values' (codes, token scales) in another.  The bounds lie in eight pieces 16
 // bytes apart, so that the four channel ranges of a warp's lanes start in
-// different banks (one piece for all would put them in the same ones).
+// different banks (in one piece they would start in the same ones).
 template <int D>
 struct KdStage {
-  static constexpr int K = 0;
-  static constexpr int V = K + kBlock * D / 2;
-  static constexpr int S = V + kBlock * D / 2;
-  static constexpr int B = S + kBlock * 8;
   static constexpr int PIECE = D;                       // bytes: D / 4 floats
   static constexpr int PITCH = PIECE + 16;
-  static constexpr int bytes = B + 8 * PITCH;
-  static constexpr int tx = kBlock * D + kBlock * 8 + 8 * D;
+  static constexpr int B = kBlock * D / 2;              // keys: codes, then the bounds
+  static constexpr int bytesK = B + 8 * PITCH;
+  static constexpr int S = kBlock * D / 2;              // values: codes, then the token scales
+  static constexpr int bytesV = S + kBlock * 8;
+  static constexpr int txK = kBlock * D / 2 + 8 * D, txV = kBlock * D / 2 + kBlock * 8;
 };
 
 // units of one (sequence, KV head) of n tokens (at least one: somebody has to
@@ -237,71 +241,69 @@ __device__ __forceinline__ KdSeg kd_seg(const Kv4DecodeArgs& a, const int64_t* s
   return s;
 }
 
-// Walks the CTA's tensor-core blocks, numbered 0, 1, ... over all its items.
-struct KdCursor {
-  int64_t u, u1, cnt, at0;
-  int lo, hi;             // numbers [lo, hi) lie in the item at hand
-  __device__ __forceinline__ void open(const Kv4DecodeArgs& a, const int64_t* s_pref) {
-    const KdSeg s = kd_seg(a, s_pref, u, u1);
-    cnt = s.cnt;
-    at0 = s.bg * a.nblk_max + s.blk0;
-    lo = hi;
-    hi += (int)s.nfast;
-  }
-  // place of block `i` in the cache (i never decreases), or -1 past the end
-  __device__ __forceinline__ int64_t find(const Kv4DecodeArgs& a, const int64_t* s_pref, int i) {
-    while (u < u1 && i >= hi) {
-      u += cnt;
-      if (u < u1) open(a, s_pref);
-    }
-    return u < u1 ? at0 + (i - lo) : -1;
-  }
+// A ring of slots with full and empty barriers.  Block i sits in slot i %
+// slots and is taken by team i % teams; slots is a multiple of teams, so a
+// slot serves one team, which has seen its last phase when it waits for the
+// next.
+struct KdRing {
+  uint8_t* data;
+  unsigned full, empty;
+  int slots;
 };
 
-// The copies that bring a block: one by each of the lanes 0 .. 10.
+// A producer warp: sends for the keys' or the values' parts of the CTA's
+// tensor-core blocks in order, as slots come free: the codes by one bulk
+// copy, the bounds or token scales by 16-byte copies of the lanes (eight bulk
+// copies of 128 bytes, one for each piece of the bounds, held the 128K-token
+// step at 62% of the memory's rate).
 template <int D>
-struct KdCopy {
-  const uint8_t* src;
-  unsigned step, dst, bytes;
-  __device__ __forceinline__ KdCopy(const csa_kv4& c, int lane) {
-    using St = KdStage<D>;
-    const int piece = max(0, lane - 3);
-    src = lane == 0 ? c.K4 : lane == 1 ? c.V4
-        : lane == 2 ? reinterpret_cast<const uint8_t*>(c.vscale)
-                    : reinterpret_cast<const uint8_t*>(c.bounds) + piece * St::PIECE;
-    step = lane < 2 ? kBlock * D / 2 : lane == 2 ? kBlock * 8 : 8 * D;
-    dst = lane == 0 ? St::K : lane == 1 ? St::V : lane == 2 ? St::S : St::B + piece * St::PITCH;
-    bytes = lane < 2 ? kBlock * D / 2 : lane == 2 ? kBlock * 8 : St::PIECE;
-  }
-  // sends for block number i, at place `at` of the cache; *sent tells whoever
-  // waits for it that the barrier's phase is the block's own
-  __device__ __forceinline__ void issue(int lane, int i, int64_t at, unsigned stage, unsigned bar, int* sent) const {
-    if (lane == 0) {
-      mbar_expect_tx(bar, KdStage<D>::tx);
-      __threadfence_block();
-      *(volatile int*)sent = i;
+__device__ __forceinline__ void kd_produce(const Kv4DecodeArgs& a, const int64_t* s_pref, int64_t u0, int64_t u1,
+                                           const KdRing& ring, bool keys) {
+  using St = KdStage<D>;
+  constexpr int codes = kBlock * D / 2;
+  const int lane = threadIdx.x & 31;
+  const unsigned size = keys ? St::bytesK : St::bytesV;
+  const unsigned side = keys ? 8 * D : kBlock * 8;        // bytes of the bounds, of the scales
+  const uint8_t* src = keys ? a.c.K4 : a.c.V4;
+  const uint8_t* side_src = reinterpret_cast<const uint8_t*>(keys ? a.c.bounds : a.c.vscale) + lane * 16;
+  // where the lane's 16 bytes go, and (keys, d = 128) its other 16: 512 bytes on
+  const unsigned to0 = codes + (keys ? lane * 16 / St::PIECE * St::PITCH + lane * 16 % St::PIECE : lane * 16);
+  const unsigned to1 = codes + (lane * 16 + 512) / St::PIECE * St::PITCH + lane * 16 % St::PIECE;
+  const bool two = side > 512;
+  const unsigned data = smem_u32(ring.data);
+  int i = 0, slot = 0, phase = 0;
+  bool dead = false;
+  for (int64_t u = u0; u < u1 && !dead;) {
+    const KdSeg s = kd_seg(a, s_pref, u, u1);
+    const int64_t at = s.bg * a.nblk_max + s.blk0;
+    const uint8_t* from = src + at * codes;
+    const uint8_t* side_from = side_src + at * side;
+    for (int64_t x = 0; x < s.nfast; ++x) {
+      dead = !mbar_wait(ring.empty + 8 * slot, phase ^ 1);    // (a new barrier's "phase -1" is complete)
+      dead = __any_sync(0xffffffffu, dead);
+      if (dead) break;
+      const unsigned to = data + slot * size, bar = ring.full + 8 * slot;
+      if (lane == 0) {
+        mbar_expect_tx(bar, codes);
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(to),
+            "l"(from), "n"(codes), "r"(bar)
+            : "memory");
+      }
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to + to0), "l"(side_from) : "memory");
+      if (two) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to + to1), "l"(side_from + 512) : "memory");
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
+      from += codes;
+      side_from += side;
+      ++i;
+      if (++slot == ring.slots) { slot = 0; phase ^= 1; }
     }
-    __syncwarp();
-    if (lane < 11)
-      asm volatile(
-          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(stage + dst),
-          "l"(src + at * step), "r"(bytes), "r"(bar)
-          : "memory");
+    u += s.cnt;
   }
-};
-
-// Waits until block i has been sent for into its slot, then for its bytes.
-// (The barrier alone does not do: its parity repeats every second round, and
-// a team may be two rounds ahead of the one that frees the slot.)  False
-// after kWaitNs.
-__device__ __forceinline__ bool kd_wait(const int* sent, int i, unsigned bar, unsigned parity) {
-  unsigned long long t0 = 0;
-  for (unsigned it = 0; *(const volatile int*)sent != i; ++it) {
-    if (it == 0) t0 = global_ns();
-    else if ((it & 63u) == 0u && global_ns() - t0 > kWaitNs) return false;
-  }
-  __threadfence_block();
-  return mbar_wait(bar, parity);
+  // all copies land before the CTA can end
+  for (int k = max(0, i - ring.slots); k < i; ++k)
+    if (!mbar_wait(ring.full + 8 * (k % ring.slots), (k / ring.slots) & 1)) dead = true;
+  if (dead && lane == 0) atomicOr(a.status, 4u);
 }
 
 // ------------------------------------------------------ tensor-core blocks
@@ -382,8 +384,11 @@ __device__ __forceinline__ void kd_fast_init(KdFast<D, RT>& f, const float* s_in
   f.fresh = true;
 }
 
-template <int D, int RT>
-__device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* st, const float* s_q) {
+// One block: its keys' part at st, its values' part at vt; between() is
+// called when the one has been read and before the other is.
+template <int D, int RT, typename Between>
+__device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* st, const uint8_t* vt, const float* s_q,
+                                              Between between) {
   using St = KdStage<D>;
   constexpr int NC = D / 4;        // channels of a lane
   constexpr int NW = D / 32;       // code words of a lane in a key row
@@ -469,7 +474,7 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
     unsigned k[4][NW];      // rows gid, gid + 8 of tile 2 pr, then of the next
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint8_t* kr = st + St::K + (32 * pr + 8 * j + gid) * (D / 2) + tid * (D / 8);
+      const uint8_t* kr = st + (32 * pr + 8 * j + gid) * (D / 2) + tid * (D / 8);
       if (D == 128) {
         const uint4 u = *reinterpret_cast<const uint4*>(kr);
         k[j][0] = u.x; k[j][1] = u.y; k[j][NW - 2] = u.z; k[j][NW - 1] = u.w;
@@ -495,6 +500,7 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[2 * pr + y][e] = RT == 8 ? t[y][0][e] + t[y][HL - 1][e] : t[y][0][e];
   }
+  between();
   // RT = 4: add the two parts; afterwards the lane has token 16 mt + gid (+ 8
   // in the upper lanes), rows ra, ra + 1, in s[mt][0], s[mt][1].
   // RT = 8: tokens gid and gid + 8 in s[mt][0..1] and s[mt][2..3].
@@ -521,7 +527,7 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
   for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
     for (int k = 0; k < TK; ++k) {
-      sc[mt][k] = *reinterpret_cast<const float2*>(st + St::S + (16 * mt + gid + (RT == 8 ? 8 * k : upper ? 8 : 0)) * 8);
+      sc[mt][k] = *reinterpret_cast<const float2*>(vt + St::S + (16 * mt + gid + (RT == 8 ? 8 * k : upper ? 8 : 0)) * 8);
       wide = fmaxf(wide, sc[mt][k].y);
     }
   // The reference moves only when a score exceeds it by more than 8 (weights
@@ -618,7 +624,7 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
     uint2 v[4];             // channels gid, gid + 8 of tile i, then of the next
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      v[j] = *reinterpret_cast<const uint2*>(st + St::V + (16 * i + 8 * j + gid) * (kBlock / 2) + tid * 8);
+      v[j] = *reinterpret_cast<const uint2*>(vt + (16 * i + 8 * j + gid) * (kBlock / 2) + tid * 8);
     float t[2][HL][4] = {};
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
@@ -680,91 +686,91 @@ __device__ __forceinline__ void kd_fast_store(KdFast<D, RT>& f, float* s_m, floa
   }
 }
 
-// shared memory: mbarriers (full and empty), warp sums, q rows, the ring
+// shared memory: barriers of the two rings, warp sums, q rows, the rings
 template <int D, int RT>
 struct KdLayout {
-  static constexpr int W = kd_warps<RT>();
-  static constexpr int bars = 0;
-  static constexpr int sent = 2 * kKdMaxStages * 8;
-  static constexpr int m = sent + kKdMaxStages * 4;
-  static constexpr int l = m + W * RT * 4;
-  static constexpr int acc = l + W * RT * 4;
-  static constexpr int q = acc + W * RT * D * 4;
+  static constexpr int bars = 0;                              // full, empty of the keys, then of the values
+  static constexpr int m = 4 * kKdMaxStages * 8;
+  static constexpr int l = m + kKdWarps * RT * 4;
+  static constexpr int acc = l + kKdWarps * RT * 4;
+  static constexpr int q = acc + kKdWarps * RT * D * 4;
   static __host__ __device__ int ring(int rows) { return q + (rows + RT - 1) / RT * RT * (D + 16) * 4; }
 };
 
 template <int D, int RT, typename E>
-__global__ void __launch_bounds__(kd_warps<RT>() * 32, 1) kv4_decode_kernel(const Kv4DecodeArgs a) {
+__global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4DecodeArgs a) {
   pdl_entry();
   using St = KdStage<D>;
   using Lt = KdLayout<D, RT>;
-  constexpr int CPL = D / 32, W = kd_warps<RT>();
+  constexpr int CPL = D / 32, W = kKdWarps;
   __shared__ int64_t s_pref[kMaxB + 1];
   __shared__ int64_t s_end[CSA_KV4_MAX_ROWS];
   __shared__ float s_inv[CSA_KV4_MAX_ROWS];
+  __shared__ KdSeg s_seg;
   extern __shared__ __align__(128) uint8_t kd_sm[];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int R = a.T * a.G, Rp = (R + RT - 1) / RT * RT;
+  // teams: warps that share a block, one tile of rows each (more than 32 rows:
+  // one team of 8, four warps left over)
+  const int ntile = Rp / RT;
+  const int team = ntile <= 1 ? 1 : ntile <= 2 ? 2 : ntile <= 4 ? 4 : 8;
+  const int nteam = W / team;
+  KdRing keys, values;
+  keys.full = smem_u32(kd_sm) + Lt::bars;
+  keys.empty = keys.full + kKdMaxStages * 8;
+  values.full = keys.empty + kKdMaxStages * 8;
+  values.empty = values.full + kKdMaxStages * 8;
+  keys.slots = a.slotsK;
+  values.slots = a.slotsV;
+  keys.data = kd_sm + Lt::ring(R);
+  values.data = keys.data + a.slotsK * St::bytesK;
+  if (tid < kKdMaxStages) {
+    // (one arrival with the codes' bytes, one of each lane of the producer)
+    mbar_init(keys.full + 8 * tid, 33);
+    mbar_init(keys.empty + 8 * tid, team);
+    mbar_init(values.full + 8 * tid, 33);
+    mbar_init(values.empty + 8 * tid, team);
+    fence_barrier_init();
+  }
+  kd_prefix(a, s_pref);
+  const int64_t total = s_pref[kMaxB];
+  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t u0 = (int64_t)blockIdx.x * per, u1 = min(total, u0 + per);
+
+  if (w >= W) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kKdRegsProducer));
+    if (w == W) kd_produce<D>(a, s_pref, u0, u1, keys, true);
+    else if (w == W + 1) kd_produce<D>(a, s_pref, u0, u1, values, false);
+    else if (w == W + 2 && blockIdx.x == 0) {
+      bool bad = false;
+      for (int b = lane; b < a.B; b += 32) {
+        bad |= a.len[b] < 0 || a.len[b] > a.n_max;
+        if (a.n_q) bad |= a.n_q[b] < 0 || a.n_q[b] > a.T;
+      }
+      const unsigned any = __any_sync(0xffffffffu, bad);
+      // (a wait that gives up flags the word two seconds later at the earliest)
+      if (lane == 0) *a.status = any ? 8u : 0u;
+    }
+    return;
+  }
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kKdRegsConsumer));
+
   float* s_m = reinterpret_cast<float*>(kd_sm + Lt::m);        // [warps][RT]
   float* s_l = reinterpret_cast<float*>(kd_sm + Lt::l);
   float* s_acc = reinterpret_cast<float*>(kd_sm + Lt::acc);    // [warps][RT][D]
   float* s_q = reinterpret_cast<float*>(kd_sm + Lt::q);        // [rows, padded] (kd_q)
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int R = a.T * a.G, Rp = (R + RT - 1) / RT * RT;
-  // teams: warps that share a block, one tile of rows each (RT = 8, more than
-  // 32 rows: one team, four warps left over)
-  const int ntile = Rp / RT;
-  const int team = ntile <= 1 ? 1 : ntile <= 2 ? 2 : ntile <= 4 ? 4 : 8;
-  const int nteam = W / team, my_team = w / team, tile = w % team;
-  const bool active = my_team < nteam;
-  const int rows = active ? min(RT, R - tile * RT) : 0;    // <= 0: a warp with no rows
-  const unsigned full = smem_u32(kd_sm) + Lt::bars, empty = full + kKdMaxStages * 8;
-  int* s_sent = reinterpret_cast<int*>(kd_sm + Lt::sent);
-  uint8_t* ring = kd_sm + Lt::ring(R);
-  if (tid < a.stages) {
-    mbar_init(full + 8 * tid, 1);
-    mbar_init(empty + 8 * tid, team);
-    s_sent[tid] = -1;
-    fence_barrier_init();
-  }
-  kd_prefix(a, s_pref);
-  // (each wait below is bounded: one that gives up marks the call and the
-  // warp goes on without waiting or copying)
+  const int my_team = w / team, tile = w % team;
+  const int rows = my_team < nteam ? min(RT, R - tile * RT) : 0;    // <= 0: a warp with no rows
+  // (Each wait is bounded: one that gives up marks the call, and the warp goes
+  // on without waiting.)
   bool dead = false;
-  const int64_t total = s_pref[kMaxB];
-  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t u0 = (int64_t)blockIdx.x * per, u1 = min(total, u0 + per);
-  // Block i of the CTA sits in slot i % stages of the ring and is taken by
-  // team i % nteam, whose first warp, once the block is used, sends for
-  // block i + stages into the same slot.
-  const bool leader = active && tile == 0;
-  const KdCopy<D> copy(a.c, lane);
-  KdCursor cur;
-  cur.u = u0; cur.u1 = u1; cur.lo = cur.hi = 0; cur.cnt = 0; cur.at0 = 0;
-  int next = my_team;               // (leaders) number of the next block to send for
-  int last = -1;                    // number of the last block sent for
-  if (leader && u0 < u1) {
-    cur.open(a, s_pref);
-    for (; next < a.stages; next += nteam) {
-      const int64_t at = cur.find(a, s_pref, next);
-      if (at < 0) break;
-      copy.issue(lane, next, at, smem_u32(ring) + next * St::bytes, full + 8 * next, s_sent + next);
-      last = next;
-    }
-  }
-  int base = 0;                     // number of the item's first block
-  int i = my_team, slot = my_team, phase = 0;   // the team's next block, its slot and parity
-  if (blockIdx.x == 0 && tid < 32) {
-    bool bad = false;
-    for (int b = lane; b < a.B; b += 32) {
-      bad |= a.len[b] < 0 || a.len[b] > a.n_max;
-      if (a.n_q) bad |= a.n_q[b] < 0 || a.n_q[b] > a.T;
-    }
-    const unsigned any = __any_sync(0xffffffffu, bad);
-    // (a wait that gives up flags the word two seconds later at the earliest)
-    if (lane == 0) *a.status = any ? 8u : 0u;
-  }
+  int base = 0;                                   // number of the item's first block
+  int i = my_team;                                // the team's next block, its slots and their parities
+  int sk = my_team, sv = my_team, pk = 0, pv = 0;
 
   for (int64_t u = u0; u < u1;) {
     const KdSeg sg = kd_seg(a, s_pref, u, u1);
+    if (tid == 0) s_seg = sg;
     for (int r = w; r < Rp; r += W) {
       const int t = r / a.G;
       float x[CPL];
@@ -796,41 +802,37 @@ __global__ void __launch_bounds__(kd_warps<RT>() * 32, 1) kv4_decode_kernel(cons
       if (lane == 0) s_inv[r] = pow2i(-k);
     }
     if (tid < Rp) s_end[tid] = tid / a.G < sg.nq ? sg.n - sg.nq + tid / a.G + 1 : 0;
-    __syncthreads();
+    bar_sync(1, W * 32);
     const int r0 = tile * RT < Rp ? tile * RT : 0;      // (tiles past the rows do nothing)
     const float* q = s_q + kd_q<D>(r0, 0);
     float* my_m = s_m + w * RT;
     float* my_l = s_l + w * RT;
     float* my_acc = s_acc + w * RT * D;
+    base += (int)sg.nfast;
     {
       KdFast<D, RT> f;
       kd_fast_init<D, RT>(f, s_inv + r0);
-      const int to = base + (int)sg.nfast;
-      while (active && i < to) {
-        if (!dead && !kd_wait(s_sent + slot, i, full + 8 * slot, phase)) dead = true;
-        if (rows > 0) kd_fast_block<D, RT>(f, ring + slot * St::bytes, q);
+      while (my_team < nteam && i < base) {
+        if (!dead && !mbar_wait(keys.full + 8 * sk, pk)) dead = true;
+        const auto between = [&]() {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(keys.empty + 8 * sk);
+          if (!dead && !mbar_wait(values.full + 8 * sv, pv)) dead = true;
+        };
+        if (rows > 0)
+          kd_fast_block<D, RT>(f, keys.data + sk * St::bytesK, values.data + sv * St::bytesV, q, between);
+        else
+          between();
         __syncwarp();
-        if (team > 1 && lane == 0) mbar_arrive(empty + 8 * slot);
-        dead = __any_sync(0xffffffffu, dead);
-        if (leader && !dead) {
-          const int64_t at = cur.find(a, s_pref, i + a.stages);
-          if (at >= 0) {
-            if (team > 1 && !mbar_wait(empty + 8 * slot, phase)) dead = true;
-            dead = __any_sync(0xffffffffu, dead);
-            if (!dead) {
-              copy.issue(lane, i + a.stages, at, smem_u32(ring) + slot * St::bytes, full + 8 * slot, s_sent + slot);
-              last = i + a.stages;
-            }
-          }
-        }
+        if (lane == 0) mbar_arrive(values.empty + 8 * sv);
         i += nteam;
-        slot += nteam;
-        if (slot >= a.stages) { slot -= a.stages; phase ^= 1; }
+        if ((sk += nteam) >= keys.slots) { sk = my_team; pk ^= 1; }
+        if ((sv += nteam) >= values.slots) { sv = my_team; pv ^= 1; }
       }
       kd_fast_store<D, RT>(f, my_m, my_l, my_acc);
     }
-    base += (int)sg.nfast;
-    if (rows > 0 && sg.nfast < sg.cnt) {
+    const KdSeg se = s_seg;       // (read back: not held in registers over the blocks)
+    if (rows > 0 && se.nfast < se.cnt) {
       // blocks that are seen in part, and the incomplete one, eight tokens
       // at a time: the state moves on to lanes that hold channels
       __syncwarp();
@@ -843,13 +845,13 @@ __global__ void __launch_bounds__(kd_warps<RT>() * 32, 1) kv4_decode_kernel(cons
       }
       const int64_t* end = s_end + r0;
       const float* inv = s_inv + r0;
-      for (int64_t x = sg.nfast * 8 + my_team; x < sg.cnt * 8; x += nteam) {
-        const int64_t blk = sg.blk0 + x / 8;
+      for (int64_t x = se.nfast * 8 + my_team; x < se.cnt * 8; x += nteam) {
+        const int64_t blk = se.blk0 + x / 8;
         const int grp = (int)(x % 8);
         const int64_t p0 = blk * kBlock;
         float kv[8][CPL], vv[8][CPL];
-        if (blk < sg.n / kBlock) {
-          const int64_t at = sg.bg * a.nblk_max + blk;
+        if (blk < se.n / kBlock) {
+          const int64_t at = se.bg * a.nblk_max + blk;
           float mn[CPL], dl[CPL];
           unsigned vw[CPL];
 #pragma unroll
@@ -875,13 +877,13 @@ __global__ void __launch_bounds__(kd_warps<RT>() * 32, 1) kv4_decode_kernel(cons
           const int i = lane & 7;
           kd_step<D, RT>(st, kv, vv, q, inv, end, p0 + first + 16 * ((i >> 1) & 1) + 8 * (i & 1) + (i >> 2), rows);
         } else {
-          if (p0 + 8 * grp >= sg.n) continue;
+          if (p0 + 8 * grp >= se.n) continue;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int t = 8 * grp + i;
-            const bool there = p0 + t < sg.n;
-            const E* kr = reinterpret_cast<const E*>(a.c.Kt) + (sg.bg * kBlock + t) * D + lane * CPL;
-            const E* vr = reinterpret_cast<const E*>(a.c.Vt) + (sg.bg * kBlock + t) * D + lane * CPL;
+            const bool there = p0 + t < se.n;
+            const E* kr = reinterpret_cast<const E*>(a.c.Kt) + (se.bg * kBlock + t) * D + lane * CPL;
+            const E* vr = reinterpret_cast<const E*>(a.c.Vt) + (se.bg * kBlock + t) * D + lane * CPL;
 #pragma unroll
             for (int c = 0; c < CPL; ++c) {
               kv[i][c] = there ? Elem<E>::get(kr, c) : 0.0f;
@@ -899,9 +901,9 @@ __global__ void __launch_bounds__(kd_warps<RT>() * 32, 1) kv4_decode_kernel(cons
         for (int c = 0; c < CPL; ++c) my_acc[r * D + lane * CPL + c] = st.acc[r][c];
       }
     }
-    __syncthreads();
+    bar_sync(1, W * 32);
     // merge the teams
-    const bool done = sg.cnt == sg.ub;
+    const bool done = se.cnt == se.ub;
     float* part = a.part + (2 * (int64_t)blockIdx.x + (u == u0 ? 0 : 1)) * R * (D + 2);
     for (int i = tid; i < R * D; i += W * 32) {
       const int r = i / D, c = i - r * D;
@@ -915,22 +917,16 @@ __global__ void __launch_bounds__(kd_warps<RT>() * 32, 1) kv4_decode_kernel(cons
         v += e * s_acc[x * D + c];
       }
       if (done) {
-        if (r / a.G < sg.nq) kd_store<D>(a, sg.b, sg.g, r, c, M, l, v);
+        if (r / a.G < se.nq) kd_store<D>(a, se.b, se.g, r, c, M, l, v);
       } else {
         if (c == 0) { part[r * (D + 2)] = M; part[r * (D + 2) + 1] = l; }
         part[r * (D + 2) + 2 + c] = v;
       }
     }
-    __syncthreads();
-    u += sg.cnt;
+    bar_sync(1, W * 32);
+    u += se.cnt;
   }
-  if (dead) {
-    // the copies that this warp sent for land before the CTA leaves
-    if (leader)
-      for (int i = max(my_team, last - a.stages / nteam * nteam); i <= last; i += nteam)
-        mbar_wait(full + 8 * (i % a.stages), (i / a.stages) & 1);
-    if (lane == 0) atomicOr(a.status, 4u);
-  }
+  if (dead && lane == 0) atomicOr(a.status, 4u);
 }
 
 // Joins the parts of the items that were cut: CTA j owns the item that holds
@@ -983,18 +979,29 @@ size_t kd_workspace(const csa_shape* s, int T) {
   return 256 + (size_t)2 * kd_ctas(s) * R * (s->d + 2) * 4;
 }
 
-// as many blocks in the ring as shared memory holds beside the rest
 constexpr int kKdSharedBytes = 232448 - 2048;    // (2 KB: static arrays)
 template <int D, int RT, typename E>
 cudaError_t launch_kv4_decode_t(Kv4DecodeArgs a, int ncta, cudaStream_t st) {
   const int rest = KdLayout<D, RT>::ring(a.T * a.G);
-  a.stages = (kKdSharedBytes - rest) / KdStage<D>::bytes;
-  if (a.stages > kKdMaxStages) a.stages = kKdMaxStages;
-  const int smem = rest + a.stages * KdStage<D>::bytes;
+  // one slot per team in each ring (an SM's shared memory holds that for every
+  // RT and d), then more while there is room: keys first, whose copies have
+  // less time (the values' come while the warp is at the keys)
+  constexpr int K = KdStage<D>::bytesK, V = KdStage<D>::bytesV;
+  const int ntile = (a.T * a.G + RT - 1) / RT;
+  const int nteam = kKdWarps / (ntile <= 1 ? 1 : ntile <= 2 ? 2 : ntile <= 4 ? 4 : 8);
+  int nk = 1, nv = 1;
+  for (bool more = true; more;) {
+    more = false;
+    if ((nk + 1) * nteam <= kKdMaxStages && nteam * ((nk + 1) * K + nv * V) <= kKdSharedBytes - rest) { ++nk; more = true; }
+    if ((nv + 1) * nteam <= kKdMaxStages && nteam * (nk * K + (nv + 1) * V) <= kKdSharedBytes - rest) { ++nv; more = true; }
+  }
+  a.slotsK = nk * nteam;
+  a.slotsV = nv * nteam;
+  const int smem = rest + a.slotsK * K + a.slotsV * V;
   const cudaError_t e =
       cudaFuncSetAttribute(kv4_decode_kernel<D, RT, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  launch_pdl(kv4_decode_kernel<D, RT, E>, dim3(ncta), dim3(kd_warps<RT>() * 32), smem, st, a);
+  launch_pdl(kv4_decode_kernel<D, RT, E>, dim3(ncta), dim3(kKdThreads), smem, st, a);
   if (ncta > 1) launch_pdl(kv4_join_kernel<D>, dim3(ncta - 1), dim3(256), 0, st, a, ncta);
   return cudaGetLastError();
 }
