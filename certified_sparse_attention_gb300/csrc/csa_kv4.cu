@@ -2,9 +2,9 @@
 // and reading rows back.
 //
 // append: one CTA per (sequence, KV head, block of 64 positions that the new
-// tokens touch).  A block that becomes whole is gathered in shared memory
-// (its first rows may lie in the kept rows Kt, Vt, the others among the new
-// ones) and coded; the rows of the block that stays incomplete are copied to
+// tokens touch).  A block that becomes whole is gathered in registers (its
+// first rows may lie in the kept rows Kt, Vt, the others among the new ones)
+// and coded; the rows of the block that stays incomplete are copied to
 // Kt, Vt.  When a call both completes a block and leaves a new incomplete
 // one, the CTA of the first block writes the kept rows, after it has read
 // the old ones: nobody else reads or writes them.
@@ -41,14 +41,6 @@ struct Kv4UnpackArgs {
   int B, Hkv;
 };
 
-// Place of token t of a block among the 64 nibbles of a V4 row, and back.
-__host__ __device__ __forceinline__ int v4_place(int t) {
-  return 16 * ((t >> 1) & 3) + 8 * (t >> 5) + 4 * (t & 1) + 2 * ((t >> 4) & 1) + ((t >> 3) & 1);
-}
-__host__ __device__ __forceinline__ int v4_token(int p) {
-  return 32 * ((p >> 3) & 1) + 16 * ((p >> 1) & 1) + 8 * (p & 1) + 2 * (p >> 4) + ((p >> 2) & 1);
-}
-
 // minimum and maximum that keep a NaN
 __device__ __forceinline__ float min_nan(float a, float b) {
   float r;
@@ -65,14 +57,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 __device__ __forceinline__ unsigned code4(float x, float m, float step) {
   return (unsigned)fminf(fmaxf(rintf(fdiv(fsub(x, m), step)), 0.0f), 15.0f);
 }
-__device__ __forceinline__ float value4(unsigned code, float m, float step) {
-  return fadd(fmul((float)code, step), m);
-}
-
-template <typename E> __device__ __forceinline__ E to_elem(float x);
-template <> __device__ __forceinline__ float to_elem<float>(float x) { return x; }
-template <> __device__ __forceinline__ __nv_bfloat16 to_elem<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-
 constexpr int kKv4Threads = 256;
 
 // the status word of a call: set by one warp of its first CTA
@@ -81,14 +65,71 @@ __device__ __forceinline__ void report_range(unsigned* status, bool bad) {
   if ((threadIdx.x & 31) == 0) *status = any ? 8u : 0u;
 }
 
+// Codes of values whose step is in the normal range: the product with the
+// reciprocal, off by less than 1e-5 (a quotient up to 15, three roundings),
+// decides unless it lies that close to the middle between two codes; only
+// then is the quotient itself computed (on 16-bit inputs, whose quotients are
+// often exactly half way, about one in a thousand).  The division on every
+// value doubled the time of a long append.
+__device__ __forceinline__ bool step_plain(float step) { return step > 1e-30f && step < 1e30f; }
+__device__ __forceinline__ unsigned code4(float x, float m, float step, float inv, bool plain) {
+  const float y = fsub(x, m) * inv;
+  const float q = rintf(y);
+  if (plain && fabsf(y - q) < 0.49999f) return (unsigned)fminf(q, 15.0f);
+  return code4(x, m, step);
+}
+
+// v[e] (e = 0 .. 7): value of row e in this lane.  Returns in v[0] the minimum
+// (maximum) over the warp of row lane % 8.
+template <bool MAX>
+__device__ __forceinline__ void reduce8_minmax(float (&v)[8]) {
+  const int lane = threadIdx.x & 31;
+  const auto op = [](float a, float b) { return MAX ? max_nan(a, b) : min_nan(a, b); };
+#pragma unroll
+  for (int s = 0; s < 3; ++s) {
+    const bool hi = (lane >> s) & 1;
+#pragma unroll
+    for (int i = 0; i < (4 >> s); ++i) {
+      const float send = hi ? v[2 * i] : v[2 * i + 1], keep = hi ? v[2 * i + 1] : v[2 * i];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, 1 << s));
+    }
+  }
+  v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 8));
+  v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
+}
+
+template <int CPL, typename E> struct Row {};      // CPL consecutive elements
+template <> struct Row<4, __nv_bfloat16> { typedef uint2 T; };
+template <> struct Row<2, __nv_bfloat16> { typedef unsigned T; };
+template <> struct Row<4, float> { typedef float4 T; };
+template <> struct Row<2, float> { typedef float2 T; };
+template <int CPL>
+__device__ __forceinline__ void row_floats(const typename Row<CPL, __nv_bfloat16>::T& r, float (&x)[CPL], __nv_bfloat16) {
+  const unsigned* u = reinterpret_cast<const unsigned*>(&r);
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) x[c] = __uint_as_float(c & 1 ? u[c / 2] & 0xFFFF0000u : u[c / 2] << 16);
+}
+template <int CPL>
+__device__ __forceinline__ void row_floats(const typename Row<CPL, float>::T& r, float (&x)[CPL], float) {
+  const float* f = reinterpret_cast<const float*>(&r);
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) x[c] = f[c];
+}
+
+// Warp w takes the eight tokens of word w of the value rows, 32 i + 16 u + 8 v
+// + 2 (w / 2) + e with i = w % 2, of which lane l holds the channels [l D / 32,
+// (l + 1) D / 32): all 16 rows (K and V) are loaded at once, a row by one
+// access of the warp, and stay in registers.  A key channel's minimum and
+// maximum go over the warps (shared memory), a value row's over the lanes.
+// Bound by memory: 32K tokens x 8 heads in bf16, read and coded.
 template <int D, typename E>
 __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const Kv4AppendArgs a) {
   pdl_entry();
-  extern __shared__ __align__(16) uint8_t sm_raw[];
-  float* s_x = reinterpret_cast<float*>(sm_raw);                 // [64][D + 1]
-  float* s_mn = s_x + kBlock * (D + 1);                          // [D]
-  float* s_dl = s_mn + D;                                        // [D]
-  const int tid = threadIdx.x;
+  constexpr int CPL = D / 32;
+  typedef typename Row<CPL, E>::T RowT;
+  __shared__ __align__(16) float s_lo[8][D], s_hi[8][D];
+  __shared__ __align__(16) unsigned s_v[8][D];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int g = blockIdx.y, b = blockIdx.z;
   if (a.status && blockIdx.x == 0 && g == 0 && b == 0 && tid < 32) {
     bool bad = false;
@@ -111,83 +152,148 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const Kv4Append
   const E* kn = reinterpret_cast<const E*>(a.k) + b * a.ks.b + g * a.ks.h;
   const E* vn = reinterpret_cast<const E*>(a.v) + b * a.vs.b + g * a.vs.h;
   if (blk < whole) {
-    const int64_t p0 = blk * kBlock;
-    const int64_t at = bg * a.nblk_max + blk;
-    for (int i = tid; i < kBlock * D; i += kKv4Threads) {
-      const int r = i / D, c = i - r * D;
-      const int64_t p = p0 + r;
-      s_x[r * (D + 1) + c] = Elem<E>::get(p < start ? Kt + r * D : kn + (p - start) * a.ks.t, c);
+    const int64_t p0 = blk * kBlock, at = bg * a.nblk_max + blk;
+    const int t0 = 32 * (w & 1) + 2 * (w >> 1);
+    RowT rk[8], rv[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int t = t0 + 16 * ((e >> 1) & 1) + 8 * (e & 1) + (e >> 2);
+      const int64_t p = p0 + t;
+      const E* k = p < start ? Kt + t * D : kn + (p - start) * a.ks.t;
+      const E* v = p < start ? Vt + t * D : vn + (p - start) * a.vs.t;
+      rk[e] = *reinterpret_cast<const RowT*>(k + lane * CPL);
+      rv[e] = *reinterpret_cast<const RowT*>(v + lane * CPL);
     }
-    __syncthreads();
     // keys: one (m, Delta) per channel
-    if (tid < D) {
-      float mn = INFINITY, mx = -INFINITY;
-      for (int r = 0; r < kBlock; ++r) {
-        mn = min_nan(mn, s_x[r * (D + 1) + tid]);
-        mx = max_nan(mx, s_x[r * (D + 1) + tid]);
-      }
-      float dl = fdiv(fsub(mx, mn), 15.0f);
-      if (dl == 0.0f) dl = 1.0f;
-      s_mn[tid] = mn; s_dl[tid] = dl;
-      a.c.bounds[at * 2 * D + tid] = mn;
-      a.c.bounds[at * 2 * D + D + tid] = dl;
-    }
-    __syncthreads();
-    unsigned* K4 = reinterpret_cast<unsigned*>(a.c.K4 + at * kBlock * (D / 2));
-    for (int i = tid; i < kBlock * D / 8; i += kKv4Threads) {
-      const int r = i / (D / 8), c = (i - r * (D / 8)) * 8;
-      unsigned w = 0;
+    float lo[CPL], hi[CPL], x[CPL];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w |= code4(s_x[r * (D + 1) + c + e], s_mn[c + e], s_dl[c + e]) << (4 * e);
-      K4[i] = w;
-    }
-    __syncthreads();
-    for (int i = tid; i < kBlock * D; i += kKv4Threads) {
-      const int r = i / D, c = i - r * D;
-      const int64_t p = p0 + r;
-      s_x[r * (D + 1) + c] = Elem<E>::get(p < start ? Vt + r * D : vn + (p - start) * a.vs.t, c);
-    }
-    __syncthreads();
-    // values: one (m, Delta) per token
-    if (tid < kBlock) {
-      float mn = INFINITY, mx = -INFINITY;
-      for (int c = 0; c < D; ++c) {
-        mn = min_nan(mn, s_x[tid * (D + 1) + c]);
-        mx = max_nan(mx, s_x[tid * (D + 1) + c]);
-      }
-      const float dl = fdiv(fsub(mx, mn), 15.0f);
-      s_mn[tid] = mn; s_dl[tid] = dl;
-      reinterpret_cast<float2*>(a.c.vscale)[at * kBlock + tid] = make_float2(mn, dl);
-    }
-    __syncthreads();
-    unsigned* V4 = reinterpret_cast<unsigned*>(a.c.V4 + at * D * (kBlock / 2));
-    for (int i = tid; i < kBlock * D / 8; i += kKv4Threads) {
-      const int c = i / (kBlock / 8), p = (i - c * (kBlock / 8)) * 8;
-      unsigned w = 0;
+    for (int c = 0; c < CPL; ++c) { lo[c] = INFINITY; hi[c] = -INFINITY; }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int t = v4_token(p + e);
-        w |= code4(s_x[t * (D + 1) + c], s_mn[t], s_dl[t]) << (4 * e);   // (Delta = 0: 0/0, code 0)
-      }
-      V4[i] = w;
+    for (int e = 0; e < 8; ++e) {
+      row_floats<CPL>(rk[e], x, E());
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) { lo[c] = min_nan(lo[c], x[c]); hi[c] = max_nan(hi[c], x[c]); }
     }
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) { s_lo[w][lane * CPL + c] = lo[c]; s_hi[w][lane * CPL + c] = hi[c]; }
+    // values: one (m, Delta) per token, over the lanes meanwhile
+    float vlo[8], vhi[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      row_floats<CPL>(rv[e], x, E());
+      vlo[e] = vhi[e] = x[0];
+#pragma unroll
+      for (int c = 1; c < CPL; ++c) { vlo[e] = min_nan(vlo[e], x[c]); vhi[e] = max_nan(vhi[e], x[c]); }
+    }
+    reduce8_minmax<false>(vlo);
+    reduce8_minmax<true>(vhi);
+    const float vstep = fdiv(fsub(vhi[0], vlo[0]), 15.0f);
+    const float vm = vlo[0], vinv = 1.0f / vstep;
+    if (lane < 8)
+      reinterpret_cast<float2*>(a.c.vscale)[at * kBlock + t0 + 16 * ((lane >> 1) & 1) + 8 * (lane & 1) + (lane >> 2)] =
+          make_float2(vm, vstep);
+    unsigned word[CPL];
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) word[c] = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float me = __shfl_sync(0xffffffffu, vm, e), de = __shfl_sync(0xffffffffu, vstep, e);
+      const float ie = __shfl_sync(0xffffffffu, vinv, e);
+      const bool plain = step_plain(de);
+      row_floats<CPL>(rv[e], x, E());
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) word[c] |= code4(x[c], me, de, ie, plain) << (4 * e);   // (Delta = 0: 0/0, code 0)
+    }
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) s_v[w][lane * CPL + c] = word[c];
     __syncthreads();
+    float inv[CPL];
+    bool plain = true;
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        lo[c] = min_nan(lo[c], s_lo[i][lane * CPL + c]);
+        hi[c] = max_nan(hi[c], s_hi[i][lane * CPL + c]);
+      }
+      hi[c] = fdiv(fsub(hi[c], lo[c]), 15.0f);     // the step from here on
+      if (hi[c] == 0.0f) hi[c] = 1.0f;
+      inv[c] = 1.0f / hi[c];
+      plain = plain && step_plain(hi[c]);
+    }
+    if (w == 0) {
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) {
+        a.c.bounds[at * 2 * D + lane * CPL + c] = lo[c];
+        a.c.bounds[at * 2 * D + D + lane * CPL + c] = hi[c];
+      }
+    }
+    uint8_t* K4 = a.c.K4 + at * kBlock * (D / 2) + lane * (CPL / 2);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int t = t0 + 16 * ((e >> 1) & 1) + 8 * (e & 1) + (e >> 2);
+      row_floats<CPL>(rk[e], x, E());
+      unsigned code = 0;
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) code |= code4(x[c], lo[c], hi[c], inv[c], plain) << (4 * c);
+      if (CPL == 4) *reinterpret_cast<uint16_t*>(K4 + t * (D / 2)) = (uint16_t)code;
+      else K4[t * (D / 2)] = (uint8_t)code;
+    }
+    // value words, four of a channel's eight by a thread
+    if (tid < 2 * D) {
+      const int c = tid >> 1, q = (tid & 1) * 4;
+      reinterpret_cast<uint4*>(a.c.V4 + at * D * (kBlock / 2))[tid] =
+          make_uint4(s_v[q][c], s_v[q + 1][c], s_v[q + 2][c], s_v[q + 3][c]);
+    }
   }
-  // the rows of the block that stays incomplete
+  // the rows of the block that stays incomplete (after every warp has read
+  // the old ones: they are all in registers since the barrier above)
   if (blk == blk0) {
     const int64_t p0 = max(start, whole * kBlock);
-    for (int64_t i = tid; i < (n - p0) * D; i += kKv4Threads) {
-      const int64_t p = p0 + i / D;
-      const int c = (int)(i % D);
-      Kt[(p % kBlock) * D + c] = kn[(p - start) * a.ks.t + c];
-      Vt[(p % kBlock) * D + c] = vn[(p - start) * a.vs.t + c];
+    const int left = (int)(n - p0);       // below 64
+    for (int r = w; r < left; r += kKv4Threads / 32) {
+      const int64_t p = p0 + r;
+      const RowT k = *reinterpret_cast<const RowT*>(kn + (p - start) * a.ks.t + lane * CPL);
+      const RowT v = *reinterpret_cast<const RowT*>(vn + (p - start) * a.vs.t + lane * CPL);
+      *reinterpret_cast<RowT*>(Kt + (p % kBlock) * D + lane * CPL) = k;
+      *reinterpret_cast<RowT*>(Vt + (p % kBlock) * D + lane * CPL) = v;
     }
   }
 }
 
+// eight codes of a word as floats: the nibble under the exponent of 2^23,
+// minus 2^23
+__device__ __forceinline__ float nibble(unsigned word, int k) {
+  return __uint_as_float(((word >> (4 * k)) & 15u) | 0x4B000000u) - 8388608.0f;
+}
+template <typename E>
+__device__ __forceinline__ void store8(E* dst, const float (&x)[8]);
+template <> __device__ __forceinline__ void store8<float>(float* dst, const float (&x)[8]) {
+  reinterpret_cast<float4*>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+template <> __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* dst, const float (&x)[8]) {
+  unsigned u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    u[i] = *reinterpret_cast<const unsigned*>(&v);
+  }
+  *reinterpret_cast<uint4*>(dst) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// Half of the threads take the keys, half the values; a thread produces eight
+// channels of a row at a time.  Keys: the eight channels' bounds stay in
+// registers while the thread walks down the rows, one code word a row.
+// Values: eight words, one of each channel, hold eight tokens of eight
+// channels; the codes pass through shared memory, eight rows 260 bytes apart
+// so that the threads of a row read different banks.
 template <int D, typename E>
 __global__ void __launch_bounds__(kKv4Threads) kv4_unpack_kernel(const Kv4UnpackArgs a) {
   pdl_entry();
+  constexpr int CG = D / 8;                         // groups of eight channels
+  constexpr int HALF = kKv4Threads / 2;
+  __shared__ unsigned s_v[CG * 65];
   const int tid = threadIdx.x;
   const int g = blockIdx.y, b = blockIdx.z;
   if (a.status && blockIdx.x == 0 && g == 0 && b == 0 && tid < 32) {
@@ -204,27 +310,69 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_unpack_kernel(const Kv4Unpack
   const int64_t blk = first / kBlock + blockIdx.x;
   const int64_t p0 = max(first, blk * kBlock), p1 = min(end, (blk + 1) * kBlock);
   if (p0 >= p1) return;
+  const int r0 = (int)(p0 - blk * kBlock), r1 = (int)(p1 - blk * kBlock);     // rows [r0, r1) of the block
   const int64_t bg = (int64_t)b * a.Hkv + g;
   const int64_t at = bg * a.nblk_max + blk;
-  const bool coded = blk < n / kBlock;
-  E* Ko = reinterpret_cast<E*>(a.K) + bg * a.rows * D;
-  E* Vo = reinterpret_cast<E*>(a.V) + bg * a.rows * D;
-  const int count = (int)(p1 - p0) * D;
-  for (int i = tid; i < count; i += kKv4Threads) {
-    const int64_t p = p0 + i / D;
-    const int r = (int)(p % kBlock), c = i % D;
-    const int64_t out = (p - first) * D + c;
-    if (!coded) {
-      Ko[out] = reinterpret_cast<const E*>(a.c.Kt)[(bg * kBlock + r) * D + c];
-      Vo[out] = reinterpret_cast<const E*>(a.c.Vt)[(bg * kBlock + r) * D + c];
-      continue;
+  // row r of the block is row blk * 64 + r - first of the output
+  const int64_t out = (bg * a.rows + blk * kBlock - first) * D;
+  E* Ko = reinterpret_cast<E*>(a.K) + out;
+  E* Vo = reinterpret_cast<E*>(a.V) + out;
+  const int cg = tid % CG;
+  if (blk >= n / kBlock) {
+    const int half = tid / HALF;
+    const E* src = reinterpret_cast<const E*>(half ? a.c.Vt : a.c.Kt) + bg * kBlock * D;
+    E* dst = half ? Vo : Ko;
+    constexpr int Q = 8 * sizeof(E) / 16;
+    for (int r = r0 + tid % HALF / CG; r < r1; r += HALF / CG) {
+#pragma unroll
+      for (int i = 0; i < Q; ++i)
+        reinterpret_cast<uint4*>(dst + r * D + cg * 8)[i] = reinterpret_cast<const uint4*>(src + r * D + cg * 8)[i];
     }
-    const unsigned kb = a.c.K4[(at * kBlock + r) * (D / 2) + c / 2];
-    Ko[out] = to_elem<E>(value4((kb >> (4 * (c & 1))) & 15u, a.c.bounds[at * 2 * D + c], a.c.bounds[at * 2 * D + D + c]));
-    const int pl = v4_place(r);
-    const unsigned vb = a.c.V4[(at * D + c) * (kBlock / 2) + pl / 2];
-    const float2 sc = reinterpret_cast<const float2*>(a.c.vscale)[at * kBlock + r];
-    Vo[out] = to_elem<E>(value4((vb >> (4 * (pl & 1))) & 15u, sc.x, sc.y));
+    return;
+  }
+  const unsigned* V4 = reinterpret_cast<const unsigned*>(a.c.V4 + at * D * (kBlock / 2));
+  for (int i = tid; i < D * 8; i += kKv4Threads) s_v[i / 64 * 65 + i % 64] = V4[i];
+  if (tid < HALF) {
+    float m[8], dl[8];
+    const float* bp = a.c.bounds + at * 2 * D + cg * 8;
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      const float4 u = *reinterpret_cast<const float4*>(bp + i), v = *reinterpret_cast<const float4*>(bp + D + i);
+      m[i] = u.x; m[i + 1] = u.y; m[i + 2] = u.z; m[i + 3] = u.w;
+      dl[i] = v.x; dl[i + 1] = v.y; dl[i + 2] = v.z; dl[i + 3] = v.w;
+    }
+    const unsigned* K4 = reinterpret_cast<const unsigned*>(a.c.K4 + at * kBlock * (D / 2));
+    constexpr int STEP = HALF / CG;                 // rows between a thread's rows
+    unsigned word[kBlock / STEP];
+#pragma unroll
+    for (int j = 0; j < kBlock / STEP; ++j) word[j] = K4[(tid / CG + j * STEP) * CG + cg];
+#pragma unroll
+    for (int j = 0; j < kBlock / STEP; ++j) {
+      const int r = tid / CG + j * STEP;
+      float x[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) x[c] = fadd(fmul(nibble(word[j], c), dl[c]), m[c]);
+      if (r >= r0 && r < r1) store8<E>(Ko + r * D + cg * 8, x);
+    }
+  }
+  __syncthreads();
+  if (tid >= HALF) {
+    // word wi: tokens 32 i + 16 u + 8 v + 2 w + e, i = wi % 2, w = wi / 2
+    for (int wi = (tid - HALF) / CG; wi < 8; wi += HALF / CG) {
+      unsigned word[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) word[c] = s_v[cg * 65 + c * 8 + wi];
+      const int t0 = 32 * (wi & 1) + 2 * (wi >> 1);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int r = t0 + 16 * ((e >> 1) & 1) + 8 * (e & 1) + (e >> 2);
+        const float2 sc = reinterpret_cast<const float2*>(a.c.vscale)[at * kBlock + r];
+        float x[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x[c] = fadd(fmul(nibble(word[c], e), sc.y), sc.x);
+        if (r >= r0 && r < r1) store8<E>(Vo + r * D + cg * 8, x);
+      }
+    }
   }
 }
 
@@ -232,10 +380,7 @@ namespace {
 
 template <int D, typename E>
 cudaError_t launch_append(const Kv4AppendArgs& a, dim3 grid, cudaStream_t st) {
-  const int smem = (kBlock * (D + 1) + 2 * D) * 4;
-  const cudaError_t e = cudaFuncSetAttribute(kv4_append_kernel<D, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  launch_pdl(kv4_append_kernel<D, E>, grid, dim3(kKv4Threads), smem, st, a);
+  launch_pdl(kv4_append_kernel<D, E>, grid, dim3(kKv4Threads), 0, st, a);
   return cudaGetLastError();
 }
 

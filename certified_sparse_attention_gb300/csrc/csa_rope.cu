@@ -11,11 +11,11 @@
 // reduction to lose digits in.
 //
 // Bound by memory: every row is read once and written once.  A row is held
-// by d / 8 lanes as two vectors of four channels each.  With split pairs
-// (i, i + rot / 2) the two vectors of a lane are partners, so the rotation
-// needs no exchange between lanes; with adjacent pairs the partners are in
-// one vector.  The lanes' eight sines and cosines serve every head of the
-// token that the lanes process.
+// by lanes with two vectors of 4 (8: bf16, 16 bytes) channels each.  With
+// split pairs (i, i + rot / 2) the two vectors of a lane are partners, so the
+// rotation needs no exchange between lanes; with adjacent pairs the partners
+// are in one vector.  A lane's sines and cosines serve every head of the
+// token that it processes.
 #include <cmath>
 
 #include "csa_args.cuh"
@@ -38,27 +38,41 @@ struct RopeArgs {
   unsigned* status;
   int64_t n_max;
   int B, T, Hq, Hkv;
+  int heads;          // heads to process: q, k and, when given, v
   int rot, interleaved, to_cache;
   int heads_per;      // heads of a token that one group of lanes processes
   int nchunk;         // groups per token
   float eps;
 };
 
-template <typename E> struct Vec4;
-template <> struct Vec4<float> {
+// VEC consecutive elements
+template <typename E, int VEC> struct Vec;
+template <> struct Vec<float, 4> {
   typedef float4 Raw;
-  static __device__ __forceinline__ float4 widen(Raw r) { return r; }
-  static __device__ __forceinline__ Raw narrow(float4 f) { return f; }
+  static __device__ __forceinline__ void widen(const Raw& r, float (&x)[4]) { x[0] = r.x; x[1] = r.y; x[2] = r.z; x[3] = r.w; }
+  static __device__ __forceinline__ Raw narrow(const float (&x)[4]) { return make_float4(x[0], x[1], x[2], x[3]); }
 };
-template <> struct Vec4<__nv_bfloat16> {
+__device__ __forceinline__ unsigned bf16_pair(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const unsigned*>(&v);
+}
+template <> struct Vec<__nv_bfloat16, 4> {
   typedef uint2 Raw;
-  static __device__ __forceinline__ float4 widen(Raw u) {
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xFFFF0000u));
+  static __device__ __forceinline__ void widen(const Raw& r, float (&x)[4]) {
+    x[0] = __uint_as_float(r.x << 16); x[1] = __uint_as_float(r.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(r.y << 16); x[3] = __uint_as_float(r.y & 0xFFFF0000u);
   }
-  static __device__ __forceinline__ Raw narrow(float4 f) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(f.x, f.y), b = __floats2bfloat162_rn(f.z, f.w);
-    return make_uint2(*reinterpret_cast<const unsigned*>(&a), *reinterpret_cast<const unsigned*>(&b));
+  static __device__ __forceinline__ Raw narrow(const float (&x)[4]) { return make_uint2(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])); }
+};
+template <> struct Vec<__nv_bfloat16, 8> {
+  typedef uint4 Raw;
+  static __device__ __forceinline__ void widen(const Raw& r, float (&x)[8]) {
+    const unsigned u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(i & 1 ? u[i / 2] & 0xFFFF0000u : u[i / 2] << 16);
+  }
+  static __device__ __forceinline__ Raw narrow(const float (&x)[8]) {
+    return make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
   }
 };
 
@@ -82,12 +96,13 @@ __device__ __forceinline__ bool new_tokens(const int64_t* len, const int64_t* n_
 constexpr int kRopeThreads = 128;
 constexpr int kRopeBatch = 4;     // rows of a group of lanes in flight
 
-template <int D, typename E>
+template <int D, int VEC, typename E>
 __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeArgs a) {
   pdl_entry();
-  constexpr int LPR = D / 8;                 // lanes per row
+  typedef Vec<E, VEC> Vx;
+  typedef typename Vx::Raw Raw;
+  constexpr int LPR = D / (2 * VEC);         // lanes per row
   constexpr int RPB = kRopeThreads / LPR;    // groups of lanes per CTA
-  typedef typename Vec4<E>::Raw Raw;
   const int j = threadIdx.x % LPR;
   const int64_t cap = a.to_cache ? a.n_max : INT64_MAX;
   if (a.status && blockIdx.x == 0 && threadIdx.x < 32) {
@@ -103,43 +118,27 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
   const int64_t tok = item / a.nchunk;
   const int chunk = (int)(item - tok * a.nchunk);
   const int b = (int)(tok / a.T), t = (int)(tok - (int64_t)b * a.T);
-  // (lanes of a warp leave together or stay together for the shuffles below:
-  // the mask of a group's shuffles names its own lanes only)
+  // (a group of lanes leaves as a whole; the shuffles below name its lanes)
   int64_t start = 0, m = 0;
   if (b >= a.B || !new_tokens(a.len, a.n_new, b, a.T, cap, start, m) || t >= m) return;
   const int64_t pos = start + t;
 
-  const bool turns_here = j < a.rot / 8;
-  int c0, c1, p0, p1;   // first channels of the two vectors, first pairs
-  if (a.interleaved) {
-    c0 = 8 * j; c1 = c0 + 4;
-    p0 = 4 * j; p1 = p0 + 2;
-  } else {
-    c0 = turns_here ? 4 * j : a.rot + 8 * (j - a.rot / 8);
-    c1 = turns_here ? c0 + a.rot / 2 : c0 + 4;
-    p0 = 4 * j; p1 = p0 + 2;
-  }
-  const int h_lo = chunk * a.heads_per, h_hi = min(h_lo + a.heads_per, a.Hq + 2 * a.Hkv);
-  float cs[4], sn[4];
+  const bool turns_here = 2 * VEC * j < a.rot;
+  // first channels of the two vectors: split pairs sit rot / 2 apart
+  const int c0 = !a.interleaved && turns_here ? VEC * j : 2 * VEC * j;
+  const int c1 = !a.interleaved && turns_here ? c0 + a.rot / 2 : c0 + VEC;
+  const int h_lo = chunk * a.heads_per, h_hi = min(h_lo + a.heads_per, a.heads);
+  float cs[VEC], sn[VEC];
   if (turns_here && h_lo < a.Hq + a.Hkv) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int p = i < 2 ? p0 + i : p1 + i - 2;
-      const long long frac = (long long)((unsigned long long)pos * a.turns[p]);   // signed: [-1/2, 1/2) turn
-      sincospif((float)frac * 1.0842021724855044e-19f, &sn[i], &cs[i]);           // 2^-63: in units of pi
+    for (int i = 0; i < VEC; ++i) {
+      const long long frac = (long long)((unsigned long long)pos * a.turns[VEC * j + i]);   // signed: [-1/2, 1/2) turn
+      sincospif((float)frac * 1.0842021724855044e-19f, &sn[i], &cs[i]);                     // 2^-63: in units of pi
     }
   }
-  float4 wq0, wq1, wk0, wk1;
-  if (a.wq) {
-    wq0 = Vec4<E>::widen(*reinterpret_cast<const Raw*>(reinterpret_cast<const E*>(a.wq) + c0));
-    wq1 = Vec4<E>::widen(*reinterpret_cast<const Raw*>(reinterpret_cast<const E*>(a.wq) + c1));
-  }
-  if (a.wk) {
-    wk0 = Vec4<E>::widen(*reinterpret_cast<const Raw*>(reinterpret_cast<const E*>(a.wk) + c0));
-    wk1 = Vec4<E>::widen(*reinterpret_cast<const Raw*>(reinterpret_cast<const E*>(a.wk) + c1));
-  }
-  const unsigned group_mask =
-      LPR == 16 ? 0xffffu << (threadIdx.x & 16) : 0xffu << (threadIdx.x & 24);
+  float w0[VEC], w1[VEC];
+  const void* have = nullptr;       // the weights that w0, w1 hold
+  const unsigned group_mask = (unsigned)((1ull << LPR) - 1) << (threadIdx.x % 32 / LPR * LPR);
   const E* qrow = reinterpret_cast<const E*>(a.q) + b * a.qs.b + t * a.qs.t;
   const E* krow = reinterpret_cast<const E*>(a.k) + b * a.ks.b + t * a.ks.t;
   const E* vrow = reinterpret_cast<const E*>(a.v) + b * a.vs.b + t * a.vs.t;
@@ -149,7 +148,7 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
 #pragma unroll
     for (int i = 0; i < kRopeBatch; ++i) {
       const int h = h0 + i;
-      if (h >= h_hi || (h >= a.Hq + a.Hkv && !a.v)) continue;
+      if (h >= h_hi) continue;
       const E* src = h < a.Hq ? qrow + h * a.qs.h
                    : h < a.Hq + a.Hkv ? krow + (h - a.Hq) * a.ks.h : vrow + (h - a.Hq - a.Hkv) * a.vs.h;
       r0[i] = *reinterpret_cast<const Raw*>(src + c0);
@@ -158,7 +157,7 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
 #pragma unroll
     for (int i = 0; i < kRopeBatch; ++i) {
       const int h = h0 + i;
-      if (h >= h_hi || (h >= a.Hq + a.Hkv && !a.v)) continue;
+      if (h >= h_hi) continue;
       E* dst;
       if (h < a.Hq) {
         dst = reinterpret_cast<E*>(a.q_out) + (((int64_t)b * a.T + t) * a.Hq + h) * D;
@@ -169,28 +168,39 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
                           : (((int64_t)b * a.T + t) * a.Hkv + g) * D);
       }
       if (h < a.Hq + a.Hkv) {
-        float4 x = Vec4<E>::widen(r0[i]), y = Vec4<E>::widen(r1[i]);
-        if (h < a.Hq ? a.wq != nullptr : a.wk != nullptr) {
-          float ss = ((x.x * x.x + x.y * x.y) + (x.z * x.z + x.w * x.w)) +
-                     ((y.x * y.x + y.y * y.y) + (y.z * y.z + y.w * y.w));
+        float x[VEC], y[VEC];
+        Vx::widen(r0[i], x);
+        Vx::widen(r1[i], y);
+        const void* wt = h < a.Hq ? a.wq : a.wk;
+        if (wt) {
+          if (wt != have) {
+            Vx::widen(*reinterpret_cast<const Raw*>(reinterpret_cast<const E*>(wt) + c0), w0);
+            Vx::widen(*reinterpret_cast<const Raw*>(reinterpret_cast<const E*>(wt) + c1), w1);
+            have = wt;
+          }
+          float ss = 0.0f;
+#pragma unroll
+          for (int c = 0; c < VEC; ++c) ss += x[c] * x[c] + y[c] * y[c];
 #pragma unroll
           for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group_mask, ss, o);
           const float inv = rsqrtf(ss * (1.0f / D) + a.eps);
-          const float4 w0 = h < a.Hq ? wq0 : wk0, w1 = h < a.Hq ? wq1 : wk1;
-          x.x *= inv * w0.x; x.y *= inv * w0.y; x.z *= inv * w0.z; x.w *= inv * w0.w;
-          y.x *= inv * w1.x; y.y *= inv * w1.y; y.z *= inv * w1.z; y.w *= inv * w1.w;
+#pragma unroll
+          for (int c = 0; c < VEC; ++c) { x[c] *= inv * w0[c]; y[c] *= inv * w1[c]; }
         }
         if (turns_here) {
           if (a.interleaved) {
-            turn_pair(x.x, x.y, cs[0], sn[0]); turn_pair(x.z, x.w, cs[1], sn[1]);
-            turn_pair(y.x, y.y, cs[2], sn[2]); turn_pair(y.z, y.w, cs[3], sn[3]);
+#pragma unroll
+            for (int c = 0; c < VEC; c += 2) {
+              turn_pair(x[c], x[c + 1], cs[c / 2], sn[c / 2]);
+              turn_pair(y[c], y[c + 1], cs[VEC / 2 + c / 2], sn[VEC / 2 + c / 2]);
+            }
           } else {
-            turn_pair(x.x, y.x, cs[0], sn[0]); turn_pair(x.y, y.y, cs[1], sn[1]);
-            turn_pair(x.z, y.z, cs[2], sn[2]); turn_pair(x.w, y.w, cs[3], sn[3]);
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) turn_pair(x[c], y[c], cs[c], sn[c]);
           }
         }
-        r0[i] = Vec4<E>::narrow(x);
-        r1[i] = Vec4<E>::narrow(y);
+        r0[i] = Vx::narrow(x);
+        r1[i] = Vx::narrow(y);
       }
       *reinterpret_cast<Raw*>(dst + c0) = r0[i];
       *reinterpret_cast<Raw*>(dst + c1) = r1[i];
@@ -198,9 +208,18 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
   }
 }
 
-template <int D, typename E>
-void launch_rope(const RopeArgs& a, int64_t blocks, cudaStream_t st) {
-  launch_pdl(qk_norm_rope_kernel<D, E>, dim3((unsigned)blocks), dim3(kRopeThreads), 0, st, a);
+template <int D, int VEC, typename E>
+cudaError_t launch_rope(RopeArgs a, int64_t tokens, cudaStream_t st) {
+  constexpr int RPB = kRopeThreads / (D / (2 * VEC));
+  // heads of a token to a group of lanes: the more, the fewer sines and
+  // cosines; but first enough groups for four CTAs on every SM
+  const int64_t per = tokens * a.heads / ((int64_t)sm_count() * 4 * RPB);
+  a.heads_per = (int)(per < 1 ? 1 : per > 16 ? 16 : per);
+  a.nchunk = (a.heads + a.heads_per - 1) / a.heads_per;
+  const int64_t blocks = (tokens * a.nchunk + RPB - 1) / RPB;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  launch_pdl(qk_norm_rope_kernel<D, VEC, E>, dim3((unsigned)blocks), dim3(kRopeThreads), 0, st, a);
+  return cudaGetLastError();
 }
 
 }  // namespace csa
@@ -255,18 +274,20 @@ csa_status csa_qk_norm_rope(const csa_shape* shape, int T, const csa_norm_rope* 
   a.q_out = q_out; a.K = K; a.V = V; a.status = status; a.n_max = shape->n_max;
   a.B = shape->B; a.T = T; a.Hq = shape->Hq; a.Hkv = shape->Hkv;
   a.rot = params->rot_dim; a.interleaved = params->interleaved; a.to_cache = to_cache; a.eps = params->norm_eps;
-  const int heads = shape->Hq + (v ? 2 : 1) * shape->Hkv;
+  a.heads = shape->Hq + (v ? 2 : 1) * shape->Hkv;
   const int64_t tokens = (int64_t)shape->B * T;
-  a.heads_per = 4;
-  a.nchunk = (heads + a.heads_per - 1) / a.heads_per;
-  const int64_t items = tokens * a.nchunk, per_cta = kRopeThreads / (d / 8);
-  const int64_t blocks = (items + per_cta - 1) / per_cta;
-  if (blocks > 0x7fffffff) return CSA_ERR_UNSUPPORTED;
   add_launches(1);
   cudaStream_t st = (cudaStream_t)stream;
-  if (d == 128) bf16 ? launch_rope<128, __nv_bfloat16>(a, blocks, st) : launch_rope<128, float>(a, blocks, st);
-  else bf16 ? launch_rope<64, __nv_bfloat16>(a, blocks, st) : launch_rope<64, float>(a, blocks, st);
-  return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+  // bf16: 16-byte accesses where the rotated part divides into them
+  const bool wide = params->rot_dim % 16 == 0;
+  cudaError_t e;
+  if (d == 128)
+    e = !bf16 ? launch_rope<128, 4, float>(a, tokens, st)
+        : wide ? launch_rope<128, 8, __nv_bfloat16>(a, tokens, st) : launch_rope<128, 4, __nv_bfloat16>(a, tokens, st);
+  else
+    e = !bf16 ? launch_rope<64, 4, float>(a, tokens, st)
+        : wide ? launch_rope<64, 8, __nv_bfloat16>(a, tokens, st) : launch_rope<64, 4, __nv_bfloat16>(a, tokens, st);
+  return e == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -692,3 +692,29 @@ def test_rope_feeds_the_certified_step():
     assert bool((err <= beta * (1 + 2e-3) + 2e-3 * dense.norm(dim=-1)).all())
     ref, _ = kv4.attention(f64(last)[0, 2], f64(K)[0, 0], f64(V)[0, 0], n)
     assert np.abs(f64(dense)[0, 2] - ref).max() <= 1e-5 * np.abs(f64(V)).max()
+
+
+@pytest.mark.parametrize("rot,inter", [(24, False), (104, False), (40, True), (16, False), (128, False)])
+def test_rope_bf16_odd_rotations_and_many_heads(rot, inter):
+    # rotated parts that do not divide into 16-byte vectors; enough tokens for
+    # several heads to a group of lanes
+    torch, csa, dev = _t()
+    rng = np.random.default_rng(rot)
+    B, T, Hq, Hkv, d = 2, 700, 20, 5, 128
+    s = csa.make_shape(B, Hq, Hkv, d, 800, "bf16")
+    f = 10000.0 ** (-np.arange(rot // 2) / (rot // 2))
+    wq, wk = rows(rng, (d,), "bf16"), rows(rng, (d,), "bf16")
+    op = csa.QKNormRope(s, dev, wq, wk, inv_freq=f, interleaved=inter)
+    q, k, v = [rows(rng, (B, T, h, d), "bf16") for h in (Hq, Hkv, Hkv)]
+    K = torch.zeros(B, Hkv, 800, d, dtype=torch.bfloat16, device=dev)
+    V = torch.zeros_like(K)
+    qo = op(q, k, v, K, V, i64([800, 705]))
+    qn, kn, qx, kx = f64(qo), f64(K), f64(q), f64(k)
+    for b, t in ((0, 0), (0, 699), (1, 350), (1, 699)):
+        pos = (100 if b == 0 else 5) + t
+        for h in range(Hq):
+            check_rope(qn[b, t, h], qx[b, t, h], f64(wq), pos, f, inter, 1e-6, "bf16")
+        for g in range(Hkv):
+            check_rope(kn[b, g, pos], kx[b, t, g], f64(wk), pos, f, inter, 1e-6, "bf16")
+    assert torch.equal(V[0, :, 100:], v[0].transpose(0, 1))
+    assert torch.equal(V[1, :, 5:705], v[1].transpose(0, 1))
