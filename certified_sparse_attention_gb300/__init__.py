@@ -594,60 +594,82 @@ class DenseDecode:
 
 # ------------------------------------- rows before the cache, 4-bit cache
 
-def _device_index(t) -> int:
-    """Index of the GPU a tensor lies on (a host check; -1: not on one)."""
-    if not getattr(t, "is_cuda", False):
-        return -1
-    i = t.get_device() if hasattr(t, "get_device") else 0
-    return i
+# The checks below run on every call of a decode loop, where the calls of a
+# token take the device a few microseconds each: they look at each tensor's
+# shape, strides, type, device and address once.
+
+def _torch_type(shape: csa_shape):
+    import torch
+    return torch.float32 if shape.dtype == CSA_F32 else torch.bfloat16
 
 
-def _same_device(want: int, **tensors) -> None:
-    """Refuse tensors that do not lie on GPU ``want`` (None ones pass)."""
-    for name, t in tensors.items():
-        if t is not None and _device_index(t) != want:
-            raise ValueError(f"{name}: a tensor on CUDA device {want} is "
-                             "required")
-
-
-def _current(want: int) -> None:
-    """The library launches on the current device: refuse another one."""
+def _call_stream(stream, device: int) -> Optional[int]:
+    """The stream handle of a call on GPU ``device``, which must be the
+    current one (the library launches there): the given stream, or the
+    current one (asked for by its raw handle: torch.cuda.current_stream()
+    makes an object, 3 us)."""
     import torch
     have = torch.cuda.current_device()
-    if have != want:
-        raise ValueError(f"the buffers lie on CUDA device {want}, the "
+    if have != device:
+        raise ValueError(f"the buffers lie on CUDA device {device}, the "
                          f"current device is {have}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return _stream(stream)
 
 
-def _element_type(t, name: str, shape: csa_shape) -> None:
-    """Refuse a tensor of another element type than the shape's."""
-    if str(t.dtype) != ("torch.float32" if shape.dtype == CSA_F32
-                        else "torch.bfloat16"):
-        raise ValueError(f"{name}: {t.dtype}, the shape's element type is "
+def _rows(t, name: str, B: int, T: int, heads: int, d: int, dtype,
+          device: int):
+    """Check a strided [B][T][heads][d] operand (T 0: any); its address and
+    its (b, t, h) strides."""
+    sz = t.shape
+    if len(sz) != 4 or sz[0] != B or sz[2] != heads or sz[3] != d or \
+            (sz[1] != T if T else sz[1] < 1):
+        raise ValueError(f"{name}: shape {list(sz)}, [{B}][{T or 'T'}]"
+                         f"[{heads}][{d}] is required")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: {t.dtype}, {dtype} is required")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: a tensor on CUDA device {device} is "
                          "required")
+    sb, st, sh, sc = t.stride()
+    p, esz = t.data_ptr(), t.element_size()
+    if sc != 1 or ((sb | st | sh) * esz | p) & 15:
+        # (the stride of an axis of length one is never used)
+        if sc != 1 or p & 15 or any(n > 1 and s * esz & 15 for n, s in
+                                    zip(sz, (sb, st, sh))):
+            raise ValueError(f"{name}: channels must be contiguous and rows "
+                             "start at multiples of 16 bytes")
+    return p, sb, st, sh
 
 
-def _rows(t, name: str, shape: csa_shape, heads: int, T=None) -> int:
-    """Check a strided [B][T][heads][d] operand of the shape's type; its T."""
-    sz = tuple(t.shape)
-    if len(sz) != 4 or sz[0] != shape.B or sz[2] != heads or \
-            sz[3] != shape.d or sz[1] < 1 or (T is not None and sz[1] != T):
-        want = f"[{shape.B}][{'T' if T is None else T}][{heads}][{shape.d}]"
-        raise ValueError(f"{name}: shape {list(sz)}, {want} is required")
-    st = t.stride()
-    esz = 4 if shape.dtype == CSA_F32 else 2
-    _element_type(t, name, shape)
-    if st[3] != 1 or t.data_ptr() % 16 or any(
-            n > 1 and s * esz % 16 for n, s in zip(sz, st[:3])):
-        raise ValueError(f"{name}: channels must be contiguous and rows "
-                         "start at multiples of 16 bytes")
-    return sz[1]
+def _whole(t, name: str, size: tuple, dtype, device: int) -> int:
+    """Check a contiguous tensor of this size, aligned to 16 bytes; its
+    address."""
+    if t.shape != size or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{name}: {t.dtype} {list(t.shape)}, a contiguous "
+                         f"{dtype} tensor {list(size)} is required")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: a tensor on CUDA device {device} is "
+                         "required")
+    p = t.data_ptr()
+    if p & 15:
+        raise ValueError(f"{name}: must start at a multiple of 16 bytes")
+    return p
 
 
-def _counts(t, name: str, B: int) -> None:
-    if str(t.dtype) != "torch.int64" or tuple(t.shape) != (B,) or not t.is_contiguous():
+def _counts(t, name: str, B: int, device: int) -> Optional[int]:
+    """Check a device int64 [B] (or None); its address."""
+    if t is None:
+        return None
+    if t.dtype.itemsize != 8 or t.dtype.is_floating_point or \
+            t.dtype.is_complex or t.shape != (B,) or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous int64 tensor [{B}] is "
                          "required")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: a tensor on CUDA device {device} is "
+                         "required")
+    return t.data_ptr()
 
 
 class QKNormRope:
@@ -665,8 +687,9 @@ class QKNormRope:
                  interleaved: bool = False):
         import torch
         self.shape = shape
-        self.status = torch.zeros(1, dtype=torch.int32, device=device)
-        self.device = _device_index(self.status)
+        self.dtype = _torch_type(shape)
+        self.status = torch.zeros(4, dtype=torch.int32, device=device)
+        self.device = self.status.get_device()
         table = [] if inv_freq is None else csa_rope_turns(inv_freq)
         if len(table) * 2 > shape.d or len(table) % 4:
             raise ValueError(f"inv_freq: {len(table)} pairs; a multiple of 4 "
@@ -674,57 +697,51 @@ class QKNormRope:
         self.turns = torch.tensor(
             [u - (1 << 64) if u >> 63 else u for u in table],
             dtype=torch.int64, device=device) if table else None
-        _same_device(self.device, wq=wq, wk=wk)
-        for name, w in (("wq", wq), ("wk", wk)):
-            if w is not None:
-                _require(w, name, shape.d * w.element_size())
-                _element_type(w, name, shape)
-                if tuple(w.shape) != (shape.d,) or w.data_ptr() % 16:
-                    raise ValueError(f"{name}: an aligned tensor "
-                                     f"[{shape.d}] is required")
+        pw = [None if w is None else
+              _whole(w, name, (shape.d,), self.dtype, self.device)
+              for name, w in (("wq", wq), ("wk", wk))]
         self.weights = (wq, wk)
         self.params = csa_norm_rope(
-            _ptr(wq), _ptr(wk), float(norm_eps), 2 * len(table),
+            pw[0], pw[1], float(norm_eps), 2 * len(table),
             1 if interleaved else 0, _ptr(self.turns))
 
     def __call__(self, q, k, v, K, V, lens_dev, n_new=None,
                  to_cache: bool = True, q_out=None, stream=None):
         """q [B][T][Hq][d], k and v [B][T][Hkv][d] (views with any strides
-        of whole 16 bytes; v None: V is left alone); K, V: the cache
+        of whole 16 bytes; v and V None: no values); K, V: the cache
         [B][Hkv][n_max][d], or with to_cache=False rows [B][T][Hkv][d].
         lens_dev: device int64 [B], the new tokens counted already; n_new:
         device int64 [B] (None: T each).  Returns q_out [B][T][Hq][d] (made
         when not given)."""
-        import torch
-        s = self.shape
-        T = _rows(q, "q", s, s.Hq)
-        _rows(k, "k", s, s.Hkv, T)
+        s, dev, dt = self.shape, self.device, self.dtype
+        B, Hq, Hkv, d = s.B, s.Hq, s.Hkv, s.d
+        pq, qb, qt, qh = _rows(q, "q", B, 0, Hq, d, dt, dev)
+        T = q.shape[1]
+        pk, kb, kt, kh = _rows(k, "k", B, T, Hkv, d, dt, dev)
+        size = (B, Hkv, s.n_max, d) if to_cache else (B, T, Hkv, d)
+        pK = _whole(K, "K", size, dt, dev)
+        pv = pV = vs = None
         if v is not None:
-            _rows(v, "v", s, s.Hkv, T)
+            if V is None:
+                raise ValueError("V: missing")
+            pv, vb, vt, vh = _rows(v, "v", B, T, Hkv, d, dt, dev)
+            pV = _whole(V, "V", size, dt, dev)
+            vs = ctypes.byref(csa_strides(vb, vt, vh))
         elif V is not None:
             raise ValueError("V: given without v")
-        _counts(lens_dev, "lens_dev", s.B)
-        if n_new is not None:
-            _counts(n_new, "n_new", s.B)
-        rows = s.B * s.Hkv * (s.n_max if to_cache else T) * s.d
-        for name, t in (("K", K), ("V", V)):
-            if t is not None:
-                _element_type(t, name, s)
-                _require(t, name, rows * t.element_size())
-        if v is not None and V is None:
-            raise ValueError("V: missing")
+        pl = _counts(lens_dev, "lens_dev", B, dev)
+        pn = _counts(n_new, "n_new", B, dev)
         if q_out is None:
-            q_out = torch.empty((s.B, T, s.Hq, s.d), dtype=q.dtype,
-                                device=q.device)
-        else:
-            _rows(q_out, "q_out", s, s.Hq, T)
-            _require(q_out, "q_out", 0)
-        _same_device(self.device, q=q, k=k, v=v, K=K, V=V, lens_dev=lens_dev,
-                     n_new=n_new, q_out=q_out)
-        _current(self.device)
-        check(csa_qk_norm_rope(s, T, self.params, q, q, k, k, v, v, lens_dev,
-                               n_new, q_out, K, V, 1 if to_cache else 0,
-                               self.status, stream), "csa_qk_norm_rope")
+            q_out = q.new_empty((B, T, Hq, d))
+        po = _whole(q_out, "q_out", (B, T, Hq, d), dt, dev)
+        st = load_library().csa_qk_norm_rope(
+            ctypes.byref(s), T, ctypes.byref(self.params), pq,
+            ctypes.byref(csa_strides(qb, qt, qh)), pk,
+            ctypes.byref(csa_strides(kb, kt, kh)), pv, vs, pl, pn, po, pK,
+            pV, 1 if to_cache else 0, self.status.data_ptr(),
+            _call_stream(stream, dev))
+        if st:
+            raise CsaError(st, "csa_qk_norm_rope")
         return q_out
 
 
@@ -742,69 +759,69 @@ class KV4Cache:
             raise CsaError(2, "KV4Cache")
         B, H, d = shape.B, shape.Hkv, shape.d
         nblk = (shape.n_max + BLOCK - 1) // BLOCK
-        el = torch.float32 if shape.dtype == CSA_F32 else torch.bfloat16
+        self.dtype = el = _torch_type(shape)
         layout = (("K4", (B, H, nblk * BLOCK, d // 2), torch.uint8),
                   ("bounds", (B, H, nblk, 2, d), torch.float32),
                   ("V4", (B, H, nblk, d, BLOCK // 2), torch.uint8),
                   ("vscale", (B, H, nblk * BLOCK, 2), torch.float32),
                   ("Kt", (B, H, BLOCK, d), el), ("Vt", (B, H, BLOCK, d), el))
-        self.status = torch.zeros(1, dtype=torch.int32, device=device)
-        self.device = _device_index(self.status)
+        self.status = torch.zeros(4, dtype=torch.int32, device=device)
+        self.device = self.status.get_device()
         if buffers is None:
             buffers = [torch.zeros(size, dtype=dt, device=device)
                        for _, size, dt in layout]
         if len(buffers) != len(layout):
             raise ValueError("buffers: K4, bounds, V4, vscale, Kt and Vt "
                              "are required")
+        at = []
         for (name, size, dt), t in zip(layout, buffers):
             n = 1
             for x in size:
                 n *= x
-            if t.dtype != dt:
-                raise ValueError(f"{name}: {dt} is required")
-            _require(t, name, n * t.element_size())
-            _same_device(self.device, **{name: t})
-            if t.data_ptr() % 16:
-                raise ValueError(f"{name}: must start at a multiple of 16 "
-                                 "bytes")
+            if t.numel() != n or not t.is_contiguous():
+                raise ValueError(f"{name}: a contiguous tensor {list(size)} "
+                                 "is required")
+            t = t.view(size)
+            at.append(_whole(t, name, size, dt, self.device))
             setattr(self, name, t)
-        self.desc = csa_kv4(*[t.data_ptr() for t in buffers])
+        self.desc = csa_kv4(*at)
 
     def append(self, k, v, lens_dev, n_new=None, stream=None) -> None:
         """Append rows k, v [B][T][Hkv][d] (views with any strides of whole
         16 bytes): n_new[b] <= T of sequence b (None: T each), which
         lens_dev counts already (device int64 [B])."""
-        s = self.shape
-        T = _rows(k, "k", s, s.Hkv)
-        _rows(v, "v", s, s.Hkv, T)
-        _counts(lens_dev, "lens_dev", s.B)
-        if n_new is not None:
-            _counts(n_new, "n_new", s.B)
-        _same_device(self.device, k=k, v=v, lens_dev=lens_dev, n_new=n_new)
-        _current(self.device)
-        check(csa_kv4_append(s, self.desc, T, k, k, v, v, lens_dev, n_new,
-                             self.status, stream), "csa_kv4_append")
+        s, dev, dt = self.shape, self.device, self.dtype
+        B, H, d = s.B, s.Hkv, s.d
+        pk, kb, kt, kh = _rows(k, "k", B, 0, H, d, dt, dev)
+        T = k.shape[1]
+        pv, vb, vt, vh = _rows(v, "v", B, T, H, d, dt, dev)
+        pl = _counts(lens_dev, "lens_dev", B, dev)
+        pn = _counts(n_new, "n_new", B, dev)
+        st = load_library().csa_kv4_append(
+            ctypes.byref(s), ctypes.byref(self.desc), T, pk,
+            ctypes.byref(csa_strides(kb, kt, kh)), pv,
+            ctypes.byref(csa_strides(vb, vt, vh)), pl, pn,
+            self.status.data_ptr(), _call_stream(stream, dev))
+        if st:
+            raise CsaError(st, "csa_kv4_append")
 
     def unpack(self, K, V, lens_dev, first=None, stream=None):
         """Read positions first[b] + i (None: from 0) below lens_dev[b] back
         into row i of K, V (contiguous [B][Hkv][rows][d]); other rows are
         left as they are.  Returns (K, V)."""
-        s = self.shape
-        sz = tuple(K.shape)
-        if len(sz) != 4 or sz[0] != s.B or sz[1] != s.Hkv or sz[2] < 1 or \
-                sz[3] != s.d or tuple(V.shape) != sz:
-            raise ValueError(f"K, V: [{s.B}][{s.Hkv}][rows][{s.d}] is "
-                             "required")
-        for name, t in (("K", K), ("V", V)):
-            _element_type(t, name, s)
-            _require(t, name, 0)
-        _counts(lens_dev, "lens_dev", s.B)
-        if first is not None:
-            _counts(first, "first", s.B)
-        _same_device(self.device, K=K, V=V, lens_dev=lens_dev, first=first)
-        _current(self.device)
-        check(csa_kv4_unpack(s, self.desc, sz[2], first, lens_dev, K, V,
-                             self.status, stream), "csa_kv4_unpack")
+        s, dev, dt = self.shape, self.device, self.dtype
+        if len(K.shape) != 4 or K.shape[2] < 1:
+            raise ValueError(f"K: [{s.B}][{s.Hkv}][rows][{s.d}] is required")
+        size = (s.B, s.Hkv, K.shape[2], s.d)
+        pK = _whole(K, "K", size, dt, dev)
+        pV = _whole(V, "V", size, dt, dev)
+        pl = _counts(lens_dev, "lens_dev", s.B, dev)
+        pf = _counts(first, "first", s.B, dev)
+        st = load_library().csa_kv4_unpack(
+            ctypes.byref(s), ctypes.byref(self.desc), size[2], pf, pl, pK,
+            pV, self.status.data_ptr(), _call_stream(stream, dev))
+        if st:
+            raise CsaError(st, "csa_kv4_unpack")
         return K, V
 
 
@@ -817,11 +834,12 @@ class KV4Decode:
                  with_lse: bool = False):
         import torch
         self.shape, self.T = shape, int(T)
+        self.dtype = _torch_type(shape)
         self.ws_bytes = csa_kv4_workspace_size(shape, self.T)
         if self.ws_bytes == 0:
             raise CsaError(2, "csa_kv4_workspace_size")
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
-        self.device = _device_index(self.ws)
+        self.device = self.ws.get_device()
         self.o = torch.zeros((shape.B, self.T, shape.Hq, shape.d),
                              dtype=torch.float32, device=device)
         self.lse = (torch.zeros((shape.B, self.T, shape.Hq),
@@ -831,19 +849,20 @@ class KV4Decode:
     def __call__(self, q, cache: KV4Cache, lens_dev, n_q=None, stream=None):
         """q [B][T][Hq][d] (a view with strides of whole 16 bytes); lens_dev
         and n_q: device int64 [B] (n_q None: T each).  Returns o."""
-        s = self.shape
-        c = cache.shape
-        if (c.B, c.Hkv, c.d, c.n_max, c.dtype) != (s.B, s.Hkv, s.d, s.n_max,
-                                                   s.dtype):
-            raise ValueError("cache: made for another shape")
-        _rows(q, "q", s, s.Hq, self.T)
-        _counts(lens_dev, "lens_dev", s.B)
-        if n_q is not None:
-            _counts(n_q, "n_q", s.B)
-        _same_device(self.device, q=q, cache=cache.K4, lens_dev=lens_dev,
-                     n_q=n_q)
-        _current(self.device)
-        check(csa_kv4_decode(s, cache.desc, self.T, q, q, lens_dev, n_q,
-                             self.o, self.lse, self.ws, self.ws_bytes,
-                             stream), "csa_kv4_decode")
+        s, c, dev = self.shape, cache.shape, self.device
+        if c.B != s.B or c.Hkv != s.Hkv or c.d != s.d or \
+                c.n_max != s.n_max or c.dtype != s.dtype or \
+                cache.device != dev:
+            raise ValueError("cache: made for another shape or device")
+        pq, qb, qt, qh = _rows(q, "q", s.B, self.T, s.Hq, s.d, self.dtype,
+                               dev)
+        pl = _counts(lens_dev, "lens_dev", s.B, dev)
+        pn = _counts(n_q, "n_q", s.B, dev)
+        st = load_library().csa_kv4_decode(
+            ctypes.byref(s), ctypes.byref(cache.desc), self.T, pq,
+            ctypes.byref(csa_strides(qb, qt, qh)), pl, pn,
+            self.o.data_ptr(), _ptr(self.lse), self.ws.data_ptr(),
+            self.ws_bytes, _call_stream(stream, dev))
+        if st:
+            raise CsaError(st, "csa_kv4_decode")
         return self.o

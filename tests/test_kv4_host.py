@@ -181,11 +181,11 @@ def test_struct_layouts_match_the_header(lib, tmp_path):
 class Fake:
     """Stands in for a CUDA tensor in host-only checks."""
 
-    is_cuda = True
-
-    def __init__(self, size, dtype="torch.bfloat16", stride=None, device=0,
+    def __init__(self, size, dtype="bfloat16", stride=None, device=0,
                  at=FAKE):
-        self.shape, self.dtype, self.dev, self.at = tuple(size), dtype, device, at
+        import torch
+        self.shape, self.dtype = torch.Size(size), getattr(torch, dtype)
+        self.dev, self.at = device, at
         st, n = [], 1
         for x in reversed(size):
             st.insert(0, n)
@@ -199,12 +199,8 @@ class Fake:
     def stride(self):
         return self.st
 
-    def numel(self):
-        return int(np.prod(self.shape))
-
     def element_size(self):
-        return {"torch.bfloat16": 2, "torch.float16": 2, "torch.float32": 4,
-                "torch.int64": 8, "torch.int32": 4}[self.dtype]
+        return self.dtype.itemsize
 
     def is_contiguous(self):
         return self.contig
@@ -213,8 +209,8 @@ class Fake:
         return self.at
 
 
-class HostFake(Fake):
-    is_cuda = False
+def HostFake(*a, **k):
+    return Fake(*a, device=-1, **k)
 
 
 def _made(cls, **kw):
@@ -225,25 +221,34 @@ def _made(cls, **kw):
     return x
 
 
-I64 = "torch.int64"
+I64 = "int64"
+
+
+class Reached(Exception):
+    pass
 
 
 @pytest.fixture
 def no_launch(monkeypatch):
-    """Any call that reaches the library is a failure; device 0 is current."""
+    """A call that would reach the library raises; device 0 is current."""
     import torch
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
 
-    def fail(*a, **k):
-        raise AssertionError("reached the library")
-    for f in ("csa_qk_norm_rope", "csa_kv4_append", "csa_kv4_unpack",
-              "csa_kv4_decode"):
-        monkeypatch.setattr(csa, f, fail)
+    class Library:
+        def __getattr__(self, name):
+            def call(*a):
+                raise Reached(name)
+            return call
+    monkeypatch.setattr(csa, "load_library", lambda: Library())
+
+
+def status():
+    return Fake([4], "int32")
 
 
 @pytest.mark.parametrize("over", [
     dict(q=Fake([2, 4, 8, 64])), dict(q=Fake([2, 8, 128])),
-    dict(q=Fake([2, 4, 8, 128], "torch.float16")),
+    dict(q=Fake([2, 4, 8, 128], "float16")),
     dict(q=Fake([2, 4, 8, 128], device=1)),
     dict(q=HostFake([2, 4, 8, 128])),
     dict(q=Fake([2, 4, 8, 128], at=FAKE + 2)),
@@ -251,19 +256,20 @@ def no_launch(monkeypatch):
     dict(q=Fake([2, 4, 8, 128], stride=[4096, 1024, 132, 1])),
     dict(k=Fake([2, 3, 2, 128])), dict(v=Fake([2, 4, 8, 128])),
     dict(v=None), dict(V=None), dict(K=Fake([2, 2, 999, 128])),
-    dict(K=Fake([2, 2, 1000, 128], "torch.float32")),
-    dict(lens_dev=Fake([2], "torch.int32")), dict(lens_dev=Fake([3], I64)),
+    dict(K=Fake([2, 2, 1000, 128], "float32")),
+    dict(lens_dev=Fake([2], "int32")), dict(lens_dev=Fake([3], I64)),
     dict(lens_dev=HostFake([2], I64)), dict(n_new=Fake([1], I64)),
     dict(q_out=Fake([2, 4, 2, 128])),
     dict(q_out=Fake([2, 4, 8, 128], stride=[8192, 2048, 256, 1]))])
 def test_binding_refuses_rope_arguments(no_launch, over):
-    op = _made(csa.QKNormRope, shape=shape(), device=0, status=None,
-               params=None)
+    import torch
+    op = _made(csa.QKNormRope, shape=shape(), device=0, status=status(),
+               params=norm(), dtype=torch.bfloat16)
     a = dict(q=Fake([2, 4, 8, 128]), k=Fake([2, 4, 2, 128]),
              v=Fake([2, 4, 2, 128]), K=Fake([2, 2, 1000, 128]),
              V=Fake([2, 2, 1000, 128]), lens_dev=Fake([2], I64),
              n_new=Fake([2], I64), q_out=Fake([2, 4, 8, 128]))
-    with pytest.raises(AssertionError, match="reached"):
+    with pytest.raises(Reached):
         op(**a, stream=0)
     a.update(over)
     with pytest.raises(ValueError):
@@ -274,12 +280,14 @@ def test_binding_refuses_rope_arguments(no_launch, over):
     dict(k=Fake([2, 4, 3, 128])), dict(v=Fake([2, 5, 2, 128])),
     dict(k=Fake([2, 0, 2, 128])), dict(v=HostFake([2, 4, 2, 128])),
     dict(lens_dev=Fake([2], I64, device=1)),
-    dict(n_new=Fake([2], "torch.float32"))])
+    dict(n_new=Fake([2], "float32"))])
 def test_binding_refuses_append_arguments(no_launch, over):
-    op = _made(csa.KV4Cache, shape=shape(), device=0, status=None, desc=None)
+    import torch
+    op = _made(csa.KV4Cache, shape=shape(), device=0, status=status(),
+               desc=cache(), dtype=torch.bfloat16)
     a = dict(k=Fake([2, 4, 2, 128]), v=Fake([2, 4, 2, 128]),
              lens_dev=Fake([2], I64), n_new=None)
-    with pytest.raises(AssertionError, match="reached"):
+    with pytest.raises(Reached):
         op.append(**a, stream=0)
     a.update(over)
     with pytest.raises(ValueError):
@@ -290,13 +298,15 @@ def test_binding_refuses_append_arguments(no_launch, over):
     dict(K=Fake([2, 2, 0, 128]), V=Fake([2, 2, 0, 128])),
     dict(V=Fake([2, 2, 6, 128])), dict(K=Fake([2, 2, 5, 64])),
     dict(K=Fake([2, 2, 5, 128], stride=[9999, 640, 128, 1])),
-    dict(V=Fake([2, 2, 5, 128], "torch.float32")),
-    dict(first=Fake([2], "torch.int32"))])
+    dict(V=Fake([2, 2, 5, 128], "float32")),
+    dict(first=Fake([2], "int32"))])
 def test_binding_refuses_unpack_arguments(no_launch, over):
-    op = _made(csa.KV4Cache, shape=shape(), device=0, status=None, desc=None)
+    import torch
+    op = _made(csa.KV4Cache, shape=shape(), device=0, status=status(),
+               desc=cache(), dtype=torch.bfloat16)
     a = dict(K=Fake([2, 2, 5, 128]), V=Fake([2, 2, 5, 128]),
              lens_dev=Fake([2], I64), first=None)
-    with pytest.raises(AssertionError, match="reached"):
+    with pytest.raises(Reached):
         op.unpack(**a, stream=0)
     a.update(over)
     with pytest.raises(ValueError):
@@ -305,17 +315,19 @@ def test_binding_refuses_unpack_arguments(no_launch, over):
 
 @pytest.mark.parametrize("over", [
     dict(q=Fake([2, 2, 8, 128])), dict(q=Fake([2, 4, 2, 128])),
-    dict(n_q=Fake([2], "torch.int32")), dict(lens_dev=HostFake([2], I64)),
-    dict(cache=_made(csa.KV4Cache, shape=shape(n_max=1001), desc=None,
-                     K4=Fake([1]))),
-    dict(cache=_made(csa.KV4Cache, shape=shape(), desc=None,
-                     K4=Fake([1], device=1)))])
+    dict(n_q=Fake([2], "int32")), dict(lens_dev=HostFake([2], I64)),
+    dict(cache=_made(csa.KV4Cache, shape=shape(n_max=1001), desc=cache(),
+                     device=0)),
+    dict(cache=_made(csa.KV4Cache, shape=shape(), desc=cache(),
+                     device=1))])
 def test_binding_refuses_decode_arguments(no_launch, over):
-    op = _made(csa.KV4Decode, shape=shape(), T=4, device=0, o=None, lse=None,
-               ws=None, ws_bytes=0)
+    import torch
+    op = _made(csa.KV4Decode, shape=shape(), T=4, device=0, lse=None,
+               o=Fake([1], "float32"), ws=Fake([1], "uint8"), ws_bytes=0,
+               dtype=torch.bfloat16)
     a = dict(q=Fake([2, 4, 8, 128]), lens_dev=Fake([2], I64), n_q=None,
-             cache=_made(csa.KV4Cache, shape=shape(), desc=None, K4=Fake([1])))
-    with pytest.raises(AssertionError, match="reached"):
+             cache=_made(csa.KV4Cache, shape=shape(), desc=cache(), device=0))
+    with pytest.raises(Reached):
         op(**a, stream=0)
     a.update(over)
     with pytest.raises(ValueError):
@@ -325,7 +337,8 @@ def test_binding_refuses_decode_arguments(no_launch, over):
 def test_another_current_device_is_refused(no_launch, monkeypatch):
     import torch
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
-    op = _made(csa.KV4Cache, shape=shape(), device=0, status=None, desc=None)
+    op = _made(csa.KV4Cache, shape=shape(), device=0, status=status(),
+               desc=cache(), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="current device"):
         op.append(Fake([2, 4, 2, 128]), Fake([2, 4, 2, 128]),
                   Fake([2], I64), stream=0)
