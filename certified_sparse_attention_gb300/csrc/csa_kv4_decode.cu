@@ -57,18 +57,19 @@ struct Kv4DecodeArgs {
   float* o;
   float* lse;
   unsigned* status;
-  float* part;          // [2 * CTAs][rows][D + 2]: m, l, acc[D]
+  float* part;          // [2 * CTAs][rows][D + 4]: acc[D], m, l, unused
   int64_t n_max, nblk_max;
   int B, T, Hq, Hkv, G;
+  int whole;            // items are not cut: one unit each
   int slotsK, slotsV;   // slots of the two rings: multiples of the number of teams
   float rs;             // log2(e) / sqrt(d): scores in units of log 2
 };
 
 constexpr int kKdWarps = 12;      // consumer warps of a CTA: three warpgroups; a fourth
-                                  // one's first two warps send for the blocks
+                                  // one's warps send for the blocks and the queries
 constexpr int kKdThreads = (kKdWarps + 4) * 32;
 // registers: 512 threads start with 128 each; the producers give theirs up
-constexpr int kKdRegsConsumer = 160, kKdRegsProducer = 32;
+constexpr int kKdRegsConsumer = 152, kKdRegsProducer = 56;
 static_assert(3 * kKdRegsConsumer + kKdRegsProducer <= 4 * 128, "more registers than the launch has");
 constexpr int kKdMaxStages = 24;  // slots of a ring
 
@@ -87,25 +88,38 @@ struct KdStage {
   static constexpr int txK = kBlock * D / 2 + 8 * D, txV = kBlock * D / 2 + kBlock * 8;
 };
 
-// units of one (sequence, KV head) of n tokens (at least one: somebody has to
-// write the output of an empty sequence)
-__device__ __forceinline__ int64_t kd_units(int64_t n) { return n > 0 ? (n + kBlock - 1) / kBlock : 1; }
-__device__ __forceinline__ int64_t kd_len(const Kv4DecodeArgs& a, int b) {
-  return min(max(a.len[b], (int64_t)0), a.n_max);
-}
-__device__ __forceinline__ int64_t kd_nq(const Kv4DecodeArgs& a, int b) {
-  return a.n_q ? min(max(a.n_q[b], (int64_t)0), (int64_t)a.T) : (int64_t)a.T;
+// What the kernels know of the batch.  The unit of work is a block of an item
+// (an item: one sequence and KV head), kKdLead more of them stand for an
+// item's own cost (its queries, its incomplete block, the merge), so that
+// runs of short items do not take longer than runs of long ones.
+struct KdBatch {
+  int64_t pref[kMaxB + 1];    // units of the sequences before b (pref[B]: all)
+  int64_t len[kMaxB];
+  int nq[kMaxB];
+};
+constexpr int kKdLead = 4;
+
+// blocks of an item, the incomplete one counted
+__device__ __forceinline__ int64_t kd_blocks(int64_t n) { return (n + kBlock - 1) / kBlock; }
+__device__ __forceinline__ int64_t kd_units(const Kv4DecodeArgs& a, int64_t n) {
+  return a.whole ? 1 : kd_blocks(n) + kKdLead;
 }
 
-// s_pref[b] = units of the sequences before b (s_pref[B]: all), by warp 0
-__device__ __forceinline__ void kd_prefix(const Kv4DecodeArgs& a, int64_t* s_pref) {
+// by warp 0, then a barrier of the CTA
+__device__ __forceinline__ void kd_batch(const Kv4DecodeArgs& a, KdBatch& s) {
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
     int64_t u[4], sum = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int b = lane * 4 + i;
-      u[i] = b < a.B ? kd_units(kd_len(a, b)) * a.Hkv : 0;
+      u[i] = 0;
+      if (b < a.B) {
+        const int64_t n = min(max(a.len[b], (int64_t)0), a.n_max);
+        s.len[b] = n;
+        s.nq[b] = a.n_q ? (int)min(max(a.n_q[b], (int64_t)0), (int64_t)a.T) : a.T;
+        u[i] = kd_units(a, n) * a.Hkv;
+      }
       sum += u[i];
     }
     int64_t x = sum;
@@ -117,32 +131,67 @@ __device__ __forceinline__ void kd_prefix(const Kv4DecodeArgs& a, int64_t* s_pre
     int64_t before = x - sum;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      s_pref[lane * 4 + i] = before;
+      s.pref[lane * 4 + i] = before;
       before += u[i];
     }
-    if (lane == 31) s_pref[kMaxB] = before;
+    if (lane == 31) s.pref[kMaxB] = before;
   }
   __syncthreads();
 }
 
-// the sequence that holds unit u: the last b with s_pref[b] <= u (sequences
-// past B hold no units and start at the end)
-__device__ __forceinline__ int kd_find(const int64_t* s_pref, int B, int64_t u) {
-  int lo = 0, hi = B - 1;
+// the part of an item that lies in the run [u, u1) of a CTA
+struct KdSeg {
+  int64_t bg, n;
+  int64_t blk0, blk1;      // its blocks [blk0, blk1)
+  int64_t step;            // its units
+  int64_t first, last;     // units of the whole item
+  int b, g, nq;
+  int nfast;               // whole blocks among its blocks (they come first)
+  int clear;               // of those, the first `clear` are seen in full by every row
+  int done;                // the whole item lies here
+};
+__device__ __forceinline__ KdSeg kd_seg(const Kv4DecodeArgs& a, const KdBatch& batch, int64_t u, int64_t u1) {
+  KdSeg s;
+  // the last b with pref[b] <= u (sequences past B hold no units)
+  int lo = 0, hi = a.B - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (s_pref[mid] <= u) lo = mid; else hi = mid - 1;
+    if (batch.pref[mid] <= u) lo = mid; else hi = mid - 1;
   }
-  return lo;
+  s.b = lo;
+  s.n = batch.len[lo];
+  s.nq = batch.nq[lo];
+  const int64_t blocks = kd_blocks(s.n), units = kd_units(a, s.n), rem = u - batch.pref[lo];
+  s.g = (rem | units) >> 32 ? (int)(rem / units) : (int)((unsigned)rem / (unsigned)units);
+  s.bg = (int64_t)s.b * a.Hkv + s.g;
+  const int64_t v0 = rem - s.g * units, v1 = min(units, v0 + (u1 - u));
+  s.step = v1 - v0;
+  s.first = u - v0;
+  s.last = s.first + units - 1;
+  s.done = v0 == 0 && v1 == units;
+  s.blk0 = a.whole ? 0 : max(v0 - kKdLead, (int64_t)0);
+  s.blk1 = a.whole ? blocks : max(v1 - kKdLead, (int64_t)0);
+  s.nfast = (int)max(min(s.n / kBlock, s.blk1) - s.blk0, (int64_t)0);
+  // the first row sees positions below n - nq + 1
+  const int64_t clear = max(s.n - s.nq + 1, (int64_t)0) / kBlock - s.blk0;
+  s.clear = (int)min(max(clear, (int64_t)0), (int64_t)s.nfast);
+  return s;
 }
 
-// writes one finished row
+// units of a CTA's run
+__device__ __forceinline__ int64_t kd_run(const KdBatch& batch, int ncta) {
+  return (batch.pref[kMaxB] + ncta - 1) / ncta;
+}
+
+// writes four channels of a finished row
 template <int D>
-__device__ __forceinline__ void kd_store(const Kv4DecodeArgs& a, int b, int g, int r, int c, float M, float l, float v) {
+__device__ __forceinline__ void kd_store(const Kv4DecodeArgs& a, int b, int g, int r, int c, float M, float l, float4 v) {
   const int t = r / a.G, h = g * a.G + r % a.G;
   const int64_t row = ((int64_t)b * a.T + t) * a.Hq + h;
   // l = 0 only where nothing was attended to
-  a.o[row * D + c] = l == 0.0f ? 0.0f : v / l;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  if (l == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  *reinterpret_cast<float4*>(a.o + row * D + c) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
   if (c == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
 }
 
@@ -215,31 +264,7 @@ __device__ __forceinline__ void kd_step(KdState<D, RT>& st, const float (&kv)[8]
   }
 }
 
-// ------------------------------------------------------- items and blocks
-
-// the part of an item that lies in a CTA's run
-struct KdSeg {
-  int b, g;
-  int64_t bg, n, nq, ub;   // ub: units of the item
-  int64_t blk0, cnt;       // units [blk0, blk0 + cnt) of it are here
-  int64_t nfast;           // of those, the first nfast are seen in full by every row
-};
-__device__ __forceinline__ KdSeg kd_seg(const Kv4DecodeArgs& a, const int64_t* s_pref, int64_t u, int64_t u1) {
-  KdSeg s;
-  s.b = kd_find(s_pref, a.B, u);
-  s.n = kd_len(a, s.b);
-  s.nq = kd_nq(a, s.b);
-  s.ub = kd_units(s.n);
-  const int64_t rem = u - s_pref[s.b];
-  s.g = (int)(rem / s.ub);
-  s.bg = (int64_t)s.b * a.Hkv + s.g;
-  s.blk0 = rem - s.g * s.ub;
-  s.cnt = min(s.ub - s.blk0, u1 - u);
-  // the first row sees positions below n - nq + 1
-  const int64_t full = min(s.n, max(s.n - s.nq + 1, (int64_t)0)) / kBlock;
-  s.nfast = min(max(full - s.blk0, (int64_t)0), s.cnt);
-  return s;
-}
+// ------------------------------------------------------- moving the blocks
 
 // A ring of slots with full and empty barriers.  Block i sits in slot i %
 // slots and is taken by team i % teams; slots is a multiple of teams, so a
@@ -257,7 +282,7 @@ struct KdRing {
 // copies of 128 bytes, one for each piece of the bounds, held the 128K-token
 // step at 62% of the memory's rate).
 template <int D>
-__device__ __forceinline__ void kd_produce(const Kv4DecodeArgs& a, const int64_t* s_pref, int64_t u0, int64_t u1,
+__device__ __forceinline__ void kd_produce(const Kv4DecodeArgs& a, const KdBatch& batch, int64_t u0, int64_t u1,
                                            const KdRing& ring, bool keys) {
   using St = KdStage<D>;
   constexpr int codes = kBlock * D / 2;
@@ -274,11 +299,11 @@ __device__ __forceinline__ void kd_produce(const Kv4DecodeArgs& a, const int64_t
   int i = 0, slot = 0, phase = 0;
   bool dead = false;
   for (int64_t u = u0; u < u1 && !dead;) {
-    const KdSeg s = kd_seg(a, s_pref, u, u1);
+    const KdSeg s = kd_seg(a, batch, u, u1);
     const int64_t at = s.bg * a.nblk_max + s.blk0;
     const uint8_t* from = src + at * codes;
     const uint8_t* side_from = side_src + at * side;
-    for (int64_t x = 0; x < s.nfast; ++x) {
+    for (int x = 0; x < s.nfast; ++x) {
       dead = !mbar_wait(ring.empty + 8 * slot, phase ^ 1);    // (a new barrier's "phase -1" is complete)
       dead = __any_sync(0xffffffffu, dead);
       if (dead) break;
@@ -298,7 +323,7 @@ __device__ __forceinline__ void kd_produce(const Kv4DecodeArgs& a, const int64_t
       ++i;
       if (++slot == ring.slots) { slot = 0; phase ^= 1; }
     }
-    u += s.cnt;
+    u += s.step;
   }
   // all copies land before the CTA can end
   for (int k = max(0, i - ring.slots); k < i; ++k)
@@ -361,13 +386,14 @@ constexpr float kKeyUnit = 2097152.0f, kValueUnit = 131072.0f;   // 2^21, 2^17
 template <int D, int RT>
 struct KdFast {
   float qinv;             // undoes the scale of the lane's row
-  float xs, most;         // scale of Delta_c, a power of two; Delta up to which it holds
+  float xs, most;         // scale of Delta_c, a power of two; Delta up to which it holds (0: not set)
   float csA, csB;         // unit of the code sums of rows ra, ra + 1
   float rA, rB;           // reference (running maximum, or up to 8 below it)
   float lA, lB, omA, omB;
-  float sv;               // scale of p_t Delta_t, a power of two
+  float svA, svB;         // scale of p_t Delta_t, a power of two (0: not set)
+  float wide;             // Delta_t up to which both hold
   float o[D / 16][4];     // channels 16 i + gid (+ 8) x operand columns 2 tid, 2 tid + 1
-  bool fresh;
+  bool newA, newB;        // the row has seen no token yet
 };
 
 template <int D, int RT>
@@ -378,17 +404,18 @@ __device__ __forceinline__ void kd_fast_init(KdFast<D, RT>& f, const float* s_in
   f.most = 0.0f;
   f.csA = f.csB = 0.0f;
   f.rA = f.rB = f.lA = f.lB = f.omA = f.omB = 0.0f;
-  f.sv = 1.0f;
+  f.svA = f.svB = f.wide = 0.0f;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) f.o[i][0] = f.o[i][1] = f.o[i][2] = f.o[i][3] = 0.0f;
-  f.fresh = true;
+  f.newA = f.newB = true;
 }
 
 // One block: its keys' part at st, its values' part at vt; between() is
-// called when the one has been read and before the other is.
-template <int D, int RT, typename Between>
+// called when the one has been read and before the other is.  MASK: row ra
+// sees the block's tokens below endA only, row ra + 1 those below endB.
+template <int D, int RT, bool MASK, typename Between>
 __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* st, const uint8_t* vt, const float* s_q,
-                                              Between between) {
+                                              int endA, int endB, Between between) {
   using St = KdStage<D>;
   constexpr int NC = D / 4;        // channels of a lane
   constexpr int NW = D / 32;       // code words of a lane in a key row
@@ -413,11 +440,11 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
     const float2 dl = *reinterpret_cast<const float2*>(st + St::B + (4 + (lane >> 3)) * St::PITCH + (lane & 7) * 8);
     top = fmaxf(dl.x, dl.y);
   }
-  if (__any_sync(0xffffffffu, f.fresh || top >= f.most)) {
+  if (__any_sync(0xffffffffu, top >= f.most)) {
     float t = top < INFINITY ? top : 0.0f;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, m));
-    if (t > 0.0f && (f.fresh || t >= f.most)) {
+    if (t > 0.0f && t >= f.most) {
       const int e = exponent(t);
       f.xs = e >= -8 && e < 3 ? 1.0f : pow2i(min(max(-e, -100), 100));
       f.most = 8.0f / f.xs;
@@ -505,7 +532,10 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
   // in the upper lanes), rows ra, ra + 1, in s[mt][0], s[mt][1].
   // RT = 8: tokens gid and gid + 8 in s[mt][0..1] and s[mt][2..3].
   constexpr int TK = RT == 8 ? 2 : 1;    // tokens of a tile in a lane
+  const auto token = [&](int mt, int k) { return 16 * mt + gid + (RT == 8 ? 8 * k : upper ? 8 : 0); };
   float big = -INFINITY;                 // (scores are relative to rA, rB)
+  float2 sc[4][TK];                      // token scales
+  float wide = 0.0f;
 #pragma unroll
   for (int mt = 0; mt < 4; ++mt) {
     if (RT == 4) {
@@ -518,63 +548,64 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
       s[mt][2] = fmaf(s[mt][2], f.csA, sA); s[mt][3] = fmaf(s[mt][3], f.csB, sB);
     }
 #pragma unroll
-    for (int k = 0; k < TK; ++k) big = fmaxf(big, fmaxf(s[mt][2 * k], s[mt][2 * k + 1]));
-  }
-  // token scales
-  float2 sc[4][TK];
-  float wide = 0.0f;
-#pragma unroll
-  for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
     for (int k = 0; k < TK; ++k) {
-      sc[mt][k] = *reinterpret_cast<const float2*>(vt + St::S + (16 * mt + gid + (RT == 8 ? 8 * k : upper ? 8 : 0)) * 8);
-      wide = fmaxf(wide, sc[mt][k].y);
+      sc[mt][k] = *reinterpret_cast<const float2*>(vt + St::S + token(mt, k) * 8);
+      if (MASK) {
+        if (token(mt, k) >= endA) s[mt][2 * k] = -INFINITY;
+        if (token(mt, k) >= endB) s[mt][2 * k + 1] = -INFINITY;
+      }
+      big = fmaxf(big, fmaxf(s[mt][2 * k], s[mt][2 * k + 1]));
+      if (!MASK || token(mt, k) < max(endA, endB)) wide = fmaxf(wide, sc[mt][k].y);
     }
+  }
   // The reference moves only when a score exceeds it by more than 8 (weights
   // up to 2^8), and the value scale only when Delta_t does not fit (Delta_t sv
   // up to 2^6): both are rare after the first block.
-  if (__any_sync(0xffffffffu, f.fresh || big > 8.0f || wide * f.sv > 64.0f)) {
-    float xA = -INFINITY, xB = -INFINITY;
+  if (__any_sync(0xffffffffu, f.newA || f.newB || big > 8.0f || wide > f.wide)) {
+    float xA = -INFINITY, xB = -INFINITY, tA = 0.0f, tB = 0.0f;
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
       for (int k = 0; k < TK; ++k) {
+        const float t = sc[mt][k].y < INFINITY ? sc[mt][k].y : 0.0f;
         xA = fmaxf(xA, s[mt][2 * k]);
         xB = fmaxf(xB, s[mt][2 * k + 1]);
+        if (!MASK || token(mt, k) < endA) tA = fmaxf(tA, t);
+        if (!MASK || token(mt, k) < endB) tB = fmaxf(tB, t);
       }
-    float t = 0.0f;
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-      for (int k = 0; k < TK; ++k) t = fmaxf(t, sc[mt][k].y < INFINITY ? sc[mt][k].y : 0.0f);
 #pragma unroll
     for (int m = (RT == 4 ? 2 : 4); m < 32; m <<= 1) {
       xA = fmaxf(xA, __shfl_xor_sync(0xffffffffu, xA, m));
       xB = fmaxf(xB, __shfl_xor_sync(0xffffffffu, xB, m));
+      tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, m));
+      tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, m));
     }
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, m));
-    // the references move up by dA, dB (the first block: to its maximum)
-    const float dA = f.fresh ? (xA > -INFINITY ? xA : 0.0f) : fmaxf(xA, 0.0f);
-    const float dB = f.fresh ? (xB > -INFINITY ? xB : 0.0f) : fmaxf(xB, 0.0f);
-    float up = 1.0f;
-    if (t > 0.0f && (f.fresh || t * f.sv > 64.0f)) {
-      const float to = pow2i(min(max(5 - exponent(t), -100), 100));   // Delta sv in [2^5, 2^6)
-      up = f.sv > 0.0f ? to / f.sv : 1.0f;
-      f.sv = to;
+    // the references move up by dA, dB (a row's first tokens: to their maximum)
+    const float dA = f.newA ? (xA > -INFINITY ? xA : 0.0f) : fmaxf(xA, 0.0f);
+    const float dB = f.newB ? (xB > -INFINITY ? xB : 0.0f) : fmaxf(xB, 0.0f);
+    const float eA = f.newA ? 1.0f : ex2(-dA), eB = f.newB ? 1.0f : ex2(-dB);
+    float upA = 1.0f, upB = 1.0f;
+    if (tA > 0.0f && (f.svA == 0.0f || tA * f.svA > 64.0f)) {
+      const float to = pow2i(min(max(5 - exponent(tA), -100), 100));   // Delta sv in [2^5, 2^6)
+      if (f.svA != 0.0f) upA = to / f.svA;
+      f.svA = to;
     }
-    if (!f.fresh) {
-      const float eA = ex2(-dA), eB = ex2(-dB);
-      f.lA *= eA; f.lB *= eB;
-      f.omA *= eA; f.omB *= eB;
+    if (tB > 0.0f && (f.svB == 0.0f || tB * f.svB > 64.0f)) {
+      const float to = pow2i(min(max(5 - exponent(tB), -100), 100));
+      if (f.svB != 0.0f) upB = to / f.svB;
+      f.svB = to;
+    }
+    f.wide = f.svA == 0.0f || f.svB == 0.0f ? 0.0f : 64.0f / fmaxf(f.svA, f.svB);
+    f.lA *= eA; f.lB *= eB;
+    f.omA *= eA; f.omB *= eB;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        f.o[i][0] *= eA * up; f.o[i][1] *= eB * up;
-        f.o[i][2] *= eA * up; f.o[i][3] *= eB * up;
-      }
+    for (int i = 0; i < D / 16; ++i) {
+      f.o[i][0] *= eA * upA; f.o[i][1] *= eB * upB;
+      f.o[i][2] *= eA * upA; f.o[i][3] *= eB * upB;
     }
     f.rA += dA; f.rB += dB;
-    f.fresh = false;
+    f.newA = f.newA && !(xA > -INFINITY);
+    f.newB = f.newB && !(xB > -INFINITY);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
@@ -594,12 +625,20 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
     for (int k = 0; k < TK; ++k) {
       const float pA = ex2(s[mt][2 * k]), pB = ex2(s[mt][2 * k + 1]);
       f.lA += pA; f.lB += pB;
-      const float m = fmaf(sc[mt][k].y, RT == 8 ? (k ? 15.0f : 0.0f) : upper ? 15.0f : 0.0f, sc[mt][k].x);
-      omA = fmaf(pA, m, omA);
-      omB = fmaf(pB, m, omB);
-      const float w = sc[mt][k].y * ((RT == 8 ? k == 1 : upper) ? -f.sv : f.sv);
-      hi[k] = half_pair(pA * w, pB * w);
-      lo[k] = half_rest(pA * w, pB * w, hi[k]);
+      const bool turned = RT == 8 ? k == 1 : upper;
+      const float y = sc[mt][k].y, m = fmaf(y, turned ? 15.0f : 0.0f, sc[mt][k].x);
+      float zA = pA * m, zB = pB * m;
+      float wA = pA * (y * (turned ? -f.svA : f.svA)), wB = pB * (y * (turned ? -f.svB : f.svB));
+      if (MASK) {
+        // an unseen token's value may be anything: it is left out, not
+        // multiplied by zero
+        if (token(mt, k) >= endA) zA = wA = 0.0f;
+        if (token(mt, k) >= endB) zB = wB = 0.0f;
+      }
+      omA += zA;
+      omB += zB;
+      hi[k] = half_pair(wA, wB);
+      lo[k] = half_rest(wA, wB, hi[k]);
     }
     if (RT == 4) {
       const unsigned got = __shfl_xor_sync(0xffffffffu, upper ? hi[0] : lo[0], 2);
@@ -664,121 +703,62 @@ __device__ __forceinline__ void kd_fast_store(KdFast<D, RT>& f, float* s_m, floa
     f.omB += __shfl_xor_sync(0xffffffffu, f.omB, m);
   }
   if (gid == 0 && !upper) {
-    s_m[ra] = f.fresh ? -INFINITY : f.rA; s_m[ra + 1] = f.fresh ? -INFINITY : f.rB;
+    s_m[ra] = f.newA ? -INFINITY : f.rA; s_m[ra + 1] = f.newB ? -INFINITY : f.rB;
     s_l[ra] = f.lA; s_l[ra + 1] = f.lB;
   }
-  const float back = kValueUnit / f.sv;
+  const float backA = f.svA == 0.0f ? 0.0f : kValueUnit / f.svA, backB = f.svB == 0.0f ? 0.0f : kValueUnit / f.svB;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) {
     if (RT == 4) {
       const float g0 = __shfl_xor_sync(0xffffffffu, upper ? f.o[i][0] : f.o[i][2], 2);
       const float g1 = __shfl_xor_sync(0xffffffffu, upper ? f.o[i][1] : f.o[i][3], 2);
       const int c = 16 * i + gid + (upper ? 8 : 0);
-      s_acc[ra * D + c] = fmaf((upper ? f.o[i][2] : f.o[i][0]) + g0, back, f.omA);
-      s_acc[(ra + 1) * D + c] = fmaf((upper ? f.o[i][3] : f.o[i][1]) + g1, back, f.omB);
+      s_acc[ra * D + c] = fmaf((upper ? f.o[i][2] : f.o[i][0]) + g0, backA, f.omA);
+      s_acc[(ra + 1) * D + c] = fmaf((upper ? f.o[i][3] : f.o[i][1]) + g1, backB, f.omB);
     } else {
       const int c = 16 * i + gid;
-      s_acc[ra * D + c] = fmaf(f.o[i][0], back, f.omA);
-      s_acc[(ra + 1) * D + c] = fmaf(f.o[i][1], back, f.omB);
-      s_acc[ra * D + c + 8] = fmaf(f.o[i][2], back, f.omA);
-      s_acc[(ra + 1) * D + c + 8] = fmaf(f.o[i][3], back, f.omB);
+      s_acc[ra * D + c] = fmaf(f.o[i][0], backA, f.omA);
+      s_acc[(ra + 1) * D + c] = fmaf(f.o[i][1], backB, f.omB);
+      s_acc[ra * D + c + 8] = fmaf(f.o[i][2], backA, f.omA);
+      s_acc[(ra + 1) * D + c + 8] = fmaf(f.o[i][3], backB, f.omB);
     }
   }
 }
 
-// shared memory: barriers of the two rings, warp sums, q rows, the rings
-template <int D, int RT>
-struct KdLayout {
-  static constexpr int bars = 0;                              // full, empty of the keys, then of the values
-  static constexpr int m = 4 * kKdMaxStages * 8;
-  static constexpr int l = m + kKdWarps * RT * 4;
-  static constexpr int acc = l + kKdWarps * RT * 4;
-  static constexpr int q = acc + kKdWarps * RT * D * 4;
-  static __host__ __device__ int ring(int rows) { return q + (rows + RT - 1) / RT * RT * (D + 16) * 4; }
+// The queries of an item and what else its warps need of it: filled by a
+// producer warp, an item ahead.
+struct KdItem {
+  KdSeg seg;
+  int64_t end[CSA_KV4_MAX_ROWS];    // row r sees positions below end[r]
+  float inv[CSA_KV4_MAX_ROWS];      // undoes the scale of row r (kd_q)
 };
 
 template <int D, int RT, typename E>
-__global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4DecodeArgs a) {
-  pdl_entry();
-  using St = KdStage<D>;
-  using Lt = KdLayout<D, RT>;
-  constexpr int CPL = D / 32, W = kKdWarps;
-  __shared__ int64_t s_pref[kMaxB + 1];
-  __shared__ int64_t s_end[CSA_KV4_MAX_ROWS];
-  __shared__ float s_inv[CSA_KV4_MAX_ROWS];
-  __shared__ KdSeg s_seg;
-  extern __shared__ __align__(128) uint8_t kd_sm[];
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+__device__ __forceinline__ void kd_queries(const Kv4DecodeArgs& a, const KdBatch& batch, int64_t u0, int64_t u1,
+                                           KdItem* items, float* s_q, unsigned full, unsigned empty) {
+  constexpr int CPL = D / 32;
+  const int lane = threadIdx.x & 31;
   const int R = a.T * a.G, Rp = (R + RT - 1) / RT * RT;
-  // teams: warps that share a block, one tile of rows each (more than 32 rows:
-  // one team of 8, four warps left over)
-  const int ntile = Rp / RT;
-  const int team = ntile <= 1 ? 1 : ntile <= 2 ? 2 : ntile <= 4 ? 4 : 8;
-  const int nteam = W / team;
-  KdRing keys, values;
-  keys.full = smem_u32(kd_sm) + Lt::bars;
-  keys.empty = keys.full + kKdMaxStages * 8;
-  values.full = keys.empty + kKdMaxStages * 8;
-  values.empty = values.full + kKdMaxStages * 8;
-  keys.slots = a.slotsK;
-  values.slots = a.slotsV;
-  keys.data = kd_sm + Lt::ring(R);
-  values.data = keys.data + a.slotsK * St::bytesK;
-  if (tid < kKdMaxStages) {
-    // (one arrival with the codes' bytes, one of each lane of the producer)
-    mbar_init(keys.full + 8 * tid, 33);
-    mbar_init(keys.empty + 8 * tid, team);
-    mbar_init(values.full + 8 * tid, 33);
-    mbar_init(values.empty + 8 * tid, team);
-    fence_barrier_init();
-  }
-  kd_prefix(a, s_pref);
-  const int64_t total = s_pref[kMaxB];
-  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t u0 = (int64_t)blockIdx.x * per, u1 = min(total, u0 + per);
-
-  if (w >= W) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kKdRegsProducer));
-    if (w == W) kd_produce<D>(a, s_pref, u0, u1, keys, true);
-    else if (w == W + 1) kd_produce<D>(a, s_pref, u0, u1, values, false);
-    else if (w == W + 2 && blockIdx.x == 0) {
-      bool bad = false;
-      for (int b = lane; b < a.B; b += 32) {
-        bad |= a.len[b] < 0 || a.len[b] > a.n_max;
-        if (a.n_q) bad |= a.n_q[b] < 0 || a.n_q[b] > a.T;
-      }
-      const unsigned any = __any_sync(0xffffffffu, bad);
-      // (a wait that gives up flags the word two seconds later at the earliest)
-      if (lane == 0) *a.status = any ? 8u : 0u;
-    }
-    return;
-  }
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kKdRegsConsumer));
-
-  float* s_m = reinterpret_cast<float*>(kd_sm + Lt::m);        // [warps][RT]
-  float* s_l = reinterpret_cast<float*>(kd_sm + Lt::l);
-  float* s_acc = reinterpret_cast<float*>(kd_sm + Lt::acc);    // [warps][RT][D]
-  float* s_q = reinterpret_cast<float*>(kd_sm + Lt::q);        // [rows, padded] (kd_q)
-  const int my_team = w / team, tile = w % team;
-  const int rows = my_team < nteam ? min(RT, R - tile * RT) : 0;    // <= 0: a warp with no rows
-  // (Each wait is bounded: one that gives up marks the call, and the warp goes
-  // on without waiting.)
+  int k = 0;
   bool dead = false;
-  int base = 0;                                   // number of the item's first block
-  int i = my_team;                                // the team's next block, its slots and their parities
-  int sk = my_team, sv = my_team, pk = 0, pv = 0;
-
-  for (int64_t u = u0; u < u1;) {
-    const KdSeg sg = kd_seg(a, s_pref, u, u1);
-    if (tid == 0) s_seg = sg;
-    for (int r = w; r < Rp; r += W) {
+  for (int64_t u = u0; u < u1 && !dead; ++k) {
+    const int buf = k & 1;
+    dead = !mbar_wait(empty + 8 * buf, ((k >> 1) & 1) ^ 1);
+    dead = __any_sync(0xffffffffu, dead);
+    if (dead) break;
+    KdItem& it = items[buf];
+    const KdSeg sg = kd_seg(a, batch, u, u1);
+    if (lane == 0) it.seg = sg;
+    const E* base = reinterpret_cast<const E*>(a.q) + sg.b * a.qs.b + (int64_t)sg.g * a.G * a.qs.h + lane * CPL;
+    float* q = s_q + buf * kd_q<D>(Rp, 0);
+#pragma unroll 4
+    for (int r = 0; r < Rp; ++r) {
       const int t = r / a.G;
       float x[CPL];
 #pragma unroll
       for (int c = 0; c < CPL; ++c) x[c] = 0.0f;
       if (t < sg.nq) {
-        const E* src = reinterpret_cast<const E*>(a.q) + sg.b * a.qs.b + t * a.qs.t +
-                       (int64_t)(sg.g * a.G + r % a.G) * a.qs.h + lane * CPL;
+        const E* src = base + t * a.qs.t + (r - t * a.G) * a.qs.h;
         if (CPL == 4) {
           const float4 v = Elem<E>::get4(src);
           x[0] = v.x; x[1] = v.y; x[CPL - 2] = v.z; x[CPL - 1] = v.w;
@@ -795,46 +775,162 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
       }
 #pragma unroll
       for (int m = 1; m < 32; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-      const int k = top > 0.0f && top < INFINITY ? min(max(11 - exponent(top), -100), 100) : 0;
-      const float up = pow2i(k);
+      const int e = top > 0.0f && top < INFINITY ? min(max(11 - exponent(top), -100), 100) : 0;
+      const float up = pow2i(e);
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) s_q[kd_q<D>(r, lane * CPL) + c] = x[c] * (c & 1 ? 0.0625f * up : up);
-      if (lane == 0) s_inv[r] = pow2i(-k);
+      for (int c = 0; c < CPL; ++c) q[kd_q<D>(r, lane * CPL) + c] = x[c] * (c & 1 ? 0.0625f * up : up);
+      if (lane == 0) {
+        it.inv[r] = pow2i(-e);
+        it.end[r] = t < sg.nq ? sg.n - sg.nq + t + 1 : 0;
+      }
     }
-    if (tid < Rp) s_end[tid] = tid / a.G < sg.nq ? sg.n - sg.nq + tid / a.G + 1 : 0;
-    bar_sync(1, W * 32);
-    const int r0 = tile * RT < Rp ? tile * RT : 0;      // (tiles past the rows do nothing)
-    const float* q = s_q + kd_q<D>(r0, 0);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(full + 8 * buf);
+    u += sg.step;
+  }
+  if (dead && lane == 0) atomicOr(a.status, 4u);
+}
+
+// shared memory: barriers (keys full, empty, values full, empty, items full,
+// empty), items, warp sums, q rows of two items, the rings
+template <int D, int RT>
+struct KdLayout {
+  static constexpr int item = (4 * kKdMaxStages + 4) * 8;
+  static constexpr int m = item + 2 * (int)sizeof(KdItem);
+  static constexpr int l = m + kKdWarps * RT * 4;
+  static constexpr int acc = (l + kKdWarps * RT * 4 + 15) / 16 * 16;
+  static constexpr int q = acc + kKdWarps * RT * D * 4;
+  static __host__ __device__ int ring(int rows) { return q + 2 * ((rows + RT - 1) / RT * RT) * (D + 16) * 4; }
+};
+
+template <int D, int RT, typename E>
+__global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4DecodeArgs a) {
+  pdl_entry();
+  using St = KdStage<D>;
+  using Lt = KdLayout<D, RT>;
+  constexpr int CPL = D / 32, W = kKdWarps;
+  __shared__ KdBatch batch;
+  extern __shared__ __align__(128) uint8_t kd_sm[];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int R = a.T * a.G, Rp = (R + RT - 1) / RT * RT;
+  // teams: warps that share a block, one tile of rows each (more than 32 rows:
+  // one team of 8, four warps left over)
+  const int ntile = Rp / RT;
+  const int team = ntile <= 1 ? 1 : ntile <= 2 ? 2 : ntile <= 4 ? 4 : 8;
+  const int nteam = W / team;
+  KdRing keys, values;
+  keys.full = smem_u32(kd_sm);
+  keys.empty = keys.full + kKdMaxStages * 8;
+  values.full = keys.empty + kKdMaxStages * 8;
+  values.empty = values.full + kKdMaxStages * 8;
+  const unsigned item_full = values.empty + kKdMaxStages * 8, item_empty = item_full + 16;
+  keys.slots = a.slotsK;
+  values.slots = a.slotsV;
+  keys.data = kd_sm + Lt::ring(R);
+  values.data = keys.data + a.slotsK * St::bytesK;
+  KdItem* items = reinterpret_cast<KdItem*>(kd_sm + Lt::item);
+  float* s_q = reinterpret_cast<float*>(kd_sm + Lt::q);        // two of [rows, padded] (kd_q)
+  if (tid >= 32 && tid < 32 + kKdMaxStages) {
+    // (full: one arrival with the codes' bytes, one of each lane of the producer)
+    const int i = tid - 32;
+    mbar_init(keys.full + 8 * i, 33);
+    mbar_init(keys.empty + 8 * i, team);
+    mbar_init(values.full + 8 * i, 33);
+    mbar_init(values.empty + 8 * i, team);
+    if (i < 2) {
+      mbar_init(item_full + 8 * i, 1);
+      mbar_init(item_empty + 8 * i, W);
+    }
+    fence_barrier_init();
+  }
+  kd_batch(a, batch);
+  const int64_t per = kd_run(batch, gridDim.x);
+  const int64_t u0 = (int64_t)blockIdx.x * per, u1 = min(batch.pref[kMaxB], u0 + per);
+
+  if (w >= W) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kKdRegsProducer));
+    if (w == W) kd_produce<D>(a, batch, u0, u1, keys, true);
+    else if (w == W + 1) kd_produce<D>(a, batch, u0, u1, values, false);
+    else if (w == W + 2) kd_queries<D, RT, E>(a, batch, u0, u1, items, s_q, item_full, item_empty);
+    else if (blockIdx.x == 0) {
+      bool bad = false;
+      for (int b = lane; b < a.B; b += 32) {
+        bad |= a.len[b] < 0 || a.len[b] > a.n_max;
+        if (a.n_q) bad |= a.n_q[b] < 0 || a.n_q[b] > a.T;
+      }
+      const unsigned any = __any_sync(0xffffffffu, bad);
+      // (a wait that gives up flags the word two seconds later at the earliest)
+      if (lane == 0) *a.status = any ? 8u : 0u;
+    }
+    return;
+  }
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kKdRegsConsumer));
+
+  float* s_m = reinterpret_cast<float*>(kd_sm + Lt::m);        // [warps][RT]
+  float* s_l = reinterpret_cast<float*>(kd_sm + Lt::l);
+  float* s_acc = reinterpret_cast<float*>(kd_sm + Lt::acc);    // [warps][RT][D]
+  const int my_team = w / team, tile = w % team;
+  const int rows = my_team < nteam ? min(RT, R - tile * RT) : 0;    // <= 0: a warp with no rows
+  const int r0 = tile * RT < Rp ? tile * RT : 0;
+  // (Each wait is bounded: one that gives up marks the call, and the warp goes
+  // on without waiting.)
+  bool dead = false;
+  int base = 0;                                   // number of the item's first block
+  int i = my_team;                                // the team's next block, its slots and their parities
+  int sk = my_team, sv = my_team, pk = 0, pv = 0;
+  int k = 0;                                      // number of the item
+
+  for (int64_t u = u0; u < u1; ++k) {
+    const int buf = k & 1;
+    if (!dead && !mbar_wait(item_full + 8 * buf, (k >> 1) & 1)) dead = true;
+    dead = __any_sync(0xffffffffu, dead);
+    if (dead) {
+      // the way through the items does not hang on the producer
+      if (lane == 0) items[buf].seg = kd_seg(a, batch, u, u1);
+      __syncwarp();
+    }
+    const KdItem& it = items[buf];
+    const float* q = s_q + kd_q<D>(buf * Rp + r0, 0);
     float* my_m = s_m + w * RT;
     float* my_l = s_l + w * RT;
     float* my_acc = s_acc + w * RT * D;
-    base += (int)sg.nfast;
     {
       KdFast<D, RT> f;
-      kd_fast_init<D, RT>(f, s_inv + r0);
-      while (my_team < nteam && i < base) {
+      kd_fast_init<D, RT>(f, it.inv + r0);
+      const int to = base + it.seg.nfast, clear = base + it.seg.clear;
+      while (my_team < nteam && i < to) {
         if (!dead && !mbar_wait(keys.full + 8 * sk, pk)) dead = true;
         const auto between = [&]() {
           __syncwarp();
           if (lane == 0) mbar_arrive(keys.empty + 8 * sk);
           if (!dead && !mbar_wait(values.full + 8 * sv, pv)) dead = true;
         };
-        if (rows > 0)
-          kd_fast_block<D, RT>(f, keys.data + sk * St::bytesK, values.data + sv * St::bytesV, q, between);
-        else
+        const uint8_t* kt = keys.data + sk * St::bytesK;
+        const uint8_t* vt = values.data + sv * St::bytesV;
+        if (rows <= 0) {
           between();
+        } else if (i < clear) {
+          kd_fast_block<D, RT, false>(f, kt, vt, q, 0, 0, between);
+        } else {
+          const int ra = 2 * (lane % 4 % (RT / 2));
+          const int64_t p0 = (it.seg.blk0 + (i - base)) * kBlock;
+          kd_fast_block<D, RT, true>(f, kt, vt, q, (int)min(max(it.end[r0 + ra] - p0, (int64_t)0), (int64_t)kBlock),
+                                     (int)min(max(it.end[r0 + ra + 1] - p0, (int64_t)0), (int64_t)kBlock), between);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(values.empty + 8 * sv);
         i += nteam;
         if ((sk += nteam) >= keys.slots) { sk = my_team; pk ^= 1; }
         if ((sv += nteam) >= values.slots) { sv = my_team; pv ^= 1; }
       }
+      base = to;
       kd_fast_store<D, RT>(f, my_m, my_l, my_acc);
     }
-    const KdSeg se = s_seg;       // (read back: not held in registers over the blocks)
-    if (rows > 0 && se.nfast < se.cnt) {
-      // blocks that are seen in part, and the incomplete one, eight tokens
-      // at a time: the state moves on to lanes that hold channels
+    // positions of the incomplete block, if it lies here
+    const int64_t p0 = it.seg.n / kBlock * kBlock;
+    const int left = it.seg.blk1 * kBlock > p0 ? (int)(it.seg.n - p0) : 0;
+    if (rows > 0 && left > 0) {
+      // eight tokens at a time: the state moves on to lanes that hold channels
       __syncwarp();
       KdState<D, RT> st;
 #pragma unroll
@@ -843,55 +939,21 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
 #pragma unroll
         for (int c = 0; c < CPL; ++c) st.acc[r][c] = my_acc[r * D + lane * CPL + c];
       }
-      const int64_t* end = s_end + r0;
-      const float* inv = s_inv + r0;
-      for (int64_t x = se.nfast * 8 + my_team; x < se.cnt * 8; x += nteam) {
-        const int64_t blk = se.blk0 + x / 8;
-        const int grp = (int)(x % 8);
-        const int64_t p0 = blk * kBlock;
+      for (int t0 = 8 * my_team; t0 < left; t0 += 8 * nteam) {
         float kv[8][CPL], vv[8][CPL];
-        if (blk < se.n / kBlock) {
-          const int64_t at = se.bg * a.nblk_max + blk;
-          float mn[CPL], dl[CPL];
-          unsigned vw[CPL];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int t = t0 + e;
+          const bool there = t < left;
+          const E* kr = reinterpret_cast<const E*>(a.c.Kt) + (it.seg.bg * kBlock + t) * D + lane * CPL;
+          const E* vr = reinterpret_cast<const E*>(a.c.Vt) + (it.seg.bg * kBlock + t) * D + lane * CPL;
 #pragma unroll
           for (int c = 0; c < CPL; ++c) {
-            mn[c] = a.c.bounds[at * 2 * D + lane * CPL + c];
-            dl[c] = a.c.bounds[at * 2 * D + D + lane * CPL + c];
-            vw[c] = reinterpret_cast<const unsigned*>(a.c.V4)[(at * D + lane * CPL + c) * 8 + grp];
+            kv[e][c] = there ? Elem<E>::get(kr, c) : 0.0f;
+            vv[e][c] = there ? Elem<E>::get(vr, c) : 0.0f;
           }
-          // word grp of a V4 row: tokens 32 i + 16 u + 8 v + 2 w + e with
-          // i = grp & 1, w = grp >> 1, nibble 4 e + 2 u + v
-          const int first = 32 * (grp & 1) + 2 * (grp >> 1);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int t = first + 16 * ((i >> 1) & 1) + 8 * (i & 1) + (i >> 2);
-            const float2 sc = reinterpret_cast<const float2*>(a.c.vscale)[at * kBlock + t];
-            const uint8_t* kr = a.c.K4 + (at * kBlock + t) * (D / 2) + lane * CPL / 2;
-#pragma unroll
-            for (int c = 0; c < CPL; ++c) {
-              kv[i][c] = fadd(fmul((float)((kr[c / 2] >> (4 * (c & 1))) & 15), dl[c]), mn[c]);
-              vv[i][c] = fadd(fmul((float)((vw[c] >> (4 * i)) & 15u), sc.y), sc.x);
-            }
-          }
-          const int i = lane & 7;
-          kd_step<D, RT>(st, kv, vv, q, inv, end, p0 + first + 16 * ((i >> 1) & 1) + 8 * (i & 1) + (i >> 2), rows);
-        } else {
-          if (p0 + 8 * grp >= se.n) continue;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int t = 8 * grp + i;
-            const bool there = p0 + t < se.n;
-            const E* kr = reinterpret_cast<const E*>(a.c.Kt) + (se.bg * kBlock + t) * D + lane * CPL;
-            const E* vr = reinterpret_cast<const E*>(a.c.Vt) + (se.bg * kBlock + t) * D + lane * CPL;
-#pragma unroll
-            for (int c = 0; c < CPL; ++c) {
-              kv[i][c] = there ? Elem<E>::get(kr, c) : 0.0f;
-              vv[i][c] = there ? Elem<E>::get(vr, c) : 0.0f;
-            }
-          }
-          kd_step<D, RT>(st, kv, vv, q, inv, end, p0 + 8 * grp + (lane & 7), rows);
         }
+        kd_step<D, RT>(st, kv, vv, q, it.inv + r0, it.end + r0, p0 + t0 + (lane & 7), rows);
       }
       __syncwarp();
 #pragma unroll
@@ -902,29 +964,29 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
       }
     }
     bar_sync(1, W * 32);
-    // merge the teams
-    const bool done = se.cnt == se.ub;
-    float* part = a.part + (2 * (int64_t)blockIdx.x + (u == u0 ? 0 : 1)) * R * (D + 2);
-    for (int i = tid; i < R * D; i += W * 32) {
-      const int r = i / D, c = i - r * D;
-      const int x0 = r / RT * RT + r % RT;       // (tile, row) of team 0's warps
-      float M = -INFINITY, l = 0.0f, v = 0.0f;
-      for (int k = 0; k < nteam; ++k) M = fmaxf(M, s_m[k * team * RT + x0]);
-      for (int k = 0; k < nteam; ++k) {
-        const int x = k * team * RT + x0;
-        const float e = s_m[x] > -INFINITY ? exp2f(s_m[x] - M) : s_l[x] == 0.0f ? 0.0f : 1.0f;
-        l += e * s_l[x];
-        v += e * s_acc[x * D + c];
+    // merge the teams, four channels of a row to a thread
+    float* part = a.part + (2 * (int64_t)blockIdx.x + (u == u0 ? 0 : 1)) * R * (D + 4);
+    for (int e = tid; e < R * (D / 4); e += W * 32) {
+      const int r = e / (D / 4), c = e % (D / 4) * 4;
+      float M = -INFINITY, l = 0.0f;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int x = r; x < nteam * team * RT; x += team * RT) M = fmaxf(M, s_m[x]);   // (the row in each team)
+      for (int x = r; x < nteam * team * RT; x += team * RT) {
+        const float s = s_m[x] > -INFINITY ? ex2(s_m[x] - M) : s_l[x] == 0.0f ? 0.0f : 1.0f;
+        const float4 y = *reinterpret_cast<const float4*>(s_acc + x * D + c);
+        l = fmaf(s, s_l[x], l);
+        v.x = fmaf(s, y.x, v.x); v.y = fmaf(s, y.y, v.y); v.z = fmaf(s, y.z, v.z); v.w = fmaf(s, y.w, v.w);
       }
-      if (done) {
-        if (r / a.G < se.nq) kd_store<D>(a, se.b, se.g, r, c, M, l, v);
+      if (it.seg.done) {
+        if (r / a.G < it.seg.nq) kd_store<D>(a, it.seg.b, it.seg.g, r, c, M, l, v);
       } else {
-        if (c == 0) { part[r * (D + 2)] = M; part[r * (D + 2) + 1] = l; }
-        part[r * (D + 2) + 2 + c] = v;
+        *reinterpret_cast<float4*>(part + r * (D + 4) + c) = v;
+        if (c == 0) { part[r * (D + 4) + D] = M; part[r * (D + 4) + D + 1] = l; }
       }
     }
+    u += it.seg.step;
     bar_sync(1, W * 32);
-    u += se.cnt;
+    if (lane == 0) mbar_arrive(item_empty + 8 * buf);
   }
   if (dead && lane == 0) atomicOr(a.status, 4u);
 }
@@ -935,51 +997,55 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
 template <int D>
 __global__ void __launch_bounds__(256) kv4_join_kernel(const Kv4DecodeArgs a, int ncta) {
   pdl_entry();
-  __shared__ int64_t s_pref[kMaxB + 1];
-  kd_prefix(a, s_pref);
-  const int64_t total = s_pref[kMaxB], per = (total + ncta - 1) / ncta;
-  const int64_t x = ((int64_t)blockIdx.x + 1) * per;
-  if (x >= total) return;
-  const int b = kd_find(s_pref, a.B, x);
-  const int64_t n = kd_len(a, b), ub = kd_units(n), rem = x - s_pref[b];
-  const int g = (int)(rem / ub);
-  const int64_t first = s_pref[b] + g * ub, last = first + ub - 1;
-  if (first == x || first / per != (int64_t)blockIdx.x) return;
-  const int c0 = (int)blockIdx.x, c1 = (int)(last / per);
+  __shared__ KdBatch batch;
+  kd_batch(a, batch);
+  const int64_t per = kd_run(batch, ncta), x = ((int64_t)blockIdx.x + 1) * per;
+  if (x >= batch.pref[kMaxB]) return;
+  const KdSeg s = kd_seg(a, batch, x, x + 1);
+  if (s.first == x || s.first / per != (int64_t)blockIdx.x) return;
+  const int c0 = (int)blockIdx.x, c1 = (int)(s.last / per);
   const int R = a.T * a.G;
-  const int64_t nq = kd_nq(a, b);
-  const int64_t stride = (int64_t)R * (D + 2);
-  const float* p0 = a.part + (2 * (int64_t)c0 + (first == c0 * per ? 0 : 1)) * stride;
-  for (int i = threadIdx.x; i < R * D; i += 256) {
-    const int r = i / D, c = i - r * D;
-    if (r / a.G >= nq) continue;
-    float M = -INFINITY, l = 0.0f, v = 0.0f;
-    for (int k = c0; k <= c1; ++k) M = fmaxf(M, (k == c0 ? p0 : a.part + 2 * k * stride)[r * (D + 2)]);
+  const int64_t stride = (int64_t)R * (D + 4);
+  const float* p0 = a.part + (2 * (int64_t)c0 + (s.first == c0 * per ? 0 : 1)) * stride;
+  for (int e = threadIdx.x; e < R * (D / 4); e += 256) {
+    const int r = e / (D / 4), c = e % (D / 4) * 4;
+    if (r / a.G >= s.nq) continue;
+    float M = -INFINITY, l = 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k = c0; k <= c1; ++k) M = fmaxf(M, ((k == c0 ? p0 : a.part + 2 * k * stride) + r * (D + 4))[D]);
+#pragma unroll 4
     for (int k = c0; k <= c1; ++k) {
-      const float* p = (k == c0 ? p0 : a.part + 2 * k * stride) + r * (D + 2);
-      const float e = p[0] > -INFINITY ? exp2f(p[0] - M) : p[1] == 0.0f ? 0.0f : 1.0f;
-      l += e * p[1];
-      v += e * p[2 + c];
+      const float* p = (k == c0 ? p0 : a.part + 2 * k * stride) + r * (D + 4);
+      const float w = p[D] > -INFINITY ? ex2(p[D] - M) : p[D + 1] == 0.0f ? 0.0f : 1.0f;
+      const float4 y = *reinterpret_cast<const float4*>(p + c);
+      l = fmaf(w, p[D + 1], l);
+      v.x = fmaf(w, y.x, v.x); v.y = fmaf(w, y.y, v.y); v.z = fmaf(w, y.z, v.z); v.w = fmaf(w, y.w, v.w);
     }
-    kd_store<D>(a, b, g, r, c, M, l, v);
+    kd_store<D>(a, s.b, s.g, r, c, M, l, v);
   }
 }
 
 namespace {
 
+// Items of up to this many blocks stay whole: two rounds of the warps over
+// them take less time than a second kernel.
+constexpr int64_t kKdWholeBlocks = 2 * kKdWarps;
+int kd_whole(const csa_shape* s) { return (s->n_max + kBlock - 1) / kBlock <= kKdWholeBlocks; }
+
 // CTAs of the decode kernel: one per SM, no more than there can be units
 int kd_ctas(const csa_shape* s) {
-  const int64_t units = (int64_t)s->B * s->Hkv * ((s->n_max + kBlock - 1) / kBlock);
+  const int64_t blocks = (s->n_max + kBlock - 1) / kBlock;
+  const int64_t units = (int64_t)s->B * s->Hkv * (kd_whole(s) ? 1 : blocks);
   const int nsm = sm_count();
   return (int)(units < nsm ? units : nsm);
 }
 
 size_t kd_workspace(const csa_shape* s, int T) {
   const int R = T * (s->Hq / s->Hkv);
-  return 256 + (size_t)2 * kd_ctas(s) * R * (s->d + 2) * 4;
+  return 256 + (kd_whole(s) ? 0 : (size_t)2 * kd_ctas(s) * R * (s->d + 4) * 4);
 }
 
-constexpr int kKdSharedBytes = 232448 - 2048;    // (2 KB: static arrays)
+constexpr int kKdSharedBytes = 232448 - (int)sizeof(KdBatch) - 64;
 template <int D, int RT, typename E>
 cudaError_t launch_kv4_decode_t(Kv4DecodeArgs a, int ncta, cudaStream_t st) {
   const int rest = KdLayout<D, RT>::ring(a.T * a.G);
@@ -1002,7 +1068,7 @@ cudaError_t launch_kv4_decode_t(Kv4DecodeArgs a, int ncta, cudaStream_t st) {
       cudaFuncSetAttribute(kv4_decode_kernel<D, RT, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   launch_pdl(kv4_decode_kernel<D, RT, E>, dim3(ncta), dim3(kKdThreads), smem, st, a);
-  if (ncta > 1) launch_pdl(kv4_join_kernel<D>, dim3(ncta - 1), dim3(256), 0, st, a, ncta);
+  if (ncta > 1 && !a.whole) launch_pdl(kv4_join_kernel<D>, dim3(ncta - 1), dim3(256), 0, st, a, ncta);
   return cudaGetLastError();
 }
 template <int D, typename E>
@@ -1045,7 +1111,8 @@ csa_status csa_kv4_decode(const csa_shape* shape, const csa_kv4* cache, int T, c
   a.B = shape->B; a.T = T; a.Hq = shape->Hq; a.Hkv = shape->Hkv; a.G = shape->Hq / shape->Hkv;
   a.rs = (float)(1.4426950408889634 / std::sqrt((double)shape->d));
   const int ncta = kd_ctas(shape);
-  add_launches(ncta > 1 ? 2 : 1);
+  a.whole = kd_whole(shape);
+  add_launches(ncta > 1 && !a.whole ? 2 : 1);
   cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t e = shape->d == 128 ? (bf16 ? launch_kv4_decode<128, __nv_bfloat16>(a, ncta, st) : launch_kv4_decode<128, float>(a, ncta, st))
                                         : (bf16 ? launch_kv4_decode<64, __nv_bfloat16>(a, ncta, st) : launch_kv4_decode<64, float>(a, ncta, st));
