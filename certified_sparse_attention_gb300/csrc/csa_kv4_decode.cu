@@ -72,6 +72,9 @@ constexpr int kKdThreads = (kKdWarps + 4) * 32;
 constexpr int kKdRegsConsumer = 152, kKdRegsProducer = 56;
 static_assert(3 * kKdRegsConsumer + kKdRegsProducer <= 4 * 128, "more registers than the launch has");
 constexpr int kKdMaxStages = 24;  // slots of a ring
+// warps of a team, for 1 .. 8 tiles (above 6 tiles: one team, four warps left
+// over)
+__host__ __device__ constexpr int kd_team(int ntile) { return ntile <= 4 ? ntile : ntile <= 6 ? 6 : 8; }
 
 // One block in shared memory: the keys' part (codes, bounds) in one ring, the
 // values' (codes, token scales) in another.  The bounds lie in eight pieces 16
@@ -98,6 +101,7 @@ struct KdBatch {
   int nq[kMaxB];
 };
 constexpr int kKdLead = 4;
+constexpr int kKdMaxCtas = 256;   // CTAs of a call (one per SM)
 
 // blocks of an item, the incomplete one counted
 __device__ __forceinline__ int64_t kd_blocks(int64_t n) { return (n + kBlock - 1) / kBlock; }
@@ -207,61 +211,119 @@ struct KdState {
   float m[RT], l[RT], acc[RT][D / 32];
 };
 
-// one online-softmax step of a warp over eight tokens: lane holds channels
-// [lane * D / 32, ...) of the eight rows; tok(lane & 7) is the position of
-// the token whose score the lane ends up with; row r sees positions below
-// s_end[r]
-template <int D, int RT>
-__device__ __forceinline__ void kd_step(KdState<D, RT>& st, const float (&kv)[8][D / 32], const float (&vv)[8][D / 32],
-                                        const float* s_q, const float* s_inv, const int64_t* s_end, int64_t pos,
-                                        int rows) {
-  constexpr int CPL = D / 32;
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// CNT consecutive elements (16 bytes aligned) as floats
+template <int CNT>
+__device__ __forceinline__ void kd_floats(const float* p, float (&x)[CNT]) {
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    if (r >= rows) break;
-    float part[8], q[CPL];
+  for (int i = 0; i < CNT; i += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(p + i);
+    x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+  }
+}
+template <int CNT>
+__device__ __forceinline__ void kd_floats(const __nv_bfloat16* p, float (&x)[CNT]) {
 #pragma unroll
-    for (int c = 0; c < CPL; ++c) q[c] = s_q[kd_q<D>(r, lane * CPL) + c] * (c & 1 ? 16.0f * s_inv[r] : s_inv[r]);
+  for (int i = 0; i < CNT; i += 8) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p + i);
+    const unsigned u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float p[CPL];
+    for (int e = 0; e < 8; ++e) x[i + e] = __uint_as_float(e & 1 ? u[e / 2] & 0xFFFF0000u : u[e / 2] << 16);
+  }
+}
+
+// One online-softmax step of a warp over `have` <= 8 full-precision tokens at
+// K, V (rows of D), the first at position pos.  Scores: lane (gid, tid) takes
+// token gid and the channels [tid D / 4, (tid + 1) D / 4) of every query row;
+// values: a lane takes the channels [lane D / 32, ...) of the state st, the
+// weights come through s_p ([8][RT] floats).  Row r sees positions below
+// s_end[r].
+template <int D, int RT, typename E>
+__device__ __forceinline__ void kd_step(KdState<D, RT>& st, const E* K, const E* V, int have, const float* s_q,
+                                        const float* s_inv, const int64_t* s_end, int64_t pos, float* s_p) {
+  constexpr int CPL = D / 32, NC = D / 4;
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
+  float vv[8][CPL];
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) p[c] = kv[i][c] * q[c];
-      part[i] = local_tree<CPL>(p);
-    }
-    float s = reduce8_rows(part);
-    const bool seen = pos < s_end[r];
-    if (!seen) s = -INFINITY;
-    float mx = s;
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-    const float mn = fmaxf(st.m[r], mx);
-    const unsigned who = __ballot_sync(0xffffffffu, seen) & 0xffu;
-    if (who == 0u) continue;
-    const float ref = mn > -INFINITY ? mn : 0.0f;
-    const float sc = exp2f(st.m[r] - ref);
-    const float p = seen ? exp2f(s - ref) : 0.0f;
-    float ps = p;
-    ps += __shfl_xor_sync(0xffffffffu, ps, 1);
-    ps += __shfl_xor_sync(0xffffffffu, ps, 2);
-    ps += __shfl_xor_sync(0xffffffffu, ps, 4);
-    st.l[r] = st.l[r] * sc + ps;
-    st.m[r] = mn;
+  for (int e = 0; e < 8; ++e) {
 #pragma unroll
-    for (int c = 0; c < CPL; ++c) st.acc[r][c] *= sc;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float pi = __shfl_sync(0xffffffffu, p, i);
-      // an unseen token's value may be anything: it is left out, not
-      // multiplied by zero
-      if (who >> i & 1u) {
-#pragma unroll
-        for (int c = 0; c < CPL; ++c) st.acc[r][c] += pi * vv[i][c];
+    for (int c = 0; c < CPL; ++c) vv[e][c] = 0.0f;
+    if (e < have) {
+      if (CPL == 4) {
+        const float4 v = Elem<E>::get4(V + e * D + lane * CPL);
+        vv[e][0] = v.x; vv[e][1] = v.y; vv[e][CPL - 2] = v.z; vv[e][CPL - 1] = v.w;
+      } else {
+        const float2 v = Elem<E>::get2(V + e * D + lane * CPL);
+        vv[e][0] = v.x; vv[e][1] = v.y;
       }
     }
   }
+  float k[NC], s[RT];
+  kd_floats<NC>(K + (gid < have ? gid : 0) * D + tid * NC, k);
+  bool cut = have < 8;                    // some row does not see some token
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    float even = 0.0f, odd = 0.0f;        // (odd channels of q carry 1/16)
+#pragma unroll
+    for (int i = 0; i < NC; i += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(s_q + kd_q<D>(r, tid * NC) + i);
+      even = fmaf(k[i], q.x, even); odd = fmaf(k[i + 1], q.y, odd);
+      even = fmaf(k[i + 2], q.z, even); odd = fmaf(k[i + 3], q.w, odd);
+    }
+    s[r] = fmaf(odd, 16.0f, even) * s_inv[r];
+    cut = cut || s_end[r] < pos + 8;
+  }
+#pragma unroll
+  for (int r = 0; r < RT; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], 1);
+#pragma unroll
+  for (int r = 0; r < RT; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], 2);
+  float top[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    if (gid >= have || pos + gid >= s_end[r]) s[r] = -INFINITY;
+    top[r] = s[r];
+  }
+#pragma unroll
+  for (int m = 4; m < 32; m <<= 1)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], m));
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const float mn = fmaxf(st.m[r], top[r]), ref = mn > -INFINITY ? mn : 0.0f;
+    const float old = ex2(st.m[r] - ref);
+    st.m[r] = mn;
+    st.l[r] *= old;
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) st.acc[r][c] *= old;
+    // an unseen token is marked
+    const bool seen = gid < have && pos + gid < s_end[r];
+    if (r * 4 / RT == tid) s_p[gid * RT + r] = seen ? ex2(s[r] - ref) : -1.0f;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float p[RT];
+#pragma unroll
+    for (int r = 0; r < RT; r += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(s_p + e * RT + r);
+      p[r] = v.x; p[r + 1] = v.y; p[r + 2] = v.z; p[r + 3] = v.w;
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      // an unseen token's value may be anything: it is left out, not
+      // multiplied by zero
+      if (!cut || !(p[r] < 0.0f)) {
+        st.l[r] += p[r];
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) st.acc[r][c] = fmaf(p[r], vv[e][c], st.acc[r][c]);
+      }
+    }
+  }
+  __syncwarp();
 }
 
 // ------------------------------------------------------- moving the blocks
@@ -359,11 +421,6 @@ __device__ __forceinline__ unsigned half_rest(float x, float y, unsigned hi) {
 __device__ __forceinline__ float pow2i(int k) { return __int_as_float((127 + k) << 23); }
 // exponent of x > 0 (subnormals: -127)
 __device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // the pair (x low, y high) in half precision, truncated
 __device__ __forceinline__ unsigned half_pair_rz(float x, float y) {
   unsigned r;
@@ -813,11 +870,9 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
   extern __shared__ __align__(128) uint8_t kd_sm[];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int R = a.T * a.G, Rp = (R + RT - 1) / RT * RT;
-  // teams: warps that share a block, one tile of rows each (more than 32 rows:
-  // one team of 8, four warps left over)
+  // teams: warps that share a block, one tile of rows each
   const int ntile = Rp / RT;
-  const int team = ntile <= 1 ? 1 : ntile <= 2 ? 2 : ntile <= 4 ? 4 : 8;
-  const int nteam = W / team;
+  const int team = kd_team(ntile), nteam = W / team;
   KdRing keys, values;
   keys.full = smem_u32(kd_sm);
   keys.empty = keys.full + kKdMaxStages * 8;
@@ -929,7 +984,7 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
     // positions of the incomplete block, if it lies here
     const int64_t p0 = it.seg.n / kBlock * kBlock;
     const int left = it.seg.blk1 * kBlock > p0 ? (int)(it.seg.n - p0) : 0;
-    if (rows > 0 && left > 0) {
+    if (rows > 0 && 8 * (i - base) < left) {
       // eight tokens at a time: the state moves on to lanes that hold channels
       __syncwarp();
       KdState<D, RT> st;
@@ -939,21 +994,13 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
 #pragma unroll
         for (int c = 0; c < CPL; ++c) st.acc[r][c] = my_acc[r * D + lane * CPL + c];
       }
-      for (int t0 = 8 * my_team; t0 < left; t0 += 8 * nteam) {
-        float kv[8][CPL], vv[8][CPL];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int t = t0 + e;
-          const bool there = t < left;
-          const E* kr = reinterpret_cast<const E*>(a.c.Kt) + (it.seg.bg * kBlock + t) * D + lane * CPL;
-          const E* vr = reinterpret_cast<const E*>(a.c.Vt) + (it.seg.bg * kBlock + t) * D + lane * CPL;
-#pragma unroll
-          for (int c = 0; c < CPL; ++c) {
-            kv[e][c] = there ? Elem<E>::get(kr, c) : 0.0f;
-            vv[e][c] = there ? Elem<E>::get(vr, c) : 0.0f;
-          }
-        }
-        kd_step<D, RT>(st, kv, vv, q, it.inv + r0, it.end + r0, p0 + t0 + (lane & 7), rows);
+      __syncwarp();
+      // (the teams go on in turn where the blocks ended; my_acc is free until
+      // the state returns to it)
+      for (int t0 = 8 * (i - base); t0 < left; t0 += 8 * nteam) {
+        const int64_t at = (it.seg.bg * kBlock + t0) * D;
+        kd_step<D, RT, E>(st, reinterpret_cast<const E*>(a.c.Kt) + at, reinterpret_cast<const E*>(a.c.Vt) + at,
+                          min(8, left - t0), q, it.inv + r0, it.end + r0, p0 + t0, my_acc);
       }
       __syncwarp();
 #pragma unroll
@@ -998,30 +1045,50 @@ template <int D>
 __global__ void __launch_bounds__(256) kv4_join_kernel(const Kv4DecodeArgs a, int ncta) {
   pdl_entry();
   __shared__ KdBatch batch;
+  __shared__ float s_w[8][kKdMaxCtas];
   kd_batch(a, batch);
   const int64_t per = kd_run(batch, ncta), x = ((int64_t)blockIdx.x + 1) * per;
   if (x >= batch.pref[kMaxB]) return;
   const KdSeg s = kd_seg(a, batch, x, x + 1);
   if (s.first == x || s.first / per != (int64_t)blockIdx.x) return;
-  const int c0 = (int)blockIdx.x, c1 = (int)(s.last / per);
-  const int R = a.T * a.G;
+  const int c0 = (int)blockIdx.x, parts = (int)(s.last / per) - c0 + 1;
+  const int R = a.T * a.G, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  // part 0 is the first or the last one of its CTA, the others the first ones
   const int64_t stride = (int64_t)R * (D + 4);
-  const float* p0 = a.part + (2 * (int64_t)c0 + (s.first == c0 * per ? 0 : 1)) * stride;
-  for (int e = threadIdx.x; e < R * (D / 4); e += 256) {
-    const int r = e / (D / 4), c = e % (D / 4) * 4;
-    if (r / a.G >= s.nq) continue;
-    float M = -INFINITY, l = 0.0f;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int k = c0; k <= c1; ++k) M = fmaxf(M, ((k == c0 ? p0 : a.part + 2 * k * stride) + r * (D + 4))[D]);
-#pragma unroll 4
-    for (int k = c0; k <= c1; ++k) {
-      const float* p = (k == c0 ? p0 : a.part + 2 * k * stride) + r * (D + 4);
-      const float w = p[D] > -INFINITY ? ex2(p[D] - M) : p[D + 1] == 0.0f ? 0.0f : 1.0f;
-      const float4 y = *reinterpret_cast<const float4*>(p + c);
-      l = fmaf(w, p[D + 1], l);
-      v.x = fmaf(w, y.x, v.x); v.y = fmaf(w, y.y, v.y); v.z = fmaf(w, y.z, v.z); v.w = fmaf(w, y.w, v.w);
+  const float* part0 = a.part + (2 * (int64_t)c0 + (s.first == c0 * per ? 0 : 1)) * stride;
+  const float* part1 = a.part + 2 * (int64_t)c0 * stride;
+  // a warp to a row: the parts' weights first, by the lanes, then the sums
+  for (int r = w; r < R && r / a.G < s.nq; r += 8) {
+    const int64_t row = r * (D + 4);
+    float M = -INFINITY;
+    for (int k = lane; k < parts; k += 32) {
+      const float m = ((k ? part1 + 2 * k * stride : part0) + row)[D];
+      s_w[w][k] = m;
+      M = fmaxf(M, m);
     }
-    kd_store<D>(a, s.b, s.g, r, c, M, l, v);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float l = 0.0f;
+    for (int k = lane; k < parts; k += 32) {
+      const float lk = ((k ? part1 + 2 * k * stride : part0) + row)[D + 1], m = s_w[w][k];
+      const float e = m > -INFINITY ? ex2(m - M) : lk == 0.0f ? 0.0f : 1.0f;
+      s_w[w][k] = e;
+      l = fmaf(e, lk, l);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    __syncwarp();
+    if (lane < D / 4) {
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+      for (int k = 0; k < parts; ++k) {
+        const float4 y = *reinterpret_cast<const float4*>((k ? part1 + 2 * k * stride : part0) + row + lane * 4);
+        const float e = s_w[w][k];
+        v.x = fmaf(e, y.x, v.x); v.y = fmaf(e, y.y, v.y); v.z = fmaf(e, y.z, v.z); v.w = fmaf(e, y.w, v.w);
+      }
+      kd_store<D>(a, s.b, s.g, r, lane * 4, M, l, v);
+    }
+    __syncwarp();
   }
 }
 
@@ -1036,7 +1103,7 @@ int kd_whole(const csa_shape* s) { return (s->n_max + kBlock - 1) / kBlock <= kK
 int kd_ctas(const csa_shape* s) {
   const int64_t blocks = (s->n_max + kBlock - 1) / kBlock;
   const int64_t units = (int64_t)s->B * s->Hkv * (kd_whole(s) ? 1 : blocks);
-  const int nsm = sm_count();
+  const int nsm = sm_count() < kKdMaxCtas ? sm_count() : kKdMaxCtas;
   return (int)(units < nsm ? units : nsm);
 }
 
@@ -1054,7 +1121,7 @@ cudaError_t launch_kv4_decode_t(Kv4DecodeArgs a, int ncta, cudaStream_t st) {
   // less time (the values' come while the warp is at the keys)
   constexpr int K = KdStage<D>::bytesK, V = KdStage<D>::bytesV;
   const int ntile = (a.T * a.G + RT - 1) / RT;
-  const int nteam = kKdWarps / (ntile <= 1 ? 1 : ntile <= 2 ? 2 : ntile <= 4 ? 4 : 8);
+  const int nteam = kKdWarps / kd_team(ntile);
   int nk = 1, nv = 1;
   for (bool more = true; more;) {
     more = false;
