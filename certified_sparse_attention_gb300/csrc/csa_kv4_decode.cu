@@ -98,7 +98,7 @@ struct KdStage {
 struct KdBatch {
   int64_t pref[kMaxB + 1];    // units of the sequences before b (pref[B]: all)
   int64_t len[kMaxB];
-  int nq[kMaxB];
+  uint8_t nq[kMaxB];
 };
 constexpr int kKdLead = 4;
 constexpr int kKdMaxCtas = 256;   // CTAs of a call (one per SM)
@@ -121,7 +121,7 @@ __device__ __forceinline__ void kd_batch(const Kv4DecodeArgs& a, KdBatch& s) {
       if (b < a.B) {
         const int64_t n = min(max(a.len[b], (int64_t)0), a.n_max);
         s.len[b] = n;
-        s.nq[b] = a.n_q ? (int)min(max(a.n_q[b], (int64_t)0), (int64_t)a.T) : a.T;
+        s.nq[b] = (uint8_t)(a.n_q ? min(max(a.n_q[b], (int64_t)0), (int64_t)a.T) : a.T);
         u[i] = kd_units(a, n) * a.Hkv;
       }
       sum += u[i];
@@ -312,11 +312,22 @@ __device__ __forceinline__ void kd_step(KdState<D, RT>& st, const E* K, const E*
       const float4 v = *reinterpret_cast<const float4*>(s_p + e * RT + r);
       p[r] = v.x; p[r + 1] = v.y; p[r + 2] = v.z; p[r + 3] = v.w;
     }
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
+    if (cut) {
       // an unseen token's value may be anything: it is left out, not
       // multiplied by zero
-      if (!cut || !(p[r] < 0.0f)) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const bool out = p[r] < 0.0f;
+        st.l[r] += out ? 0.0f : p[r];
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+          const float sum = fmaf(p[r], vv[e][c], st.acc[r][c]);
+          st.acc[r][c] = out ? st.acc[r][c] : sum;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
         st.l[r] += p[r];
 #pragma unroll
         for (int c = 0; c < CPL; ++c) st.acc[r][c] = fmaf(p[r], vv[e][c], st.acc[r][c]);
@@ -468,11 +479,15 @@ __device__ __forceinline__ void kd_fast_init(KdFast<D, RT>& f, const float* s_in
 }
 
 // One block: its keys' part at st, its values' part at vt; between() is
-// called when the one has been read and before the other is.  MASK: row ra
-// sees the block's tokens below endA only, row ra + 1 those below endB.
-template <int D, int RT, bool MASK, typename Between>
+// called when the one has been read and before the other is.  masked: row ra
+// sees the block's tokens below endA only, row ra + 1 those below endB.  The
+// block goes through in two halves of 32 tokens by loops that stay loops:
+// unrolled, the code was more than the instruction caches could feed to warps
+// that are each at another place of it (at 8 rows the warps spent a third of
+// their time waiting for instructions).
+template <int D, int RT, typename Between>
 __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* st, const uint8_t* vt, const float* s_q,
-                                              int endA, int endB, Between between) {
+                                              bool masked, int endA, int endB, Between between) {
   using St = KdStage<D>;
   constexpr int NC = D / 4;        // channels of a lane
   constexpr int NW = D / 32;       // code words of a lane in a key row
@@ -497,7 +512,7 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
     const float2 dl = *reinterpret_cast<const float2*>(st + St::B + (4 + (lane >> 3)) * St::PITCH + (lane & 7) * 8);
     top = fmaxf(dl.x, dl.y);
   }
-  if (__any_sync(0xffffffffu, top >= f.most)) {
+  if (__builtin_expect(__any_sync(0xffffffffu, top >= f.most), 0)) {
     float t = top < INFINITY ? top : 0.0f;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, m));
@@ -510,235 +525,244 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
     f.csA = __shfl_sync(0xffffffffu, c, 4 * ra);
     f.csB = __shfl_sync(0xffffffffu, c, 4 * ra + 4);
   }
-  float x[NC];
-#pragma unroll
-  for (int i = 0; i < NC; i += 4) {
-    const float4 q = *reinterpret_cast<const float4*>(sq + i), dl = *reinterpret_cast<const float4*>(sd + i);
-    x[i] = q.x * dl.x; x[i + 1] = q.y * dl.y; x[i + 2] = q.z * dl.z; x[i + 3] = q.w * dl.w;
-  }
-  if (f.xs != 1.0f) {
-#pragma unroll
-    for (int i = 0; i < NC; ++i) x[i] *= f.xs;
-  }
-  // (RT = 4: the lanes gid and gid + 4 take half of the channels each)
-  constexpr int QM = RT == 4 ? NC / 2 : NC;
-  const int half = RT == 4 ? (gid >> 2) * QM : 0;
+  // Scores of the four tiles of 16 tokens, two code words (16 channels of a
+  // lane) at a time: q_c Delta_c as the operand (column gid, channel pairs (8
+  // w + 0, 4), (1, 5), (2, 6), (3, 7); high part = the leading 11 bits, low
+  // part = the rest), and sum_c q_c m_c beside it, in float32.  (RT = 4: the
+  // lanes gid and gid + 4 take half of the channels of that each.)  Matrix
+  // instructions truncate their sums: they start from zero.
+  float t[4][4] = {};
   float qm = 0.0f, qm1 = 0.0f;
+  const unsigned cut = RT == 8 || gid >= 4 ? 0xffffe000u : 0u;
+#pragma unroll 1
+  for (int wp = 0; wp < NW / 2; ++wp) {
+    unsigned bq[HL][2][4];
 #pragma unroll
-  for (int i = 0; i < QM; i += 4) {
-    const float4 q = *reinterpret_cast<const float4*>(sq + half + i), mn = *reinterpret_cast<const float4*>(sm + half + i);
-    qm = fmaf(q.x, mn.x, qm); qm1 = fmaf(q.y, mn.y, qm1);
-    qm = fmaf(q.z, mn.z, qm); qm1 = fmaf(q.w, mn.w, qm1);
+    for (int w = 0; w < 2; ++w) {
+      const int c = wp * 16 + w * 8;
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(sq + c + i), dl = *reinterpret_cast<const float4*>(sd + c + i);
+        x[i] = q.x * dl.x; x[i + 1] = q.y * dl.y; x[i + 2] = q.z * dl.z; x[i + 3] = q.w * dl.w;
+        if (RT == 8) {
+          const float4 mn = *reinterpret_cast<const float4*>(sm + c + i);
+          qm = fmaf(q.x, mn.x, qm); qm1 = fmaf(q.y, mn.y, qm1);
+          qm = fmaf(q.z, mn.z, qm); qm1 = fmaf(q.w, mn.w, qm1);
+        }
+      }
+      if (RT == 4) {
+        const int h = c + (gid >> 2) * 4;
+        const float4 q = *reinterpret_cast<const float4*>(sq + h), mn = *reinterpret_cast<const float4*>(sm + h);
+        qm = fmaf(q.x, mn.x, qm); qm1 = fmaf(q.y, mn.y, qm1);
+        qm = fmaf(q.z, mn.z, qm); qm1 = fmaf(q.w, mn.w, qm1);
+      }
+      if (f.xs != 1.0f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= f.xs;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float u = x[e], v = x[e + 4];
+        if (RT == 8) bq[0][w][e] = half_pair_rz(u, v);
+        bq[HL - 1][w][e] = half_pair_rz(u - __uint_as_float(__float_as_uint(u) & cut), v - __uint_as_float(__float_as_uint(v) & cut));
+      }
+    }
+#pragma unroll
+    for (int pr = 0; pr < 2; ++pr) {
+      uint2 k[4];                        // rows gid, gid + 8 of tile 2 pr, then of the next
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        k[j] = *reinterpret_cast<const uint2*>(st + (32 * pr + 8 * j + gid) * (D / 2) + tid * (D / 8) + wp * 8);
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const unsigned ka = w ? k[2 * y].y : k[2 * y].x, kb = w ? k[2 * y + 1].y : k[2 * y + 1].x;
+            const unsigned a = z ? ka >> 5 : ka << 3, b = z ? kb >> 5 : kb << 3;
+#pragma unroll
+            for (int h = HL - 1; h >= 0; --h)
+              mma_f16(t[2 * pr + y], a & kNibA, b & kNibA, a & kNibB, b & kNibB, bq[h][w][2 * z], bq[h][w][2 * z + 1]);
+          }
+    }
   }
-  qm = fmaf(qm1, 16.0f, qm) * f.qinv;
+  between();
+  qm = fmaf(qm1, 16.0f, qm) * f.qinv;    // (odd channels carry 1/16)
   qm += __shfl_xor_sync(0xffffffffu, qm, 1);
   qm += __shfl_xor_sync(0xffffffffu, qm, 2);
   if (RT == 4) qm += __shfl_xor_sync(0xffffffffu, qm, 16);
   const float sA = __shfl_sync(0xffffffffu, qm, 4 * ra) - f.rA, sB = __shfl_sync(0xffffffffu, qm, 4 * ra + 4) - f.rB;
-
-  // the operand: column gid, channel pairs (8 w + 0, 4), (1, 5), (2, 6), (3,
-  // 7); high part = the leading 11 bits, low part = the rest
-  unsigned bq[HL][NW][4];
-  const unsigned cut = RT == 8 || gid >= 4 ? 0xffffe000u : 0u;
+  // The scores relative to rA, rB, of a half's two tiles.  RT = 4: the two
+  // parts are added; the lane has token 16 y + gid (+ 8 in the upper lanes) of
+  // its half, rows ra, ra + 1, in s[y][0], s[y][1]; RT = 8: tokens gid and gid
+  // + 8 in s[y][0..1], s[y][2..3].
+  constexpr int TK = RT == 8 ? 2 : 1;    // tokens of a tile in a lane
+  float s[2][2 * TK], later[2][2 * TK];  // of the half at hand, and of the other
 #pragma unroll
-  for (int w = 0; w < NW; ++w)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float u = x[8 * w + e], v = x[8 * w + e + 4];
-      if (RT == 8) bq[0][w][e] = half_pair_rz(u, v);
-      bq[HL - 1][w][e] = half_pair_rz(u - __uint_as_float(__float_as_uint(u) & cut), v - __uint_as_float(__float_as_uint(v) & cut));
+  for (int y = 0; y < 4; ++y) {
+    float v[4];
+    if (RT == 4) {
+      const float g0 = __shfl_xor_sync(0xffffffffu, upper ? t[y][0] : t[y][2], 2);
+      const float g1 = __shfl_xor_sync(0xffffffffu, upper ? t[y][1] : t[y][3], 2);
+      v[0] = fmaf((upper ? t[y][2] : t[y][0]) + g0, f.csA, sA);
+      v[1] = fmaf((upper ? t[y][3] : t[y][1]) + g1, f.csB, sB);
+    } else {
+      v[0] = fmaf(t[y][0], f.csA, sA); v[1] = fmaf(t[y][1], f.csB, sB);
+      v[2] = fmaf(t[y][2], f.csA, sA); v[3] = fmaf(t[y][3], f.csB, sB);
     }
+#pragma unroll
+    for (int e = 0; e < 2 * TK; ++e) (y < 2 ? s[y] : later[y - 2])[e] = v[e];
+  }
 
-  // scores of the four tiles of 16 tokens, two at a time (matrix instructions
-  // truncate their sums: chains start from zero, each part its own, and sum_c
-  // q_c m_c is added in float32)
-  float s[4][4];
+#pragma unroll 1
+  for (int hf = 0; hf < 2; ++hf) {
+    const auto token = [&](int y, int k) { return 32 * hf + 16 * y + gid + (RT == 8 ? 8 * k : upper ? 8 : 0); };
+    float2 sc[2][TK];                    // token scales
+    float big = -INFINITY, wide = 0.0f;
 #pragma unroll
-  for (int pr = 0; pr < 2; ++pr) {
-    unsigned k[4][NW];      // rows gid, gid + 8 of tile 2 pr, then of the next
+    for (int y = 0; y < 2; ++y)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint8_t* kr = st + (32 * pr + 8 * j + gid) * (D / 2) + tid * (D / 8);
-      if (D == 128) {
-        const uint4 u = *reinterpret_cast<const uint4*>(kr);
-        k[j][0] = u.x; k[j][1] = u.y; k[j][NW - 2] = u.z; k[j][NW - 1] = u.w;
+      for (int k = 0; k < TK; ++k) {
+        sc[y][k] = *reinterpret_cast<const float2*>(vt + St::S + token(y, k) * 8);
+        if (masked) {
+          if (token(y, k) >= endA) s[y][2 * k] = -INFINITY;
+          if (token(y, k) >= endB) s[y][2 * k + 1] = -INFINITY;
+        }
+        big = fmaxf(big, fmaxf(s[y][2 * k], s[y][2 * k + 1]));
+        if (!masked || token(y, k) < max(endA, endB)) wide = fmaxf(wide, sc[y][k].y);
+      }
+    // The reference moves only when a score exceeds it by more than 8 (weights
+    // up to 2^8), and the value scale only when Delta_t does not fit (Delta_t
+    // sv up to 2^6): both are rare after the first block.
+    if (__builtin_expect(__any_sync(0xffffffffu, f.newA || f.newB || big > 8.0f || wide > f.wide), 0)) {
+      float xA = -INFINITY, xB = -INFINITY, tA = 0.0f, tB = 0.0f;
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int k = 0; k < TK; ++k) {
+          const float t = sc[y][k].y < INFINITY ? sc[y][k].y : 0.0f;
+          xA = fmaxf(xA, s[y][2 * k]);
+          xB = fmaxf(xB, s[y][2 * k + 1]);
+          if (!masked || token(y, k) < endA) tA = fmaxf(tA, t);
+          if (!masked || token(y, k) < endB) tB = fmaxf(tB, t);
+        }
+#pragma unroll
+      for (int m = (RT == 4 ? 2 : 4); m < 32; m <<= 1) {
+        xA = fmaxf(xA, __shfl_xor_sync(0xffffffffu, xA, m));
+        xB = fmaxf(xB, __shfl_xor_sync(0xffffffffu, xB, m));
+        tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, m));
+        tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, m));
+      }
+      // the references move up by dA, dB (a row's first tokens: to their maximum)
+      const float dA = f.newA ? (xA > -INFINITY ? xA : 0.0f) : fmaxf(xA, 0.0f);
+      const float dB = f.newB ? (xB > -INFINITY ? xB : 0.0f) : fmaxf(xB, 0.0f);
+      const float eA = f.newA ? 1.0f : ex2(-dA), eB = f.newB ? 1.0f : ex2(-dB);
+      float upA = 1.0f, upB = 1.0f;
+      if (tA > 0.0f && (f.svA == 0.0f || tA * f.svA > 64.0f)) {
+        const float to = pow2i(min(max(5 - exponent(tA), -100), 100));   // Delta sv in [2^5, 2^6)
+        if (f.svA != 0.0f) upA = to / f.svA;
+        f.svA = to;
+      }
+      if (tB > 0.0f && (f.svB == 0.0f || tB * f.svB > 64.0f)) {
+        const float to = pow2i(min(max(5 - exponent(tB), -100), 100));
+        if (f.svB != 0.0f) upB = to / f.svB;
+        f.svB = to;
+      }
+      f.wide = f.svA == 0.0f || f.svB == 0.0f ? 0.0f : 64.0f / fmaxf(f.svA, f.svB);
+      f.lA *= eA; f.lB *= eB;
+      f.omA *= eA; f.omB *= eB;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        f.o[i][0] *= eA * upA; f.o[i][1] *= eB * upB;
+        f.o[i][2] *= eA * upA; f.o[i][3] *= eB * upB;
+      }
+      f.rA += dA; f.rB += dB;
+      f.newA = f.newA && !(xA > -INFINITY);
+      f.newB = f.newB && !(xB > -INFINITY);
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int k = 0; k < TK; ++k) {
+          s[y][2 * k] -= dA; s[y][2 * k + 1] -= dB;
+          later[y][2 * k] -= dA; later[y][2 * k + 1] -= dB;
+        }
+    }
+    // Weights and the second operand: column gid, token pairs.  The tokens
+    // gid + 8 of a tile enter as 15 - n with the opposite sign, and with m +
+    // 15 Delta for m: the sums of codes, all positive, would outgrow the
+    // differences that the output consists of (values around zero) and leave
+    // them their rounding errors.
+    float omA = 0.0f, omB = 0.0f;
+    unsigned bp[HL][2][2];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      unsigned hi[TK], lo[TK];
+#pragma unroll
+      for (int k = 0; k < TK; ++k) {
+        const float pA = ex2(s[y][2 * k]), pB = ex2(s[y][2 * k + 1]);
+        f.lA += pA; f.lB += pB;
+        const bool turned = RT == 8 ? k == 1 : upper;
+        const float dl = sc[y][k].y, m = fmaf(dl, turned ? 15.0f : 0.0f, sc[y][k].x);
+        float wA = pA * (dl * (turned ? -f.svA : f.svA)), wB = pB * (dl * (turned ? -f.svB : f.svB));
+        if (__builtin_expect(masked, 0)) {
+          // an unseen token's value may be anything: it is left out, not
+          // multiplied by zero
+          if (token(y, k) >= endA) wA = 0.0f; else omA = fmaf(pA, m, omA);
+          if (token(y, k) >= endB) wB = 0.0f; else omB = fmaf(pB, m, omB);
+        } else {
+          omA = fmaf(pA, m, omA);
+          omB = fmaf(pB, m, omB);
+        }
+        hi[k] = half_pair(wA, wB);
+        lo[k] = half_rest(wA, wB, hi[k]);
+      }
+      if (RT == 4) {
+        const unsigned got = __shfl_xor_sync(0xffffffffu, upper ? hi[0] : lo[0], 2);
+        bp[0][y][0] = transpose8(upper ? got : hi[0]);
+        bp[0][y][1] = transpose8(upper ? lo[0] : got);
       } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(kr);
-        k[j][0] = u.x; k[j][1] = u.y;
+        bp[0][y][0] = transpose8(hi[0]);
+        bp[0][y][1] = transpose8(hi[TK - 1]);
+        bp[HL - 1][y][0] = transpose8(lo[0]);
+        bp[HL - 1][y][1] = transpose8(lo[TK - 1]);
       }
     }
-    float t[2][HL][4] = {};
+    // (the two halves of a tile's tokens cancel: RT = 4 has them in lane pairs)
+    if (RT == 4) {
+      omA += __shfl_xor_sync(0xffffffffu, omA, 2);
+      omB += __shfl_xor_sync(0xffffffffu, omB, 2);
+    }
+    f.omA += omA;
+    f.omB += omB;
 #pragma unroll
-    for (int w = 0; w < NW; ++w)
+    for (int i = 0; i < D / 16; i += 2) {
+      unsigned v[4];          // channels gid, gid + 8 of tile i, then of the next
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = *reinterpret_cast<const unsigned*>(vt + (16 * i + 8 * j + gid) * (kBlock / 2) + tid * 8 + hf * 4);
+      float t[2][4] = {};
+#pragma unroll
+      for (int h = HL - 1; h >= 0; --h)  // (low parts first)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const unsigned a = v[2 * z], b = v[2 * z + 1];
+            const unsigned a0 = (y ? a >> 1 : a << 7) & kNibB, b0 = (y ? b >> 1 : b << 7) & kNibB;
+            const unsigned a1 = ~(y ? a >> 5 : a << 3) & kNibB, b1 = ~(y ? b >> 5 : b << 3) & kNibB;
+            mma_f16(t[z], a0, b0, a1, b1, bp[h][y][0], bp[h][y][1]);
+          }
 #pragma unroll
       for (int z = 0; z < 2; ++z)
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const unsigned a = z ? k[2 * y][w] >> 5 : k[2 * y][w] << 3, b = z ? k[2 * y + 1][w] >> 5 : k[2 * y + 1][w] << 3;
-#pragma unroll
-          for (int h = 0; h < HL; ++h)
-            mma_f16(t[y][h], a & kNibA, b & kNibA, a & kNibB, b & kNibB, bq[h][w][2 * z], bq[h][w][2 * z + 1]);
-        }
+        for (int e = 0; e < 4; ++e) f.o[i + z][e] += t[z][e];
+    }
 #pragma unroll
     for (int y = 0; y < 2; ++y)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[2 * pr + y][e] = RT == 8 ? t[y][0][e] + t[y][HL - 1][e] : t[y][0][e];
-  }
-  between();
-  // RT = 4: add the two parts; afterwards the lane has token 16 mt + gid (+ 8
-  // in the upper lanes), rows ra, ra + 1, in s[mt][0], s[mt][1].
-  // RT = 8: tokens gid and gid + 8 in s[mt][0..1] and s[mt][2..3].
-  constexpr int TK = RT == 8 ? 2 : 1;    // tokens of a tile in a lane
-  const auto token = [&](int mt, int k) { return 16 * mt + gid + (RT == 8 ? 8 * k : upper ? 8 : 0); };
-  float big = -INFINITY;                 // (scores are relative to rA, rB)
-  float2 sc[4][TK];                      // token scales
-  float wide = 0.0f;
-#pragma unroll
-  for (int mt = 0; mt < 4; ++mt) {
-    if (RT == 4) {
-      const float g0 = __shfl_xor_sync(0xffffffffu, upper ? s[mt][0] : s[mt][2], 2);
-      const float g1 = __shfl_xor_sync(0xffffffffu, upper ? s[mt][1] : s[mt][3], 2);
-      s[mt][0] = fmaf((upper ? s[mt][2] : s[mt][0]) + g0, f.csA, sA);
-      s[mt][1] = fmaf((upper ? s[mt][3] : s[mt][1]) + g1, f.csB, sB);
-    } else {
-      s[mt][0] = fmaf(s[mt][0], f.csA, sA); s[mt][1] = fmaf(s[mt][1], f.csB, sB);
-      s[mt][2] = fmaf(s[mt][2], f.csA, sA); s[mt][3] = fmaf(s[mt][3], f.csB, sB);
-    }
-#pragma unroll
-    for (int k = 0; k < TK; ++k) {
-      sc[mt][k] = *reinterpret_cast<const float2*>(vt + St::S + token(mt, k) * 8);
-      if (MASK) {
-        if (token(mt, k) >= endA) s[mt][2 * k] = -INFINITY;
-        if (token(mt, k) >= endB) s[mt][2 * k + 1] = -INFINITY;
-      }
-      big = fmaxf(big, fmaxf(s[mt][2 * k], s[mt][2 * k + 1]));
-      if (!MASK || token(mt, k) < max(endA, endB)) wide = fmaxf(wide, sc[mt][k].y);
-    }
-  }
-  // The reference moves only when a score exceeds it by more than 8 (weights
-  // up to 2^8), and the value scale only when Delta_t does not fit (Delta_t sv
-  // up to 2^6): both are rare after the first block.
-  if (__any_sync(0xffffffffu, f.newA || f.newB || big > 8.0f || wide > f.wide)) {
-    float xA = -INFINITY, xB = -INFINITY, tA = 0.0f, tB = 0.0f;
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-      for (int k = 0; k < TK; ++k) {
-        const float t = sc[mt][k].y < INFINITY ? sc[mt][k].y : 0.0f;
-        xA = fmaxf(xA, s[mt][2 * k]);
-        xB = fmaxf(xB, s[mt][2 * k + 1]);
-        if (!MASK || token(mt, k) < endA) tA = fmaxf(tA, t);
-        if (!MASK || token(mt, k) < endB) tB = fmaxf(tB, t);
-      }
-#pragma unroll
-    for (int m = (RT == 4 ? 2 : 4); m < 32; m <<= 1) {
-      xA = fmaxf(xA, __shfl_xor_sync(0xffffffffu, xA, m));
-      xB = fmaxf(xB, __shfl_xor_sync(0xffffffffu, xB, m));
-      tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, m));
-      tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, m));
-    }
-    // the references move up by dA, dB (a row's first tokens: to their maximum)
-    const float dA = f.newA ? (xA > -INFINITY ? xA : 0.0f) : fmaxf(xA, 0.0f);
-    const float dB = f.newB ? (xB > -INFINITY ? xB : 0.0f) : fmaxf(xB, 0.0f);
-    const float eA = f.newA ? 1.0f : ex2(-dA), eB = f.newB ? 1.0f : ex2(-dB);
-    float upA = 1.0f, upB = 1.0f;
-    if (tA > 0.0f && (f.svA == 0.0f || tA * f.svA > 64.0f)) {
-      const float to = pow2i(min(max(5 - exponent(tA), -100), 100));   // Delta sv in [2^5, 2^6)
-      if (f.svA != 0.0f) upA = to / f.svA;
-      f.svA = to;
-    }
-    if (tB > 0.0f && (f.svB == 0.0f || tB * f.svB > 64.0f)) {
-      const float to = pow2i(min(max(5 - exponent(tB), -100), 100));
-      if (f.svB != 0.0f) upB = to / f.svB;
-      f.svB = to;
-    }
-    f.wide = f.svA == 0.0f || f.svB == 0.0f ? 0.0f : 64.0f / fmaxf(f.svA, f.svB);
-    f.lA *= eA; f.lB *= eB;
-    f.omA *= eA; f.omB *= eB;
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      f.o[i][0] *= eA * upA; f.o[i][1] *= eB * upB;
-      f.o[i][2] *= eA * upA; f.o[i][3] *= eB * upB;
-    }
-    f.rA += dA; f.rB += dB;
-    f.newA = f.newA && !(xA > -INFINITY);
-    f.newB = f.newB && !(xB > -INFINITY);
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-      for (int k = 0; k < TK; ++k) { s[mt][2 * k] -= dA; s[mt][2 * k + 1] -= dB; }
-  }
-  // Weights and the second operand: column gid, token pairs.  The tokens
-  // gid + 8 of a tile enter as 15 - n with the opposite sign, and
-  // with m + 15 Delta for m: the sums of codes, all positive, would outgrow
-  // the differences that the output consists of (values around zero) and
-  // leave them their rounding errors.
-  float omA = 0.0f, omB = 0.0f;
-  unsigned bp[HL][4][2];
-#pragma unroll
-  for (int mt = 0; mt < 4; ++mt) {
-    unsigned hi[TK], lo[TK];
-#pragma unroll
-    for (int k = 0; k < TK; ++k) {
-      const float pA = ex2(s[mt][2 * k]), pB = ex2(s[mt][2 * k + 1]);
-      f.lA += pA; f.lB += pB;
-      const bool turned = RT == 8 ? k == 1 : upper;
-      const float y = sc[mt][k].y, m = fmaf(y, turned ? 15.0f : 0.0f, sc[mt][k].x);
-      float zA = pA * m, zB = pB * m;
-      float wA = pA * (y * (turned ? -f.svA : f.svA)), wB = pB * (y * (turned ? -f.svB : f.svB));
-      if (MASK) {
-        // an unseen token's value may be anything: it is left out, not
-        // multiplied by zero
-        if (token(mt, k) >= endA) zA = wA = 0.0f;
-        if (token(mt, k) >= endB) zB = wB = 0.0f;
-      }
-      omA += zA;
-      omB += zB;
-      hi[k] = half_pair(wA, wB);
-      lo[k] = half_rest(wA, wB, hi[k]);
-    }
-    if (RT == 4) {
-      const unsigned got = __shfl_xor_sync(0xffffffffu, upper ? hi[0] : lo[0], 2);
-      bp[0][mt][0] = transpose8(upper ? got : hi[0]);
-      bp[0][mt][1] = transpose8(upper ? lo[0] : got);
-    } else {
-      bp[0][mt][0] = transpose8(hi[0]);
-      bp[0][mt][1] = transpose8(hi[TK - 1]);
-      bp[HL - 1][mt][0] = transpose8(lo[0]);
-      bp[HL - 1][mt][1] = transpose8(lo[TK - 1]);
-    }
-  }
-  // (the two halves of the tokens cancel: RT = 4 has them in lane pairs)
-  if (RT == 4) {
-    omA += __shfl_xor_sync(0xffffffffu, omA, 2);
-    omB += __shfl_xor_sync(0xffffffffu, omB, 2);
-  }
-  f.omA += omA;
-  f.omB += omB;
-#pragma unroll
-  for (int i = 0; i < D / 16; i += 2) {
-    uint2 v[4];             // channels gid, gid + 8 of tile i, then of the next
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      v[j] = *reinterpret_cast<const uint2*>(vt + (16 * i + 8 * j + gid) * (kBlock / 2) + tid * 8);
-    float t[2][HL][4] = {};
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const unsigned a = mt < 2 ? v[2 * y].x : v[2 * y].y, b = mt < 2 ? v[2 * y + 1].x : v[2 * y + 1].y;
-        const unsigned a0 = (mt & 1 ? a >> 1 : a << 7) & kNibB, b0 = (mt & 1 ? b >> 1 : b << 7) & kNibB;
-        const unsigned a1 = ~(mt & 1 ? a >> 5 : a << 3) & kNibB, b1 = ~(mt & 1 ? b >> 5 : b << 3) & kNibB;
-#pragma unroll
-        for (int h = 0; h < HL; ++h) mma_f16(t[y][h], a0, b0, a1, b1, bp[h][mt][0], bp[h][mt][1]);
-      }
-#pragma unroll
-    for (int y = 0; y < 2; ++y)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (RT == 8) f.o[i + y][e] += t[y][HL - 1][e];
-        f.o[i + y][e] += t[y][0][e];
-      }
+      for (int e = 0; e < 2 * TK; ++e) s[y][e] = later[y][e];
   }
 }
 
@@ -789,6 +813,10 @@ struct KdItem {
   int64_t end[CSA_KV4_MAX_ROWS];    // row r sees positions below end[r]
   float inv[CSA_KV4_MAX_ROWS];      // undoes the scale of row r (kd_q)
 };
+// where an item's merged sums go
+struct KdDone {
+  int b, g, nq, done, part;
+};
 
 template <int D, int RT, typename E>
 __device__ __forceinline__ void kd_queries(const Kv4DecodeArgs& a, const KdBatch& batch, int64_t u0, int64_t u1,
@@ -808,6 +836,16 @@ __device__ __forceinline__ void kd_queries(const Kv4DecodeArgs& a, const KdBatch
     if (lane == 0) it.seg = sg;
     const E* base = reinterpret_cast<const E*>(a.q) + sg.b * a.qs.b + (int64_t)sg.g * a.G * a.qs.h + lane * CPL;
     float* q = s_q + buf * kd_q<D>(Rp, 0);
+    // the rows of the incomplete block, if it lies here, on their way to L2
+    if (sg.blk1 > sg.n / kBlock) {
+      const int bytes = (int)(sg.n % kBlock) * D * (int)sizeof(E);
+      const char* kt = reinterpret_cast<const char*>(a.c.Kt) + sg.bg * kBlock * D * (int)sizeof(E);
+      const char* vt = reinterpret_cast<const char*>(a.c.Vt) + sg.bg * kBlock * D * (int)sizeof(E);
+      for (int x = lane * 128; x < bytes; x += 32 * 128) {
+        asm volatile("prefetch.global.L2 [%0];\n" ::"l"(kt + x));
+        asm volatile("prefetch.global.L2 [%0];\n" ::"l"(vt + x));
+      }
+    }
 #pragma unroll 4
     for (int r = 0; r < Rp; ++r) {
       const int t = r / a.G;
@@ -849,14 +887,14 @@ __device__ __forceinline__ void kd_queries(const Kv4DecodeArgs& a, const KdBatch
 }
 
 // shared memory: barriers (keys full, empty, values full, empty, items full,
-// empty), items, warp sums, q rows of two items, the rings
+// empty, left), items, warp sums, q rows of two items, the rings
 template <int D, int RT>
 struct KdLayout {
-  static constexpr int item = (4 * kKdMaxStages + 4) * 8;
+  static constexpr int item = (4 * kKdMaxStages + 6) * 8;
   static constexpr int m = item + 2 * (int)sizeof(KdItem);
-  static constexpr int l = m + kKdWarps * RT * 4;
-  static constexpr int acc = (l + kKdWarps * RT * 4 + 15) / 16 * 16;
-  static constexpr int q = acc + kKdWarps * RT * D * 4;
+  static constexpr int l = m + 2 * kKdWarps * RT * 4;
+  static constexpr int acc = (l + 2 * kKdWarps * RT * 4 + 15) / 16 * 16;
+  static constexpr int q = acc + 2 * kKdWarps * RT * D * 4;
   static __host__ __device__ int ring(int rows) { return q + 2 * ((rows + RT - 1) / RT * RT) * (D + 16) * 4; }
 };
 
@@ -867,6 +905,7 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
   using Lt = KdLayout<D, RT>;
   constexpr int CPL = D / 32, W = kKdWarps;
   __shared__ KdBatch batch;
+  __shared__ KdDone s_done[2];
   extern __shared__ __align__(128) uint8_t kd_sm[];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int R = a.T * a.G, Rp = (R + RT - 1) / RT * RT;
@@ -878,7 +917,7 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
   keys.empty = keys.full + kKdMaxStages * 8;
   values.full = keys.empty + kKdMaxStages * 8;
   values.empty = values.full + kKdMaxStages * 8;
-  const unsigned item_full = values.empty + kKdMaxStages * 8, item_empty = item_full + 16;
+  const unsigned item_full = values.empty + kKdMaxStages * 8, item_empty = item_full + 16, left_item = item_empty + 16;
   keys.slots = a.slotsK;
   values.slots = a.slotsV;
   keys.data = kd_sm + Lt::ring(R);
@@ -896,6 +935,7 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
       mbar_init(item_full + 8 * i, 1);
       mbar_init(item_empty + 8 * i, W);
     }
+    if (i == 0) mbar_init(left_item, W);
     fence_barrier_init();
   }
   kd_batch(a, batch);
@@ -921,9 +961,9 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
   }
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kKdRegsConsumer));
 
-  float* s_m = reinterpret_cast<float*>(kd_sm + Lt::m);        // [warps][RT]
+  float* s_m = reinterpret_cast<float*>(kd_sm + Lt::m);        // [2][warps][RT]
   float* s_l = reinterpret_cast<float*>(kd_sm + Lt::l);
-  float* s_acc = reinterpret_cast<float*>(kd_sm + Lt::acc);    // [warps][RT][D]
+  float* s_acc = reinterpret_cast<float*>(kd_sm + Lt::acc);    // [2][warps][RT][D]
   const int my_team = w / team, tile = w % team;
   const int rows = my_team < nteam ? min(RT, R - tile * RT) : 0;    // <= 0: a warp with no rows
   const int r0 = tile * RT < Rp ? tile * RT : 0;
@@ -935,20 +975,58 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
   int sk = my_team, sv = my_team, pk = 0, pv = 0;
   int k = 0;                                      // number of the item
 
-  for (int64_t u = u0; u < u1; ++k) {
+  // The warps do not wait for one another at the end of an item: each leaves
+  // its sums (there is room for two items) and goes on, and merges its share
+  // of an item when it gets to the end of the next one, by when the others
+  // have left theirs.  (With a barrier for each item the warps stood still
+  // until the slowest had finished its last block: an item cost as much as 20
+  // blocks.)  Nobody overwrites sums that are still to be merged: whoever
+  // leaves those of item k + 1 has seen everybody leave those of item k, each
+  // after its share of item k - 1.
+  const auto merge = [&](int buf) {
+    // four channels of a row to a thread, over the teams
+    const float* m = s_m + buf * W * RT;
+    const float* l = s_l + buf * W * RT;
+    const float* acc = s_acc + buf * W * RT * D;
+    const KdDone to = s_done[buf];
+    float* part = a.part + (2 * (int64_t)blockIdx.x + to.part) * R * (D + 4);
+    for (int e = tid; e < R * (D / 4); e += W * 32) {
+      const int r = e / (D / 4), c = e % (D / 4) * 4;
+      float M = -INFINITY, sum = 0.0f;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+      for (int x = r; x < nteam * team * RT; x += team * RT) M = fmaxf(M, m[x]);   // (the row in each team)
+#pragma unroll 4
+      for (int x = r; x < nteam * team * RT; x += team * RT) {
+        const float s = m[x] > -INFINITY ? ex2(m[x] - M) : l[x] == 0.0f ? 0.0f : 1.0f;
+        const float4 y = *reinterpret_cast<const float4*>(acc + x * D + c);
+        sum = fmaf(s, l[x], sum);
+        v.x = fmaf(s, y.x, v.x); v.y = fmaf(s, y.y, v.y); v.z = fmaf(s, y.z, v.z); v.w = fmaf(s, y.w, v.w);
+      }
+      if (to.done) {
+        if (r / a.G < to.nq) kd_store<D>(a, to.b, to.g, r, c, M, sum, v);
+      } else {
+        *reinterpret_cast<float4*>(part + r * (D + 4) + c) = v;
+        if (c == 0) { part[r * (D + 4) + D] = M; part[r * (D + 4) + D + 1] = sum; }
+      }
+    }
+  };
+
+  const int run = (int)(u1 - u0);
+  for (int u = 0; u < run; ++k) {
     const int buf = k & 1;
     if (!dead && !mbar_wait(item_full + 8 * buf, (k >> 1) & 1)) dead = true;
     dead = __any_sync(0xffffffffu, dead);
     if (dead) {
       // the way through the items does not hang on the producer
-      if (lane == 0) items[buf].seg = kd_seg(a, batch, u, u1);
+      if (lane == 0) items[buf].seg = kd_seg(a, batch, u0 + u, u0 + run);
       __syncwarp();
     }
     const KdItem& it = items[buf];
     const float* q = s_q + kd_q<D>(buf * Rp + r0, 0);
-    float* my_m = s_m + w * RT;
-    float* my_l = s_l + w * RT;
-    float* my_acc = s_acc + w * RT * D;
+    float* my_m = s_m + (buf * W + w) * RT;
+    float* my_l = s_l + (buf * W + w) * RT;
+    float* my_acc = s_acc + (buf * W + w) * RT * D;
     {
       KdFast<D, RT> f;
       kd_fast_init<D, RT>(f, it.inv + r0);
@@ -964,13 +1042,16 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
         const uint8_t* vt = values.data + sv * St::bytesV;
         if (rows <= 0) {
           between();
-        } else if (i < clear) {
-          kd_fast_block<D, RT, false>(f, kt, vt, q, 0, 0, between);
         } else {
-          const int ra = 2 * (lane % 4 % (RT / 2));
-          const int64_t p0 = (it.seg.blk0 + (i - base)) * kBlock;
-          kd_fast_block<D, RT, true>(f, kt, vt, q, (int)min(max(it.end[r0 + ra] - p0, (int64_t)0), (int64_t)kBlock),
-                                     (int)min(max(it.end[r0 + ra + 1] - p0, (int64_t)0), (int64_t)kBlock), between);
+          const bool masked = i >= clear;
+          int endA = kBlock, endB = kBlock;
+          if (masked) {
+            const int ra = 2 * (lane % 4 % (RT / 2));
+            const int64_t p0 = (it.seg.blk0 + (i - base)) * kBlock;
+            endA = (int)min(max(it.end[r0 + ra] - p0, (int64_t)0), (int64_t)kBlock);
+            endB = (int)min(max(it.end[r0 + ra + 1] - p0, (int64_t)0), (int64_t)kBlock);
+          }
+          kd_fast_block<D, RT>(f, kt, vt, q, masked, endA, endB, between);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(values.empty + 8 * sv);
@@ -979,6 +1060,10 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
         if ((sv += nteam) >= values.slots) { sv = my_team; pv ^= 1; }
       }
       base = to;
+      if (k > 0) {
+        if (!dead && !mbar_wait(left_item, (k - 1) & 1)) dead = true;
+        merge(buf ^ 1);
+      }
       kd_fast_store<D, RT>(f, my_m, my_l, my_acc);
     }
     // positions of the incomplete block, if it lies here
@@ -1010,30 +1095,22 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
         for (int c = 0; c < CPL; ++c) my_acc[r * D + lane * CPL + c] = st.acc[r][c];
       }
     }
-    bar_sync(1, W * 32);
-    // merge the teams, four channels of a row to a thread
-    float* part = a.part + (2 * (int64_t)blockIdx.x + (u == u0 ? 0 : 1)) * R * (D + 4);
-    for (int e = tid; e < R * (D / 4); e += W * 32) {
-      const int r = e / (D / 4), c = e % (D / 4) * 4;
-      float M = -INFINITY, l = 0.0f;
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int x = r; x < nteam * team * RT; x += team * RT) M = fmaxf(M, s_m[x]);   // (the row in each team)
-      for (int x = r; x < nteam * team * RT; x += team * RT) {
-        const float s = s_m[x] > -INFINITY ? ex2(s_m[x] - M) : s_l[x] == 0.0f ? 0.0f : 1.0f;
-        const float4 y = *reinterpret_cast<const float4*>(s_acc + x * D + c);
-        l = fmaf(s, s_l[x], l);
-        v.x = fmaf(s, y.x, v.x); v.y = fmaf(s, y.y, v.y); v.z = fmaf(s, y.z, v.z); v.w = fmaf(s, y.w, v.w);
-      }
-      if (it.seg.done) {
-        if (r / a.G < it.seg.nq) kd_store<D>(a, it.seg.b, it.seg.g, r, c, M, l, v);
-      } else {
-        *reinterpret_cast<float4*>(part + r * (D + 4) + c) = v;
-        if (c == 0) { part[r * (D + 4) + D] = M; part[r * (D + 4) + D + 1] = l; }
-      }
+    if (tid == 0) {
+      KdDone& d = s_done[buf];
+      d.b = it.seg.b; d.g = it.seg.g; d.nq = it.seg.nq;
+      d.done = it.seg.done;
+      d.part = u == 0 ? 0 : 1;
     }
-    u += it.seg.step;
-    bar_sync(1, W * 32);
-    if (lane == 0) mbar_arrive(item_empty + 8 * buf);
+    u += (int)it.seg.step;
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(item_empty + 8 * buf);
+      mbar_arrive(left_item);
+    }
+  }
+  if (k > 0) {
+    if (!dead && !mbar_wait(left_item, (k - 1) & 1)) dead = true;
+    merge((k - 1) & 1);
   }
   if (dead && lane == 0) atomicOr(a.status, 4u);
 }
@@ -1112,7 +1189,7 @@ size_t kd_workspace(const csa_shape* s, int T) {
   return 256 + (kd_whole(s) ? 0 : (size_t)2 * kd_ctas(s) * R * (s->d + 4) * 4);
 }
 
-constexpr int kKdSharedBytes = 232448 - (int)sizeof(KdBatch) - 64;
+constexpr int kKdSharedBytes = 232448 - (int)sizeof(KdBatch) - 128;
 template <int D, int RT, typename E>
 cudaError_t launch_kv4_decode_t(Kv4DecodeArgs a, int ncta, cudaStream_t st) {
   const int rest = KdLayout<D, RT>::ring(a.T * a.G);
