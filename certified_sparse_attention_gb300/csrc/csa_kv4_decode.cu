@@ -61,7 +61,8 @@ struct Kv4DecodeArgs {
   int64_t n_max, nblk_max;
   int B, T, Hq, Hkv, G;
   int whole;            // items are not cut: one unit each
-  int slotsK, slotsV;   // slots of the two rings: multiples of the number of teams
+  int depth;            // ring slots of a team
+  int defer;            // room for two items' sums: merged an item later
   float rs;             // log2(e) / sqrt(d): scores in units of log 2
 };
 
@@ -71,13 +72,13 @@ constexpr int kKdThreads = (kKdWarps + 4) * 32;
 // registers: 512 threads start with 128 each; the producers give theirs up
 constexpr int kKdRegsConsumer = 152, kKdRegsProducer = 56;
 static_assert(3 * kKdRegsConsumer + kKdRegsProducer <= 4 * 128, "more registers than the launch has");
-constexpr int kKdMaxStages = 24;  // slots of a ring
+constexpr int kKdMaxSlots = 48;   // slots of a CTA's ring
 // warps of a team, for 1 .. 8 tiles (above 6 tiles: one team, four warps left
 // over)
 __host__ __device__ constexpr int kd_team(int ntile) { return ntile <= 4 ? ntile : ntile <= 6 ? 6 : 8; }
 
-// One block in shared memory: the keys' part (codes, bounds) in one ring, the
-// values' (codes, token scales) in another.  The bounds lie in eight pieces 16
+// A block in shared memory, in two parts: keys (codes, bounds) and values
+// (codes, token scales).  The bounds lie in eight pieces 16
 // bytes apart, so that the four channel ranges of a warp's lanes start in
 // different banks (in one piece they would start in the same ones).
 template <int D>
@@ -88,7 +89,14 @@ struct KdStage {
   static constexpr int bytesK = B + 8 * PITCH;
   static constexpr int S = kBlock * D / 2;              // values: codes, then the token scales
   static constexpr int bytesV = S + kBlock * 8;
-  static constexpr int txK = kBlock * D / 2 + 8 * D, txV = kBlock * D / 2 + kBlock * 8;
+  // a team's ring of `depth` slots, and slot s in it: with an even depth a slot
+  // holds always keys or always values
+  static __host__ __device__ constexpr int ring(int depth) {
+    return depth % 2 ? depth * (bytesK > bytesV ? bytesK : bytesV) : depth / 2 * (bytesK + bytesV);
+  }
+  static __host__ __device__ constexpr int slot(int depth, int s) {
+    return depth % 2 ? s * (bytesK > bytesV ? bytesK : bytesV) : s / 2 * (bytesK + bytesV) + s % 2 * bytesK;
+  }
 };
 
 // What the kernels know of the batch.  The unit of work is a block of an item
@@ -339,14 +347,15 @@ __device__ __forceinline__ void kd_step(KdState<D, RT>& st, const E* K, const E*
 
 // ------------------------------------------------------- moving the blocks
 
-// A ring of slots with full and empty barriers.  Block i sits in slot i %
-// slots and is taken by team i % teams; slots is a multiple of teams, so a
-// slot serves one team, which has seen its last phase when it waits for the
-// next.
+// The ring: `depth` slots for each team, with full and empty barriers.  Block
+// i is taken by team i % nteam, whose parts (keys, values, keys, ...) go
+// through its own slots in turn: a team has seen a slot's last phase when it
+// waits for the next.  With three slots the copies of a part have the time of
+// a whole block to arrive (with two, half a block: not enough at 12 warps).
 struct KdRing {
   uint8_t* data;
   unsigned full, empty;
-  int slots;
+  int nteam, depth;
 };
 
 // A producer warp: sends for the keys' or the values' parts of the CTA's
@@ -360,7 +369,6 @@ __device__ __forceinline__ void kd_produce(const Kv4DecodeArgs& a, const KdBatch
   using St = KdStage<D>;
   constexpr int codes = kBlock * D / 2;
   const int lane = threadIdx.x & 31;
-  const unsigned size = keys ? St::bytesK : St::bytesV;
   const unsigned side = keys ? 8 * D : kBlock * 8;        // bytes of the bounds, of the scales
   const uint8_t* src = keys ? a.c.K4 : a.c.V4;
   const uint8_t* side_src = reinterpret_cast<const uint8_t*>(keys ? a.c.bounds : a.c.vscale) + lane * 16;
@@ -369,18 +377,19 @@ __device__ __forceinline__ void kd_produce(const Kv4DecodeArgs& a, const KdBatch
   const unsigned to1 = codes + (lane * 16 + 512) / St::PIECE * St::PITCH + lane * 16 % St::PIECE;
   const bool two = side > 512;
   const unsigned data = smem_u32(ring.data);
-  int i = 0, slot = 0, phase = 0;
+  int blocks = 0, team = 0, s = keys ? 0 : 1, phase = 0;
   bool dead = false;
   for (int64_t u = u0; u < u1 && !dead;) {
-    const KdSeg s = kd_seg(a, batch, u, u1);
-    const int64_t at = s.bg * a.nblk_max + s.blk0;
+    const KdSeg sg = kd_seg(a, batch, u, u1);
+    const int64_t at = sg.bg * a.nblk_max + sg.blk0;
     const uint8_t* from = src + at * codes;
     const uint8_t* side_from = side_src + at * side;
-    for (int x = 0; x < s.nfast; ++x) {
+    for (int x = 0; x < sg.nfast; ++x) {
+      const int slot = team * ring.depth + s;
       dead = !mbar_wait(ring.empty + 8 * slot, phase ^ 1);    // (a new barrier's "phase -1" is complete)
       dead = __any_sync(0xffffffffu, dead);
       if (dead) break;
-      const unsigned to = data + slot * size, bar = ring.full + 8 * slot;
+      const unsigned to = data + team * St::ring(ring.depth) + St::slot(ring.depth, s), bar = ring.full + 8 * slot;
       if (lane == 0) {
         mbar_expect_tx(bar, codes);
         asm volatile(
@@ -393,14 +402,24 @@ __device__ __forceinline__ void kd_produce(const Kv4DecodeArgs& a, const KdBatch
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
       from += codes;
       side_from += side;
-      ++i;
-      if (++slot == ring.slots) { slot = 0; phase ^= 1; }
+      ++blocks;
+      if (++team == ring.nteam) {
+        team = 0;
+        s += 2;
+        if (s >= ring.depth) { s -= ring.depth; phase ^= 1; }
+      }
     }
-    u += s.step;
+    u += sg.step;
   }
-  // all copies land before the CTA can end
-  for (int k = max(0, i - ring.slots); k < i; ++k)
-    if (!mbar_wait(ring.full + 8 * (k % ring.slots), (k / ring.slots) & 1)) dead = true;
+  // all copies land before the CTA can end: of each team (a lane each) the
+  // last parts, whose slots are not used again
+  if (lane < ring.nteam) {
+    const int parts = 2 * ((blocks - lane + ring.nteam - 1) / ring.nteam);
+    for (int n = max(0, parts - ring.depth); n < parts; ++n)
+      if ((n & 1) == (keys ? 0 : 1) && !mbar_wait(ring.full + 8 * (lane * ring.depth + n % ring.depth), n / ring.depth & 1))
+        dead = true;
+  }
+  dead = __any_sync(0xffffffffu, dead);
   if (dead && lane == 0) atomicOr(a.status, 4u);
 }
 
@@ -886,16 +905,17 @@ __device__ __forceinline__ void kd_queries(const Kv4DecodeArgs& a, const KdBatch
   if (dead && lane == 0) atomicOr(a.status, 4u);
 }
 
-// shared memory: barriers (keys full, empty, values full, empty, items full,
-// empty, left), items, warp sums, q rows of two items, the rings
+// shared memory: barriers (ring full, empty, items full, empty, left, merged),
+// items, warp sums, q rows of two items, the ring
 template <int D, int RT>
 struct KdLayout {
-  static constexpr int item = (4 * kKdMaxStages + 6) * 8;
-  static constexpr int m = item + 2 * (int)sizeof(KdItem);
-  static constexpr int l = m + 2 * kKdWarps * RT * 4;
-  static constexpr int acc = (l + 2 * kKdWarps * RT * 4 + 15) / 16 * 16;
-  static constexpr int q = acc + 2 * kKdWarps * RT * D * 4;
-  static __host__ __device__ int ring(int rows) { return q + 2 * ((rows + RT - 1) / RT * RT) * (D + 16) * 4; }
+  static constexpr int item = (2 * kKdMaxSlots + 6) * 8;
+  static constexpr int sums = item + 2 * (int)sizeof(KdItem);
+  static constexpr int sum = kKdWarps * RT * (D + 2) * 4;      // acc[RT][D] of the warps, m[RT], l[RT]
+  static __host__ __device__ int q(int defer) { return sums + (defer ? 2 : 1) * sum; }
+  static __host__ __device__ int ring(int rows, int defer) {
+    return q(defer) + 2 * ((rows + RT - 1) / RT * RT) * (D + 16) * 4;
+  }
 };
 
 template <int D, int RT, typename E>
@@ -912,30 +932,29 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
   // teams: warps that share a block, one tile of rows each
   const int ntile = Rp / RT;
   const int team = kd_team(ntile), nteam = W / team;
-  KdRing keys, values;
-  keys.full = smem_u32(kd_sm);
-  keys.empty = keys.full + kKdMaxStages * 8;
-  values.full = keys.empty + kKdMaxStages * 8;
-  values.empty = values.full + kKdMaxStages * 8;
-  const unsigned item_full = values.empty + kKdMaxStages * 8, item_empty = item_full + 16, left_item = item_empty + 16;
-  keys.slots = a.slotsK;
-  values.slots = a.slotsV;
-  keys.data = kd_sm + Lt::ring(R);
-  values.data = keys.data + a.slotsK * St::bytesK;
+  KdRing ring;
+  ring.full = smem_u32(kd_sm);
+  ring.empty = ring.full + kKdMaxSlots * 8;
+  ring.data = kd_sm + Lt::ring(R, a.defer);
+  ring.nteam = nteam;
+  ring.depth = a.depth;
+  const unsigned item_full = ring.empty + kKdMaxSlots * 8, item_empty = item_full + 16;
+  const unsigned left_item = item_empty + 16, merged = left_item + 8;
   KdItem* items = reinterpret_cast<KdItem*>(kd_sm + Lt::item);
-  float* s_q = reinterpret_cast<float*>(kd_sm + Lt::q);        // two of [rows, padded] (kd_q)
-  if (tid >= 32 && tid < 32 + kKdMaxStages) {
+  float* s_q = reinterpret_cast<float*>(kd_sm + Lt::q(a.defer));        // two of [rows, padded] (kd_q)
+  if (tid >= 32 && tid < 32 + kKdMaxSlots) {
     // (full: one arrival with the codes' bytes, one of each lane of the producer)
     const int i = tid - 32;
-    mbar_init(keys.full + 8 * i, 33);
-    mbar_init(keys.empty + 8 * i, team);
-    mbar_init(values.full + 8 * i, 33);
-    mbar_init(values.empty + 8 * i, team);
+    mbar_init(ring.full + 8 * i, 33);
+    mbar_init(ring.empty + 8 * i, team);
     if (i < 2) {
       mbar_init(item_full + 8 * i, 1);
       mbar_init(item_empty + 8 * i, W);
     }
-    if (i == 0) mbar_init(left_item, W);
+    if (i == 0) {
+      mbar_init(left_item, W);
+      mbar_init(merged, W);
+    }
     fence_barrier_init();
   }
   kd_batch(a, batch);
@@ -944,8 +963,7 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
 
   if (w >= W) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kKdRegsProducer));
-    if (w == W) kd_produce<D>(a, batch, u0, u1, keys, true);
-    else if (w == W + 1) kd_produce<D>(a, batch, u0, u1, values, false);
+    if (w < W + 2) kd_produce<D>(a, batch, u0, u1, ring, w == W);
     else if (w == W + 2) kd_queries<D, RT, E>(a, batch, u0, u1, items, s_q, item_full, item_empty);
     else if (blockIdx.x == 0) {
       bool bad = false;
@@ -961,9 +979,8 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
   }
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kKdRegsConsumer));
 
-  float* s_m = reinterpret_cast<float*>(kd_sm + Lt::m);        // [2][warps][RT]
-  float* s_l = reinterpret_cast<float*>(kd_sm + Lt::l);
-  float* s_acc = reinterpret_cast<float*>(kd_sm + Lt::acc);    // [2][warps][RT][D]
+  // the warps' sums of an item: acc [W][RT][D], then m and l [W][RT]
+  const auto sums = [&](int buf) { return reinterpret_cast<float*>(kd_sm + Lt::sums + (a.defer ? buf : 0) * Lt::sum); };
   const int my_team = w / team, tile = w % team;
   const int rows = my_team < nteam ? min(RT, R - tile * RT) : 0;    // <= 0: a warp with no rows
   const int r0 = tile * RT < Rp ? tile * RT : 0;
@@ -971,23 +988,23 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
   // on without waiting.)
   bool dead = false;
   int base = 0;                                   // number of the item's first block
-  int i = my_team;                                // the team's next block, its slots and their parities
-  int sk = my_team, sv = my_team, pk = 0, pv = 0;
+  int i = my_team;                                // the team's next block
+  int part = 0, phase = 0;                        // the slot of its next part, and its parity
   int k = 0;                                      // number of the item
 
-  // The warps do not wait for one another at the end of an item: each leaves
-  // its sums (there is room for two items) and goes on, and merges its share
-  // of an item when it gets to the end of the next one, by when the others
-  // have left theirs.  (With a barrier for each item the warps stood still
-  // until the slowest had finished its last block: an item cost as much as 20
+  // The end of an item: each warp leaves its sums, and when all have, merges a
+  // share of them.  With room for two items' sums (defer) a warp does not wait
+  // for the others: it goes on, and merges its share when it gets to the end
+  // of the next item, by when the others have left theirs.  (Waiting at each
+  // item costs RT = 8, whose items are short work for 12 warps, as much as 20
   // blocks.)  Nobody overwrites sums that are still to be merged: whoever
   // leaves those of item k + 1 has seen everybody leave those of item k, each
-  // after its share of item k - 1.
+  // after its share of item k - 1; without defer, everybody merge item k.
   const auto merge = [&](int buf) {
     // four channels of a row to a thread, over the teams
-    const float* m = s_m + buf * W * RT;
-    const float* l = s_l + buf * W * RT;
-    const float* acc = s_acc + buf * W * RT * D;
+    const float* acc = sums(buf);
+    const float* m = acc + W * RT * D;
+    const float* l = m + W * RT;
     const KdDone to = s_done[buf];
     float* part = a.part + (2 * (int64_t)blockIdx.x + to.part) * R * (D + 4);
     for (int e = tid; e < R * (D / 4); e += W * 32) {
@@ -1024,22 +1041,25 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
     }
     const KdItem& it = items[buf];
     const float* q = s_q + kd_q<D>(buf * Rp + r0, 0);
-    float* my_m = s_m + (buf * W + w) * RT;
-    float* my_l = s_l + (buf * W + w) * RT;
-    float* my_acc = s_acc + (buf * W + w) * RT * D;
+    float* my_acc = sums(buf) + w * RT * D;
+    float* my_m = sums(buf) + W * RT * D + w * RT;
+    float* my_l = my_m + W * RT;
     {
       KdFast<D, RT> f;
       kd_fast_init<D, RT>(f, it.inv + r0);
       const int to = base + it.seg.nfast, clear = base + it.seg.clear;
       while (my_team < nteam && i < to) {
-        if (!dead && !mbar_wait(keys.full + 8 * sk, pk)) dead = true;
+        const int sk = my_team * ring.depth + part;
+        const uint8_t* kt = ring.data + my_team * St::ring(ring.depth) + St::slot(ring.depth, part);
+        if (!dead && !mbar_wait(ring.full + 8 * sk, phase)) dead = true;
+        if (++part == ring.depth) { part = 0; phase ^= 1; }
+        const int sv = my_team * ring.depth + part;
         const auto between = [&]() {
           __syncwarp();
-          if (lane == 0) mbar_arrive(keys.empty + 8 * sk);
-          if (!dead && !mbar_wait(values.full + 8 * sv, pv)) dead = true;
+          if (lane == 0) mbar_arrive(ring.empty + 8 * sk);
+          if (!dead && !mbar_wait(ring.full + 8 * sv, phase)) dead = true;
         };
-        const uint8_t* kt = keys.data + sk * St::bytesK;
-        const uint8_t* vt = values.data + sv * St::bytesV;
+        const uint8_t* vt = ring.data + my_team * St::ring(ring.depth) + St::slot(ring.depth, part);
         if (rows <= 0) {
           between();
         } else {
@@ -1054,15 +1074,14 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
           kd_fast_block<D, RT>(f, kt, vt, q, masked, endA, endB, between);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(values.empty + 8 * sv);
+        if (lane == 0) mbar_arrive(ring.empty + 8 * sv);
+        if (++part == ring.depth) { part = 0; phase ^= 1; }
         i += nteam;
-        if ((sk += nteam) >= keys.slots) { sk = my_team; pk ^= 1; }
-        if ((sv += nteam) >= values.slots) { sv = my_team; pv ^= 1; }
       }
       base = to;
       if (k > 0) {
-        if (!dead && !mbar_wait(left_item, (k - 1) & 1)) dead = true;
-        merge(buf ^ 1);
+        if (!dead && !mbar_wait(a.defer ? left_item : merged, (k - 1) & 1)) dead = true;
+        if (a.defer) merge(buf ^ 1);
       }
       kd_fast_store<D, RT>(f, my_m, my_l, my_acc);
     }
@@ -1107,8 +1126,14 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
       mbar_arrive(item_empty + 8 * buf);
       mbar_arrive(left_item);
     }
+    if (!a.defer) {
+      if (!dead && !mbar_wait(left_item, k & 1)) dead = true;
+      merge(buf);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(merged);
+    }
   }
-  if (k > 0) {
+  if (k > 0 && a.defer) {
     if (!dead && !mbar_wait(left_item, (k - 1) & 1)) dead = true;
     merge((k - 1) & 1);
   }
@@ -1192,22 +1217,17 @@ size_t kd_workspace(const csa_shape* s, int T) {
 constexpr int kKdSharedBytes = 232448 - (int)sizeof(KdBatch) - 128;
 template <int D, int RT, typename E>
 cudaError_t launch_kv4_decode_t(Kv4DecodeArgs a, int ncta, cudaStream_t st) {
-  const int rest = KdLayout<D, RT>::ring(a.T * a.G);
-  // one slot per team in each ring (an SM's shared memory holds that for every
-  // RT and d), then more while there is room: keys first, whose copies have
-  // less time (the values' come while the warp is at the keys)
-  constexpr int K = KdStage<D>::bytesK, V = KdStage<D>::bytesV;
-  const int ntile = (a.T * a.G + RT - 1) / RT;
-  const int nteam = kKdWarps / kd_team(ntile);
-  int nk = 1, nv = 1;
-  for (bool more = true; more;) {
-    more = false;
-    if ((nk + 1) * nteam <= kKdMaxStages && nteam * ((nk + 1) * K + nv * V) <= kKdSharedBytes - rest) { ++nk; more = true; }
-    if ((nv + 1) * nteam <= kKdMaxStages && nteam * (nk * K + (nv + 1) * V) <= kKdSharedBytes - rest) { ++nv; more = true; }
-  }
-  a.slotsK = nk * nteam;
-  a.slotsV = nv * nteam;
-  const int smem = rest + a.slotsK * K + a.slotsV * V;
+  // Two slots for a team at least (there is room for that for every RT and d),
+  // three or more if possible, then room for two items' sums, then more slots.
+  using Lt = KdLayout<D, RT>;
+  const int ntile = (a.T * a.G + RT - 1) / RT, nteam = kKdWarps / kd_team(ntile);
+  const auto fits = [&](int depth, int defer) {
+    return depth * nteam <= kKdMaxSlots && Lt::ring(a.T * a.G, defer) + nteam * KdStage<D>::ring(depth) <= kKdSharedBytes;
+  };
+  a.defer = fits(3, 1) || (!fits(3, 0) && fits(2, 1));
+  a.depth = 2;
+  while (fits(a.depth + 1, a.defer)) ++a.depth;
+  const int smem = Lt::ring(a.T * a.G, a.defer) + nteam * KdStage<D>::ring(a.depth);
   const cudaError_t e =
       cudaFuncSetAttribute(kv4_decode_kernel<D, RT, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
