@@ -61,8 +61,7 @@ struct Kv4DecodeArgs {
   int64_t n_max, nblk_max;
   int B, T, Hq, Hkv, G;
   int whole;            // items are not cut: one unit each
-  int depth;            // ring slots of a team
-  int defer;            // room for two items' sums: merged an item later
+  int slotsK, slotsV;   // slots of the two rings: multiples of the number of teams
   float rs;             // log2(e) / sqrt(d): scores in units of log 2
 };
 
@@ -72,13 +71,13 @@ constexpr int kKdThreads = (kKdWarps + 4) * 32;
 // registers: 512 threads start with 128 each; the producers give theirs up
 constexpr int kKdRegsConsumer = 152, kKdRegsProducer = 56;
 static_assert(3 * kKdRegsConsumer + kKdRegsProducer <= 4 * 128, "more registers than the launch has");
-constexpr int kKdMaxSlots = 48;   // slots of a CTA's ring
+constexpr int kKdMaxStages = 24;  // slots of a ring
 // warps of a team, for 1 .. 8 tiles (above 6 tiles: one team, four warps left
 // over)
 __host__ __device__ constexpr int kd_team(int ntile) { return ntile <= 4 ? ntile : ntile <= 6 ? 6 : 8; }
 
-// A block in shared memory, in two parts: keys (codes, bounds) and values
-// (codes, token scales).  The bounds lie in eight pieces 16
+// One block in shared memory: the keys' part (codes, bounds) in one ring, the
+// values' (codes, token scales) in another.  The bounds lie in eight pieces 16
 // bytes apart, so that the four channel ranges of a warp's lanes start in
 // different banks (in one piece they would start in the same ones).
 template <int D>
@@ -89,14 +88,7 @@ struct KdStage {
   static constexpr int bytesK = B + 8 * PITCH;
   static constexpr int S = kBlock * D / 2;              // values: codes, then the token scales
   static constexpr int bytesV = S + kBlock * 8;
-  // a team's ring of `depth` slots, and slot s in it: with an even depth a slot
-  // holds always keys or always values
-  static __host__ __device__ constexpr int ring(int depth) {
-    return depth % 2 ? depth * (bytesK > bytesV ? bytesK : bytesV) : depth / 2 * (bytesK + bytesV);
-  }
-  static __host__ __device__ constexpr int slot(int depth, int s) {
-    return depth % 2 ? s * (bytesK > bytesV ? bytesK : bytesV) : s / 2 * (bytesK + bytesV) + s % 2 * bytesK;
-  }
+  static constexpr int txK = kBlock * D / 2 + 8 * D, txV = kBlock * D / 2 + kBlock * 8;
 };
 
 // What the kernels know of the batch.  The unit of work is a block of an item
@@ -106,9 +98,9 @@ struct KdStage {
 struct KdBatch {
   int64_t pref[kMaxB + 1];    // units of the sequences before b (pref[B]: all)
   int64_t len[kMaxB];
-  uint8_t nq[kMaxB];
+  int nq[kMaxB];
 };
-constexpr int kKdLead = 4;
+constexpr int kKdLead = 12;
 constexpr int kKdMaxCtas = 256;   // CTAs of a call (one per SM)
 
 // blocks of an item, the incomplete one counted
@@ -129,7 +121,7 @@ __device__ __forceinline__ void kd_batch(const Kv4DecodeArgs& a, KdBatch& s) {
       if (b < a.B) {
         const int64_t n = min(max(a.len[b], (int64_t)0), a.n_max);
         s.len[b] = n;
-        s.nq[b] = (uint8_t)(a.n_q ? min(max(a.n_q[b], (int64_t)0), (int64_t)a.T) : a.T);
+        s.nq[b] = a.n_q ? (int)min(max(a.n_q[b], (int64_t)0), (int64_t)a.T) : a.T;
         u[i] = kd_units(a, n) * a.Hkv;
       }
       sum += u[i];
@@ -320,22 +312,11 @@ __device__ __forceinline__ void kd_step(KdState<D, RT>& st, const E* K, const E*
       const float4 v = *reinterpret_cast<const float4*>(s_p + e * RT + r);
       p[r] = v.x; p[r + 1] = v.y; p[r + 2] = v.z; p[r + 3] = v.w;
     }
-    if (cut) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
       // an unseen token's value may be anything: it is left out, not
       // multiplied by zero
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const bool out = p[r] < 0.0f;
-        st.l[r] += out ? 0.0f : p[r];
-#pragma unroll
-        for (int c = 0; c < CPL; ++c) {
-          const float sum = fmaf(p[r], vv[e][c], st.acc[r][c]);
-          st.acc[r][c] = out ? st.acc[r][c] : sum;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
+      if (!cut || !(p[r] < 0.0f)) {
         st.l[r] += p[r];
 #pragma unroll
         for (int c = 0; c < CPL; ++c) st.acc[r][c] = fmaf(p[r], vv[e][c], st.acc[r][c]);
@@ -347,15 +328,14 @@ __device__ __forceinline__ void kd_step(KdState<D, RT>& st, const E* K, const E*
 
 // ------------------------------------------------------- moving the blocks
 
-// The ring: `depth` slots for each team, with full and empty barriers.  Block
-// i is taken by team i % nteam, whose parts (keys, values, keys, ...) go
-// through its own slots in turn: a team has seen a slot's last phase when it
-// waits for the next.  With three slots the copies of a part have the time of
-// a whole block to arrive (with two, half a block: not enough at 12 warps).
+// A ring of slots with full and empty barriers.  Block i sits in slot i %
+// slots and is taken by team i % teams; slots is a multiple of teams, so a
+// slot serves one team, which has seen its last phase when it waits for the
+// next.
 struct KdRing {
   uint8_t* data;
   unsigned full, empty;
-  int nteam, depth;
+  int slots;
 };
 
 // A producer warp: sends for the keys' or the values' parts of the CTA's
@@ -369,6 +349,7 @@ __device__ __forceinline__ void kd_produce(const Kv4DecodeArgs& a, const KdBatch
   using St = KdStage<D>;
   constexpr int codes = kBlock * D / 2;
   const int lane = threadIdx.x & 31;
+  const unsigned size = keys ? St::bytesK : St::bytesV;
   const unsigned side = keys ? 8 * D : kBlock * 8;        // bytes of the bounds, of the scales
   const uint8_t* src = keys ? a.c.K4 : a.c.V4;
   const uint8_t* side_src = reinterpret_cast<const uint8_t*>(keys ? a.c.bounds : a.c.vscale) + lane * 16;
@@ -377,19 +358,18 @@ __device__ __forceinline__ void kd_produce(const Kv4DecodeArgs& a, const KdBatch
   const unsigned to1 = codes + (lane * 16 + 512) / St::PIECE * St::PITCH + lane * 16 % St::PIECE;
   const bool two = side > 512;
   const unsigned data = smem_u32(ring.data);
-  int blocks = 0, team = 0, s = keys ? 0 : 1, phase = 0;
+  int i = 0, slot = 0, phase = 0;
   bool dead = false;
   for (int64_t u = u0; u < u1 && !dead;) {
-    const KdSeg sg = kd_seg(a, batch, u, u1);
-    const int64_t at = sg.bg * a.nblk_max + sg.blk0;
+    const KdSeg s = kd_seg(a, batch, u, u1);
+    const int64_t at = s.bg * a.nblk_max + s.blk0;
     const uint8_t* from = src + at * codes;
     const uint8_t* side_from = side_src + at * side;
-    for (int x = 0; x < sg.nfast; ++x) {
-      const int slot = team * ring.depth + s;
+    for (int x = 0; x < s.nfast; ++x) {
       dead = !mbar_wait(ring.empty + 8 * slot, phase ^ 1);    // (a new barrier's "phase -1" is complete)
       dead = __any_sync(0xffffffffu, dead);
       if (dead) break;
-      const unsigned to = data + team * St::ring(ring.depth) + St::slot(ring.depth, s), bar = ring.full + 8 * slot;
+      const unsigned to = data + slot * size, bar = ring.full + 8 * slot;
       if (lane == 0) {
         mbar_expect_tx(bar, codes);
         asm volatile(
@@ -402,24 +382,14 @@ __device__ __forceinline__ void kd_produce(const Kv4DecodeArgs& a, const KdBatch
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
       from += codes;
       side_from += side;
-      ++blocks;
-      if (++team == ring.nteam) {
-        team = 0;
-        s += 2;
-        if (s >= ring.depth) { s -= ring.depth; phase ^= 1; }
-      }
+      ++i;
+      if (++slot == ring.slots) { slot = 0; phase ^= 1; }
     }
-    u += sg.step;
+    u += s.step;
   }
-  // all copies land before the CTA can end: of each team (a lane each) the
-  // last parts, whose slots are not used again
-  if (lane < ring.nteam) {
-    const int parts = 2 * ((blocks - lane + ring.nteam - 1) / ring.nteam);
-    for (int n = max(0, parts - ring.depth); n < parts; ++n)
-      if ((n & 1) == (keys ? 0 : 1) && !mbar_wait(ring.full + 8 * (lane * ring.depth + n % ring.depth), n / ring.depth & 1))
-        dead = true;
-  }
-  dead = __any_sync(0xffffffffu, dead);
+  // all copies land before the CTA can end
+  for (int k = max(0, i - ring.slots); k < i; ++k)
+    if (!mbar_wait(ring.full + 8 * (k % ring.slots), (k / ring.slots) & 1)) dead = true;
   if (dead && lane == 0) atomicOr(a.status, 4u);
 }
 
@@ -431,6 +401,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], unsigned a0, unsigned a1,
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// the same with d = 0 before
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0,
+                                              unsigned b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ unsigned transpose8(unsigned x) {
   unsigned y;
@@ -462,6 +440,7 @@ __device__ __forceinline__ unsigned half_pair_rz(float x, float y) {
 // is the lowest exponent bit, where the subnormal numbers go on as normal
 // ones of the same spacing)
 constexpr unsigned kNibA = 0x00780078u, kNibB = 0x07800780u;
+constexpr int kKdChains = 4;      // sums of values in turn
 constexpr float kKeyUnit = 2097152.0f, kValueUnit = 131072.0f;   // 2^21, 2^17
 
 // The state of a warp over the tensor-core blocks of an item.  Lane (gid =
@@ -498,15 +477,15 @@ __device__ __forceinline__ void kd_fast_init(KdFast<D, RT>& f, const float* s_in
 }
 
 // One block: its keys' part at st, its values' part at vt; between() is
-// called when the one has been read and before the other is.  masked: row ra
+// called when the one has been read and before the other is.  MASK: row ra
 // sees the block's tokens below endA only, row ra + 1 those below endB.  The
-// block goes through in two halves of 32 tokens by loops that stay loops:
-// unrolled, the code was more than the instruction caches could feed to warps
-// that are each at another place of it (at 8 rows the warps spent a third of
-// their time waiting for instructions).
-template <int D, int RT, typename Between>
+// channels go through a loop that stays a loop: unrolled, the code was more
+// than the instruction caches could feed to warps that are each at another
+// place of it (at 8 rows the warps spent a third of their time waiting for
+// instructions).
+template <int D, int RT, bool MASK, typename Between>
 __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* st, const uint8_t* vt, const float* s_q,
-                                              bool masked, int endA, int endB, Between between) {
+                                              int endA, int endB, Between between) {
   using St = KdStage<D>;
   constexpr int NC = D / 4;        // channels of a lane
   constexpr int NW = D / 32;       // code words of a lane in a key row
@@ -550,62 +529,108 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
   // part = the rest), and sum_c q_c m_c beside it, in float32.  (RT = 4: the
   // lanes gid and gid + 4 take half of the channels of that each.)  Matrix
   // instructions truncate their sums: they start from zero.
-  float t[4][4] = {};
+  float t[4][4];
+  if (RT == 8) {
+#pragma unroll
+    for (int y = 0; y < 4; ++y) t[y][0] = t[y][1] = t[y][2] = t[y][3] = 0.0f;
+  }
   float qm = 0.0f, qm1 = 0.0f;
   const unsigned cut = RT == 8 || gid >= 4 ? 0xffffe000u : 0u;
-#pragma unroll 1
-  for (int wp = 0; wp < NW / 2; ++wp) {
-    unsigned bq[HL][2][4];
+  if constexpr (RT == 4) {
+    float x[NC];
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const int c = wp * 16 + w * 8;
-      float x[8];
+    for (int i = 0; i < NC; i += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(sq + i), dl = *reinterpret_cast<const float4*>(sd + i);
+      x[i] = q.x * dl.x; x[i + 1] = q.y * dl.y; x[i + 2] = q.z * dl.z; x[i + 3] = q.w * dl.w;
+    }
+    if (__builtin_expect(f.xs != 1.0f, 0)) {
 #pragma unroll
-      for (int i = 0; i < 8; i += 4) {
-        const float4 q = *reinterpret_cast<const float4*>(sq + c + i), dl = *reinterpret_cast<const float4*>(sd + c + i);
-        x[i] = q.x * dl.x; x[i + 1] = q.y * dl.y; x[i + 2] = q.z * dl.z; x[i + 3] = q.w * dl.w;
-        if (RT == 8) {
-          const float4 mn = *reinterpret_cast<const float4*>(sm + c + i);
-          qm = fmaf(q.x, mn.x, qm); qm1 = fmaf(q.y, mn.y, qm1);
-          qm = fmaf(q.z, mn.z, qm); qm1 = fmaf(q.w, mn.w, qm1);
-        }
-      }
-      if (RT == 4) {
-        const int h = c + (gid >> 2) * 4;
-        const float4 q = *reinterpret_cast<const float4*>(sq + h), mn = *reinterpret_cast<const float4*>(sm + h);
-        qm = fmaf(q.x, mn.x, qm); qm1 = fmaf(q.y, mn.y, qm1);
-        qm = fmaf(q.z, mn.z, qm); qm1 = fmaf(q.w, mn.w, qm1);
-      }
-      if (f.xs != 1.0f) {
+      for (int i = 0; i < NC; ++i) x[i] *= f.xs;
+    }
+    unsigned bq[NW][4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= f.xs;
-      }
+    for (int w = 0; w < NW; ++w) {
+      const int h = 8 * w + (gid >> 2) * 4;
+      const float4 q = *reinterpret_cast<const float4*>(sq + h), mn = *reinterpret_cast<const float4*>(sm + h);
+      qm = fmaf(q.x, mn.x, qm); qm1 = fmaf(q.y, mn.y, qm1);
+      qm = fmaf(q.z, mn.z, qm); qm1 = fmaf(q.w, mn.w, qm1);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float u = x[e], v = x[e + 4];
-        if (RT == 8) bq[0][w][e] = half_pair_rz(u, v);
-        bq[HL - 1][w][e] = half_pair_rz(u - __uint_as_float(__float_as_uint(u) & cut), v - __uint_as_float(__float_as_uint(v) & cut));
+        const float u = x[8 * w + e], v = x[8 * w + e + 4];
+        bq[w][e] = half_pair_rz(u - __uint_as_float(__float_as_uint(u) & cut), v - __uint_as_float(__float_as_uint(v) & cut));
       }
     }
 #pragma unroll
-    for (int pr = 0; pr < 2; ++pr) {
-      uint2 k[4];                        // rows gid, gid + 8 of tile 2 pr, then of the next
+    for (int pr = 0; pr < 4; pr += 2) {
+      unsigned k[2 * 2][NW];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        k[j] = *reinterpret_cast<const uint2*>(st + (32 * pr + 8 * j + gid) * (D / 2) + tid * (D / 8) + wp * 8);
+      for (int j = 0; j < 2 * 2; ++j) {
+        const uint8_t* kr = st + (16 * pr + 8 * j + gid) * (D / 2) + tid * (D / 8);
+        if (D == 128) {
+          const uint4 u = *reinterpret_cast<const uint4*>(kr);
+          k[j][0] = u.x; k[j][1] = u.y; k[j][NW - 2] = u.z; k[j][NW - 1] = u.w;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(kr);
+          k[j][0] = u.x; k[j][1] = u.y;
+        }
+      }
 #pragma unroll
-      for (int w = 0; w < 2; ++w)
+      for (int w = 0; w < NW; ++w)
 #pragma unroll
         for (int z = 0; z < 2; ++z)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const unsigned ka = w ? k[2 * y].y : k[2 * y].x, kb = w ? k[2 * y + 1].y : k[2 * y + 1].x;
-            const unsigned a = z ? ka >> 5 : ka << 3, b = z ? kb >> 5 : kb << 3;
-#pragma unroll
-            for (int h = HL - 1; h >= 0; --h)
-              mma_f16(t[2 * pr + y], a & kNibA, b & kNibA, a & kNibB, b & kNibB, bq[h][w][2 * z], bq[h][w][2 * z + 1]);
+            const unsigned a = z ? k[2 * y][w] >> 5 : k[2 * y][w] << 3, b = z ? k[2 * y + 1][w] >> 5 : k[2 * y + 1][w] << 3;
+            if (w == 0 && z == 0) mma_f16_first(t[pr + y], a & kNibA, b & kNibA, a & kNibB, b & kNibB, bq[w][2 * z], bq[w][2 * z + 1]);
+            else mma_f16(t[pr + y], a & kNibA, b & kNibA, a & kNibB, b & kNibB, bq[w][2 * z], bq[w][2 * z + 1]);
           }
     }
+  } else
+#pragma unroll 1
+  for (int wp = 0; wp < NW / 2; ++wp) {
+    unsigned bq[HL][2][4];
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int c = wp * 16 + i;
+      const float4 q = *reinterpret_cast<const float4*>(sq + c), dl = *reinterpret_cast<const float4*>(sd + c);
+      const float4 mn = *reinterpret_cast<const float4*>(sm + c);
+      x[i] = q.x * dl.x; x[i + 1] = q.y * dl.y; x[i + 2] = q.z * dl.z; x[i + 3] = q.w * dl.w;
+      qm = fmaf(q.x, mn.x, qm); qm1 = fmaf(q.y, mn.y, qm1);
+      qm = fmaf(q.z, mn.z, qm); qm1 = fmaf(q.w, mn.w, qm1);
+    }
+    if (__builtin_expect(f.xs != 1.0f, 0)) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] *= f.xs;
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float u = x[8 * w + e], v = x[8 * w + e + 4];
+        bq[0][w][e] = half_pair_rz(u, v);
+        bq[HL - 1][w][e] = half_pair_rz(u - __uint_as_float(__float_as_uint(u) & cut), v - __uint_as_float(__float_as_uint(v) & cut));
+      }
+    uint2 k[8];                          // rows gid, gid + 8 of the tiles
+#pragma unroll
+    for (int j = 0; j < 8; ++j) k[j] = *reinterpret_cast<const uint2*>(st + (8 * j + gid) * (D / 2) + tid * (D / 8) + wp * 8);
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        unsigned op[4][4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const unsigned ka = w ? k[2 * y].y : k[2 * y].x, kb = w ? k[2 * y + 1].y : k[2 * y + 1].x;
+          const unsigned a = z ? ka >> 5 : ka << 3, b = z ? kb >> 5 : kb << 3;
+          op[y][0] = a & kNibA; op[y][1] = b & kNibA; op[y][2] = a & kNibB; op[y][3] = b & kNibB;
+        }
+#pragma unroll
+        for (int h = HL - 1; h >= 0; --h)
+#pragma unroll
+          for (int y = 0; y < 4; ++y)    // (four independent sums in turn: one has to wait 31 cycles for its last)
+            mma_f16(t[y], op[y][0], op[y][1], op[y][2], op[y][3], bq[h][w][2 * z], bq[h][w][2 * z + 1]);
+      }
   }
   between();
   qm = fmaf(qm1, 16.0f, qm) * f.qinv;    // (odd channels carry 1/16)
@@ -613,175 +638,173 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
   qm += __shfl_xor_sync(0xffffffffu, qm, 2);
   if (RT == 4) qm += __shfl_xor_sync(0xffffffffu, qm, 16);
   const float sA = __shfl_sync(0xffffffffu, qm, 4 * ra) - f.rA, sB = __shfl_sync(0xffffffffu, qm, 4 * ra + 4) - f.rB;
-  // The scores relative to rA, rB, of a half's two tiles.  RT = 4: the two
-  // parts are added; the lane has token 16 y + gid (+ 8 in the upper lanes) of
-  // its half, rows ra, ra + 1, in s[y][0], s[y][1]; RT = 8: tokens gid and gid
-  // + 8 in s[y][0..1], s[y][2..3].
+  // The scores relative to rA, rB.  RT = 4: the two parts are added; the lane
+  // has token 16 y + gid (+ 8 in the upper lanes), rows ra, ra + 1, in
+  // t[y][0], t[y][1]; RT = 8: tokens gid and gid + 8 in t[y][0..1], t[y][2..3].
   constexpr int TK = RT == 8 ? 2 : 1;    // tokens of a tile in a lane
-  float s[2][2 * TK], later[2][2 * TK];  // of the half at hand, and of the other
+  const auto token = [&](int y, int k) { return 16 * y + gid + (RT == 8 ? 8 * k : upper ? 8 : 0); };
+  float2 sc[4][TK];                      // token scales
+  float big = -INFINITY, wide = 0.0f;
 #pragma unroll
   for (int y = 0; y < 4; ++y) {
-    float v[4];
     if (RT == 4) {
       const float g0 = __shfl_xor_sync(0xffffffffu, upper ? t[y][0] : t[y][2], 2);
       const float g1 = __shfl_xor_sync(0xffffffffu, upper ? t[y][1] : t[y][3], 2);
-      v[0] = fmaf((upper ? t[y][2] : t[y][0]) + g0, f.csA, sA);
-      v[1] = fmaf((upper ? t[y][3] : t[y][1]) + g1, f.csB, sB);
+      t[y][0] = fmaf((upper ? t[y][2] : t[y][0]) + g0, f.csA, sA);
+      t[y][1] = fmaf((upper ? t[y][3] : t[y][1]) + g1, f.csB, sB);
     } else {
-      v[0] = fmaf(t[y][0], f.csA, sA); v[1] = fmaf(t[y][1], f.csB, sB);
-      v[2] = fmaf(t[y][2], f.csA, sA); v[3] = fmaf(t[y][3], f.csB, sB);
+      t[y][0] = fmaf(t[y][0], f.csA, sA); t[y][1] = fmaf(t[y][1], f.csB, sB);
+      t[y][2] = fmaf(t[y][2], f.csA, sA); t[y][3] = fmaf(t[y][3], f.csB, sB);
     }
 #pragma unroll
-    for (int e = 0; e < 2 * TK; ++e) (y < 2 ? s[y] : later[y - 2])[e] = v[e];
+    for (int k = 0; k < TK; ++k) sc[y][k] = *reinterpret_cast<const float2*>(vt + St::S + token(y, k) * 8);
   }
-
-#pragma unroll 1
-  for (int hf = 0; hf < 2; ++hf) {
-    const auto token = [&](int y, int k) { return 32 * hf + 16 * y + gid + (RT == 8 ? 8 * k : upper ? 8 : 0); };
-    float2 sc[2][TK];                    // token scales
-    float big = -INFINITY, wide = 0.0f;
+  if (MASK) {
+    // an unseen token's value may be anything
 #pragma unroll
-    for (int y = 0; y < 2; ++y)
+    for (int y = 0; y < 4; ++y)
 #pragma unroll
       for (int k = 0; k < TK; ++k) {
-        sc[y][k] = *reinterpret_cast<const float2*>(vt + St::S + token(y, k) * 8);
-        if (masked) {
-          if (token(y, k) >= endA) s[y][2 * k] = -INFINITY;
-          if (token(y, k) >= endB) s[y][2 * k + 1] = -INFINITY;
-        }
-        big = fmaxf(big, fmaxf(s[y][2 * k], s[y][2 * k + 1]));
-        if (!masked || token(y, k) < max(endA, endB)) wide = fmaxf(wide, sc[y][k].y);
+        if (token(y, k) >= endA) t[y][2 * k] = -INFINITY;
+        if (token(y, k) >= endB) t[y][2 * k + 1] = -INFINITY;
+        if (token(y, k) >= max(endA, endB)) sc[y][k] = make_float2(0.0f, 0.0f);
       }
-    // The reference moves only when a score exceeds it by more than 8 (weights
-    // up to 2^8), and the value scale only when Delta_t does not fit (Delta_t
-    // sv up to 2^6): both are rare after the first block.
-    if (__builtin_expect(__any_sync(0xffffffffu, f.newA || f.newB || big > 8.0f || wide > f.wide), 0)) {
-      float xA = -INFINITY, xB = -INFINITY, tA = 0.0f, tB = 0.0f;
+  }
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
+  for (int y = 0; y < 4; ++y)
 #pragma unroll
-        for (int k = 0; k < TK; ++k) {
-          const float t = sc[y][k].y < INFINITY ? sc[y][k].y : 0.0f;
-          xA = fmaxf(xA, s[y][2 * k]);
-          xB = fmaxf(xB, s[y][2 * k + 1]);
-          if (!masked || token(y, k) < endA) tA = fmaxf(tA, t);
-          if (!masked || token(y, k) < endB) tB = fmaxf(tB, t);
-        }
-#pragma unroll
-      for (int m = (RT == 4 ? 2 : 4); m < 32; m <<= 1) {
-        xA = fmaxf(xA, __shfl_xor_sync(0xffffffffu, xA, m));
-        xB = fmaxf(xB, __shfl_xor_sync(0xffffffffu, xB, m));
-        tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, m));
-        tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, m));
-      }
-      // the references move up by dA, dB (a row's first tokens: to their maximum)
-      const float dA = f.newA ? (xA > -INFINITY ? xA : 0.0f) : fmaxf(xA, 0.0f);
-      const float dB = f.newB ? (xB > -INFINITY ? xB : 0.0f) : fmaxf(xB, 0.0f);
-      const float eA = f.newA ? 1.0f : ex2(-dA), eB = f.newB ? 1.0f : ex2(-dB);
-      float upA = 1.0f, upB = 1.0f;
-      if (tA > 0.0f && (f.svA == 0.0f || tA * f.svA > 64.0f)) {
-        const float to = pow2i(min(max(5 - exponent(tA), -100), 100));   // Delta sv in [2^5, 2^6)
-        if (f.svA != 0.0f) upA = to / f.svA;
-        f.svA = to;
-      }
-      if (tB > 0.0f && (f.svB == 0.0f || tB * f.svB > 64.0f)) {
-        const float to = pow2i(min(max(5 - exponent(tB), -100), 100));
-        if (f.svB != 0.0f) upB = to / f.svB;
-        f.svB = to;
-      }
-      f.wide = f.svA == 0.0f || f.svB == 0.0f ? 0.0f : 64.0f / fmaxf(f.svA, f.svB);
-      f.lA *= eA; f.lB *= eB;
-      f.omA *= eA; f.omB *= eB;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        f.o[i][0] *= eA * upA; f.o[i][1] *= eB * upB;
-        f.o[i][2] *= eA * upA; f.o[i][3] *= eB * upB;
-      }
-      f.rA += dA; f.rB += dB;
-      f.newA = f.newA && !(xA > -INFINITY);
-      f.newB = f.newB && !(xB > -INFINITY);
-#pragma unroll
-      for (int y = 0; y < 2; ++y)
-#pragma unroll
-        for (int k = 0; k < TK; ++k) {
-          s[y][2 * k] -= dA; s[y][2 * k + 1] -= dB;
-          later[y][2 * k] -= dA; later[y][2 * k + 1] -= dB;
-        }
+    for (int k = 0; k < TK; ++k) {
+      big = fmaxf(big, fmaxf(t[y][2 * k], t[y][2 * k + 1]));
+      wide = fmaxf(wide, sc[y][k].y);
     }
-    // Weights and the second operand: column gid, token pairs.  The tokens
-    // gid + 8 of a tile enter as 15 - n with the opposite sign, and with m +
-    // 15 Delta for m: the sums of codes, all positive, would outgrow the
-    // differences that the output consists of (values around zero) and leave
-    // them their rounding errors.
-    float omA = 0.0f, omB = 0.0f;
-    unsigned bp[HL][2][2];
+  // The reference moves only when a score exceeds it by more than 8 (weights
+  // up to 2^8), and the value scale only when Delta_t does not fit (Delta_t sv
+  // up to 2^6): both are rare after the first block.
+  if (__builtin_expect(__any_sync(0xffffffffu, f.newA || f.newB || big > 8.0f || wide > f.wide), 0)) {
+    float xA = -INFINITY, xB = -INFINITY, tA = 0.0f, tB = 0.0f;
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      unsigned hi[TK], lo[TK];
+    for (int y = 0; y < 4; ++y)
 #pragma unroll
       for (int k = 0; k < TK; ++k) {
-        const float pA = ex2(s[y][2 * k]), pB = ex2(s[y][2 * k + 1]);
-        f.lA += pA; f.lB += pB;
-        const bool turned = RT == 8 ? k == 1 : upper;
-        const float dl = sc[y][k].y, m = fmaf(dl, turned ? 15.0f : 0.0f, sc[y][k].x);
-        float wA = pA * (dl * (turned ? -f.svA : f.svA)), wB = pB * (dl * (turned ? -f.svB : f.svB));
-        if (__builtin_expect(masked, 0)) {
-          // an unseen token's value may be anything: it is left out, not
-          // multiplied by zero
-          if (token(y, k) >= endA) wA = 0.0f; else omA = fmaf(pA, m, omA);
-          if (token(y, k) >= endB) wB = 0.0f; else omB = fmaf(pB, m, omB);
-        } else {
-          omA = fmaf(pA, m, omA);
-          omB = fmaf(pB, m, omB);
-        }
-        hi[k] = half_pair(wA, wB);
-        lo[k] = half_rest(wA, wB, hi[k]);
+        const float w = sc[y][k].y < INFINITY ? sc[y][k].y : 0.0f;
+        xA = fmaxf(xA, t[y][2 * k]);
+        xB = fmaxf(xB, t[y][2 * k + 1]);
+        if (!MASK || token(y, k) < endA) tA = fmaxf(tA, w);
+        if (!MASK || token(y, k) < endB) tB = fmaxf(tB, w);
       }
-      if (RT == 4) {
-        const unsigned got = __shfl_xor_sync(0xffffffffu, upper ? hi[0] : lo[0], 2);
-        bp[0][y][0] = transpose8(upper ? got : hi[0]);
-        bp[0][y][1] = transpose8(upper ? lo[0] : got);
+#pragma unroll
+    for (int m = (RT == 4 ? 2 : 4); m < 32; m <<= 1) {
+      xA = fmaxf(xA, __shfl_xor_sync(0xffffffffu, xA, m));
+      xB = fmaxf(xB, __shfl_xor_sync(0xffffffffu, xB, m));
+      tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, m));
+      tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, m));
+    }
+    // the references move up by dA, dB (a row's first tokens: to their maximum)
+    const float dA = f.newA ? (xA > -INFINITY ? xA : 0.0f) : fmaxf(xA, 0.0f);
+    const float dB = f.newB ? (xB > -INFINITY ? xB : 0.0f) : fmaxf(xB, 0.0f);
+    const float eA = f.newA ? 1.0f : ex2(-dA), eB = f.newB ? 1.0f : ex2(-dB);
+    float upA = 1.0f, upB = 1.0f;
+    if (tA > 0.0f && (f.svA == 0.0f || tA * f.svA > 64.0f)) {
+      const float to = pow2i(min(max(5 - exponent(tA), -100), 100));   // Delta sv in [2^5, 2^6)
+      if (f.svA != 0.0f) upA = __fdividef(to, f.svA);                  // (powers of two: exact)
+      f.svA = to;
+    }
+    if (tB > 0.0f && (f.svB == 0.0f || tB * f.svB > 64.0f)) {
+      const float to = pow2i(min(max(5 - exponent(tB), -100), 100));
+      if (f.svB != 0.0f) upB = __fdividef(to, f.svB);
+      f.svB = to;
+    }
+    f.wide = f.svA == 0.0f || f.svB == 0.0f ? 0.0f : __fdividef(64.0f, fmaxf(f.svA, f.svB));
+    f.lA *= eA; f.lB *= eB;
+    f.omA *= eA; f.omB *= eB;
+    upA *= eA; upB *= eB;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      f.o[i][0] *= upA; f.o[i][1] *= upB;
+      f.o[i][2] *= upA; f.o[i][3] *= upB;
+    }
+    f.rA += dA; f.rB += dB;
+    f.newA = f.newA && !(xA > -INFINITY);
+    f.newB = f.newB && !(xB > -INFINITY);
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+#pragma unroll
+      for (int k = 0; k < TK; ++k) { t[y][2 * k] -= dA; t[y][2 * k + 1] -= dB; }
+  }
+  // Weights and the second operand: column gid, token pairs.  The tokens gid +
+  // 8 of a tile enter as 15 - n with the opposite sign, and with m + 15 Delta
+  // for m: the sums of codes, all positive, would outgrow the differences that
+  // the output consists of (values around zero) and leave them their rounding
+  // errors.
+  float omA = 0.0f, omB = 0.0f;
+  unsigned bp[HL][4][2];
+#pragma unroll
+  for (int y = 0; y < 4; ++y) {
+    unsigned hi[TK], lo[TK];
+#pragma unroll
+    for (int k = 0; k < TK; ++k) {
+      const float pA = ex2(t[y][2 * k]), pB = ex2(t[y][2 * k + 1]);
+      f.lA += pA; f.lB += pB;
+      const bool turned = RT == 8 ? k == 1 : upper;
+      const float dl = sc[y][k].y, m = fmaf(dl, turned ? 15.0f : 0.0f, sc[y][k].x);
+      float wA = pA * (dl * (turned ? -f.svA : f.svA)), wB = pB * (dl * (turned ? -f.svB : f.svB));
+      if (MASK) {
+        // left out, not multiplied by zero
+        if (token(y, k) >= endA) wA = 0.0f; else omA = fmaf(pA, m, omA);
+        if (token(y, k) >= endB) wB = 0.0f; else omB = fmaf(pB, m, omB);
       } else {
-        bp[0][y][0] = transpose8(hi[0]);
-        bp[0][y][1] = transpose8(hi[TK - 1]);
-        bp[HL - 1][y][0] = transpose8(lo[0]);
-        bp[HL - 1][y][1] = transpose8(lo[TK - 1]);
+        omA = fmaf(pA, m, omA);
+        omB = fmaf(pB, m, omB);
       }
+      hi[k] = half_pair(wA, wB);
+      lo[k] = half_rest(wA, wB, hi[k]);
     }
-    // (the two halves of a tile's tokens cancel: RT = 4 has them in lane pairs)
     if (RT == 4) {
-      omA += __shfl_xor_sync(0xffffffffu, omA, 2);
-      omB += __shfl_xor_sync(0xffffffffu, omB, 2);
+      const unsigned got = __shfl_xor_sync(0xffffffffu, upper ? hi[0] : lo[0], 2);
+      bp[0][y][0] = transpose8(upper ? got : hi[0]);
+      bp[0][y][1] = transpose8(upper ? lo[0] : got);
+    } else {
+      bp[0][y][0] = transpose8(hi[0]);
+      bp[0][y][1] = transpose8(hi[TK - 1]);
+      bp[HL - 1][y][0] = transpose8(lo[0]);
+      bp[HL - 1][y][1] = transpose8(lo[TK - 1]);
     }
-    f.omA += omA;
-    f.omB += omB;
+  }
+  // (the two halves of a tile's tokens cancel: RT = 4 has them in lane pairs)
+  if (RT == 4) {
+    omA += __shfl_xor_sync(0xffffffffu, omA, 2);
+    omB += __shfl_xor_sync(0xffffffffu, omB, 2);
+  }
+  f.omA += omA;
+  f.omB += omB;
 #pragma unroll
-    for (int i = 0; i < D / 16; i += 2) {
-      unsigned v[4];          // channels gid, gid + 8 of tile i, then of the next
+  for (int i = 0; i < D / 16; i += kKdChains) {
+    uint2 v[2 * kKdChains];              // channels gid, gid + 8 of the tiles i, i + 1, ...
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[j] = *reinterpret_cast<const unsigned*>(vt + (16 * i + 8 * j + gid) * (kBlock / 2) + tid * 8 + hf * 4);
-      float t[2][4] = {};
+    for (int j = 0; j < 2 * kKdChains; ++j)
+      v[j] = *reinterpret_cast<const uint2*>(vt + (16 * i + 8 * j + gid) * (kBlock / 2) + tid * 8);
+    float u[kKdChains][4];
 #pragma unroll
-      for (int h = HL - 1; h >= 0; --h)  // (low parts first)
+    for (int y = 0; y < 4; ++y) {
+      unsigned op[kKdChains][4];
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+      for (int z = 0; z < kKdChains; ++z) {
+        const unsigned a = y < 2 ? v[2 * z].x : v[2 * z].y, b = y < 2 ? v[2 * z + 1].x : v[2 * z + 1].y;
+        op[z][0] = (y & 1 ? a >> 1 : a << 7) & kNibB; op[z][1] = (y & 1 ? b >> 1 : b << 7) & kNibB;
+        op[z][2] = ~(y & 1 ? a >> 5 : a << 3) & kNibB; op[z][3] = ~(y & 1 ? b >> 5 : b << 3) & kNibB;
+      }
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const unsigned a = v[2 * z], b = v[2 * z + 1];
-            const unsigned a0 = (y ? a >> 1 : a << 7) & kNibB, b0 = (y ? b >> 1 : b << 7) & kNibB;
-            const unsigned a1 = ~(y ? a >> 5 : a << 3) & kNibB, b1 = ~(y ? b >> 5 : b << 3) & kNibB;
-            mma_f16(t[z], a0, b0, a1, b1, bp[h][y][0], bp[h][y][1]);
-          }
+      for (int h = HL - 1; h >= 0; --h)
 #pragma unroll
-      for (int z = 0; z < 2; ++z)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f.o[i + z][e] += t[z][e];
+        for (int z = 0; z < kKdChains; ++z) {
+          if (y == 0 && h == HL - 1) mma_f16_first(u[z], op[z][0], op[z][1], op[z][2], op[z][3], bp[h][y][0], bp[h][y][1]);
+          else mma_f16(u[z], op[z][0], op[z][1], op[z][2], op[z][3], bp[h][y][0], bp[h][y][1]);
+        }
     }
 #pragma unroll
-    for (int y = 0; y < 2; ++y)
+    for (int z = 0; z < kKdChains; ++z)
 #pragma unroll
-      for (int e = 0; e < 2 * TK; ++e) s[y][e] = later[y][e];
+      for (int e = 0; e < 4; ++e) f.o[i + z][e] += u[z][e];
   }
 }
 
@@ -832,10 +855,6 @@ struct KdItem {
   int64_t end[CSA_KV4_MAX_ROWS];    // row r sees positions below end[r]
   float inv[CSA_KV4_MAX_ROWS];      // undoes the scale of row r (kd_q)
 };
-// where an item's merged sums go
-struct KdDone {
-  int b, g, nq, done, part;
-};
 
 template <int D, int RT, typename E>
 __device__ __forceinline__ void kd_queries(const Kv4DecodeArgs& a, const KdBatch& batch, int64_t u0, int64_t u1,
@@ -855,16 +874,6 @@ __device__ __forceinline__ void kd_queries(const Kv4DecodeArgs& a, const KdBatch
     if (lane == 0) it.seg = sg;
     const E* base = reinterpret_cast<const E*>(a.q) + sg.b * a.qs.b + (int64_t)sg.g * a.G * a.qs.h + lane * CPL;
     float* q = s_q + buf * kd_q<D>(Rp, 0);
-    // the rows of the incomplete block, if it lies here, on their way to L2
-    if (sg.blk1 > sg.n / kBlock) {
-      const int bytes = (int)(sg.n % kBlock) * D * (int)sizeof(E);
-      const char* kt = reinterpret_cast<const char*>(a.c.Kt) + sg.bg * kBlock * D * (int)sizeof(E);
-      const char* vt = reinterpret_cast<const char*>(a.c.Vt) + sg.bg * kBlock * D * (int)sizeof(E);
-      for (int x = lane * 128; x < bytes; x += 32 * 128) {
-        asm volatile("prefetch.global.L2 [%0];\n" ::"l"(kt + x));
-        asm volatile("prefetch.global.L2 [%0];\n" ::"l"(vt + x));
-      }
-    }
 #pragma unroll 4
     for (int r = 0; r < Rp; ++r) {
       const int t = r / a.G;
@@ -905,17 +914,16 @@ __device__ __forceinline__ void kd_queries(const Kv4DecodeArgs& a, const KdBatch
   if (dead && lane == 0) atomicOr(a.status, 4u);
 }
 
-// shared memory: barriers (ring full, empty, items full, empty, left, merged),
-// items, warp sums, q rows of two items, the ring
+// shared memory: barriers (keys full, empty, values full, empty, items full,
+// empty), items, warp sums, q rows of two items, the rings
 template <int D, int RT>
 struct KdLayout {
-  static constexpr int item = (2 * kKdMaxSlots + 6) * 8;
-  static constexpr int sums = item + 2 * (int)sizeof(KdItem);
-  static constexpr int sum = kKdWarps * RT * (D + 2) * 4;      // acc[RT][D] of the warps, m[RT], l[RT]
-  static __host__ __device__ int q(int defer) { return sums + (defer ? 2 : 1) * sum; }
-  static __host__ __device__ int ring(int rows, int defer) {
-    return q(defer) + 2 * ((rows + RT - 1) / RT * RT) * (D + 16) * 4;
-  }
+  static constexpr int item = (4 * kKdMaxStages + 4) * 8;
+  static constexpr int m = item + 2 * (int)sizeof(KdItem);
+  static constexpr int l = m + kKdWarps * RT * 4;
+  static constexpr int acc = (l + kKdWarps * RT * 4 + 15) / 16 * 16;
+  static constexpr int q = acc + kKdWarps * RT * D * 4;
+  static __host__ __device__ int ring(int rows) { return q + 2 * ((rows + RT - 1) / RT * RT) * (D + 16) * 4; }
 };
 
 template <int D, int RT, typename E>
@@ -925,35 +933,34 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
   using Lt = KdLayout<D, RT>;
   constexpr int CPL = D / 32, W = kKdWarps;
   __shared__ KdBatch batch;
-  __shared__ KdDone s_done[2];
   extern __shared__ __align__(128) uint8_t kd_sm[];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int R = a.T * a.G, Rp = (R + RT - 1) / RT * RT;
   // teams: warps that share a block, one tile of rows each
   const int ntile = Rp / RT;
   const int team = kd_team(ntile), nteam = W / team;
-  KdRing ring;
-  ring.full = smem_u32(kd_sm);
-  ring.empty = ring.full + kKdMaxSlots * 8;
-  ring.data = kd_sm + Lt::ring(R, a.defer);
-  ring.nteam = nteam;
-  ring.depth = a.depth;
-  const unsigned item_full = ring.empty + kKdMaxSlots * 8, item_empty = item_full + 16;
-  const unsigned left_item = item_empty + 16, merged = left_item + 8;
+  KdRing keys, values;
+  keys.full = smem_u32(kd_sm);
+  keys.empty = keys.full + kKdMaxStages * 8;
+  values.full = keys.empty + kKdMaxStages * 8;
+  values.empty = values.full + kKdMaxStages * 8;
+  const unsigned item_full = values.empty + kKdMaxStages * 8, item_empty = item_full + 16;
+  keys.slots = a.slotsK;
+  values.slots = a.slotsV;
+  keys.data = kd_sm + Lt::ring(R);
+  values.data = keys.data + a.slotsK * St::bytesK;
   KdItem* items = reinterpret_cast<KdItem*>(kd_sm + Lt::item);
-  float* s_q = reinterpret_cast<float*>(kd_sm + Lt::q(a.defer));        // two of [rows, padded] (kd_q)
-  if (tid >= 32 && tid < 32 + kKdMaxSlots) {
+  float* s_q = reinterpret_cast<float*>(kd_sm + Lt::q);        // two of [rows, padded] (kd_q)
+  if (tid >= 32 && tid < 32 + kKdMaxStages) {
     // (full: one arrival with the codes' bytes, one of each lane of the producer)
     const int i = tid - 32;
-    mbar_init(ring.full + 8 * i, 33);
-    mbar_init(ring.empty + 8 * i, team);
+    mbar_init(keys.full + 8 * i, 33);
+    mbar_init(keys.empty + 8 * i, team);
+    mbar_init(values.full + 8 * i, 33);
+    mbar_init(values.empty + 8 * i, team);
     if (i < 2) {
       mbar_init(item_full + 8 * i, 1);
       mbar_init(item_empty + 8 * i, W);
-    }
-    if (i == 0) {
-      mbar_init(left_item, W);
-      mbar_init(merged, W);
     }
     fence_barrier_init();
   }
@@ -963,7 +970,8 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
 
   if (w >= W) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kKdRegsProducer));
-    if (w < W + 2) kd_produce<D>(a, batch, u0, u1, ring, w == W);
+    if (w == W) kd_produce<D>(a, batch, u0, u1, keys, true);
+    else if (w == W + 1) kd_produce<D>(a, batch, u0, u1, values, false);
     else if (w == W + 2) kd_queries<D, RT, E>(a, batch, u0, u1, items, s_q, item_full, item_empty);
     else if (blockIdx.x == 0) {
       bool bad = false;
@@ -979,8 +987,9 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
   }
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kKdRegsConsumer));
 
-  // the warps' sums of an item: acc [W][RT][D], then m and l [W][RT]
-  const auto sums = [&](int buf) { return reinterpret_cast<float*>(kd_sm + Lt::sums + (a.defer ? buf : 0) * Lt::sum); };
+  float* s_m = reinterpret_cast<float*>(kd_sm + Lt::m);        // [warps][RT]
+  float* s_l = reinterpret_cast<float*>(kd_sm + Lt::l);
+  float* s_acc = reinterpret_cast<float*>(kd_sm + Lt::acc);    // [warps][RT][D]
   const int my_team = w / team, tile = w % team;
   const int rows = my_team < nteam ? min(RT, R - tile * RT) : 0;    // <= 0: a warp with no rows
   const int r0 = tile * RT < Rp ? tile * RT : 0;
@@ -988,101 +997,54 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
   // on without waiting.)
   bool dead = false;
   int base = 0;                                   // number of the item's first block
-  int i = my_team;                                // the team's next block
-  int part = 0, phase = 0;                        // the slot of its next part, and its parity
+  int i = my_team;                                // the team's next block, its slots and their parities
+  int sk = my_team, sv = my_team, pk = 0, pv = 0;
   int k = 0;                                      // number of the item
 
-  // The end of an item: each warp leaves its sums, and when all have, merges a
-  // share of them.  With room for two items' sums (defer) a warp does not wait
-  // for the others: it goes on, and merges its share when it gets to the end
-  // of the next item, by when the others have left theirs.  (Waiting at each
-  // item costs RT = 8, whose items are short work for 12 warps, as much as 20
-  // blocks.)  Nobody overwrites sums that are still to be merged: whoever
-  // leaves those of item k + 1 has seen everybody leave those of item k, each
-  // after its share of item k - 1; without defer, everybody merge item k.
-  const auto merge = [&](int buf) {
-    // four channels of a row to a thread, over the teams
-    const float* acc = sums(buf);
-    const float* m = acc + W * RT * D;
-    const float* l = m + W * RT;
-    const KdDone to = s_done[buf];
-    float* part = a.part + (2 * (int64_t)blockIdx.x + to.part) * R * (D + 4);
-    for (int e = tid; e < R * (D / 4); e += W * 32) {
-      const int r = e / (D / 4), c = e % (D / 4) * 4;
-      float M = -INFINITY, sum = 0.0f;
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-      for (int x = r; x < nteam * team * RT; x += team * RT) M = fmaxf(M, m[x]);   // (the row in each team)
-#pragma unroll 4
-      for (int x = r; x < nteam * team * RT; x += team * RT) {
-        const float s = m[x] > -INFINITY ? ex2(m[x] - M) : l[x] == 0.0f ? 0.0f : 1.0f;
-        const float4 y = *reinterpret_cast<const float4*>(acc + x * D + c);
-        sum = fmaf(s, l[x], sum);
-        v.x = fmaf(s, y.x, v.x); v.y = fmaf(s, y.y, v.y); v.z = fmaf(s, y.z, v.z); v.w = fmaf(s, y.w, v.w);
-      }
-      if (to.done) {
-        if (r / a.G < to.nq) kd_store<D>(a, to.b, to.g, r, c, M, sum, v);
-      } else {
-        *reinterpret_cast<float4*>(part + r * (D + 4) + c) = v;
-        if (c == 0) { part[r * (D + 4) + D] = M; part[r * (D + 4) + D + 1] = sum; }
-      }
-    }
-  };
-
-  const int run = (int)(u1 - u0);
-  for (int u = 0; u < run; ++k) {
+  for (int64_t u = u0; u < u1; ++k) {
     const int buf = k & 1;
     if (!dead && !mbar_wait(item_full + 8 * buf, (k >> 1) & 1)) dead = true;
     dead = __any_sync(0xffffffffu, dead);
     if (dead) {
       // the way through the items does not hang on the producer
-      if (lane == 0) items[buf].seg = kd_seg(a, batch, u0 + u, u0 + run);
+      if (lane == 0) items[buf].seg = kd_seg(a, batch, u, u1);
       __syncwarp();
     }
     const KdItem& it = items[buf];
     const float* q = s_q + kd_q<D>(buf * Rp + r0, 0);
-    float* my_acc = sums(buf) + w * RT * D;
-    float* my_m = sums(buf) + W * RT * D + w * RT;
-    float* my_l = my_m + W * RT;
+    float* my_m = s_m + w * RT;
+    float* my_l = s_l + w * RT;
+    float* my_acc = s_acc + w * RT * D;
     {
       KdFast<D, RT> f;
       kd_fast_init<D, RT>(f, it.inv + r0);
       const int to = base + it.seg.nfast, clear = base + it.seg.clear;
       while (my_team < nteam && i < to) {
-        const int sk = my_team * ring.depth + part;
-        const uint8_t* kt = ring.data + my_team * St::ring(ring.depth) + St::slot(ring.depth, part);
-        if (!dead && !mbar_wait(ring.full + 8 * sk, phase)) dead = true;
-        if (++part == ring.depth) { part = 0; phase ^= 1; }
-        const int sv = my_team * ring.depth + part;
+        if (!dead && !mbar_wait(keys.full + 8 * sk, pk)) dead = true;
         const auto between = [&]() {
           __syncwarp();
-          if (lane == 0) mbar_arrive(ring.empty + 8 * sk);
-          if (!dead && !mbar_wait(ring.full + 8 * sv, phase)) dead = true;
+          if (lane == 0) mbar_arrive(keys.empty + 8 * sk);
+          if (!dead && !mbar_wait(values.full + 8 * sv, pv)) dead = true;
         };
-        const uint8_t* vt = ring.data + my_team * St::ring(ring.depth) + St::slot(ring.depth, part);
+        const uint8_t* kt = keys.data + sk * St::bytesK;
+        const uint8_t* vt = values.data + sv * St::bytesV;
         if (rows <= 0) {
           between();
+        } else if (i < clear) {
+          kd_fast_block<D, RT, false>(f, kt, vt, q, 0, 0, between);
         } else {
-          const bool masked = i >= clear;
-          int endA = kBlock, endB = kBlock;
-          if (masked) {
-            const int ra = 2 * (lane % 4 % (RT / 2));
-            const int64_t p0 = (it.seg.blk0 + (i - base)) * kBlock;
-            endA = (int)min(max(it.end[r0 + ra] - p0, (int64_t)0), (int64_t)kBlock);
-            endB = (int)min(max(it.end[r0 + ra + 1] - p0, (int64_t)0), (int64_t)kBlock);
-          }
-          kd_fast_block<D, RT>(f, kt, vt, q, masked, endA, endB, between);
+          const int ra = 2 * (lane % 4 % (RT / 2));
+          const int64_t p0 = (it.seg.blk0 + (i - base)) * kBlock;
+          kd_fast_block<D, RT, true>(f, kt, vt, q, (int)min(max(it.end[r0 + ra] - p0, (int64_t)0), (int64_t)kBlock),
+                                     (int)min(max(it.end[r0 + ra + 1] - p0, (int64_t)0), (int64_t)kBlock), between);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(ring.empty + 8 * sv);
-        if (++part == ring.depth) { part = 0; phase ^= 1; }
+        if (lane == 0) mbar_arrive(values.empty + 8 * sv);
         i += nteam;
+        if ((sk += nteam) >= keys.slots) { sk = my_team; pk ^= 1; }
+        if ((sv += nteam) >= values.slots) { sv = my_team; pv ^= 1; }
       }
       base = to;
-      if (k > 0) {
-        if (!dead && !mbar_wait(a.defer ? left_item : merged, (k - 1) & 1)) dead = true;
-        if (a.defer) merge(buf ^ 1);
-      }
       kd_fast_store<D, RT>(f, my_m, my_l, my_acc);
     }
     // positions of the incomplete block, if it lies here
@@ -1114,28 +1076,30 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
         for (int c = 0; c < CPL; ++c) my_acc[r * D + lane * CPL + c] = st.acc[r][c];
       }
     }
-    if (tid == 0) {
-      KdDone& d = s_done[buf];
-      d.b = it.seg.b; d.g = it.seg.g; d.nq = it.seg.nq;
-      d.done = it.seg.done;
-      d.part = u == 0 ? 0 : 1;
+    bar_sync(1, W * 32);
+    // merge the teams, four channels of a row to a thread
+    float* part = a.part + (2 * (int64_t)blockIdx.x + (u == u0 ? 0 : 1)) * R * (D + 4);
+    for (int e = tid; e < R * (D / 4); e += W * 32) {
+      const int r = e / (D / 4), c = e % (D / 4) * 4;
+      float M = -INFINITY, l = 0.0f;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int x = r; x < nteam * team * RT; x += team * RT) M = fmaxf(M, s_m[x]);   // (the row in each team)
+      for (int x = r; x < nteam * team * RT; x += team * RT) {
+        const float s = s_m[x] > -INFINITY ? ex2(s_m[x] - M) : s_l[x] == 0.0f ? 0.0f : 1.0f;
+        const float4 y = *reinterpret_cast<const float4*>(s_acc + x * D + c);
+        l = fmaf(s, s_l[x], l);
+        v.x = fmaf(s, y.x, v.x); v.y = fmaf(s, y.y, v.y); v.z = fmaf(s, y.z, v.z); v.w = fmaf(s, y.w, v.w);
+      }
+      if (it.seg.done) {
+        if (r / a.G < it.seg.nq) kd_store<D>(a, it.seg.b, it.seg.g, r, c, M, l, v);
+      } else {
+        *reinterpret_cast<float4*>(part + r * (D + 4) + c) = v;
+        if (c == 0) { part[r * (D + 4) + D] = M; part[r * (D + 4) + D + 1] = l; }
+      }
     }
-    u += (int)it.seg.step;
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(item_empty + 8 * buf);
-      mbar_arrive(left_item);
-    }
-    if (!a.defer) {
-      if (!dead && !mbar_wait(left_item, k & 1)) dead = true;
-      merge(buf);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(merged);
-    }
-  }
-  if (k > 0 && a.defer) {
-    if (!dead && !mbar_wait(left_item, (k - 1) & 1)) dead = true;
-    merge((k - 1) & 1);
+    u += it.seg.step;
+    bar_sync(1, W * 32);
+    if (lane == 0) mbar_arrive(item_empty + 8 * buf);
   }
   if (dead && lane == 0) atomicOr(a.status, 4u);
 }
@@ -1214,20 +1178,25 @@ size_t kd_workspace(const csa_shape* s, int T) {
   return 256 + (kd_whole(s) ? 0 : (size_t)2 * kd_ctas(s) * R * (s->d + 4) * 4);
 }
 
-constexpr int kKdSharedBytes = 232448 - (int)sizeof(KdBatch) - 128;
+constexpr int kKdSharedBytes = 232448 - (int)sizeof(KdBatch) - 64;
 template <int D, int RT, typename E>
 cudaError_t launch_kv4_decode_t(Kv4DecodeArgs a, int ncta, cudaStream_t st) {
-  // Two slots for a team at least (there is room for that for every RT and d),
-  // three or more if possible, then room for two items' sums, then more slots.
-  using Lt = KdLayout<D, RT>;
-  const int ntile = (a.T * a.G + RT - 1) / RT, nteam = kKdWarps / kd_team(ntile);
-  const auto fits = [&](int depth, int defer) {
-    return depth * nteam <= kKdMaxSlots && Lt::ring(a.T * a.G, defer) + nteam * KdStage<D>::ring(depth) <= kKdSharedBytes;
-  };
-  a.defer = fits(3, 1) || (!fits(3, 0) && fits(2, 1));
-  a.depth = 2;
-  while (fits(a.depth + 1, a.defer)) ++a.depth;
-  const int smem = Lt::ring(a.T * a.G, a.defer) + nteam * KdStage<D>::ring(a.depth);
+  const int rest = KdLayout<D, RT>::ring(a.T * a.G);
+  // one slot per team in each ring (an SM's shared memory holds that for every
+  // RT and d), then more while there is room: keys first, whose copies have
+  // less time (the values' come while the warp is at the keys)
+  constexpr int K = KdStage<D>::bytesK, V = KdStage<D>::bytesV;
+  const int ntile = (a.T * a.G + RT - 1) / RT;
+  const int nteam = kKdWarps / kd_team(ntile);
+  int nk = 1, nv = 1;
+  for (bool more = true; more;) {
+    more = false;
+    if ((nk + 1) * nteam <= kKdMaxStages && nteam * ((nk + 1) * K + nv * V) <= kKdSharedBytes - rest) { ++nk; more = true; }
+    if ((nv + 1) * nteam <= kKdMaxStages && nteam * (nk * K + (nv + 1) * V) <= kKdSharedBytes - rest) { ++nv; more = true; }
+  }
+  a.slotsK = nk * nteam;
+  a.slotsV = nv * nteam;
+  const int smem = rest + a.slotsK * K + a.slotsV * V;
   const cudaError_t e =
       cudaFuncSetAttribute(kv4_decode_kernel<D, RT, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
