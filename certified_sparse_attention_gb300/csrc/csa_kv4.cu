@@ -65,18 +65,31 @@ __device__ __forceinline__ void report_range(unsigned* status, bool bad) {
   if ((threadIdx.x & 31) == 0) *status = any ? 8u : 0u;
 }
 
-// Codes of values whose step is in the normal range: the product with the
-// reciprocal, off by less than 1e-5 (a quotient up to 15, three roundings),
-// decides unless it lies that close to the middle between two codes; only
-// then is the quotient itself computed (on 16-bit inputs, whose quotients are
-// often exactly half way, about one in a thousand).  The division on every
-// value doubled the time of a long append.
+// Codes of CPL values, each on top of kCodeBase.  Where the step is in the normal range the
+// product with the reciprocal, off by less than 1e-5 (a quotient up to 15,
+// three roundings), decides unless it lies that close to the middle between
+// two codes; only then is the quotient itself computed (on 16-bit inputs, whose
+// quotients are often exactly half way, for about one value in a thousand).
+// The division on every value doubled the time of a long append.  Adding
+// 3 * 2^22 rounds to an integer, which then stands in the low bits.
+constexpr float kCodeRound = 12582912.0f;
+constexpr unsigned kCodeBase = 0x4B400000u;      // the bits of kCodeRound
 __device__ __forceinline__ bool step_plain(float step) { return step > 1e-30f && step < 1e30f; }
-__device__ __forceinline__ unsigned code4(float x, float m, float step, float inv, bool plain) {
-  const float y = fsub(x, m) * inv;
-  const float q = rintf(y);
-  if (plain && fabsf(y - q) < 0.49999f) return (unsigned)fminf(q, 15.0f);
-  return code4(x, m, step);
+template <int CPL>
+__device__ __forceinline__ void codes4(const float (&x)[CPL], const float (&m)[CPL], const float (&step)[CPL],
+                                           const float (&inv)[CPL], bool plain, unsigned (&code)[CPL]) {
+  float off = 0.0f;
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) {
+    const float y = fsub(x[c], m[c]) * inv[c];
+    const float q = fadd(y, kCodeRound);
+    off = fmaxf(off, fabsf(fsub(y, fsub(q, kCodeRound))));
+    code[c] = __float_as_uint(fminf(q, kCodeRound + 15.0f));
+  }
+  if (!(plain && off < 0.49999f)) {
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) code[c] = kCodeBase + code4(x[c], m[c], step[c]);
+  }
 }
 
 // v[e] (e = 0 .. 7): value of row e in this lane.  Returns in v[0] the minimum
@@ -123,7 +136,7 @@ __device__ __forceinline__ void row_floats(const typename Row<CPL, float>::T& r,
 // maximum go over the warps (shared memory), a value row's over the lanes.
 // Bound by memory: 32K tokens x 8 heads in bf16, read and coded.
 template <int D, typename E>
-__global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const Kv4AppendArgs a) {
+__global__ void __launch_bounds__(kKv4Threads, sizeof(E) == 2 ? 3 : 2) kv4_append_kernel(const Kv4AppendArgs a) {
   pdl_entry();
   constexpr int CPL = D / 32;
   typedef typename Row<CPL, E>::T RowT;
@@ -192,17 +205,21 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const Kv4Append
     if (lane < 8)
       reinterpret_cast<float2*>(a.c.vscale)[at * kBlock + t0 + 16 * ((lane >> 1) & 1) + 8 * (lane & 1) + (lane >> 2)] =
           make_float2(vm, vstep);
-    unsigned word[CPL];
+    unsigned word[CPL], code[CPL];
 #pragma unroll
-    for (int c = 0; c < CPL; ++c) word[c] = 0;
+    for (int c = 0; c < CPL; ++c) word[c] = 0u - kCodeBase * 0x11111111u;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float me = __shfl_sync(0xffffffffu, vm, e), de = __shfl_sync(0xffffffffu, vstep, e);
-      const float ie = __shfl_sync(0xffffffffu, vinv, e);
-      const bool plain = step_plain(de);
-      row_floats<CPL>(rv[e], x, E());
+      float me[CPL], de[CPL], ie[CPL];
+      me[0] = __shfl_sync(0xffffffffu, vm, e);
+      de[0] = __shfl_sync(0xffffffffu, vstep, e);
+      ie[0] = __shfl_sync(0xffffffffu, vinv, e);
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) word[c] |= code4(x[c], me, de, ie, plain) << (4 * e);   // (Delta = 0: 0/0, code 0)
+      for (int c = 1; c < CPL; ++c) { me[c] = me[0]; de[c] = de[0]; ie[c] = ie[0]; }
+      row_floats<CPL>(rv[e], x, E());
+      codes4<CPL>(x, me, de, ie, step_plain(de[0]), code);       // (Delta = 0: 0/0, code 0)
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) word[c] += code[c] << (4 * e);
     }
 #pragma unroll
     for (int c = 0; c < CPL; ++c) s_v[w][lane * CPL + c] = word[c];
@@ -233,11 +250,12 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const Kv4Append
     for (int e = 0; e < 8; ++e) {
       const int t = t0 + 16 * ((e >> 1) & 1) + 8 * (e & 1) + (e >> 2);
       row_floats<CPL>(rk[e], x, E());
-      unsigned code = 0;
+      codes4<CPL>(x, lo, hi, inv, plain, code);
+      unsigned all = 0u - (unsigned)(((1ull << 4 * CPL) - 1) / 15 * kCodeBase);
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) code |= code4(x[c], lo[c], hi[c], inv[c], plain) << (4 * c);
-      if (CPL == 4) *reinterpret_cast<uint16_t*>(K4 + t * (D / 2)) = (uint16_t)code;
-      else K4[t * (D / 2)] = (uint8_t)code;
+      for (int c = 0; c < CPL; ++c) all += code[c] << (4 * c);
+      if (CPL == 4) *reinterpret_cast<uint16_t*>(K4 + t * (D / 2)) = (uint16_t)all;
+      else K4[t * (D / 2)] = (uint8_t)all;
     }
     // value words, four of a channel's eight by a thread
     if (tid < 2 * D) {
@@ -261,10 +279,10 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const Kv4Append
   }
 }
 
-// eight codes of a word as floats: the nibble under the exponent of 2^23,
-// minus 2^23
-__device__ __forceinline__ float nibble(unsigned word, int k) {
-  return __uint_as_float(((word >> (4 * k)) & 15u) | 0x4B000000u) - 8388608.0f;
+// Code k of a word as a float: the nibble under the exponent of 2^23, minus
+// 2^23.  lo = word & 0x0F0F0F0F, hi = word >> 4 & 0x0F0F0F0F.
+__device__ __forceinline__ float nibble(unsigned lo, unsigned hi, int k) {
+  return __uint_as_float(__byte_perm(k & 1 ? hi : lo, 0x4B000000u, 0x7440 + k / 2)) - 8388608.0f;
 }
 template <typename E>
 __device__ __forceinline__ void store8(E* dst, const float (&x)[8]);
@@ -332,6 +350,8 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_unpack_kernel(const Kv4Unpack
   }
   const unsigned* V4 = reinterpret_cast<const unsigned*>(a.c.V4 + at * D * (kBlock / 2));
   for (int i = tid; i < D * 8; i += kKv4Threads) s_v[i / 64 * 65 + i % 64] = V4[i];
+  constexpr int STEP = HALF / CG;                   // groups of threads, each of which holds all channels of a row
+  const int sub = tid % HALF / CG;
   if (tid < HALF) {
     float m[8], dl[8];
     const float* bp = a.c.bounds + at * 2 * D + cg * 8;
@@ -342,35 +362,55 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_unpack_kernel(const Kv4Unpack
       dl[i] = v.x; dl[i + 1] = v.y; dl[i + 2] = v.z; dl[i + 3] = v.w;
     }
     const unsigned* K4 = reinterpret_cast<const unsigned*>(a.c.K4 + at * kBlock * (D / 2));
-    constexpr int STEP = HALF / CG;                 // rows between a thread's rows
     unsigned word[kBlock / STEP];
 #pragma unroll
-    for (int j = 0; j < kBlock / STEP; ++j) word[j] = K4[(tid / CG + j * STEP) * CG + cg];
+    for (int j = 0; j < kBlock / STEP; ++j) word[j] = K4[(sub + j * STEP) * CG + cg];
+    bar_sync(1, kKv4Threads);
+    E* dst = Ko + sub * D + cg * 8;
 #pragma unroll
     for (int j = 0; j < kBlock / STEP; ++j) {
-      const int r = tid / CG + j * STEP;
+      const int r = sub + j * STEP;
+      const unsigned lo = word[j] & 0x0F0F0F0Fu, hi = word[j] >> 4 & 0x0F0F0F0Fu;
       float x[8];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) x[c] = fadd(fmul(nibble(word[j], c), dl[c]), m[c]);
-      if (r >= r0 && r < r1) store8<E>(Ko + r * D + cg * 8, x);
+      for (int c = 0; c < 8; ++c) x[c] = fadd(fmul(nibble(lo, hi, c), dl[c]), m[c]);
+      if (r >= r0 && r < r1) store8<E>(dst + j * STEP * D, x);
     }
-  }
-  __syncthreads();
-  if (tid >= HALF) {
+  } else {
     // word wi: tokens 32 i + 16 u + 8 v + 2 w + e, i = wi % 2, w = wi / 2
-    for (int wi = (tid - HALF) / CG; wi < 8; wi += HALF / CG) {
-      unsigned word[8];
+    constexpr int N = 8 / STEP > 1 ? 8 / STEP : 1;  // words of a thread
+    float2 sc[N][8];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) word[c] = s_v[cg * 65 + c * 8 + wi];
+    for (int k = 0; k < N; ++k) {
+      const int wi = sub + k * STEP, t0 = 32 * (wi & 1) + 2 * (wi >> 1 & 3);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {                 // two tokens' (m, Delta), e = 0 and 1, side by side
+        const float4 two = *reinterpret_cast<const float4*>(a.c.vscale + (at * kBlock + t0 + 16 * (u >> 1) + 8 * (u & 1)) * 2);
+        sc[k][u] = make_float2(two.x, two.y);
+        sc[k][u + 4] = make_float2(two.z, two.w);
+      }
+    }
+    bar_sync(1, kKv4Threads);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int wi = sub + k * STEP;
+      if (wi >= 8) break;                           // (d = 64: sixteen groups)
+      unsigned lo[8], hi[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const unsigned word = s_v[cg * 65 + c * 8 + wi];
+        lo[c] = word & 0x0F0F0F0Fu;
+        hi[c] = word >> 4 & 0x0F0F0F0Fu;
+      }
       const int t0 = 32 * (wi & 1) + 2 * (wi >> 1);
+      E* dst = Vo + t0 * D + cg * 8;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int r = t0 + 16 * ((e >> 1) & 1) + 8 * (e & 1) + (e >> 2);
-        const float2 sc = reinterpret_cast<const float2*>(a.c.vscale)[at * kBlock + r];
+        const int dr = 16 * ((e >> 1) & 1) + 8 * (e & 1) + (e >> 2), r = t0 + dr;
         float x[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) x[c] = fadd(fmul(nibble(word[c], e), sc.y), sc.x);
-        if (r >= r0 && r < r1) store8<E>(Vo + r * D + cg * 8, x);
+        for (int c = 0; c < 8; ++c) x[c] = fadd(fmul(nibble(lo[c], hi[c], e), sc[k][e].y), sc[k][e].x);
+        if (r >= r0 && r < r1) store8<E>(dst + dr * D, x);
       }
     }
   }

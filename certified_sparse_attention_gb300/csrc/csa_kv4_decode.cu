@@ -100,7 +100,7 @@ struct KdBatch {
   int64_t len[kMaxB];
   int nq[kMaxB];
 };
-constexpr int kKdLead = 12;
+constexpr int kKdLead = 16;
 constexpr int kKdMaxCtas = 256;   // CTAs of a call (one per SM)
 
 // blocks of an item, the incomplete one counted

@@ -76,11 +76,15 @@ template <> struct Vec<__nv_bfloat16, 8> {
   }
 };
 
-// (a, b) <- the rotated pair
-__device__ __forceinline__ void turn_pair(float& a, float& b, float cs, float sn) {
-  const float x = a * cs - b * sn;
-  b = a * sn + b * cs;
-  a = x;
+// The elements of a lane's pair i: of split pairs, channel i of both vectors;
+// of adjacent ones, channels 2 i and 2 i + 1 of the two vectors in a row.
+template <bool INTER, int VEC>
+__device__ __forceinline__ float& pair_a(float (&x)[VEC], float (&y)[VEC], int i) {
+  return !INTER ? x[i] : i < VEC / 2 ? x[2 * i] : y[2 * i - VEC];
+}
+template <bool INTER, int VEC>
+__device__ __forceinline__ float& pair_b(float (&x)[VEC], float (&y)[VEC], int i) {
+  return !INTER ? y[i] : i < VEC / 2 ? x[2 * i + 1] : y[2 * i + 1 - VEC];
 }
 
 // Sequence b's first new position and number of new tokens; false (nothing
@@ -96,8 +100,8 @@ __device__ __forceinline__ bool new_tokens(const int64_t* len, const int64_t* n_
 constexpr int kRopeThreads = 128;
 constexpr int kRopeBatch = 4;     // rows of a group of lanes in flight
 
-template <int D, int VEC, typename E>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeArgs a) {
+template <int D, int VEC, bool INTER, typename E>
+__global__ void __launch_bounds__(kRopeThreads, 4) qk_norm_rope_kernel(const RopeArgs a) {
   pdl_entry();
   typedef Vec<E, VEC> Vx;
   typedef typename Vx::Raw Raw;
@@ -125,85 +129,112 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
 
   const bool turns_here = 2 * VEC * j < a.rot;
   // first channels of the two vectors: split pairs sit rot / 2 apart
-  const int c0 = !a.interleaved && turns_here ? VEC * j : 2 * VEC * j;
-  const int c1 = !a.interleaved && turns_here ? c0 + a.rot / 2 : c0 + VEC;
+  const int c0 = !INTER && turns_here ? VEC * j : 2 * VEC * j;
+  const int c1 = !INTER && turns_here ? c0 + a.rot / 2 : c0 + VEC;
   const int h_lo = chunk * a.heads_per, h_hi = min(h_lo + a.heads_per, a.heads);
-  float cs[VEC], sn[VEC];
-  if (turns_here && h_lo < a.Hq + a.Hkv) {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const long long frac = (long long)((unsigned long long)pos * a.turns[VEC * j + i]);   // signed: [-1/2, 1/2) turn
-      sincospif((float)frac * 1.0842021724855044e-19f, &sn[i], &cs[i]);                     // 2^-63: in units of pi
-    }
-  }
-  float w0[VEC], w1[VEC];
-  const void* have = nullptr;       // the weights that w0, w1 hold
   const unsigned group_mask = (unsigned)((1ull << LPR) - 1) << (threadIdx.x % 32 / LPR * LPR);
-  const E* qrow = reinterpret_cast<const E*>(a.q) + b * a.qs.b + t * a.qs.t;
-  const E* krow = reinterpret_cast<const E*>(a.k) + b * a.ks.b + t * a.ks.t;
-  const E* vrow = reinterpret_cast<const E*>(a.v) + b * a.vs.b + t * a.vs.t;
 
-  for (int h0 = h_lo; h0 < h_hi; h0 += kRopeBatch) {
+  float cs[VEC], sn[VEC];
+
+  // the chunk's heads of q, of k and of v in turn
+  bool have_turns = false;
+#pragma unroll 1
+  for (int part = 0; part < 3; ++part) {
+    const int first = part == 0 ? 0 : part == 1 ? a.Hq : a.Hq + a.Hkv;      // the part's first head
+    const int lo = max(h_lo, first) - first;
+    const int hi = min(h_hi, part == 0 ? a.Hq : first + a.Hkv) - first;
+    if (lo >= hi) continue;
+    const csa_strides& st = part == 0 ? a.qs : part == 1 ? a.ks : a.vs;
+    const E* src = reinterpret_cast<const E*>(part == 0 ? a.q : part == 1 ? a.k : a.v) + b * st.b + t * st.t + lo * st.h;
     Raw r0[kRopeBatch], r1[kRopeBatch];
+    const auto load = [&](int h) {
 #pragma unroll
-    for (int i = 0; i < kRopeBatch; ++i) {
-      const int h = h0 + i;
-      if (h >= h_hi) continue;
-      const E* src = h < a.Hq ? qrow + h * a.qs.h
-                   : h < a.Hq + a.Hkv ? krow + (h - a.Hq) * a.ks.h : vrow + (h - a.Hq - a.Hkv) * a.vs.h;
-      r0[i] = *reinterpret_cast<const Raw*>(src + c0);
-      r1[i] = *reinterpret_cast<const Raw*>(src + c1);
+      for (int i = 0; i < kRopeBatch; ++i) {
+        if (h + i >= hi) continue;
+        r0[i] = *reinterpret_cast<const Raw*>(src + c0);
+        r1[i] = *reinterpret_cast<const Raw*>(src + c1);
+        src += st.h;
+      }
+    };
+    load(lo);       // (on their way during the sines and cosines)
+    E* dst = reinterpret_cast<E*>(part == 0 ? a.q_out : part == 1 ? a.K : a.V);
+    int64_t dstep = D;
+    if (part == 0) {
+      dst += (((int64_t)b * a.T + t) * a.Hq + lo) * D;
+    } else if (a.to_cache) {
+      dst += (((int64_t)b * a.Hkv + lo) * a.n_max + pos) * D;
+      dstep = a.n_max * D;
+    } else {
+      dst += (((int64_t)b * a.T + t) * a.Hkv + lo) * D;
     }
+    // pair i of the lane: (x_a, x_b) <- (x_a wa cos - x_b wb sin, x_a wa sin + x_b wb cos)
+    float ac[VEC], bs[VEC], as[VEC], bc[VEC];
+    const void* wt = part == 0 ? a.wq : a.wk;
+    if (part < 2) {
+      float w0[VEC], w1[VEC];
 #pragma unroll
-    for (int i = 0; i < kRopeBatch; ++i) {
-      const int h = h0 + i;
-      if (h >= h_hi) continue;
-      E* dst;
-      if (h < a.Hq) {
-        dst = reinterpret_cast<E*>(a.q_out) + (((int64_t)b * a.T + t) * a.Hq + h) * D;
-      } else {
-        const int g = h < a.Hq + a.Hkv ? h - a.Hq : h - a.Hq - a.Hkv;
-        dst = reinterpret_cast<E*>(h < a.Hq + a.Hkv ? a.K : a.V) +
-              (a.to_cache ? (((int64_t)b * a.Hkv + g) * a.n_max + pos) * D
-                          : (((int64_t)b * a.T + t) * a.Hkv + g) * D);
+      for (int c = 0; c < VEC; ++c) w0[c] = w1[c] = 1.0f;
+      if (wt) {
+        Vx::widen(*reinterpret_cast<const Raw*>(reinterpret_cast<const E*>(wt) + c0), w0);
+        Vx::widen(*reinterpret_cast<const Raw*>(reinterpret_cast<const E*>(wt) + c1), w1);
       }
-      if (h < a.Hq + a.Hkv) {
-        float x[VEC], y[VEC];
-        Vx::widen(r0[i], x);
-        Vx::widen(r1[i], y);
-        const void* wt = h < a.Hq ? a.wq : a.wk;
-        if (wt) {
-          if (wt != have) {
-            Vx::widen(*reinterpret_cast<const Raw*>(reinterpret_cast<const E*>(wt) + c0), w0);
-            Vx::widen(*reinterpret_cast<const Raw*>(reinterpret_cast<const E*>(wt) + c1), w1);
-            have = wt;
+      if (!have_turns) {
+        have_turns = true;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          cs[i] = 1.0f;
+          sn[i] = 0.0f;
+          if (turns_here) {
+            const long long frac = (long long)((unsigned long long)pos * a.turns[VEC * j + i]);   // signed: [-1/2, 1/2) turn
+            sincospif((float)frac * 1.0842021724855044e-19f, &sn[i], &cs[i]);                     // 2^-63: in units of pi
           }
-          float ss = 0.0f;
-#pragma unroll
-          for (int c = 0; c < VEC; ++c) ss += x[c] * x[c] + y[c] * y[c];
-#pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group_mask, ss, o);
-          const float inv = rsqrtf(ss * (1.0f / D) + a.eps);
-#pragma unroll
-          for (int c = 0; c < VEC; ++c) { x[c] *= inv * w0[c]; y[c] *= inv * w1[c]; }
         }
-        if (turns_here) {
-          if (a.interleaved) {
+      }
 #pragma unroll
-            for (int c = 0; c < VEC; c += 2) {
-              turn_pair(x[c], x[c + 1], cs[c / 2], sn[c / 2]);
-              turn_pair(y[c], y[c + 1], cs[VEC / 2 + c / 2], sn[VEC / 2 + c / 2]);
+      for (int i = 0; i < VEC; ++i) {
+        const float wa = pair_a<INTER, VEC>(w0, w1, i), wb = pair_b<INTER, VEC>(w0, w1, i);
+        ac[i] = wa * cs[i]; bs[i] = wb * sn[i]; as[i] = wa * sn[i]; bc[i] = wb * cs[i];
+      }
+    }
+#pragma unroll 1
+    for (int h = lo; h < hi; h += kRopeBatch) {
+      if (h != lo) load(h);
+#pragma unroll
+      for (int i = 0; i < kRopeBatch; ++i) {
+        if (h + i >= hi) continue;
+        if (part < 2) {
+          float x[VEC], y[VEC];
+          Vx::widen(r0[i], x);
+          Vx::widen(r1[i], y);
+          if (wt) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) ss += x[c] * x[c] + y[c] * y[c];
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group_mask, ss, o);
+            const float inv = rsqrtf(ss * (1.0f / D) + a.eps);
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) { x[c] *= inv; y[c] *= inv; }
+          }
+#pragma unroll
+          for (int c = 0; c < VEC; ++c) {
+            float &xa = pair_a<INTER, VEC>(x, y, c), &xb = pair_b<INTER, VEC>(x, y, c);
+            if (turns_here) {
+              const float u = xa * ac[c] - xb * bs[c];
+              xb = xa * as[c] + xb * bc[c];
+              xa = u;
+            } else {          // (no partner: one that is infinite would reach it through 0 times infinity)
+              xa *= ac[c];
+              xb *= bc[c];
             }
-          } else {
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) turn_pair(x[c], y[c], cs[c], sn[c]);
           }
+          r0[i] = Vx::narrow(x);
+          r1[i] = Vx::narrow(y);
         }
-        r0[i] = Vx::narrow(x);
-        r1[i] = Vx::narrow(y);
+        *reinterpret_cast<Raw*>(dst + c0) = r0[i];
+        *reinterpret_cast<Raw*>(dst + c1) = r1[i];
+        dst += dstep;
       }
-      *reinterpret_cast<Raw*>(dst + c0) = r0[i];
-      *reinterpret_cast<Raw*>(dst + c1) = r1[i];
     }
   }
 }
@@ -214,11 +245,13 @@ cudaError_t launch_rope(RopeArgs a, int64_t tokens, cudaStream_t st) {
   // heads of a token to a group of lanes: the more, the fewer sines and
   // cosines; but first enough groups for four CTAs on every SM
   const int64_t per = tokens * a.heads / ((int64_t)sm_count() * 4 * RPB);
-  a.heads_per = (int)(per < 1 ? 1 : per > 16 ? 16 : per);
+  a.heads_per = (int)(per < 1 ? 1 : per > 64 ? 64 : per);
   a.nchunk = (a.heads + a.heads_per - 1) / a.heads_per;
   const int64_t blocks = (tokens * a.nchunk + RPB - 1) / RPB;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  launch_pdl(qk_norm_rope_kernel<D, VEC, E>, dim3((unsigned)blocks), dim3(kRopeThreads), 0, st, a);
+  const dim3 grid((unsigned)blocks), block(kRopeThreads);
+  if (a.interleaved) launch_pdl(qk_norm_rope_kernel<D, VEC, true, E>, grid, block, 0, st, a);
+  else launch_pdl(qk_norm_rope_kernel<D, VEC, false, E>, grid, block, 0, st, a);
   return cudaGetLastError();
 }
 
