@@ -75,6 +75,12 @@ __device__ __forceinline__ void report_range(unsigned* status, bool bad) {
 constexpr float kCodeRound = 12582912.0f;
 constexpr unsigned kCodeBase = 0x4B400000u;      // the bits of kCodeRound
 __device__ __forceinline__ bool step_plain(float step) { return step > 1e-30f && step < 1e30f; }
+// 1 / x to one unit in the last place
+__device__ __forceinline__ float approx_rcp(float x) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 template <int CPL>
 __device__ __forceinline__ void codes4(const float (&x)[CPL], const float (&m)[CPL], const float (&step)[CPL],
                                            const float (&inv)[CPL], bool plain, unsigned (&code)[CPL]) {
@@ -92,18 +98,17 @@ __device__ __forceinline__ void codes4(const float (&x)[CPL], const float (&m)[C
   }
 }
 
-// v[e] (e = 0 .. 7): value of row e in this lane.  Returns in v[0] the minimum
-// (maximum) over the warp of row lane % 8.
-template <bool MAX>
-__device__ __forceinline__ void reduce8_minmax(float (&v)[8]) {
+// v[e] (e = 0 .. 7): value of row e in this lane.  Returns in v[0] op over the
+// warp of row lane % 8.
+template <typename U, typename Op>
+__device__ __forceinline__ void reduce8(U (&v)[8], const Op op) {
   const int lane = threadIdx.x & 31;
-  const auto op = [](float a, float b) { return MAX ? max_nan(a, b) : min_nan(a, b); };
 #pragma unroll
   for (int s = 0; s < 3; ++s) {
     const bool hi = (lane >> s) & 1;
 #pragma unroll
     for (int i = 0; i < (4 >> s); ++i) {
-      const float send = hi ? v[2 * i] : v[2 * i + 1], keep = hi ? v[2 * i + 1] : v[2 * i];
+      const U send = hi ? v[2 * i] : v[2 * i + 1], keep = hi ? v[2 * i + 1] : v[2 * i];
       v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, 1 << s));
     }
   }
@@ -129,18 +134,91 @@ __device__ __forceinline__ void row_floats(const typename Row<CPL, float>::T& r,
   for (int c = 0; c < CPL; ++c) x[c] = f[c];
 }
 
+// element by element; bf16 in pairs, which loses nothing
+__device__ __forceinline__ unsigned min2_nan(unsigned a, unsigned b) {
+  unsigned r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned max2_nan(unsigned a, unsigned b) {
+  unsigned r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <bool MAX> __device__ __forceinline__ float pick(float a, float b) { return MAX ? max_nan(a, b) : min_nan(a, b); }
+template <bool MAX> __device__ __forceinline__ unsigned pick(unsigned a, unsigned b) { return MAX ? max2_nan(a, b) : min2_nan(a, b); }
+template <bool MAX> __device__ __forceinline__ uint2 pick(uint2 a, uint2 b) { return make_uint2(pick<MAX>(a.x, b.x), pick<MAX>(a.y, b.y)); }
+template <bool MAX> __device__ __forceinline__ float2 pick(float2 a, float2 b) { return make_float2(pick<MAX>(a.x, b.x), pick<MAX>(a.y, b.y)); }
+template <bool MAX> __device__ __forceinline__ float4 pick(float4 a, float4 b) {
+  return make_float4(pick<MAX>(a.x, b.x), pick<MAX>(a.y, b.y), pick<MAX>(a.z, b.z), pick<MAX>(a.w, b.w));
+}
+
+// lo, hi: over the warp, minimum and maximum of row lane % 8 of eight rows of
+// which each lane holds a part
+__device__ __forceinline__ void rows_minmax(const unsigned (&r)[8], float& lo, float& hi) {
+  // (minimum, -maximum) of a row as a pair, so that one minimum serves both
+  unsigned v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const unsigned neg = r[e] ^ 0x80008000u;
+    v[e] = min2_nan(__byte_perm(r[e], neg, 0x5410), __byte_perm(r[e], neg, 0x7632));
+  }
+  reduce8(v, [](unsigned a, unsigned b) { return min2_nan(a, b); });
+  lo = __uint_as_float(v[0] << 16);
+  hi = -__uint_as_float(v[0] & 0xFFFF0000u);
+}
+__device__ __forceinline__ void rows_minmax(const uint2 (&r)[8], float& lo, float& hi) {
+  unsigned v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const unsigned a = min2_nan(r[e].x, r[e].y), b = max2_nan(r[e].x, r[e].y) ^ 0x80008000u;
+    v[e] = min2_nan(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+  }
+  reduce8(v, [](unsigned a, unsigned b) { return min2_nan(a, b); });
+  lo = __uint_as_float(v[0] << 16);
+  hi = -__uint_as_float(v[0] & 0xFFFF0000u);
+}
+__device__ __forceinline__ void reduce_both(float (&l)[8], float (&h)[8], float& lo, float& hi) {
+  reduce8(l, [](float a, float b) { return min_nan(a, b); });
+  reduce8(h, [](float a, float b) { return max_nan(a, b); });
+  lo = l[0];
+  hi = h[0];
+}
+__device__ __forceinline__ void rows_minmax(const float2 (&r)[8], float& lo, float& hi) {
+  float l[8], h[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) { l[e] = min_nan(r[e].x, r[e].y); h[e] = max_nan(r[e].x, r[e].y); }
+  reduce_both(l, h, lo, hi);
+}
+__device__ __forceinline__ void rows_minmax(const float4 (&r)[8], float& lo, float& hi) {
+  float l[8], h[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    l[e] = min_nan(min_nan(r[e].x, r[e].y), min_nan(r[e].z, r[e].w));
+    h[e] = max_nan(max_nan(r[e].x, r[e].y), max_nan(r[e].z, r[e].w));
+  }
+  reduce_both(l, h, lo, hi);
+}
+
 // Warp w takes the eight tokens of word w of the value rows, 32 i + 16 u + 8 v
 // + 2 (w / 2) + e with i = w % 2, of which lane l holds the channels [l D / 32,
 // (l + 1) D / 32): all 16 rows (K and V) are loaded at once, a row by one
 // access of the warp, and stay in registers.  A key channel's minimum and
 // maximum go over the warps (shared memory), a value row's over the lanes.
-// Bound by memory: 32K tokens x 8 heads in bf16, read and coded.
+//
+// 32K tokens x 8 heads x 128, bf16: 52 us for 134 MB read and 42 MB written,
+// a little over a third of the copy bandwidth.  It is the instructions that
+// count (35 an element of K and V on a thread at first, 25 now, issue slots
+// 62% busy): a code costs nine, minimum and maximum of bf16 are taken in pairs
+// (72 -> 52 us, with the addresses of a block whose rows are all new).  Three
+// CTAs on an SM; two, with no limit on registers, took 62 us, four 51 with
+// spills.  float32 rows need twice the registers: two CTAs.
 template <int D, typename E>
 __global__ void __launch_bounds__(kKv4Threads, sizeof(E) == 2 ? 3 : 2) kv4_append_kernel(const Kv4AppendArgs a) {
   pdl_entry();
   constexpr int CPL = D / 32;
   typedef typename Row<CPL, E>::T RowT;
-  __shared__ __align__(16) float s_lo[8][D], s_hi[8][D];
+  __shared__ __align__(16) RowT s_lo[8][32], s_hi[8][32];
   __shared__ __align__(16) unsigned s_v[8][D];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int g = blockIdx.y, b = blockIdx.z;
@@ -168,40 +246,36 @@ __global__ void __launch_bounds__(kKv4Threads, sizeof(E) == 2 ? 3 : 2) kv4_appen
     const int64_t p0 = blk * kBlock, at = bg * a.nblk_max + blk;
     const int t0 = 32 * (w & 1) + 2 * (w >> 1);
     RowT rk[8], rv[8];
+    if (p0 >= start) {          // all rows are new
+      const E* k = kn + (p0 - start + t0) * a.ks.t + lane * CPL;
+      const E* v = vn + (p0 - start + t0) * a.vs.t + lane * CPL;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int t = t0 + 16 * ((e >> 1) & 1) + 8 * (e & 1) + (e >> 2);
-      const int64_t p = p0 + t;
-      const E* k = p < start ? Kt + t * D : kn + (p - start) * a.ks.t;
-      const E* v = p < start ? Vt + t * D : vn + (p - start) * a.vs.t;
-      rk[e] = *reinterpret_cast<const RowT*>(k + lane * CPL);
-      rv[e] = *reinterpret_cast<const RowT*>(v + lane * CPL);
+      for (int e = 0; e < 8; ++e) {
+        const int t = 16 * ((e >> 1) & 1) + 8 * (e & 1) + (e >> 2);
+        rk[e] = *reinterpret_cast<const RowT*>(k + t * a.ks.t);
+        rv[e] = *reinterpret_cast<const RowT*>(v + t * a.vs.t);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int t = t0 + 16 * ((e >> 1) & 1) + 8 * (e & 1) + (e >> 2);
+        const int64_t p = p0 + t;
+        const E* k = p < start ? Kt + t * D : kn + (p - start) * a.ks.t;
+        const E* v = p < start ? Vt + t * D : vn + (p - start) * a.vs.t;
+        rk[e] = *reinterpret_cast<const RowT*>(k + lane * CPL);
+        rv[e] = *reinterpret_cast<const RowT*>(v + lane * CPL);
+      }
     }
     // keys: one (m, Delta) per channel
-    float lo[CPL], hi[CPL], x[CPL];
+    RowT klo = rk[0], khi = rk[0];
 #pragma unroll
-    for (int c = 0; c < CPL; ++c) { lo[c] = INFINITY; hi[c] = -INFINITY; }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      row_floats<CPL>(rk[e], x, E());
-#pragma unroll
-      for (int c = 0; c < CPL; ++c) { lo[c] = min_nan(lo[c], x[c]); hi[c] = max_nan(hi[c], x[c]); }
-    }
-#pragma unroll
-    for (int c = 0; c < CPL; ++c) { s_lo[w][lane * CPL + c] = lo[c]; s_hi[w][lane * CPL + c] = hi[c]; }
+    for (int e = 1; e < 8; ++e) { klo = pick<false>(klo, rk[e]); khi = pick<true>(khi, rk[e]); }
+    s_lo[w][lane] = klo;
+    s_hi[w][lane] = khi;
     // values: one (m, Delta) per token, over the lanes meanwhile
-    float vlo[8], vhi[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      row_floats<CPL>(rv[e], x, E());
-      vlo[e] = vhi[e] = x[0];
-#pragma unroll
-      for (int c = 1; c < CPL; ++c) { vlo[e] = min_nan(vlo[e], x[c]); vhi[e] = max_nan(vhi[e], x[c]); }
-    }
-    reduce8_minmax<false>(vlo);
-    reduce8_minmax<true>(vhi);
-    const float vstep = fdiv(fsub(vhi[0], vlo[0]), 15.0f);
-    const float vm = vlo[0], vinv = 1.0f / vstep;
+    float x[CPL], vm, vhi;
+    rows_minmax(rv, vm, vhi);
+    const float vstep = fdiv(fsub(vhi, vm), 15.0f), vinv = approx_rcp(vstep);
     if (lane < 8)
       reinterpret_cast<float2*>(a.c.vscale)[at * kBlock + t0 + 16 * ((lane >> 1) & 1) + 8 * (lane & 1) + (lane >> 2)] =
           make_float2(vm, vstep);
@@ -224,18 +298,19 @@ __global__ void __launch_bounds__(kKv4Threads, sizeof(E) == 2 ? 3 : 2) kv4_appen
 #pragma unroll
     for (int c = 0; c < CPL; ++c) s_v[w][lane * CPL + c] = word[c];
     __syncthreads();
-    float inv[CPL];
+    klo = s_lo[0][lane];
+    khi = s_hi[0][lane];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) { klo = pick<false>(klo, s_lo[i][lane]); khi = pick<true>(khi, s_hi[i][lane]); }
+    float lo[CPL], hi[CPL], inv[CPL];
+    row_floats<CPL>(klo, lo, E());
+    row_floats<CPL>(khi, hi, E());
     bool plain = true;
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        lo[c] = min_nan(lo[c], s_lo[i][lane * CPL + c]);
-        hi[c] = max_nan(hi[c], s_hi[i][lane * CPL + c]);
-      }
       hi[c] = fdiv(fsub(hi[c], lo[c]), 15.0f);     // the step from here on
       if (hi[c] == 0.0f) hi[c] = 1.0f;
-      inv[c] = 1.0f / hi[c];
+      inv[c] = approx_rcp(hi[c]);
       plain = plain && step_plain(hi[c]);
     }
     if (w == 0) {
@@ -305,7 +380,12 @@ template <> __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16*
 // registers while the thread walks down the rows, one code word a row.
 // Values: eight words, one of each channel, hold eight tokens of eight
 // channels; the codes pass through shared memory, eight rows 260 bytes apart
-// so that the threads of a row read different banks.
+// so that the threads of a row read different banks, and the tokens' scales
+// are on their way meanwhile (loaded after the barrier: 151 us where it is 126).
+//
+// Bound by memory: 128K tokens x 8 heads x 128 to bf16, 696 MB in 126 us,
+// 5.5 TB/s or 81% of the copy bandwidth.  Stores marked as streaming made no
+// difference.
 template <int D, typename E>
 __global__ void __launch_bounds__(kKv4Threads) kv4_unpack_kernel(const Kv4UnpackArgs a) {
   pdl_entry();

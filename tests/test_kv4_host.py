@@ -112,7 +112,8 @@ def test_unpack_refusals(lib, over, want):
     (dict(o=None), INVALID), (dict(qs=ODD), INVALID), (dict(qs=None), INVALID),
     (dict(q=FAKE + 8), INVALID), (dict(cache=cache(K4=FAKE + 8)), INVALID),
     (dict(workspace=None), WORKSPACE), (dict(workspace=FAKE + 16), WORKSPACE),
-    (dict(workspace_bytes=256), WORKSPACE),
+    (dict(workspace_bytes=255), WORKSPACE),
+    (dict(shape=shape(n_max=100000), workspace_bytes=256), WORKSPACE),
     (dict(shape=shape(d=96)), UNSUPPORTED)])
 def test_decode_refusals(lib, over, want):
     a = dict(shape=shape(), cache=cache(), T=4, q=FAKE, qs=strides(),
@@ -123,7 +124,9 @@ def test_decode_refusals(lib, over, want):
 
 
 def test_workspace_size(lib):
-    s = shape()
+    # one word and, where a sequence may be cut, the parts' sums
+    assert csa.csa_kv4_workspace_size(shape(), 1) == 256
+    s = shape(n_max=100000)
     assert csa.csa_kv4_workspace_size(s, 1) > 256
     assert csa.csa_kv4_workspace_size(s, 16) > csa.csa_kv4_workspace_size(s, 1)
     assert csa.csa_kv4_workspace_size(s, 0) == 0
