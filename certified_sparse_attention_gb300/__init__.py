@@ -662,14 +662,23 @@ def _counts(t, name: str, B: int, device: int) -> Optional[int]:
     """Check a device int64 [B] (or None); its address."""
     if t is None:
         return None
-    if t.dtype.itemsize != 8 or t.dtype.is_floating_point or \
-            t.dtype.is_complex or t.shape != (B,) or not t.is_contiguous():
+    ty = t.dtype
+    if ty.itemsize != 8 or ty.is_floating_point or ty.is_complex or \
+            not ty.is_signed or t.shape != (B,) or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous int64 tensor [{B}] is "
                          "required")
     if t.get_device() != device:
         raise ValueError(f"{name}: a tensor on CUDA device {device} is "
                          "required")
     return t.data_ptr()
+
+
+def _settled(device: int) -> None:
+    """Wait for what a constructor has sent to its device (buffers set to
+    zero, tables): a first call on another stream would not."""
+    import torch
+    if device >= 0 and not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(device).synchronize()
 
 
 class QKNormRope:
@@ -680,7 +689,8 @@ class QKNormRope:
     side); inv_freq: the rotated pairs' angles per position in radians (2 x
     their number = the rotated channels, a multiple of 8; None: no
     rotation); interleaved: pair i is channels (2i, 2i + 1) instead of (i,
-    i + rot_dim / 2).  ``status`` is the device word csa_check reads."""
+    i + rot_dim / 2).  ``status`` is the device word csa_check reads; each
+    call sets it anew."""
 
     def __init__(self, shape: csa_shape, device, wq=None, wk=None,
                  norm_eps: float = 1e-6, inv_freq=None,
@@ -704,6 +714,7 @@ class QKNormRope:
         self.params = csa_norm_rope(
             pw[0], pw[1], float(norm_eps), 2 * len(table),
             1 if interleaved else 0, _ptr(self.turns))
+        _settled(self.device)
 
     def __call__(self, q, k, v, K, V, lens_dev, n_new=None,
                  to_cache: bool = True, q_out=None, stream=None):
@@ -712,7 +723,8 @@ class QKNormRope:
         [B][Hkv][n_max][d], or with to_cache=False rows [B][T][Hkv][d].
         lens_dev: device int64 [B], the new tokens counted already; n_new:
         device int64 [B] (None: T each).  Returns q_out [B][T][Hq][d] (made
-        when not given)."""
+        when not given, on the current stream: needed with ``stream``, where
+        that memory may still be in use)."""
         s, dev, dt = self.shape, self.device, self.dtype
         B, Hq, Hkv, d = s.B, s.Hq, s.Hkv, s.d
         pq, qb, qt, qh = _rows(q, "q", B, 0, Hq, d, dt, dev)
@@ -732,6 +744,8 @@ class QKNormRope:
         pl = _counts(lens_dev, "lens_dev", B, dev)
         pn = _counts(n_new, "n_new", B, dev)
         if q_out is None:
+            if stream is not None:
+                raise ValueError("q_out: required when a stream is given")
             q_out = q.new_empty((B, T, Hq, d))
         po = _whole(q_out, "q_out", (B, T, Hq, d), dt, dev)
         st = load_library().csa_qk_norm_rope(
@@ -785,6 +799,7 @@ class KV4Cache:
             at.append(_whole(t, name, size, dt, self.device))
             setattr(self, name, t)
         self.desc = csa_kv4(*at)
+        _settled(self.device)
 
     def append(self, k, v, lens_dev, n_new=None, stream=None) -> None:
         """Append rows k, v [B][T][Hkv][d] (views with any strides of whole
@@ -845,6 +860,7 @@ class KV4Decode:
         self.lse = (torch.zeros((shape.B, self.T, shape.Hq),
                                 dtype=torch.float32, device=device)
                     if with_lse else None)
+        _settled(self.device)
 
     def __call__(self, q, cache: KV4Cache, lens_dev, n_q=None, stream=None):
         """q [B][T][Hq][d] (a view with strides of whole 16 bytes); lens_dev

@@ -425,14 +425,15 @@ size_t csa_kv4_workspace_size(const csa_shape* shape, int T);
  * every sequence (T = 1: a decode step; more: drafted tokens or a short
  * chunk): o = softmax(q K^T / sqrt d) V with K, V the values the cache stands
  * for; token t of sequence b, at position len[b] - n_q[b] + t, attends to
- * the positions up to its own.  Softmax statistics and sums in float32.
+ * the positions up to its own.  Softmax statistics and sums in float32;
+ * keys and values up to 2^100 in magnitude (sums of larger ones overflow).
  *   q    device [B][T][Hq][d], type `dtype`, strides qs
  *   len  device [B] int64, 0 <= len[b] <= n_max, its tokens appended already
  *   n_q  device [B] int64, or NULL: T each
  *   o    device [B][T][Hq][d] float; rows t >= n_q[b] are left as they are; a
  *        row with no position to attend to is 0
  *   lse  device [B][T][Hq] float, or NULL: ln sum exp(s) of each row (-inf
- *        for a row with nothing to attend to)
+ *        for a row with nothing to attend to), rows t >= n_q[b] as in o
  *   workspace  device, csa_kv4_workspace_size bytes, 256-byte aligned, one
  *        per call in flight (two captured graphs that share one must not
  *        replay at the same time); contents on entry do not matter.  It

@@ -446,6 +446,79 @@ def test_decode_longer(dtype, d, G, lens):
     check_decode(f64(o), f64(op.lse), f64(q), model, lens, [1] * len(lens), G)
 
 
+@pytest.mark.parametrize("dtype,d,G,T", [
+    ("bf16", 128, 4, 2), ("bf16", 64, 8, 8), ("f32", 128, 4, 5),
+    ("bf16", 128, 1, 16), ("f32", 64, 2, 1)])
+def test_decode_tokens_over_cut_sequences(dtype, d, G, T):
+    # several query tokens, ragged, with sequences cut over CTAs at blocks
+    # that some tokens see in part
+    torch, csa, dev = _t()
+    rng = np.random.default_rng(7 * T + G)
+    lens = [0, 1, 64, 1700, 5003, 130, 4992]
+    nq = [min(T, 1 + i % T) for i in range(len(lens))]
+    nq[0], nq[1], nq[3] = T, T, 0
+    s, cache, model = filled(rng, dtype, d, 2, lens, 5100, 2 * G, step=4096)
+    q = rows(rng, (len(lens), T, 2 * G, d), dtype)
+    op = csa.KV4Decode(s, dev, T, with_lse=True)
+    assert op.ws_bytes > 256
+    op.ws.fill_(0xFF)
+    op.o.fill_(55.0)
+    o = op(q, cache, i64(lens), i64(nq))
+    assert csa.csa_check(op.ws) == 0
+    on = f64(o)
+    check_decode(on, f64(op.lse), f64(q), model, lens, nq, G)
+    for b in range(len(lens)):
+        assert np.all(on[b, nq[b]:] == 55.0)
+    first = o.clone()
+    assert torch.equal(first, op(q, cache, i64(lens), i64(nq)))
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -90, 2.0 ** 98])
+def test_decode_extreme_magnitudes(scale):
+    # up to the documented 2^100, q scaled against k
+    torch, csa, dev = _t()
+    rng = np.random.default_rng(77)
+    d, n = 64, 64 * 3 + 11
+    s = csa.make_shape(1, 4, 1, d, n, "f32")
+    k = (rng.uniform(-1, 1, (1, n, 1, d)) * scale).astype(np.float32)
+    v = (rng.uniform(-1, 1, (1, n, 1, d)) * scale).astype(np.float32)
+    q = (rng.normal(size=(1, 1, 4, d)) / scale).astype(np.float32)
+    to = lambda x: torch.from_numpy(np.ascontiguousarray(x, np.float32)).to(dev)
+    cache, model = csa.KV4Cache(s, dev), Model(1, 1, d)
+    cache.append(to(k), to(v), i64([n]))
+    model.add(k, v, [n])
+    op = csa.KV4Decode(s, dev, 1, with_lse=True)
+    o = op(to(q), cache, i64([n]))
+    check_decode(f64(o), f64(op.lse), q.astype(np.float64), model, [n], [1], 4)
+
+
+def test_first_call_on_another_stream():
+    # buffers and outputs are ready for any stream once they are made, however
+    # far behind the stream is that made them
+    torch, csa, dev = _t()
+    rng = np.random.default_rng(5)
+    lens = [90, 128]
+    s = csa.make_shape(2, 4, 2, 64, 200, "bf16")
+    k, v = rows(rng, (2, 128, 2, 64), "bf16"), rows(rng, (2, 128, 2, 64), "bf16")
+    q = rows(rng, (2, 1, 4, 64), "bf16")
+    ln = i64(lens)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream(dev)
+
+    def run(stream):
+        cache, op = csa.KV4Cache(s, dev), csa.KV4Decode(s, dev)
+        with torch.cuda.stream(stream):
+            cache.append(k, v, ln, ln)
+            op(q, cache, ln)
+        return cache, op
+    want = run(torch.cuda.current_stream())[1].o.clone()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)
+    cache, op = run(side)
+    torch.cuda.synchronize()
+    assert torch.equal(op.o, want)
+
+
 def test_decode_many_short_sequences():
     torch, csa, dev = _t()
     rng = np.random.default_rng(31)

@@ -262,7 +262,8 @@ def status():
     dict(K=Fake([2, 2, 1000, 128], "float32")),
     dict(lens_dev=Fake([2], "int32")), dict(lens_dev=Fake([3], I64)),
     dict(lens_dev=HostFake([2], I64)), dict(n_new=Fake([1], I64)),
-    dict(q_out=Fake([2, 4, 2, 128])),
+    dict(lens_dev=Fake([2], "uint64")), dict(n_new=Fake([2], "float64")),
+    dict(q_out=None), dict(q_out=Fake([2, 4, 2, 128])),
     dict(q_out=Fake([2, 4, 8, 128], stride=[8192, 2048, 256, 1]))])
 def test_binding_refuses_rope_arguments(no_launch, over):
     import torch
