@@ -4,22 +4,22 @@
 // stands for (whole blocks of 64 tokens in codes, the incomplete last block
 // in full precision).
 //
-// Work is split over the long axis by units of one block of one (sequence,
-// KV head): the units of the whole batch, in order, are dealt to the CTAs in
-// equal runs, whatever the lengths, which are read on the device.  A CTA
-// walks its run item by item (an item: one (sequence, KV head)); its warps
-// take the blocks in turn, each with its own running maximum and sums, and
-// merge them in shared memory.  An item that lies in one CTA is finished
-// there; the parts of the others (at most two per CTA: its first and its
-// last item) go to the workspace, and a second kernel joins them, one CTA
-// for each item that was cut.
+// Work is split over the long axis by units of about one block of one
+// (sequence, KV head), an item: the units of the whole batch, in order, are
+// dealt to the CTAs in equal runs, whatever the lengths, which are read on the
+// device.  A CTA walks its run item by item; its warps take the blocks in
+// turn, each with its own running maximum and sums, and merge them in shared
+// memory.  An item that lies in one CTA is finished there; the parts of the
+// others (at most two per CTA, of its first and its last item) go to the
+// workspace, and a second kernel joins them.  Where no sequence can be longer
+// than 24 blocks, items are not cut and there is no second kernel.
 //
 // The rows of an item are its T * G query vectors (G query heads share the
 // KV head).  A warp handles a tile of 4 or 8 rows; with more than 8 rows the
-// warps of a CTA form teams of 2, 4 or 8 that share the blocks.
+// warps of a CTA form teams of 2 to 8 that share the blocks.
 //
-// Whole blocks that every row sees in full go through the tensor cores with
-// the codes themselves as one operand.  A key is k_c = m_c + Delta_c n_c, so
+// Whole blocks go through the tensor cores with the codes themselves as one
+// operand.  A key is k_c = m_c + Delta_c n_c, so
 //   q.k = sum_c q_c m_c + sum_c (q_c Delta_c) n_c,
 // and a value row is v = m_t + Delta_t n, so
 //   sum_t p_t v_t = sum_t p_t m_t + sum_t (p_t Delta_t) n_t :
@@ -35,12 +35,21 @@
 // a single one would leave 2^-12 of every score), and the products are
 // summed in float32.  With up to 4 rows the two parts
 // fill the 8 columns of one instruction (m16n8k16: codes are the 16-row
-// side); with 8 rows each part takes an instruction.  Blocks that some row
-// sees in part, and the incomplete block, take a plain path (kd_step).
+// side); with 8 rows each part takes an instruction.  The incomplete block
+// takes a plain path (kd_step).
 //
-// Blocks come by bulk copies into a ring of shared-memory stages per team,
-// each stage on an mbarrier; the first blocks of the next item are on their
-// way while the current one is merged.
+// Blocks come by bulk copies into two rings of shared memory, keys and values,
+// each slot on an mbarrier; producer warps run ahead over the items, so the
+// first blocks and the queries of the next item are on their way while the
+// current one is merged.
+//
+// What bounds it: not the memory but the instructions of the consumer warps
+// (an eighth-KB block takes a warp 1300 to 1500, three warps on a scheduler
+// issue 0.45 to 0.51 a cycle, tensor pipe 22 to 28% busy).  One sequence of
+// 512K tokens in all, 8 KV heads, 4 query heads each: 131 us for 638 MB, 4.9
+// TB/s, 72% of the copy bandwidth (loads alone 104 us).  Batch of 64, up to 8K
+// tokens, 8 query heads each: 128 us for 369 MB, 2.9 TB/s.  Before the codes
+// went through the tensor cores those were 1250 and 1217 us.
 #include <cmath>
 #include <cuda_fp16.h>
 
@@ -91,10 +100,15 @@ struct KdStage {
   static constexpr int txK = kBlock * D / 2 + 8 * D, txV = kBlock * D / 2 + kBlock * 8;
 };
 
-// What the kernels know of the batch.  The unit of work is a block of an item
-// (an item: one sequence and KV head), kKdLead more of them stand for an
-// item's own cost (its queries, its incomplete block, the merge), so that
-// runs of short items do not take longer than runs of long ones.
+// What the kernels know of the batch.  An item is one sequence and KV head.
+// Its units of work, in order: kKdLead for its own cost (its queries, the
+// merge), its whole blocks, and what its incomplete block costs.  The weights
+// follow fits to the times of single CTAs (batch of 64, 8 query heads to a KV
+// head: a block 0.30 us, an item 3.8 to 4.6 us, an incomplete block 1.7 us and
+// 0.06 us a token).  With 16 units for an item and one for its incomplete
+// block the last CTA of that batch took 144 us where the mean was 119; a lead
+// of 8 and of 12 with lighter incomplete blocks took 133 and 131 us for the
+// call, this 128 (drafts of 16 rows 116, 117 and 120).
 struct KdBatch {
   int64_t pref[kMaxB + 1];    // units of the sequences before b (pref[B]: all)
   int64_t len[kMaxB];
@@ -103,10 +117,13 @@ struct KdBatch {
 constexpr int kKdLead = 16;
 constexpr int kKdMaxCtas = 256;   // CTAs of a call (one per SM)
 
-// blocks of an item, the incomplete one counted
-__device__ __forceinline__ int64_t kd_blocks(int64_t n) { return (n + kBlock - 1) / kBlock; }
+// units of the incomplete block (an empty item has one)
+__device__ __forceinline__ int kd_tail(int64_t n) {
+  const int left = (int)(n % kBlock);
+  return left ? 6 + left / 4 : n == 0;
+}
 __device__ __forceinline__ int64_t kd_units(const Kv4DecodeArgs& a, int64_t n) {
-  return a.whole ? 1 : kd_blocks(n) + kKdLead;
+  return a.whole ? 1 : kKdLead + n / kBlock + kd_tail(n);
 }
 
 // by warp 0, then a barrier of the CTA
@@ -145,14 +162,15 @@ __device__ __forceinline__ void kd_batch(const Kv4DecodeArgs& a, KdBatch& s) {
 
 // the part of an item that lies in the run [u, u1) of a CTA
 struct KdSeg {
-  int64_t bg, n;
-  int64_t blk0, blk1;      // its blocks [blk0, blk1)
+  int64_t bg, n, blk0;     // its first block
   int64_t step;            // its units
-  int64_t first, last;     // units of the whole item
+  int64_t start, last;     // the item's first and last units that stand for work done where they lie
   int b, g, nq;
-  int nfast;               // whole blocks among its blocks (they come first)
+  int nfast;               // whole blocks
   int clear;               // of those, the first `clear` are seen in full by every row
-  int done;                // the whole item lies here
+  int left;                // tokens of the incomplete block
+  bool any;                // there is something to do
+  bool cut0, cut1;         // the item has parts in the run before, in the one after
 };
 __device__ __forceinline__ KdSeg kd_seg(const Kv4DecodeArgs& a, const KdBatch& batch, int64_t u, int64_t u1) {
   KdSeg s;
@@ -165,17 +183,23 @@ __device__ __forceinline__ KdSeg kd_seg(const Kv4DecodeArgs& a, const KdBatch& b
   s.b = lo;
   s.n = batch.len[lo];
   s.nq = batch.nq[lo];
-  const int64_t blocks = kd_blocks(s.n), units = kd_units(a, s.n), rem = u - batch.pref[lo];
+  const int64_t units = kd_units(a, s.n), rem = u - batch.pref[lo], whole = s.n / kBlock;
   s.g = (rem | units) >> 32 ? (int)(rem / units) : (int)((unsigned)rem / (unsigned)units);
   s.bg = (int64_t)s.b * a.Hkv + s.g;
   const int64_t v0 = rem - s.g * units, v1 = min(units, v0 + (u1 - u));
   s.step = v1 - v0;
-  s.first = u - v0;
-  s.last = s.first + units - 1;
-  s.done = v0 == 0 && v1 == units;
-  s.blk0 = a.whole ? 0 : max(v0 - kKdLead, (int64_t)0);
-  s.blk1 = a.whole ? blocks : max(v1 - kKdLead, (int64_t)0);
-  s.nfast = (int)max(min(s.n / kBlock, s.blk1) - s.blk0, (int64_t)0);
+  // Work begins with the first block; the incomplete block is done where the
+  // middle of its units lies.
+  const int tail = kd_tail(s.n);
+  const int64_t w0 = a.whole ? 0 : kKdLead, w1 = a.whole ? 0 : kKdLead + whole + (tail ? tail / 2 : -1);
+  s.start = u - v0 + w0;
+  s.last = u - v0 + w1;
+  s.any = v0 <= w1 && v1 > w0;
+  s.cut0 = v0 > w0;
+  s.cut1 = v1 <= w1;
+  s.blk0 = a.whole ? 0 : min(max(v0 - kKdLead, (int64_t)0), whole);
+  s.nfast = (int)((a.whole ? whole : min(max(v1 - kKdLead, (int64_t)0), whole)) - s.blk0);
+  s.left = v0 <= w1 && w1 < v1 ? (int)(s.n % kBlock) : 0;
   // the first row sees positions below n - nq + 1
   const int64_t clear = max(s.n - s.nq + 1, (int64_t)0) / kBlock - s.blk0;
   s.clear = (int)min(max(clear, (int64_t)0), (int64_t)s.nfast);
@@ -185,6 +209,14 @@ __device__ __forceinline__ KdSeg kd_seg(const Kv4DecodeArgs& a, const KdBatch& b
 // units of a CTA's run
 __device__ __forceinline__ int64_t kd_run(const KdBatch& batch, int ncta) {
   return (batch.pref[kMaxB] + ncta - 1) / ncta;
+}
+// the run without what is nothing to do at its ends: the units of an item whose
+// work lies in the run before or in the one after
+__device__ __forceinline__ void kd_trim(const Kv4DecodeArgs& a, const KdBatch& batch, int64_t& u0, int64_t& u1) {
+  if (a.whole || u0 >= u1) return;
+  const KdSeg s = kd_seg(a, batch, u0, u1), e = kd_seg(a, batch, u1 - 1, u1);
+  if (e.start >= u1) u1 = max(u0, e.start - kKdLead);
+  if (!s.any) u0 = min(u1, u0 + s.step);
 }
 
 // writes four channels of a finished row
@@ -864,6 +896,7 @@ __device__ __forceinline__ void kd_queries(const Kv4DecodeArgs& a, const KdBatch
   const int R = a.T * a.G, Rp = (R + RT - 1) / RT * RT;
   int k = 0;
   bool dead = false;
+  kd_trim(a, batch, u0, u1);
   for (int64_t u = u0; u < u1 && !dead; ++k) {
     const int buf = k & 1;
     dead = !mbar_wait(empty + 8 * buf, ((k >> 1) & 1) ^ 1);
@@ -966,7 +999,7 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
   }
   kd_batch(a, batch);
   const int64_t per = kd_run(batch, gridDim.x);
-  const int64_t u0 = (int64_t)blockIdx.x * per, u1 = min(batch.pref[kMaxB], u0 + per);
+  int64_t u0 = (int64_t)blockIdx.x * per, u1 = min(batch.pref[kMaxB], u0 + per);
 
   if (w >= W) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kKdRegsProducer));
@@ -1000,6 +1033,7 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
   int i = my_team;                                // the team's next block, its slots and their parities
   int sk = my_team, sv = my_team, pk = 0, pv = 0;
   int k = 0;                                      // number of the item
+  kd_trim(a, batch, u0, u1);
 
   for (int64_t u = u0; u < u1; ++k) {
     const int buf = k & 1;
@@ -1047,9 +1081,9 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
       base = to;
       kd_fast_store<D, RT>(f, my_m, my_l, my_acc);
     }
-    // positions of the incomplete block, if it lies here
+    // the incomplete block, if it is to be done here
     const int64_t p0 = it.seg.n / kBlock * kBlock;
-    const int left = it.seg.blk1 * kBlock > p0 ? (int)(it.seg.n - p0) : 0;
+    const int left = it.seg.left;
     if (rows > 0 && 8 * (i - base) < left) {
       // eight tokens at a time: the state moves on to lanes that hold channels
       __syncwarp();
@@ -1078,7 +1112,7 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
     }
     bar_sync(1, W * 32);
     // merge the teams, four channels of a row to a thread
-    float* part = a.part + (2 * (int64_t)blockIdx.x + (u == u0 ? 0 : 1)) * R * (D + 4);
+    float* part = a.part + (2 * (int64_t)blockIdx.x + (it.seg.cut0 ? 0 : 1)) * R * (D + 4);
     for (int e = tid; e < R * (D / 4); e += W * 32) {
       const int r = e / (D / 4), c = e % (D / 4) * 4;
       float M = -INFINITY, l = 0.0f;
@@ -1090,7 +1124,7 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
         l = fmaf(s, s_l[x], l);
         v.x = fmaf(s, y.x, v.x); v.y = fmaf(s, y.y, v.y); v.z = fmaf(s, y.z, v.z); v.w = fmaf(s, y.w, v.w);
       }
-      if (it.seg.done) {
+      if (!it.seg.cut0 && !it.seg.cut1) {
         if (r / a.G < it.seg.nq) kd_store<D>(a, it.seg.b, it.seg.g, r, c, M, l, v);
       } else {
         *reinterpret_cast<float4*>(part + r * (D + 4) + c) = v;
@@ -1104,58 +1138,67 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
   if (dead && lane == 0) atomicOr(a.status, 4u);
 }
 
-// Joins the parts of the items that were cut: CTA j owns the item that holds
-// the border between the runs of CTAs j and j + 1, if j is the first CTA of
-// that item.
+// Joins the parts of the items that were cut: CTAs (j, y) own the item of
+// which CTA j of the decode kernel did the beginning, if it did not do all of
+// it; a warp to a row, eight rows to a CTA.  Which item that is depends on the
+// lengths alone, so it is found before the wait for the decode kernel (whose
+// own wait has seen the lengths written; CTAs with nothing to do wait too:
+// the next kernel takes this grid's end for the decode kernel's).  Weights and
+// the first eight parts are read at once: done one after the other, eight rows
+// to a CTA's eight warps in turn, the join took 10 us after a batch of 64 and
+// 17 after drafts of 16 rows.
+constexpr int kKdJoinWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(256) kv4_join_kernel(const Kv4DecodeArgs a, int ncta) {
-  pdl_entry();
+__global__ void __launch_bounds__(kKdJoinWarps * 32) kv4_join_kernel(const Kv4DecodeArgs a, int ncta) {
   __shared__ KdBatch batch;
-  __shared__ float s_w[8][kKdMaxCtas];
+  __shared__ float s_w[kKdJoinWarps][kKdMaxCtas];
   kd_batch(a, batch);
-  const int64_t per = kd_run(batch, ncta), x = ((int64_t)blockIdx.x + 1) * per;
-  if (x >= batch.pref[kMaxB]) return;
+  const int64_t per = kd_run(batch, ncta), x = min(((int64_t)blockIdx.x + 1) * per, batch.pref[kMaxB] - 1);
   const KdSeg s = kd_seg(a, batch, x, x + 1);
-  if (s.first == x || s.first / per != (int64_t)blockIdx.x) return;
-  const int c0 = (int)blockIdx.x, parts = (int)(s.last / per) - c0 + 1;
-  const int R = a.T * a.G, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  // part 0 is the first or the last one of its CTA, the others the first ones
+  const int c0 = (int)(s.start / per), parts = (int)(s.last / per) - c0 + 1;
+  const int R = a.T * a.G, lane = threadIdx.x & 31, w = threadIdx.x >> 5, r = blockIdx.y * kKdJoinWarps + w;
+  pdl_entry();
+  if (c0 != (int)blockIdx.x || parts == 1 || r >= R || r / a.G >= s.nq) return;
+  // part 0 is the last one of its CTA, the others the first ones
   const int64_t stride = (int64_t)R * (D + 4);
-  const float* part0 = a.part + (2 * (int64_t)c0 + (s.first == c0 * per ? 0 : 1)) * stride;
-  const float* part1 = a.part + 2 * (int64_t)c0 * stride;
-  // a warp to a row: the parts' weights first, by the lanes, then the sums
-  for (int r = w; r < R && r / a.G < s.nq; r += 8) {
-    const int64_t row = r * (D + 4);
-    float M = -INFINITY;
-    for (int k = lane; k < parts; k += 32) {
-      const float m = ((k ? part1 + 2 * k * stride : part0) + row)[D];
-      s_w[w][k] = m;
-      M = fmaxf(M, m);
-    }
+  const float* part0 = a.part + (2 * (int64_t)c0 + 1) * stride + r * (D + 4);
+  const float* part1 = a.part + 2 * (int64_t)c0 * stride + r * (D + 4);
+  const auto at = [&](int k) { return k ? part1 + 2 * k * stride : part0; };
+  const int c = lane % (D / 4) * 4;
+  float4 y[8];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float l = 0.0f;
-    for (int k = lane; k < parts; k += 32) {
-      const float lk = ((k ? part1 + 2 * k * stride : part0) + row)[D + 1], m = s_w[w][k];
-      const float e = m > -INFINITY ? ex2(m - M) : lk == 0.0f ? 0.0f : 1.0f;
-      s_w[w][k] = e;
-      l = fmaf(e, lk, l);
-    }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    __syncwarp();
-    if (lane < D / 4) {
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-      for (int k = 0; k < parts; ++k) {
-        const float4 y = *reinterpret_cast<const float4*>((k ? part1 + 2 * k * stride : part0) + row + lane * 4);
-        const float e = s_w[w][k];
-        v.x = fmaf(e, y.x, v.x); v.y = fmaf(e, y.y, v.y); v.z = fmaf(e, y.z, v.z); v.w = fmaf(e, y.w, v.w);
-      }
-      kd_store<D>(a, s.b, s.g, r, lane * 4, M, l, v);
-    }
-    __syncwarp();
+  for (int k = 0; k < 8; ++k)
+    if (k < parts) y[k] = *reinterpret_cast<const float4*>(at(k) + c);
+  float M = -INFINITY, l = 0.0f;
+  for (int k = lane; k < parts; k += 32) {
+    const float2 ml = *reinterpret_cast<const float2*>(at(k) + D);
+    // (the running maximum of the lane's own parts)
+    const float top = fmaxf(M, ml.x), ref = top > -INFINITY ? top : 0.0f;
+    l = l * ex2(M - ref) + ml.y * (ml.x > -INFINITY ? ex2(ml.x - ref) : ml.y == 0.0f ? 0.0f : 1.0f);
+    M = top;
+    s_w[w][k] = ml.x > -INFINITY ? ml.x : ml.y == 0.0f ? -INFINITY : NAN;
   }
+  float top = M;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float ref = top > -INFINITY ? top : 0.0f;
+  l *= ex2(M - ref);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  __syncwarp();
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int k0 = 0; k0 < parts; k0 += 8) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k0 && k0 + k < parts) y[k] = *reinterpret_cast<const float4*>(at(k0 + k) + c);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (k0 + k >= parts) continue;
+      const float e = ex2(s_w[w][k0 + k] - ref);
+      v[0] = fmaf(e, y[k].x, v[0]); v[1] = fmaf(e, y[k].y, v[1]); v[2] = fmaf(e, y[k].z, v[2]); v[3] = fmaf(e, y[k].w, v[3]);
+    }
+  }
+  if (lane < D / 4) kd_store<D>(a, s.b, s.g, r, c, top, l, make_float4(v[0], v[1], v[2], v[3]));
 }
 
 namespace {
@@ -1201,7 +1244,7 @@ cudaError_t launch_kv4_decode_t(Kv4DecodeArgs a, int ncta, cudaStream_t st) {
       cudaFuncSetAttribute(kv4_decode_kernel<D, RT, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   launch_pdl(kv4_decode_kernel<D, RT, E>, dim3(ncta), dim3(kKdThreads), smem, st, a);
-  if (ncta > 1 && !a.whole) launch_pdl(kv4_join_kernel<D>, dim3(ncta - 1), dim3(256), 0, st, a, ncta);
+  if (ncta > 1 && !a.whole) launch_pdl(kv4_join_kernel<D>, dim3(ncta - 1, (a.T * a.G + kKdJoinWarps - 1) / kKdJoinWarps), dim3(kKdJoinWarps * 32), 0, st, a, ncta);
   return cudaGetLastError();
 }
 template <int D, typename E>
