@@ -25,11 +25,13 @@
 //   sum_t p_t v_t = sum_t p_t m_t + sum_t (p_t Delta_t) n_t :
 // no code is ever converted or scaled.  A nibble in a zeroed 16-bit word is
 // already a half-precision number (n 2^-17 in bits 7..10), which matrix
-// instructions multiply exactly: eight key codes cost two shifts and four
-// ANDs.  The instructions line products up by their operands' exponents and
-// count leading zeros as digits, so nibbles stand as high as they can: at
-// bits 0..3 and 4..7 the 128K-token output was off by 2.3e-5, here by 1e-6
-// (values, whose errors weigh more, all at 7..10; half of the keys at 3..6).
+// instructions multiply exactly: eight codes cost four shifts and four ANDs.
+// The instructions line products up by their operands' exponents and count
+// leading zeros as digits, so nibbles stand as high as they can (at bits 0..3
+// and 4..7, two shifts less, the 128K-token output was off by 2.3e-5), and they
+// truncate their sums, so the small parts below have sums of their own.  Over
+// 40 random shapes the outputs' mean error against 64 bits is 0.9 times that
+// of the same attention in float32 (largest 2e-6).
 // The other operand, q_c Delta_c or p_t Delta_t, is scaled by a power of two
 // to the top of the half-precision range and split into two halves (22 bits:
 // a single one would leave 2^-12 of every score), and the products are
@@ -44,12 +46,12 @@
 // current one is merged.
 //
 // What bounds it: not the memory but the instructions of the consumer warps
-// (an eighth-KB block takes a warp 1300 to 1500, three warps on a scheduler
-// issue 0.45 to 0.51 a cycle, tensor pipe 22 to 28% busy).  One sequence of
-// 512K tokens in all, 8 KV heads, 4 query heads each: 131 us for 638 MB, 4.9
-// TB/s, 72% of the copy bandwidth (loads alone 104 us).  Batch of 64, up to 8K
-// tokens, 8 query heads each: 128 us for 369 MB, 2.9 TB/s.  Before the codes
-// went through the tensor cores those were 1250 and 1217 us.
+// (a block takes a warp 1200 to 1600; three warps on a scheduler issue 0.45 to
+// 0.51 a cycle, the tensor pipe is 22 to 28% busy).  Four sequences of 128K
+// tokens, 8 KV heads, 4 query heads each: 133 us for 638 MB, 4.8 TB/s, 71% of
+// the copy bandwidth (the loads alone 104 us).  Batch of 64, up to 8K tokens, 8
+// query heads each: 130 us for 369 MB, 2.8 TB/s.  Before the codes went through
+// the tensor cores those were 1250 and 1217 us.
 #include <cmath>
 #include <cuda_fp16.h>
 
@@ -108,7 +110,7 @@ struct KdStage {
 // 0.06 us a token).  With 16 units for an item and one for its incomplete
 // block the last CTA of that batch took 144 us where the mean was 119; a lead
 // of 8 and of 12 with lighter incomplete blocks took 133 and 131 us for the
-// call, this 128 (drafts of 16 rows 116, 117 and 120).
+// call, this 128 (drafts of 24 rows 116, 117 and 120).
 struct KdBatch {
   int64_t pref[kMaxB + 1];    // units of the sequences before b (pref[B]: all)
   int64_t len[kMaxB];
@@ -234,8 +236,7 @@ __device__ __forceinline__ void kd_store(const Kv4DecodeArgs& a, int b, int g, i
 // The query rows of an item in shared memory: row r starts at r (D + 16), its
 // channels in four pieces 4 floats apart (bank offsets, as for the bounds).
 // They are log2(e) / sqrt(d) q times a power of two that puts the row's
-// largest at 2^11 .. 2^12 (undone by s_inv[r]), odd channels times 1/16 more:
-// their codes stand 16 times higher in the operand.
+// largest at 2^11 .. 2^12 (undone by s_inv[r]).
 template <int D> __device__ __forceinline__ constexpr int kd_q(int r, int c) { return r * (D + 16) + c + c / (D / 4) * 4; }
 
 template <int D, int RT>
@@ -299,14 +300,14 @@ __device__ __forceinline__ void kd_step(KdState<D, RT>& st, const E* K, const E*
   bool cut = have < 8;                    // some row does not see some token
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    float even = 0.0f, odd = 0.0f;        // (odd channels of q carry 1/16)
+    float even = 0.0f, odd = 0.0f;
 #pragma unroll
     for (int i = 0; i < NC; i += 4) {
       const float4 q = *reinterpret_cast<const float4*>(s_q + kd_q<D>(r, tid * NC) + i);
       even = fmaf(k[i], q.x, even); odd = fmaf(k[i + 1], q.y, odd);
       even = fmaf(k[i + 2], q.z, even); odd = fmaf(k[i + 3], q.w, odd);
     }
-    s[r] = fmaf(odd, 16.0f, even) * s_inv[r];
+    s[r] = (even + odd) * s_inv[r];
     cut = cut || s_end[r] < pos + 8;
   }
 #pragma unroll
@@ -468,12 +469,18 @@ __device__ __forceinline__ unsigned half_pair_rz(float x, float y) {
   return r;
 }
 
-// Nibbles of a half word in bits 3..6 and 7..10: n 2^-21 and n 2^-17 (bit 10
-// is the lowest exponent bit, where the subnormal numbers go on as normal
-// ones of the same spacing)
-constexpr unsigned kNibA = 0x00780078u, kNibB = 0x07800780u;
+// A nibble of a half word in bits 7..10: n 2^-17 (bit 10 is the lowest exponent
+// bit, where the subnormal numbers go on as normal ones of the same spacing)
+constexpr unsigned kNib = 0x07800780u;
+// nibbles 2 z and 2 z + 1 of the half words of a and b
+__device__ __forceinline__ void kd_key_operand(unsigned a, unsigned b, int z, unsigned (&op)[4]) {
+  op[0] = (z ? a >> 1 : a << 7) & kNib;
+  op[1] = (z ? b >> 1 : b << 7) & kNib;
+  op[2] = (z ? a >> 5 : a << 3) & kNib;
+  op[3] = (z ? b >> 5 : b << 3) & kNib;
+}
 constexpr int kKdChains = 4;      // sums of values in turn
-constexpr float kKeyUnit = 2097152.0f, kValueUnit = 131072.0f;   // 2^21, 2^17
+constexpr float kCodeUnit = 131072.0f;   // 2^17
 
 // The state of a warp over the tensor-core blocks of an item.  Lane (gid =
 // lane / 4, tid = lane % 4) works on query row gid % RT (RT = 4: lanes with
@@ -551,7 +558,7 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
       f.xs = e >= -8 && e < 3 ? 1.0f : pow2i(min(max(-e, -100), 100));
       f.most = 8.0f / f.xs;
     }
-    const float c = kKeyUnit * f.qinv / f.xs;
+    const float c = kCodeUnit * f.qinv / f.xs;
     f.csA = __shfl_sync(0xffffffffu, c, 4 * ra);
     f.csB = __shfl_sync(0xffffffffu, c, 4 * ra + 4);
   }
@@ -561,14 +568,16 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
   // part = the rest), and sum_c q_c m_c beside it, in float32.  (RT = 4: the
   // lanes gid and gid + 4 take half of the channels of that each.)  Matrix
   // instructions truncate their sums: they start from zero.
-  float t[4][4];
+  float t[4][4], low[4][4];
   if (RT == 8) {
 #pragma unroll
-    for (int y = 0; y < 4; ++y) t[y][0] = t[y][1] = t[y][2] = t[y][3] = 0.0f;
+    for (int y = 0; y < 4; ++y) t[y][0] = t[y][1] = t[y][2] = t[y][3] = low[y][0] = low[y][1] = low[y][2] = low[y][3] = 0.0f;
   }
   float qm = 0.0f, qm1 = 0.0f;
   const unsigned cut = RT == 8 || gid >= 4 ? 0xffffe000u : 0u;
   if constexpr (RT == 4) {
+    // (the low part is truncated too: a quarter of a step more, to half of one, takes most of the bias away)
+    const float up = gid >= 4 ? 1.0f + 0x1p-12f : 1.0f;
     float x[NC];
 #pragma unroll
     for (int i = 0; i < NC; i += 4) {
@@ -589,7 +598,7 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float u = x[8 * w + e], v = x[8 * w + e + 4];
-        bq[w][e] = half_pair_rz(u - __uint_as_float(__float_as_uint(u) & cut), v - __uint_as_float(__float_as_uint(v) & cut));
+        bq[w][e] = half_pair_rz((u - __uint_as_float(__float_as_uint(u) & cut)) * up, (v - __uint_as_float(__float_as_uint(v) & cut)) * up);
       }
     }
 #pragma unroll
@@ -612,9 +621,10 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
         for (int z = 0; z < 2; ++z)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const unsigned a = z ? k[2 * y][w] >> 5 : k[2 * y][w] << 3, b = z ? k[2 * y + 1][w] >> 5 : k[2 * y + 1][w] << 3;
-            if (w == 0 && z == 0) mma_f16_first(t[pr + y], a & kNibA, b & kNibA, a & kNibB, b & kNibB, bq[w][2 * z], bq[w][2 * z + 1]);
-            else mma_f16(t[pr + y], a & kNibA, b & kNibA, a & kNibB, b & kNibB, bq[w][2 * z], bq[w][2 * z + 1]);
+            unsigned op[4];
+            kd_key_operand(k[2 * y][w], k[2 * y + 1][w], z, op);
+            if (w == 0 && z == 0) mma_f16_first(t[pr + y], op[0], op[1], op[2], op[3], bq[w][2 * z], bq[w][2 * z + 1]);
+            else mma_f16(t[pr + y], op[0], op[1], op[2], op[3], bq[w][2 * z], bq[w][2 * z + 1]);
           }
     }
   } else
@@ -641,7 +651,7 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
       for (int e = 0; e < 4; ++e) {
         const float u = x[8 * w + e], v = x[8 * w + e + 4];
         bq[0][w][e] = half_pair_rz(u, v);
-        bq[HL - 1][w][e] = half_pair_rz(u - __uint_as_float(__float_as_uint(u) & cut), v - __uint_as_float(__float_as_uint(v) & cut));
+        bq[HL - 1][w][e] = half_pair(u - __uint_as_float(__float_as_uint(u) & cut), v - __uint_as_float(__float_as_uint(v) & cut));
       }
     uint2 k[8];                          // rows gid, gid + 8 of the tiles
 #pragma unroll
@@ -653,19 +663,23 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
         unsigned op[4][4];
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          const unsigned ka = w ? k[2 * y].y : k[2 * y].x, kb = w ? k[2 * y + 1].y : k[2 * y + 1].x;
-          const unsigned a = z ? ka >> 5 : ka << 3, b = z ? kb >> 5 : kb << 3;
-          op[y][0] = a & kNibA; op[y][1] = b & kNibA; op[y][2] = a & kNibB; op[y][3] = b & kNibB;
+          kd_key_operand(w ? k[2 * y].y : k[2 * y].x, w ? k[2 * y + 1].y : k[2 * y + 1].x, z, op[y]);
         }
 #pragma unroll
-        for (int h = HL - 1; h >= 0; --h)
+        for (int y = 0; y < 4; ++y)      // (four independent sums in turn: one has to wait 31 cycles for its last)
+          mma_f16(low[y], op[y][0], op[y][1], op[y][2], op[y][3], bq[HL - 1][w][2 * z], bq[HL - 1][w][2 * z + 1]);
 #pragma unroll
-          for (int y = 0; y < 4; ++y)    // (four independent sums in turn: one has to wait 31 cycles for its last)
-            mma_f16(t[y], op[y][0], op[y][1], op[y][2], op[y][3], bq[h][w][2 * z], bq[h][w][2 * z + 1]);
+        for (int y = 0; y < 4; ++y) mma_f16(t[y], op[y][0], op[y][1], op[y][2], op[y][3], bq[0][w][2 * z], bq[0][w][2 * z + 1]);
       }
   }
+  if (RT == 8) {
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) t[y][k] += low[y][k];
+  }
   between();
-  qm = fmaf(qm1, 16.0f, qm) * f.qinv;    // (odd channels carry 1/16)
+  qm = (qm + qm1) * f.qinv;
   qm += __shfl_xor_sync(0xffffffffu, qm, 1);
   qm += __shfl_xor_sync(0xffffffffu, qm, 2);
   if (RT == 4) qm += __shfl_xor_sync(0xffffffffu, qm, 16);
@@ -822,8 +836,8 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
 #pragma unroll
       for (int z = 0; z < kKdChains; ++z) {
         const unsigned a = y < 2 ? v[2 * z].x : v[2 * z].y, b = y < 2 ? v[2 * z + 1].x : v[2 * z + 1].y;
-        op[z][0] = (y & 1 ? a >> 1 : a << 7) & kNibB; op[z][1] = (y & 1 ? b >> 1 : b << 7) & kNibB;
-        op[z][2] = ~(y & 1 ? a >> 5 : a << 3) & kNibB; op[z][3] = ~(y & 1 ? b >> 5 : b << 3) & kNibB;
+        op[z][0] = (y & 1 ? a >> 1 : a << 7) & kNib; op[z][1] = (y & 1 ? b >> 1 : b << 7) & kNib;
+        op[z][2] = ~(y & 1 ? a >> 5 : a << 3) & kNib; op[z][3] = ~(y & 1 ? b >> 5 : b << 3) & kNib;
       }
 #pragma unroll
       for (int h = HL - 1; h >= 0; --h)
@@ -861,7 +875,7 @@ __device__ __forceinline__ void kd_fast_store(KdFast<D, RT>& f, float* s_m, floa
     s_m[ra] = f.newA ? -INFINITY : f.rA; s_m[ra + 1] = f.newB ? -INFINITY : f.rB;
     s_l[ra] = f.lA; s_l[ra + 1] = f.lB;
   }
-  const float backA = f.svA == 0.0f ? 0.0f : kValueUnit / f.svA, backB = f.svB == 0.0f ? 0.0f : kValueUnit / f.svB;
+  const float backA = f.svA == 0.0f ? 0.0f : kCodeUnit / f.svA, backB = f.svB == 0.0f ? 0.0f : kCodeUnit / f.svB;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) {
     if (RT == 4) {
@@ -934,7 +948,7 @@ __device__ __forceinline__ void kd_queries(const Kv4DecodeArgs& a, const KdBatch
       const int e = top > 0.0f && top < INFINITY ? min(max(11 - exponent(top), -100), 100) : 0;
       const float up = pow2i(e);
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) q[kd_q<D>(r, lane * CPL) + c] = x[c] * (c & 1 ? 0.0625f * up : up);
+      for (int c = 0; c < CPL; ++c) q[kd_q<D>(r, lane * CPL) + c] = x[c] * up;
       if (lane == 0) {
         it.inv[r] = pow2i(-e);
         it.end[r] = t < sg.nq ? sg.n - sg.nq + t + 1 : 0;
@@ -1146,7 +1160,7 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
 // the next kernel takes this grid's end for the decode kernel's).  Weights and
 // the first eight parts are read at once: done one after the other, eight rows
 // to a CTA's eight warps in turn, the join took 10 us after a batch of 64 and
-// 17 after drafts of 16 rows.
+// 17 after drafts of 24 rows.
 constexpr int kKdJoinWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(kKdJoinWarps * 32) kv4_join_kernel(const Kv4DecodeArgs a, int ncta) {
