@@ -46,8 +46,8 @@
 // current one is merged.
 //
 // What bounds it: not the memory but the instructions of the consumer warps
-// (a block takes a warp 1200 to 1600; three warps on a scheduler issue 0.45 to
-// 0.51 a cycle, the tensor pipe is 22 to 28% busy).  Four sequences of 128K
+// (a block takes a warp about 1300, with 8 rows 1600; three warps on a scheduler
+// issue 0.47 to 0.54 a cycle, the tensor pipe is 21 to 33% busy).  Four sequences of 128K
 // tokens, 8 KV heads, 4 query heads each: 133 us for 638 MB, 4.8 TB/s, 71% of
 // the copy bandwidth (the loads alone 104 us).  Batch of 64, up to 8K tokens, 8
 // query heads each: 130 us for 369 MB, 2.8 TB/s.  Before the codes went through
@@ -99,7 +99,6 @@ struct KdStage {
   static constexpr int bytesK = B + 8 * PITCH;
   static constexpr int S = kBlock * D / 2;              // values: codes, then the token scales
   static constexpr int bytesV = S + kBlock * 8;
-  static constexpr int txK = kBlock * D / 2 + 8 * D, txV = kBlock * D / 2 + kBlock * 8;
 };
 
 // What the kernels know of the batch.  An item is one sequence and KV head.
