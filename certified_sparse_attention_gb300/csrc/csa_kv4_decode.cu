@@ -50,7 +50,7 @@
 // issue 0.47 to 0.54 a cycle, the tensor pipe is 21 to 33% busy).  Four sequences of 128K
 // tokens, 8 KV heads, 4 query heads each: 133 us for 638 MB, 4.8 TB/s, 71% of
 // the copy bandwidth (the loads alone 104 us).  Batch of 64, up to 8K tokens, 8
-// query heads each: 130 us for 369 MB, 2.8 TB/s.  Before the codes went through
+// query heads each: 128 us for 369 MB, 2.9 TB/s.  Before the codes went through
 // the tensor cores those were 1250 and 1217 us.
 #include <cmath>
 #include <cuda_fp16.h>
@@ -268,20 +268,26 @@ __device__ __forceinline__ void kd_floats(const __nv_bfloat16* p, float (&x)[CNT
   }
 }
 
-// One online-softmax step of a warp over `have` <= 8 full-precision tokens at
-// K, V (rows of D), the first at position pos.  Scores: lane (gid, tid) takes
-// token gid and the channels [tid D / 4, (tid + 1) D / 4) of every query row;
-// values: a lane takes the channels [lane D / 32, ...) of the state st, the
-// weights come through s_p ([8][RT] floats).  Row r sees positions below
+// One online-softmax step of a warp over `have` <= NT full-precision tokens at
+// K, V (rows of D), the first at position pos.  Scores: lane (gid,
+// tid) takes token gid and the channels [tid NC, (tid + 1) NC) of every query
+// row; values: a lane takes the channels [lane D / 32, ...) of the state st, the
+// weights come through s_p ([NT][RT] floats).  Row r sees positions below
 // s_end[r].
+//
+// With 8 rows four tokens to a step, so that more warps share a block's tokens
+// (batch of 64: 128 us, with eight 130; drafts of 24 rows 120 and 123); with 4
+// rows, where a step costs half, eight (one sequence of 1000 tokens: 12.5 us,
+// with four 14.4: some warps then have steps after their second block).
+template <int RT> constexpr int kKdStep = RT == 8 ? 4 : 8;
 template <int D, int RT, typename E>
 __device__ __forceinline__ void kd_step(KdState<D, RT>& st, const E* K, const E* V, int have, const float* s_q,
                                         const float* s_inv, const int64_t* s_end, int64_t pos, float* s_p) {
-  constexpr int CPL = D / 32, NC = D / 4;
-  const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
-  float vv[8][CPL];
+  constexpr int CPL = D / 32, NT = kKdStep<RT>, LPT = 32 / NT, NC = D / LPT;
+  const int lane = threadIdx.x & 31, gid = lane / LPT, tid = lane % LPT;
+  float vv[NT][CPL];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < NT; ++e) {
 #pragma unroll
     for (int c = 0; c < CPL; ++c) vv[e][c] = 0.0f;
     if (e < have) {
@@ -296,7 +302,7 @@ __device__ __forceinline__ void kd_step(KdState<D, RT>& st, const E* K, const E*
   }
   float k[NC], s[RT];
   kd_floats<NC>(K + (gid < have ? gid : 0) * D + tid * NC, k);
-  bool cut = have < 8;                    // some row does not see some token
+  bool cut = have < NT;                   // some row does not see some token
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     float even = 0.0f, odd = 0.0f;
@@ -307,12 +313,12 @@ __device__ __forceinline__ void kd_step(KdState<D, RT>& st, const E* K, const E*
       even = fmaf(k[i + 2], q.z, even); odd = fmaf(k[i + 3], q.w, odd);
     }
     s[r] = (even + odd) * s_inv[r];
-    cut = cut || s_end[r] < pos + 8;
+    cut = cut || s_end[r] < pos + NT;
   }
 #pragma unroll
-  for (int r = 0; r < RT; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], 1);
+  for (int m = 1; m < LPT; m <<= 1)
 #pragma unroll
-  for (int r = 0; r < RT; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], 2);
+    for (int r = 0; r < RT; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], m);
   float top[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
@@ -320,7 +326,7 @@ __device__ __forceinline__ void kd_step(KdState<D, RT>& st, const E* K, const E*
     top[r] = s[r];
   }
 #pragma unroll
-  for (int m = 4; m < 32; m <<= 1)
+  for (int m = LPT; m < 32; m <<= 1)
 #pragma unroll
     for (int r = 0; r < RT; ++r) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], m));
 #pragma unroll
@@ -333,11 +339,11 @@ __device__ __forceinline__ void kd_step(KdState<D, RT>& st, const E* K, const E*
     for (int c = 0; c < CPL; ++c) st.acc[r][c] *= old;
     // an unseen token is marked
     const bool seen = gid < have && pos + gid < s_end[r];
-    if (r * 4 / RT == tid) s_p[gid * RT + r] = seen ? ex2(s[r] - ref) : -1.0f;
+    if (r * LPT / RT == tid) s_p[gid * RT + r] = seen ? ex2(s[r] - ref) : -1.0f;
   }
   __syncwarp();
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < NT; ++e) {
     float p[RT];
 #pragma unroll
     for (int r = 0; r < RT; r += 4) {
@@ -1097,8 +1103,8 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
     // the incomplete block, if it is to be done here
     const int64_t p0 = it.seg.n / kBlock * kBlock;
     const int left = it.seg.left;
-    if (rows > 0 && 8 * (i - base) < left) {
-      // eight tokens at a time: the state moves on to lanes that hold channels
+    if (rows > 0 && kKdStep<RT> * (i - base) < left) {
+      // a few tokens at a time: the state moves on to lanes that hold channels
       __syncwarp();
       KdState<D, RT> st;
 #pragma unroll
@@ -1110,10 +1116,10 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
       __syncwarp();
       // (the teams go on in turn where the blocks ended; my_acc is free until
       // the state returns to it)
-      for (int t0 = 8 * (i - base); t0 < left; t0 += 8 * nteam) {
+      for (int t0 = kKdStep<RT> * (i - base); t0 < left; t0 += kKdStep<RT> * nteam) {
         const int64_t at = (it.seg.bg * kBlock + t0) * D;
         kd_step<D, RT, E>(st, reinterpret_cast<const E*>(a.c.Kt) + at, reinterpret_cast<const E*>(a.c.Vt) + at,
-                          min(8, left - t0), q, it.inv + r0, it.end + r0, p0 + t0, my_acc);
+                          min(kKdStep<RT>, left - t0), q, it.inv + r0, it.end + r0, p0 + t0, my_acc);
       }
       __syncwarp();
 #pragma unroll
