@@ -594,6 +594,8 @@ class DenseDecode:
 
 # ------------------------------------- rows before the cache, 4-bit cache
 
+# For inference: no gradient flows through these calls.
+
 # The checks below run on every call of a decode loop, where the calls of a
 # token take the device a few microseconds each: they look at each tensor's
 # shape, strides, type, device and address once.
