@@ -50,7 +50,7 @@
 // issue 0.47 to 0.54 a cycle, the tensor pipe is 21 to 33% busy).  Four sequences of 128K
 // tokens, 8 KV heads, 4 query heads each: 133 us for 638 MB, 4.8 TB/s, 71% of
 // the copy bandwidth (the loads alone 104 us).  Batch of 64, up to 8K tokens, 8
-// query heads each: 128 us for 369 MB, 2.9 TB/s.  Before the codes went through
+// query heads each: 126 us for 369 MB, 2.9 TB/s.  Before the codes went through
 // the tensor cores those were 1250 and 1217 us.
 #include <cmath>
 #include <cuda_fp16.h>
@@ -900,7 +900,10 @@ __device__ __forceinline__ void kd_fast_store(KdFast<D, RT>& f, float* s_m, floa
 }
 
 // The queries of an item and what else its warps need of it: filled by a
-// producer warp, an item ahead.
+// producer warp, four rows at a time, an item ahead; tiles of 8 by two, half of
+// the rows each (one took 12 us for 64 rows; drafts of 24 rows 114 us, with one
+// 121, the batch of 64 with 8 rows 126 and 128).
+template <int RT> constexpr int kKdQueryWarps = RT == 8 ? 2 : 1;
 struct KdItem {
   KdSeg seg;
   int64_t end[CSA_KV4_MAX_ROWS];    // row r sees positions below end[r]
@@ -909,10 +912,10 @@ struct KdItem {
 
 template <int D, int RT, typename E>
 __device__ __forceinline__ void kd_queries(const Kv4DecodeArgs& a, const KdBatch& batch, int64_t u0, int64_t u1,
-                                           KdItem* items, float* s_q, unsigned full, unsigned empty) {
+                                           KdItem* items, float* s_q, unsigned full, unsigned empty, int part) {
   constexpr int CPL = D / 32;
   const int lane = threadIdx.x & 31;
-  const int R = a.T * a.G, Rp = (R + RT - 1) / RT * RT;
+  const int R = a.T * a.G, Rp = (R + RT - 1) / RT * RT, per = Rp / kKdQueryWarps<RT>;
   int k = 0;
   bool dead = false;
   kd_trim(a, batch, u0, u1);
@@ -923,11 +926,11 @@ __device__ __forceinline__ void kd_queries(const Kv4DecodeArgs& a, const KdBatch
     if (dead) break;
     KdItem& it = items[buf];
     const KdSeg sg = kd_seg(a, batch, u, u1);
-    if (lane == 0) it.seg = sg;
+    if (lane == 0 && part == 0) it.seg = sg;
     const E* base = reinterpret_cast<const E*>(a.q) + sg.b * a.qs.b + (int64_t)sg.g * a.G * a.qs.h + lane * CPL;
     float* q = s_q + buf * kd_q<D>(Rp, 0);
 #pragma unroll 4
-    for (int r = 0; r < Rp; ++r) {
+    for (int r = part * per; r < (part + 1) * per; ++r) {
       const int t = r / a.G;
       float x[CPL];
 #pragma unroll
@@ -1011,7 +1014,7 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
     mbar_init(values.full + 8 * i, 33);
     mbar_init(values.empty + 8 * i, team);
     if (i < 2) {
-      mbar_init(item_full + 8 * i, 1);
+      mbar_init(item_full + 8 * i, kKdQueryWarps<RT>);
       mbar_init(item_empty + 8 * i, W);
     }
     fence_barrier_init();
@@ -1022,10 +1025,7 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
 
   if (w >= W) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kKdRegsProducer));
-    if (w == W) kd_produce<D>(a, batch, u0, u1, keys, true);
-    else if (w == W + 1) kd_produce<D>(a, batch, u0, u1, values, false);
-    else if (w == W + 2) kd_queries<D, RT, E>(a, batch, u0, u1, items, s_q, item_full, item_empty);
-    else if (blockIdx.x == 0) {
+    const auto report = [&]() {
       bool bad = false;
       for (int b = lane; b < a.B; b += 32) {
         bad |= a.len[b] < 0 || a.len[b] > a.n_max;
@@ -1034,6 +1034,19 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
       const unsigned any = __any_sync(0xffffffffu, bad);
       // (a wait that gives up flags the word two seconds later at the earliest)
       if (lane == 0) *a.status = any ? 8u : 0u;
+    };
+    // (one order of the branches for both made the consumers of 4 rows spill: the
+    // 128K-token batch took 144 us, not 134)
+    if constexpr (kKdQueryWarps<RT> == 1) {
+      if (w == W) kd_produce<D>(a, batch, u0, u1, keys, true);
+      else if (w == W + 1) kd_produce<D>(a, batch, u0, u1, values, false);
+      else if (w == W + 2) kd_queries<D, RT, E>(a, batch, u0, u1, items, s_q, item_full, item_empty, 0);
+      else if (blockIdx.x == 0) report();
+    } else {
+      if (blockIdx.x == 0 && w == W + 1) report();
+      if (w == W) kd_produce<D>(a, batch, u0, u1, keys, true);
+      else if (w == W + 1) kd_produce<D>(a, batch, u0, u1, values, false);
+      else kd_queries<D, RT, E>(a, batch, u0, u1, items, s_q, item_full, item_empty, w - W - 2);
     }
     return;
   }
