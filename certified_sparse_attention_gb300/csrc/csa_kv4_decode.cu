@@ -1236,7 +1236,8 @@ __global__ void __launch_bounds__(kKdJoinWarps * 32) kv4_join_kernel(const Kv4De
 namespace {
 
 // Items of up to this many blocks stay whole: two rounds of the warps over
-// them take less time than a second kernel.
+// them take less time than a second kernel (128 items, 8 rows each: 20.5 us at
+// 1500 tokens, 29.6 us at 1700, where they are cut).
 constexpr int64_t kKdWholeBlocks = 2 * kKdWarps;
 int kd_whole(const csa_shape* s) { return (s->n_max + kBlock - 1) / kBlock <= kKdWholeBlocks; }
 
