@@ -47,7 +47,7 @@
 //
 // What bounds it: not the memory but the instructions of the consumer warps
 // (a block takes a warp about 1300, with 8 rows 1600; three warps on a scheduler
-// issue 0.47 to 0.54 a cycle, the tensor pipe is 21 to 33% busy).  Four sequences of 128K
+// issue 0.48 to 0.54 a cycle, the tensor pipe is 21 to 34% busy).  Four sequences of 128K
 // tokens, 8 KV heads, 4 query heads each: 133 us for 638 MB, 4.8 TB/s, 71% of
 // the copy bandwidth (the loads alone 104 us).  Batch of 64, up to 8K tokens, 8
 // query heads each: 126 us for 369 MB, 2.9 TB/s.  Before the codes went through
