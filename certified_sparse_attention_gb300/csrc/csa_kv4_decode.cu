@@ -501,10 +501,36 @@ struct KdFast {
   float rA, rB;           // reference (running maximum, or up to 8 below it)
   float lA, lB, omA, omB;
   float svA, svB;         // scale of p_t Delta_t, a power of two (0: not set)
-  float wide;             // Delta_t up to which both hold
+  float wide;             // p_t Delta_t up to which both hold
   float o[D / 16][4];     // channels 16 i + gid (+ 8) x operand columns 2 tid, 2 tid + 1
   bool newA, newB;        // the row has seen no token yet
 };
+
+// The scale sv of a row's operands p_t Delta_t, from what is summed: the
+// largest of them, weights included, that the row has met since sv was set
+// lies in [2^5, 2^15) / sv, so the two halves' floor of 2^-25 is 2^-30 of it
+// or less.  (A scale from Delta_t alone cost a row up to 2^-9 of its output
+// beside a token of values 2^20 times larger at no weight.)
+constexpr int kKdScaleMin = -109, kKdScaleMax = 110;     // exponents of sv
+// first p_t Delta_t that sv is too large for, 2^15 / sv; below zero for sv = 0
+__device__ __forceinline__ float kd_scale_end(float sv) { return __uint_as_float(0x86800000u - __float_as_uint(sv)); }
+// sv fitted to a block whose largest p_t Delta_t is top; returns the sums' factor
+__device__ __forceinline__ float kd_scale_fit(float& sv, float top) {
+  if (!(top > 0.0f && top >= kd_scale_end(sv))) return 1.0f;
+  const float to = pow2i(min(max(5 - exponent(top), kKdScaleMin), kKdScaleMax));
+  const float up = sv == 0.0f ? 1.0f : __fdividef(to, sv);        // (powers of two: exact)
+  sv = to;
+  return up;
+}
+// The row's reference moves up by d, its sums shrink by e = 2^-d: sv follows.
+// Returns the sums' factor.
+__device__ __forceinline__ float kd_scale_follow(float& sv, float d, float e) {
+  if (e == 0.0f) sv = 0.0f;      // (nothing is left of the sums)
+  if (sv == 0.0f) return e;
+  const float up = pow2i(min((int)fminf(d, 120.0f), kKdScaleMax - exponent(sv)));
+  sv *= up;
+  return e * up;
+}
 
 template <int D, int RT>
 __device__ __forceinline__ void kd_fast_init(KdFast<D, RT>& f, const float* s_inv) {
@@ -514,7 +540,8 @@ __device__ __forceinline__ void kd_fast_init(KdFast<D, RT>& f, const float* s_in
   f.most = 0.0f;
   f.csA = f.csB = 0.0f;
   f.rA = f.rB = f.lA = f.lB = f.omA = f.omB = 0.0f;
-  f.svA = f.svB = f.wide = 0.0f;
+  f.svA = f.svB = 0.0f;
+  f.wide = kd_scale_end(0.0f);
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) f.o[i][0] = f.o[i][1] = f.o[i][2] = f.o[i][3] = 0.0f;
   f.newA = f.newB = true;
@@ -729,58 +756,56 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
       wide = fmaxf(wide, sc[y][k].y);
     }
   // The reference moves only when a score exceeds it by more than 8 (weights
-  // up to 2^8), and the value scale only when Delta_t does not fit (Delta_t sv
-  // up to 2^6): both are rare after the first block.
-  if (__builtin_expect(__any_sync(0xffffffffu, f.newA || f.newB || big > 8.0f || wide > f.wide), 0)) {
+  // up to 2^8), and the value scale only when it or a p_t Delta_t asks for
+  // it; the lane's largest weight times its largest step says that none does.
+  // Both are rare after the first block.
+  if (__builtin_expect(__any_sync(0xffffffffu, f.newA || f.newB || big > 8.0f || ex2(big) * wide >= f.wide), 0)) {
     float xA = -INFINITY, xB = -INFINITY, tA = 0.0f, tB = 0.0f;
 #pragma unroll
     for (int y = 0; y < 4; ++y)
 #pragma unroll
       for (int k = 0; k < TK; ++k) {
-        const float w = sc[y][k].y < INFINITY ? sc[y][k].y : 0.0f;
         xA = fmaxf(xA, t[y][2 * k]);
         xB = fmaxf(xB, t[y][2 * k + 1]);
-        if (!MASK || token(y, k) < endA) tA = fmaxf(tA, w);
-        if (!MASK || token(y, k) < endB) tB = fmaxf(tB, w);
       }
 #pragma unroll
     for (int m = (RT == 4 ? 2 : 4); m < 32; m <<= 1) {
       xA = fmaxf(xA, __shfl_xor_sync(0xffffffffu, xA, m));
       xB = fmaxf(xB, __shfl_xor_sync(0xffffffffu, xB, m));
-      tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, m));
-      tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, m));
     }
     // the references move up by dA, dB (a row's first tokens: to their maximum)
     const float dA = f.newA ? (xA > -INFINITY ? xA : 0.0f) : fmaxf(xA, 0.0f);
     const float dB = f.newB ? (xB > -INFINITY ? xB : 0.0f) : fmaxf(xB, 0.0f);
     const float eA = f.newA ? 1.0f : ex2(-dA), eB = f.newB ? 1.0f : ex2(-dB);
-    float upA = 1.0f, upB = 1.0f;
-    if (tA > 0.0f && (f.svA == 0.0f || tA * f.svA > 64.0f)) {
-      const float to = pow2i(min(max(5 - exponent(tA), -100), 100));   // Delta sv in [2^5, 2^6)
-      if (f.svA != 0.0f) upA = __fdividef(to, f.svA);                  // (powers of two: exact)
-      f.svA = to;
-    }
-    if (tB > 0.0f && (f.svB == 0.0f || tB * f.svB > 64.0f)) {
-      const float to = pow2i(min(max(5 - exponent(tB), -100), 100));
-      if (f.svB != 0.0f) upB = __fdividef(to, f.svB);
-      f.svB = to;
-    }
-    f.wide = f.svA == 0.0f || f.svB == 0.0f ? 0.0f : __fdividef(64.0f, fmaxf(f.svA, f.svB));
+    float upA = kd_scale_follow(f.svA, f.newA ? 0.0f : dA, eA), upB = kd_scale_follow(f.svB, f.newB ? 0.0f : dB, eB);
     f.lA *= eA; f.lB *= eB;
     f.omA *= eA; f.omB *= eB;
-    upA *= eA; upB *= eB;
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      f.o[i][0] *= upA; f.o[i][1] *= upB;
-      f.o[i][2] *= upA; f.o[i][3] *= upB;
-    }
     f.rA += dA; f.rB += dB;
     f.newA = f.newA && !(xA > -INFINITY);
     f.newB = f.newB && !(xB > -INFINITY);
 #pragma unroll
     for (int y = 0; y < 4; ++y)
 #pragma unroll
-      for (int k = 0; k < TK; ++k) { t[y][2 * k] -= dA; t[y][2 * k + 1] -= dB; }
+      for (int k = 0; k < TK; ++k) {
+        t[y][2 * k] -= dA;
+        t[y][2 * k + 1] -= dB;
+        const float wA = ex2(t[y][2 * k]) * sc[y][k].y, wB = ex2(t[y][2 * k + 1]) * sc[y][k].y;
+        if ((!MASK || token(y, k) < endA) && wA < INFINITY) tA = fmaxf(tA, wA);
+        if ((!MASK || token(y, k) < endB) && wB < INFINITY) tB = fmaxf(tB, wB);
+      }
+#pragma unroll
+    for (int m = (RT == 4 ? 2 : 4); m < 32; m <<= 1) {
+      tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, m));
+      tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, m));
+    }
+    upA *= kd_scale_fit(f.svA, tA);
+    upB *= kd_scale_fit(f.svB, tB);
+    f.wide = fminf(kd_scale_end(f.svA), kd_scale_end(f.svB));
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      f.o[i][0] *= upA; f.o[i][1] *= upB;
+      f.o[i][2] *= upA; f.o[i][3] *= upB;
+    }
   }
   // Weights and the second operand: column gid, token pairs.  The tokens gid +
   // 8 of a tile enter as 15 - n with the opposite sign, and with m + 15 Delta
@@ -798,7 +823,7 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
       f.lA += pA; f.lB += pB;
       const bool turned = RT == 8 ? k == 1 : upper;
       const float dl = sc[y][k].y, m = fmaf(dl, turned ? 15.0f : 0.0f, sc[y][k].x);
-      float wA = pA * (dl * (turned ? -f.svA : f.svA)), wB = pB * (dl * (turned ? -f.svB : f.svB));
+      float wA = pA * dl * (turned ? -f.svA : f.svA), wB = pB * dl * (turned ? -f.svB : f.svB);
       if (MASK) {
         // left out, not multiplied by zero
         if (token(y, k) >= endA) wA = 0.0f; else omA = fmaf(pA, m, omA);

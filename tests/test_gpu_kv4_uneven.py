@@ -1,0 +1,155 @@
+"""csa_kv4_decode on keys and values of very uneven sizes, against float64.
+
+Each row's error is bounded by what that row attends to, not by the largest
+key or value in sight.  With P_t the weights, mag_t the magnitude |m| + 15
+Delta of a token's value and S_t = sum_c |q_c| (|m_c| + 15 Delta_c) / sqrt d
+the one of its key's products (|v| and |k| in the incomplete block):
+  * a score is off by eps_t <= (2^-21 + 8 sqrt(d) 2^-24) S_t: products to 22
+    bits, d roundings of independent sign at eight standard deviations;
+  * that moves the output o by sum_t P_t x_t (v_t - o) over the sum of the
+    moved weights, x_t between +-(exp(eps_t) - 1): at most 2 sum_t P_t |x_t|
+    max_c |v_t - o| while sum_t P_t |x_t| <= 1/2;
+  * weights and sums over n tokens add (2^-20 + 8 sqrt(n) 2^-24) sum_t P_t
+    mag_t.
+"""
+import numpy as np
+import pytest
+
+from oracle import kv4
+from oracle.quantize import quantize_keys
+from tests.gpu_common import ensure_built
+
+pytestmark = pytest.mark.gpu
+BLOCK = 64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    ensure_built()
+
+
+def stands(k, v):
+    """What the cache of float32 rows k, v [n][d] stands for, and the
+    magnitudes of its keys [n][d] and values [n]."""
+    k, v = k.copy(), v.copy()
+    magk, magv = np.abs(k).astype(np.float64), np.abs(v).max(1).astype(np.float64)
+    w = len(k) // BLOCK * BLOCK
+    if w:
+        c, _, m, dl = quantize_keys(k[:w], w)
+        m, dl = np.repeat(m, BLOCK, 0), np.repeat(dl, BLOCK, 0)
+        k[:w] = kv4.stands_for(c, m, dl)
+        magk[:w] = np.abs(m).astype(np.float64) + 15.0 * dl
+        c, m, dl = kv4.quantize_values(v[:w])
+        v[:w] = kv4.stands_for(c, m[:, None], dl[:, None])
+        magv[:w] = np.abs(m).astype(np.float64) + 15.0 * dl
+    return k, v, magk, magv
+
+
+def decode(q, k, v):
+    """Output [T][G][d] of the library for q [T][G][d], k, v [n][d], float32."""
+    import torch
+    import certified_sparse_attention_gb300 as csa
+    dev = torch.device("cuda:0")
+    T, G, d = q.shape
+    n = len(k)
+    s = csa.make_shape(1, G, 1, d, n, "f32")
+    cache = csa.KV4Cache(s, dev)
+    to = lambda x: torch.from_numpy(np.ascontiguousarray(x, np.float32)).to(dev)
+    ln = torch.tensor([n], dtype=torch.int64, device=dev)
+    cache.append(to(k)[None, :, None], to(v)[None, :, None], ln)
+    op = csa.KV4Decode(s, dev, T)
+    o = op(to(q)[None], cache, ln)
+    assert csa.csa_check(op.ws) == 0
+    return o[0].double().cpu().numpy()
+
+
+def check(q, k, v):
+    """Every row within its own bound; returns the errors relative to the
+    rows' sum_t P_t mag_t, and those of float32 attention."""
+    o = decode(q, k, v)
+    T, G, d = q.shape
+    n = len(k)
+    ks, vs, magk, magv = stands(k, v)
+    mine, plain = [], []
+    for t in range(T):
+        seen = n - T + t + 1
+        for h in range(G):
+            x = q[t, h].astype(np.float64)
+            s = ks[:seen].astype(np.float64) @ x / np.sqrt(d)
+            p = np.exp(s - s.max())
+            p /= p.sum()
+            ref = p @ vs[:seen].astype(np.float64)
+            S = magk[:seen] @ np.abs(x) / np.sqrt(d)
+            with np.errstate(over="ignore"):
+                e = np.expm1((2.0 ** -21 + 8 * np.sqrt(d) * 2.0 ** -24) * S)
+            e = np.where(p == 0, 0.0, e)
+            A = p @ magv[:seen]
+            assert p @ e <= 0.5
+            away = np.abs(vs[:seen].astype(np.float64) - ref).max(1)
+            lim = 2 * (p @ (e * away)) + \
+                (2.0 ** -20 + 8 * np.sqrt(seen) * 2.0 ** -24) * A
+            err = np.abs(o[t, h] - ref).max()
+            assert err <= lim, (t, h, err / A, lim / A)
+            mine.append(err / A)
+            s = (ks[:seen] @ q[t, h]) / np.float32(np.sqrt(d))
+            p = np.exp(s - s.max())
+            plain.append(np.abs((p / p.sum()) @ vs[:seen] - ref).max() / A)
+    return max(mine), max(plain)
+
+
+SHAPES = [(4, 1), (8, 1), (4, 3), (8, 8)]      # G, T: tiles of 4 and of 8 rows, 1 to 8 of them
+
+
+def case(rng, G, T, d, n):
+    """Queries around u = (+-1)_c, keys and values around 0."""
+    u = np.where(rng.random(d) < 0.5, -1.0, 1.0)
+    q = (u + 0.1 * rng.normal(size=(T, G, d))).astype(np.float32)
+    k = (0.1 * rng.normal(size=(n, d))).astype(np.float32)
+    v = rng.normal(size=(n, d)).astype(np.float32)
+    return u, q, k, v
+
+
+@pytest.mark.parametrize("G,T", SHAPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("ratio", [2.0 ** 10, 2.0 ** 16, 2.0 ** 20])
+@pytest.mark.parametrize("large,at", [(3, 9), (3, 64 * 12 + 1), (64 * 11 + 5, 64 * 11 + 40),
+                                      (64 * 23 + 60, 64 * 23 + 2), (64 * 23 + 60, 0)])
+def test_values_of_tokens_that_do_not_count(G, T, d, ratio, large, at):
+    # every row attends to one token; another one, at a weight of e^-40, has
+    # values larger by the ratio: in the first, a later and the last whole
+    # block, the two in one block and apart
+    rng = np.random.default_rng([G, T, d, at])
+    u, q, k, v = case(rng, G, T, d, 64 * 24 + 7)
+    k[at] = (20.0 / np.sqrt(d)) * u
+    k[large] = -k[at]
+    v[large] *= ratio
+    check(q, k, v)
+
+
+@pytest.mark.parametrize("G,T", SHAPES)
+def test_values_shrink_and_grow_along_the_sequence(G, T):
+    # every block's values 2^6 smaller than the one's before (then larger),
+    # while the scores rise (fall) by as much, so that all of them count
+    rng = np.random.default_rng([G, T])
+    d, n = 64, 64 * 16 + 3
+    u, q, k, v = case(rng, G, T, d, n)
+    step = np.minimum(np.arange(n) // BLOCK, 15) - 7.5
+    for sign in (1.0, -1.0):
+        kk = k + (sign * step[:, None] * 6 * np.log(2.0) / np.sqrt(d)) * u
+        vv = v * (2.0 ** (-6 * sign * step))[:, None]
+        check(q, kk.astype(np.float32), vv.astype(np.float32))
+
+
+@pytest.mark.parametrize("G,T", SHAPES)
+@pytest.mark.parametrize("scale", [2.0 ** -98, 2.0 ** -40, 2.0 ** 40, 2.0 ** 96])
+def test_values_of_one_size_that_jump_once(G, T, scale):
+    # constant rows (no step) in the first blocks, then values of any size
+    rng = np.random.default_rng([G, T, 5])
+    d, n = 64, 64 * 20
+    _, q, k, v = case(rng, G, T, d, n)
+    v *= np.float32(scale)
+    v[:64 * 13] = np.float32(0.5 * scale)
+    check(q, k, v)
