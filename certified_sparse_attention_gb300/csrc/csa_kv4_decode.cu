@@ -463,7 +463,7 @@ __device__ __forceinline__ unsigned half_rest(float x, float y, unsigned hi) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
   return half_pair(x - f.x, y - f.y);
 }
-// 2^k, |k| <= 126
+// 2^k, -126 <= k <= 127
 __device__ __forceinline__ float pow2i(int k) { return __int_as_float((127 + k) << 23); }
 // exponent of x > 0 (subnormals: -127)
 __device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
@@ -496,7 +496,9 @@ constexpr float kCodeUnit = 131072.0f;   // 2^17
 template <int D, int RT>
 struct KdFast {
   float qinv;             // undoes the scale of the lane's row
-  float xs, most;         // scale of Delta_c, a power of two; Delta up to which it holds (0: not set)
+  float xs;               // scale of the lane's row's q_c Delta_c, a power of two
+  float most;             // Delta_c from which some row's may be too large
+  int at;                 // where a block holds Delta_c of the lane's row's largest q_c
   float csA, csB;         // unit of the code sums of rows ra, ra + 1
   float rA, rB;           // reference (running maximum, or up to 8 below it)
   float lA, lB, omA, omB;
@@ -532,13 +534,48 @@ __device__ __forceinline__ float kd_scale_follow(float& sv, float d, float e) {
   return e * up;
 }
 
+// The scale xs of a row's operands q_c Delta_c: the largest in a block lies in
+// [2, 2^15) / xs, so the two halves' floor of 2^-25 is 2^-26 of it or less.
+// A row's largest q_c lies in [2^11, 2^12) (kd_q), which says that without a
+// look at the products where no step of the block is 2^3 / xs or more and the
+// one of that channel is 2^-10 / xs or more: xs stays 1 for usual keys.
+// Otherwise this looks at them, row by row.  (A scale from the steps alone, kept
+// when they got smaller, lost every digit of the scores beside a channel of
+// large keys and small queries.)
+constexpr float kKdMost = 8.0f, kKdLeast = 0x1p-10f;
 template <int D, int RT>
-__device__ __forceinline__ void kd_fast_init(KdFast<D, RT>& f, const float* s_inv) {
-  const int lane = threadIdx.x & 31, gid = lane >> 2;
+__device__ __forceinline__ void kd_rescale(KdFast<D, RT>& f, const float* sq, const float* sd) {
+  float mx = 0.0f;
+#pragma unroll 1
+  for (int i = 0; i < D / 4; i += 4) {
+    const float4 q = *reinterpret_cast<const float4*>(sq + i), dl = *reinterpret_cast<const float4*>(sd + i);
+    mx = fmaxf(mx, fmaxf(fmaxf(fabsf(q.x * dl.x), fabsf(q.y * dl.y)), fmaxf(fabsf(q.z * dl.z), fabsf(q.w * dl.w))));
+  }
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  if (mx > 0.0f && mx < INFINITY && !(mx * f.xs >= 2.0f && mx * f.xs < 32768.0f)) {
+    const int e = exponent(mx);
+    f.xs = e >= 1 && e < 15 ? 1.0f : pow2i(min(max(11 - e, -120), 120));
+  }
+  const float high = __uint_as_float(__reduce_max_sync(0xffffffffu, mx > 0.0f ? __float_as_uint(f.xs) : 0u));
+  if (mx == 0.0f && high > 0.0f) f.xs = high;       // (a row of zeros, for instance a padded one)
+  f.most = high > 0.0f ? kKdMost / high : kKdMost;
+  const float c = pow2i(min(max(17 + exponent(f.qinv) - exponent(f.xs), -126), 127));
+  const int ra = 2 * (threadIdx.x % 4 % (RT / 2));
+  f.csA = __shfl_sync(0xffffffffu, c, 4 * ra);
+  f.csB = __shfl_sync(0xffffffffu, c, 4 * ra + 4);
+}
+
+template <int D, int RT>
+__device__ __forceinline__ void kd_fast_init(KdFast<D, RT>& f, const float* s_inv, const int* s_top) {
+  const int lane = threadIdx.x & 31, gid = lane >> 2, ra = 2 * (lane % 4 % (RT / 2));
   f.qinv = s_inv[gid % RT];
   f.xs = 1.0f;
-  f.most = 0.0f;
-  f.csA = f.csB = 0.0f;
+  f.most = kKdMost;
+  // (within the block also when a wait gave up and nobody filled the item in)
+  f.at = (int)(min((unsigned)s_top[gid % RT], (unsigned)KdStage<D>::bytesK - 4) & ~3u);
+  f.csA = kCodeUnit * s_inv[ra];
+  f.csB = kCodeUnit * s_inv[ra + 1];
   f.rA = f.rB = f.lA = f.lB = f.omA = f.omB = 0.0f;
   f.svA = f.svB = 0.0f;
   f.wide = kd_scale_end(0.0f);
@@ -569,10 +606,6 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
   const float* sq = s_q + kd_q<D>(gid % RT, tid * NC);
   const float* sm = reinterpret_cast<const float*>(st + St::B + tid * St::PITCH);
   const float* sd = reinterpret_cast<const float*>(st + St::B + (4 + tid) * St::PITCH);
-  // Keep q_c Delta_c (q below 2^12) below 2^15: steps between 2^-8 and 2^3
-  // need no scale of their own.  (Steps that get smaller later keep an
-  // absolute error of the score that only shrinks.)  The lanes check 4 (2)
-  // steps each.
   float top;
   if (D == 128) {
     const float4 dl = *reinterpret_cast<const float4*>(st + St::B + (4 + (lane >> 3)) * St::PITCH + (lane & 7) * 16);
@@ -581,19 +614,8 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
     const float2 dl = *reinterpret_cast<const float2*>(st + St::B + (4 + (lane >> 3)) * St::PITCH + (lane & 7) * 8);
     top = fmaxf(dl.x, dl.y);
   }
-  if (__builtin_expect(__any_sync(0xffffffffu, top >= f.most), 0)) {
-    float t = top < INFINITY ? top : 0.0f;
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, m));
-    if (t > 0.0f && t >= f.most) {
-      const int e = exponent(t);
-      f.xs = e >= -8 && e < 3 ? 1.0f : pow2i(min(max(-e, -100), 100));
-      f.most = 8.0f / f.xs;
-    }
-    const float c = kCodeUnit * f.qinv / f.xs;
-    f.csA = __shfl_sync(0xffffffffu, c, 4 * ra);
-    f.csB = __shfl_sync(0xffffffffu, c, 4 * ra + 4);
-  }
+  const float own = *reinterpret_cast<const float*>(st + f.at);
+  if (__builtin_expect(__any_sync(0xffffffffu, top >= f.most || own * f.xs < kKdLeast), 0)) kd_rescale<D, RT>(f, sq, sd);
   // Scores of the four tiles of 16 tokens, two code words (16 channels of a
   // lane) at a time: q_c Delta_c as the operand (column gid, channel pairs (8
   // w + 0, 4), (1, 5), (2, 6), (3, 7); high part = the leading 11 bits, low
@@ -933,6 +955,7 @@ struct KdItem {
   KdSeg seg;
   int64_t end[CSA_KV4_MAX_ROWS];    // row r sees positions below end[r]
   float inv[CSA_KV4_MAX_ROWS];      // undoes the scale of row r (kd_q)
+  int top[CSA_KV4_MAX_ROWS];        // where a block holds Delta_c of the largest of row r
 };
 
 template <int D, int RT, typename E>
@@ -970,19 +993,23 @@ __device__ __forceinline__ void kd_queries(const Kv4DecodeArgs& a, const KdBatch
           x[0] = v.x; x[1] = v.y;
         }
       }
-      float top = 0.0f;
+      // the row's largest in magnitude, without its last 7 bits, and its channel
+      unsigned key = 0;
 #pragma unroll
       for (int c = 0; c < CPL; ++c) {
         x[c] *= a.rs;
-        top = fmaxf(top, fabsf(x[c]));
+        key = max(key, (__float_as_uint(x[c]) & 0x7fffff80u) + lane * CPL + c);
       }
 #pragma unroll
-      for (int m = 1; m < 32; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+      for (int m = 1; m < 32; m <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, m));
+      const float top = __uint_as_float(key & ~127u);
       const int e = top > 0.0f && top < INFINITY ? min(max(11 - exponent(top), -100), 100) : 0;
       const float up = pow2i(e);
 #pragma unroll
       for (int c = 0; c < CPL; ++c) q[kd_q<D>(r, lane * CPL) + c] = x[c] * up;
       if (lane == 0) {
+        const int c = key & 127;
+        it.top[r] = KdStage<D>::B + (4 + c / (D / 4)) * KdStage<D>::PITCH + c % (D / 4) * 4;
         it.inv[r] = pow2i(-e);
         it.end[r] = t < sg.nq ? sg.n - sg.nq + t + 1 : 0;
       }
@@ -1108,7 +1135,7 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
     float* my_acc = s_acc + w * RT * D;
     {
       KdFast<D, RT> f;
-      kd_fast_init<D, RT>(f, it.inv + r0);
+      kd_fast_init<D, RT>(f, it.inv + r0, it.top + r0);
       const int to = base + it.seg.nfast, clear = base + it.seg.clear;
       while (my_team < nteam && i < to) {
         if (!dead && !mbar_wait(keys.full + 8 * sk, pk)) dead = true;

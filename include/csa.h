@@ -425,8 +425,11 @@ size_t csa_kv4_workspace_size(const csa_shape* shape, int T);
  * every sequence (T = 1: a decode step; more: drafted tokens or a short
  * chunk): o = softmax(q K^T / sqrt d) V with K, V the values the cache stands
  * for; token t of sequence b, at position len[b] - n_q[b] + t, attends to
- * the positions up to its own.  Softmax statistics and sums in float32;
- * keys and values up to 2^100 in magnitude (sums of larger ones overflow).
+ * the positions up to its own.  Softmax statistics and sums in float32; a
+ * score's products q_c k_c are held to about 2^-22 of the block's largest
+ * |q_c| (|m_c| + 15 Delta_c) (a channel that is constant over the block has
+ * Delta_c = 1), the weighted values likewise.  Queries, keys and values up to
+ * 2^100 in magnitude (sums of larger ones overflow).
  *   q    device [B][T][Hq][d], type `dtype`, strides qs
  *   len  device [B] int64, 0 <= len[b] <= n_max, its tokens appended already
  *   n_q  device [B] int64, or NULL: T each

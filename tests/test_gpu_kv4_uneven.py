@@ -153,3 +153,47 @@ def test_values_of_one_size_that_jump_once(G, T, scale):
     v *= np.float32(scale)
     v[:64 * 13] = np.float32(0.5 * scale)
     check(q, k, v)
+
+
+@pytest.mark.parametrize("G,T", SHAPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("first", [True, False])
+def test_keys_large_where_the_query_is_small(G, T, d, first):
+    # a channel of keys around 2^30 against a query of 2^-30 there, or of 0,
+    # in the first block only or in all of them
+    rng = np.random.default_rng([G, T, d])
+    n = 64 * 15 + 9
+    for small in (2.0 ** -30, 0.0):
+        _, q, k, v = case(rng, G, T, d, n)
+        k *= 8
+        k[:64 if first else n, 5] *= np.float32(2.0 ** 30)
+        q[..., 5] = small
+        check(q, k, v)
+
+
+@pytest.mark.parametrize("G,T", SHAPES)
+@pytest.mark.parametrize("scale", [2.0 ** -60, 2.0 ** -24, 2.0 ** -9, 2.0 ** 9, 2.0 ** 24, 2.0 ** 60])
+def test_keys_of_any_size_with_channels_of_zeros(G, T, scale):
+    # heads padded with zeros (whose step is 1), queries that make up for the
+    # size of the keys; keys that get smaller on the way
+    rng = np.random.default_rng([G, T, 3])
+    d, n = 64, 64 * 15
+    for shrink in (1.0, 2.0 ** -20):
+        _, q, k, v = case(rng, G, T, d, n)
+        k *= 8 * scale
+        k[64 * 7:] *= shrink
+        q /= scale
+        k[:, 40:] = 0
+        q[..., 40:] = 0
+        check(q, k.astype(np.float32), v)
+
+
+def test_queries_of_very_different_sizes_share_a_tile():
+    # rows of one tile from 2^-40 to 2^40, and rows of zeros
+    rng = np.random.default_rng(3)
+    for G, T in SHAPES:
+        _, q, k, v = case(rng, G, T, 64, 64 * 9 + 2)
+        k *= np.float32(2.0 ** -40)
+        q *= (2.0 ** np.linspace(-40, 40, T * G)).reshape(T, G, 1).astype(np.float32)
+        q[0, G // 2] = 0
+        check(q, k, v)
