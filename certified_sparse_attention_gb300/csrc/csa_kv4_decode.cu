@@ -737,14 +737,16 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
   qm += __shfl_xor_sync(0xffffffffu, qm, 1);
   qm += __shfl_xor_sync(0xffffffffu, qm, 2);
   if (RT == 4) qm += __shfl_xor_sync(0xffffffffu, qm, 16);
-  const float sA = __shfl_sync(0xffffffffu, qm, 4 * ra) - f.rA, sB = __shfl_sync(0xffffffffu, qm, 4 * ra + 4) - f.rB;
-  // The scores relative to rA, rB.  RT = 4: the two parts are added; the lane
+  const float sA = __shfl_sync(0xffffffffu, qm, 4 * ra), sB = __shfl_sync(0xffffffffu, qm, 4 * ra + 4);
+  // The scores.  (Not yet relative to rA, rB: the difference is rounded to the
+  // digits of the larger, and a reference that is about to move may be far
+  // from the scores.)  RT = 4: the two parts are added; the lane
   // has token 16 y + gid (+ 8 in the upper lanes), rows ra, ra + 1, in
   // t[y][0], t[y][1]; RT = 8: tokens gid and gid + 8 in t[y][0..1], t[y][2..3].
   constexpr int TK = RT == 8 ? 2 : 1;    // tokens of a tile in a lane
   const auto token = [&](int y, int k) { return 16 * y + gid + (RT == 8 ? 8 * k : upper ? 8 : 0); };
   float2 sc[4][TK];                      // token scales
-  float big = -INFINITY, wide = 0.0f;
+  float xA = -INFINITY, xB = -INFINITY, wide = 0.0f;
 #pragma unroll
   for (int y = 0; y < 4; ++y) {
     if (RT == 4) {
@@ -774,44 +776,38 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
   for (int y = 0; y < 4; ++y)
 #pragma unroll
     for (int k = 0; k < TK; ++k) {
-      big = fmaxf(big, fmaxf(t[y][2 * k], t[y][2 * k + 1]));
+      xA = fmaxf(xA, t[y][2 * k]);
+      xB = fmaxf(xB, t[y][2 * k + 1]);
       wide = fmaxf(wide, sc[y][k].y);
     }
   // The reference moves only when a score exceeds it by more than 8 (weights
   // up to 2^8), and the value scale only when it or a p_t Delta_t asks for
   // it; the lane's largest weight times its largest step says that none does.
   // Both are rare after the first block.
+  const float big = fmaxf(xA - f.rA, xB - f.rB);
   if (__builtin_expect(__any_sync(0xffffffffu, f.newA || f.newB || big > 8.0f || ex2(big) * wide >= f.wide), 0)) {
-    float xA = -INFINITY, xB = -INFINITY, tA = 0.0f, tB = 0.0f;
-#pragma unroll
-    for (int y = 0; y < 4; ++y)
-#pragma unroll
-      for (int k = 0; k < TK; ++k) {
-        xA = fmaxf(xA, t[y][2 * k]);
-        xB = fmaxf(xB, t[y][2 * k + 1]);
-      }
+    float tA = 0.0f, tB = 0.0f;
 #pragma unroll
     for (int m = (RT == 4 ? 2 : 4); m < 32; m <<= 1) {
       xA = fmaxf(xA, __shfl_xor_sync(0xffffffffu, xA, m));
       xB = fmaxf(xB, __shfl_xor_sync(0xffffffffu, xB, m));
     }
-    // the references move up by dA, dB (a row's first tokens: to their maximum)
-    const float dA = f.newA ? (xA > -INFINITY ? xA : 0.0f) : fmaxf(xA, 0.0f);
-    const float dB = f.newB ? (xB > -INFINITY ? xB : 0.0f) : fmaxf(xB, 0.0f);
-    const float eA = f.newA ? 1.0f : ex2(-dA), eB = f.newB ? 1.0f : ex2(-dB);
-    float upA = kd_scale_follow(f.svA, f.newA ? 0.0f : dA, eA), upB = kd_scale_follow(f.svB, f.newB ? 0.0f : dB, eB);
+    // the references move up to the maximum
+    const float nA = f.newA ? (xA > -INFINITY ? xA : 0.0f) : fmaxf(f.rA, xA);
+    const float nB = f.newB ? (xB > -INFINITY ? xB : 0.0f) : fmaxf(f.rB, xB);
+    const float dA = f.newA ? 0.0f : nA - f.rA, dB = f.newB ? 0.0f : nB - f.rB;
+    const float eA = ex2(-dA), eB = ex2(-dB);
+    float upA = kd_scale_follow(f.svA, dA, eA), upB = kd_scale_follow(f.svB, dB, eB);
     f.lA *= eA; f.lB *= eB;
     f.omA *= eA; f.omB *= eB;
-    f.rA += dA; f.rB += dB;
+    f.rA = nA; f.rB = nB;
     f.newA = f.newA && !(xA > -INFINITY);
     f.newB = f.newB && !(xB > -INFINITY);
 #pragma unroll
     for (int y = 0; y < 4; ++y)
 #pragma unroll
       for (int k = 0; k < TK; ++k) {
-        t[y][2 * k] -= dA;
-        t[y][2 * k + 1] -= dB;
-        const float wA = ex2(t[y][2 * k]) * sc[y][k].y, wB = ex2(t[y][2 * k + 1]) * sc[y][k].y;
+        const float wA = ex2(t[y][2 * k] - nA) * sc[y][k].y, wB = ex2(t[y][2 * k + 1] - nB) * sc[y][k].y;
         if ((!MASK || token(y, k) < endA) && wA < INFINITY) tA = fmaxf(tA, wA);
         if ((!MASK || token(y, k) < endB) && wB < INFINITY) tB = fmaxf(tB, wB);
       }
@@ -841,7 +837,7 @@ __device__ __forceinline__ void kd_fast_block(KdFast<D, RT>& f, const uint8_t* s
     unsigned hi[TK], lo[TK];
 #pragma unroll
     for (int k = 0; k < TK; ++k) {
-      const float pA = ex2(t[y][2 * k]), pB = ex2(t[y][2 * k + 1]);
+      const float pA = ex2(t[y][2 * k] - f.rA), pB = ex2(t[y][2 * k + 1] - f.rB);
       f.lA += pA; f.lB += pB;
       const bool turned = RT == 8 ? k == 1 : upper;
       const float dl = sc[y][k].y, m = fmaf(dl, turned ? 15.0f : 0.0f, sc[y][k].x);

@@ -197,3 +197,17 @@ def test_queries_of_very_different_sizes_share_a_tile():
         q *= (2.0 ** np.linspace(-40, 40, T * G)).reshape(T, G, 1).astype(np.float32)
         q[0, G // 2] = 0
         check(q, k, v)
+
+
+@pytest.mark.parametrize("G,T", SHAPES)
+@pytest.mark.parametrize("low", [2.0 ** 10, 2.0 ** 14, 2.0 ** 18])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_after_blocks_of_very_low_ones(G, T, low, d):
+    # the first half of the blocks score about -low throughout; the two tokens
+    # that every row attends to (one code apart) lie in one block after them
+    rng = np.random.default_rng([G, T, d])
+    u, q, k, v = case(rng, G, T, d, 64 * 23 + 7)
+    k[:64 * 12] -= ((low / np.sqrt(d)) * u).astype(np.float32)
+    k[64 * 13 + 3] = (20.0 / np.sqrt(d)) * u
+    k[64 * 13 + 40] = (18.6 / np.sqrt(d)) * u
+    check(q, k, v)
