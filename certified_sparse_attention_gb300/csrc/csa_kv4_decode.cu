@@ -1302,7 +1302,11 @@ size_t kd_workspace(const csa_shape* s, int T) {
   return 256 + (kd_whole(s) ? 0 : (size_t)2 * kd_ctas(s) * R * (s->d + 4) * 4);
 }
 
-constexpr int kKdSharedBytes = 232448 - (int)sizeof(KdBatch) - 64;
+// Dynamic shared memory there can be: a CTA's 227 KB without the kernel's own.
+// The limit is set to this on every call, whatever the call needs: it belongs to
+// the function, and another host thread's call may lie between the setting and
+// the launch.
+constexpr int kKdSharedBytes = 232448 - ((int)sizeof(KdBatch) + 127) / 128 * 128;
 template <int D, int RT, typename E>
 cudaError_t launch_kv4_decode_t(Kv4DecodeArgs a, int ncta, cudaStream_t st) {
   const int rest = KdLayout<D, RT>::ring(a.T * a.G);
@@ -1322,7 +1326,7 @@ cudaError_t launch_kv4_decode_t(Kv4DecodeArgs a, int ncta, cudaStream_t st) {
   a.slotsV = nv * nteam;
   const int smem = rest + a.slotsK * K + a.slotsV * V;
   const cudaError_t e =
-      cudaFuncSetAttribute(kv4_decode_kernel<D, RT, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      cudaFuncSetAttribute(kv4_decode_kernel<D, RT, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKdSharedBytes);
   if (e != cudaSuccess) return e;
   launch_pdl(kv4_decode_kernel<D, RT, E>, dim3(ncta), dim3(kKdThreads), smem, st, a);
   if (ncta > 1 && !a.whole) launch_pdl(kv4_join_kernel<D>, dim3(ncta - 1, (a.T * a.G + kKdJoinWarps - 1) / kKdJoinWarps), dim3(kKdJoinWarps * 32), 0, st, a, ncta);
