@@ -211,3 +211,17 @@ def test_scores_after_blocks_of_very_low_ones(G, T, low, d):
     k[64 * 13 + 3] = (20.0 / np.sqrt(d)) * u
     k[64 * 13 + 40] = (18.6 / np.sqrt(d)) * u
     check(q, k, v)
+
+
+def test_errors_next_to_those_of_float32_attention():
+    # operands in two halves keep 22 bits for 24, and matrix instructions
+    # truncate where float32 rounds: four times two
+    rng = np.random.default_rng(40)
+    mine = plain = 0.0
+    for _ in range(12):
+        G, T = SHAPES[rng.integers(len(SHAPES))]
+        d, n = int(rng.choice([64, 128])), int(rng.integers(64, 3000))
+        _, q, k, v = case(rng, G, T, d, n)
+        a, b = check(q, 8 * k, v)
+        mine, plain = mine + a, plain + b
+    assert mine <= 8 * plain, mine / plain
