@@ -109,7 +109,8 @@ class csa_norm_rope(ctypes.Structure):
 class csa_kv4(ctypes.Structure):
     _fields_ = [("K4", ctypes.c_void_p), ("bounds", ctypes.c_void_p),
                 ("V4", ctypes.c_void_p), ("vscale", ctypes.c_void_p),
-                ("Kt", ctypes.c_void_p), ("Vt", ctypes.c_void_p)]
+                ("Kt", ctypes.c_void_p), ("Vt", ctypes.c_void_p),
+                ("refused", ctypes.c_void_p)]
 
 
 _lib = None
@@ -766,7 +767,10 @@ class KV4Cache:
     shape: K4, bounds, V4, vscale of the whole blocks of 64 tokens, Kt, Vt
     the rows of the incomplete last one.  buffers: those six tensors, in
     that order, instead of new ones.  ``status`` is the device word
-    csa_check reads after append or unpack."""
+    csa_check reads after append or unpack, which each set it anew;
+    ``refused`` the one an append that had to leave a sequence out flags and
+    nothing clears (``refused.zero_()`` does): checked at any later time,
+    csa_check(cache.refused) tells whether every append went in."""
 
     def __init__(self, shape: csa_shape, device, buffers=None):
         import torch
@@ -782,6 +786,7 @@ class KV4Cache:
                   ("vscale", (B, H, nblk * BLOCK, 2), torch.float32),
                   ("Kt", (B, H, BLOCK, d), el), ("Vt", (B, H, BLOCK, d), el))
         self.status = torch.zeros(4, dtype=torch.int32, device=device)
+        self.refused = torch.zeros(4, dtype=torch.int32, device=device)
         self.device = self.status.get_device()
         if buffers is None:
             buffers = [torch.zeros(size, dtype=dt, device=device)
@@ -800,7 +805,7 @@ class KV4Cache:
             t = t.view(size)
             at.append(_whole(t, name, size, dt, self.device))
             setattr(self, name, t)
-        self.desc = csa_kv4(*at)
+        self.desc = csa_kv4(*at, self.refused.data_ptr())
         _settled(self.device)
 
     def append(self, k, v, lens_dev, n_new=None, stream=None) -> None:

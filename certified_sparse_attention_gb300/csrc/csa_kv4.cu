@@ -59,10 +59,14 @@ __device__ __forceinline__ unsigned code4(float x, float m, float step) {
 }
 constexpr int kKv4Threads = 256;
 
-// the status word of a call: set by one warp of its first CTA
-__device__ __forceinline__ void report_range(unsigned* status, bool bad) {
+// the status word of a call and the word that keeps refusals (either may be
+// null): set by one warp of its first CTA
+__device__ __forceinline__ void report_range(unsigned* status, unsigned* refused, bool bad) {
   const unsigned any = __any_sync(0xffffffffu, bad);
-  if ((threadIdx.x & 31) == 0) *status = any ? 8u : 0u;
+  if ((threadIdx.x & 31) == 0) {
+    if (status) *status = any ? 8u : 0u;
+    if (refused && any) *refused = 8u;
+  }
 }
 
 // Codes of CPL values, each on top of kCodeBase.  Where the step is in the normal range the
@@ -222,13 +226,13 @@ __global__ void __launch_bounds__(kKv4Threads, sizeof(E) == 2 ? 3 : 2) kv4_appen
   __shared__ __align__(16) unsigned s_v[8][D];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int g = blockIdx.y, b = blockIdx.z;
-  if (a.status && blockIdx.x == 0 && g == 0 && b == 0 && tid < 32) {
+  if ((a.status || a.c.refused) && blockIdx.x == 0 && g == 0 && b == 0 && tid < 32) {
     bool bad = false;
     for (int i = tid; i < a.B; i += 32) {
       const int64_t n = a.len[i], m = a.n_new ? a.n_new[i] : a.T;
       bad |= m < 0 || m > a.T || n < m || n > a.n_max;
     }
-    report_range(a.status, bad);
+    report_range(a.status, a.c.refused, bad);
   }
   const int64_t n = a.len[b], m = a.n_new ? a.n_new[b] : (int64_t)a.T;
   if (m <= 0 || m > a.T || n < m || n > a.n_max) return;
@@ -400,7 +404,7 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_unpack_kernel(const Kv4Unpack
       const int64_t n = a.len[i], f = a.first ? a.first[i] : 0;
       bad |= n < 0 || n > a.n_max || f < 0;
     }
-    report_range(a.status, bad);
+    report_range(a.status, nullptr, bad);
   }
   const int64_t n = a.len[b], first = a.first ? a.first[b] : 0;
   if (n < 0 || n > a.n_max || first < 0 || first >= n) return;
@@ -514,7 +518,8 @@ cudaError_t launch_unpack(const Kv4UnpackArgs& a, dim3 grid, cudaStream_t st) {
 
 bool kv4_cache_ok(const csa_kv4* c) {
   return c && c->K4 && c->bounds && c->V4 && c->vscale && c->Kt && c->Vt && aligned16(c->K4) && aligned16(c->bounds) &&
-         aligned16(c->V4) && aligned16(c->vscale) && aligned16(c->Kt) && aligned16(c->Vt);
+         aligned16(c->V4) && aligned16(c->vscale) && aligned16(c->Kt) && aligned16(c->Vt) &&
+         ((uintptr_t)c->refused & 3) == 0;
 }
 
 }  // namespace csa

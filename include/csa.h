@@ -390,6 +390,10 @@ typedef struct {
   float* vscale;
   void* Kt;
   void* Vt;
+  uint32_t* refused;   /* NULL, or a device word that csa_kv4_append sets to the */
+                       /* flag of CSA_ERR_INVALID_ARG when a sequence is out of  */
+                       /* range, and that no call clears: a refusal stays there, */
+                       /* whatever is called next, until the caller sets it to 0 */
 } csa_kv4;
 
 /* Appends n_new[b] <= T tokens to every sequence; len[b] counts them already
@@ -398,7 +402,7 @@ typedef struct {
  *   k, v   device [B][T][Hkv][d] with strides ks, vs; rows t >= n_new[b] are
  *          not read
  *   len, n_new, status: as in csa_qk_norm_rope (len <= n_max); a sequence
- *          out of range is left as it was */
+ *          out of range is left as it was, and cache->refused says so too */
 csa_status csa_kv4_append(const csa_shape* shape, const csa_kv4* cache, int T,
                           const void* k, const csa_strides* ks, const void* v,
                           const csa_strides* vs, const int64_t* len,
@@ -512,7 +516,7 @@ csa_status csa_profile_read(csa_phase_times* out);
  * `workspace` by the last csa_decode_step, csa_decode_step_device,
  * csa_dense_decode or csa_kv4_decode that used it, or in the status word of
  * the last csa_qk_norm_rope, csa_kv4_append or csa_kv4_unpack that was given
- * this address: CSA_OK, CSA_ERR_NONFINITE, CSA_ERR_WORKSPACE,
+ * this address (a csa_kv4's `refused`: of all appends since it was 0): CSA_OK, CSA_ERR_NONFINITE, CSA_ERR_WORKSPACE,
  * CSA_ERR_TIMEOUT (a bounded wait of a kernel gave up) or
  * CSA_ERR_INVALID_ARG (a device length out of range); or CSA_ERR_CUDA if the
  * stream reports an error. */

@@ -392,3 +392,15 @@ def test_rotation_keeps_norms_and_relative_angles():
                    np.linalg.norm(q)) < 1e-12
     ones = kv4.norm_rope(q, np.ones(32), 0.0, 0, [], False)
     assert abs(np.mean(ones ** 2) - 1) < 1e-12
+
+
+def test_word_of_refusals_is_checked(lib):
+    for bad in (FAKE + 1, FAKE + 2):
+        c = cache(refused=bad)
+        assert csa.csa_kv4_append(shape(), c, 4, FAKE, strides(heads=2), FAKE,
+                                  strides(heads=2), FAKE, None, None,
+                                  0) == INVALID
+        assert csa.csa_kv4_unpack(shape(), c, 10, None, FAKE, FAKE, FAKE, None,
+                                  0) == INVALID
+        assert csa.csa_kv4_decode(shape(), c, 4, FAKE, strides(), FAKE, None,
+                                  FAKE, None, FAKE, 1 << 40, 0) == INVALID
