@@ -11,6 +11,8 @@ the one of its key's products (|v| and |k| in the incomplete block):
     max_c |v_t - o| while sum_t P_t |x_t| <= 1/2;
   * weights and sums over n tokens add (2^-20 + 8 sqrt(n) 2^-24) sum_t P_t
     mag_t.
+The logarithm of the sum of weights is off by at most 2 sum_t P_t |x_t| + 2^-20
++ 8 sqrt(n) 2^-24, and its own roundings.
 """
 import numpy as np
 import pytest
@@ -48,28 +50,36 @@ def stands(k, v):
     return k, v, magk, magv
 
 
-def decode(q, k, v):
-    """Output [T][G][d] of the library for q [T][G][d], k, v [n][d], float32."""
+def decode(q, k, v, dtype):
+    """Output [T][G][d] and lse [T][G] of the library for q [T][G][d], k, v
+    [n][d], float32 arrays of values of the type."""
     import torch
     import certified_sparse_attention_gb300 as csa
     dev = torch.device("cuda:0")
     T, G, d = q.shape
     n = len(k)
-    s = csa.make_shape(1, G, 1, d, n, "f32")
+    s = csa.make_shape(1, G, 1, d, n, dtype)
     cache = csa.KV4Cache(s, dev)
-    to = lambda x: torch.from_numpy(np.ascontiguousarray(x, np.float32)).to(dev)
+    el = torch.bfloat16 if dtype == "bf16" else torch.float32
+    to = lambda x: torch.from_numpy(np.ascontiguousarray(x, np.float32)).to(dev).to(el)
     ln = torch.tensor([n], dtype=torch.int64, device=dev)
     cache.append(to(k)[None, :, None], to(v)[None, :, None], ln)
-    op = csa.KV4Decode(s, dev, T)
+    op = csa.KV4Decode(s, dev, T, with_lse=True)
     o = op(to(q)[None], cache, ln)
     assert csa.csa_check(op.ws) == 0
-    return o[0].double().cpu().numpy()
+    return o[0].double().cpu().numpy(), op.lse[0].double().cpu().numpy()
 
 
-def check(q, k, v):
+def bf16(x):
+    """float32 values rounded to bf16."""
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(x, np.float32)).bfloat16().float().numpy()
+
+
+def check(q, k, v, dtype="f32"):
     """Every row within its own bound; returns the errors relative to the
     rows' sum_t P_t mag_t, and those of float32 attention."""
-    o = decode(q, k, v)
+    o, lse = decode(q, k, v, dtype)
     T, G, d = q.shape
     n = len(k)
     ks, vs, magk, magv = stands(k, v)
@@ -93,6 +103,9 @@ def check(q, k, v):
                 (2.0 ** -20 + 8 * np.sqrt(seen) * 2.0 ** -24) * A
             err = np.abs(o[t, h] - ref).max()
             assert err <= lim, (t, h, err / A, lim / A)
+            ls = s.max() + np.log(np.exp(s - s.max()).sum())
+            lim = 2 * (p @ e) + 2.0 ** -20 + 8 * np.sqrt(seen) * 2.0 ** -24 + 2.0 ** -22 * abs(ls)
+            assert abs(lse[t, h] - ls) <= lim, (t, h, lse[t, h], ls, lim)
             mine.append(err / A)
             s = (ks[:seen] @ q[t, h]) / np.float32(np.sqrt(d))
             p = np.exp(s - s.max())
@@ -225,3 +238,20 @@ def test_errors_next_to_those_of_float32_attention():
         a, b = check(q, 8 * k, v)
         mine, plain = mine + a, plain + b
     assert mine <= 8 * plain, mine / plain
+
+
+@pytest.mark.parametrize("G,T", SHAPES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_uneven_bf16(G, T, d):
+    # large values at no weight, a channel of large keys where the query is
+    # 0, and low blocks first, together, in 16 bits
+    rng = np.random.default_rng([G, T, d, 16])
+    u, q, k, v = case(rng, G, T, d, 64 * 22 + 30)
+    q[..., 7] = u[7] = 0.0
+    k[:64 * 11] -= ((2.0 ** 12 / np.sqrt(d)) * u).astype(np.float32)
+    k[64 * 15 + 8] = (20.0 / np.sqrt(d)) * u
+    k[64 * 15 + 44] = (18.0 / np.sqrt(d)) * u
+    k[::5, 7] *= 2.0 ** 24
+    k[64 * 15 + 50] = -k[64 * 15 + 8]
+    v[64 * 15 + 50] *= 2.0 ** 18
+    check(bf16(q), bf16(k), bf16(v), "bf16")
