@@ -29,29 +29,33 @@
 // The instructions line products up by their operands' exponents and count
 // leading zeros as digits, so nibbles stand as high as they can (at bits 0..3
 // and 4..7, two shifts less, the 128K-token output was off by 2.3e-5), and they
-// truncate their sums, so the small parts below have sums of their own.  Over
-// 40 random shapes the outputs' mean error against 64 bits is 0.9 times that
-// of the same attention in float32 (largest 2e-6).
+// truncate their sums, so the small parts below have sums of their own.
 // The other operand, q_c Delta_c or p_t Delta_t, is scaled by a power of two
 // to the top of the half-precision range and split into two halves (22 bits:
 // a single one would leave 2^-12 of every score), and the products are
-// summed in float32.  With up to 4 rows the two parts
-// fill the 8 columns of one instruction (m16n8k16: codes are the 16-row
-// side); with 8 rows each part takes an instruction.  The incomplete block
-// takes a plain path (kd_step).
+// summed in float32.  Each row has scales of its own, which follow the products
+// themselves (kd_rescale, kd_scale_fit): what a row does not attend to, and
+// channels that its query is small in, cost it no digits.  Over 40 random
+// shapes the outputs' error against 64 bits is 0.88 times that of the same
+// attention in float32 (mean of the ratios; the largest 2.0).  With up to 4
+// rows the two parts fill the 8 columns of one instruction (m16n8k16: codes are
+// the 16-row side); with 8 rows each part takes an instruction.  The incomplete
+// block takes a plain path (kd_step).
 //
 // Blocks come by bulk copies into two rings of shared memory, keys and values,
 // each slot on an mbarrier; producer warps run ahead over the items, so the
 // first blocks and the queries of the next item are on their way while the
 // current one is merged.
 //
-// What bounds it: not the memory but the instructions of the consumer warps
-// (a block takes a warp about 1300, with 8 rows 1600; three warps on a scheduler
-// issue 0.48 to 0.54 a cycle, the tensor pipe is 21 to 34% busy).  Four sequences of 128K
-// tokens, 8 KV heads, 4 query heads each: 133 us for 638 MB, 4.8 TB/s, 71% of
-// the copy bandwidth (the loads alone 104 us).  Batch of 64, up to 8K tokens, 8
-// query heads each: 126 us for 369 MB, 2.9 TB/s.  Before the codes went through
-// the tensor cores those were 1250 and 1217 us.
+// What bounds it: neither the memory (15 to 58% busy) nor the tensor pipe (21 to
+// 34%) nor the issue slots (48 to 54%), but latency: a block is a chain of about
+// 1300 instructions of its warp, with 8 rows 1600, and registers allow three
+// such warps to a scheduler.  (With d = 128, 8 rows spill 136 bytes a thread, 100
+// without the producers' code, and 4 rows of float32 queries 80.)  Four
+// sequences of 128K tokens, 8 KV heads, 4 query heads each: 136 us for 638 MB,
+// 4.7 TB/s, 69% of the copy bandwidth.  Batch of 64, up to 8K tokens, 8 query
+// heads each: 131 us for 369 MB, 2.8 TB/s.  Before the codes went through the
+// tensor cores those were 1250 and 1217 us.
 #include <cmath>
 #include <cuda_fp16.h>
 
@@ -109,7 +113,10 @@ struct KdStage {
 // 0.06 us a token).  With 16 units for an item and one for its incomplete
 // block the last CTA of that batch took 144 us where the mean was 119; a lead
 // of 8 and of 12 with lighter incomplete blocks took 133 and 131 us for the
-// call, this 128 (drafts of 24 rows 116, 117 and 120).
+// call, this 128 (drafts of 24 rows 116, 117 and 120).  The fit is that batch's,
+// twelve teams of one warp; larger teams, whose blocks weigh more beside an
+// item's own cost, have the same weights and would want a smaller lead.  An item
+// whose sequence has no query token (n_q = 0) is walked like any other.
 struct KdBatch {
   int64_t pref[kMaxB + 1];    // units of the sequences before b (pref[B]: all)
   int64_t len[kMaxB];
@@ -1283,9 +1290,20 @@ __global__ void __launch_bounds__(kKdJoinWarps * 32) kv4_join_kernel(const Kv4De
 
 namespace {
 
-// Items of up to this many blocks stay whole: two rounds of the warps over
-// them take less time than a second kernel (128 items, 8 rows each: 20.5 us at
-// 1500 tokens, 29.6 us at 1700, where they are cut).
+// Items of up to this many blocks stay whole: with tiles of one warp two rounds
+// of the twelve teams, which take less time than a second kernel where there are
+// items for most SMs.  Whole / cut, us, bf16, d = 128:
+//                     500 tokens    1000 tokens    1500 tokens
+//   128 items,  4 rows  14 / 19       15 / 22        19 / 25
+//               8 rows  16 / 25       19 / 27        22 / 30
+//              24 rows  31 / 40       37 / 47        44 / 51
+//              64 rows  79 / 96       99 / 116      116 / 128
+//     8 items,  4 rows  12 / 13       13 / 14        15 / 14
+//               8 rows  14 / 17       18 / 16        19 / 16
+//              24 rows  28 / 27       34 / 26        38 / 23
+//              64 rows  73 / 58       87 / 54       101 / 47
+// So the rule is right for a batch, and costs few items of many rows up to
+// twice their time: it knows neither the number of items nor that of teams.
 constexpr int64_t kKdWholeBlocks = 2 * kKdWarps;
 int kd_whole(const csa_shape* s) { return (s->n_max + kBlock - 1) / kBlock <= kKdWholeBlocks; }
 

@@ -367,8 +367,11 @@ csa_status csa_qk_norm_rope(const csa_shape* shape, int T,
  * token), values per token over their d channels: m = min, Delta = fl((max -
  * min) / 15), code = clamp(rint(fl(fl(v - m) / Delta)), 0, 15), all codes 0
  * where Delta = 0.  A code stands for fl(fl(code Delta) + m).  The rows of the
- * incomplete last block are kept as they are, until the block is whole.  A
- * NaN or infinity in a block makes everything its key channel, or its
+ * incomplete last block are kept as they are, until the block is whole: right
+ * after that even the newest token is held in 4 bits.  (Coarser than schemes
+ * that keep a window of recent tokens in full precision, or code a token's
+ * values in groups of channels: here one outlying channel sets the step of all
+ * d.)  A NaN or infinity in a block makes everything its key channel, or its
  * value's token, stands for NaN.
  *
  *   K4      [B][Hkv][nblk_max * 64][d/2]    as above
