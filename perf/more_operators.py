@@ -5,7 +5,7 @@ the chosen blocks (``csa_kv8_decode_blocks``).
 With ``own`` false, ``run`` computes an operator from elementary torch operations; with ``own`` true it makes the calls a user
 makes of the library.  Lengths live on the device, as in a decode loop replayed from a CUDA graph.
 
-The 8-bit cache of one (sequence, KV head), in blocks of 64 tokens.  A code is a sign bit (128) and a magnitude up to 127:
+The 8-bit cache of one (sequence, KV head), in blocks of 64 tokens.  Codes -127 .. 127 are held plus 128:
   K8      [8][d/64][8][64] per block: element (j, h, g, c) is token 16 (g / 2) + 2 j + g % 2, channel 64 h + c
   V8      [d][64] per block: row = channel
   scale   [2] per block: the step of its keys, that of its values (largest magnitude / 127)
@@ -228,14 +228,13 @@ def run(s):
 
 
 def _coded(c):
-    """Whole numbers -127 .. 127 as sign and magnitude."""
-    return torch.where(c < 0, 128 - c, c).to(torch.uint8)
+    """Whole numbers -127 .. 127 as the cache holds them."""
+    return (c + 128).to(torch.uint8)
 
 
 def _number(code):
     """... and back, in f32."""
-    c = code.float()
-    return torch.where(c >= 128, 128 - c, c)
+    return code.float() - 128
 
 
 def _step(top):
@@ -447,8 +446,7 @@ def _place(d):
 
 
 def _signed(code):
-    c = code.long()
-    return (c % 128 * (1 - 2 * (c // 128))).double()
+    return (code.long() - 128).double()
 
 
 def _exact_block(s, b, h, j):
@@ -498,7 +496,7 @@ def _exact_append(s):
                 y = c * step
                 if new is s["k"]:
                     ends = torch.stack([c.max(2).values, c.min(2).values], 2)
-                    flat[b, :, base // BLOCK:whole // BLOCK] = (ends.abs() + 128 * (ends < 0)).to(torch.uint8)
+                    flat[b, :, base // BLOCK:whole // BLOCK] = (ends + 128).to(torch.uint8)
             x = torch.cat([y.reshape(H, -1, d), left], 1)
             rows[b, :, :m] = x[:, r:]
             if n % BLOCK:
