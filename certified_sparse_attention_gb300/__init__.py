@@ -34,7 +34,9 @@ EXPORTED = ("csa_workspace_size", "csa_quantize_keys", "csa_decode_step",
             "csa_dense_decode_static", "csa_decode_step_device",
             "csa_quantize_keys8", "csa_decode_step_refined",
             "csa_rope_turns", "csa_qk_norm_rope", "csa_kv4_append",
-            "csa_kv4_unpack", "csa_kv4_workspace_size", "csa_kv4_decode")
+            "csa_kv4_unpack", "csa_kv4_workspace_size", "csa_kv4_decode",
+            "csa_kv8_append", "csa_kv8_unpack", "csa_kv8_workspace_size",
+            "csa_kv8_decode", "csa_kv8_select", "csa_kv8_decode_blocks")
 # size of the fixed scratch array behind csa_dense_decode_static
 DENSE_STATIC_SCRATCH_BYTES = 16 << 20
 STATS_FIELDS = 10
@@ -113,6 +115,13 @@ class csa_kv4(ctypes.Structure):
                 ("refused", ctypes.c_void_p)]
 
 
+class csa_kv8(ctypes.Structure):
+    _fields_ = [("K8", ctypes.c_void_p), ("V8", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("span", ctypes.c_void_p),
+                ("Kt", ctypes.c_void_p), ("Vt", ctypes.c_void_p),
+                ("refused", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -180,6 +189,28 @@ def load_library(path: str = LIB_PATH):
     lib.csa_kv4_decode.argtypes = [P(csa_shape), P(csa_kv4), ctypes.c_int, vp,
                                    P(csa_strides), vp, vp, vp, vp, vp, sz, vp]
     lib.csa_kv4_decode.restype = ctypes.c_int
+    lib.csa_kv8_append.argtypes = [P(csa_shape), P(csa_kv8), ctypes.c_int, vp,
+                                   P(csa_strides), vp, P(csa_strides), vp, vp,
+                                   vp, vp]
+    lib.csa_kv8_append.restype = ctypes.c_int
+    lib.csa_kv8_unpack.argtypes = [P(csa_shape), P(csa_kv8), ctypes.c_int64,
+                                   vp, vp, vp, vp, vp, vp]
+    lib.csa_kv8_unpack.restype = ctypes.c_int
+    lib.csa_kv8_workspace_size.argtypes = [P(csa_shape), ctypes.c_int,
+                                           ctypes.c_int]
+    lib.csa_kv8_workspace_size.restype = sz
+    lib.csa_kv8_decode.argtypes = [P(csa_shape), P(csa_kv8), ctypes.c_int, vp,
+                                   P(csa_strides), vp, vp, vp, vp, vp, sz, vp]
+    lib.csa_kv8_decode.restype = ctypes.c_int
+    lib.csa_kv8_select.argtypes = [P(csa_shape), P(csa_kv8), ctypes.c_int, vp,
+                                   P(csa_strides), vp, vp, ctypes.c_int,
+                                   ctypes.c_int, ctypes.c_int, vp, vp, vp, vp]
+    lib.csa_kv8_select.restype = ctypes.c_int
+    lib.csa_kv8_decode_blocks.argtypes = [P(csa_shape), P(csa_kv8),
+                                          ctypes.c_int, vp, P(csa_strides),
+                                          vp, vp, vp, vp, ctypes.c_int, vp,
+                                          vp, vp, sz, vp]
+    lib.csa_kv8_decode_blocks.restype = ctypes.c_int
     lib.csa_check.argtypes = [vp, vp]
     lib.csa_check.restype = ctypes.c_int
     lib.csa_workspace_layout.argtypes = [P(csa_shape), P(csa_params),
@@ -411,6 +442,55 @@ def csa_kv4_decode(shape, cache, T, q, qs, lens_dev, n_q, o, lse, workspace,
         ctypes.byref(shape), ctypes.byref(cache), int(T), _ptr(q),
         _ref(_strides(qs)), _ptr(lens_dev), _ptr(n_q), _ptr(o), _ptr(lse),
         _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def csa_kv8_append(shape, cache, T, k, ks, v, vs, lens_dev, n_new, status,
+                   stream=None) -> int:
+    """cache: csa_kv8; the other arguments as csa_qk_norm_rope."""
+    return load_library().csa_kv8_append(
+        ctypes.byref(shape), ctypes.byref(cache), int(T), _ptr(k),
+        _ref(_strides(ks)), _ptr(v), _ref(_strides(vs)), _ptr(lens_dev),
+        _ptr(n_new), _ptr(status), _stream(stream))
+
+
+def csa_kv8_unpack(shape, cache, rows, first, lens_dev, K, V, status,
+                   stream=None) -> int:
+    return load_library().csa_kv8_unpack(
+        ctypes.byref(shape), ctypes.byref(cache), int(rows), _ptr(first),
+        _ptr(lens_dev), _ptr(K), _ptr(V), _ptr(status), _stream(stream))
+
+
+def csa_kv8_workspace_size(shape: csa_shape, T: int = 1,
+                           n_sel: int = 0) -> int:
+    return int(load_library().csa_kv8_workspace_size(ctypes.byref(shape),
+                                                     int(T), int(n_sel)))
+
+
+def csa_kv8_decode(shape, cache, T, q, qs, lens_dev, n_q, o, lse, workspace,
+                   workspace_bytes, stream=None) -> int:
+    return load_library().csa_kv8_decode(
+        ctypes.byref(shape), ctypes.byref(cache), int(T), _ptr(q),
+        _ref(_strides(qs)), _ptr(lens_dev), _ptr(n_q), _ptr(o), _ptr(lse),
+        _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def csa_kv8_select(shape, cache, T, q, qs, lens_dev, n_q, n_sel, n_first,
+                   n_last, blocks, count, status, stream=None) -> int:
+    return load_library().csa_kv8_select(
+        ctypes.byref(shape), ctypes.byref(cache), int(T), _ptr(q),
+        _ref(_strides(qs)), _ptr(lens_dev), _ptr(n_q), int(n_sel),
+        int(n_first), int(n_last), _ptr(blocks), _ptr(count), _ptr(status),
+        _stream(stream))
+
+
+def csa_kv8_decode_blocks(shape, cache, T, q, qs, lens_dev, n_q, blocks,
+                          count, n_sel, o, lse, workspace, workspace_bytes,
+                          stream=None) -> int:
+    return load_library().csa_kv8_decode_blocks(
+        ctypes.byref(shape), ctypes.byref(cache), int(T), _ptr(q),
+        _ref(_strides(qs)), _ptr(lens_dev), _ptr(n_q), _ptr(blocks),
+        _ptr(count), int(n_sel), _ptr(o), _ptr(lse), _ptr(workspace),
+        int(workspace_bytes), _stream(stream))
 
 
 def csa_profile_enable(on: bool) -> int:
@@ -762,29 +842,19 @@ class QKNormRope:
         return q_out
 
 
-class KV4Cache:
-    """Device buffers of a K/V cache held in 4 bits (csa_kv4), for one
-    shape: K4, bounds, V4, vscale of the whole blocks of 64 tokens, Kt, Vt
-    the rows of the incomplete last one.  buffers: those six tensors, in
-    that order, instead of new ones.  ``status`` is the device word
-    csa_check reads after append or unpack, which each set it anew;
-    ``refused`` the one an append that had to leave a sequence out flags and
-    nothing clears (``refused.zero_()`` does): checked at any later time,
-    csa_check(cache.refused) tells whether every append went in."""
+class _CodedCache:
+    """A K/V cache held in codes: its device buffers, append and unpack, for
+    the classes below (which name the buffers, the descriptor and the entry
+    points)."""
 
     def __init__(self, shape: csa_shape, device, buffers=None):
         import torch
         self.shape = shape
-        if csa_kv4_workspace_size(shape, 1) == 0:
-            raise CsaError(2, "KV4Cache")
-        B, H, d = shape.B, shape.Hkv, shape.d
+        if not self._supported(shape):
+            raise CsaError(2, type(self).__name__)
+        self.dtype = _torch_type(shape)
         nblk = (shape.n_max + BLOCK - 1) // BLOCK
-        self.dtype = el = _torch_type(shape)
-        layout = (("K4", (B, H, nblk * BLOCK, d // 2), torch.uint8),
-                  ("bounds", (B, H, nblk, 2, d), torch.float32),
-                  ("V4", (B, H, nblk, d, BLOCK // 2), torch.uint8),
-                  ("vscale", (B, H, nblk * BLOCK, 2), torch.float32),
-                  ("Kt", (B, H, BLOCK, d), el), ("Vt", (B, H, BLOCK, d), el))
+        layout = self._layout(shape.B, shape.Hkv, nblk, shape.d)
         self.status = torch.zeros(4, dtype=torch.int32, device=device)
         self.refused = torch.zeros(4, dtype=torch.int32, device=device)
         self.device = self.status.get_device()
@@ -792,8 +862,9 @@ class KV4Cache:
             buffers = [torch.zeros(size, dtype=dt, device=device)
                        for _, size, dt in layout]
         if len(buffers) != len(layout):
-            raise ValueError("buffers: K4, bounds, V4, vscale, Kt and Vt "
-                             "are required")
+            names = [name for name, _, _ in layout]
+            raise ValueError(f"buffers: {', '.join(names[:-1])} and "
+                             f"{names[-1]} are required")
         at = []
         for (name, size, dt), t in zip(layout, buffers):
             n = 1
@@ -805,7 +876,7 @@ class KV4Cache:
             t = t.view(size)
             at.append(_whole(t, name, size, dt, self.device))
             setattr(self, name, t)
-        self.desc = csa_kv4(*at, self.refused.data_ptr())
+        self.desc = self._desc(*at, self.refused.data_ptr())
         _settled(self.device)
 
     def append(self, k, v, lens_dev, n_new=None, stream=None) -> None:
@@ -819,13 +890,13 @@ class KV4Cache:
         pv, vb, vt, vh = _rows(v, "v", B, T, H, d, dt, dev)
         pl = _counts(lens_dev, "lens_dev", B, dev)
         pn = _counts(n_new, "n_new", B, dev)
-        st = load_library().csa_kv4_append(
+        st = getattr(load_library(), self._append)(
             ctypes.byref(s), ctypes.byref(self.desc), T, pk,
             ctypes.byref(csa_strides(kb, kt, kh)), pv,
             ctypes.byref(csa_strides(vb, vt, vh)), pl, pn,
             self.status.data_ptr(), _call_stream(stream, dev))
         if st:
-            raise CsaError(st, "csa_kv4_append")
+            raise CsaError(st, self._append)
 
     def unpack(self, K, V, lens_dev, first=None, stream=None):
         """Read positions first[b] + i (None: from 0) below lens_dev[b] back
@@ -839,12 +910,60 @@ class KV4Cache:
         pV = _whole(V, "V", size, dt, dev)
         pl = _counts(lens_dev, "lens_dev", s.B, dev)
         pf = _counts(first, "first", s.B, dev)
-        st = load_library().csa_kv4_unpack(
+        st = getattr(load_library(), self._unpack)(
             ctypes.byref(s), ctypes.byref(self.desc), size[2], pf, pl, pK,
             pV, self.status.data_ptr(), _call_stream(stream, dev))
         if st:
-            raise CsaError(st, "csa_kv4_unpack")
+            raise CsaError(st, self._unpack)
         return K, V
+
+
+class KV4Cache(_CodedCache):
+    """Device buffers of a K/V cache held in 4 bits (csa_kv4), for one
+    shape: K4, bounds, V4, vscale of the whole blocks of 64 tokens, Kt, Vt
+    the rows of the incomplete last one.  buffers: those six tensors, in
+    that order, instead of new ones.  ``status`` is the device word
+    csa_check reads after append or unpack, which each set it anew;
+    ``refused`` the one an append that had to leave a sequence out flags and
+    nothing clears (``refused.zero_()`` does): checked at any later time,
+    csa_check(cache.refused) tells whether every append went in."""
+
+    _desc, _append, _unpack = csa_kv4, "csa_kv4_append", "csa_kv4_unpack"
+
+    @staticmethod
+    def _supported(shape):
+        return csa_kv4_workspace_size(shape, 1) != 0
+
+    def _layout(self, B, H, nblk, d):
+        import torch
+        u8, f32, el = torch.uint8, torch.float32, self.dtype
+        return (("K4", (B, H, nblk * BLOCK, d // 2), u8),
+                ("bounds", (B, H, nblk, 2, d), f32),
+                ("V4", (B, H, nblk, d, BLOCK // 2), u8),
+                ("vscale", (B, H, nblk * BLOCK, 2), f32),
+                ("Kt", (B, H, BLOCK, d), el), ("Vt", (B, H, BLOCK, d), el))
+
+
+class KV8Cache(_CodedCache):
+    """Device buffers of a K/V cache held in 8 bits (csa_kv8), for one
+    shape: K8, V8, scale, span of the whole blocks of 64 tokens, Kt, Vt the
+    rows of the incomplete last one; buffers, ``status`` and ``refused`` as
+    in KV4Cache."""
+
+    _desc, _append, _unpack = csa_kv8, "csa_kv8_append", "csa_kv8_unpack"
+
+    @staticmethod
+    def _supported(shape):
+        return csa_kv8_workspace_size(shape, 1) != 0
+
+    def _layout(self, B, H, nblk, d):
+        import torch
+        u8, el = torch.uint8, self.dtype
+        return (("K8", (B, H, nblk, 8, d // 64, 8, 64), u8),
+                ("V8", (B, H, nblk, d, BLOCK), u8),
+                ("scale", (B, H, nblk, 2), torch.float32),
+                ("span", (B, H, nblk, 2, d), u8),
+                ("Kt", (B, H, BLOCK, d), el), ("Vt", (B, H, BLOCK, d), el))
 
 
 class KV4Decode:
@@ -888,4 +1007,150 @@ class KV4Decode:
             self.ws_bytes, _call_stream(stream, dev))
         if st:
             raise CsaError(st, "csa_kv4_decode")
+        return self.o
+
+
+def _same_cache(shape: csa_shape, device: int, cache) -> None:
+    c = cache.shape if isinstance(cache, KV8Cache) else None
+    if c is None or c.B != shape.B or c.Hkv != shape.Hkv or \
+            c.d != shape.d or c.n_max != shape.n_max or \
+            c.dtype != shape.dtype or cache.device != device:
+        raise ValueError("cache: a KV8Cache of the same shape and device is "
+                         "required")
+
+
+class KV8Decode:
+    """Owns the workspace and outputs of csa_kv8_decode for one shape and up
+    to T query tokens per sequence: o [B][T][Hq][d] (float32) and, with
+    with_lse, lse [B][T][Hq].  One object serves one call at a time."""
+
+    def __init__(self, shape: csa_shape, device, T: int = 1,
+                 with_lse: bool = False):
+        import torch
+        self.shape, self.T = shape, int(T)
+        self.dtype = _torch_type(shape)
+        self.ws_bytes = csa_kv8_workspace_size(shape, self.T)
+        if self.ws_bytes == 0:
+            raise CsaError(2, "csa_kv8_workspace_size")
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+        self.device = self.ws.get_device()
+        self.o = torch.zeros((shape.B, self.T, shape.Hq, shape.d),
+                             dtype=torch.float32, device=device)
+        self.lse = (torch.zeros((shape.B, self.T, shape.Hq),
+                                dtype=torch.float32, device=device)
+                    if with_lse else None)
+        _settled(self.device)
+
+    def __call__(self, q, cache: KV8Cache, lens_dev, n_q=None, stream=None):
+        """q [B][T][Hq][d] (a view with strides of whole 16 bytes); lens_dev
+        and n_q: device int64 [B] (n_q None: T each).  Returns o."""
+        s, dev = self.shape, self.device
+        _same_cache(s, dev, cache)
+        pq, qb, qt, qh = _rows(q, "q", s.B, self.T, s.Hq, s.d, self.dtype,
+                               dev)
+        pl = _counts(lens_dev, "lens_dev", s.B, dev)
+        pn = _counts(n_q, "n_q", s.B, dev)
+        st = load_library().csa_kv8_decode(
+            ctypes.byref(s), ctypes.byref(cache.desc), self.T, pq,
+            ctypes.byref(csa_strides(qb, qt, qh)), pl, pn,
+            self.o.data_ptr(), _ptr(self.lse), self.ws.data_ptr(),
+            self.ws_bytes, _call_stream(stream, dev))
+        if st:
+            raise CsaError(st, "csa_kv8_decode")
+        return self.o
+
+
+class KV8Sparse:
+    """Attention over n_sel blocks of the 8-bit cache, chosen for each query
+    token and KV head by a cheap score (csa_kv8_select, csa_kv8_decode_blocks):
+    the first n_first blocks, the last n_last up to the token's own, and the
+    best of the others.  Owns the workspace and outputs for one shape and up to
+    T query tokens per sequence: blocks [B][T][Hkv][n_sel] and count
+    [B][T][Hkv] (int32), o [B][T][Hq][d] (float32) and, with with_lse, lse
+    [B][T][Hq].  One object serves one call at a time.  ``status`` is the
+    device word csa_check reads after select, ``ws`` the one after attend."""
+
+    def __init__(self, shape: csa_shape, device, n_sel: int, T: int = 1,
+                 n_first: int = 1, n_last: int = 2, with_lse: bool = False):
+        import torch
+        self.shape, self.T, self.n_sel = shape, int(T), int(n_sel)
+        self.n_first, self.n_last = int(n_first), int(n_last)
+        if self.n_first < 0 or self.n_last < 1 or \
+                self.n_first + self.n_last > self.n_sel:
+            raise ValueError("n_first >= 0, n_last >= 1 and n_first + n_last "
+                             "<= n_sel are required")
+        self.dtype = _torch_type(shape)
+        self.ws_bytes = csa_kv8_workspace_size(shape, self.T, self.n_sel)
+        if self.ws_bytes == 0:
+            raise CsaError(2, "csa_kv8_workspace_size")
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+        self.device = self.ws.get_device()
+        B, Hq, H, n = shape.B, shape.Hq, shape.Hkv, self.n_sel
+        self.status = torch.zeros(4, dtype=torch.int32, device=device)
+        self.blocks = torch.zeros((B, self.T, H, n), dtype=torch.int32,
+                                  device=device)
+        self.count = torch.zeros((B, self.T, H), dtype=torch.int32,
+                                 device=device)
+        self.o = torch.zeros((B, self.T, Hq, shape.d), dtype=torch.float32,
+                             device=device)
+        self.lse = (torch.zeros((B, self.T, Hq), dtype=torch.float32,
+                                device=device) if with_lse else None)
+        _settled(self.device)
+
+    def _inputs(self, q, cache, lens_dev, n_q):
+        s, dev = self.shape, self.device
+        _same_cache(s, dev, cache)
+        pq, qb, qt, qh = _rows(q, "q", s.B, self.T, s.Hq, s.d, self.dtype,
+                               dev)
+        return (ctypes.byref(s), ctypes.byref(cache.desc), self.T, pq,
+                ctypes.byref(csa_strides(qb, qt, qh)),
+                _counts(lens_dev, "lens_dev", s.B, dev),
+                _counts(n_q, "n_q", s.B, dev))
+
+    def _select(self, args, stream) -> None:
+        st = load_library().csa_kv8_select(
+            *args, self.n_sel, self.n_first, self.n_last,
+            self.blocks.data_ptr(), self.count.data_ptr(),
+            self.status.data_ptr(), stream)
+        if st:
+            raise CsaError(st, "csa_kv8_select")
+
+    def _attend(self, args, blocks: int, count: int, stream) -> None:
+        st = load_library().csa_kv8_decode_blocks(
+            *args, blocks, count, self.n_sel, self.o.data_ptr(),
+            _ptr(self.lse), self.ws.data_ptr(), self.ws_bytes, stream)
+        if st:
+            raise CsaError(st, "csa_kv8_decode_blocks")
+
+    def __call__(self, q, cache: KV8Cache, lens_dev, n_q=None, stream=None):
+        """select and attend: arguments as in KV8Decode.  Returns o."""
+        args = self._inputs(q, cache, lens_dev, n_q)
+        on = _call_stream(stream, self.device)
+        self._select(args, on)
+        self._attend(args, self.blocks.data_ptr(), self.count.data_ptr(), on)
+        return self.o
+
+    def select(self, q, cache: KV8Cache, lens_dev, n_q=None, stream=None):
+        """The choice alone.  Returns (blocks, count)."""
+        self._select(self._inputs(q, cache, lens_dev, n_q),
+                     _call_stream(stream, self.device))
+        return self.blocks, self.count
+
+    def attend(self, q, cache: KV8Cache, lens_dev, n_q=None, blocks=None,
+               count=None, stream=None):
+        """The attention alone, over the blocks last chosen, or over the
+        caller's lists: blocks int32 [B][T][Hkv][n_sel], of which count (int32
+        [B][T][Hkv]) are read, ascending, each at most once and none past the
+        token's own (the rows of a list that is not so are NaN).  Returns o."""
+        args = self._inputs(q, cache, lens_dev, n_q)
+        if (blocks is None) != (count is None):
+            raise ValueError("blocks and count: both or none are required")
+        pb, pc = self.blocks.data_ptr(), self.count.data_ptr()
+        if blocks is not None:
+            import torch
+            pb = _whole(blocks, "blocks", self.blocks.shape, torch.int32,
+                        self.device)
+            pc = _whole(count, "count", self.count.shape, torch.int32,
+                        self.device)
+        self._attend(args, pb, pc, _call_stream(stream, self.device))
         return self.o

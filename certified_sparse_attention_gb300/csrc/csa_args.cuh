@@ -195,6 +195,7 @@ inline bool strides_ok(const csa_strides* s, int64_t unit, int B, int T, int hea
   return s && (B == 1 || s->b % unit == 0) && (T == 1 || s->t % unit == 0) && (heads == 1 || s->h % unit == 0);
 }
 bool kv4_cache_ok(const csa_kv4* c);            // arrays present and aligned
+bool kv8_cache_ok(const csa_kv8* c);
 
 // Unique id of the calling thread's current CUDA context (the driver's
 // cuCtxGetId, reached through the runtime's driver entry points, so that the

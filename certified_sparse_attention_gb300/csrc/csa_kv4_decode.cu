@@ -57,28 +57,10 @@
 // heads each: 131 us for 369 MB, 2.8 TB/s.  Before the codes went through the
 // tensor cores those were 1250 and 1217 us.
 #include <cmath>
-#include <cuda_fp16.h>
 
-#include "csa_args.cuh"
+#include "csa_decode.cuh"
 
 namespace csa {
-
-struct Kv4DecodeArgs {
-  csa_kv4 c;
-  const void* q;
-  csa_strides qs;
-  const int64_t* len;
-  const int64_t* n_q;
-  float* o;
-  float* lse;
-  unsigned* status;
-  float* part;          // [2 * CTAs][rows][D + 4]: acc[D], m, l, unused
-  int64_t n_max, nblk_max;
-  int B, T, Hq, Hkv, G;
-  int whole;            // items are not cut: one unit each
-  int slotsK, slotsV;   // slots of the two rings: multiples of the number of teams
-  float rs;             // log2(e) / sqrt(d): scores in units of log 2
-};
 
 constexpr int kKdWarps = 12;      // consumer warps of a CTA: three warpgroups; a fourth
                                   // one's warps send for the blocks and the queries
@@ -105,282 +87,27 @@ struct KdStage {
   static constexpr int bytesV = S + kBlock * 8;
 };
 
-// What the kernels know of the batch.  An item is one sequence and KV head.
-// Its units of work, in order: kKdLead for its own cost (its queries, the
-// merge), its whole blocks, and what its incomplete block costs.  The weights
-// follow fits to the times of single CTAs (batch of 64, 8 query heads to a KV
-// head: a block 0.30 us, an item 3.8 to 4.6 us, an incomplete block 1.7 us and
-// 0.06 us a token).  With 16 units for an item and one for its incomplete
-// block the last CTA of that batch took 144 us where the mean was 119; a lead
-// of 8 and of 12 with lighter incomplete blocks took 133 and 131 us for the
-// call, this 128 (drafts of 24 rows 116, 117 and 120).  The fit is that batch's,
-// twelve teams of one warp; larger teams, whose blocks weigh more beside an
-// item's own cost, have the same weights and would want a smaller lead.  An item
-// whose sequence has no query token (n_q = 0) is walked like any other.
-struct KdBatch {
-  int64_t pref[kMaxB + 1];    // units of the sequences before b (pref[B]: all)
-  int64_t len[kMaxB];
-  int nq[kMaxB];
-};
-constexpr int kKdLead = 16;
-constexpr int kKdMaxCtas = 256;   // CTAs of a call (one per SM)
+struct Kv4DecodeArgs : DecodeArgs {
+  csa_kv4 c;
+  int slotsK, slotsV;   // slots of the two rings: multiples of the number of teams
 
-// units of the incomplete block (an empty item has one)
-__device__ __forceinline__ int kd_tail(int64_t n) {
-  const int left = (int)(n % kBlock);
-  return left ? 6 + left / 4 : n == 0;
-}
-__device__ __forceinline__ int64_t kd_units(const Kv4DecodeArgs& a, int64_t n) {
-  return a.whole ? 1 : kKdLead + n / kBlock + kd_tail(n);
-}
-
-// by warp 0, then a barrier of the CTA
-__device__ __forceinline__ void kd_batch(const Kv4DecodeArgs& a, KdBatch& s) {
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    int64_t u[4], sum = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int b = lane * 4 + i;
-      u[i] = 0;
-      if (b < a.B) {
-        const int64_t n = min(max(a.len[b], (int64_t)0), a.n_max);
-        s.len[b] = n;
-        s.nq[b] = a.n_q ? (int)min(max(a.n_q[b], (int64_t)0), (int64_t)a.T) : a.T;
-        u[i] = kd_units(a, n) * a.Hkv;
-      }
-      sum += u[i];
-    }
-    int64_t x = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    int64_t before = x - sum;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s.pref[lane * 4 + i] = before;
-      before += u[i];
-    }
-    if (lane == 31) s.pref[kMaxB] = before;
+  // What an item and its incomplete block cost, in blocks (KdBatch).  The weights
+  // follow fits to the times of single CTAs (batch of 64, 8 query heads to a KV
+  // head: a block 0.30 us, an item 3.8 to 4.6 us, an incomplete block 1.7 us and
+  // 0.06 us a token).  With 16 units for an item and one for its incomplete
+  // block the last CTA of that batch took 144 us where the mean was 119; a lead
+  // of 8 and of 12 with lighter incomplete blocks took 133 and 131 us for the
+  // call, this 128 (drafts of 24 rows 116, 117 and 120).  The fit is that batch's,
+  // twelve teams of one warp; larger teams, whose blocks weigh more beside an
+  // item's own cost, have the same weights and would want a smaller lead.  An item
+  // whose sequence has no query token (n_q = 0) is walked like any other.
+  static constexpr int kLead = 16, kTailBase = 6, kTailStep = 4;
+  static constexpr bool kPerToken = false;
+  // where a block holds Delta_c
+  template <int D>
+  static __device__ __forceinline__ int top(int c) {
+    return KdStage<D>::B + (4 + c / (D / 4)) * KdStage<D>::PITCH + c % (D / 4) * 4;
   }
-  __syncthreads();
-}
-
-// the part of an item that lies in the run [u, u1) of a CTA
-struct KdSeg {
-  int64_t bg, n, blk0;     // its first block
-  int64_t step;            // its units
-  int64_t start, last;     // the item's first and last units that stand for work done where they lie
-  int b, g, nq;
-  int nfast;               // whole blocks
-  int clear;               // of those, the first `clear` are seen in full by every row
-  int left;                // tokens of the incomplete block
-  bool any;                // there is something to do
-  bool cut0, cut1;         // the item has parts in the run before, in the one after
-};
-__device__ __forceinline__ KdSeg kd_seg(const Kv4DecodeArgs& a, const KdBatch& batch, int64_t u, int64_t u1) {
-  KdSeg s;
-  // the last b with pref[b] <= u (sequences past B hold no units)
-  int lo = 0, hi = a.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (batch.pref[mid] <= u) lo = mid; else hi = mid - 1;
-  }
-  s.b = lo;
-  s.n = batch.len[lo];
-  s.nq = batch.nq[lo];
-  const int64_t units = kd_units(a, s.n), rem = u - batch.pref[lo], whole = s.n / kBlock;
-  s.g = (rem | units) >> 32 ? (int)(rem / units) : (int)((unsigned)rem / (unsigned)units);
-  s.bg = (int64_t)s.b * a.Hkv + s.g;
-  const int64_t v0 = rem - s.g * units, v1 = min(units, v0 + (u1 - u));
-  s.step = v1 - v0;
-  // Work begins with the first block; the incomplete block is done where the
-  // middle of its units lies.
-  const int tail = kd_tail(s.n);
-  const int64_t w0 = a.whole ? 0 : kKdLead, w1 = a.whole ? 0 : kKdLead + whole + (tail ? tail / 2 : -1);
-  s.start = u - v0 + w0;
-  s.last = u - v0 + w1;
-  s.any = v0 <= w1 && v1 > w0;
-  s.cut0 = v0 > w0;
-  s.cut1 = v1 <= w1;
-  s.blk0 = a.whole ? 0 : min(max(v0 - kKdLead, (int64_t)0), whole);
-  s.nfast = (int)((a.whole ? whole : min(max(v1 - kKdLead, (int64_t)0), whole)) - s.blk0);
-  s.left = v0 <= w1 && w1 < v1 ? (int)(s.n % kBlock) : 0;
-  // the first row sees positions below n - nq + 1
-  const int64_t clear = max(s.n - s.nq + 1, (int64_t)0) / kBlock - s.blk0;
-  s.clear = (int)min(max(clear, (int64_t)0), (int64_t)s.nfast);
-  return s;
-}
-
-// units of a CTA's run
-__device__ __forceinline__ int64_t kd_run(const KdBatch& batch, int ncta) {
-  return (batch.pref[kMaxB] + ncta - 1) / ncta;
-}
-// the run without what is nothing to do at its ends: the units of an item whose
-// work lies in the run before or in the one after
-__device__ __forceinline__ void kd_trim(const Kv4DecodeArgs& a, const KdBatch& batch, int64_t& u0, int64_t& u1) {
-  if (a.whole || u0 >= u1) return;
-  const KdSeg s = kd_seg(a, batch, u0, u1), e = kd_seg(a, batch, u1 - 1, u1);
-  if (e.start >= u1) u1 = max(u0, e.start - kKdLead);
-  if (!s.any) u0 = min(u1, u0 + s.step);
-}
-
-// writes four channels of a finished row
-template <int D>
-__device__ __forceinline__ void kd_store(const Kv4DecodeArgs& a, int b, int g, int r, int c, float M, float l, float4 v) {
-  const int t = r / a.G, h = g * a.G + r % a.G;
-  const int64_t row = ((int64_t)b * a.T + t) * a.Hq + h;
-  // l = 0 only where nothing was attended to
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  if (l == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  *reinterpret_cast<float4*>(a.o + row * D + c) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-  if (c == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
-}
-
-// The query rows of an item in shared memory: row r starts at r (D + 16), its
-// channels in four pieces 4 floats apart (bank offsets, as for the bounds).
-// They are log2(e) / sqrt(d) q times a power of two that puts the row's
-// largest at 2^11 .. 2^12 (undone by s_inv[r]).
-template <int D> __device__ __forceinline__ constexpr int kd_q(int r, int c) { return r * (D + 16) + c + c / (D / 4) * 4; }
-
-template <int D, int RT>
-struct KdState {
-  float m[RT], l[RT], acc[RT][D / 32];
-};
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// CNT consecutive elements (16 bytes aligned) as floats
-template <int CNT>
-__device__ __forceinline__ void kd_floats(const float* p, float (&x)[CNT]) {
-#pragma unroll
-  for (int i = 0; i < CNT; i += 4) {
-    const float4 v = *reinterpret_cast<const float4*>(p + i);
-    x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
-  }
-}
-template <int CNT>
-__device__ __forceinline__ void kd_floats(const __nv_bfloat16* p, float (&x)[CNT]) {
-#pragma unroll
-  for (int i = 0; i < CNT; i += 8) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p + i);
-    const unsigned u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[i + e] = __uint_as_float(e & 1 ? u[e / 2] & 0xFFFF0000u : u[e / 2] << 16);
-  }
-}
-
-// One online-softmax step of a warp over `have` <= NT full-precision tokens at
-// K, V (rows of D), the first at position pos.  Scores: lane (gid,
-// tid) takes token gid and the channels [tid NC, (tid + 1) NC) of every query
-// row; values: a lane takes the channels [lane D / 32, ...) of the state st, the
-// weights come through s_p ([NT][RT] floats).  Row r sees positions below
-// s_end[r].
-//
-// With 8 rows four tokens to a step, so that more warps share a block's tokens
-// (batch of 64: 128 us, with eight 130; drafts of 24 rows 120 and 123); with 4
-// rows, where a step costs half, eight (one sequence of 1000 tokens: 12.5 us,
-// with four 14.4: some warps then have steps after their second block).
-template <int RT> constexpr int kKdStep = RT == 8 ? 4 : 8;
-template <int D, int RT, typename E>
-__device__ __forceinline__ void kd_step(KdState<D, RT>& st, const E* K, const E* V, int have, const float* s_q,
-                                        const float* s_inv, const int64_t* s_end, int64_t pos, float* s_p) {
-  constexpr int CPL = D / 32, NT = kKdStep<RT>, LPT = 32 / NT, NC = D / LPT;
-  const int lane = threadIdx.x & 31, gid = lane / LPT, tid = lane % LPT;
-  float vv[NT][CPL];
-#pragma unroll
-  for (int e = 0; e < NT; ++e) {
-#pragma unroll
-    for (int c = 0; c < CPL; ++c) vv[e][c] = 0.0f;
-    if (e < have) {
-      if (CPL == 4) {
-        const float4 v = Elem<E>::get4(V + e * D + lane * CPL);
-        vv[e][0] = v.x; vv[e][1] = v.y; vv[e][CPL - 2] = v.z; vv[e][CPL - 1] = v.w;
-      } else {
-        const float2 v = Elem<E>::get2(V + e * D + lane * CPL);
-        vv[e][0] = v.x; vv[e][1] = v.y;
-      }
-    }
-  }
-  float k[NC], s[RT];
-  kd_floats<NC>(K + (gid < have ? gid : 0) * D + tid * NC, k);
-  bool cut = have < NT;                   // some row does not see some token
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    float even = 0.0f, odd = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NC; i += 4) {
-      const float4 q = *reinterpret_cast<const float4*>(s_q + kd_q<D>(r, tid * NC) + i);
-      even = fmaf(k[i], q.x, even); odd = fmaf(k[i + 1], q.y, odd);
-      even = fmaf(k[i + 2], q.z, even); odd = fmaf(k[i + 3], q.w, odd);
-    }
-    s[r] = (even + odd) * s_inv[r];
-    cut = cut || s_end[r] < pos + NT;
-  }
-#pragma unroll
-  for (int m = 1; m < LPT; m <<= 1)
-#pragma unroll
-    for (int r = 0; r < RT; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], m);
-  float top[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    if (gid >= have || pos + gid >= s_end[r]) s[r] = -INFINITY;
-    top[r] = s[r];
-  }
-#pragma unroll
-  for (int m = LPT; m < 32; m <<= 1)
-#pragma unroll
-    for (int r = 0; r < RT; ++r) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], m));
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const float mn = fmaxf(st.m[r], top[r]), ref = mn > -INFINITY ? mn : 0.0f;
-    const float old = ex2(st.m[r] - ref);
-    st.m[r] = mn;
-    st.l[r] *= old;
-#pragma unroll
-    for (int c = 0; c < CPL; ++c) st.acc[r][c] *= old;
-    // an unseen token is marked
-    const bool seen = gid < have && pos + gid < s_end[r];
-    if (r * LPT / RT == tid) s_p[gid * RT + r] = seen ? ex2(s[r] - ref) : -1.0f;
-  }
-  __syncwarp();
-#pragma unroll
-  for (int e = 0; e < NT; ++e) {
-    float p[RT];
-#pragma unroll
-    for (int r = 0; r < RT; r += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(s_p + e * RT + r);
-      p[r] = v.x; p[r + 1] = v.y; p[r + 2] = v.z; p[r + 3] = v.w;
-    }
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      // an unseen token's value may be anything: it is left out, not
-      // multiplied by zero
-      if (!cut || !(p[r] < 0.0f)) {
-        st.l[r] += p[r];
-#pragma unroll
-        for (int c = 0; c < CPL; ++c) st.acc[r][c] = fmaf(p[r], vv[e][c], st.acc[r][c]);
-      }
-    }
-  }
-  __syncwarp();
-}
-
-// ------------------------------------------------------- moving the blocks
-
-// A ring of slots with full and empty barriers.  Block i sits in slot i %
-// slots and is taken by team i % teams; slots is a multiple of teams, so a
-// slot serves one team, which has seen its last phase when it waits for the
-// next.
-struct KdRing {
-  uint8_t* data;
-  unsigned full, empty;
-  int slots;
 };
 
 // A producer warp: sends for the keys' or the values' parts of the CTA's
@@ -436,49 +163,6 @@ __device__ __forceinline__ void kd_produce(const Kv4DecodeArgs& a, const KdBatch
   for (int k = max(0, i - ring.slots); k < i; ++k)
     if (!mbar_wait(ring.full + 8 * (k % ring.slots), (k / ring.slots) & 1)) dead = true;
   if (dead && lane == 0) atomicOr(a.status, 4u);
-}
-
-// ------------------------------------------------------ tensor-core blocks
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0,
-                                        unsigned b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// the same with d = 0 before
-__device__ __forceinline__ void mma_f16_first(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0,
-                                              unsigned b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
-}
-__device__ __forceinline__ unsigned transpose8(unsigned x) {
-  unsigned y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
-  return y;
-}
-// two float32 numbers as half-precision parts: hi = the rounded pair (x low,
-// y high), lo = the rounded remainders
-__device__ __forceinline__ unsigned half_pair(float x, float y) {
-  const __half2 h = __floats2half2_rn(x, y);
-  return *reinterpret_cast<const unsigned*>(&h);
-}
-__device__ __forceinline__ unsigned half_rest(float x, float y, unsigned hi) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  return half_pair(x - f.x, y - f.y);
-}
-// 2^k, -126 <= k <= 127
-__device__ __forceinline__ float pow2i(int k) { return __int_as_float((127 + k) << 23); }
-// exponent of x > 0 (subnormals: -127)
-__device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
-// the pair (x low, y high) in half precision, truncated
-__device__ __forceinline__ unsigned half_pair_rz(float x, float y) {
-  unsigned r;
-  asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
-  return r;
 }
 
 // A nibble of a half word in bits 7..10: n 2^-17 (bit 10 is the lowest exponent
@@ -949,80 +633,6 @@ __device__ __forceinline__ void kd_fast_store(KdFast<D, RT>& f, float* s_m, floa
   }
 }
 
-// The queries of an item and what else its warps need of it: filled by a
-// producer warp, four rows at a time, an item ahead; tiles of 8 by two, half of
-// the rows each (one took 12 us for 64 rows; drafts of 24 rows 114 us, with one
-// 121, the batch of 64 with 8 rows 126 and 128).
-template <int RT> constexpr int kKdQueryWarps = RT == 8 ? 2 : 1;
-struct KdItem {
-  KdSeg seg;
-  int64_t end[CSA_KV4_MAX_ROWS];    // row r sees positions below end[r]
-  float inv[CSA_KV4_MAX_ROWS];      // undoes the scale of row r (kd_q)
-  int top[CSA_KV4_MAX_ROWS];        // where a block holds Delta_c of the largest of row r
-};
-
-template <int D, int RT, typename E>
-__device__ __forceinline__ void kd_queries(const Kv4DecodeArgs& a, const KdBatch& batch, int64_t u0, int64_t u1,
-                                           KdItem* items, float* s_q, unsigned full, unsigned empty, int part) {
-  constexpr int CPL = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int R = a.T * a.G, Rp = (R + RT - 1) / RT * RT, per = Rp / kKdQueryWarps<RT>;
-  int k = 0;
-  bool dead = false;
-  kd_trim(a, batch, u0, u1);
-  for (int64_t u = u0; u < u1 && !dead; ++k) {
-    const int buf = k & 1;
-    dead = !mbar_wait(empty + 8 * buf, ((k >> 1) & 1) ^ 1);
-    dead = __any_sync(0xffffffffu, dead);
-    if (dead) break;
-    KdItem& it = items[buf];
-    const KdSeg sg = kd_seg(a, batch, u, u1);
-    if (lane == 0 && part == 0) it.seg = sg;
-    const E* base = reinterpret_cast<const E*>(a.q) + sg.b * a.qs.b + (int64_t)sg.g * a.G * a.qs.h + lane * CPL;
-    float* q = s_q + buf * kd_q<D>(Rp, 0);
-#pragma unroll 4
-    for (int r = part * per; r < (part + 1) * per; ++r) {
-      const int t = r / a.G;
-      float x[CPL];
-#pragma unroll
-      for (int c = 0; c < CPL; ++c) x[c] = 0.0f;
-      if (t < sg.nq) {
-        const E* src = base + t * a.qs.t + (r - t * a.G) * a.qs.h;
-        if (CPL == 4) {
-          const float4 v = Elem<E>::get4(src);
-          x[0] = v.x; x[1] = v.y; x[CPL - 2] = v.z; x[CPL - 1] = v.w;
-        } else {
-          const float2 v = Elem<E>::get2(src);
-          x[0] = v.x; x[1] = v.y;
-        }
-      }
-      // the row's largest in magnitude, without its last 7 bits, and its channel
-      unsigned key = 0;
-#pragma unroll
-      for (int c = 0; c < CPL; ++c) {
-        x[c] *= a.rs;
-        key = max(key, (__float_as_uint(x[c]) & 0x7fffff80u) + lane * CPL + c);
-      }
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, m));
-      const float top = __uint_as_float(key & ~127u);
-      const int e = top > 0.0f && top < INFINITY ? min(max(11 - exponent(top), -100), 100) : 0;
-      const float up = pow2i(e);
-#pragma unroll
-      for (int c = 0; c < CPL; ++c) q[kd_q<D>(r, lane * CPL) + c] = x[c] * up;
-      if (lane == 0) {
-        const int c = key & 127;
-        it.top[r] = KdStage<D>::B + (4 + c / (D / 4)) * KdStage<D>::PITCH + c % (D / 4) * 4;
-        it.inv[r] = pow2i(-e);
-        it.end[r] = t < sg.nq ? sg.n - sg.nq + t + 1 : 0;
-      }
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(full + 8 * buf);
-    u += sg.step;
-  }
-  if (dead && lane == 0) atomicOr(a.status, 4u);
-}
 
 // shared memory: barriers (keys full, empty, values full, empty, items full,
 // empty), items, warp sums, q rows of two items, the rings
@@ -1212,7 +822,7 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
         v.x = fmaf(s, y.x, v.x); v.y = fmaf(s, y.y, v.y); v.z = fmaf(s, y.z, v.z); v.w = fmaf(s, y.w, v.w);
       }
       if (!it.seg.cut0 && !it.seg.cut1) {
-        if (r / a.G < it.seg.nq) kd_store<D>(a, it.seg.b, it.seg.g, r, c, M, l, v);
+        if (r / a.G < it.seg.nq) kd_store<D>(a, it.seg, r, c, M, l, v);
       } else {
         *reinterpret_cast<float4*>(part + r * (D + 4) + c) = v;
         if (c == 0) { part[r * (D + 4) + D] = M; part[r * (D + 4) + D + 1] = l; }
@@ -1225,68 +835,6 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
   if (dead && lane == 0) atomicOr(a.status, 4u);
 }
 
-// Joins the parts of the items that were cut: CTAs (j, y) own the item of
-// which CTA j of the decode kernel did the beginning, if it did not do all of
-// it; a warp to a row, eight rows to a CTA.  Which item that is depends on the
-// lengths alone, so it is found before the wait for the decode kernel (whose
-// own wait has seen the lengths written; CTAs with nothing to do wait too:
-// the next kernel takes this grid's end for the decode kernel's).  Weights and
-// the first eight parts are read at once: done one after the other, eight rows
-// to a CTA's eight warps in turn, the join took 10 us after a batch of 64 and
-// 17 after drafts of 24 rows.
-constexpr int kKdJoinWarps = 8;
-template <int D>
-__global__ void __launch_bounds__(kKdJoinWarps * 32) kv4_join_kernel(const Kv4DecodeArgs a, int ncta) {
-  __shared__ KdBatch batch;
-  __shared__ float s_w[kKdJoinWarps][kKdMaxCtas];
-  kd_batch(a, batch);
-  const int64_t per = kd_run(batch, ncta), x = min(((int64_t)blockIdx.x + 1) * per, batch.pref[kMaxB] - 1);
-  const KdSeg s = kd_seg(a, batch, x, x + 1);
-  const int c0 = (int)(s.start / per), parts = (int)(s.last / per) - c0 + 1;
-  const int R = a.T * a.G, lane = threadIdx.x & 31, w = threadIdx.x >> 5, r = blockIdx.y * kKdJoinWarps + w;
-  pdl_entry();
-  if (c0 != (int)blockIdx.x || parts == 1 || r >= R || r / a.G >= s.nq) return;
-  // part 0 is the last one of its CTA, the others the first ones
-  const int64_t stride = (int64_t)R * (D + 4);
-  const float* part0 = a.part + (2 * (int64_t)c0 + 1) * stride + r * (D + 4);
-  const float* part1 = a.part + 2 * (int64_t)c0 * stride + r * (D + 4);
-  const auto at = [&](int k) { return k ? part1 + 2 * k * stride : part0; };
-  const int c = lane % (D / 4) * 4;
-  float4 y[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    if (k < parts) y[k] = *reinterpret_cast<const float4*>(at(k) + c);
-  float M = -INFINITY, l = 0.0f;
-  for (int k = lane; k < parts; k += 32) {
-    const float2 ml = *reinterpret_cast<const float2*>(at(k) + D);
-    // (the running maximum of the lane's own parts)
-    const float top = fmaxf(M, ml.x), ref = top > -INFINITY ? top : 0.0f;
-    l = l * ex2(M - ref) + ml.y * (ml.x > -INFINITY ? ex2(ml.x - ref) : ml.y == 0.0f ? 0.0f : 1.0f);
-    M = top;
-    s_w[w][k] = ml.x > -INFINITY ? ml.x : ml.y == 0.0f ? -INFINITY : NAN;
-  }
-  float top = M;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const float ref = top > -INFINITY ? top : 0.0f;
-  l *= ex2(M - ref);
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  __syncwarp();
-  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k0 = 0; k0 < parts; k0 += 8) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k0 && k0 + k < parts) y[k] = *reinterpret_cast<const float4*>(at(k0 + k) + c);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (k0 + k >= parts) continue;
-      const float e = ex2(s_w[w][k0 + k] - ref);
-      v[0] = fmaf(e, y[k].x, v[0]); v[1] = fmaf(e, y[k].y, v[1]); v[2] = fmaf(e, y[k].z, v[2]); v[3] = fmaf(e, y[k].w, v[3]);
-    }
-  }
-  if (lane < D / 4) kd_store<D>(a, s.b, s.g, r, c, top, l, make_float4(v[0], v[1], v[2], v[3]));
-}
 
 namespace {
 
@@ -1347,7 +895,7 @@ cudaError_t launch_kv4_decode_t(Kv4DecodeArgs a, int ncta, cudaStream_t st) {
       cudaFuncSetAttribute(kv4_decode_kernel<D, RT, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKdSharedBytes);
   if (e != cudaSuccess) return e;
   launch_pdl(kv4_decode_kernel<D, RT, E>, dim3(ncta), dim3(kKdThreads), smem, st, a);
-  if (ncta > 1 && !a.whole) launch_pdl(kv4_join_kernel<D>, dim3(ncta - 1, (a.T * a.G + kKdJoinWarps - 1) / kKdJoinWarps), dim3(kKdJoinWarps * 32), 0, st, a, ncta);
+  if (ncta > 1 && !a.whole) launch_pdl(decode_join_kernel<D, Kv4DecodeArgs>, dim3(ncta - 1, (a.T * a.G + kKdJoinWarps - 1) / kKdJoinWarps), dim3(kKdJoinWarps * 32), 0, st, a, ncta);
   return cudaGetLastError();
 }
 template <int D, typename E>

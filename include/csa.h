@@ -458,6 +458,124 @@ csa_status csa_kv4_decode(const csa_shape* shape, const csa_kv4* cache, int T,
                           float* lse, void* workspace, size_t workspace_bytes,
                           void* stream);
 
+/* ---- a K/V cache held in 8 bits ----
+ *
+ * Between the 16-bit caches of the decode entry points and the 4-bit one: whole
+ * blocks of 64 tokens (aligned to position 0) are held as 8-bit codes with one
+ * step for a block's keys and one for its values, per KV head:
+ *   step = fl(max |x| / 127) over the block's 64 rows of d channels (1 where
+ *   that is 0), code = clamp(rint(fl(x / step)), -127, 127), held plus 128;
+ * a code stands for fl(code step).  The rows of the incomplete last block are
+ * kept as they are, until the block is whole.  A NaN or infinity in a block's
+ * keys makes all of its keys stand for NaN, one in its values all of its values.
+ * Each block also has its keys' span, each channel's largest and smallest code,
+ * which csa_kv8_select scores blocks by.
+ *
+ *   K8      [B][Hkv][nblk_max][8][d/64][8][64]  uint8: element (j, h, g, c) of
+ *           a block is token 16 (g / 2) + 2 j + g % 2, channel 64 h + c: a
+ *           matrix instruction's operand order
+ *   V8      [B][Hkv][nblk_max][d][64]           uint8: a row holds one channel
+ *           of the block's tokens
+ *   scale   [B][Hkv][nblk_max][2]               float: the keys' step, the values'
+ *   span    [B][Hkv][nblk_max][2][d]            uint8: largest, smallest key code
+ *   Kt, Vt  [B][Hkv][64][d]                     type `dtype`: row p % 64 of the
+ *           incomplete block holds position p
+ * All device memory, 16-byte aligned.  260 bytes per token and KV head at
+ * d = 128, against 512 in bf16 and 152 in 4 bits.  Lengths are device arrays
+ * read in stream order, so a token's calls can be captured into one CUDA graph. */
+typedef struct {
+  uint8_t* K8;
+  uint8_t* V8;
+  float* scale;
+  uint8_t* span;
+  void* Kt;
+  void* Vt;
+  uint32_t* refused;   /* as in csa_kv4: what csa_kv8_append refused               */
+} csa_kv8;
+
+/* Appends n_new[b] <= T tokens to every sequence: arguments, strides, lengths
+ * and refusals as in csa_kv4_append. */
+csa_status csa_kv8_append(const csa_shape* shape, const csa_kv8* cache, int T,
+                          const void* k, const csa_strides* ks, const void* v,
+                          const csa_strides* vs, const int64_t* len,
+                          const int64_t* n_new, uint32_t* status,
+                          void* stream);
+
+/* Reads rows back as the values they stand for, rounded to `dtype`: arguments
+ * and refusals as in csa_kv4_unpack. */
+csa_status csa_kv8_unpack(const csa_shape* shape, const csa_kv8* cache,
+                          int64_t rows, const int64_t* first,
+                          const int64_t* len, void* K, void* V,
+                          uint32_t* status, void* stream);
+
+/* Bytes of workspace for up to T query tokens per sequence on the current
+ * device: csa_kv8_decode's with n_sel = 0, else csa_kv8_decode_blocks' with
+ * lists of up to n_sel blocks.  0 when the arguments are invalid. */
+size_t csa_kv8_workspace_size(const csa_shape* shape, int T, int n_sel);
+
+/* Decode attention over the 8-bit cache, for the last n_q[b] <= T tokens of
+ * every sequence: o = softmax(q K^T / sqrt d) V with K, V the values the cache
+ * stands for.  Positions, masks, outputs, workspace and limits (T <= 16, T * Hq /
+ * Hkv <= 64) as in csa_kv4_decode.  Softmax statistics and sums in float32; a
+ * query element is held to 2^-22 of itself or 2^-48 of its row's largest,
+ * whichever is more, a weight to 2^-22 of itself or 2^-37 of its block's
+ * largest. */
+csa_status csa_kv8_decode(const csa_shape* shape, const csa_kv8* cache, int T,
+                          const void* q, const csa_strides* qs,
+                          const int64_t* len, const int64_t* n_q, float* o,
+                          float* lse, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/* Chooses the blocks that each query token of each KV head attends to: of the
+ * blocks 0 .. own, own the block of the token's position, the first n_first, the
+ * last n_last (own among them) and those of the highest scores, n_sel in all, or
+ * all of them if there are no more.  Uncertified: nothing bounds the weight of
+ * what is left out (csa_decode_step does that, over 16-bit caches).
+ * A block's score is the largest over the group's query heads h of
+ *   fl(fl(I step_blk) step_h),   I = sum_c q8_c (q8_c >= 0 ? hi_c : lo_c),
+ * hi and lo the block's span, step_blk its keys' step, step_h = fl(max_c |q_c| /
+ * 127) (1 where that is 0) and q8_c = clamp(rint(fl(q_c / step_h)), -127, 127):
+ * what the query, rounded to 8 bits, could score with a key of the block at most
+ * (times sqrt d).  I is a whole number below 2^24, so scores and choice are the
+ * same on every run; equal scores go to the lower block, a NaN counts as
+ * +infinity.
+ *   q       device [B][T][Hq][d], type `dtype`, strides qs
+ *   len     device [B] int64, its tokens appended already; n_q device [B] int64
+ *           or NULL (T each); token t of sequence b is at position len[b] -
+ *           n_q[b] + t
+ *   blocks  device [B][T][Hkv][n_sel] int32: block numbers, ascending, then -1
+ *   count   device [B][T][Hkv] int32: how many; rows t >= n_q[b] of both are left
+ *           as they are; a row before position 0 has none
+ *   status  as in csa_qk_norm_rope (set for len outside [0, n_max], n_q outside
+ *           [0, T]; that sequence's rows are not written)
+ * 1 <= n_sel <= CSA_KV8_MAX_SEL, n_first >= 0, n_last >= 1, n_first + n_last <=
+ * n_sel; T <= 16, T * Hq / Hkv <= 64 and n_max <= CSA_KV8_MAX_SELECT_TOKENS, else
+ * CSA_ERR_UNSUPPORTED. */
+#define CSA_KV8_MAX_SEL 1024
+#define CSA_KV8_MAX_SELECT_TOKENS (3 << 20)
+csa_status csa_kv8_select(const csa_shape* shape, const csa_kv8* cache, int T,
+                          const void* q, const csa_strides* qs,
+                          const int64_t* len, const int64_t* n_q, int n_sel,
+                          int n_first, int n_last, int32_t* blocks,
+                          int32_t* count, uint32_t* status, void* stream);
+
+/* csa_kv8_decode over listed blocks: each query token attends, in KV head g, to
+ * the positions up to its own of the blocks that its list names (blocks
+ * [B][T][Hkv][n_sel], count [B][T][Hkv], as csa_kv8_select writes them or the
+ * caller makes them).  A list has to be ascending, with no block twice and none
+ * below 0 or past the token's own (entries from count on
+ * are not read); the rows of one that is not, or with a count
+ * outside [0, n_sel], are NaN.  An empty list gives 0 (lse -inf).
+ * 1 <= n_sel <= CSA_KV8_MAX_SEL; other arguments, limits and errors as in
+ * csa_kv8_decode, workspace from csa_kv8_workspace_size with this n_sel. */
+csa_status csa_kv8_decode_blocks(const csa_shape* shape, const csa_kv8* cache,
+                                 int T, const void* q, const csa_strides* qs,
+                                 const int64_t* len, const int64_t* n_q,
+                                 const int32_t* blocks, const int32_t* count,
+                                 int n_sel, float* o, float* lse,
+                                 void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
 /* Where csa_decode_step keeps its intermediate arrays inside the workspace
  * (byte offsets), for diagnostics and parity tests.  Valid after the step's
  * stream has synchronised, until the workspace is reused.
@@ -517,9 +635,11 @@ csa_status csa_profile_read(csa_phase_times* out);
 
 /* Synchronises `stream`, then returns the device status word recorded in
  * `workspace` by the last csa_decode_step, csa_decode_step_device,
- * csa_dense_decode or csa_kv4_decode that used it, or in the status word of
- * the last csa_qk_norm_rope, csa_kv4_append or csa_kv4_unpack that was given
- * this address (a csa_kv4's `refused`: of all appends since it was 0): CSA_OK, CSA_ERR_NONFINITE, CSA_ERR_WORKSPACE,
+ * csa_dense_decode, csa_kv4_decode, csa_kv8_decode or csa_kv8_decode_blocks
+ * that used it, or in the status word of the last csa_qk_norm_rope,
+ * csa_kv4_append, csa_kv4_unpack, csa_kv8_append, csa_kv8_unpack or
+ * csa_kv8_select that was given this address (the `refused` of a csa_kv4 or
+ * csa_kv8: of all appends since it was 0): CSA_OK, CSA_ERR_NONFINITE, CSA_ERR_WORKSPACE,
  * CSA_ERR_TIMEOUT (a bounded wait of a kernel gave up) or
  * CSA_ERR_INVALID_ARG (a device length out of range); or CSA_ERR_CUDA if the
  * stream reports an error. */
