@@ -11,6 +11,8 @@
 //                                 KV head), which attends to a list of blocks of
 //                                 its own, n_sel at most; otherwise an item is
 //                                 all tokens of a sequence, over all its blocks
+//   kPlainQ                       query rows keep their own digits: log2(e) /
+//                                 sqrt(d) goes into what undoes a row's scale
 //   top<D>(c)                     what the kernel wants to know of the channel c
 //                                 of a row's largest query element
 #pragma once
@@ -214,8 +216,8 @@ __device__ __forceinline__ void kd_store(const A& a, const KdSeg& s, int r, int 
 
 // The query rows of an item in shared memory: row r starts at r (D + 16), its
 // channels in four pieces 4 floats apart (bank offsets, as for the bounds).
-// They are log2(e) / sqrt(d) q times a power of two that puts the row's
-// largest at 2^11 .. 2^12 (undone by s_inv[r]).
+// They are log2(e) / sqrt(d) q (kPlainQ: q) times a power of two that puts the
+// row's largest at 2^11 .. 2^12 (undone by s_inv[r]).
 template <int D> __device__ __forceinline__ constexpr int kd_q(int r, int c) { return r * (D + 16) + c + c / (D / 4) * 4; }
 
 template <int D, int RT>
@@ -451,7 +453,7 @@ __device__ __forceinline__ void kd_queries(const A& a, const KdBatch& batch, int
       unsigned key = 0;
 #pragma unroll
       for (int c = 0; c < CPL; ++c) {
-        x[c] *= a.rs;
+        if constexpr (!A::kPlainQ) x[c] *= a.rs;
         key = max(key, (__float_as_uint(x[c]) & 0x7fffff80u) + lane * CPL + c);
       }
 #pragma unroll
@@ -464,7 +466,7 @@ __device__ __forceinline__ void kd_queries(const A& a, const KdBatch& batch, int
       if (lane == 0) {
         const int c = key & 127;
         it.top[r] = A::template top<D>(c);
-        it.inv[r] = pow2i(-e);
+        it.inv[r] = A::kPlainQ ? a.rs * pow2i(-e) : pow2i(-e);
         it.end[r] = t < sg.nq ? sg.n - sg.nq + t + 1 : 0;
       }
     }

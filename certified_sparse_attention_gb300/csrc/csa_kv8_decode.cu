@@ -41,7 +41,7 @@ constexpr int kK8Warps = 8;       // consumer warps of a CTA: two warpgroups; a 
                                   // warps send for the blocks and the queries
 constexpr int kK8Threads = (kK8Warps + 4) * 32;
 // registers: 384 threads start with 168 each; the producers give theirs up
-constexpr int kK8RegsConsumer = 216, kK8RegsProducer = 72;
+constexpr int kK8RegsConsumer = 200, kK8RegsProducer = 104;
 static_assert(2 * kK8RegsConsumer + kK8RegsProducer <= 3 * 168, "more registers than the launch has");
 constexpr int kK8MaxStages = 32;  // slots of a ring
 // warps of a team, for 1 .. 8 tiles
@@ -55,7 +55,7 @@ struct Kv8DecodeArgs : DecodeArgs {
   int n_sel;
   int slotsK, slotsV;     // slots of the two rings: multiples of the number of teams
   static constexpr int kLead = 8, kTailBase = 3, kTailStep = 8;
-  static constexpr bool kPerToken = LIST;
+  static constexpr bool kPerToken = LIST, kPlainQ = true;
   template <int D>
   static __device__ __forceinline__ int top(int c) { return c; }
 };
@@ -162,6 +162,33 @@ __device__ __forceinline__ void k8_init(K8Fast<D>& f, const float* s_q, const fl
   for (int i = 0; i < D / 8; ++i) f.o[i][0] = f.o[i][1] = 0.0f;
 }
 
+// What a row takes from a block whose scores are up to `top` in this lane: ref is
+// the row's largest, share = 2^(ref - f.r), both 0 where it sees nothing of the
+// block (and takes nothing from it, whatever the block's step).
+struct K8Share {
+  float ref, share;
+  bool seen;
+};
+template <int D>
+__device__ __forceinline__ K8Share k8_share(K8Fast<D>& f, float top) {
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  // The sums' reference moves only when a block's maximum exceeds it by more
+  // than 8 (weights up to 2^8).
+  if (__builtin_expect(__any_sync(0xffffffffu, top > f.r + 8.0f), 0)) {
+    const float r = top > f.r + 8.0f ? top : f.r, e = r == f.r ? 1.0f : ex2(f.r - r);
+    f.r = r;
+    f.l *= e;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) { f.o[i][0] *= e; f.o[i][1] *= e; }
+  }
+  K8Share s;
+  s.seen = top > -INFINITY;
+  s.ref = s.seen ? top : 0.0f;
+  s.share = s.seen ? ex2(top - f.r) : 0.0f;
+  return s;
+}
+
 // One block: its keys at kt, its values at vt, steps ks and vs; between() is
 // called when the keys have been read and before the values are.  MASK: the
 // lane's row sees the block's tokens below end only.
@@ -200,20 +227,8 @@ __device__ __forceinline__ void k8_block(K8Fast<D>& f, const uint8_t* kt, const 
       if (MASK && 16 * tid + 2 * j + e >= end) x[j][e] = -INFINITY;
       top = fmaxf(top, x[j][e]);
     }
-  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  // The sums' reference moves only when a block's maximum exceeds it by more
-  // than 8 (weights up to 2^8).
-  if (__builtin_expect(__any_sync(0xffffffffu, top > f.r + 8.0f), 0)) {
-    const float r = top > f.r + 8.0f ? top : f.r, e = r == f.r ? 1.0f : ex2(f.r - r);
-    f.r = r;
-    f.l *= e;
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) { f.o[i][0] *= e; f.o[i][1] *= e; }
-  }
-  // (a row that sees nothing of the block takes nothing from it, whatever its step)
-  const bool seen = top > -INFINITY;
-  const float ref = seen ? top : 0.0f, share = seen ? ex2(top - f.r) : 0.0f, weight = seen ? share * vs : 0.0f;
+  const K8Share sh = k8_share<D>(f, top);
+  const float ref = sh.ref, share = sh.share, weight = sh.seen ? share * vs : 0.0f;
   unsigned p[4][4];
   float sum = 0.0f;
 #pragma unroll
@@ -259,7 +274,114 @@ __device__ __forceinline__ void k8_fast_store(K8Fast<D>& f, float* s_m, float* s
     *reinterpret_cast<float2*>(s_acc + gid * D + 8 * i + 2 * tid) = make_float2(f.o[i][0], f.o[i][1]);
 }
 
-// The incomplete block's tokens that fall to the warp, RT rows of its tile: first
+// ---------------------------------------------------- the incomplete block
+
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0,
+                                               unsigned b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0,
+                                         unsigned b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ unsigned bf16_pair(float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const unsigned*>(&h);
+}
+__device__ __forceinline__ float bf16_low(unsigned u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf16_high(unsigned u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+// Eight tokens of the incomplete block in bf16, on the tensor cores too: keys and
+// queries as they are (products of two bf16 numbers are exact), weights in
+// three bf16 parts.  The rows come straight from memory, sent for before the
+// item's blocks are worked on, zeros past the last one.
+constexpr int kK8Few = 8;
+template <int D>
+struct K8Rows {
+  uint4 k[D / 32];        // token gid: channels 64 h + 16 tid + (0..15)
+  unsigned v[D / 8];      // token gid: channels 8 i + 2 tid, + 1
+};
+template <int D>
+__device__ __forceinline__ void k8_rows_load(K8Rows<D>& x, const __nv_bfloat16* K, const __nv_bfloat16* V, int first, int left) {
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
+  const bool in = first + gid < left;
+  const uint4* k = reinterpret_cast<const uint4*>(K + (first + gid) * D + 16 * tid);
+  const unsigned* v = reinterpret_cast<const unsigned*>(V + (first + gid) * D + 2 * tid);
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) x.k[i] = in ? k[i / 2 * 8 + i % 2] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) x.v[i] = in ? v[4 * i] : 0u;
+}
+// ... which the lane's row sees below end (of the tokens from first on)
+template <int D>
+__device__ __forceinline__ void k8_rows(K8Fast<D>& f, K8Rows<D>& x, const float* s_q, int end, const __nv_bfloat16* V, int left) {
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
+  float s[4];
+#pragma unroll
+  for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float4 q = *reinterpret_cast<const float4*>(s_q + kd_q<D>(gid, 64 * h + 16 * tid) + 4 * c);
+      const uint4 k = x.k[2 * h + c / 2];
+      const unsigned a0 = bf16_pair(q.x, q.y), a2 = bf16_pair(q.z, q.w);
+      if (h == 0 && c == 0) mma_bf16_first(s, a0, 0u, a2, 0u, k.x, k.y);
+      else mma_bf16(s, a0, 0u, a2, 0u, c & 1 ? k.z : k.x, c & 1 ? k.w : k.y);
+    }
+  const int t0 = 2 * tid;
+  const float sa = t0 < end ? s[0] * f.inv : -INFINITY, sb = t0 + 1 < end ? s[1] * f.inv : -INFINITY;
+  const K8Share sh = k8_share<D>(f, fmaxf(sa, sb));
+  const float pa = ex2(sa - sh.ref), pb = ex2(sb - sh.ref);
+  f.l = fmaf(pa + pb, sh.share, f.l);
+  // infinities and NaNs: what a row does not see must not reach it, and parts
+  // that are 0 would make NaNs of infinities
+  unsigned most = 0u;
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    const unsigned u = x.v[i] & 0x7FFF7FFFu;
+    most = __vmaxu2(most, u);
+  }
+  const bool odd = (most & 0xFFFFu) >= 0x7F80u || (most >> 16) >= 0x7F80u;
+  if (__builtin_expect(__any_sync(0xffffffffu, odd), 0)) {
+#pragma unroll 1
+    for (int t = 0; t < kK8Few; ++t) {
+      const float p = __shfl_sync(0xffffffffu, t & 1 ? pb : pa, lane & 28 | t >> 1);
+      if (t >= left || t >= end) continue;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const unsigned u = *reinterpret_cast<const unsigned*>(V + t * D + 8 * i + 2 * tid);
+        if ((u & 0x7F80u) == 0x7F80u) f.o[i][0] = fmaf(p * sh.share, bf16_low(u), f.o[i][0]);
+        if ((u & 0x7F800000u) == 0x7F800000u) f.o[i][1] = fmaf(p * sh.share, bf16_high(u), f.o[i][1]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      if ((x.v[i] & 0x7F80u) == 0x7F80u) x.v[i] &= 0xFFFF0000u;
+      if ((x.v[i] & 0x7F800000u) == 0x7F800000u) x.v[i] &= 0xFFFFu;
+    }
+    __syncwarp();
+  }
+  const unsigned hi = bf16_pair(pa, pb);
+  const float ra = pa - bf16_low(hi), rb = pb - bf16_high(hi);
+  const unsigned mid = bf16_pair(ra, rb), lo = bf16_pair(ra - bf16_low(mid), rb - bf16_high(mid));
+  // rows: high and middle parts; the second eight of the 16 summed tokens are
+  // the same ones again, with the low parts
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    const unsigned v = transpose8(x.v[i]);
+    float y[4];
+    mma_bf16_first(y, hi, mid, lo, 0u, v, v);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) f.o[i][e] = fmaf(y[e] + y[e + 2], sh.share, f.o[i][e]);
+  }
+}
+
+// float32: the incomplete block's tokens that fall to the warp, RT rows of its tile: first
 // the ones at first, then those at step further, and so on below left.
 template <int D, int RT, typename E>
 __device__ __forceinline__ void k8_tail(const E* K, const E* V, int first, int step, int left, const float* q, const float* inv,
@@ -390,10 +512,22 @@ __global__ void __launch_bounds__(kK8Threads, 1) kv8_decode_kernel(const A a) {
     float* my_m = s_m + w * 8;
     float* my_l = s_l + w * 8;
     float* my_acc = s_acc + w * 8 * D;
+    // the incomplete block, if it is to be done here: the teams go on in turn
+    // where the blocks ended, a few tokens at a time
+    const int64_t tail0 = it.seg.n / kBlock * kBlock, at = it.seg.bg * kBlock * D;
+    const int left = it.seg.left, to = base + it.seg.nfast, clear = base + it.seg.clear;
+    const E* Kt = reinterpret_cast<const E*>(a.c.Kt) + at;
+    const E* Vt = reinterpret_cast<const E*>(a.c.Vt) + at;
     {
       K8Fast<D> f;
       k8_init<D>(f, q, it.inv + r0);
-      const int to = base + it.seg.nfast, clear = base + it.seg.clear;
+      constexpr bool few = sizeof(E) == 2;
+      K8Rows<D> few_rows;
+      int few_at = kBlock;
+      if constexpr (few) {
+        if (left > 0 && rows > 0) few_at = kK8Few * ((i < to ? i + (to - i + nteam - 1) / nteam * nteam : i) - to);
+        if (few_at < left) k8_rows_load<D>(few_rows, Kt, Vt, few_at, left);
+      }
       while (i < to) {
         if (!dead && !mbar_wait(keys.full + 8 * sk, pk)) dead = true;
         const float2 step = side[sk];
@@ -420,18 +554,22 @@ __global__ void __launch_bounds__(kK8Threads, 1) kv8_decode_kernel(const A a) {
         if ((sv += nteam) >= values.slots) { sv = my_team; pv ^= 1; }
       }
       base = to;
+      if constexpr (few) {
+        const int end = (int)min(max(it.end[r0 + (lane >> 2)] - tail0, (int64_t)0), (int64_t)left);
+        while (few_at < left) {
+          k8_rows<D>(f, few_rows, q, end - few_at, Vt + few_at * D, left - few_at);
+          few_at += kK8Few * nteam;
+          if (few_at < left) k8_rows_load<D>(few_rows, Kt, Vt, few_at, left);
+        }
+      }
       k8_fast_store<D>(f, my_m, my_l, my_acc);
     }
-    // the incomplete block, if it is to be done here: the teams go on in turn
-    // where the blocks ended, a few tokens at a time
-    const int64_t p0 = it.seg.n / kBlock * kBlock, at = it.seg.bg * kBlock * D;
-    const int left = it.seg.left;
-    const E* Kt = reinterpret_cast<const E*>(a.c.Kt) + at;
-    const E* Vt = reinterpret_cast<const E*>(a.c.Vt) + at;
-    if (rows > 4 && kKdStep<8> * (i - base) < left)
-      k8_tail<D, 8, E>(Kt, Vt, i - base, nteam, left, q, it.inv + r0, it.end + r0, p0, my_m, my_l, my_acc);
-    else if (rows > 0 && rows <= 4 && kKdStep<4> * (i - base) < left)
-      k8_tail<D, 4, E>(Kt, Vt, i - base, nteam, left, q, it.inv + r0, it.end + r0, p0, my_m, my_l, my_acc);
+    if constexpr (sizeof(E) == 4) {
+      if (rows > 4 && kKdStep<8> * (i - base) < left)
+        k8_tail<D, 8, E>(Kt, Vt, i - base, nteam, left, q, it.inv + r0, it.end + r0, tail0, my_m, my_l, my_acc);
+      else if (rows > 0 && rows <= 4 && kKdStep<4> * (i - base) < left)
+        k8_tail<D, 4, E>(Kt, Vt, i - base, nteam, left, q, it.inv + r0, it.end + r0, tail0, my_m, my_l, my_acc);
+    }
     bar_sync(1, W * 32);
     // merge the teams, four channels of a row to a thread
     float* part = a.part + (2 * (int64_t)blockIdx.x + (it.seg.cut0 ? 0 : 1)) * R * (D + 4);
