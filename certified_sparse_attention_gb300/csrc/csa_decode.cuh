@@ -11,11 +11,18 @@
 //                                 KV head), which attends to a list of blocks of
 //                                 its own, n_sel at most; otherwise an item is
 //                                 all tokens of a sequence, over all its blocks
+//   kMaxCtas                      CTAs of a call at most
 //   kPlainQ                       query rows keep their own digits: log2(e) /
 //                                 sqrt(d) goes into what undoes a row's scale
+//   pitch<D>(rows), put<D>(q, r, lane, x, up)
+//                                 how query rows lie in shared memory: floats of
+//                                 `rows` of them, and channels lane D / 32 ... of
+//                                 row r, x up, being laid down
 //   top<D>(c)                     what the kernel wants to know of the channel c
 //                                 of a row's largest query element
 #pragma once
+
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -51,7 +58,6 @@ struct KdBatch {
   int64_t len[kMaxB];
   int nq[kMaxB];
 };
-constexpr int kKdMaxCtas = 256;   // CTAs of a call (one per SM)
 
 // units of the incomplete block (an empty item has one)
 template <typename A>
@@ -112,18 +118,24 @@ struct KdSeg {
   int64_t step;            // its units
   int64_t start, last;     // the item's first and last units that stand for work done where they lie
   int b, g, nq;
-  int t;                   // kPerToken: the query token
   int nfast;               // whole blocks
   int clear;               // of those, the first `clear` are seen in full by every row
   int left;                // tokens of the incomplete block
   bool any;                // there is something to do
   bool cut0, cut1;         // the item has parts in the run before, in the one after
-  bool bad;                // kPerToken: the list is not one (kd_list)
-  int64_t own;             // kPerToken: first position of the token's own block
+};
+// ... of one query token
+struct KdTokenSeg : KdSeg {
+  int t;                   // the query token
+  bool bad;                // its list is not one (kd_list)
+  int64_t own;             // first position of the token's own block
 };
 template <typename A>
-__device__ __forceinline__ KdSeg kd_seg(const A& a, const KdBatch& batch, int64_t u, int64_t u1) {
-  KdSeg s;
+using KdSegOf = std::conditional_t<A::kPerToken, KdTokenSeg, KdSeg>;
+
+template <typename A>
+__device__ __forceinline__ KdSegOf<A> kd_seg(const A& a, const KdBatch& batch, int64_t u, int64_t u1) {
+  KdSegOf<A> s;
   // the last b with pref[b] <= u (sequences past B hold no units)
   int lo = 0, hi = a.B - 1;
   while (lo < hi) {
@@ -161,12 +173,14 @@ __device__ __forceinline__ KdSeg kd_seg(const A& a, const KdBatch& batch, int64_
   return s;
 }
 
+// kPerToken: list entries of an item that its queries' warps leave in shared memory
+constexpr int kKdIds = 128;
 // kPerToken: the item's list of blocks, of which [blk0, blk0 + nfast) are the
 // run's; by a whole warp.  A list is ascending and ends at the token's own block
 // at the latest, so only its last entry can be the incomplete block, or a whole
 // one that the token does not see in full.
 template <typename A>
-__device__ __forceinline__ const int32_t* kd_list(const A& a, KdSeg& s) {
+__device__ __forceinline__ const int32_t* kd_list(const A& a, KdTokenSeg& s) {
   const int lane = threadIdx.x & 31;
   const int64_t row = ((int64_t)s.b * a.T + s.t) * a.Hkv + s.g, pos = s.n - s.nq + s.t;
   const int32_t* ids = a.blocks + row * a.n_sel;
@@ -197,15 +211,16 @@ __device__ __forceinline__ int64_t kd_run(const KdBatch& batch, int ncta) {
 template <typename A>
 __device__ __forceinline__ void kd_trim(const A& a, const KdBatch& batch, int64_t& u0, int64_t& u1) {
   if (a.whole || u0 >= u1) return;
-  const KdSeg s = kd_seg(a, batch, u0, u1), e = kd_seg(a, batch, u1 - 1, u1);
+  const KdSegOf<A> s = kd_seg(a, batch, u0, u1), e = kd_seg(a, batch, u1 - 1, u1);
   if (e.start >= u1) u1 = max(u0, e.start - A::kLead);
   if (!s.any) u0 = min(u1, u0 + s.step);
 }
 
 // writes four channels of a finished row
 template <int D, typename A>
-__device__ __forceinline__ void kd_store(const A& a, const KdSeg& s, int r, int c, float M, float l, float4 v) {
-  const int t = A::kPerToken ? s.t : r / a.G, h = s.g * a.G + (A::kPerToken ? r : r % a.G);
+__device__ __forceinline__ void kd_store(const A& a, const KdSegOf<A>& s, int r, int c, float M, float l, float4 v) {
+  int t = r / a.G, h = s.g * a.G + r % a.G;
+  if constexpr (A::kPerToken) { t = s.t; h = s.g * a.G + r; }
   const int64_t row = ((int64_t)s.b * a.T + t) * a.Hq + h;
   // l = 0 only where nothing was attended to
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -218,7 +233,7 @@ __device__ __forceinline__ void kd_store(const A& a, const KdSeg& s, int r, int 
 // channels in four pieces 4 floats apart (bank offsets, as for the bounds).
 // They are log2(e) / sqrt(d) q (kPlainQ: q) times a power of two that puts the
 // row's largest at 2^11 .. 2^12 (undone by s_inv[r]).
-template <int D> __device__ __forceinline__ constexpr int kd_q(int r, int c) { return r * (D + 16) + c + c / (D / 4) * 4; }
+template <int D> __host__ __device__ __forceinline__ constexpr int kd_q(int r, int c) { return r * (D + 16) + c + c / (D / 4) * 4; }
 
 template <int D, int RT>
 struct KdState {
@@ -406,8 +421,9 @@ __device__ __forceinline__ unsigned half_pair_rz(float x, float y) {
 // the rows each (one took 12 us for 64 rows; drafts of 24 rows 114 us, with one
 // 121, the batch of 64 with 8 rows 126 and 128).
 template <int RT> constexpr int kKdQueryWarps = RT == 8 ? 2 : 1;
+template <typename A>
 struct KdItem {
-  KdSeg seg;
+  KdSegOf<A> seg;
   int64_t end[CSA_KV4_MAX_ROWS];    // row r sees positions below end[r]
   float inv[CSA_KV4_MAX_ROWS];      // undoes the scale of row r (kd_q)
   int top[CSA_KV4_MAX_ROWS];        // of the channel of the largest of row r: A::top
@@ -415,7 +431,8 @@ struct KdItem {
 
 template <int D, int RT, typename E, typename A>
 __device__ __forceinline__ void kd_queries(const A& a, const KdBatch& batch, int64_t u0, int64_t u1,
-                                           KdItem* items, float* s_q, unsigned full, unsigned empty, int part) {
+                                           KdItem<A>* items, float* s_q, unsigned full, unsigned empty, int part,
+                                           int32_t* s_ids = nullptr) {
   constexpr int CPL = D / 32;
   const int lane = threadIdx.x & 31;
   const int R = kd_rows(a), Rp = (R + RT - 1) / RT * RT, per = Rp / kKdQueryWarps<RT>;
@@ -427,15 +444,20 @@ __device__ __forceinline__ void kd_queries(const A& a, const KdBatch& batch, int
     dead = !mbar_wait(empty + 8 * buf, ((k >> 1) & 1) ^ 1);
     dead = __any_sync(0xffffffffu, dead);
     if (dead) break;
-    KdItem& it = items[buf];
-    KdSeg sg = kd_seg(a, batch, u, u1);
-    if constexpr (A::kPerToken) kd_list(a, sg);
+    KdItem<A>& it = items[buf];
+    KdSegOf<A> sg = kd_seg(a, batch, u, u1);
+    if constexpr (A::kPerToken) {
+      const int32_t* ids = kd_list(a, sg) + sg.blk0;
+      if (part == 0)
+        for (int x = lane; x < min(sg.nfast, kKdIds); x += 32) s_ids[buf * kKdIds + x] = ids[x];
+    }
     if (lane == 0 && part == 0) it.seg = sg;
     const E* base = reinterpret_cast<const E*>(a.q) + sg.b * a.qs.b + (int64_t)sg.g * a.G * a.qs.h + lane * CPL;
-    float* q = s_q + buf * kd_q<D>(Rp, 0);
+    float* q = s_q + buf * A::template pitch<D>(Rp);
 #pragma unroll 4
     for (int r = part * per; r < (part + 1) * per; ++r) {
-      const int t = A::kPerToken ? r < R ? sg.t : a.T : r / a.G;
+      int t = r / a.G;
+      if constexpr (A::kPerToken) t = r < R ? sg.t : a.T;
       float x[CPL];
 #pragma unroll
       for (int c = 0; c < CPL; ++c) x[c] = 0.0f;
@@ -461,8 +483,7 @@ __device__ __forceinline__ void kd_queries(const A& a, const KdBatch& batch, int
       const float top = __uint_as_float(key & ~127u);
       const int e = top > 0.0f && top < INFINITY ? min(max(11 - exponent(top), -100), 100) : 0;
       const float up = pow2i(e);
-#pragma unroll
-      for (int c = 0; c < CPL; ++c) q[kd_q<D>(r, lane * CPL) + c] = x[c] * up;
+      A::template put<D>(q, r, lane, x, up);
       if (lane == 0) {
         const int c = key & 127;
         it.top[r] = A::template top<D>(c);
@@ -490,14 +511,14 @@ constexpr int kKdJoinWarps = 8;
 template <int D, typename A>
 __global__ void __launch_bounds__(kKdJoinWarps * 32) decode_join_kernel(const A a, int ncta) {
   __shared__ KdBatch batch;
-  __shared__ float s_w[kKdJoinWarps][kKdMaxCtas];
+  __shared__ float s_w[kKdJoinWarps][A::kMaxCtas];
   kd_batch(a, batch);
   if (A::kPerToken && batch.pref[kMaxB] == 0) {      // no query token at all
     pdl_entry();
     return;
   }
   const int64_t per = kd_run(batch, ncta), x = min(((int64_t)blockIdx.x + 1) * per, batch.pref[kMaxB] - 1);
-  const KdSeg s = kd_seg(a, batch, x, x + 1);
+  const KdSegOf<A> s = kd_seg(a, batch, x, x + 1);
   const int c0 = (int)(s.start / per), parts = (int)(s.last / per) - c0 + 1;
   const int R = kd_rows(a), lane = threadIdx.x & 31, w = threadIdx.x >> 5, r = blockIdx.y * kKdJoinWarps + w;
   pdl_entry();

@@ -103,6 +103,14 @@ struct Kv4DecodeArgs : DecodeArgs {
   // whose sequence has no query token (n_q = 0) is walked like any other.
   static constexpr int kLead = 16, kTailBase = 6, kTailStep = 4;
   static constexpr bool kPerToken = false, kPlainQ = false;
+  static constexpr int kMaxCtas = 256;     // one per SM
+  template <int D>
+  static __host__ __device__ __forceinline__ constexpr int pitch(int rows) { return kd_q<D>(rows, 0); }
+  template <int D>
+  static __device__ __forceinline__ void put(float* q, int r, int lane, const float (&x)[D / 32], float up) {
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) q[kd_q<D>(r, lane * (D / 32)) + c] = x[c] * up;
+  }
   // where a block holds Delta_c
   template <int D>
   static __device__ __forceinline__ int top(int c) {
@@ -639,7 +647,7 @@ __device__ __forceinline__ void kd_fast_store(KdFast<D, RT>& f, float* s_m, floa
 template <int D, int RT>
 struct KdLayout {
   static constexpr int item = (4 * kKdMaxStages + 4) * 8;
-  static constexpr int m = item + 2 * (int)sizeof(KdItem);
+  static constexpr int m = item + 2 * (int)sizeof(KdItem<Kv4DecodeArgs>);
   static constexpr int l = m + kKdWarps * RT * 4;
   static constexpr int acc = (l + kKdWarps * RT * 4 + 15) / 16 * 16;
   static constexpr int q = acc + kKdWarps * RT * D * 4;
@@ -669,7 +677,7 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
   values.slots = a.slotsV;
   keys.data = kd_sm + Lt::ring(R);
   values.data = keys.data + a.slotsK * St::bytesK;
-  KdItem* items = reinterpret_cast<KdItem*>(kd_sm + Lt::item);
+  KdItem<Kv4DecodeArgs>* items = reinterpret_cast<KdItem<Kv4DecodeArgs>*>(kd_sm + Lt::item);
   float* s_q = reinterpret_cast<float*>(kd_sm + Lt::q);        // two of [rows, padded] (kd_q)
   if (tid >= 32 && tid < 32 + kKdMaxStages) {
     // (full: one arrival with the codes' bytes, one of each lane of the producer)
@@ -741,7 +749,7 @@ __global__ void __launch_bounds__(kKdThreads, 1) kv4_decode_kernel(const Kv4Deco
       if (lane == 0) items[buf].seg = kd_seg(a, batch, u, u1);
       __syncwarp();
     }
-    const KdItem& it = items[buf];
+    const KdItem<Kv4DecodeArgs>& it = items[buf];
     const float* q = s_q + kd_q<D>(buf * Rp + r0, 0);
     float* my_m = s_m + w * RT;
     float* my_l = s_l + w * RT;
@@ -859,7 +867,7 @@ int kd_whole(const csa_shape* s) { return (s->n_max + kBlock - 1) / kBlock <= kK
 int kd_ctas(const csa_shape* s) {
   const int64_t blocks = (s->n_max + kBlock - 1) / kBlock;
   const int64_t units = (int64_t)s->B * s->Hkv * (kd_whole(s) ? 1 : blocks);
-  const int nsm = sm_count() < kKdMaxCtas ? sm_count() : kKdMaxCtas;
+  const int nsm = sm_count() < Kv4DecodeArgs::kMaxCtas ? sm_count() : Kv4DecodeArgs::kMaxCtas;
   return (int)(units < nsm ? units : nsm);
 }
 

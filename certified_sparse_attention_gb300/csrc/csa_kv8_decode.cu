@@ -29,23 +29,32 @@
 // are relative to the block's own maximum, so that their parts' floor is 2^-37 of
 // that whatever came before.
 //
-// Blocks come by bulk copies into two rings of shared memory, keys and values,
-// each slot on an mbarrier; producer warps run ahead over the items.
+// Each warp has a slot of shared memory for a block's keys and one for its values
+// (a team shares its two).  As it is done with one it sends for the next block's
+// itself, a bulk copy that completes on an mbarrier, into the next item too.
 #include <cmath>
 
 #include "csa_decode.cuh"
 
 namespace csa {
 
-constexpr int kK8Warps = 8;       // consumer warps of a CTA: two warpgroups; a third one's
-                                  // warps send for the blocks and the queries
+constexpr int kK8Warps = 12;      // consumer warps of a CTA: three warpgroups; two warps of a
+                                  // fourth one fetch the queries
 constexpr int kK8Threads = (kK8Warps + 4) * 32;
-// registers: 384 threads start with 168 each; the producers give theirs up
-constexpr int kK8RegsConsumer = 200, kK8RegsProducer = 104;
-static_assert(2 * kK8RegsConsumer + kK8RegsProducer <= 3 * 168, "more registers than the launch has");
-constexpr int kK8MaxStages = 32;  // slots of a ring
-// warps of a team, for 1 .. 8 tiles
-__host__ __device__ constexpr int k8_team(int ntile) { return ntile <= 2 ? ntile : ntile <= 4 ? 4 : 8; }
+// registers: 512 threads start with 128 each; those of the queries give theirs up
+constexpr int kK8RegsConsumer = 144, kK8RegsQueries = 80;
+static_assert(3 * kK8RegsConsumer + kK8RegsQueries <= 4 * 128, "more registers than the launch has");
+// warps of a team, for 1 .. 8 tiles of 8 rows (above 6 tiles: one team, four warps
+// left over)
+__host__ __device__ constexpr int k8_team(int ntile) { return ntile <= 4 ? ntile : ntile <= 6 ? 6 : 8; }
+
+__device__ __forceinline__ unsigned half_bits(float x) { return __half_as_ushort(__float2half_rn(x)); }
+// high parts of x and y, and what is left of them in units of 2^-12
+__device__ __forceinline__ void k8_parts(float x, float y, unsigned& hi, unsigned& lo) {
+  hi = half_pair(x, y);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  lo = half_pair((x - f.x) * 4096.0f, (y - f.y) * 4096.0f);
+}
 
 template <bool LIST>
 struct Kv8DecodeArgs : DecodeArgs {
@@ -53,66 +62,28 @@ struct Kv8DecodeArgs : DecodeArgs {
   const int32_t* blocks;  // LIST: [B][T][Hkv][n_sel], count [B][T][Hkv]
   const int32_t* count;
   int n_sel;
-  int slotsK, slotsV;     // slots of the two rings: multiples of the number of teams
   static constexpr int kLead = 8, kTailBase = 3, kTailStep = 8;
   static constexpr bool kPerToken = LIST, kPlainQ = true;
+  static constexpr int kMaxCtas = 256;     // one per SM
+  // Query rows as the matrix instructions' operand: of each tile of 8 rows, the
+  // channels 64 h + 16 tid + 4 s + (0..3) of row gid are 16 bytes, (h, s, lane) in
+  // that order: high parts of the first two, their low parts, the same of the others.
+  template <int D>
+  static __host__ __device__ __forceinline__ constexpr int pitch(int rows) { return rows * D; }
+  template <int D>
+  static __device__ __forceinline__ void put(float* q, int r, int lane, const float (&x)[D / 32], float up) {
+    const int c = lane * (D / 32);
+    unsigned* at = reinterpret_cast<unsigned*>(q + (r & ~7) * D) + ((c / 64 * 4 + c % 16 / 4) * 32 + (r & 7) * 4 + c % 64 / 16) * 4 + c % 4;
+#pragma unroll
+    for (int i = 0; i < D / 32; i += 2) {
+      unsigned hi, lo;
+      k8_parts(x[i] * up, x[i + 1] * up, hi, lo);
+      *reinterpret_cast<uint2*>(at + i) = make_uint2(hi, lo);
+    }
+  }
   template <int D>
   static __device__ __forceinline__ int top(int c) { return c; }
 };
-
-// -------------------------------------------------------- moving the blocks
-
-// A producer warp: sends for the keys' or the values' codes of the CTA's whole
-// blocks in order, as slots come free, by one bulk copy each (and a block's two
-// steps beside its keys).
-template <int D, typename A>
-__device__ __forceinline__ void k8_produce(const A& a, const KdBatch& batch, int64_t u0, int64_t u1, const KdRing& ring,
-                                           unsigned side, bool keys) {
-  constexpr unsigned codes = kBlock * D;
-  const int lane = threadIdx.x & 31;
-  const uint8_t* src = keys ? a.c.K8 : a.c.V8;
-  const unsigned data = smem_u32(ring.data);
-  int i = 0, slot = 0, phase = 0;
-  bool dead = false;
-  kd_trim(a, batch, u0, u1);
-  for (int64_t u = u0; u < u1 && !dead;) {
-    KdSeg s = kd_seg(a, batch, u, u1);
-    const int32_t* ids = nullptr;
-    if constexpr (A::kPerToken) ids = kd_list(a, s);
-    int id = 0;
-    for (int x = 0; x < s.nfast; ++x) {
-      int64_t at = s.bg * a.nblk_max;
-      if constexpr (A::kPerToken) {
-        if ((x & 31) == 0) id = x + lane < s.nfast ? ids[s.blk0 + x + lane] : 0;
-        at += __shfl_sync(0xffffffffu, id, x & 31);
-      } else {
-        at += s.blk0 + x;
-      }
-      dead = !mbar_wait(ring.empty + 8 * slot, phase ^ 1);    // (a new barrier's "phase -1" is complete)
-      dead = __any_sync(0xffffffffu, dead);
-      if (dead) break;
-      if (lane == 0) {
-        const unsigned bar = ring.full + 8 * slot;
-        mbar_expect_tx(bar, codes);
-        asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(data + slot * codes),
-            "l"(src + at * codes), "n"(codes), "r"(bar)
-            : "memory");
-        if (keys) {
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(side + slot * 8), "l"(a.c.scale + at * 2) : "memory");
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
-        }
-      }
-      ++i;
-      if (++slot == ring.slots) { slot = 0; phase ^= 1; }
-    }
-    u += s.step;
-  }
-  // all copies land before the CTA can end
-  for (int k = max(0, i - ring.slots); k < i; ++k)
-    if (!mbar_wait(ring.full + 8 * (k % ring.slots), (k / ring.slots) & 1)) dead = true;
-  if (dead && lane == 0) atomicOr(a.status, 4u);
-}
 
 // ------------------------------------------------------ tensor-core blocks
 
@@ -126,41 +97,16 @@ __device__ __forceinline__ void k8_numbers(unsigned word, unsigned& b0, unsigned
   b0 = *reinterpret_cast<const unsigned*>(&h0);
   b1 = *reinterpret_cast<const unsigned*>(&h1);
 }
-// high parts of x and y, and what is left of them in units of 2^-12
-__device__ __forceinline__ void k8_parts(float x, float y, unsigned& hi, unsigned& lo) {
-  hi = half_pair(x, y);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  lo = half_pair((x - f.x) * 4096.0f, (y - f.y) * 4096.0f);
-}
+__device__ __forceinline__ unsigned word_of(const uint4& v, int s) { return s == 0 ? v.x : s == 1 ? v.y : s == 2 ? v.z : v.w; }
 
-// The state of a warp over the tensor-core blocks of an item; the lane's row is
-// gid.
+// The state of a warp over the blocks of an item; the lane's row is gid.
 template <int D>
 struct K8Fast {
-  unsigned qa[D / 64][4][4];   // query operand: channels 64 h + 16 tid + 4 s + (0..3), high and low parts
   float inv;                   // undoes the row's scale
   float r;                     // reference of the sums: the running maximum, or up to 8 below it
   float l;                     // sum of the lane's own tokens' weights
   float o[D / 8][2];           // channels 8 i + 2 tid, + 1
 };
-
-template <int D>
-__device__ __forceinline__ void k8_init(K8Fast<D>& f, const float* s_q, const float* s_inv) {
-  const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
-#pragma unroll
-  for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const float4 x = *reinterpret_cast<const float4*>(s_q + kd_q<D>(gid, 64 * h + 16 * tid) + 4 * s);
-      k8_parts(x.x, x.y, f.qa[h][s][0], f.qa[h][s][1]);
-      k8_parts(x.z, x.w, f.qa[h][s][2], f.qa[h][s][3]);
-    }
-  f.inv = s_inv[gid];
-  f.r = -INFINITY;
-  f.l = 0.0f;
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i) f.o[i][0] = f.o[i][1] = 0.0f;
-}
 
 // What a row takes from a block whose scores are up to `top` in this lane: ref is
 // the row's largest, share = 2^(ref - f.r), both 0 where it sees nothing of the
@@ -189,18 +135,22 @@ __device__ __forceinline__ K8Share k8_share(K8Fast<D>& f, float top) {
   return s;
 }
 
-// One block: its keys at kt, its values at vt, steps ks and vs; between() is
-// called when the keys have been read and before the values are.  MASK: the
-// lane's row sees the block's tokens below end only.
-template <int D, bool MASK, typename Between>
-__device__ __forceinline__ void k8_block(K8Fast<D>& f, const uint8_t* kt, const uint8_t* vt, float ks, float vs, int end,
-                                         Between between) {
+// One block: query operand at qa (K8Args::put; the lane's), keys at kt, values at
+// vt, steps ks and vs; between() is called when the keys have been read and before
+// the values are.  The lane's row sees the block's tokens below end; masked: some
+// row does not see all of them.
+template <int D, typename Between>
+__device__ __forceinline__ void k8_block(K8Fast<D>& f, const uint4* qa, const uint8_t* kt, const uint8_t* vt, float ks, float vs,
+                                         bool masked, int end, Between between) {
   const int lane = threadIdx.x & 31, tid = lane & 3;
   float x[8][4];
 #pragma unroll
   for (int j = 0; j < 8; ++j) x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.0f;
+#pragma unroll 1
+  for (int h = 0; h < D / 64; ++h) {
+    uint4 q[4];
 #pragma unroll
-  for (int h = 0; h < D / 64; ++h)
+    for (int s = 0; s < 4; ++s) q[s] = qa[(h * 4 + s) * 32];
 #pragma unroll
     for (int j0 = 0; j0 < 8; j0 += 4) {
       uint4 k[4];
@@ -211,35 +161,42 @@ __device__ __forceinline__ void k8_block(K8Fast<D>& f, const uint8_t* kt, const 
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           unsigned b0, b1;
-          k8_numbers(s == 0 ? k[j].x : s == 1 ? k[j].y : s == 2 ? k[j].z : k[j].w, b0, b1);
-          mma_f16(x[j0 + j], f.qa[h][s][0], f.qa[h][s][1], f.qa[h][s][2], f.qa[h][s][3], b0, b1);
+          k8_numbers(word_of(k[j], s), b0, b1);
+          mma_f16(x[j0 + j], q[s].x, q[s].y, q[s].z, q[s].w, b0, b1);
         }
     }
+  }
   between();
   // scores: x[j][e] of token 16 tid + 2 j + e
   const float unit = ks * f.inv;
-  float top = -INFINITY;
+  float top = -INFINITY, top1 = -INFINITY;
 #pragma unroll
   for (int j = 0; j < 8; ++j)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      x[j][e] = fmaf(x[j][e + 2], kLowUnit, x[j][e]) * unit;
-      if (MASK && 16 * tid + 2 * j + e >= end) x[j][e] = -INFINITY;
-      top = fmaxf(top, x[j][e]);
-    }
-  const K8Share sh = k8_share<D>(f, top);
-  const float ref = sh.ref, share = sh.share, weight = sh.seen ? share * vs : 0.0f;
+    for (int e = 0; e < 2; ++e) x[j][e] = fmaf(x[j][e + 2], kLowUnit, x[j][e]) * unit;
+  if (__builtin_expect(masked, 0)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (16 * tid + 2 * j + e >= end) x[j][e] = -INFINITY;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) { top = fmaxf(top, x[j][0]); top1 = fmaxf(top1, x[j][1]); }
+  const K8Share sh = k8_share<D>(f, fmaxf(top, top1));
+  const float weight = sh.seen ? sh.share * vs : 0.0f;
   unsigned p[4][4];
-  float sum = 0.0f;
+  float sum = 0.0f, sum1 = 0.0f;
 #pragma unroll
   for (int s = 0; s < 4; ++s)
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const float pa = ex2(x[2 * s + u][0] - ref), pb = ex2(x[2 * s + u][1] - ref);
-      sum += pa + pb;
+      const float pa = ex2(x[2 * s + u][0] - sh.ref), pb = ex2(x[2 * s + u][1] - sh.ref);
+      sum += pa;
+      sum1 += pb;
       k8_parts(pa, pb, p[s][2 * u], p[s][2 * u + 1]);
     }
-  f.l = fmaf(sum, share, f.l);
+  f.l = fmaf(sum + sum1, sh.share, f.l);
 #pragma unroll
   for (int i0 = 0; i0 < D / 8; i0 += 4) {
     uint4 v[4];
@@ -251,7 +208,7 @@ __device__ __forceinline__ void k8_block(K8Fast<D>& f, const uint8_t* kt, const 
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         unsigned b0, b1;
-        k8_numbers(s == 0 ? v[i].x : s == 1 ? v[i].y : s == 2 ? v[i].z : v[i].w, b0, b1);
+        k8_numbers(word_of(v[i], s), b0, b1);
         if (s == 0) mma_f16_first(y[i], p[s][0], p[s][1], p[s][2], p[s][3], b0, b1);
         else mma_f16(y[i], p[s][0], p[s][1], p[s][2], p[s][3], b0, b1);
       }
@@ -262,27 +219,8 @@ __device__ __forceinline__ void k8_block(K8Fast<D>& f, const uint8_t* kt, const 
   }
 }
 
-// the warp's sums as rows [8] of m, l and acc[D] in shared memory
-template <int D>
-__device__ __forceinline__ void k8_fast_store(K8Fast<D>& f, float* s_m, float* s_l, float* s_acc) {
-  const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
-  f.l += __shfl_xor_sync(0xffffffffu, f.l, 1);
-  f.l += __shfl_xor_sync(0xffffffffu, f.l, 2);
-  if (tid == 0) { s_m[gid] = f.r; s_l[gid] = f.l; }
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i)
-    *reinterpret_cast<float2*>(s_acc + gid * D + 8 * i + 2 * tid) = make_float2(f.o[i][0], f.o[i][1]);
-}
-
 // ---------------------------------------------------- the incomplete block
 
-__device__ __forceinline__ void mma_bf16_first(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0,
-                                               unsigned b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
-}
 __device__ __forceinline__ void mma_bf16(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0,
                                          unsigned b1) {
   asm volatile(
@@ -296,163 +234,220 @@ __device__ __forceinline__ unsigned bf16_pair(float x, float y) {
 }
 __device__ __forceinline__ float bf16_low(unsigned u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_high(unsigned u) { return __uint_as_float(u & 0xFFFF0000u); }
-
-// Eight tokens of the incomplete block in bf16, on the tensor cores too: keys and
-// queries as they are (products of two bf16 numbers are exact), weights in
-// three bf16 parts.  The rows come straight from memory, sent for before the
-// item's blocks are worked on, zeros past the last one.
-constexpr int kK8Few = 8;
-template <int D>
-struct K8Rows {
-  uint4 k[D / 32];        // token gid: channels 64 h + 16 tid + (0..15)
-  unsigned v[D / 8];      // token gid: channels 8 i + 2 tid, + 1
-};
-template <int D>
-__device__ __forceinline__ void k8_rows_load(K8Rows<D>& x, const __nv_bfloat16* K, const __nv_bfloat16* V, int first, int left) {
-  const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
-  const bool in = first + gid < left;
-  const uint4* k = reinterpret_cast<const uint4*>(K + (first + gid) * D + 16 * tid);
-  const unsigned* v = reinterpret_cast<const unsigned*>(V + (first + gid) * D + 2 * tid);
+// x and y as N bf16 parts each: the rounded pair, the rounded remainders, ...
+template <int N>
+__device__ __forceinline__ void bf16_parts(float x, float y, unsigned (&p)[N]) {
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) x.k[i] = in ? k[i / 2 * 8 + i % 2] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i) x.v[i] = in ? v[4 * i] : 0u;
+  for (int i = 0; i < N; ++i) {
+    p[i] = bf16_pair(x, y);
+    if (i + 1 < N) { x -= bf16_low(p[i]); y -= bf16_high(p[i]); }
+  }
 }
-// ... which the lane's row sees below end (of the tokens from first on)
-template <int D>
-__device__ __forceinline__ void k8_rows(K8Fast<D>& f, K8Rows<D>& x, const float* s_q, int end, const __nv_bfloat16* V, int left) {
+// two channels of a row
+__device__ __forceinline__ float2 pair_of(const __nv_bfloat16* p) {
+  const unsigned u = *reinterpret_cast<const unsigned*>(p);
+  return make_float2(bf16_low(u), bf16_high(u));
+}
+__device__ __forceinline__ float2 pair_of(const float* p) { return *reinterpret_cast<const float2*>(p); }
+// four channels
+__device__ __forceinline__ float4 four_of(const __nv_bfloat16* p) { return Elem<__nv_bfloat16>::get4(p); }
+__device__ __forceinline__ float4 four_of(const float* p) { return Elem<float>::get4(p); }
+__device__ __forceinline__ bool odd_number(float x) { return !(fabsf(x) < INFINITY); }
+
+// Eight tokens of the incomplete block at K, V, `left` of them there, of which the
+// lane's row sees those below end; on the tensor cores too.  Keys and queries are
+// split into bf16 parts (a bf16 number is one; float32 ones are three, whose
+// products are all summed), weights into three: the instruction's 16 rows are
+// the high and middle parts, and the low ones stand in its second eight tokens,
+// which are the first ones again.
+constexpr int kK8Few = 8;
+template <int D, typename E>
+__device__ __forceinline__ void k8_rows(K8Fast<D>& f, const uint4* qa, const E* K, const E* V, int left, int end) {
+  constexpr int N = sizeof(E) == 2 ? 1 : 3;
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
-  float s[4];
+  const bool in = gid < left;
+  const E* kr = K + gid * D + 16 * tid;
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int h = 0; h < D / 64; ++h)
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const float4 q = *reinterpret_cast<const float4*>(s_q + kd_q<D>(gid, 64 * h + 16 * tid) + 4 * c);
-      const uint4 k = x.k[2 * h + c / 2];
-      const unsigned a0 = bf16_pair(q.x, q.y), a2 = bf16_pair(q.z, q.w);
-      if (h == 0 && c == 0) mma_bf16_first(s, a0, 0u, a2, 0u, k.x, k.y);
-      else mma_bf16(s, a0, 0u, a2, 0u, c & 1 ? k.z : k.x, c & 1 ? k.w : k.y);
+      const uint4 q = qa[(h * 4 + c) * 32];
+      const float4 k = in ? four_of(kr + 64 * h + 4 * c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      unsigned a[2][N], b[2][N];
+      bf16_parts<N>(k.x, k.y, b[0]);
+      bf16_parts<N>(k.z, k.w, b[1]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const unsigned hi = e ? q.z : q.x, lo = e ? q.w : q.y;
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&hi)), y = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+        bf16_parts<N>(fmaf(y.x, kLowUnit, x.x), fmaf(y.y, kLowUnit, x.y), a[e]);
+      }
+#pragma unroll
+      for (int i = N - 1; i >= 0; --i) {
+        mma_bf16(s, a[0][0], N > 1 ? a[0][N / 2] : 0u, a[1][0], N > 1 ? a[1][N / 2] : 0u, b[0][i], b[1][i]);
+        if (N > 1) mma_bf16(s, a[0][N - 1], 0u, a[1][N - 1], 0u, b[0][i], b[1][i]);
+      }
     }
   const int t0 = 2 * tid;
-  const float sa = t0 < end ? s[0] * f.inv : -INFINITY, sb = t0 + 1 < end ? s[1] * f.inv : -INFINITY;
+  const float sa = t0 < end ? (s[0] + s[2]) * f.inv : -INFINITY, sb = t0 + 1 < end ? (s[1] + s[3]) * f.inv : -INFINITY;
   const K8Share sh = k8_share<D>(f, fmaxf(sa, sb));
   const float pa = ex2(sa - sh.ref), pb = ex2(sb - sh.ref);
   f.l = fmaf(pa + pb, sh.share, f.l);
-  // infinities and NaNs: what a row does not see must not reach it, and parts
-  // that are 0 would make NaNs of infinities
-  unsigned most = 0u;
+  unsigned p[3];
+  bf16_parts<3>(pa, pb, p);
+  bool odd = false;
+  const E* vr = V + gid * D + 2 * tid;
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) {
-    const unsigned u = x.v[i] & 0x7FFF7FFFu;
-    most = __vmaxu2(most, u);
-  }
-  const bool odd = (most & 0xFFFFu) >= 0x7F80u || (most >> 16) >= 0x7F80u;
-  if (__builtin_expect(__any_sync(0xffffffffu, odd), 0)) {
-#pragma unroll 1
-    for (int t = 0; t < kK8Few; ++t) {
-      const float p = __shfl_sync(0xffffffffu, t & 1 ? pb : pa, lane & 28 | t >> 1);
-      if (t >= left || t >= end) continue;
+    float2 v = in ? pair_of(vr + 8 * i) : make_float2(0.0f, 0.0f);
+    // (infinities and NaNs are left to the loop below)
+    const bool ox = odd_number(v.x), oy = odd_number(v.y);
+    odd = odd || ox || oy;
+    unsigned b[N];
+    bf16_parts<N>(ox ? 0.0f : v.x, oy ? 0.0f : v.y, b);
+    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const unsigned u = *reinterpret_cast<const unsigned*>(V + t * D + 8 * i + 2 * tid);
-        if ((u & 0x7F80u) == 0x7F80u) f.o[i][0] = fmaf(p * sh.share, bf16_low(u), f.o[i][0]);
-        if ((u & 0x7F800000u) == 0x7F800000u) f.o[i][1] = fmaf(p * sh.share, bf16_high(u), f.o[i][1]);
-      }
+    for (int k = N - 1; k >= 0; --k) {
+      const unsigned t = transpose8(b[k]);
+      mma_bf16(y, p[0], p[1], p[2], 0u, t, t);
     }
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      if ((x.v[i] & 0x7F80u) == 0x7F80u) x.v[i] &= 0xFFFF0000u;
-      if ((x.v[i] & 0x7F800000u) == 0x7F800000u) x.v[i] &= 0xFFFFu;
-    }
-    __syncwarp();
-  }
-  const unsigned hi = bf16_pair(pa, pb);
-  const float ra = pa - bf16_low(hi), rb = pb - bf16_high(hi);
-  const unsigned mid = bf16_pair(ra, rb), lo = bf16_pair(ra - bf16_low(mid), rb - bf16_high(mid));
-  // rows: high and middle parts; the second eight of the 16 summed tokens are
-  // the same ones again, with the low parts
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    const unsigned v = transpose8(x.v[i]);
-    float y[4];
-    mma_bf16_first(y, hi, mid, lo, 0u, v, v);
 #pragma unroll
     for (int e = 0; e < 2; ++e) f.o[i][e] = fmaf(y[e] + y[e + 2], sh.share, f.o[i][e]);
   }
+  // what a row does not see must not reach it, and parts that are 0 would make
+  // NaNs of infinities: those values are taken one by one
+  if (__builtin_expect(__any_sync(0xffffffffu, odd), 0)) {
+#pragma unroll 1
+    for (int t = 0; t < kK8Few; ++t) {
+      const float w = __shfl_sync(0xffffffffu, t & 1 ? pb : pa, lane & 28 | t >> 1) * sh.share;
+      if (t >= left || t >= end) continue;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const float2 v = pair_of(V + t * D + 8 * i + 2 * tid);
+        if (odd_number(v.x)) f.o[i][0] = fmaf(w, v.x, f.o[i][0]);
+        if (odd_number(v.y)) f.o[i][1] = fmaf(w, v.y, f.o[i][1]);
+      }
+    }
+    __syncwarp();
+  }
 }
-
-// float32: the incomplete block's tokens that fall to the warp, RT rows of its tile: first
-// the ones at first, then those at step further, and so on below left.
-template <int D, int RT, typename E>
-__device__ __forceinline__ void k8_tail(const E* K, const E* V, int first, int step, int left, const float* q, const float* inv,
-                                        const int64_t* end, int64_t p0, float* my_m, float* my_l, float* my_acc) {
-  constexpr int CPL = D / 32;
+// the rows of tokens [first, first + 8) below left on their way to the cache
+template <int D, typename E>
+__device__ __forceinline__ void k8_rows_ahead(const E* K, const E* V, int first, int left) {
   const int lane = threadIdx.x & 31;
-  // the state moves on to lanes that hold channels
-  __syncwarp();
-  KdState<D, RT> st;
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    st.m[r] = my_m[r]; st.l[r] = my_l[r];
-#pragma unroll
-    for (int c = 0; c < CPL; ++c) st.acc[r][c] = my_acc[r * D + lane * CPL + c];
-  }
-  __syncwarp();
-  // (my_acc is free until the state returns to it)
-  for (int t0 = kKdStep<RT> * first; t0 < left; t0 += kKdStep<RT> * step)
-    kd_step<D, RT, E>(st, K + t0 * D, V + t0 * D, min(kKdStep<RT>, left - t0), q, inv, end, p0 + t0, my_acc);
-  __syncwarp();
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    if (lane == 0) { my_m[r] = st.m[r]; my_l[r] = st.l[r]; }
-#pragma unroll
-    for (int c = 0; c < CPL; ++c) my_acc[r * D + lane * CPL + c] = st.acc[r][c];
+  constexpr int lines = D * (int)sizeof(E) / 128;       // 128-byte lines of a row
+  for (int x = lane; x < 2 * kK8Few * lines; x += 32) {
+    const int row = first + x / lines % kK8Few;
+    if (row < left)
+      asm volatile("prefetch.global.L2 [%0];\n" ::"l"((const char*)((x < kK8Few * lines ? K : V) + row * D) + x % lines * 128));
   }
 }
 
-// shared memory: barriers (keys full, empty, values full, empty, items full,
-// empty), items, warp sums, q rows of two items, steps of the keys' slots, the rings
+// --------------------------------------------------------------- the sums
+
+// rows of a warp's sums in shared memory lie D + 8 floats apart (bank offsets)
+template <int D> constexpr int kK8Pitch = D + 8;
+
+// the warp's sums as rows [8] of m, l and acc[D] in shared memory
 template <int D>
+__device__ __forceinline__ void k8_store(K8Fast<D>& f, float* s_m, float* s_l, float* s_acc) {
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
+  f.l += __shfl_xor_sync(0xffffffffu, f.l, 1);
+  f.l += __shfl_xor_sync(0xffffffffu, f.l, 2);
+  if (tid == 0) { s_m[gid] = f.r; s_l[gid] = f.l; }
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i)
+    *reinterpret_cast<float2*>(s_acc + gid * kK8Pitch<D> + 8 * i + 2 * tid) = make_float2(f.o[i][0], f.o[i][1]);
+}
+// factor of sums relative to m where they become relative to M
+__device__ __forceinline__ float k8_factor(float m, float l, float M) { return m > -INFINITY ? ex2(m - M) : l == 0.0f ? 0.0f : 1.0f; }
+// the same where another warp's sums of the rows lie already: both
+template <int D>
+__device__ __forceinline__ void k8_add(K8Fast<D>& f, float* s_m, float* s_l, float* s_acc) {
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
+  f.l += __shfl_xor_sync(0xffffffffu, f.l, 1);
+  f.l += __shfl_xor_sync(0xffffffffu, f.l, 2);
+  const float m = s_m[gid], l = s_l[gid], M = fmaxf(f.r, m), mine = k8_factor(f.r, f.l, M), its = k8_factor(m, l, M);
+  __syncwarp();
+  if (tid == 0) { s_m[gid] = M; s_l[gid] = fmaf(its, l, mine * f.l); }
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    float2* at = reinterpret_cast<float2*>(s_acc + gid * kK8Pitch<D> + 8 * i + 2 * tid);
+    const float2 x = *at;
+    *at = make_float2(fmaf(its, x.x, mine * f.o[i][0]), fmaf(its, x.y, mine * f.o[i][1]));
+  }
+}
+
+// --------------------------------------------------------------- the kernel
+
+// Warps whose sums lie in shared memory at once: four (and the others add theirs
+// in turn) where twelve slots of keys and of values leave no room for more.
+template <int D>
+__host__ __device__ constexpr int k8_kept(int team) { return D == 128 && team == 1 ? 4 : kK8Warps; }
+
+// shared memory: barriers (keys, values full, empty, items full, empty), items,
+// list entries and q rows of two items, warp sums, the slots
+template <int D, typename A>
 struct K8Layout {
-  static constexpr int item = (4 * kK8MaxStages + 4) * 8;
-  static constexpr int m = item + 2 * (int)sizeof(KdItem);
+  static constexpr int item = (4 * kK8Warps + 4) * 8;
+  static constexpr int ids = item + 2 * (int)sizeof(KdItem<A>);
+  static constexpr int m = ids + (A::kPerToken ? 2 * kKdIds * 4 : 0);
   static constexpr int l = m + kK8Warps * 8 * 4;
-  static constexpr int acc = (l + kK8Warps * 8 * 4 + 15) / 16 * 16;
-  static constexpr int side = acc + kK8Warps * 8 * D * 4;
-  static constexpr int q = side + kK8MaxStages * 8;
-  static __host__ __device__ int ring(int rows) { return (q + 2 * ((rows + 7) / 8 * 8) * (D + 16) * 4 + 127) / 128 * 128; }
+  static constexpr int q = (l + kK8Warps * 8 * 4 + 15) / 16 * 16;
+  static __host__ __device__ int acc(int rows) { return q + 2 * ((rows + 7) / 8 * 8) * D * 4; }
+  static __host__ __device__ int slots(int rows) {
+    return (acc(rows) + k8_kept<D>(k8_team((rows + 7) / 8)) * 8 * kK8Pitch<D> * 4 + 127) / 128 * 128;
+  }
 };
+
+// whether the phase of parity `parity` is complete, for a whole warp
+__device__ __forceinline__ bool mbar_test(unsigned bar, unsigned parity) {
+  unsigned done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, done);
+}
+__device__ __forceinline__ void k8_send(unsigned to, const uint8_t* from, unsigned bytes, unsigned bar) {
+  mbar_expect_tx(bar, bytes);
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(to), "l"(from),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+// where block x of an item lies
+template <typename A>
+__device__ __forceinline__ int64_t k8_at(const A& a, const KdSegOf<A>& s, const int32_t* s_ids, int x) {
+  if constexpr (A::kPerToken) {
+    const int id = x < kKdIds ? s_ids[x] : a.blocks[(((int64_t)s.b * a.T + s.t) * a.Hkv + s.g) * a.n_sel + s.blk0 + x];
+    return s.bg * a.nblk_max + id;
+  } else {
+    return s.bg * a.nblk_max + s.blk0 + x;
+  }
+}
 
 template <int D, typename E, typename A>
 __global__ void __launch_bounds__(kK8Threads, 1) kv8_decode_kernel(const A a) {
   pdl_entry();
-  using Lt = K8Layout<D>;
+  using Lt = K8Layout<D, A>;
   constexpr int W = kK8Warps;
+  constexpr unsigned bytes = kBlock * D;
   __shared__ KdBatch batch;
   extern __shared__ __align__(128) uint8_t k8_sm[];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int R = kd_rows(a), Rp = (R + 7) / 8 * 8;
   // teams: warps that share a block, one tile of rows each
-  const int team = k8_team(Rp / 8), nteam = W / team;
-  KdRing keys, values;
-  keys.full = smem_u32(k8_sm);
-  keys.empty = keys.full + kK8MaxStages * 8;
-  values.full = keys.empty + kK8MaxStages * 8;
-  values.empty = values.full + kK8MaxStages * 8;
-  const unsigned item_full = values.empty + kK8MaxStages * 8, item_empty = item_full + 16;
-  keys.slots = a.slotsK;
-  values.slots = a.slotsV;
-  keys.data = k8_sm + Lt::ring(R);
-  values.data = keys.data + a.slotsK * kBlock * D;
-  KdItem* items = reinterpret_cast<KdItem*>(k8_sm + Lt::item);
-  float* s_q = reinterpret_cast<float*>(k8_sm + Lt::q);        // two of [rows, padded] (kd_q)
-  if (tid >= 32 && tid < 32 + kK8MaxStages) {
-    // (keys full: one arrival with the codes' bytes, one of the steps' copy)
+  const int team = k8_team(Rp / 8), nteam = W / team, kept = k8_kept<D>(team);
+  const unsigned bars = smem_u32(k8_sm), item_full = bars + 4 * W * 8, item_empty = item_full + 16;
+  KdItem<A>* items = reinterpret_cast<KdItem<A>*>(k8_sm + Lt::item);
+  int32_t* s_ids = reinterpret_cast<int32_t*>(k8_sm + Lt::ids);
+  float* s_q = reinterpret_cast<float*>(k8_sm + Lt::q);        // two of [rows, padded][D]
+  if (tid >= 32 && tid < 32 + 2 * W) {
     const int i = tid - 32;
-    mbar_init(keys.full + 8 * i, 2);
-    mbar_init(keys.empty + 8 * i, team);
-    mbar_init(values.full + 8 * i, 1);
-    mbar_init(values.empty + 8 * i, team);
+    mbar_init(bars + 8 * i, 1);                                // full: keys, values of the teams in turn
+    mbar_init(bars + 8 * (2 * W + i), team);                   // empty
     if (i < 2) {
       mbar_init(item_full + 8 * i, kKdQueryWarps<8>);
       mbar_init(item_empty + 8 * i, W);
@@ -464,8 +459,8 @@ __global__ void __launch_bounds__(kK8Threads, 1) kv8_decode_kernel(const A a) {
   int64_t u0 = (int64_t)blockIdx.x * per, u1 = min(batch.pref[kMaxB], u0 + per);
 
   if (w >= W) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kK8RegsProducer));
-    if (blockIdx.x == 0 && w == W + 1) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kK8RegsQueries));
+    if (blockIdx.x == 0 && w == W + 3) {
       bool bad = false;
       for (int b = lane; b < a.B; b += 32) {
         bad |= a.len[b] < 0 || a.len[b] > a.n_max;
@@ -475,128 +470,171 @@ __global__ void __launch_bounds__(kK8Threads, 1) kv8_decode_kernel(const A a) {
       // (a wait that gives up flags the word two seconds later at the earliest)
       if (lane == 0) *a.status = any ? 8u : 0u;
     }
-    if (w == W) k8_produce<D>(a, batch, u0, u1, keys, smem_u32(k8_sm) + Lt::side, true);
-    else if (w == W + 1) k8_produce<D>(a, batch, u0, u1, values, 0, false);
-    else kd_queries<D, 8, E>(a, batch, u0, u1, items, s_q, item_full, item_empty, w - W - 2);
+    if (w < W + kKdQueryWarps<8>) kd_queries<D, 8, E>(a, batch, u0, u1, items, s_q, item_full, item_empty, w - W, s_ids);
     return;
   }
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kK8RegsConsumer));
 
   float* s_m = reinterpret_cast<float*>(k8_sm + Lt::m);        // [warps][8]
   float* s_l = reinterpret_cast<float*>(k8_sm + Lt::l);
-  float* s_acc = reinterpret_cast<float*>(k8_sm + Lt::acc);    // [warps][8][D]
-  const float2* side = reinterpret_cast<const float2*>(k8_sm + Lt::side);
+  float* s_acc = reinterpret_cast<float*>(k8_sm + Lt::acc(R));  // [kept][8][kK8Pitch]
   const int my_team = w / team, tile = w % team;
-  const int rows = min(8, R - tile * 8);          // <= 0: a warp with no rows
+  const int rows = my_team < nteam ? min(8, R - tile * 8) : 0;    // <= 0: a warp with no rows
   const int r0 = tile * 8 < Rp ? tile * 8 : 0;
+  // the team's slots and barriers: keys, values
+  const uint8_t* kt = k8_sm + Lt::slots(R) + 2 * min(my_team, nteam - 1) * bytes;
+  const uint8_t* vt = kt + bytes;
+  const unsigned full = bars + 16 * my_team, empty = full + 16 * W;
   // (Each wait is bounded: one that gives up marks the call, and the warp goes
   // on without waiting.)
   bool dead = false;
-  int base = 0;                                   // number of the item's first block
-  int i = my_team;                                // the team's next block, its slots and their parities
-  int sk = my_team, sv = my_team, pk = 0, pv = 0;
+  int x = my_team;                                // the team's next block of the item
+  int phase = 0;                                  // parity of its slots
+  bool sent = false;                              // the team's first warp has sent for it, and
+  float2 step = make_float2(0.0f, 0.0f);          // its steps are known
   int k = 0;                                      // number of the item
   kd_trim(a, batch, u0, u1);
 
   for (int64_t u = u0; u < u1; ++k) {
     const int buf = k & 1;
-    if (!dead && !mbar_wait(item_full + 8 * buf, (k >> 1) & 1)) dead = true;
-    dead = __any_sync(0xffffffffu, dead);
+    if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(item_full + 8 * buf, (k >> 1) & 1));
     if (dead) {
-      // the way through the items does not hang on the producer
+      // the way through the items does not hang on the queries' warps
       if (lane == 0) items[buf].seg = kd_seg(a, batch, u, u1);
       __syncwarp();
     }
-    const KdItem& it = items[buf];
-    const float* q = s_q + kd_q<D>(buf * Rp + r0, 0);
-    float* my_m = s_m + w * 8;
-    float* my_l = s_l + w * 8;
-    float* my_acc = s_acc + w * 8 * D;
+    const KdItem<A>& it = items[buf];
+    const int n = my_team < nteam ? it.seg.nfast : 0, left = it.seg.left;
+    const uint4* qa = reinterpret_cast<const uint4*>(s_q + (buf * Rp + r0) * D) + lane;
+    float* my_m = s_m + w % kept * 8;
+    float* my_l = s_l + w % kept * 8;
+    float* my_acc = s_acc + w % kept * 8 * kK8Pitch<D>;
     // the incomplete block, if it is to be done here: the teams go on in turn
-    // where the blocks ended, a few tokens at a time
-    const int64_t tail0 = it.seg.n / kBlock * kBlock, at = it.seg.bg * kBlock * D;
-    const int left = it.seg.left, to = base + it.seg.nfast, clear = base + it.seg.clear;
-    const E* Kt = reinterpret_cast<const E*>(a.c.Kt) + at;
-    const E* Vt = reinterpret_cast<const E*>(a.c.Vt) + at;
-    {
-      K8Fast<D> f;
-      k8_init<D>(f, q, it.inv + r0);
-      constexpr bool few = sizeof(E) == 2;
-      K8Rows<D> few_rows;
-      int few_at = kBlock;
-      if constexpr (few) {
-        if (left > 0 && rows > 0) few_at = kK8Few * ((i < to ? i + (to - i + nteam - 1) / nteam * nteam : i) - to);
-        if (few_at < left) k8_rows_load<D>(few_rows, Kt, Vt, few_at, left);
+    // where the blocks end, eight tokens at a time
+    const int64_t tail0 = it.seg.n / kBlock * kBlock;
+    const E* Kt = reinterpret_cast<const E*>(a.c.Kt) + it.seg.bg * kBlock * D;
+    const E* Vt = reinterpret_cast<const E*>(a.c.Vt) + it.seg.bg * kBlock * D;
+    const int few = rows <= 0 ? kBlock : kK8Few * ((x < n ? x + (n - x + nteam - 1) / nteam * nteam : x) - n);
+    if (few < left) k8_rows_ahead<D>(Kt, Vt, few, left);
+    if (x < n && !sent && !dead) {
+      const int64_t at = k8_at(a, it.seg, s_ids + buf * kKdIds, x);
+      if (tile == 0 && lane == 0) {
+        // (the team's other warps are done with both slots: nothing was sent for since)
+        if (team > 1) {
+          mbar_wait(empty, phase ^ 1);
+          mbar_wait(empty + 8, phase ^ 1);
+        }
+        k8_send(smem_u32(kt), a.c.K8 + at * bytes, bytes, full);
+        k8_send(smem_u32(vt), a.c.V8 + at * bytes, bytes, full + 8);
       }
-      while (i < to) {
-        if (!dead && !mbar_wait(keys.full + 8 * sk, pk)) dead = true;
-        const float2 step = side[sk];
-        const auto between = [&]() {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(keys.empty + 8 * sk);
-          if (!dead && !mbar_wait(values.full + 8 * sv, pv)) dead = true;
-        };
-        const uint8_t* kt = keys.data + sk * kBlock * D;
-        const uint8_t* vt = values.data + sv * kBlock * D;
-        if (rows <= 0) {
-          between();
-        } else if (i < clear) {
-          k8_block<D, false>(f, kt, vt, step.x, step.y, 0, between);
-        } else {
-          const int64_t p0 = A::kPerToken ? it.seg.own : (it.seg.blk0 + (i - base)) * kBlock;
-          k8_block<D, true>(f, kt, vt, step.x, step.y, (int)min(max(it.end[r0 + (lane >> 2)] - p0, (int64_t)0), (int64_t)kBlock),
-                            between);
+      step = *reinterpret_cast<const float2*>(a.c.scale + at * 2);
+    }
+    __syncwarp();
+    K8Fast<D> f;
+    f.inv = it.inv[r0 + (lane >> 2)];
+    f.r = -INFINITY;
+    f.l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) f.o[i][0] = f.o[i][1] = 0.0f;
+    const int64_t u_next = u + it.seg.step;
+    while (x < n) {
+      if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(full, phase));
+      const float ks = step.x, vs = step.y;
+      int64_t at = 0;
+      // The keys are read: the next block's, of this item or the next one, if
+      // that is known.
+      const auto between = [&]() {
+        __syncwarp();
+        sent = x + nteam < n;
+        if (sent) {
+          at = k8_at(a, it.seg, s_ids + buf * kKdIds, x + nteam);
+        } else if (u_next < u1 && mbar_test(item_full + 8 * (buf ^ 1), ((k + 1) >> 1) & 1)) {
+          const KdSegOf<A>& next = items[buf ^ 1].seg;
+          sent = x + nteam - n < next.nfast;
+          if (sent) at = k8_at(a, next, s_ids + (buf ^ 1) * kKdIds, x + nteam - n);
+        }
+        sent = sent && !dead;
+        if (team > 1 && lane == 0) mbar_arrive(empty);
+        if (sent) {
+          if (tile == 0 && lane == 0) {
+            if (team > 1) mbar_wait(empty, phase);
+            k8_send(smem_u32(kt), a.c.K8 + at * bytes, bytes, full);
+          }
+          step = *reinterpret_cast<const float2*>(a.c.scale + at * 2);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(values.empty + 8 * sv);
-        i += nteam;
-        if ((sk += nteam) >= keys.slots) { sk = my_team; pk ^= 1; }
-        if ((sv += nteam) >= values.slots) { sv = my_team; pv ^= 1; }
+        if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(full + 8, phase));
+      };
+      if (rows <= 0) {
+        between();
+      } else {
+        const int64_t p0 = [&] {
+          if constexpr (A::kPerToken) return it.seg.own;
+          else return (it.seg.blk0 + x) * kBlock;
+        }();
+        const bool masked = x >= it.seg.clear;
+        k8_block<D>(f, qa, kt, vt, ks, vs, masked, masked ? (int)min(max(it.end[r0 + (lane >> 2)] - p0, (int64_t)0), (int64_t)kBlock) : 0,
+                    between);
       }
-      base = to;
-      if constexpr (few) {
-        const int end = (int)min(max(it.end[r0 + (lane >> 2)] - tail0, (int64_t)0), (int64_t)left);
-        while (few_at < left) {
-          k8_rows<D>(f, few_rows, q, end - few_at, Vt + few_at * D, left - few_at);
-          few_at += kK8Few * nteam;
-          if (few_at < left) k8_rows_load<D>(few_rows, Kt, Vt, few_at, left);
-        }
+      __syncwarp();
+      if (team > 1 && lane == 0) mbar_arrive(empty + 8);
+      if (sent && tile == 0 && lane == 0) {
+        if (team > 1) mbar_wait(empty + 8, phase);
+        k8_send(smem_u32(vt), a.c.V8 + at * bytes, bytes, full + 8);
       }
-      k8_fast_store<D>(f, my_m, my_l, my_acc);
+      __syncwarp();
+      phase ^= 1;
+      x += nteam;
     }
-    if constexpr (sizeof(E) == 4) {
-      if (rows > 4 && kKdStep<8> * (i - base) < left)
-        k8_tail<D, 8, E>(Kt, Vt, i - base, nteam, left, q, it.inv + r0, it.end + r0, tail0, my_m, my_l, my_acc);
-      else if (rows > 0 && rows <= 4 && kKdStep<4> * (i - base) < left)
-        k8_tail<D, 4, E>(Kt, Vt, i - base, nteam, left, q, it.inv + r0, it.end + r0, tail0, my_m, my_l, my_acc);
+    if (few < left) {
+      const int end = (int)min(max(it.end[r0 + (lane >> 2)] - tail0, (int64_t)0), (int64_t)left);
+#pragma unroll 1
+      for (int t = few; t < left; t += kK8Few * nteam) k8_rows<D, E>(f, qa, Kt + t * D, Vt + t * D, left - t, end - t);
+    }
+    x -= n;
+    for (int w0 = W - kept; w0 >= 0; w0 -= kept) {
+      if (w0 < W - kept) bar_sync(1, W * 32);
+      if (w >= w0 && w < w0 + kept) {
+        if (w0 == W - kept) k8_store<D>(f, my_m, my_l, my_acc);
+        else k8_add<D>(f, my_m, my_l, my_acc);
+      }
     }
     bar_sync(1, W * 32);
     // merge the teams, four channels of a row to a thread
     float* part = a.part + (2 * (int64_t)blockIdx.x + (it.seg.cut0 ? 0 : 1)) * R * (D + 4);
+    const int kept_rows = kept < W ? kept * 8 : nteam * team * 8;
     for (int e = tid; e < R * (D / 4); e += W * 32) {
       const int r = e / (D / 4), c = e % (D / 4) * 4;
       float M = -INFINITY, l = 0.0f;
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int x = r; x < W * 8; x += team * 8) M = fmaxf(M, s_m[x]);   // (the row in each team)
-      for (int x = r; x < W * 8; x += team * 8) {
-        const float s = s_m[x] > -INFINITY ? ex2(s_m[x] - M) : s_l[x] == 0.0f ? 0.0f : 1.0f;
-        const float4 y = *reinterpret_cast<const float4*>(s_acc + x * D + c);
-        l = fmaf(s, s_l[x], l);
-        v.x = fmaf(s, y.x, v.x); v.y = fmaf(s, y.y, v.y); v.z = fmaf(s, y.z, v.z); v.w = fmaf(s, y.w, v.w);
+      for (int y = r; y < kept_rows; y += team * 8) M = fmaxf(M, s_m[y]);   // (the row in each team)
+      for (int y = r; y < kept_rows; y += team * 8) {
+        const float s = k8_factor(s_m[y], s_l[y], M);
+        const float4 z = *reinterpret_cast<const float4*>(s_acc + y * kK8Pitch<D> + c);
+        l = fmaf(s, s_l[y], l);
+        v.x = fmaf(s, z.x, v.x); v.y = fmaf(s, z.y, v.y); v.z = fmaf(s, z.z, v.z); v.w = fmaf(s, z.w, v.w);
       }
-      if (A::kPerToken && it.seg.bad) { M = 0.0f; l = v.x = v.y = v.z = v.w = NAN; }
+      bool mine = r / a.G < it.seg.nq;
+      if constexpr (A::kPerToken) {
+        mine = true;
+        if (it.seg.bad) { M = 0.0f; l = v.x = v.y = v.z = v.w = NAN; }
+      }
       if (!it.seg.cut0 && !it.seg.cut1) {
-        if (A::kPerToken || r / a.G < it.seg.nq) kd_store<D>(a, it.seg, r, c, M, l, v);
+        if (mine) kd_store<D>(a, it.seg, r, c, M, l, v);
       } else {
         *reinterpret_cast<float4*>(part + r * (D + 4) + c) = v;
         if (c == 0) { part[r * (D + 4) + D] = M; part[r * (D + 4) + D + 1] = l; }
       }
     }
-    u += it.seg.step;
+    u = u_next;
     bar_sync(1, W * 32);
     if (lane == 0) mbar_arrive(item_empty + 8 * buf);
   }
-  if (dead && lane == 0) atomicOr(a.status, 4u);
+  if (dead) {
+    // copies in flight land before the CTA can end (of whichever phase)
+    for (int i = 0; i < 4; ++i) mbar_wait(full + 8 * (i & 1), i >> 1);
+    if (lane == 0) atomicOr(a.status, 4u);
+  }
 }
 
 namespace {
@@ -612,7 +650,7 @@ int k8_whole(const csa_shape* s, int n_sel) { return k8_blocks(s, n_sel) <= kK8W
 // CTAs of the decode kernel: one per SM, no more than there can be units
 int k8_ctas(const csa_shape* s, int T, int n_sel) {
   const int64_t units = (int64_t)s->B * s->Hkv * (n_sel ? T : 1) * (k8_whole(s, n_sel) ? 1 : k8_blocks(s, n_sel));
-  const int nsm = sm_count() < kKdMaxCtas ? sm_count() : kKdMaxCtas;
+  const int nsm = sm_count() < Kv8DecodeArgs<true>::kMaxCtas ? sm_count() : Kv8DecodeArgs<true>::kMaxCtas;
   return (int)(units < nsm ? units : nsm);
 }
 
@@ -628,21 +666,8 @@ size_t k8_workspace(const csa_shape* s, int T, int n_sel) {
 constexpr int kK8SharedBytes = 232448 - ((int)sizeof(KdBatch) + 127) / 128 * 128;
 template <int D, typename E, typename A>
 cudaError_t launch_kv8_decode_t(A a, int ncta, cudaStream_t st) {
-  const int R = kd_rows(a), rest = K8Layout<D>::ring(R);
-  // one slot per team in each ring (an SM's shared memory holds that for every
-  // number of rows), then more while there is room: keys first, whose copies
-  // have less time (the values' come while the warp is at the keys)
-  constexpr int bytes = kBlock * D;
-  const int nteam = kK8Warps / k8_team((R + 7) / 8);
-  int nk = 1, nv = 1;
-  for (bool more = true; more;) {
-    more = false;
-    if ((nk + 1) * nteam <= kK8MaxStages && nteam * (nk + 1 + nv) * bytes <= kK8SharedBytes - rest) { ++nk; more = true; }
-    if ((nv + 1) * nteam <= kK8MaxStages && nteam * (nk + nv + 1) * bytes <= kK8SharedBytes - rest) { ++nv; more = true; }
-  }
-  a.slotsK = nk * nteam;
-  a.slotsV = nv * nteam;
-  const int smem = rest + (a.slotsK + a.slotsV) * bytes;
+  const int R = kd_rows(a), nteam = kK8Warps / k8_team((R + 7) / 8);
+  const int smem = K8Layout<D, A>::slots(R) + 2 * nteam * kBlock * D;
   const cudaError_t e =
       cudaFuncSetAttribute(kv8_decode_kernel<D, E, A>, cudaFuncAttributeMaxDynamicSharedMemorySize, kK8SharedBytes);
   if (e != cudaSuccess) return e;
