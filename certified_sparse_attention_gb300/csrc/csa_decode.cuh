@@ -14,10 +14,8 @@
 //   kMaxCtas                      CTAs of a call at most
 //   kPlainQ                       query rows keep their own digits: log2(e) /
 //                                 sqrt(d) goes into what undoes a row's scale
-//   pitch<D>(rows), put<D>(q, r, lane, x, up)
-//                                 how query rows lie in shared memory: floats of
-//                                 `rows` of them, and channels lane D / 32 ... of
-//                                 row r, x up, being laid down
+//   put<D>(q, r, lane, x, up)     lays channels lane D / 32 ... of query row r,
+//                                 x up, down in shared memory
 //   top<D>(c)                     what the kernel wants to know of the channel c
 //                                 of a row's largest query element
 #pragma once
@@ -133,21 +131,16 @@ struct KdTokenSeg : KdSeg {
 template <typename A>
 using KdSegOf = std::conditional_t<A::kPerToken, KdTokenSeg, KdSeg>;
 
+// item i of sequence b, whose units begin at v0 of them at unit u
 template <typename A>
-__device__ __forceinline__ KdSegOf<A> kd_seg(const A& a, const KdBatch& batch, int64_t u, int64_t u1) {
+__device__ __forceinline__ KdSegOf<A> kd_seg_at(const A& a, const KdBatch& batch, int b, int i, int64_t units, int64_t v0, int64_t u,
+                                                int64_t u1) {
   KdSegOf<A> s;
-  // the last b with pref[b] <= u (sequences past B hold no units)
-  int lo = 0, hi = a.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (batch.pref[mid] <= u) lo = mid; else hi = mid - 1;
-  }
-  s.b = lo;
-  s.n = batch.len[lo];
-  s.nq = batch.nq[lo];
-  const int64_t units = kd_units(a, s.n), rem = u - batch.pref[lo], whole = kd_blocks(a, s.n);
-  s.g = (rem | units) >> 32 ? (int)(rem / units) : (int)((unsigned)rem / (unsigned)units);
-  const int64_t v0 = rem - s.g * units, v1 = min(units, v0 + (u1 - u));
+  s.b = b;
+  s.n = batch.len[b];
+  s.nq = batch.nq[b];
+  const int64_t whole = kd_blocks(a, s.n), v1 = min(units, v0 + (u1 - u));
+  s.g = i;
   if constexpr (A::kPerToken) {
     s.t = s.g / a.Hkv;
     s.g -= s.t * a.Hkv;
@@ -172,6 +165,30 @@ __device__ __forceinline__ KdSegOf<A> kd_seg(const A& a, const KdBatch& batch, i
   s.clear = (int)min(max(clear, (int64_t)0), (int64_t)s.nfast);
   return s;
 }
+template <typename A>
+__device__ __forceinline__ KdSegOf<A> kd_seg(const A& a, const KdBatch& batch, int64_t u, int64_t u1) {
+  // the last b with pref[b] <= u (sequences past B hold no units)
+  int lo = 0, hi = a.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (batch.pref[mid] <= u) lo = mid; else hi = mid - 1;
+  }
+  const int64_t units = kd_units(a, batch.len[lo]), rem = u - batch.pref[lo];
+  const int i = (rem | units) >> 32 ? (int)(rem / units) : (int)((unsigned)rem / (unsigned)units);
+  return kd_seg_at(a, batch, lo, i, units, rem - i * units, u, u1);
+}
+// the one after s, at its end u < u1
+template <typename A>
+__device__ __forceinline__ KdSegOf<A> kd_next(const A& a, const KdBatch& batch, const KdSegOf<A>& s, int64_t u, int64_t u1) {
+  int b = s.b, i = s.g + 1;
+  if constexpr (A::kPerToken) i += s.t * a.Hkv;
+  if (u >= batch.pref[b + 1]) {
+    i = 0;
+    do ++b;
+    while (u >= batch.pref[b + 1]);
+  }
+  return kd_seg_at(a, batch, b, i, kd_units(a, batch.len[b]), 0, u, u1);
+}
 
 // kPerToken: list entries of an item that its queries' warps leave in shared memory
 constexpr int kKdIds = 128;
@@ -185,14 +202,17 @@ __device__ __forceinline__ const int32_t* kd_list(const A& a, KdTokenSeg& s) {
   const int64_t row = ((int64_t)s.b * a.T + s.t) * a.Hkv + s.g, pos = s.n - s.nq + s.t;
   const int32_t* ids = a.blocks + row * a.n_sel;
   const int64_t own = pos < 0 ? -1 : pos / kBlock;
+  // (entries are looked at from `count` on too, so that nothing waits for it)
   const int count = a.count[row];
   bool bad = count < 0 || count > a.n_sel;
-  for (int x = lane; x < (bad ? 0 : count); x += 32) {
+  int end = -1;
+  for (int x = lane; x < a.n_sel; x += 32) {
     const int id = ids[x], before = x ? ids[x - 1] : -1;
-    bad |= id <= before || id > own;
+    bad |= x < count && (id <= before || id > own);
+    if (x == count - 1) end = id;
   }
   s.bad = __any_sync(0xffffffffu, bad);
-  const int64_t last = s.bad || count == 0 ? -1 : ids[count - 1];
+  const int64_t last = s.bad ? -1 : __reduce_max_sync(0xffffffffu, end);
   const bool tail = last == s.n / kBlock;
   const int coded = s.bad ? 0 : count - tail;
   s.own = own * kBlock;
@@ -416,11 +436,8 @@ __device__ __forceinline__ unsigned half_pair_rz(float x, float y) {
   return r;
 }
 
-// The queries of an item and what else its warps need of it: filled by a
-// producer warp, four rows at a time, an item ahead; tiles of 8 by two, half of
-// the rows each (one took 12 us for 64 rows; drafts of 24 rows 114 us, with one
-// 121, the batch of 64 with 8 rows 126 and 128).
-template <int RT> constexpr int kKdQueryWarps = RT == 8 ? 2 : 1;
+// The queries of an item and what else its warps need of it: filled by producer
+// warps, four rows at a time, an item ahead.
 template <typename A>
 struct KdItem {
   KdSegOf<A> seg;
@@ -429,73 +446,49 @@ struct KdItem {
   int top[CSA_KV4_MAX_ROWS];        // of the channel of the largest of row r: A::top
 };
 
-template <int D, int RT, typename E, typename A>
-__device__ __forceinline__ void kd_queries(const A& a, const KdBatch& batch, int64_t u0, int64_t u1,
-                                           KdItem<A>* items, float* s_q, unsigned full, unsigned empty, int part,
-                                           int32_t* s_ids = nullptr) {
+// the rows [r0, r1) of an item, but for it.seg
+template <int D, typename E, typename A>
+__device__ __forceinline__ void kd_item_queries(const A& a, const KdSegOf<A>& sg, KdItem<A>& it, float* q, int r0, int r1) {
   constexpr int CPL = D / 32;
   const int lane = threadIdx.x & 31;
-  const int R = kd_rows(a), Rp = (R + RT - 1) / RT * RT, per = Rp / kKdQueryWarps<RT>;
-  int k = 0;
-  bool dead = false;
-  kd_trim(a, batch, u0, u1);
-  for (int64_t u = u0; u < u1 && !dead; ++k) {
-    const int buf = k & 1;
-    dead = !mbar_wait(empty + 8 * buf, ((k >> 1) & 1) ^ 1);
-    dead = __any_sync(0xffffffffu, dead);
-    if (dead) break;
-    KdItem<A>& it = items[buf];
-    KdSegOf<A> sg = kd_seg(a, batch, u, u1);
-    if constexpr (A::kPerToken) {
-      const int32_t* ids = kd_list(a, sg) + sg.blk0;
-      if (part == 0)
-        for (int x = lane; x < min(sg.nfast, kKdIds); x += 32) s_ids[buf * kKdIds + x] = ids[x];
-    }
-    if (lane == 0 && part == 0) it.seg = sg;
-    const E* base = reinterpret_cast<const E*>(a.q) + sg.b * a.qs.b + (int64_t)sg.g * a.G * a.qs.h + lane * CPL;
-    float* q = s_q + buf * A::template pitch<D>(Rp);
+  const E* base = reinterpret_cast<const E*>(a.q) + sg.b * a.qs.b + (int64_t)sg.g * a.G * a.qs.h + lane * CPL;
 #pragma unroll 4
-    for (int r = part * per; r < (part + 1) * per; ++r) {
-      int t = r / a.G;
-      if constexpr (A::kPerToken) t = r < R ? sg.t : a.T;
-      float x[CPL];
+  for (int r = r0; r < r1; ++r) {
+    int t = r / a.G;
+    if constexpr (A::kPerToken) t = r < a.G ? sg.t : a.T;
+    float x[CPL];
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) x[c] = 0.0f;
-      if (t < sg.nq) {
-        const E* src = base + t * a.qs.t + (A::kPerToken ? r : r - t * a.G) * a.qs.h;
-        if (CPL == 4) {
-          const float4 v = Elem<E>::get4(src);
-          x[0] = v.x; x[1] = v.y; x[CPL - 2] = v.z; x[CPL - 1] = v.w;
-        } else {
-          const float2 v = Elem<E>::get2(src);
-          x[0] = v.x; x[1] = v.y;
-        }
-      }
-      // the row's largest in magnitude, without its last 7 bits, and its channel
-      unsigned key = 0;
-#pragma unroll
-      for (int c = 0; c < CPL; ++c) {
-        if constexpr (!A::kPlainQ) x[c] *= a.rs;
-        key = max(key, (__float_as_uint(x[c]) & 0x7fffff80u) + lane * CPL + c);
-      }
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, m));
-      const float top = __uint_as_float(key & ~127u);
-      const int e = top > 0.0f && top < INFINITY ? min(max(11 - exponent(top), -100), 100) : 0;
-      const float up = pow2i(e);
-      A::template put<D>(q, r, lane, x, up);
-      if (lane == 0) {
-        const int c = key & 127;
-        it.top[r] = A::template top<D>(c);
-        it.inv[r] = A::kPlainQ ? a.rs * pow2i(-e) : pow2i(-e);
-        it.end[r] = t < sg.nq ? sg.n - sg.nq + t + 1 : 0;
+    for (int c = 0; c < CPL; ++c) x[c] = 0.0f;
+    if (t < sg.nq) {
+      const E* src = base + t * a.qs.t + (A::kPerToken ? r : r - t * a.G) * a.qs.h;
+      if (CPL == 4) {
+        const float4 v = Elem<E>::get4(src);
+        x[0] = v.x; x[1] = v.y; x[CPL - 2] = v.z; x[CPL - 1] = v.w;
+      } else {
+        const float2 v = Elem<E>::get2(src);
+        x[0] = v.x; x[1] = v.y;
       }
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(full + 8 * buf);
-    u += sg.step;
+    // the row's largest in magnitude, without its last 7 bits, and its channel
+    unsigned key = 0;
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) {
+      if constexpr (!A::kPlainQ) x[c] *= a.rs;
+      key = max(key, (__float_as_uint(x[c]) & 0x7fffff80u) + lane * CPL + c);
+    }
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, m));
+    const float top = __uint_as_float(key & ~127u);
+    const int e = top > 0.0f && top < INFINITY ? min(max(11 - exponent(top), -100), 100) : 0;
+    const float up = pow2i(e);
+    A::template put<D>(q, r, lane, x, up);
+    if (lane == 0) {
+      const int c = key & 127;
+      it.top[r] = A::template top<D>(c);
+      it.inv[r] = A::kPlainQ ? a.rs * pow2i(-e) : pow2i(-e);
+      it.end[r] = t < sg.nq ? sg.n - sg.nq + t + 1 : 0;
+    }
   }
-  if (dead && lane == 0) atomicOr(a.status, 4u);
 }
 
 // Joins the parts of the items that were cut: CTAs (j, y) own the item of

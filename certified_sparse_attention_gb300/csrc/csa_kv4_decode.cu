@@ -105,8 +105,6 @@ struct Kv4DecodeArgs : DecodeArgs {
   static constexpr bool kPerToken = false, kPlainQ = false;
   static constexpr int kMaxCtas = 256;     // one per SM
   template <int D>
-  static __host__ __device__ __forceinline__ constexpr int pitch(int rows) { return kd_q<D>(rows, 0); }
-  template <int D>
   static __device__ __forceinline__ void put(float* q, int r, int lane, const float (&x)[D / 32], float up) {
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) q[kd_q<D>(r, lane * (D / 32)) + c] = x[c] * up;
@@ -641,6 +639,35 @@ __device__ __forceinline__ void kd_fast_store(KdFast<D, RT>& f, float* s_m, floa
   }
 }
 
+
+// Queries come by one producer warp, tiles of 8 by two, half of the rows each (one
+// took 12 us for 64 rows; drafts of 24 rows 114 us, with one 121, the batch of 64
+// with 8 rows 126 and 128).
+template <int RT> constexpr int kKdQueryWarps = RT == 8 ? 2 : 1;
+
+template <int D, int RT, typename E>
+__device__ __forceinline__ void kd_queries(const Kv4DecodeArgs& a, const KdBatch& batch, int64_t u0, int64_t u1,
+                                           KdItem<Kv4DecodeArgs>* items, float* s_q, unsigned full, unsigned empty, int part) {
+  const int lane = threadIdx.x & 31;
+  const int R = a.T * a.G, Rp = (R + RT - 1) / RT * RT, per = Rp / kKdQueryWarps<RT>;
+  int k = 0;
+  bool dead = false;
+  kd_trim(a, batch, u0, u1);
+  for (int64_t u = u0; u < u1 && !dead; ++k) {
+    const int buf = k & 1;
+    dead = !mbar_wait(empty + 8 * buf, ((k >> 1) & 1) ^ 1);
+    dead = __any_sync(0xffffffffu, dead);
+    if (dead) break;
+    KdItem<Kv4DecodeArgs>& it = items[buf];
+    const KdSeg sg = kd_seg(a, batch, u, u1);
+    if (lane == 0 && part == 0) it.seg = sg;
+    kd_item_queries<D, E>(a, sg, it, s_q + buf * kd_q<D>(Rp, 0), part * per, (part + 1) * per);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(full + 8 * buf);
+    u += sg.step;
+  }
+  if (dead && lane == 0) atomicOr(a.status, 4u);
+}
 
 // shared memory: barriers (keys full, empty, values full, empty, items full,
 // empty), items, warp sums, q rows of two items, the rings

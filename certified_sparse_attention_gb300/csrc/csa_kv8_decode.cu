@@ -38,17 +38,13 @@
 
 namespace csa {
 
-constexpr int kK8Warps = 12;      // consumer warps of a CTA: three warpgroups; two warps of a
-                                  // fourth one fetch the queries
-constexpr int kK8Threads = (kK8Warps + 4) * 32;
-// registers: 512 threads start with 128 each; those of the queries give theirs up
-constexpr int kK8RegsConsumer = 144, kK8RegsQueries = 80;
-static_assert(3 * kK8RegsConsumer + kK8RegsQueries <= 4 * 128, "more registers than the launch has");
-// warps of a team, for 1 .. 8 tiles of 8 rows (above 6 tiles: one team, four warps
-// left over)
-__host__ __device__ constexpr int k8_team(int ntile) { return ntile <= 4 ? ntile : ntile <= 6 ? 6 : 8; }
+// W: consumer warps of a CTA
+constexpr int kK8Side = 2;        // ... and warps that fetch the queries and merge the sums
+template <int W> constexpr int kK8Threads = (W + kK8Side) * 32;
+constexpr int kK8Items = 3;       // items whose queries are there at once
+// warps of a team, for 1 .. 8 tiles of 8 rows (those that are left over idle)
+__host__ __device__ constexpr int k8_team(int ntile) { return ntile; }
 
-__device__ __forceinline__ unsigned half_bits(float x) { return __half_as_ushort(__float2half_rn(x)); }
 // high parts of x and y, and what is left of them in units of 2^-12
 __device__ __forceinline__ void k8_parts(float x, float y, unsigned& hi, unsigned& lo) {
   hi = half_pair(x, y);
@@ -62,14 +58,16 @@ struct Kv8DecodeArgs : DecodeArgs {
   const int32_t* blocks;  // LIST: [B][T][Hkv][n_sel], count [B][T][Hkv]
   const int32_t* count;
   int n_sel;
-  static constexpr int kLead = 8, kTailBase = 3, kTailStep = 8;
+  // Fitted to the times of single CTAs (batch of 64, 8 query heads to a KV head: a
+  // block 0.355 us, an item 1.5 to 3 us, its incomplete block 1.5 us).  Leads of 5
+  // and of 12 take the same time there; 128 sequences of up to 2000 tokens take 101,
+  // 94 and 92 us with 5, 8 and 12, one CTA's worth of drafts 115, 116 and 118.
+  static constexpr int kLead = 8, kTailBase = 4, kTailStep = 64;
   static constexpr bool kPerToken = LIST, kPlainQ = true;
   static constexpr int kMaxCtas = 256;     // one per SM
   // Query rows as the matrix instructions' operand: of each tile of 8 rows, the
   // channels 64 h + 16 tid + 4 s + (0..3) of row gid are 16 bytes, (h, s, lane) in
   // that order: high parts of the first two, their low parts, the same of the others.
-  template <int D>
-  static __host__ __device__ __forceinline__ constexpr int pitch(int rows) { return rows * D; }
   template <int D>
   static __device__ __forceinline__ void put(float* q, int r, int lane, const float (&x)[D / 32], float up) {
     const int c = lane * (D / 32);
@@ -244,6 +242,8 @@ __device__ __forceinline__ void bf16_parts(float x, float y, unsigned (&p)[N]) {
   }
 }
 // two channels of a row
+template <typename E> struct PairOf { typedef unsigned T; };
+template <> struct PairOf<float> { typedef float2 T; };
 __device__ __forceinline__ float2 pair_of(const __nv_bfloat16* p) {
   const unsigned u = *reinterpret_cast<const unsigned*>(p);
   return make_float2(bf16_low(u), bf16_high(u));
@@ -267,6 +267,10 @@ __device__ __forceinline__ void k8_rows(K8Fast<D>& f, const uint4* qa, const E* 
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
   const bool in = gid < left;
   const E* kr = K + gid * D + 16 * tid;
+  const E* vr = V + gid * D + 2 * tid;
+  typename PairOf<E>::T vraw[D / 8];       // (on their way while the scores are made)
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) vraw[i] = in ? *reinterpret_cast<const typename PairOf<E>::T*>(vr + 8 * i) : typename PairOf<E>::T();
   float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int h = 0; h < D / 64; ++h)
@@ -297,10 +301,9 @@ __device__ __forceinline__ void k8_rows(K8Fast<D>& f, const uint4* qa, const E* 
   unsigned p[3];
   bf16_parts<3>(pa, pb, p);
   bool odd = false;
-  const E* vr = V + gid * D + 2 * tid;
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) {
-    float2 v = in ? pair_of(vr + 8 * i) : make_float2(0.0f, 0.0f);
+    const float2 v = pair_of(reinterpret_cast<const E*>(&vraw[i]));
     // (infinities and NaNs are left to the loop below)
     const bool ox = odd_number(v.x), oy = odd_number(v.y);
     odd = odd || ox || oy;
@@ -362,43 +365,20 @@ __device__ __forceinline__ void k8_store(K8Fast<D>& f, float* s_m, float* s_l, f
 }
 // factor of sums relative to m where they become relative to M
 __device__ __forceinline__ float k8_factor(float m, float l, float M) { return m > -INFINITY ? ex2(m - M) : l == 0.0f ? 0.0f : 1.0f; }
-// the same where another warp's sums of the rows lie already: both
-template <int D>
-__device__ __forceinline__ void k8_add(K8Fast<D>& f, float* s_m, float* s_l, float* s_acc) {
-  const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
-  f.l += __shfl_xor_sync(0xffffffffu, f.l, 1);
-  f.l += __shfl_xor_sync(0xffffffffu, f.l, 2);
-  const float m = s_m[gid], l = s_l[gid], M = fmaxf(f.r, m), mine = k8_factor(f.r, f.l, M), its = k8_factor(m, l, M);
-  __syncwarp();
-  if (tid == 0) { s_m[gid] = M; s_l[gid] = fmaf(its, l, mine * f.l); }
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    float2* at = reinterpret_cast<float2*>(s_acc + gid * kK8Pitch<D> + 8 * i + 2 * tid);
-    const float2 x = *at;
-    *at = make_float2(fmaf(its, x.x, mine * f.o[i][0]), fmaf(its, x.y, mine * f.o[i][1]));
-  }
-}
 
 // --------------------------------------------------------------- the kernel
 
-// Warps whose sums lie in shared memory at once: four (and the others add theirs
-// in turn) where twelve slots of keys and of values leave no room for more.
-template <int D>
-__host__ __device__ constexpr int k8_kept(int team) { return D == 128 && team == 1 ? 4 : kK8Warps; }
-
-// shared memory: barriers (keys, values full, empty, items full, empty), items,
-// list entries and q rows of two items, warp sums, the slots
-template <int D, typename A>
+// shared memory: barriers (keys and values full, empty, items full, sums full,
+// empty), items, their list entries, warp sums, their q rows, the slots
+template <int D, int W, typename A>
 struct K8Layout {
-  static constexpr int item = (4 * kK8Warps + 4) * 8;
-  static constexpr int ids = item + 2 * (int)sizeof(KdItem<A>);
-  static constexpr int m = ids + (A::kPerToken ? 2 * kKdIds * 4 : 0);
-  static constexpr int l = m + kK8Warps * 8 * 4;
-  static constexpr int q = (l + kK8Warps * 8 * 4 + 15) / 16 * 16;
-  static __host__ __device__ int acc(int rows) { return q + 2 * ((rows + 7) / 8 * 8) * D * 4; }
-  static __host__ __device__ int slots(int rows) {
-    return (acc(rows) + k8_kept<D>(k8_team((rows + 7) / 8)) * 8 * kK8Pitch<D> * 4 + 127) / 128 * 128;
-  }
+  static constexpr int item = (4 * W + kK8Items + 3) * 8;
+  static constexpr int ids = item + kK8Items * (int)sizeof(KdItem<A>);
+  static constexpr int m = ids + (A::kPerToken ? kK8Items * kKdIds * 4 : 0);
+  static constexpr int l = m + W * 8 * 4;
+  static constexpr int acc = (l + W * 8 * 4 + 15) / 16 * 16;
+  static constexpr int q = acc + W * 8 * kK8Pitch<D> * 4;
+  static __host__ __device__ int slots(int rows) { return (q + kK8Items * ((rows + 7) / 8 * 8) * D * 4 + 127) / 128 * 128; }
 };
 
 // whether the phase of parity `parity` is complete, for a whole warp
@@ -428,39 +408,141 @@ __device__ __forceinline__ int64_t k8_at(const A& a, const KdSegOf<A>& s, const 
   }
 }
 
-template <int D, typename E, typename A>
-__global__ void __launch_bounds__(kK8Threads, 1) kv8_decode_kernel(const A a) {
+// D / 32 floats at p (a lane's channels of a row)
+template <int CPL>
+__device__ __forceinline__ void floats_in(float (&x)[CPL], const float* p) {
+  if (CPL == 4) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    x[0] = v.x; x[1] = v.y; x[CPL - 2] = v.z; x[CPL - 1] = v.w;
+  } else {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    x[0] = v.x; x[1] = v.y;
+  }
+}
+template <int CPL>
+__device__ __forceinline__ void floats_out(float* p, const float (&x)[CPL]) {
+  if (CPL == 4) *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[CPL - 2], x[CPL - 1]);
+  else *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+}
+
+// The item's sums from its teams' (in regions of a warp's 8 rows each), by a side
+// warp: rows [r0, r1), four at a time.  First a lane to a team, then D / 32 channels
+// to a lane.
+template <int D, typename A>
+__device__ __forceinline__ void k8_merge(const A& a, const KdSegOf<A>& s, int nteam, int team, const float* s_m, const float* s_l,
+                                         const float* s_acc, int r0, int r1) {
+  constexpr int CPL = D / 32, N = 4;
+  const int lane = threadIdx.x & 31, R = kd_rows(a), glog = 31 - __clz(a.G);
+  float* part = a.part + (2 * (int64_t)blockIdx.x + (s.cut0 ? 0 : 1)) * R * (D + 4) + lane * CPL;
+  for (int r = r0; r < min(r1, R); r += N) {
+    float M[N], l[N], f[N], v[N][CPL];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int x = lane * team * 8 + r + i;
+      const bool in = lane < nteam;
+      M[i] = f[i] = in ? s_m[x] : -INFINITY;
+      l[i] = in ? s_l[x] : 0.0f;
+    }
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) M[i] = fmaxf(M[i], __shfl_xor_sync(0xffffffffu, M[i], o));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      M[i] = __shfl_sync(0xffffffffu, M[i], 0);
+      f[i] = k8_factor(f[i], l[i], M[i]);
+      l[i] *= f[i];
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) v[i][c] = 0.0f;
+    }
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+#pragma unroll 2
+    for (int y = 0; y < nteam; ++y) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float z[CPL];
+        floats_in<CPL>(z, s_acc + (y * team * 8 + r + i) * kK8Pitch<D> + lane * CPL);
+        const float w = __shfl_sync(0xffffffffu, f[i], y);
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) v[i][c] = fmaf(w, z[c], v[i][c]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      l[i] = __shfl_sync(0xffffffffu, l[i], 0);
+      if (r + i >= R) continue;
+      int t = (r + i) >> glog, h = s.g * a.G + ((r + i) & (a.G - 1));
+      if constexpr (A::kPerToken) {
+        t = s.t;
+        if (s.bad) {
+          M[i] = 0.0f;
+          l[i] = NAN;
+#pragma unroll
+          for (int c = 0; c < CPL; ++c) v[i][c] = NAN;
+        }
+      }
+      if (s.cut0 || s.cut1) {
+        float* to = part + (r + i) * (D + 4);
+        floats_out<CPL>(to, v[i]);
+        if (lane == 0) { to[D] = M[i]; to[D + 1] = l[i]; }
+      } else if (t < s.nq) {
+        const int64_t row = ((int64_t)s.b * a.T + t) * a.Hq + h;
+        // l = 0 only where nothing was attended to
+        const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) v[i][c] = l[i] == 0.0f ? 0.0f : v[i][c] * inv;
+        floats_out<CPL>(a.o + row * D + lane * CPL, v[i]);
+        if (lane == 0 && a.lse) a.lse[row] = l[i] == 0.0f ? -INFINITY : (M[i] + log2f(l[i])) * 0.69314718055994531f;
+      }
+    }
+  }
+}
+
+template <int D, int W, typename E, typename A>
+__global__ void __launch_bounds__(kK8Threads<W>, 1) kv8_decode_kernel(const A a) {
   pdl_entry();
-  using Lt = K8Layout<D, A>;
-  constexpr int W = kK8Warps;
+  using Lt = K8Layout<D, W, A>;
   constexpr unsigned bytes = kBlock * D;
   __shared__ KdBatch batch;
   extern __shared__ __align__(128) uint8_t k8_sm[];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int R = kd_rows(a), Rp = (R + 7) / 8 * 8;
   // teams: warps that share a block, one tile of rows each
-  const int team = k8_team(Rp / 8), nteam = W / team, kept = k8_kept<D>(team);
-  const unsigned bars = smem_u32(k8_sm), item_full = bars + 4 * W * 8, item_empty = item_full + 16;
+  const int team = k8_team(Rp / 8), nteam = W / team;
+  const unsigned bars = smem_u32(k8_sm), item_full = bars + 4 * W * 8, sums_full = item_full + 8 * kK8Items, sums_empty = sums_full + 8;
   KdItem<A>* items = reinterpret_cast<KdItem<A>*>(k8_sm + Lt::item);
   int32_t* s_ids = reinterpret_cast<int32_t*>(k8_sm + Lt::ids);
-  float* s_q = reinterpret_cast<float*>(k8_sm + Lt::q);        // two of [rows, padded][D]
+  float* s_q = reinterpret_cast<float*>(k8_sm + Lt::q);        // [items][rows, padded][D]
+  float* s_m = reinterpret_cast<float*>(k8_sm + Lt::m);        // [warps][8]
+  float* s_l = reinterpret_cast<float*>(k8_sm + Lt::l);
+  float* s_acc = reinterpret_cast<float*>(k8_sm + Lt::acc);    // [warps][8][kK8Pitch]
   if (tid >= 32 && tid < 32 + 2 * W) {
     const int i = tid - 32;
     mbar_init(bars + 8 * i, 1);                                // full: keys, values of the teams in turn
     mbar_init(bars + 8 * (2 * W + i), team);                   // empty
-    if (i < 2) {
-      mbar_init(item_full + 8 * i, kKdQueryWarps<8>);
-      mbar_init(item_empty + 8 * i, W);
+    if (i < kK8Items) mbar_init(item_full + 8 * i, kK8Side);
+    if (i == 0) {
+      mbar_init(sums_full, W);
+      mbar_init(sums_empty, kK8Side);
     }
     fence_barrier_init();
   }
   kd_batch(a, batch);
   const int64_t per = kd_run(batch, gridDim.x);
   int64_t u0 = (int64_t)blockIdx.x * per, u1 = min(batch.pref[kMaxB], u0 + per);
+  kd_trim(a, batch, u0, u1);
+  // (Each wait is bounded: one that gives up marks the call, and the warp goes
+  // on without waiting.)
+  bool dead = false;
 
   if (w >= W) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kK8RegsQueries));
-    if (blockIdx.x == 0 && w == W + 3) {
+    // The side warps: each item's queries and what else is known of it, ahead of
+    // the sums, which they merge while the others are at the next items.
+    const int part = w - W;
+    if (blockIdx.x == 0 && part == 1) {
       bool bad = false;
       for (int b = lane; b < a.B; b += 32) {
         bad |= a.len[b] < 0 || a.len[b] > a.n_max;
@@ -470,14 +552,40 @@ __global__ void __launch_bounds__(kK8Threads, 1) kv8_decode_kernel(const A a) {
       // (a wait that gives up flags the word two seconds later at the earliest)
       if (lane == 0) *a.status = any ? 8u : 0u;
     }
-    if (w < W + kKdQueryWarps<8>) kd_queries<D, 8, E>(a, batch, u0, u1, items, s_q, item_full, item_empty, w - W, s_ids);
+    int64_t u = u0;
+    KdSegOf<A> sg;
+    const auto fetch = [&](int buf) {
+      if (u >= u1) return;
+      KdItem<A>& it = items[buf];
+      sg = u == u0 ? kd_seg(a, batch, u, u1) : kd_next(a, batch, sg, u, u1);
+      if constexpr (A::kPerToken) {
+        const int32_t* ids = kd_list(a, sg) + sg.blk0;
+        if (part == 0)
+          for (int x = lane; x < min(sg.nfast, kKdIds); x += 32) s_ids[buf * kKdIds + x] = ids[x];
+      }
+      if (lane == 0 && part == 0) it.seg = sg;
+      kd_item_queries<D, E>(a, sg, it, s_q + buf * Rp * D, part * (Rp / kK8Side), (part + 1) * (Rp / kK8Side));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(item_full + 8 * buf);
+      u += sg.step;
+    };
+    for (int buf = 0; buf < kK8Items; ++buf) fetch(buf);
+    int64_t done = u0;
+    for (int k = 0, buf = 0; done < u1; ++k) {
+      if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(sums_full, k & 1));
+      const KdSegOf<A> s = items[buf].seg;
+      k8_merge<D>(a, s, nteam, team, s_m, s_l, s_acc, part * (Rp / kK8Side), (part + 1) * (Rp / kK8Side));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sums_empty);
+      done += s.step;
+      bar_sync(1, kK8Side * 32);                  // both have read the item
+      fetch(buf);
+      if (++buf == kK8Items) buf = 0;
+    }
+    if (dead && lane == 0) atomicOr(a.status, 4u);
     return;
   }
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kK8RegsConsumer));
 
-  float* s_m = reinterpret_cast<float*>(k8_sm + Lt::m);        // [warps][8]
-  float* s_l = reinterpret_cast<float*>(k8_sm + Lt::l);
-  float* s_acc = reinterpret_cast<float*>(k8_sm + Lt::acc(R));  // [kept][8][kK8Pitch]
   const int my_team = w / team, tile = w % team;
   const int rows = my_team < nteam ? min(8, R - tile * 8) : 0;    // <= 0: a warp with no rows
   const int r0 = tile * 8 < Rp ? tile * 8 : 0;
@@ -485,35 +593,31 @@ __global__ void __launch_bounds__(kK8Threads, 1) kv8_decode_kernel(const A a) {
   const uint8_t* kt = k8_sm + Lt::slots(R) + 2 * min(my_team, nteam - 1) * bytes;
   const uint8_t* vt = kt + bytes;
   const unsigned full = bars + 16 * my_team, empty = full + 16 * W;
-  // (Each wait is bounded: one that gives up marks the call, and the warp goes
-  // on without waiting.)
-  bool dead = false;
-  int x = my_team;                                // the team's next block of the item
+  // An item's work goes to the teams in turn, its blocks and then its incomplete
+  // block by eight tokens, and on with the next item.
+  int x = my_team;                                // the team's next turn in the item
   int phase = 0;                                  // parity of its slots
-  bool sent = false;                              // the team's first warp has sent for it, and
-  float2 step = make_float2(0.0f, 0.0f);          // its steps are known
-  int k = 0;                                      // number of the item
-  kd_trim(a, batch, u0, u1);
+  bool sent = false;                              // the team's first warp has sent for that block,
+  float2 step = make_float2(0.0f, 0.0f);          // and its steps are known
+  int k = 0, buf = 0, turn = 0;                   // number of the item, its place, its parity there
 
   for (int64_t u = u0; u < u1; ++k) {
-    const int buf = k & 1;
-    if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(item_full + 8 * buf, (k >> 1) & 1));
+    if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(item_full + 8 * buf, turn));
     if (dead) {
-      // the way through the items does not hang on the queries' warps
+      // the way through the items does not hang on the side warps
       if (lane == 0) items[buf].seg = kd_seg(a, batch, u, u1);
       __syncwarp();
     }
+    const int buf1 = buf + 1 == kK8Items ? 0 : buf + 1, turn1 = buf1 ? turn : turn ^ 1;      // the next item's
     const KdItem<A>& it = items[buf];
     const int n = my_team < nteam ? it.seg.nfast : 0, left = it.seg.left;
     const uint4* qa = reinterpret_cast<const uint4*>(s_q + (buf * Rp + r0) * D) + lane;
-    float* my_m = s_m + w % kept * 8;
-    float* my_l = s_l + w % kept * 8;
-    float* my_acc = s_acc + w % kept * 8 * kK8Pitch<D>;
-    // the incomplete block, if it is to be done here: the teams go on in turn
-    // where the blocks end, eight tokens at a time
+    // (the incomplete block, if it is to be done here)
     const int64_t tail0 = it.seg.n / kBlock * kBlock;
     const E* Kt = reinterpret_cast<const E*>(a.c.Kt) + it.seg.bg * kBlock * D;
     const E* Vt = reinterpret_cast<const E*>(a.c.Vt) + it.seg.bg * kBlock * D;
+    const int turns = n + (left + kK8Few - 1) / kK8Few;
+    const int x1 = x < turns ? x + (turns - x + nteam - 1) / nteam * nteam - turns : x - turns;   // the team's first turn in the next item
     const int few = rows <= 0 ? kBlock : kK8Few * ((x < n ? x + (n - x + nteam - 1) / nteam * nteam : x) - n);
     if (few < left) k8_rows_ahead<D>(Kt, Vt, few, left);
     if (x < n && !sent && !dead) {
@@ -548,10 +652,10 @@ __global__ void __launch_bounds__(kK8Threads, 1) kv8_decode_kernel(const A a) {
         sent = x + nteam < n;
         if (sent) {
           at = k8_at(a, it.seg, s_ids + buf * kKdIds, x + nteam);
-        } else if (u_next < u1 && mbar_test(item_full + 8 * (buf ^ 1), ((k + 1) >> 1) & 1)) {
-          const KdSegOf<A>& next = items[buf ^ 1].seg;
-          sent = x + nteam - n < next.nfast;
-          if (sent) at = k8_at(a, next, s_ids + (buf ^ 1) * kKdIds, x + nteam - n);
+        } else if (u_next < u1 && mbar_test(item_full + 8 * buf1, turn1)) {
+          const KdSegOf<A>& next = items[buf1].seg;
+          sent = x1 < next.nfast;
+          if (sent) at = k8_at(a, next, s_ids + buf1 * kKdIds, x1);
         }
         sent = sent && !dead;
         if (team > 1 && lane == 0) mbar_arrive(empty);
@@ -591,44 +695,15 @@ __global__ void __launch_bounds__(kK8Threads, 1) kv8_decode_kernel(const A a) {
 #pragma unroll 1
       for (int t = few; t < left; t += kK8Few * nteam) k8_rows<D, E>(f, qa, Kt + t * D, Vt + t * D, left - t, end - t);
     }
-    x -= n;
-    for (int w0 = W - kept; w0 >= 0; w0 -= kept) {
-      if (w0 < W - kept) bar_sync(1, W * 32);
-      if (w >= w0 && w < w0 + kept) {
-        if (w0 == W - kept) k8_store<D>(f, my_m, my_l, my_acc);
-        else k8_add<D>(f, my_m, my_l, my_acc);
-      }
-    }
-    bar_sync(1, W * 32);
-    // merge the teams, four channels of a row to a thread
-    float* part = a.part + (2 * (int64_t)blockIdx.x + (it.seg.cut0 ? 0 : 1)) * R * (D + 4);
-    const int kept_rows = kept < W ? kept * 8 : nteam * team * 8;
-    for (int e = tid; e < R * (D / 4); e += W * 32) {
-      const int r = e / (D / 4), c = e % (D / 4) * 4;
-      float M = -INFINITY, l = 0.0f;
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int y = r; y < kept_rows; y += team * 8) M = fmaxf(M, s_m[y]);   // (the row in each team)
-      for (int y = r; y < kept_rows; y += team * 8) {
-        const float s = k8_factor(s_m[y], s_l[y], M);
-        const float4 z = *reinterpret_cast<const float4*>(s_acc + y * kK8Pitch<D> + c);
-        l = fmaf(s, s_l[y], l);
-        v.x = fmaf(s, z.x, v.x); v.y = fmaf(s, z.y, v.y); v.z = fmaf(s, z.z, v.z); v.w = fmaf(s, z.w, v.w);
-      }
-      bool mine = r / a.G < it.seg.nq;
-      if constexpr (A::kPerToken) {
-        mine = true;
-        if (it.seg.bad) { M = 0.0f; l = v.x = v.y = v.z = v.w = NAN; }
-      }
-      if (!it.seg.cut0 && !it.seg.cut1) {
-        if (mine) kd_store<D>(a, it.seg, r, c, M, l, v);
-      } else {
-        *reinterpret_cast<float4*>(part + r * (D + 4) + c) = v;
-        if (c == 0) { part[r * (D + 4) + D] = M; part[r * (D + 4) + D + 1] = l; }
-      }
-    }
+    x = x1;
+    // the sums, once those of the item before have been merged
+    if (k > 0 && !dead) dead = __any_sync(0xffffffffu, !mbar_wait(sums_empty, (k - 1) & 1));
+    k8_store<D>(f, s_m + w * 8, s_l + w * 8, s_acc + w * 8 * kK8Pitch<D>);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(sums_full);        // (and the item's place may be filled again)
     u = u_next;
-    bar_sync(1, W * 32);
-    if (lane == 0) mbar_arrive(item_empty + 8 * buf);
+    buf = buf1;
+    turn = turn1;
   }
   if (dead) {
     // copies in flight land before the CTA can end (of whichever phase)
@@ -640,7 +715,7 @@ __global__ void __launch_bounds__(kK8Threads, 1) kv8_decode_kernel(const A a) {
 namespace {
 
 // Items of up to this many blocks stay whole.
-constexpr int64_t kK8WholeBlocks = 2 * kK8Warps;
+constexpr int64_t kK8WholeBlocks = 16;
 int64_t k8_blocks(const csa_shape* s, int n_sel) {
   const int64_t blocks = (s->n_max + kBlock - 1) / kBlock;
   return n_sel && n_sel < blocks ? n_sel : blocks;
@@ -664,22 +739,32 @@ size_t k8_workspace(const csa_shape* s, int T, int n_sel) {
 // the function, and another host thread's call may lie between the setting and
 // the launch.
 constexpr int kK8SharedBytes = 232448 - ((int)sizeof(KdBatch) + 127) / 128 * 128;
-template <int D, typename E, typename A>
-cudaError_t launch_kv8_decode_t(A a, int ncta, cudaStream_t st) {
-  const int R = kd_rows(a), nteam = kK8Warps / k8_team((R + 7) / 8);
-  const int smem = K8Layout<D, A>::slots(R) + 2 * nteam * kBlock * D;
+template <int D, int W, typename E, typename A>
+cudaError_t launch_kv8_decode_t(const A& a, int ncta, cudaStream_t st) {
+  const int R = kd_rows(a), nteam = W / k8_team((R + 7) / 8);
+  const int smem = K8Layout<D, W, A>::slots(R) + 2 * nteam * kBlock * D;
   const cudaError_t e =
-      cudaFuncSetAttribute(kv8_decode_kernel<D, E, A>, cudaFuncAttributeMaxDynamicSharedMemorySize, kK8SharedBytes);
+      cudaFuncSetAttribute(kv8_decode_kernel<D, W, E, A>, cudaFuncAttributeMaxDynamicSharedMemorySize, kK8SharedBytes);
   if (e != cudaSuccess) return e;
-  launch_pdl(kv8_decode_kernel<D, E, A>, dim3(ncta), dim3(kK8Threads), smem, st, a);
+  launch_pdl(kv8_decode_kernel<D, W, E, A>, dim3(ncta), dim3(kK8Threads<W>), smem, st, a);
   if (ncta > 1 && !a.whole)
     launch_pdl(decode_join_kernel<D, A>, dim3(ncta - 1, (R + kKdJoinWarps - 1) / kKdJoinWarps), dim3(kKdJoinWarps * 32), 0, st, a, ncta);
   return cudaGetLastError();
 }
+template <int D, typename E, typename A>
+cudaError_t launch_kv8_decode_w(const A& a, int ncta, cudaStream_t st) {
+  // One tile of rows is bound by memory: as many warps as there is shared memory for
+  // their slots.  Several are bound by the instructions, and teams share slots: as
+  // many warps as 128 registers allow (drafts of 24 rows: 120 us with ten, 104
+  // with fourteen; the batch of 64 takes all of the shared memory with ten).
+  if constexpr (!A::kPerToken)         // (lists have one tile)
+    if (kd_rows(a) > 8) return launch_kv8_decode_t<D, 14, E>(a, ncta, st);
+  return launch_kv8_decode_t<D, 10, E>(a, ncta, st);
+}
 template <typename A>
 cudaError_t launch_kv8_decode(const A& a, int d, bool bf16, int ncta, cudaStream_t st) {
-  return d == 128 ? (bf16 ? launch_kv8_decode_t<128, __nv_bfloat16>(a, ncta, st) : launch_kv8_decode_t<128, float>(a, ncta, st))
-                  : (bf16 ? launch_kv8_decode_t<64, __nv_bfloat16>(a, ncta, st) : launch_kv8_decode_t<64, float>(a, ncta, st));
+  return d == 128 ? (bf16 ? launch_kv8_decode_w<128, __nv_bfloat16>(a, ncta, st) : launch_kv8_decode_w<128, float>(a, ncta, st))
+                  : (bf16 ? launch_kv8_decode_w<64, __nv_bfloat16>(a, ncta, st) : launch_kv8_decode_w<64, float>(a, ncta, st));
 }
 
 bool k8_args_ok(const csa_shape* s, int T, csa_status* st) {

@@ -563,8 +563,8 @@ csa_status csa_kv8_select(const csa_shape* shape, const csa_kv8* cache, int T,
  * the positions up to its own of the blocks that its list names (blocks
  * [B][T][Hkv][n_sel], count [B][T][Hkv], as csa_kv8_select writes them or the
  * caller makes them).  A list has to be ascending, with no block twice and none
- * below 0 or past the token's own (entries from count on
- * are not read); the rows of one that is not, or with a count
+ * below 0 or past the token's own (what stands from count on
+ * does not matter); the rows of one that is not, or with a count
  * outside [0, n_sel], are NaN.  An empty list gives 0 (lse -inf).
  * 1 <= n_sel <= CSA_KV8_MAX_SEL; other arguments, limits and errors as in
  * csa_kv8_decode, workspace from csa_kv8_workspace_size with this n_sel. */
