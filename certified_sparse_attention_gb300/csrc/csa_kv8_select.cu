@@ -10,8 +10,10 @@
 // instruction.  The blocks' spans go from memory to the operands' registers, 16
 // bytes a lane, each read once per cluster.  A token's scores are collected, as
 // ordered integers, in the shared memory of one CTA of the cluster, which then
-// finds the n_sel-th largest digit by digit and writes the blocks above it, and
+// finds the n_sel-th largest by histograms and writes the blocks above it, and
 // the first ones equal to it, in ascending order.
+#include <algorithm>
+
 #include <cuda_fp16.h>
 
 #include "csa_rows.cuh"
@@ -31,12 +33,12 @@ struct Kv8SelectArgs {
   int B, T, Hkv, G;
   int n_sel, n_first, n_last;
   int tokens;              // of a cluster
-  int cluster;             // CTAs of a cluster
+  int clog;                // log2 of the CTAs of a cluster
+  int stages;              // chunks of spans on their way at once
 };
 
-constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
-constexpr int kSelRows = 16;
-constexpr unsigned kSelForced = 0xFFFFFFFFu;      // above every score
+constexpr int kSelStages = 4;
+constexpr int kSelRows = 16;      // query rows of a cluster at most
 
 __device__ __forceinline__ unsigned cluster_rank() {
   unsigned r;
@@ -68,91 +70,159 @@ __device__ __forceinline__ unsigned two_codes(unsigned word, int sel) {
 // a score as an ordered integer; a NaN counts as +infinity, -0 as 0
 __device__ __forceinline__ unsigned score_key(float s) { return ord_of(s == s ? s + 0.0f : INFINITY); }
 
-// The n_sel largest of the keys [0, n), n > n_sel, equal ones from the lowest:
-// their places to out, ascending.  By the whole CTA.
-__device__ void select_keys(const unsigned* key, int n, int n_sel, int32_t* out) {
-  __shared__ unsigned s_hist[256];
-  __shared__ unsigned s_found[2];
-  __shared__ int s_gt[kSelWarps], s_eq[kSelWarps];
+// four bins to a thread
+template <int NT> constexpr int kSelBinLog = NT == 256 ? 10 : 11;
+template <int NT>
+struct SelShared {
+  uint4 hist[NT];                             // from the uppermost bins down
+  unsigned lo[NT / 32], hi[NT / 32];
+  unsigned sum[NT / 32];
+  unsigned bin, above, count;
+  int gt[NT / 32], eq[NT / 32];
+};
+
+// The n_sel best blocks of [0, n), n > n_sel: the first n_first, the last n_last and
+// those of the largest keys, equal ones from the lowest; to out, ascending.  By the
+// whole CTA of NT threads.  The keys' own range is cut into 4 NT bins (digits of the
+// number would put most of them in a few, one addition after the other), the one at
+// which they reach the number wanted is cut again, and so on: two times as a rule.
+template <int NT>
+__device__ void select_keys(SelShared<NT>& sh, const unsigned* key, int n, int n_sel, int n_first, int n_last, int32_t* out) {
+  constexpr int NW = NT / 32, bins = 4 * NT, N = 8;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int end = (n + kSelThreads - 1) / kSelThreads * kSelThreads;
-  unsigned prefix = 0, mask = 0;
-  int need = n_sel;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    s_hist[tid] = 0;
+  // N keys to a thread at a time: with one, a pass waited for shared memory once
+  // for each
+  const auto each = [&](int from, int to, const auto& f) {
+    for (int i0 = from + tid; i0 < to; i0 += N * NT) {
+      unsigned k[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) k[j] = i0 + j * NT < to ? key[i0 + j * NT] : 0u;
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (i0 + j * NT < to) f(k[j]);
+    }
+  };
+  const int end = n - n_last;                 // keys [n_first, end) compete
+  unsigned need = n_sel - n_first - n_last;
+  unsigned lo = 0xFFFFFFFFu, hi = 0u;
+  each(n_first, end, [&](unsigned k) {
+    lo = min(lo, k);
+    hi = max(hi, k);
+  });
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) { sh.lo[w] = lo; sh.hi[w] = hi; }
+  sh.hist[tid] = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NW; ++i) { lo = min(lo, sh.lo[i]); hi = max(hi, sh.hi[i]); }
+  // keys of [lo, hi] are in play, those above are chosen; none is wanted of a range
+  // if need is 0
+  int shift = max(32 - __clz(hi - lo) - kSelBinLog<NT>, 0);
+  while (need) {
+    const unsigned span = hi - lo;
+    unsigned* hist = reinterpret_cast<unsigned*>(sh.hist) + (bins - 1);
+    each(n_first, end, [&](unsigned k) {
+      const unsigned off = k - lo;
+      if (k >= lo && off <= span) atomicAdd(hist - (int)(off >> shift), 1u);
+    });
     __syncthreads();
-    for (int i = tid; i < end; i += kSelThreads) {
-      // (neighbouring scores share their first digits: one addition for each
-      // different digit of a warp)
-      const bool in = i < n && (key[i] & mask) == prefix;
-      const unsigned digit = in ? key[i] >> shift & 255u : 256u;
-      const unsigned peers = __match_any_sync(0xffffffffu, digit);
-      if (in && lane == __ffs(peers) - 1) atomicAdd(&s_hist[digit], __popc(peers));
+    // the bin at which the keys from the largest down reach `need`
+    const uint4 h4 = sh.hist[tid];
+    sh.hist[tid] = make_uint4(0u, 0u, 0u, 0u);
+    const unsigned h[4] = {h4.x, h4.y, h4.z, h4.w}, sum = h4.x + h4.y + h4.z + h4.w;
+    unsigned upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    if (lane == 31) sh.sum[w] = upto;
+    __syncthreads();
+    unsigned above = upto - sum;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) above += i < w ? sh.sum[i] : 0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (above < need && above + h[k] >= need) {
+        sh.bin = bins - 1 - (tid * 4 + k);
+        sh.above = above;
+        sh.count = h[k];
+      }
+      above += h[k];
     }
     __syncthreads();
-    if (w == 0) {
-      // the digit at which the keys from the largest down reach `need`
-      unsigned h[8], sum = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) { h[k] = s_hist[255 - (lane * 8 + k)]; sum += h[k]; }
-      unsigned upto = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
-      }
-      unsigned above = upto - sum;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (above < (unsigned)need && above + h[k] >= (unsigned)need) {
-          s_found[0] = 255 - (lane * 8 + k);
-          s_found[1] = above;
-        }
-        above += h[k];
-      }
-    }
-    __syncthreads();
-    prefix |= s_found[0] << shift;
-    mask |= 255u << shift;
-    need -= (int)s_found[1];
+    need -= sh.above;
+    lo += sh.bin << shift;
+    hi = min(hi, lo + ((1u << shift) - 1u));
+    if (shift == 0 || sh.count == need) break;
+    shift = max(shift - kSelBinLog<NT>, 0);
+    // (what has been found is read by all before the next pass writes it)
     __syncthreads();
   }
-  // keys above prefix, and the first `need` of those equal to it
-  const int per = end / kSelWarps, i0 = w * per;
+  // keys above hi, and the first `need` of [lo, hi]
+  constexpr int M = 4;
+  const int per = (n + M * NT - 1) / (M * NT) * M * 32, i0 = w * per, i1 = min(i0 + per, n);
+  const auto rank = [&](int i, unsigned k, bool& isg, bool& ise) {
+    isg = i < n && (i < n_first || i >= end || k > hi);
+    ise = i < n && !isg && need && k >= lo;
+  };
   int gt = 0, eq = 0;
-  for (int i = i0 + lane; i < i0 + per; i += 32) {
-    const unsigned k = i < n ? key[i] : 0u;
-    gt += __popc(__ballot_sync(0xffffffffu, i < n && k > prefix));
-    eq += __popc(__ballot_sync(0xffffffffu, i < n && k == prefix));
+  for (int i = i0 + lane; i < i1 + lane; i += 32 * M) {
+    unsigned k[M];
+#pragma unroll
+    for (int j = 0; j < M; ++j) k[j] = i + 32 * j < n ? key[i + 32 * j] : 0u;
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      bool isg, ise;
+      rank(i + 32 * j, k[j], isg, ise);
+      gt += __popc(__ballot_sync(0xffffffffu, isg));
+      eq += __popc(__ballot_sync(0xffffffffu, ise));
+    }
   }
-  if (lane == 0) { s_gt[w] = gt; s_eq[w] = eq; }
+  if (lane == 0) { sh.gt[w] = gt; sh.eq[w] = eq; }
   __syncthreads();
   gt = eq = 0;
-  for (int i = 0; i < w; ++i) { gt += s_gt[i]; eq += s_eq[i]; }
+#pragma unroll
+  for (int i = 0; i < NW; ++i) {
+    gt += i < w ? sh.gt[i] : 0;
+    eq += i < w ? sh.eq[i] : 0;
+  }
   const unsigned below = (1u << lane) - 1u;
-  for (int i = i0 + lane; i < i0 + per; i += 32) {
-    const unsigned k = i < n ? key[i] : 0u;
-    const bool isg = i < n && k > prefix, ise = i < n && k == prefix;
-    const unsigned mg = __ballot_sync(0xffffffffu, isg), me = __ballot_sync(0xffffffffu, ise);
-    const int before = eq + __popc(me & below);
-    if (isg || (ise && before < need)) out[gt + __popc(mg & below) + min(before, need)] = i;
-    gt += __popc(mg);
-    eq += __popc(me);
+  for (int i = i0 + lane; i < i1 + lane; i += 32 * M) {
+    unsigned k[M];
+#pragma unroll
+    for (int j = 0; j < M; ++j) k[j] = i + 32 * j < n ? key[i + 32 * j] : 0u;
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      bool isg, ise;
+      rank(i + 32 * j, k[j], isg, ise);
+      const unsigned mg = __ballot_sync(0xffffffffu, isg), me = __ballot_sync(0xffffffffu, ise);
+      const int before = eq + __popc(me & below);
+      if (isg || (ise && before < (int)need)) out[gt + __popc(mg & below) + min(before, (int)need)] = i + 32 * j;
+      gt += __popc(mg);
+      eq += __popc(me);
+    }
   }
   __syncthreads();
 }
 
-template <int D, typename E>
-__global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const Kv8SelectArgs a) {
+// ROWS: 8 where no cluster has more rows, else 16
+template <int D, int ROWS, int NT, typename E>
+__global__ void __launch_bounds__(NT, NT == 256 ? ROWS == 8 ? 3 : 2 : 1) kv8_select_kernel(const Kv8SelectArgs a) {
   pdl_entry();
-  constexpr int CPL = D / 32, KS = D / 64;
+  constexpr int CPL = D / 32, KS = D / 64, NW = NT / 32, CHUNK = 8 * NW;   // (CHUNK: blocks whose spans come by one copy)
   typedef typename Row<CPL, E>::T RowT;
-  __shared__ __align__(16) __half s_code[kSelRows][D + 8];
-  __shared__ float s_step[kSelRows];
-  extern __shared__ __align__(16) unsigned s_key[];     // [tokens of this CTA][nblk_max]
+  __shared__ __align__(16) __half s_code[ROWS][D + 8];
+  __shared__ float s_step[ROWS];
+  __shared__ SelShared<NT> s_sel;
+  __shared__ __align__(8) unsigned long long s_bar[2 * kSelStages];      // chunks full, empty
+  extern __shared__ __align__(128) uint8_t s_dyn[];     // [stages] chunks, [tokens of this CTA][nblk_max] keys
+  constexpr unsigned chunk_bytes = CHUNK * 2 * D;
+  unsigned* s_key = reinterpret_cast<unsigned*>(s_dyn + a.stages * chunk_bytes);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, gid = lane >> 2, tig = lane & 3;
-  const int rank = a.cluster > 1 ? (int)cluster_rank() : 0;
-  const int tile = blockIdx.x / a.cluster, g = blockIdx.y, b = blockIdx.z;
+  const int cluster = 1 << a.clog, rank = cluster > 1 ? (int)cluster_rank() : 0;
+  const int tile = blockIdx.x >> a.clog, g = blockIdx.y, b = blockIdx.z;
   if (a.status && blockIdx.x == 0 && g == 0 && b == 0 && w == 0) {
     bool bad = false;
     for (int i = lane; i < a.B; i += 32) {
@@ -163,25 +233,63 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const Kv8Select
   }
   // (what follows returns or goes on for a whole cluster)
   const int64_t n = a.len[b], m = a.n_q ? a.n_q[b] : (int64_t)a.T;
+  const int t0 = tile * a.tokens;
+  // the rows' query elements: row r = w (+ 8) is head r % G of token t0 + r / G
+  // (sent for before the lengths are known; tokens past T are not there)
+  RowT raw[(ROWS + NW - 1) / NW];
+  const int glog = 31 - __clz(a.G);
+#pragma unroll
+  for (int i = 0; i < (ROWS + NW - 1) / NW; ++i) {
+    const int r = w + i * NW, t = r >> glog;
+    raw[i] = RowT();
+    if (r < ROWS && t < a.tokens && t0 + t < a.T)
+      raw[i] = *reinterpret_cast<const RowT*>(reinterpret_cast<const E*>(a.q) + b * a.qs.b + (int64_t)(t0 + t) * a.qs.t +
+                                              (int64_t)(g * a.G + (r & (a.G - 1))) * a.qs.h + lane * CPL);
+  }
   if (n < 0 || n > a.n_max || m < 0 || m > a.T) return;
-  const int t0 = tile * a.tokens, tokens = min((int)m - t0, a.tokens);
+  const int tokens = min((int)m - t0, a.tokens);
   if (tokens <= 0) return;
   const int64_t pos0 = n - m + t0, last = pos0 + tokens - 1;
   const int own = last < 0 ? -1 : (int)(last / kBlock);          // the last token's
   const int64_t bg = (int64_t)b * a.Hkv + g;
   if (own >= a.n_sel) {
     // blocks [0, own) are whole (and every token's own block is chosen anyway)
-    if (a.cluster > 1) cluster_arrive();
-    for (int r = w; r < kSelRows; r += kSelWarps) {
-      const int t = r / a.G;
-      float x[CPL], top = 0.0f;
-#pragma unroll
-      for (int c = 0; c < CPL; ++c) x[c] = 0.0f;
-      if (t < tokens) {
-        const E* src = reinterpret_cast<const E*>(a.q) + b * a.qs.b + (int64_t)(t0 + t) * a.qs.t +
-                       (int64_t)(g * a.G + r % a.G) * a.qs.h + lane * CPL;
-        row_floats<CPL>(*reinterpret_cast<const RowT*>(src), x, E());
+    if (cluster > 1) cluster_arrive();
+    // chunks rank, rank + cluster, ... of the blocks are this CTA's, eight blocks
+    // of each a warp's
+    const uint8_t* span = a.c.span + bg * a.nblk_max * 2 * D;
+    const float2* scale = reinterpret_cast<const float2*>(a.c.scale) + bg * a.nblk_max;
+    const int chunks = ((own + CHUNK - 1) / CHUNK - rank + cluster - 1) >> a.clog;
+    const unsigned full = smem_u32(s_bar), empty = full + 8 * kSelStages, data = smem_u32(s_dyn);
+    bool dead = false;
+    const auto send = [&](int c, int stage) {
+      const int j = (rank + (c << a.clog)) * CHUNK;
+      const unsigned size = (unsigned)min(CHUNK, own - j) * 2 * D;
+      mbar_expect_tx(full + 8 * stage, size);
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                       data + stage * chunk_bytes),
+                   "l"(span + (int64_t)j * 2 * D), "r"(size), "r"(full + 8 * stage)
+                   : "memory");
+    };
+    if (tid == 0) {
+      for (int i = 0; i < a.stages; ++i) {
+        mbar_init(full + 8 * i, 1);
+        mbar_init(empty + 8 * i, NW);
       }
+      fence_barrier_init();
+      for (int c = 0; c < min(chunks, a.stages); ++c) send(c, c);
+    }
+    // the steps of the lane's two blocks of a chunk, sent for a chunk ahead
+    const auto step_of = [&](int c, int e) {
+      return scale[min((rank + (c << a.clog)) * CHUNK + w * 8 + 2 * tig + e, own - 1)].x;
+    };
+    float next_a = step_of(0, 0), next_b = step_of(0, 1);
+#pragma unroll
+    for (int i = 0; i < (ROWS + NW - 1) / NW; ++i) {
+      const int r = w + i * NW;
+      if (r >= ROWS) break;
+      float x[CPL], top = 0.0f;
+      row_floats<CPL>(raw[i], x, E());
 #pragma unroll
       for (int c = 0; c < CPL; ++c) top = max_nan(top, fabsf(x[c]));
 #pragma unroll
@@ -198,7 +306,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const Kv8Select
     __syncthreads();
     // operands: channels 64 h + 16 tig + 4 s + (0..3) of rows gid, gid + 8; the
     // positive parts against the upper ends, the negative ones against the lower
-    unsigned qa[2][KS][4][4];
+    unsigned qa[2][KS][4][4];            // (rows 8 .. 15 are zeros with ROWS = 8)
     const __half2 zero = __float2half2_rn(0.0f);
 #pragma unroll
     for (int h = 0; h < KS; ++h)
@@ -206,69 +314,94 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const Kv8Select
       for (int s = 0; s < 4; ++s)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
+          if (ROWS == 8 && (e & 1)) {
+            qa[0][h][s][e] = qa[1][h][s][e] = 0u;
+            continue;
+          }
           const __half2 c = *reinterpret_cast<const __half2*>(&s_code[gid + (e & 1) * 8][64 * h + 16 * tig + 4 * s + (e >> 1) * 2]);
           qa[0][h][s][e] = half2_bits(__hmax2(c, zero));
           qa[1][h][s][e] = half2_bits(__hmin2(c, zero));
         }
-    const float step0 = s_step[gid], step1 = s_step[gid + 8];
-    if (a.cluster > 1) cluster_wait();            // every CTA of the cluster has begun
-    const uint8_t* span = a.c.span + bg * a.nblk_max * 2 * D + 16 * tig;
-    const float2* scale = reinterpret_cast<const float2*>(a.c.scale) + bg * a.nblk_max;
-    const int tok0 = gid / a.G, tok1 = (gid + 8) / a.G;
-    const bool put0 = gid % a.G == 0 && tok0 < tokens, put1 = gid % a.G == 0 && tok1 < tokens;
-    for (int j0 = (rank * kSelWarps + w) * 8; j0 < own; j0 += a.cluster * kSelWarps * 8) {
-      const uint8_t* src = span + (int64_t)min(j0 + gid, own - 1) * 2 * D;
+    const float step0 = s_step[gid], step1 = s_step[gid + ROWS - 8];
+    if (cluster > 1) cluster_wait();            // every CTA of the cluster has begun
+    const int tok0 = gid >> glog, tok1 = (gid + 8) >> glog;
+    const bool lead = (gid & (a.G - 1)) == 0, put0 = lead && tok0 < tokens, put1 = ROWS == 16 && lead && tok1 < tokens;
+    int stage = 0, phase = 0, before = 0;         // of the chunk, and the stage of the one before
+    for (int c = 0; c < chunks; ++c) {
+      const int j0 = (rank + (c << a.clog)) * CHUNK + w * 8;
+      if (tid == 0 && c > 0 && c - 1 + a.stages < chunks) {
+        // the chunk before has been read
+        if (!mbar_wait(empty + 8 * before, stage ? phase : phase ^ 1)) dead = true;
+        send(c - 1 + a.stages, before);
+      }
+      const float fa = next_a, fb = next_b;
+      next_a = step_of(c + 1, 0);
+      next_b = step_of(c + 1, 1);
+      __syncwarp();
+      if (!mbar_wait(full + 8 * stage, phase)) dead = true;
       uint4 k[2][KS];
+      const uint8_t* src = s_dyn + stage * chunk_bytes + (w * 8 + gid) * 2 * D + 16 * tig;
 #pragma unroll
       for (int p = 0; p < 2; ++p)
 #pragma unroll
         for (int h = 0; h < KS; ++h) k[p][h] = *reinterpret_cast<const uint4*>(src + p * D + 64 * h);
-      const int ja = j0 + 2 * tig, jb = ja + 1;
-      const float sa = scale[min(ja, own - 1)].x, sb = scale[min(jb, own - 1)].x;
-      float x[2][4];
+      float x[2][KS][4];
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        x[p][0] = x[p][1] = x[p][2] = x[p][3] = 0.0f;
+      for (int h = 0; h < KS; ++h)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) x[p][h][0] = x[p][h][1] = x[p][h][2] = x[p][h][3] = 0.0f;
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
 #pragma unroll
         for (int h = 0; h < KS; ++h)
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
+          for (int p = 0; p < 2; ++p) {
             const unsigned word = s == 0 ? k[p][h].x : s == 1 ? k[p][h].y : s == 2 ? k[p][h].z : k[p][h].w;
-            mma_rows(x[p], qa[p][h][s], two_codes(word, 0x4140), two_codes(word, 0x4342));
+            mma_rows(x[p][h], qa[p][h][s], two_codes(word, 0x4140), two_codes(word, 0x4342));
           }
-      }
-      float v[4];
+      constexpr int NV = ROWS / 4;          // scores of a lane
+      float v[NV];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = fmul(fmul(x[0][e] + x[1][e], e & 1 ? sb : sa), e < 2 ? step0 : step1);
+      for (int e = 0; e < NV; ++e) {
+        float sum = x[0][0][e] + x[1][0][e];
+        if (KS == 2) sum += x[0][KS - 1][e] + x[1][KS - 1][e];
+        v[e] = fmul(fmul(sum, e & 1 ? fb : fa), e < 2 ? step0 : step1);
+      }
       for (int o = 1; o < a.G; o <<= 1)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = max_nan(v[e], __shfl_xor_sync(0xffffffffu, v[e], 4 * o));
+        for (int e = 0; e < NV; ++e) v[e] = max_nan(v[e], __shfl_xor_sync(0xffffffffu, v[e], 4 * o));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = e & 1 ? jb : ja, tok = e < 2 ? tok0 : tok1;
+      for (int e = 0; e < NV; ++e) {
+        const int j = j0 + 2 * tig + (e & 1), tok = e < 2 ? tok0 : tok1;
         if ((e < 2 ? put0 : put1) && j < own) {
-          unsigned* at = s_key + (int64_t)(tok / a.cluster) * a.nblk_max + j;
-          if (a.cluster > 1) store_cluster(at, tok % a.cluster, score_key(v[e]));
+          unsigned* at = s_key + (int64_t)(tok >> a.clog) * a.nblk_max + j;
+          if (cluster > 1) store_cluster(at, tok & (cluster - 1), score_key(v[e]));
           else *at = score_key(v[e]);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + 8 * stage);
+      before = stage;
+      if (++stage == a.stages) { stage = 0; phase ^= 1; }
     }
-    if (a.cluster > 1) { cluster_arrive(); cluster_wait(); }
+    // (each wait is bounded; what was sent for has landed when the last chunk's has
+    // been waited for, or is waited for here)
+    if (dead) {
+      for (int i = 0; i < 2 * a.stages; ++i) mbar_wait(full + 8 * (i >> 1), i & 1);
+      if (a.status) atomicOr(a.status, 4u);
+    }
+    if (cluster > 1) { cluster_arrive(); cluster_wait(); }
     else __syncthreads();
   }
-  for (int tok = rank; tok < tokens; tok += a.cluster) {
+  for (int tok = rank; tok < tokens; tok += cluster) {
     const int64_t pos = pos0 + tok, row = ((int64_t)b * a.T + t0 + tok) * a.Hkv + g;
     const int n_cand = pos < 0 ? 0 : (int)(pos / kBlock) + 1;
     int32_t* out = a.blocks + row * a.n_sel;
     if (tid == 0) a.count[row] = min(n_cand, a.n_sel);
     if (n_cand <= a.n_sel) {
-      for (int i = tid; i < a.n_sel; i += kSelThreads) out[i] = i < n_cand ? i : -1;
+      for (int i = tid; i < a.n_sel; i += NT) out[i] = i < n_cand ? i : -1;
     } else {
-      unsigned* key = s_key + (int64_t)(tok / a.cluster) * a.nblk_max;
-      for (int i = tid; i < a.n_first; i += kSelThreads) key[i] = kSelForced;
-      for (int i = tid; i < a.n_last; i += kSelThreads) key[n_cand - 1 - i] = kSelForced;
-      __syncthreads();
-      select_keys(key, n_cand, a.n_sel, out);
+      select_keys<NT>(s_sel, s_key + (int64_t)(tok >> a.clog) * a.nblk_max, n_cand, a.n_sel, a.n_first, a.n_last, out);
     }
   }
 }
@@ -279,25 +412,16 @@ namespace {
 // CSA_KV8_MAX_SELECT_TOKENS / 64 blocks at most, more rows of fewer
 constexpr int kSelShared = CSA_KV8_MAX_SELECT_TOKENS / kBlock * 4;
 
-template <int D, typename E>
-cudaError_t launch_select(Kv8SelectArgs a, cudaStream_t st) {
-  const int row = (int)a.nblk_max * 4;
-  int tokens = kSelRows / a.G < a.T ? kSelRows / a.G : a.T, cluster = 1;
-  // More CTAs to a cluster while the card has room for them and each of their
-  // warps has blocks to score.
-  while (cluster < 8 && a.nblk_max > 64 * cluster &&
-         (int64_t)a.B * a.Hkv * ((a.T + tokens - 1) / tokens) * cluster <= sm_count())
-    cluster *= 2;
-  const int fit = kSelShared / row * cluster;
-  if (tokens > fit) tokens = fit;
-  a.tokens = tokens;
-  a.cluster = cluster;
-  cudaError_t e = cudaFuncSetAttribute(kv8_select_kernel<D, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelShared);
+template <int D, int ROWS, int NT, typename E>
+cudaError_t launch_select_t(const Kv8SelectArgs& a, cudaStream_t st) {
+  constexpr int chunk = NT / 4 * 2 * D;
+  const int cluster = 1 << a.clog;
+  cudaError_t e = cudaFuncSetAttribute(kv8_select_kernel<D, ROWS, NT, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelShared + 64 * 2 * D);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.T + tokens - 1) / tokens * cluster, a.Hkv, a.B);
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = (size_t)((tokens + cluster - 1) / cluster) * row;
+  cfg.gridDim = dim3((a.T + a.tokens - 1) / a.tokens * cluster, a.Hkv, a.B);
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = (size_t)((a.tokens + cluster - 1) / cluster) * a.nblk_max * 4 + (size_t)a.stages * chunk;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -307,8 +431,29 @@ cudaError_t launch_select(Kv8SelectArgs a, cudaStream_t st) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, kv8_select_kernel<D, E>, a);
+  e = cudaLaunchKernelEx(&cfg, kv8_select_kernel<D, ROWS, NT, E>, a);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+template <int D, typename E>
+cudaError_t launch_select(Kv8SelectArgs a, cudaStream_t st) {
+  int tokens = kSelRows / a.G < a.T ? kSelRows / a.G : a.T, cluster = 1;
+  // More CTAs to a cluster while the card has room for them and each of their
+  // warps has blocks to score.
+  const int64_t tiles = (int64_t)a.B * a.Hkv * ((a.T + tokens - 1) / tokens);
+  while (cluster < 8 && a.nblk_max > 64 * cluster && tiles * cluster <= sm_count()) cluster *= 2;
+  const int64_t fit = kSelShared / (a.nblk_max * 4) * cluster;
+  if (tokens > fit) tokens = (int)fit;
+  a.tokens = tokens;
+  a.clog = cluster == 1 ? 0 : cluster == 2 ? 1 : cluster == 4 ? 2 : 3;
+  // Sixteen warps to a CTA where even clusters of eight leave SMs idle and the
+  // context is long.
+  const int64_t rows = (tokens + cluster - 1) / cluster * a.nblk_max * 4;
+  const bool wide = tiles * cluster <= sm_count() && a.nblk_max >= 4096 && rows + 64 * 2 * D <= kSelShared;
+  const int64_t blocks = wide ? 128 : 64, chunk = blocks * 2 * D, chunks = (a.nblk_max + blocks * cluster - 1) / (blocks * cluster);
+  a.stages = (int)std::min(std::min((int64_t)kSelStages, chunks), (kSelShared + 64 * 2 * D - rows) / chunk);
+  if (tokens * a.G <= 8)
+    return wide ? launch_select_t<D, 8, 512, E>(a, st) : launch_select_t<D, 8, 256, E>(a, st);
+  return wide ? launch_select_t<D, 16, 512, E>(a, st) : launch_select_t<D, 16, 256, E>(a, st);
 }
 
 }  // namespace
