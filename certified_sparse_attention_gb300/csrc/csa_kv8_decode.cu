@@ -271,11 +271,12 @@ __device__ __forceinline__ void k8_rows(K8Fast<D>& f, const uint4* qa, const E* 
   typename PairOf<E>::T vraw[D / 8];       // (on their way while the scores are made)
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) vraw[i] = in ? *reinterpret_cast<const typename PairOf<E>::T*>(vr + 8 * i) : typename PairOf<E>::T();
-  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float s4[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};      // (two sums in turn: less to wait for)
 #pragma unroll
   for (int h = 0; h < D / 64; ++h)
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
+      float(&s)[4] = s4[c & 1];
       const uint4 q = qa[(h * 4 + c) * 32];
       const float4 k = in ? four_of(kr + 64 * h + 4 * c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       unsigned a[2][N], b[2][N];
@@ -294,7 +295,8 @@ __device__ __forceinline__ void k8_rows(K8Fast<D>& f, const uint4* qa, const E* 
       }
     }
   const int t0 = 2 * tid;
-  const float sa = t0 < end ? (s[0] + s[2]) * f.inv : -INFINITY, sb = t0 + 1 < end ? (s[1] + s[3]) * f.inv : -INFINITY;
+  const float sa = t0 < end ? (s4[0][0] + s4[1][0] + (s4[0][2] + s4[1][2])) * f.inv : -INFINITY;
+  const float sb = t0 + 1 < end ? (s4[0][1] + s4[1][1] + (s4[0][3] + s4[1][3])) * f.inv : -INFINITY;
   const K8Share sh = k8_share<D>(f, fmaxf(sa, sb));
   const float pa = ex2(sa - sh.ref), pb = ex2(sb - sh.ref);
   f.l = fmaf(pa + pb, sh.share, f.l);
@@ -511,7 +513,8 @@ __global__ void __launch_bounds__(kK8Threads<W>, 1) kv8_decode_kernel(const A a)
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int R = kd_rows(a), Rp = (R + 7) / 8 * 8;
   // teams: warps that share a block, one tile of rows each
-  const int team = k8_team(Rp / 8), nteam = W / team;
+  // (ten warps are for one tile)
+  const int team = W == 10 ? 1 : k8_team(Rp / 8), nteam = W / team;
   const unsigned bars = smem_u32(k8_sm), item_full = bars + 4 * W * 8, sums_full = item_full + 8 * kK8Items, sums_empty = sums_full + 8;
   KdItem<A>* items = reinterpret_cast<KdItem<A>*>(k8_sm + Lt::item);
   int32_t* s_ids = reinterpret_cast<int32_t*>(k8_sm + Lt::ids);
