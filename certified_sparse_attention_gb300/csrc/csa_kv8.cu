@@ -56,9 +56,9 @@ __device__ __forceinline__ unsigned code8(float x, float step) {
 
 // Codes of CPL values, in the low byte of each word (what is above it is not
 // theirs).  Where the step is in the normal range the product with the
-// reciprocal, off by less than 5e-5 (a quotient up to 127, three roundings),
-// decides unless it lies that close to the middle between two codes; only then
-// is the quotient itself computed.  Adding 3 * 2^22 + 128 rounds to an integer
+// reciprocal decides unless it lies within 3e-5 of the middle between two codes
+// (a quotient up to 127: the reciprocal's unit in the last place is 1.6e-5 of it,
+// the quotient's own rounding 0.8e-5); only then is the quotient itself computed.  Adding 3 * 2^22 + 128 rounds to an integer
 // and leaves it, plus 128, in the low byte.
 constexpr float kCode8Round = 12582912.0f + 128.0f;
 template <int CPL>
@@ -66,11 +66,11 @@ __device__ __forceinline__ void codes8(const float (&x)[CPL], float step, float 
   float off = 0.0f;
 #pragma unroll
   for (int c = 0; c < CPL; ++c) {
-    const float y = x[c] * inv, q = fadd(y, kCode8Round);
-    off = fmaxf(off, fabsf(fsub(y, fsub(q, kCode8Round))));
+    const float q = fmaf(x[c], inv, kCode8Round);
+    off = fmaxf(off, fabsf(fmaf(x[c], inv, kCode8Round - q)));
     code[c] = __float_as_uint(q);
   }
-  if (!(plain && off < 0.4999f)) {
+  if (!(plain && off < 0.49997f)) {
 #pragma unroll
     for (int c = 0; c < CPL; ++c) code[c] = code8(x[c], step);
   }
