@@ -1,13 +1,15 @@
 // The choice of blocks by a cheap score (csa_kv8_select).
 //
-// A cluster of CTAs takes up to 16 query rows of one (sequence, KV head): the
-// query heads of 16 / G tokens.  Scores are exact whole numbers before their two
+// A cluster of CTAs takes up to 8 query rows of one (sequence, KV head): the
+// query heads of 8 / G tokens.  Scores are exact whole numbers before their two
 // roundings:
 //   I = sum_c q_c (q_c >= 0 ? hi_c : lo_c) = sum_c q+_c hi_c + sum_c q-_c lo_c,
 // q+ and q- the positive and negative parts of the query's 8-bit codes: one
-// product of 2 d channels, on the tensor cores in half precision (codes and their
-// products are whole, sums stay below 2^24), 16 rows x 8 blocks x 16 channels an
-// instruction.  The blocks' spans go from memory to the operands' registers, 16
+// product of 2 d channels, on the tensor cores in half precision, 16 blocks x 8 rows x
+// 16 channels an instruction (their rate bounds it: with rows and blocks the other
+// way round, half of each instruction idle, 4 x 128K tokens took 17 us).  The codes enter 1152 too large, which the sums of q+
+// and q- correct; each sum is over 64 channels, below 64 127 1279 < 2^24, so all of
+// it is exact.  The blocks' spans go from memory to the operands' registers, 16
 // bytes a lane, each read once per cluster.  A token's scores are collected, as
 // ordered integers, in the shared memory of one CTA of the cluster, which then
 // finds the n_sel-th largest by histograms and writes the blocks above it, and
@@ -34,11 +36,12 @@ struct Kv8SelectArgs {
   int n_sel, n_first, n_last;
   int tokens;              // of a cluster
   int clog;                // log2 of the CTAs of a cluster
-  int stages;              // chunks of spans on their way at once
+  int stages;              // chunks of spans in shared memory at once
+  int chunk;               // blocks of a chunk
 };
 
-constexpr int kSelStages = 4;
-constexpr int kSelRows = 16;      // query rows of a cluster at most
+constexpr int kSelStages = 2;
+constexpr int kSelRows = 8;       // query rows of a cluster at most
 
 __device__ __forceinline__ unsigned cluster_rank() {
   unsigned r;
@@ -60,13 +63,9 @@ __device__ __forceinline__ void mma_rows(float (&d)[4], const unsigned (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ unsigned half2_bits(__half2 h) { return *reinterpret_cast<const unsigned*>(&h); }
-// two of a word's four codes as half-precision numbers (a byte under the
-// exponent of 1024, minus 1152)
-__device__ __forceinline__ unsigned two_codes(unsigned word, int sel) {
-  const unsigned u = __byte_perm(word, 0x64646464u, sel);
-  return half2_bits(__hsub2(*reinterpret_cast<const __half2*>(&u),
-                            __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480))));
-}
+// two of a word's four codes as half-precision numbers 1152 larger: a byte under the
+// exponent of 1024
+__device__ __forceinline__ unsigned two_codes(unsigned word, int sel) { return __byte_perm(word, 0x64646464u, sel); }
 // a score as an ordered integer; a NaN counts as +infinity, -0 as 0
 __device__ __forceinline__ unsigned score_key(float s) { return ord_of(s == s ? s + 0.0f : INFINITY); }
 
@@ -207,18 +206,17 @@ __device__ void select_keys(SelShared<NT>& sh, const unsigned* key, int n, int n
   __syncthreads();
 }
 
-// ROWS: 8 where no cluster has more rows, else 16
-template <int D, int ROWS, int NT, typename E>
-__global__ void __launch_bounds__(NT, NT == 256 ? ROWS == 8 ? 3 : 2 : 1) kv8_select_kernel(const Kv8SelectArgs a) {
+template <int D, int NT, typename E>
+__global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) kv8_select_kernel(const Kv8SelectArgs a) {
   pdl_entry();
-  constexpr int CPL = D / 32, KS = D / 64, NW = NT / 32, CHUNK = 8 * NW;   // (CHUNK: blocks whose spans come by one copy)
+  constexpr int CPL = D / 32, KS = D / 64, NW = NT / 32;
   typedef typename Row<CPL, E>::T RowT;
-  __shared__ __align__(16) __half s_code[ROWS][D + 8];
-  __shared__ float s_step[ROWS];
+  __shared__ __align__(16) __half s_code[kSelRows][D + 8];
+  __shared__ float s_step[kSelRows], s_extra[kSelRows][2][KS];   // (1152 times the sums of q+, q- over 64 channels)
   __shared__ SelShared<NT> s_sel;
   __shared__ __align__(8) unsigned long long s_bar[2 * kSelStages];      // chunks full, empty
   extern __shared__ __align__(128) uint8_t s_dyn[];     // [stages] chunks, [tokens of this CTA][nblk_max] keys
-  constexpr unsigned chunk_bytes = CHUNK * 2 * D;
+  const unsigned chunk_bytes = a.chunk * 2 * D;
   unsigned* s_key = reinterpret_cast<unsigned*>(s_dyn + a.stages * chunk_bytes);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, gid = lane >> 2, tig = lane & 3;
   const int cluster = 1 << a.clog, rank = cluster > 1 ? (int)cluster_rank() : 0;
@@ -234,18 +232,13 @@ __global__ void __launch_bounds__(NT, NT == 256 ? ROWS == 8 ? 3 : 2 : 1) kv8_sel
   // (what follows returns or goes on for a whole cluster)
   const int64_t n = a.len[b], m = a.n_q ? a.n_q[b] : (int64_t)a.T;
   const int t0 = tile * a.tokens;
-  // the rows' query elements: row r = w (+ 8) is head r % G of token t0 + r / G
-  // (sent for before the lengths are known; tokens past T are not there)
-  RowT raw[(ROWS + NW - 1) / NW];
+  // the rows' query elements: row r = w is head r % G of token t0 + r / G (sent for
+  // before the lengths are known; tokens past T are not there)
+  RowT raw = RowT();
   const int glog = 31 - __clz(a.G);
-#pragma unroll
-  for (int i = 0; i < (ROWS + NW - 1) / NW; ++i) {
-    const int r = w + i * NW, t = r >> glog;
-    raw[i] = RowT();
-    if (r < ROWS && t < a.tokens && t0 + t < a.T)
-      raw[i] = *reinterpret_cast<const RowT*>(reinterpret_cast<const E*>(a.q) + b * a.qs.b + (int64_t)(t0 + t) * a.qs.t +
-                                              (int64_t)(g * a.G + (r & (a.G - 1))) * a.qs.h + lane * CPL);
-  }
+  if (w < kSelRows && (w >> glog) < a.tokens && t0 + (w >> glog) < a.T)
+    raw = *reinterpret_cast<const RowT*>(reinterpret_cast<const E*>(a.q) + b * a.qs.b + (int64_t)(t0 + (w >> glog)) * a.qs.t +
+                                         (int64_t)(g * a.G + (w & (a.G - 1))) * a.qs.h + lane * CPL);
   if (n < 0 || n > a.n_max || m < 0 || m > a.T) return;
   const int tokens = min((int)m - t0, a.tokens);
   if (tokens <= 0) return;
@@ -255,16 +248,16 @@ __global__ void __launch_bounds__(NT, NT == 256 ? ROWS == 8 ? 3 : 2 : 1) kv8_sel
   if (own >= a.n_sel) {
     // blocks [0, own) are whole (and every token's own block is chosen anyway)
     if (cluster > 1) cluster_arrive();
-    // chunks rank, rank + cluster, ... of the blocks are this CTA's, eight blocks
+    // chunks rank, rank + cluster, ... of the blocks are this CTA's, sixteen blocks
     // of each a warp's
     const uint8_t* span = a.c.span + bg * a.nblk_max * 2 * D;
     const float2* scale = reinterpret_cast<const float2*>(a.c.scale) + bg * a.nblk_max;
-    const int chunks = ((own + CHUNK - 1) / CHUNK - rank + cluster - 1) >> a.clog;
+    const int chunks = ((own + a.chunk - 1) / a.chunk - rank + cluster - 1) >> a.clog;
     const unsigned full = smem_u32(s_bar), empty = full + 8 * kSelStages, data = smem_u32(s_dyn);
     bool dead = false;
     const auto send = [&](int c, int stage) {
-      const int j = (rank + (c << a.clog)) * CHUNK;
-      const unsigned size = (unsigned)min(CHUNK, own - j) * 2 * D;
+      const int j = (rank + (c << a.clog)) * a.chunk;
+      const unsigned size = (unsigned)min(a.chunk, own - j) * 2 * D;
       mbar_expect_tx(full + 8 * stage, size);
       asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
                        data + stage * chunk_bytes),
@@ -281,54 +274,71 @@ __global__ void __launch_bounds__(NT, NT == 256 ? ROWS == 8 ? 3 : 2 : 1) kv8_sel
     }
     // the steps of the lane's two blocks of a chunk, sent for a chunk ahead
     const auto step_of = [&](int c, int e) {
-      return scale[min((rank + (c << a.clog)) * CHUNK + w * 8 + 2 * tig + e, own - 1)].x;
+      return scale[min((rank + (c << a.clog)) * a.chunk + w * 16 + gid + 8 * e, own - 1)].x;
     };
     float next_a = step_of(0, 0), next_b = step_of(0, 1);
-#pragma unroll
-    for (int i = 0; i < (ROWS + NW - 1) / NW; ++i) {
-      const int r = w + i * NW;
-      if (r >= ROWS) break;
+    if (w < kSelRows) {
+      const int r = w;
       float x[CPL], top = 0.0f;
-      row_floats<CPL>(raw[i], x, E());
+      row_floats<CPL>(raw, x, E());
 #pragma unroll
       for (int c = 0; c < CPL; ++c) top = max_nan(top, fabsf(x[c]));
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
       float step = fdiv(top, 127.0f);
       if (step == 0.0f) step = 1.0f;
+      float plus = 0.0f, minus = 0.0f;
 #pragma unroll
       for (int c = 0; c < CPL; ++c) {
-        const float y = rintf(fdiv(x[c], step));
-        s_code[r][lane * CPL + c] = __float2half_rn(y == y ? fminf(fmaxf(y, -127.0f), 127.0f) : 0.0f);
+        float y = rintf(fdiv(x[c], step));
+        y = y == y ? fminf(fmaxf(y, -127.0f), 127.0f) : 0.0f;
+        s_code[r][lane * CPL + c] = __float2half_rn(y);
+        plus += fmaxf(y, 0.0f);
+        minus += fminf(y, 0.0f);
+      }
+#pragma unroll
+      for (int o = 1; o < 32 / KS; o <<= 1) {
+        plus += __shfl_xor_sync(0xffffffffu, plus, o);
+        minus += __shfl_xor_sync(0xffffffffu, minus, o);
+      }
+      if (lane % (32 / KS) == 0) {
+        s_extra[r][0][lane / (32 / KS)] = 1152.0f * plus;
+        s_extra[r][1][lane / (32 / KS)] = 1152.0f * minus;
       }
       if (lane == 0) s_step[r] = step;
     }
     __syncthreads();
-    // operands: channels 64 h + 16 tig + 4 s + (0..3) of rows gid, gid + 8; the
-    // positive parts against the upper ends, the negative ones against the lower
-    unsigned qa[2][KS][4][4];            // (rows 8 .. 15 are zeros with ROWS = 8)
+    // operands: channels 64 h + 16 tig + 4 s + (0..3) of row gid; the positive parts
+    // against the upper ends, the negative ones against the lower
+    unsigned qb[2][KS][4][2];
     const __half2 zero = __float2half2_rn(0.0f);
 #pragma unroll
     for (int h = 0; h < KS; ++h)
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+      for (int s = 0; s < 4; ++s) {
+        const uint2 u = *reinterpret_cast<const uint2*>(&s_code[gid][64 * h + 16 * tig + 4 * s]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (ROWS == 8 && (e & 1)) {
-            qa[0][h][s][e] = qa[1][h][s][e] = 0u;
-            continue;
-          }
-          const __half2 c = *reinterpret_cast<const __half2*>(&s_code[gid + (e & 1) * 8][64 * h + 16 * tig + 4 * s + (e >> 1) * 2]);
-          qa[0][h][s][e] = half2_bits(__hmax2(c, zero));
-          qa[1][h][s][e] = half2_bits(__hmin2(c, zero));
+        for (int e = 0; e < 2; ++e) {
+          const unsigned x = e ? u.y : u.x;
+          const __half2 c = *reinterpret_cast<const __half2*>(&x);
+          qb[0][h][s][e] = half2_bits(__hmax2(c, zero));
+          qb[1][h][s][e] = half2_bits(__hmin2(c, zero));
         }
-    const float step0 = s_step[gid], step1 = s_step[gid + ROWS - 8];
+      }
+    // the lane's scores are of the rows 2 tig, 2 tig + 1
+    float extra[2][2][KS], row_step[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      row_step[e] = s_step[2 * tig + e];
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int h = 0; h < KS; ++h) extra[e][p][h] = s_extra[2 * tig + e][p][h];
+    }
     if (cluster > 1) cluster_wait();            // every CTA of the cluster has begun
-    const int tok0 = gid >> glog, tok1 = (gid + 8) >> glog;
-    const bool lead = (gid & (a.G - 1)) == 0, put0 = lead && tok0 < tokens, put1 = ROWS == 16 && lead && tok1 < tokens;
     int stage = 0, phase = 0, before = 0;         // of the chunk, and the stage of the one before
     for (int c = 0; c < chunks; ++c) {
-      const int j0 = (rank + (c << a.clog)) * CHUNK + w * 8;
+      const int j0 = (rank + (c << a.clog)) * a.chunk + w * 16;
       if (tid == 0 && c > 0 && c - 1 + a.stages < chunks) {
         // the chunk before has been read
         if (!mbar_wait(empty + 8 * before, stage ? phase : phase ^ 1)) dead = true;
@@ -339,44 +349,50 @@ __global__ void __launch_bounds__(NT, NT == 256 ? ROWS == 8 ? 3 : 2 : 1) kv8_sel
       next_b = step_of(c + 1, 1);
       __syncwarp();
       if (!mbar_wait(full + 8 * stage, phase)) dead = true;
-      uint4 k[2][KS];
-      const uint8_t* src = s_dyn + stage * chunk_bytes + (w * 8 + gid) * 2 * D + 16 * tig;
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int h = 0; h < KS; ++h) k[p][h] = *reinterpret_cast<const uint4*>(src + p * D + 64 * h);
-      float x[2][KS][4];
-#pragma unroll
-      for (int h = 0; h < KS; ++h)
-#pragma unroll
-        for (int p = 0; p < 2; ++p) x[p][h][0] = x[p][h][1] = x[p][h][2] = x[p][h][3] = 0.0f;
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
+      if (w * 16 < a.chunk && j0 < own) {
+        const uint8_t* src = s_dyn + stage * chunk_bytes + (w * 16 + gid) * 2 * D + 16 * tig;
+        float x[2][KS][4];
 #pragma unroll
         for (int h = 0; h < KS; ++h)
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
-            const unsigned word = s == 0 ? k[p][h].x : s == 1 ? k[p][h].y : s == 2 ? k[p][h].z : k[p][h].w;
-            mma_rows(x[p][h], qa[p][h][s], two_codes(word, 0x4140), two_codes(word, 0x4342));
+            const uint4 k0 = *reinterpret_cast<const uint4*>(src + p * D + 64 * h), k1 = *reinterpret_cast<const uint4*>(src + 16 * D + p * D + 64 * h);
+            x[p][h][0] = x[p][h][1] = x[p][h][2] = x[p][h][3] = 0.0f;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              const unsigned w0 = s == 0 ? k0.x : s == 1 ? k0.y : s == 2 ? k0.z : k0.w, w1 = s == 0 ? k1.x : s == 1 ? k1.y : s == 2 ? k1.z : k1.w;
+              const unsigned op[4] = {two_codes(w0, 0x4140), two_codes(w1, 0x4140), two_codes(w0, 0x4342), two_codes(w1, 0x4342)};
+              mma_rows(x[p][h], op, qb[p][h][s][0], qb[p][h][s][1]);
+            }
           }
-      constexpr int NV = ROWS / 4;          // scores of a lane
-      float v[NV];
+        // v[e]: block gid (+ 8 with e / 2), row 2 tig + e % 2
+        float v[4];
 #pragma unroll
-      for (int e = 0; e < NV; ++e) {
-        float sum = x[0][0][e] + x[1][0][e];
-        if (KS == 2) sum += x[0][KS - 1][e] + x[1][KS - 1][e];
-        v[e] = fmul(fmul(sum, e & 1 ? fb : fa), e < 2 ? step0 : step1);
-      }
-      for (int o = 1; o < a.G; o <<= 1)
+        for (int e = 0; e < 4; ++e) {
+          float sum = 0.0f;
 #pragma unroll
-        for (int e = 0; e < NV; ++e) v[e] = max_nan(v[e], __shfl_xor_sync(0xffffffffu, v[e], 4 * o));
+          for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int e = 0; e < NV; ++e) {
-        const int j = j0 + 2 * tig + (e & 1), tok = e < 2 ? tok0 : tok1;
-        if ((e < 2 ? put0 : put1) && j < own) {
-          unsigned* at = s_key + (int64_t)(tok >> a.clog) * a.nblk_max + j;
-          if (cluster > 1) store_cluster(at, tok & (cluster - 1), score_key(v[e]));
-          else *at = score_key(v[e]);
+            for (int h = 0; h < KS; ++h) sum += x[p][h][e] - extra[e & 1][p][h];
+          v[e] = fmul(fmul(sum, e < 2 ? fa : fb), row_step[e & 1]);
+        }
+        // the largest over a token's rows
+        if (a.G >= 2) {
+          v[0] = max_nan(v[0], v[1]);
+          v[2] = max_nan(v[2], v[3]);
+          for (int o = 1; 2 * o < a.G; o <<= 1) {
+            v[0] = max_nan(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+            v[2] = max_nan(v[2], __shfl_xor_sync(0xffffffffu, v[2], o));
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = j0 + gid + (e & 2) * 4, r = 2 * tig + (e & 1), tok = r >> glog;
+          if ((r & (a.G - 1)) == 0 && tok < tokens && j < own) {
+            unsigned* at = s_key + (int64_t)(tok >> a.clog) * a.nblk_max + j;
+            if (cluster > 1) store_cluster(at, tok & (cluster - 1), score_key(v[e]));
+            else *at = score_key(v[e]);
+          }
         }
       }
       __syncwarp();
@@ -408,20 +424,20 @@ __global__ void __launch_bounds__(NT, NT == 256 ? ROWS == 8 ? 3 : 2 : 1) kv8_sel
 
 namespace {
 
-// shared memory for the scores of a CTA's tokens: one row of
-// CSA_KV8_MAX_SELECT_TOKENS / 64 blocks at most, more rows of fewer
-constexpr int kSelShared = CSA_KV8_MAX_SELECT_TOKENS / kBlock * 4;
+// dynamic shared memory there can be: the scores of one token of
+// CSA_KV8_MAX_SELECT_TOKENS / 64 blocks, or of more tokens of fewer, and a chunk of 64
+// spans
+constexpr int kSelShared = CSA_KV8_MAX_SELECT_TOKENS / kBlock * 4 + 64 * 2 * 128;
 
-template <int D, int ROWS, int NT, typename E>
-cudaError_t launch_select_t(const Kv8SelectArgs& a, cudaStream_t st) {
-  constexpr int chunk = NT / 4 * 2 * D;
+template <int D, int NT, typename E>
+cudaError_t launch_select_t(const Kv8SelectArgs& a, size_t smem, cudaStream_t st) {
   const int cluster = 1 << a.clog;
-  cudaError_t e = cudaFuncSetAttribute(kv8_select_kernel<D, ROWS, NT, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelShared + 64 * 2 * D);
+  cudaError_t e = cudaFuncSetAttribute(kv8_select_kernel<D, NT, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelShared);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((a.T + a.tokens - 1) / a.tokens * cluster, a.Hkv, a.B);
   cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = (size_t)((a.tokens + cluster - 1) / cluster) * a.nblk_max * 4 + (size_t)a.stages * chunk;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -431,29 +447,34 @@ cudaError_t launch_select_t(const Kv8SelectArgs& a, cudaStream_t st) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, kv8_select_kernel<D, ROWS, NT, E>, a);
+  e = cudaLaunchKernelEx(&cfg, kv8_select_kernel<D, NT, E>, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 template <int D, typename E>
 cudaError_t launch_select(Kv8SelectArgs a, cudaStream_t st) {
-  int tokens = kSelRows / a.G < a.T ? kSelRows / a.G : a.T, cluster = 1;
+  int tokens = kSelRows / a.G < a.T ? kSelRows / a.G : a.T, cluster = 1, clog = 0;
   // More CTAs to a cluster while the card has room for them and each of their
   // warps has blocks to score.
   const int64_t tiles = (int64_t)a.B * a.Hkv * ((a.T + tokens - 1) / tokens);
-  while (cluster < 8 && a.nblk_max > 64 * cluster && tiles * cluster <= sm_count()) cluster *= 2;
-  const int64_t fit = kSelShared / (a.nblk_max * 4) * cluster;
+  while (cluster < 8 && a.nblk_max > 64 * cluster && tiles * cluster <= sm_count()) {
+    cluster *= 2;
+    ++clog;
+  }
+  // room for a chunk of 64 blocks and the tokens' scores
+  constexpr int64_t least = 64 * 2 * D;
+  const int64_t fit = (kSelShared - least) / (a.nblk_max * 4) * cluster;
   if (tokens > fit) tokens = (int)fit;
-  a.tokens = tokens;
-  a.clog = cluster == 1 ? 0 : cluster == 2 ? 1 : cluster == 4 ? 2 : 3;
-  // Sixteen warps to a CTA where even clusters of eight leave SMs idle and the
-  // context is long.
   const int64_t rows = (tokens + cluster - 1) / cluster * a.nblk_max * 4;
-  const bool wide = tiles * cluster <= sm_count() && a.nblk_max >= 4096 && rows + 64 * 2 * D <= kSelShared;
-  const int64_t blocks = wide ? 128 : 64, chunk = blocks * 2 * D, chunks = (a.nblk_max + blocks * cluster - 1) / (blocks * cluster);
-  a.stages = (int)std::min(std::min((int64_t)kSelStages, chunks), (kSelShared + 64 * 2 * D - rows) / chunk);
-  if (tokens * a.G <= 8)
-    return wide ? launch_select_t<D, 8, 512, E>(a, st) : launch_select_t<D, 8, 256, E>(a, st);
-  return wide ? launch_select_t<D, 16, 512, E>(a, st) : launch_select_t<D, 16, 256, E>(a, st);
+  // Sixteen warps to a CTA where even clusters of eight leave SMs idle and the
+  // context is long; all of them at work where there is room for their chunk.
+  const bool wide = tiles * cluster <= sm_count() && a.nblk_max >= 4096 && rows + 4 * least <= kSelShared;
+  a.tokens = tokens;
+  a.clog = clog;
+  a.chunk = wide ? 256 : rows + 2 * least <= kSelShared ? 128 : 64;
+  const int64_t chunks = (a.nblk_max + a.chunk * cluster - 1) / (a.chunk * cluster);
+  a.stages = (int)std::min(std::min((int64_t)kSelStages, chunks), (kSelShared - rows) / (a.chunk * 2 * D));
+  const size_t smem = (size_t)(rows + a.stages * a.chunk * 2 * D);
+  return wide ? launch_select_t<D, 512, E>(a, smem, st) : launch_select_t<D, 256, E>(a, smem, st);
 }
 
 }  // namespace
