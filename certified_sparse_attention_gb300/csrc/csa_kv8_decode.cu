@@ -12,8 +12,8 @@
 // second kernel.  An item is a sequence and KV head with its T * G query rows;
 // over lists, where each token has blocks of its own, a token's G rows.
 //
-// A warp handles a tile of 8 rows; with more the warps of a CTA form teams of 2
-// to 8 that share the blocks.  Codes become half-precision numbers exactly (a
+// A warp handles one tile of 8 rows, or two; with more the warps of a CTA form teams
+// that share the blocks.  Codes become half-precision numbers exactly (a
 // byte under the exponent of 1024, minus 1152), the other operand is split into
 // two half-precision parts: the 16 rows of a matrix instruction (m16n8k16) are
 // the high parts of the 8 query rows, or weights, and their low parts, 2^12
@@ -38,13 +38,14 @@
 
 namespace csa {
 
-// W: consumer warps of a CTA
+// W: consumer warps of a CTA, MT: tiles of 8 rows to each
 constexpr int kK8Side = 2;        // ... and warps that fetch the queries and merge the sums
-template <int W> constexpr int kK8Threads = (W + kK8Side) * 32;
+// (MT = 2: and two that only fill a warpgroup, from which registers move to the
+// consumers': the launch has 168 a thread)
+template <int W, int MT> constexpr int kK8Threads = (W + kK8Side * MT) * 32;
+constexpr int kK8RegsConsumer = 208, kK8RegsSide = 88;
+static_assert(2 * kK8RegsConsumer + kK8RegsSide <= 3 * 168, "more registers than the launch has");
 constexpr int kK8Items = 3;       // items whose queries are there at once
-// warps of a team, for 1 .. 8 tiles of 8 rows (those that are left over idle)
-__host__ __device__ constexpr int k8_team(int ntile) { return ntile; }
-
 // high parts of x and y, and what is left of them in units of 2^-12
 __device__ __forceinline__ void k8_parts(float x, float y, unsigned& hi, unsigned& lo) {
   hi = half_pair(x, y);
@@ -133,22 +134,27 @@ __device__ __forceinline__ K8Share k8_share(K8Fast<D>& f, float top) {
   return s;
 }
 
-// One block: query operand at qa (K8Args::put; the lane's), keys at kt, values at
-// vt, steps ks and vs; between() is called when the keys have been read and before
-// the values are.  The lane's row sees the block's tokens below end; masked: some
-// row does not see all of them.
-template <int D, typename Between>
-__device__ __forceinline__ void k8_block(K8Fast<D>& f, const uint4* qa, const uint8_t* kt, const uint8_t* vt, float ks, float vs,
-                                         bool masked, int end, Between between) {
+// One block for MT tiles of rows, whose codes are converted once: query operands at
+// qa (put; the lane's), 2 D apart, keys at kt, values at vt, steps ks and vs;
+// between() is called when the keys have been read and before the values are.  The
+// lane's rows see the block's tokens below end; masked: some row does not see all of
+// them.
+template <int D, int MT, typename Between>
+__device__ __forceinline__ void k8_block(K8Fast<D> (&f)[MT], const uint4* qa, const uint8_t* kt, const uint8_t* vt, float ks, float vs,
+                                         bool masked, const int (&end)[MT], Between between) {
   const int lane = threadIdx.x & 31, tid = lane & 3;
-  float x[8][4];
+  float x[MT][8][4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.0f;
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[t][j][0] = x[t][j][1] = x[t][j][2] = x[t][j][3] = 0.0f;
 #pragma unroll 1
   for (int h = 0; h < D / 64; ++h) {
-    uint4 q[4];
+    uint4 q[MT][4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) q[s] = qa[(h * 4 + s) * 32];
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) q[t][s] = qa[2 * D * t + (h * 4 + s) * 32];
 #pragma unroll
     for (int j0 = 0; j0 < 8; j0 += 4) {
       uint4 k[4];
@@ -160,60 +166,72 @@ __device__ __forceinline__ void k8_block(K8Fast<D>& f, const uint4* qa, const ui
         for (int j = 0; j < 4; ++j) {
           unsigned b0, b1;
           k8_numbers(word_of(k[j], s), b0, b1);
-          mma_f16(x[j0 + j], q[s].x, q[s].y, q[s].z, q[s].w, b0, b1);
+#pragma unroll
+          for (int t = 0; t < MT; ++t) mma_f16(x[t][j0 + j], q[t][s].x, q[t][s].y, q[t][s].z, q[t][s].w, b0, b1);
         }
     }
   }
   between();
-  // scores: x[j][e] of token 16 tid + 2 j + e
-  const float unit = ks * f.inv;
-  float top = -INFINITY, top1 = -INFINITY;
+  unsigned p[MT][4][4];
+  float weight[MT];
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) x[j][e] = fmaf(x[j][e + 2], kLowUnit, x[j][e]) * unit;
-  if (__builtin_expect(masked, 0)) {
+  for (int t = 0; t < MT; ++t) {
+    // scores: x[t][j][e] of token 16 tid + 2 j + e
+    const float unit = ks * f[t].inv;
+    float top = -INFINITY, top1 = -INFINITY;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (16 * tid + 2 * j + e >= end) x[j][e] = -INFINITY;
-  }
+      for (int e = 0; e < 2; ++e) x[t][j][e] = fmaf(x[t][j][e + 2], kLowUnit, x[t][j][e]) * unit;
+    if (__builtin_expect(masked, 0)) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) { top = fmaxf(top, x[j][0]); top1 = fmaxf(top1, x[j][1]); }
-  const K8Share sh = k8_share<D>(f, fmaxf(top, top1));
-  const float weight = sh.seen ? sh.share * vs : 0.0f;
-  unsigned p[4][4];
-  float sum = 0.0f, sum1 = 0.0f;
+      for (int j = 0; j < 8; ++j)
 #pragma unroll
-  for (int s = 0; s < 4; ++s)
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const float pa = ex2(x[2 * s + u][0] - sh.ref), pb = ex2(x[2 * s + u][1] - sh.ref);
-      sum += pa;
-      sum1 += pb;
-      k8_parts(pa, pb, p[s][2 * u], p[s][2 * u + 1]);
+        for (int e = 0; e < 2; ++e)
+          if (16 * tid + 2 * j + e >= end[t]) x[t][j][e] = -INFINITY;
     }
-  f.l = fmaf(sum + sum1, sh.share, f.l);
 #pragma unroll
-  for (int i0 = 0; i0 < D / 8; i0 += 4) {
-    uint4 v[4];
-    float y[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(vt + (i0 + i) * 512 + lane * 16);
+    for (int j = 0; j < 8; ++j) { top = fmaxf(top, x[t][j][0]); top1 = fmaxf(top1, x[t][j][1]); }
+    const K8Share sh = k8_share<D>(f[t], fmaxf(top, top1));
+    weight[t] = sh.seen ? sh.share * vs : 0.0f;
+    float sum = 0.0f, sum1 = 0.0f;
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int u = 0; u < 2; ++u) {
+        const float pa = ex2(x[t][2 * s + u][0] - sh.ref), pb = ex2(x[t][2 * s + u][1] - sh.ref);
+        sum += pa;
+        sum1 += pb;
+        k8_parts(pa, pb, p[t][s][2 * u], p[t][s][2 * u + 1]);
+      }
+    f[t].l = fmaf(sum + sum1, sh.share, f[t].l);
+  }
+  constexpr int N = 4 / MT;              // n-tiles of channels at a time
+#pragma unroll
+  for (int i0 = 0; i0 < D / 8; i0 += N) {
+    uint4 v[N];
+    float y[MT][N][4];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = *reinterpret_cast<const uint4*>(vt + (i0 + i) * 512 + lane * 16);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
         unsigned b0, b1;
         k8_numbers(word_of(v[i], s), b0, b1);
-        if (s == 0) mma_f16_first(y[i], p[s][0], p[s][1], p[s][2], p[s][3], b0, b1);
-        else mma_f16(y[i], p[s][0], p[s][1], p[s][2], p[s][3], b0, b1);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          if (s == 0) mma_f16_first(y[t][i], p[t][s][0], p[t][s][1], p[t][s][2], p[t][s][3], b0, b1);
+          else mma_f16(y[t][i], p[t][s][0], p[t][s][1], p[t][s][2], p[t][s][3], b0, b1);
+        }
       }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) f.o[i0 + i][e] = fmaf(fmaf(y[i][e + 2], kLowUnit, y[i][e]), weight, f.o[i0 + i][e]);
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          f[t].o[i0 + i][e] = fmaf(fmaf(y[t][i][e + 2], kLowUnit, y[t][i][e]), weight[t], f[t].o[i0 + i][e]);
   }
 }
 
@@ -351,11 +369,12 @@ __device__ __forceinline__ void k8_rows_ahead(const E* K, const E* V, int first,
 
 // --------------------------------------------------------------- the sums
 
-// rows of a warp's sums in shared memory lie D + 8 floats apart (bank offsets)
-template <int D> constexpr int kK8Pitch = D + 8;
+// rows of a warp's sums in shared memory lie D + 8 floats apart (bank offsets; with
+// two tiles there is room for D + 4)
+template <int D, int MT> constexpr int kK8Pitch = D + 8 / MT;
 
 // the warp's sums as rows [8] of m, l and acc[D] in shared memory
-template <int D>
+template <int D, int MT>
 __device__ __forceinline__ void k8_store(K8Fast<D>& f, float* s_m, float* s_l, float* s_acc) {
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
   f.l += __shfl_xor_sync(0xffffffffu, f.l, 1);
@@ -363,7 +382,7 @@ __device__ __forceinline__ void k8_store(K8Fast<D>& f, float* s_m, float* s_l, f
   if (tid == 0) { s_m[gid] = f.r; s_l[gid] = f.l; }
 #pragma unroll
   for (int i = 0; i < D / 8; ++i)
-    *reinterpret_cast<float2*>(s_acc + gid * kK8Pitch<D> + 8 * i + 2 * tid) = make_float2(f.o[i][0], f.o[i][1]);
+    *reinterpret_cast<float2*>(s_acc + gid * kK8Pitch<D, MT> + 8 * i + 2 * tid) = make_float2(f.o[i][0], f.o[i][1]);
 }
 // factor of sums relative to m where they become relative to M
 __device__ __forceinline__ float k8_factor(float m, float l, float M) { return m > -INFINITY ? ex2(m - M) : l == 0.0f ? 0.0f : 1.0f; }
@@ -371,16 +390,16 @@ __device__ __forceinline__ float k8_factor(float m, float l, float M) { return m
 // --------------------------------------------------------------- the kernel
 
 // shared memory: barriers (keys and values full, empty, items full, sums full,
-// empty), items, their list entries, warp sums, their q rows, the slots
-template <int D, int W, typename A>
+// empty), items, their list entries, sums of W * MT tiles, q rows, the slots
+template <int D, int W, int MT, typename A>
 struct K8Layout {
   static constexpr int item = (4 * W + kK8Items + 3) * 8;
   static constexpr int ids = item + kK8Items * (int)sizeof(KdItem<A>);
   static constexpr int m = ids + (A::kPerToken ? kK8Items * kKdIds * 4 : 0);
-  static constexpr int l = m + W * 8 * 4;
-  static constexpr int acc = (l + W * 8 * 4 + 15) / 16 * 16;
-  static constexpr int q = acc + W * 8 * kK8Pitch<D> * 4;
-  static __host__ __device__ int slots(int rows) { return (q + kK8Items * ((rows + 7) / 8 * 8) * D * 4 + 127) / 128 * 128; }
+  static constexpr int l = m + W * MT * 8 * 4;
+  static constexpr int acc = (l + W * MT * 8 * 4 + 15) / 16 * 16;
+  static constexpr int q = acc + W * MT * 8 * kK8Pitch<D, MT> * 4;
+  static constexpr __host__ __device__ int slots(int rows) { return (q + kK8Items * rows * D * 4 + 127) / 128 * 128; }     // (padded rows)
 };
 
 // whether the phase of parity `parity` is complete, for a whole warp
@@ -427,11 +446,10 @@ __device__ __forceinline__ void floats_out(float* p, const float (&x)[CPL]) {
   else *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
 }
 
-// The item's sums from its teams' (in regions of a warp's 8 rows each), by a side
-// warp: rows [r0, r1), four at a time.  First a lane to a team, then D / 32 channels
-// to a lane.
-template <int D, typename A>
-__device__ __forceinline__ void k8_merge(const A& a, const KdSegOf<A>& s, int nteam, int team, const float* s_m, const float* s_l,
+// The item's sums from its teams' (team_rows rows each), by a side warp: rows
+// [r0, r1), four at a time.  First a lane to a team, then D / 32 channels to a lane.
+template <int D, int MT, typename A>
+__device__ __forceinline__ void k8_merge(const A& a, const KdSegOf<A>& s, int nteam, int team_rows, const float* s_m, const float* s_l,
                                          const float* s_acc, int r0, int r1) {
   constexpr int CPL = D / 32, N = 4;
   const int lane = threadIdx.x & 31, R = kd_rows(a), glog = 31 - __clz(a.G);
@@ -440,7 +458,7 @@ __device__ __forceinline__ void k8_merge(const A& a, const KdSegOf<A>& s, int nt
     float M[N], l[N], f[N], v[N][CPL];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int x = lane * team * 8 + r + i;
+      const int x = lane * team_rows + r + i;
       const bool in = lane < nteam;
       M[i] = f[i] = in ? s_m[x] : -INFINITY;
       l[i] = in ? s_l[x] : 0.0f;
@@ -466,7 +484,7 @@ __device__ __forceinline__ void k8_merge(const A& a, const KdSegOf<A>& s, int nt
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         float z[CPL];
-        floats_in<CPL>(z, s_acc + (y * team * 8 + r + i) * kK8Pitch<D> + lane * CPL);
+        floats_in<CPL>(z, s_acc + (y * team_rows + r + i) * kK8Pitch<D, MT> + lane * CPL);
         const float w = __shfl_sync(0xffffffffu, f[i], y);
 #pragma unroll
         for (int c = 0; c < CPL; ++c) v[i][c] = fmaf(w, z[c], v[i][c]);
@@ -503,18 +521,18 @@ __device__ __forceinline__ void k8_merge(const A& a, const KdSegOf<A>& s, int nt
   }
 }
 
-template <int D, int W, typename E, typename A>
-__global__ void __launch_bounds__(kK8Threads<W>, 1) kv8_decode_kernel(const A a) {
+template <int D, int W, int MT, typename E, typename A>
+__global__ void __launch_bounds__(kK8Threads<W, MT>, 1) kv8_decode_kernel(const A a) {
   pdl_entry();
-  using Lt = K8Layout<D, W, A>;
+  using Lt = K8Layout<D, W, MT, A>;
   constexpr unsigned bytes = kBlock * D;
   __shared__ KdBatch batch;
   extern __shared__ __align__(128) uint8_t k8_sm[];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int R = kd_rows(a), Rp = (R + 7) / 8 * 8;
-  // teams: warps that share a block, one tile of rows each
+  const int R = kd_rows(a), Rp = (R + 8 * MT - 1) / (8 * MT) * (8 * MT);
+  // teams: warps that share a block, MT tiles of rows each (those left over idle)
   // (ten warps are for one tile)
-  const int team = W == 10 ? 1 : k8_team(Rp / 8), nteam = W / team;
+  const int team = W == 10 ? 1 : Rp / (8 * MT), nteam = W / team;
   const unsigned bars = smem_u32(k8_sm), item_full = bars + 4 * W * 8, sums_full = item_full + 8 * kK8Items, sums_empty = sums_full + 8;
   KdItem<A>* items = reinterpret_cast<KdItem<A>*>(k8_sm + Lt::item);
   int32_t* s_ids = reinterpret_cast<int32_t*>(k8_sm + Lt::ids);
@@ -544,7 +562,9 @@ __global__ void __launch_bounds__(kK8Threads<W>, 1) kv8_decode_kernel(const A a)
   if (w >= W) {
     // The side warps: each item's queries and what else is known of it, ahead of
     // the sums, which they merge while the others are at the next items.
+    if constexpr (MT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kK8RegsSide));
     const int part = w - W;
+    if (part >= kK8Side) return;
     if (blockIdx.x == 0 && part == 1) {
       bool bad = false;
       for (int b = lane; b < a.B; b += 32) {
@@ -577,7 +597,7 @@ __global__ void __launch_bounds__(kK8Threads<W>, 1) kv8_decode_kernel(const A a)
     for (int k = 0, buf = 0; done < u1; ++k) {
       if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(sums_full, k & 1));
       const KdSegOf<A> s = items[buf].seg;
-      k8_merge<D>(a, s, nteam, team, s_m, s_l, s_acc, part * (Rp / kK8Side), (part + 1) * (Rp / kK8Side));
+      k8_merge<D, MT>(a, s, nteam, team * MT * 8, s_m, s_l, s_acc, part * (Rp / kK8Side), (part + 1) * (Rp / kK8Side));
       __syncwarp();
       if (lane == 0) mbar_arrive(sums_empty);
       done += s.step;
@@ -589,11 +609,12 @@ __global__ void __launch_bounds__(kK8Threads<W>, 1) kv8_decode_kernel(const A a)
     return;
   }
 
+  if constexpr (MT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kK8RegsConsumer));
   const int my_team = w / team, tile = w % team;
-  const int rows = my_team < nteam ? min(8, R - tile * 8) : 0;    // <= 0: a warp with no rows
-  const int r0 = tile * 8 < Rp ? tile * 8 : 0;
+  const bool works = my_team < nteam;             // (a warp with rows)
+  const int r0 = works ? tile * 8 * MT : 0;
   // the team's slots and barriers: keys, values
-  const uint8_t* kt = k8_sm + Lt::slots(R) + 2 * min(my_team, nteam - 1) * bytes;
+  const uint8_t* kt = k8_sm + Lt::slots(Rp) + 2 * min(my_team, nteam - 1) * bytes;
   const uint8_t* vt = kt + bytes;
   const unsigned full = bars + 16 * my_team, empty = full + 16 * W;
   // An item's work goes to the teams in turn, its blocks and then its incomplete
@@ -621,7 +642,7 @@ __global__ void __launch_bounds__(kK8Threads<W>, 1) kv8_decode_kernel(const A a)
     const E* Vt = reinterpret_cast<const E*>(a.c.Vt) + it.seg.bg * kBlock * D;
     const int turns = n + (left + kK8Few - 1) / kK8Few;
     const int x1 = x < turns ? x + (turns - x + nteam - 1) / nteam * nteam - turns : x - turns;   // the team's first turn in the next item
-    const int few = rows <= 0 ? kBlock : kK8Few * ((x < n ? x + (n - x + nteam - 1) / nteam * nteam : x) - n);
+    const int few = !works ? kBlock : kK8Few * ((x < n ? x + (n - x + nteam - 1) / nteam * nteam : x) - n);
     if (few < left) k8_rows_ahead<D>(Kt, Vt, few, left);
     if (x < n && !sent && !dead) {
       const int64_t at = k8_at(a, it.seg, s_ids + buf * kKdIds, x);
@@ -637,12 +658,19 @@ __global__ void __launch_bounds__(kK8Threads<W>, 1) kv8_decode_kernel(const A a)
       step = *reinterpret_cast<const float2*>(a.c.scale + at * 2);
     }
     __syncwarp();
-    K8Fast<D> f;
-    f.inv = it.inv[r0 + (lane >> 2)];
-    f.r = -INFINITY;
-    f.l = 0.0f;
+    K8Fast<D> f[MT];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) f.o[i][0] = f.o[i][1] = 0.0f;
+    for (int t = 0; t < MT; ++t) {
+      f[t].inv = it.inv[r0 + 8 * t + (lane >> 2)];
+      f[t].r = -INFINITY;
+      f[t].l = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) f[t].o[i][0] = f[t].o[i][1] = 0.0f;
+    }
+    // the end of what the lane's row of tile t sees, from position p on, up to `most`
+    const auto end_of = [&](int t, int64_t p, int most) {
+      return (int)min(max(it.end[r0 + 8 * t + (lane >> 2)] - p, (int64_t)0), (int64_t)most);
+    };
     const int64_t u_next = u + it.seg.step;
     while (x < n) {
       if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(full, phase));
@@ -672,17 +700,15 @@ __global__ void __launch_bounds__(kK8Threads<W>, 1) kv8_decode_kernel(const A a)
         __syncwarp();
         if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(full + 8, phase));
       };
-      if (rows <= 0) {
-        between();
-      } else {
-        const int64_t p0 = [&] {
-          if constexpr (A::kPerToken) return it.seg.own;
-          else return (it.seg.blk0 + x) * kBlock;
-        }();
-        const bool masked = x >= it.seg.clear;
-        k8_block<D>(f, qa, kt, vt, ks, vs, masked, masked ? (int)min(max(it.end[r0 + (lane >> 2)] - p0, (int64_t)0), (int64_t)kBlock) : 0,
-                    between);
-      }
+      const int64_t p0 = [&] {
+        if constexpr (A::kPerToken) return it.seg.own;
+        else return (it.seg.blk0 + x) * kBlock;
+      }();
+      const bool masked = x >= it.seg.clear;
+      int end[MT];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) end[t] = masked ? end_of(t, p0, kBlock) : 0;
+      k8_block<D, MT>(f, qa, kt, vt, ks, vs, masked, end, between);
       __syncwarp();
       if (team > 1 && lane == 0) mbar_arrive(empty + 8);
       if (sent && tile == 0 && lane == 0) {
@@ -694,14 +720,19 @@ __global__ void __launch_bounds__(kK8Threads<W>, 1) kv8_decode_kernel(const A a)
       x += nteam;
     }
     if (few < left) {
-      const int end = (int)min(max(it.end[r0 + (lane >> 2)] - tail0, (int64_t)0), (int64_t)left);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const int end = end_of(t, tail0, left);
 #pragma unroll 1
-      for (int t = few; t < left; t += kK8Few * nteam) k8_rows<D, E>(f, qa, Kt + t * D, Vt + t * D, left - t, end - t);
+        for (int i = few; i < left; i += kK8Few * nteam) k8_rows<D, E>(f[t], qa + 2 * D * t, Kt + i * D, Vt + i * D, left - i, end - i);
+      }
     }
     x = x1;
     // the sums, once those of the item before have been merged
     if (k > 0 && !dead) dead = __any_sync(0xffffffffu, !mbar_wait(sums_empty, (k - 1) & 1));
-    k8_store<D>(f, s_m + w * 8, s_l + w * 8, s_acc + w * 8 * kK8Pitch<D>);
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+      k8_store<D, MT>(f[t], s_m + (w * MT + t) * 8, s_l + (w * MT + t) * 8, s_acc + (w * MT + t) * 8 * kK8Pitch<D, MT>);
     __syncwarp();
     if (lane == 0) mbar_arrive(sums_full);        // (and the item's place may be filled again)
     u = u_next;
@@ -742,27 +773,34 @@ size_t k8_workspace(const csa_shape* s, int T, int n_sel) {
 // the function, and another host thread's call may lie between the setting and
 // the launch.
 constexpr int kK8SharedBytes = 232448 - ((int)sizeof(KdBatch) + 127) / 128 * 128;
-template <int D, int W, typename E, typename A>
+template <int D, int W, int MT, typename E, typename A>
 cudaError_t launch_kv8_decode_t(const A& a, int ncta, cudaStream_t st) {
-  const int R = kd_rows(a), nteam = W / k8_team((R + 7) / 8);
-  const int smem = K8Layout<D, W, A>::slots(R) + 2 * nteam * kBlock * D;
+  const int R = kd_rows(a), Rp = (R + 8 * MT - 1) / (8 * MT) * (8 * MT), nteam = W / (Rp / (8 * MT));
+  constexpr int least = W == 14 ? 24 : 8 * MT;     // padded rows there are at least: the most teams
+  static_assert(K8Layout<D, W, MT, A>::slots(least) + 2 * (W * 8 * MT / least) * kBlock * D <= kK8SharedBytes, "shared memory");
+  const int smem = K8Layout<D, W, MT, A>::slots(Rp) + 2 * nteam * kBlock * D;
   const cudaError_t e =
-      cudaFuncSetAttribute(kv8_decode_kernel<D, W, E, A>, cudaFuncAttributeMaxDynamicSharedMemorySize, kK8SharedBytes);
+      cudaFuncSetAttribute(kv8_decode_kernel<D, W, MT, E, A>, cudaFuncAttributeMaxDynamicSharedMemorySize, kK8SharedBytes);
   if (e != cudaSuccess) return e;
-  launch_pdl(kv8_decode_kernel<D, W, E, A>, dim3(ncta), dim3(kK8Threads<W>), smem, st, a);
+  launch_pdl(kv8_decode_kernel<D, W, MT, E, A>, dim3(ncta), dim3(kK8Threads<W, MT>), smem, st, a);
   if (ncta > 1 && !a.whole)
     launch_pdl(decode_join_kernel<D, A>, dim3(ncta - 1, (R + kKdJoinWarps - 1) / kKdJoinWarps), dim3(kKdJoinWarps * 32), 0, st, a, ncta);
   return cudaGetLastError();
 }
+// Ten warps for one tile of rows.  With more, eight warps of two tiles each, whose
+// codes are converted once for both, where eight are shared out evenly, i.e. with 2,
+// 4 or 8 tiles, else fourteen of one.  8 sequences of up to 20,000 tokens, d = 128,
+// eight of two against fourteen of one in us: 16 rows 72 against 80, 24 rows 121
+// against 104, 32 rows 122 against 139, 40 rows 213 against 192, 48 rows 213 against
+// 196, 56 rows 230 against 233, 64 rows 232 against 307.
 template <int D, typename E, typename A>
 cudaError_t launch_kv8_decode_w(const A& a, int ncta, cudaStream_t st) {
-  // One tile of rows is bound by memory: as many warps as there is shared memory for
-  // their slots.  Several are bound by the instructions, and teams share slots: as
-  // many warps as 128 registers allow (drafts of 24 rows: 120 us with ten, 104
-  // with fourteen; the batch of 64 takes all of the shared memory with ten).
   if constexpr (!A::kPerToken)         // (lists have one tile)
-    if (kd_rows(a) > 8) return launch_kv8_decode_t<D, 14, E>(a, ncta, st);
-  return launch_kv8_decode_t<D, 10, E>(a, ncta, st);
+    if (kd_rows(a) > 8) {
+      const int tiles = (kd_rows(a) + 7) / 8;
+      return (tiles & (tiles - 1)) == 0 ? launch_kv8_decode_t<D, 8, 2, E>(a, ncta, st) : launch_kv8_decode_t<D, 14, 1, E>(a, ncta, st);
+    }
+  return launch_kv8_decode_t<D, 10, 1, E>(a, ncta, st);
 }
 template <typename A>
 cudaError_t launch_kv8_decode(const A& a, int d, bool bf16, int ncta, cudaStream_t st) {
