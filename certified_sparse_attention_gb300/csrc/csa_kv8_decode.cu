@@ -39,6 +39,7 @@
 namespace csa {
 
 // W: consumer warps of a CTA, MT: tiles of 8 rows to each
+constexpr int kK8Warps = 10;      // W for one tile of rows
 constexpr int kK8Side = 2;        // ... and warps that fetch the queries and merge the sums
 // (MT = 2: and two that only fill a warpgroup, from which registers move to the
 // consumers': the launch has 168 a thread)
@@ -531,8 +532,7 @@ __global__ void __launch_bounds__(kK8Threads<W, MT>, 1) kv8_decode_kernel(const 
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int R = kd_rows(a), Rp = (R + 8 * MT - 1) / (8 * MT) * (8 * MT);
   // teams: warps that share a block, MT tiles of rows each (those left over idle)
-  // (ten warps are for one tile)
-  const int team = W == 10 ? 1 : Rp / (8 * MT), nteam = W / team;
+  const int team = W == kK8Warps ? 1 : Rp / (8 * MT), nteam = W / team;
   const unsigned bars = smem_u32(k8_sm), item_full = bars + 4 * W * 8, sums_full = item_full + 8 * kK8Items, sums_empty = sums_full + 8;
   KdItem<A>* items = reinterpret_cast<KdItem<A>*>(k8_sm + Lt::item);
   int32_t* s_ids = reinterpret_cast<int32_t*>(k8_sm + Lt::ids);
@@ -748,24 +748,45 @@ __global__ void __launch_bounds__(kK8Threads<W, MT>, 1) kv8_decode_kernel(const 
 
 namespace {
 
-// Items of up to this many blocks stay whole.
+// Items stay whole, and need no second kernel, where their blocks are one round of
+// a CTA's warps at most, and up to 16 blocks where there are items for a quarter of
+// the SMs.  Whole / cut, us, bf16, d = 128:
+//                     500 tokens     1000 tokens    1500 tokens    2000 tokens
+//     8 items,  8 rows  10.0 / 11.0    12.4 / 11.7    15.0 / 12.4    18.1 / 12.6
+//              24 rows  21.5 / 17.6    27.3 / 18.2    34.4 / 19.0    40.9 / 19.3
+//              64 rows  45.9 / 34.9    60.0 / 35.5    74.9 / 34.9    89.1 / 35.6
+//    32 items,  8 rows        -        13.2 / 13.2    15.8 / 13.4    19.1 / 13.9
+//              32 rows        -        33.8 / 26.2    41.8 / 27.9    49.1 / 30.8
+//    64 items,  8 rows        -        13.3 / 16.0    16.2 / 16.7    21.2 / 19.9
+//              32 rows        -        34.0 / 33.0    44.9 / 38.5    54.5 / 46.3
+//   160 items,  8 rows        -        23.4 / 25.4    27.8 / 29.1    32.7 / 31.1
+//              32 rows        -        62.3 / 59.7    78.9 / 67.8    92.9 / 73.8
+//   512 items,  8 rows        -        40.5 / 42.3    48.0 / 50.9    55.9 / 58.0
+//              32 rows        -         115 / 127      145 / 145      176 / 168
+// (160 are one more than the SMs have in a round: the worst for whole ones.)
 constexpr int64_t kK8WholeBlocks = 16;
 int64_t k8_blocks(const csa_shape* s, int n_sel) {
   const int64_t blocks = (s->n_max + kBlock - 1) / kBlock;
   return n_sel && n_sel < blocks ? n_sel : blocks;
 }
-int k8_whole(const csa_shape* s, int n_sel) { return k8_blocks(s, n_sel) <= kK8WholeBlocks; }
+int64_t k8_items(const csa_shape* s, int T, int n_sel) { return (int64_t)s->B * s->Hkv * (n_sel ? T : 1); }
+int k8_rows_of(const csa_shape* s, int T, int n_sel) { return (n_sel ? 1 : T) * (s->Hq / s->Hkv); }
+int k8_whole(const csa_shape* s, int T, int n_sel) {
+  const int64_t blocks = k8_blocks(s, n_sel);
+  return blocks * ((k8_rows_of(s, T, n_sel) + 7) / 8) <= kK8Warps ||
+         (blocks <= kK8WholeBlocks && 4 * k8_items(s, T, n_sel) > sm_count());
+}
 
 // CTAs of the decode kernel: one per SM, no more than there can be units
 int k8_ctas(const csa_shape* s, int T, int n_sel) {
-  const int64_t units = (int64_t)s->B * s->Hkv * (n_sel ? T : 1) * (k8_whole(s, n_sel) ? 1 : k8_blocks(s, n_sel));
+  const int64_t units = k8_items(s, T, n_sel) * (k8_whole(s, T, n_sel) ? 1 : k8_blocks(s, n_sel));
   const int nsm = sm_count() < Kv8DecodeArgs<true>::kMaxCtas ? sm_count() : Kv8DecodeArgs<true>::kMaxCtas;
   return (int)(units < nsm ? units : nsm);
 }
 
 size_t k8_workspace(const csa_shape* s, int T, int n_sel) {
-  const int R = (n_sel ? 1 : T) * (s->Hq / s->Hkv);
-  return 256 + (k8_whole(s, n_sel) ? 0 : (size_t)2 * k8_ctas(s, T, n_sel) * R * (s->d + 4) * 4);
+  const size_t rows = 2 * (size_t)k8_ctas(s, T, n_sel) * k8_rows_of(s, T, n_sel);
+  return 256 + (k8_whole(s, T, n_sel) ? 0 : rows * (s->d + 4) * 4);
 }
 
 // Dynamic shared memory there can be: a CTA's 227 KB without the kernel's own.
@@ -800,7 +821,7 @@ cudaError_t launch_kv8_decode_w(const A& a, int ncta, cudaStream_t st) {
       const int tiles = (kd_rows(a) + 7) / 8;
       return (tiles & (tiles - 1)) == 0 ? launch_kv8_decode_t<D, 8, 2, E>(a, ncta, st) : launch_kv8_decode_t<D, 14, 1, E>(a, ncta, st);
     }
-  return launch_kv8_decode_t<D, 10, 1, E>(a, ncta, st);
+  return launch_kv8_decode_t<D, kK8Warps, 1, E>(a, ncta, st);
 }
 template <typename A>
 cudaError_t launch_kv8_decode(const A& a, int d, bool bf16, int ncta, cudaStream_t st) {
@@ -835,7 +856,7 @@ csa_status k8_decode(const csa_shape* shape, const csa_kv8* cache, int T, const 
   a.B = shape->B; a.T = T; a.Hq = shape->Hq; a.Hkv = shape->Hkv; a.G = shape->Hq / shape->Hkv;
   a.rs = (float)(1.4426950408889634 / std::sqrt((double)shape->d));
   const int ncta = k8_ctas(shape, T, n_sel);
-  a.whole = k8_whole(shape, n_sel);
+  a.whole = k8_whole(shape, T, n_sel);
   add_launches(ncta > 1 && !a.whole ? 2 : 1);
   const cudaError_t e = launch_kv8_decode(a, shape->d, bf16, ncta, (cudaStream_t)stream);
   return e == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;

@@ -465,9 +465,12 @@ cudaError_t launch_select(Kv8SelectArgs a, cudaStream_t st) {
   const int64_t fit = (kSelShared - least) / (a.nblk_max * 4) * cluster;
   if (tokens > fit) tokens = (int)fit;
   const int64_t rows = (tokens + cluster - 1) / cluster * a.nblk_max * 4;
-  // Sixteen warps to a CTA where even clusters of eight leave SMs idle and the
-  // context is long; all of them at work where there is room for their chunk.
-  const bool wide = tiles * cluster <= sm_count() && a.nblk_max >= 4096 && rows + 4 * least <= kSelShared;
+  // Sixteen warps to a CTA where the context is long and there are CTAs for half
+  // of the SMs at most (clusters of eight lie within groups of SMs, and a card full
+  // of them, one CTA to an SM, takes two rounds); all of them at work where there is
+  // room for their chunk.  Sixteen / eight, us: 1 sequence of 128K tokens 8.4 / 8.1,
+  // 256K 10.5 / 11.8, 1M 24 / 33; 2 sequences (a full card) 128K 12 / 9, 256K 16 / 13.
+  const bool wide = 2 * tiles * cluster <= sm_count() && a.nblk_max >= 4096 && rows + 4 * least <= kSelShared;
   a.tokens = tokens;
   a.clog = clog;
   a.chunk = wide ? 256 : rows + 2 * least <= kSelShared ? 128 : 64;
