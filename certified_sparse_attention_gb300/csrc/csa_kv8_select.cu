@@ -14,6 +14,10 @@
 // ordered integers, in the shared memory of one CTA of the cluster, which then
 // finds the n_sel-th largest by histograms and writes the blocks above it, and
 // the first ones equal to it, in ascending order.
+//
+// d = 128, 32 / 8 heads: 64 sequences of 2K to 16K tokens 12.6 us, one of 1M 23.5:
+// the latency of phases that depend on one another (query codes, operands, scores,
+// ranking: about half of the last), not the 17 or 35 MB of spans.
 #include <algorithm>
 
 #include <cuda_fp16.h>
