@@ -1,8 +1,8 @@
 // Decode attention over a K/V cache whose whole blocks of 64 tokens are held
 // in codes and whose incomplete last block is held in full precision: what the
 // kernels for the different codes share.  That is how the batch's work is dealt
-// to the CTAs, the queries of an item, the incomplete block's plain path, the
-// rows' outputs and the join of items that were cut.
+// to the CTAs, the queries of an item, the rows' outputs and the join of items
+// that were cut.
 //
 // The argument block A of a kernel is derived from DecodeArgs and says
 //   kLead, kTailBase, kTailStep   what an item and its incomplete block cost, in
@@ -249,149 +249,11 @@ __device__ __forceinline__ void kd_store(const A& a, const KdSegOf<A>& s, int r,
   if (c == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
 }
 
-// The query rows of an item in shared memory: row r starts at r (D + 16), its
-// channels in four pieces 4 floats apart (bank offsets, as for the bounds).
-// They are log2(e) / sqrt(d) q (kPlainQ: q) times a power of two that puts the
-// row's largest at 2^11 .. 2^12 (undone by s_inv[r]).
-template <int D> __host__ __device__ __forceinline__ constexpr int kd_q(int r, int c) { return r * (D + 16) + c + c / (D / 4) * 4; }
-
-template <int D, int RT>
-struct KdState {
-  float m[RT], l[RT], acc[RT][D / 32];
-};
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// CNT consecutive elements (16 bytes aligned) as floats
-template <int CNT>
-__device__ __forceinline__ void kd_floats(const float* p, float (&x)[CNT]) {
-#pragma unroll
-  for (int i = 0; i < CNT; i += 4) {
-    const float4 v = *reinterpret_cast<const float4*>(p + i);
-    x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
-  }
-}
-template <int CNT>
-__device__ __forceinline__ void kd_floats(const __nv_bfloat16* p, float (&x)[CNT]) {
-#pragma unroll
-  for (int i = 0; i < CNT; i += 8) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p + i);
-    const unsigned u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[i + e] = __uint_as_float(e & 1 ? u[e / 2] & 0xFFFF0000u : u[e / 2] << 16);
-  }
-}
-
-// One online-softmax step of a warp over `have` <= NT full-precision tokens at
-// K, V (rows of D), the first at position pos.  Scores: lane (gid,
-// tid) takes token gid and the channels [tid NC, (tid + 1) NC) of every query
-// row; values: a lane takes the channels [lane D / 32, ...) of the state st, the
-// weights come through s_p ([NT][RT] floats).  Row r sees positions below
-// s_end[r].
-//
-// With 8 rows four tokens to a step, so that more warps share a block's tokens
-// (batch of 64: 128 us, with eight 130; drafts of 24 rows 120 and 123); with 4
-// rows, where a step costs half, eight (one sequence of 1000 tokens: 12.5 us,
-// with four 14.4: some warps then have steps after their second block).
-template <int RT> constexpr int kKdStep = RT == 8 ? 4 : 8;
-template <int D, int RT, typename E>
-__device__ __forceinline__ void kd_step(KdState<D, RT>& st, const E* K, const E* V, int have, const float* s_q,
-                                        const float* s_inv, const int64_t* s_end, int64_t pos, float* s_p) {
-  constexpr int CPL = D / 32, NT = kKdStep<RT>, LPT = 32 / NT, NC = D / LPT;
-  const int lane = threadIdx.x & 31, gid = lane / LPT, tid = lane % LPT;
-  float vv[NT][CPL];
-#pragma unroll
-  for (int e = 0; e < NT; ++e) {
-#pragma unroll
-    for (int c = 0; c < CPL; ++c) vv[e][c] = 0.0f;
-    if (e < have) {
-      if (CPL == 4) {
-        const float4 v = Elem<E>::get4(V + e * D + lane * CPL);
-        vv[e][0] = v.x; vv[e][1] = v.y; vv[e][CPL - 2] = v.z; vv[e][CPL - 1] = v.w;
-      } else {
-        const float2 v = Elem<E>::get2(V + e * D + lane * CPL);
-        vv[e][0] = v.x; vv[e][1] = v.y;
-      }
-    }
-  }
-  float k[NC], s[RT];
-  kd_floats<NC>(K + (gid < have ? gid : 0) * D + tid * NC, k);
-  bool cut = have < NT;                   // some row does not see some token
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    float even = 0.0f, odd = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NC; i += 4) {
-      const float4 q = *reinterpret_cast<const float4*>(s_q + kd_q<D>(r, tid * NC) + i);
-      even = fmaf(k[i], q.x, even); odd = fmaf(k[i + 1], q.y, odd);
-      even = fmaf(k[i + 2], q.z, even); odd = fmaf(k[i + 3], q.w, odd);
-    }
-    s[r] = (even + odd) * s_inv[r];
-    cut = cut || s_end[r] < pos + NT;
-  }
-#pragma unroll
-  for (int m = 1; m < LPT; m <<= 1)
-#pragma unroll
-    for (int r = 0; r < RT; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], m);
-  float top[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    if (gid >= have || pos + gid >= s_end[r]) s[r] = -INFINITY;
-    top[r] = s[r];
-  }
-#pragma unroll
-  for (int m = LPT; m < 32; m <<= 1)
-#pragma unroll
-    for (int r = 0; r < RT; ++r) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], m));
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const float mn = fmaxf(st.m[r], top[r]), ref = mn > -INFINITY ? mn : 0.0f;
-    const float old = ex2(st.m[r] - ref);
-    st.m[r] = mn;
-    st.l[r] *= old;
-#pragma unroll
-    for (int c = 0; c < CPL; ++c) st.acc[r][c] *= old;
-    // an unseen token is marked
-    const bool seen = gid < have && pos + gid < s_end[r];
-    if (r * LPT / RT == tid) s_p[gid * RT + r] = seen ? ex2(s[r] - ref) : -1.0f;
-  }
-  __syncwarp();
-#pragma unroll
-  for (int e = 0; e < NT; ++e) {
-    float p[RT];
-#pragma unroll
-    for (int r = 0; r < RT; r += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(s_p + e * RT + r);
-      p[r] = v.x; p[r + 1] = v.y; p[r + 2] = v.z; p[r + 3] = v.w;
-    }
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      // an unseen token's value may be anything: it is left out, not
-      // multiplied by zero
-      if (!cut || !(p[r] < 0.0f)) {
-        st.l[r] += p[r];
-#pragma unroll
-        for (int c = 0; c < CPL; ++c) st.acc[r][c] = fmaf(p[r], vv[e][c], st.acc[r][c]);
-      }
-    }
-  }
-  __syncwarp();
-}
-
-// ------------------------------------------------------- moving the blocks
-
-// A ring of slots with full and empty barriers.  Block i sits in slot i %
-// slots and is taken by team i % teams; slots is a multiple of teams, so a
-// slot serves one team, which has seen its last phase when it waits for the
-// next.
-struct KdRing {
-  uint8_t* data;
-  unsigned full, empty;
-  int slots;
-};
 
 // ------------------------------------------------------ tensor-core blocks
 
@@ -421,28 +283,19 @@ __device__ __forceinline__ unsigned half_pair(float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
   return *reinterpret_cast<const unsigned*>(&h);
 }
-__device__ __forceinline__ unsigned half_rest(float x, float y, unsigned hi) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  return half_pair(x - f.x, y - f.y);
-}
 // 2^k, -126 <= k <= 127
 __device__ __forceinline__ float pow2i(int k) { return __int_as_float((127 + k) << 23); }
 // exponent of x > 0 (subnormals: -127)
 __device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
-// the pair (x low, y high) in half precision, truncated
-__device__ __forceinline__ unsigned half_pair_rz(float x, float y) {
-  unsigned r;
-  asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
-  return r;
-}
-
 // The queries of an item and what else its warps need of it: filled by producer
-// warps, four rows at a time, an item ahead.
+// warps, four rows at a time, ahead of the sums.  Query rows are log2(e) / sqrt(d) q
+// (kPlainQ: q) times a power of two that puts the row's largest at 2^11 .. 2^12
+// (undone by inv), laid out by A::put.
 template <typename A>
 struct KdItem {
   KdSegOf<A> seg;
   int64_t end[CSA_KV4_MAX_ROWS];    // row r sees positions below end[r]
-  float inv[CSA_KV4_MAX_ROWS];      // undoes the scale of row r (kd_q)
+  float inv[CSA_KV4_MAX_ROWS];      // undoes the scale of row r
   int top[CSA_KV4_MAX_ROWS];        // of the channel of the largest of row r: A::top
 };
 

@@ -6,14 +6,15 @@
 //   I = sum_c q_c (q_c >= 0 ? hi_c : lo_c) = sum_c q+_c hi_c + sum_c q-_c lo_c,
 // q+ and q- the positive and negative parts of the query's 8-bit codes: one
 // product of 2 d channels, on the tensor cores in half precision, 16 blocks x 8 rows x
-// 16 channels an instruction (their rate bounds it: with rows and blocks the other
-// way round, half of each instruction idle, 4 x 128K tokens took 17 us).  The codes enter 1152 too large, which the sums of q+
-// and q- correct; each sum is over 64 channels, below 64 127 1279 < 2^24, so all of
-// it is exact.  The blocks' spans go from memory to the operands' registers, 16
-// bytes a lane, each read once per cluster.  A token's scores are collected, as
-// ordered integers, in the shared memory of one CTA of the cluster, which then
-// finds the n_sel-th largest by histograms and writes the blocks above it, and
-// the first ones equal to it, in ascending order.
+// 16 channels an instruction (with rows and blocks the other way round, half of each
+// instruction idle, 4 x 128K tokens took 17 us, now 12).  The codes enter 1152 too
+// large, which the sums of q+ and q- correct; each sum is over 64 channels, below
+// 64 127 1279 < 2^24, so all of it is exact.  The blocks' spans go from memory to
+// shared memory by bulk copies and from there to the operands' registers, 16 bytes
+// a lane, each once per cluster.  A token's scores are collected, as ordered
+// integers, in the shared memory of one CTA of the cluster, which then finds the
+// n_sel-th largest by histograms and writes the blocks above it, and the first ones
+// equal to it, in ascending order.
 //
 // d = 128, 32 / 8 heads: 64 sequences of 2K to 16K tokens 12.6 us, one of 1M 23.5:
 // the latency of phases that depend on one another (query codes, operands, scores,

@@ -312,7 +312,8 @@ def check_decode(o, lse, q, model, lens, nq, G):
 
 
 @pytest.mark.parametrize("G,T", [(1, 1), (2, 1), (4, 1), (8, 1), (4, 2), (1, 5),
-                                 (2, 3), (4, 5), (8, 3), (8, 8), (1, 16), (4, 16)])
+                                 (2, 3), (4, 5), (8, 3), (8, 8), (1, 16), (4, 16),
+                                 (8, 2), (8, 4), (8, 6), (8, 7)])
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64), ("f32", 128), ("bf16", 64)])
 def test_decode(G, T, dtype, d):
     torch, csa, dev = _t()
