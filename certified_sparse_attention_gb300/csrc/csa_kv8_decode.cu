@@ -71,6 +71,7 @@ struct Kv8DecodeArgs : DecodeArgs {
   const int32_t* blocks;  // LIST: [B][T][Hkv][n_sel], count [B][T][Hkv]
   const int32_t* count;
   int n_sel;
+  int clog;               // whole: log2 of the CTAs that share an item
   // Fitted to the times of single CTAs (batch of 64, 8 query heads to a KV head: a
   // block 0.355 us, an item 1.5 to 3 us, its incomplete block 1.5 us).  Leads of 5
   // and of 12 take the same time there; 128 sequences of up to 2000 tokens take 101,
@@ -458,13 +459,55 @@ __device__ __forceinline__ void floats_out(float* p, const float (&x)[CPL]) {
   else *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
 }
 
+// shared memory of CTA `rank` of the cluster
+__device__ __forceinline__ unsigned cluster_at(unsigned own, unsigned rank) {
+  unsigned at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(at) : "r"(own), "r"(rank));
+  return at;
+}
+__device__ __forceinline__ float4 cluster_load4(unsigned at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];\n" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 cluster_load2(unsigned at) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];\n" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
+}
+// every CTA's side warps (the other warps take no part: they end)
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+
+// a finished row: the lane's D / 32 channels
+template <int D, typename A>
+__device__ __forceinline__ void k8_out(const A& a, const KdSegOf<A>& s, int r, float M, float l, float (&v)[D / 32]) {
+  constexpr int CPL = D / 32;
+  const int lane = threadIdx.x & 31, glog = 31 - __clz(a.G);
+  int t = r >> glog;
+  const int h = s.g * a.G + (r & (a.G - 1));
+  if constexpr (A::kPerToken) t = s.t;
+  if (t >= s.nq) return;
+  const int64_t row = ((int64_t)s.b * a.T + t) * a.Hq + h;
+  // l = 0 only where nothing was attended to
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) v[c] = l == 0.0f ? 0.0f : v[c] * inv;
+  floats_out<CPL>(a.o + row * D + lane * CPL, v);
+  if (lane == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
+}
+
 // The item's sums from its teams' (team_rows rows each), by a side warp: rows
 // [r0, r1), four at a time.  First a lane to a team, then D / 32 channels to a lane.
+// Where the CTA has a part of the item only they go to the workspace, or to `keep`
+// (rows of D, then m and l of each) for the other CTAs of the cluster.
 template <int D, int MT, typename A>
 __device__ __forceinline__ void k8_merge(const A& a, const KdSegOf<A>& s, int nteam, int team_rows, const float* s_m, const float* s_l,
-                                         const float* s_acc, int r0, int r1) {
+                                         const float* s_acc, float* keep, int r0, int r1) {
   constexpr int CPL = D / 32, N = 4;
-  const int lane = threadIdx.x & 31, R = kd_rows(a), glog = 31 - __clz(a.G);
+  const int lane = threadIdx.x & 31, R = kd_rows(a);
   float* part = a.part + (2 * (int64_t)blockIdx.x + (s.cut0 ? 0 : 1)) * R * (D + 4) + lane * CPL;
   for (int r = r0; r < min(r1, R); r += N) {
     float M[N], l[N], f[N], v[N][CPL];
@@ -506,9 +549,7 @@ __device__ __forceinline__ void k8_merge(const A& a, const KdSegOf<A>& s, int nt
     for (int i = 0; i < N; ++i) {
       l[i] = __shfl_sync(0xffffffffu, l[i], 0);
       if (r + i >= R) continue;
-      int t = (r + i) >> glog, h = s.g * a.G + ((r + i) & (a.G - 1));
       if constexpr (A::kPerToken) {
-        t = s.t;
         if (s.bad) {
           M[i] = 0.0f;
           l[i] = NAN;
@@ -516,20 +557,72 @@ __device__ __forceinline__ void k8_merge(const A& a, const KdSegOf<A>& s, int nt
           for (int c = 0; c < CPL; ++c) v[i][c] = NAN;
         }
       }
-      if (s.cut0 || s.cut1) {
+      if (a.clog) {
+        floats_out<CPL>(keep + (r + i) * D + lane * CPL, v[i]);
+        if (lane == 0) *reinterpret_cast<float2*>(keep + R * D + 2 * (r + i)) = make_float2(M[i], l[i]);
+      } else if (s.cut0 || s.cut1) {
         float* to = part + (r + i) * (D + 4);
         floats_out<CPL>(to, v[i]);
         if (lane == 0) { to[D] = M[i]; to[D + 1] = l[i]; }
-      } else if (t < s.nq) {
-        const int64_t row = ((int64_t)s.b * a.T + t) * a.Hq + h;
-        // l = 0 only where nothing was attended to
-        const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
-#pragma unroll
-        for (int c = 0; c < CPL; ++c) v[i][c] = l[i] == 0.0f ? 0.0f : v[i][c] * inv;
-        floats_out<CPL>(a.o + row * D + lane * CPL, v[i]);
-        if (lane == 0 && a.lse) a.lse[row] = l[i] == 0.0f ? -INFINITY : (M[i] + log2f(l[i])) * 0.69314718055994531f;
+      } else {
+        k8_out<D>(a, s, r + i, M[i], l[i], v[i]);
       }
     }
+  }
+}
+
+// The share of CTA `rank` of the 2^clog that take an item together: whole blocks in
+// turn, the incomplete one with the first share, which is the smallest.
+template <typename S>
+__device__ __forceinline__ void k8_take(S& s, int rank, int clog) {
+  const int lo = (int)((int64_t)s.nfast * rank >> clog), hi = (int)((int64_t)s.nfast * (rank + 1) >> clog);
+  s.blk0 += lo;
+  s.nfast = hi - lo;
+  s.clear = min(max(s.clear - lo, 0), s.nfast);
+  if (rank) s.left = 0;
+}
+// The item's sums from its CTAs' (keep), by side warp `part` of CTA `rank`: rows
+// rank, rank + the CTAs, ...  First a lane to a CTA, then D / 32 channels to a lane.
+template <int D, typename A>
+__device__ __forceinline__ void k8_join(const A& a, const KdSegOf<A>& s, const float* keep, int rank, int part) {
+  constexpr int CPL = D / 32, N = 8;
+  const int lane = threadIdx.x & 31, R = kd_rows(a), n = 1 << a.clog;
+  const unsigned at = smem_u32(keep);
+  for (int r = rank + part * n; r < R; r += kK8Side * n) {
+    float z[N][CPL];
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (k < n) {
+        const unsigned from = cluster_at(at + (r * D + lane * CPL) * 4, k);
+        if (CPL == 4) {
+          const float4 y = cluster_load4(from);
+          z[k][0] = y.x; z[k][1] = y.y; z[k][CPL - 2] = y.z; z[k][CPL - 1] = y.w;
+        } else {
+          const float2 y = cluster_load2(from);
+          z[k][0] = y.x; z[k][1] = y.y;
+        }
+      }
+    const float2 ml = lane < n ? cluster_load2(cluster_at(at + (R * D + 2 * r) * 4, lane)) : make_float2(-INFINITY, 0.0f);
+    float M = ml.x;
+#pragma unroll
+    for (int o = 1; o < N; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    M = __shfl_sync(0xffffffffu, M, 0);
+    const float f = k8_factor(ml.x, ml.y, M);
+    float l = ml.y * f, v[CPL];
+#pragma unroll
+    for (int o = 1; o < N; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    l = __shfl_sync(0xffffffffu, l, 0);
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) v[c] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const float w = __shfl_sync(0xffffffffu, f, k);
+      if (k < n) {
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) v[c] = fmaf(w, z[k][c], v[c]);
+      }
+    }
+    k8_out<D>(a, s, r, M, l, v);
   }
 }
 
@@ -563,8 +656,9 @@ __global__ void __launch_bounds__(kK8Threads<W, MT>, 1) kv8_decode_kernel(const 
     fence_barrier_init();
   }
   kd_batch(a, batch);
-  const int64_t per = kd_run(batch, gridDim.x);
-  int64_t u0 = (int64_t)blockIdx.x * per, u1 = min(batch.pref[kMaxB], u0 + per);
+  const int64_t per = kd_run(batch, gridDim.x >> a.clog);
+  const int rank = blockIdx.x & ((1 << a.clog) - 1);
+  int64_t u0 = (int64_t)(blockIdx.x >> a.clog) * per, u1 = min(batch.pref[kMaxB], u0 + per);
   kd_trim(a, batch, u0, u1);
   // (Each wait is bounded: one that gives up marks the call, and the warp goes
   // on without waiting.)
@@ -592,8 +686,11 @@ __global__ void __launch_bounds__(kK8Threads<W, MT>, 1) kv8_decode_kernel(const 
       if (u >= u1) return;
       KdItem<A>& it = items[buf];
       sg = u == u0 ? kd_seg(a, batch, u, u1) : kd_next(a, batch, sg, u, u1);
+      const int32_t* ids = nullptr;
+      if constexpr (A::kPerToken) ids = kd_list(a, sg);
+      if (a.clog) k8_take(sg, rank, a.clog);
       if constexpr (A::kPerToken) {
-        const int32_t* ids = kd_list(a, sg) + sg.blk0;
+        ids += sg.blk0;
         if (part == 0)
           for (int x = lane; x < min(sg.nfast, kKdIds); x += 32) s_ids[buf * kKdIds + x] = ids[x];
       }
@@ -604,11 +701,12 @@ __global__ void __launch_bounds__(kK8Threads<W, MT>, 1) kv8_decode_kernel(const 
       u += sg.step;
     };
     for (int buf = 0; buf < kK8Items; ++buf) fetch(buf);
+    float* keep = s_q + Rp * D;                   // (with a.clog there is one item: the other places are free)
     int64_t done = u0;
     for (int k = 0, buf = 0; done < u1; ++k) {
       if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(sums_full, k & 1));
       const KdSegOf<A> s = items[buf].seg;
-      k8_merge<D, MT>(a, s, nteam, team * MT * 8, s_m, s_l, s_acc, part * (Rp / kK8Side), (part + 1) * (Rp / kK8Side));
+      k8_merge<D, MT>(a, s, nteam, team * MT * 8, s_m, s_l, s_acc, keep, part * (Rp / kK8Side), (part + 1) * (Rp / kK8Side));
       __syncwarp();
       if (lane == 0) mbar_arrive(sums_empty);
       done += s.step;
@@ -617,6 +715,11 @@ __global__ void __launch_bounds__(kK8Threads<W, MT>, 1) kv8_decode_kernel(const 
       if (++buf == kK8Items) buf = 0;
     }
     if (dead && lane == 0) atomicOr(a.status, 4u);
+    if (a.clog && u0 < u1) {
+      cluster_sync();
+      k8_join<D>(a, items[0].seg, keep, rank, part);
+      cluster_sync();                             // (its shared memory has been read)
+    }
     return;
   }
 
@@ -782,14 +885,33 @@ int64_t k8_blocks(const csa_shape* s, int n_sel) {
 }
 int64_t k8_items(const csa_shape* s, int T, int n_sel) { return (int64_t)s->B * s->Hkv * (n_sel ? T : 1); }
 int k8_rows_of(const csa_shape* s, int T, int n_sel) { return (n_sel ? 1 : T) * (s->Hq / s->Hkv); }
+// Few items of few blocks: 2, 4 or 8 CTAs to an item, which join their sums through
+// shared memory, where that makes two rounds of their warps at most, or four with
+// CTAs for more than half of the SMs.  Eight only for half of the SMs: a card full
+// of such clusters, which lie within groups of SMs, takes two rounds.  Shared /
+// cut, us, bf16, d = 128:
+//                      1000 tokens    2000 tokens    4000 tokens    8000 tokens
+//    8 items,  4 rows  11.4 / 12.0    10.5 / 12.2    11.5 / 13.9    13.8 / 14.4
+//             20 rows  16.7 / 18.0    16.9 / 19.1    21.3 / 20.4    27.4 / 23.8
+//             64 rows  34.4 / 37.0    35.4 / 36.9    45.7 / 39.9    58.6 / 47.1
+//   32 items,  4 rows  12.0 / 13.0    11.6 / 13.9    17.0 / 18.2    24.2 / 24.3
+//             16 rows  17.3 / 20.4    20.2 / 22.9    27.4 / 27.9    33.6 / 36.4
+int k8_clog(const csa_shape* s, int T, int n_sel) {
+  const int64_t items = k8_items(s, T, n_sel), work = k8_blocks(s, n_sel) * ((k8_rows_of(s, T, n_sel) + 7) / 8);
+  int clog = 0;
+  while (clog < 3 && (items << (clog + 1)) <= (clog < 2 ? sm_count() : sm_count() / 2) && work > (kK8Warps << clog)) ++clog;
+  const int rounds = 2 * (items << clog) <= sm_count() ? 2 : 4;
+  return work <= ((int64_t)rounds * kK8Warps << clog) ? clog : 0;
+}
 int k8_whole(const csa_shape* s, int T, int n_sel) {
   const int64_t blocks = k8_blocks(s, n_sel);
   return blocks * ((k8_rows_of(s, T, n_sel) + 7) / 8) <= kK8Warps ||
-         (blocks <= kK8WholeBlocks && 4 * k8_items(s, T, n_sel) > sm_count());
+         (blocks <= kK8WholeBlocks && 4 * k8_items(s, T, n_sel) > sm_count()) || k8_clog(s, T, n_sel);
 }
 
 // CTAs of the decode kernel: one per SM, no more than there can be units
 int k8_ctas(const csa_shape* s, int T, int n_sel) {
+  if (k8_clog(s, T, n_sel)) return (int)k8_items(s, T, n_sel) << k8_clog(s, T, n_sel);
   const int64_t units = k8_items(s, T, n_sel) * (k8_whole(s, T, n_sel) ? 1 : k8_blocks(s, n_sel));
   const int nsm = sm_count() < Kv8DecodeArgs<true>::kMaxCtas ? sm_count() : Kv8DecodeArgs<true>::kMaxCtas;
   return (int)(units < nsm ? units : nsm);
@@ -814,7 +936,21 @@ cudaError_t launch_kv8_decode_t(const A& a, int ncta, cudaStream_t st) {
   const cudaError_t e =
       cudaFuncSetAttribute(kv8_decode_kernel<D, W, MT, E, A>, cudaFuncAttributeMaxDynamicSharedMemorySize, kK8SharedBytes);
   if (e != cudaSuccess) return e;
-  launch_pdl(kv8_decode_kernel<D, W, MT, E, A>, dim3(ncta), dim3(kK8Threads<W, MT>), smem, st, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ncta);
+  cfg.blockDim = dim3(kK8Threads<W, MT>);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1 << a.clog;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.clog ? 2 : 1;
+  const cudaError_t le = cudaLaunchKernelEx(&cfg, kv8_decode_kernel<D, W, MT, E, A>, a);
+  if (le != cudaSuccess) return le;
   if (ncta > 1 && !a.whole)
     launch_pdl(decode_join_kernel<D, A>, dim3(ncta - 1, (R + kKdJoinWarps - 1) / kKdJoinWarps), dim3(kKdJoinWarps * 32), 0, st, a, ncta);
   return cudaGetLastError();
@@ -868,6 +1004,7 @@ csa_status k8_decode(const csa_shape* shape, const csa_kv8* cache, int T, const 
   a.rs = (float)(1.4426950408889634 / std::sqrt((double)shape->d));
   const int ncta = k8_ctas(shape, T, n_sel);
   a.whole = k8_whole(shape, T, n_sel);
+  a.clog = k8_clog(shape, T, n_sel);
   add_launches(ncta > 1 && !a.whole ? 2 : 1);
   const cudaError_t e = launch_kv8_decode(a, shape->d, bf16, ncta, (cudaStream_t)stream);
   return e == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;

@@ -348,14 +348,16 @@ def test_decode(G, T, dtype, d):
 @pytest.mark.parametrize("dtype,d,G,lens", [
     ("bf16", 128, 4, [20011]), ("f32", 64, 8, [9000, 64 * 200, 77]),
     ("bf16", 64, 1, [4096] * 5), ("f32", 128, 2, [5000, 1])])
-def test_decode_longer(dtype, d, G, lens):
-    # items cut over many CTAs, joined from the workspace
+@pytest.mark.parametrize("n_max", [0, 70000])
+def test_decode_longer(dtype, d, G, lens, n_max):
+    # items cut over many CTAs, joined from the workspace (always with room for 70000
+    # tokens), or shared by a few
     torch, csa, dev = _t()
     rng = np.random.default_rng(len(lens) + d)
-    s, cache, model = filled(rng, dtype, d, 1, lens, max(lens), G, step=4096)
+    s, cache, model = filled(rng, dtype, d, 1, lens, max(lens + [n_max]), G, step=4096)
     q = rows(rng, (len(lens), 1, G, d), dtype)
     op = csa.KV8Decode(s, dev, 1, with_lse=True)
-    assert op.ws_bytes > 256
+    assert op.ws_bytes > 256 or not n_max
     op.ws.fill_(0xFF)
     o = op(q, cache, i64(lens))
     assert csa.csa_check(op.ws) == 0
@@ -365,18 +367,47 @@ def test_decode_longer(dtype, d, G, lens):
 @pytest.mark.parametrize("dtype,d,G,T", [
     ("bf16", 128, 4, 2), ("bf16", 64, 8, 8), ("f32", 128, 4, 5),
     ("bf16", 128, 1, 16), ("f32", 64, 2, 1), ("bf16", 128, 8, 3)])
-def test_decode_tokens_over_cut_sequences(dtype, d, G, T):
+@pytest.mark.parametrize("n_max", [5100, 30000])
+def test_decode_tokens_over_cut_sequences(dtype, d, G, T, n_max):
     # several query tokens, ragged, with sequences cut over CTAs at blocks
-    # that some tokens see in part
+    # that some tokens see in part (always with room for 30000 tokens), or shared
     torch, csa, dev = _t()
     rng = np.random.default_rng(7 * T + G)
     lens = [0, 1, 64, 1700, 5003, 130, 4992]
     nq = [min(T, 1 + i % T) for i in range(len(lens))]
     nq[0], nq[1], nq[3] = T, T, 0
-    s, cache, model = filled(rng, dtype, d, 2, lens, 5100, 2 * G, step=4096)
+    s, cache, model = filled(rng, dtype, d, 2, lens, n_max, 2 * G, step=4096)
     q = rows(rng, (len(lens), T, 2 * G, d), dtype)
     op = csa.KV8Decode(s, dev, T, with_lse=True)
-    assert op.ws_bytes > 256
+    assert op.ws_bytes > 256 or n_max == 5100
+    op.ws.fill_(0xFF)
+    op.o.fill_(55.0)
+    o = op(q, cache, i64(lens), i64(nq))
+    assert csa.csa_check(op.ws) == 0
+    on = f64(o)
+    check_decode(on, f64(op.lse), f64(q), model, lens, nq, G)
+    for b in range(len(lens)):
+        assert np.all(on[b, nq[b]:] == 55.0)
+    first = o.clone()
+    assert torch.equal(first, op(q, cache, i64(lens), i64(nq)))
+
+
+@pytest.mark.parametrize("dtype,d,H,G,T,lens", [
+    ("bf16", 128, 1, 4, 1, [1400]), ("f32", 64, 1, 2, 5, [64 * 31 + 63]), ("bf16", 64, 2, 8, 2, [700, 1300]),
+    ("f32", 128, 3, 4, 4, [0, 1, 65, 1000, 1407]), ("bf16", 128, 8, 8, 8, [520, 64]), ("bf16", 128, 7, 1, 3, [1291] * 10),
+    ("f32", 64, 2, 8, 7, [830] * 3), ("bf16", 128, 4, 8, 1, [1408, 5, 1344, 1345])])
+def test_decode_items_shared_by_ctas(dtype, d, H, G, T, lens):
+    # two, four or eight CTAs to an item: the fewest blocks there can be to each, shares
+    # without any, idle sequences, the incomplete block beside them
+    torch, csa, dev = _t()
+    rng = np.random.default_rng(100 * T + len(lens))
+    n_max = max(lens) + 7
+    nq = [i * 5 % (T + 1) for i in range(len(lens))]
+    nq[0] = T
+    s, cache, model = filled(rng, dtype, d, H, lens, n_max, H * G, step=1024)
+    q = rows(rng, (len(lens), T, H * G, d), dtype)
+    op = csa.KV8Decode(s, dev, T, with_lse=True)
+    assert op.ws_bytes == 256
     op.ws.fill_(0xFF)
     op.o.fill_(55.0)
     o = op(q, cache, i64(lens), i64(nq))
