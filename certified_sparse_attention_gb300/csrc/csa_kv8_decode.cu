@@ -891,15 +891,20 @@ int k8_rows_of(const csa_shape* s, int T, int n_sel) { return (n_sel ? 1 : T) * 
 // of such clusters, which lie within groups of SMs, takes two rounds.  Shared /
 // cut, us, bf16, d = 128:
 //                      1000 tokens    2000 tokens    4000 tokens    8000 tokens
-//    8 items,  4 rows  11.4 / 12.0    10.5 / 12.2    11.5 / 13.9    13.8 / 14.4
+//    8 items,  4 rows   9.8 / 12.0    10.5 / 12.2    11.5 / 13.9    13.8 / 14.4
 //             20 rows  16.7 / 18.0    16.9 / 19.1    21.3 / 20.4    27.4 / 23.8
 //             64 rows  34.4 / 37.0    35.4 / 36.9    45.7 / 39.9    58.6 / 47.1
-//   32 items,  4 rows  12.0 / 13.0    11.6 / 13.9    17.0 / 18.2    24.2 / 24.3
+//   32 items,  4 rows  10.6 / 13.0    11.6 / 13.9    17.0 / 18.2    24.2 / 24.3
 //             16 rows  17.3 / 20.4    20.2 / 22.9    27.4 / 27.9    33.6 / 36.4
+// As many as leave each more than 2 blocks of a tile, beside the incomplete one's
+// up to eight turns (1000 tokens, 4 rows: 9.8 us, with 10 blocks to a CTA 11.4), of
+// lists more than 10; six blocks stay together (300 tokens: 9.0 us, shared 9.7).
 int k8_clog(const csa_shape* s, int T, int n_sel) {
-  const int64_t items = k8_items(s, T, n_sel), work = k8_blocks(s, n_sel) * ((k8_rows_of(s, T, n_sel) + 7) / 8);
+  const int tiles = (k8_rows_of(s, T, n_sel) + 7) / 8, least = n_sel || 2 * tiles > kK8Warps ? kK8Warps : 2 * tiles;
+  const int64_t items = k8_items(s, T, n_sel), work = k8_blocks(s, n_sel) * tiles;
   int clog = 0;
-  while (clog < 3 && (items << (clog + 1)) <= (clog < 2 ? sm_count() : sm_count() / 2) && work > (kK8Warps << clog)) ++clog;
+  if (work <= 6) return 0;
+  while (clog < 3 && (items << (clog + 1)) <= (clog < 2 ? sm_count() : sm_count() / 2) && work > ((int64_t)least << clog)) ++clog;
   const int rounds = 2 * (items << clog) <= sm_count() ? 2 : 4;
   return work <= ((int64_t)rounds * kK8Warps << clog) ? clog : 0;
 }
