@@ -475,7 +475,7 @@ __device__ __forceinline__ float2 cluster_load2(unsigned at) {
   asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];\n" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
   return v;
 }
-// every CTA's side warps (the other warps take no part: they end)
+// all threads of the cluster that have not ended
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
@@ -581,14 +581,14 @@ __device__ __forceinline__ void k8_take(S& s, int rank, int clog) {
   s.clear = min(max(s.clear - lo, 0), s.nfast);
   if (rank) s.left = 0;
 }
-// The item's sums from its CTAs' (keep), by side warp `part` of CTA `rank`: rows
+// The item's sums from its CTAs' (keep), by warp `part` of `parts` of CTA `rank`: rows
 // rank, rank + the CTAs, ...  First a lane to a CTA, then D / 32 channels to a lane.
 template <int D, typename A>
-__device__ __forceinline__ void k8_join(const A& a, const KdSegOf<A>& s, const float* keep, int rank, int part) {
+__device__ __forceinline__ void k8_join(const A& a, const KdSegOf<A>& s, const float* keep, int rank, int part, int parts) {
   constexpr int CPL = D / 32, N = 8;
   const int lane = threadIdx.x & 31, R = kd_rows(a), n = 1 << a.clog;
   const unsigned at = smem_u32(keep);
-  for (int r = rank + part * n; r < R; r += kK8Side * n) {
+  for (int r = rank + part * n; r < R; r += parts * n) {
     float z[N][CPL];
 #pragma unroll
     for (int k = 0; k < N; ++k)
@@ -663,10 +663,33 @@ __global__ void __launch_bounds__(kK8Threads<W, MT>, 1) kv8_decode_kernel(const 
   // (Each wait is bounded: one that gives up marks the call, and the warp goes
   // on without waiting.)
   bool dead = false;
+  // An item's part of the run that begins at u, its queries (rows [r0, r1)) and what
+  // else is known of it; writer: by the warp that writes what is the item's.
+  KdSegOf<A> sg;
+  const auto fetch = [&](int64_t u, int buf, bool writer, int r0, int r1) {
+    KdItem<A>& it = items[buf];
+    sg = u == u0 ? kd_seg(a, batch, u, u1) : kd_next(a, batch, sg, u, u1);
+    const int32_t* ids = nullptr;
+    if constexpr (A::kPerToken) ids = kd_list(a, sg);
+    if (a.clog) k8_take(sg, rank, a.clog);
+    if constexpr (A::kPerToken) {
+      ids += sg.blk0;
+      if (writer)
+        for (int x = lane; x < min(sg.nfast, kKdIds); x += 32) s_ids[buf * kKdIds + x] = ids[x];
+    }
+    if (lane == 0 && writer) it.seg = sg;
+    kd_item_queries<D, E>(a, sg, it, s_q + buf * Rp * D, r0, r1);
+  };
+  // the first item's by all warps
+  if (u0 < u1) {
+    const int each = (Rp + W + kK8Side - 1) / (W + kK8Side);
+    if (w < W + kK8Side) fetch(u0, 0, w == W, min(w * each, Rp), min((w + 1) * each, Rp));
+  }
+  __syncthreads();
 
   if (w >= W) {
-    // The side warps: each item's queries and what else is known of it, ahead of
-    // the sums, which they merge while the others are at the next items.
+    // The side warps: the next items' queries and what else is known of them, ahead
+    // of the sums, which they merge while the others are at the items after.
     if constexpr (MT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kK8RegsSide));
     const int part = w - W;
     if (part >= kK8Side) return;
@@ -681,45 +704,28 @@ __global__ void __launch_bounds__(kK8Threads<W, MT>, 1) kv8_decode_kernel(const 
       if (lane == 0) *a.status = any ? 8u : 0u;
     }
     int64_t u = u0;
-    KdSegOf<A> sg;
-    const auto fetch = [&](int buf) {
+    const auto ahead = [&](int buf) {
       if (u >= u1) return;
-      KdItem<A>& it = items[buf];
-      sg = u == u0 ? kd_seg(a, batch, u, u1) : kd_next(a, batch, sg, u, u1);
-      const int32_t* ids = nullptr;
-      if constexpr (A::kPerToken) ids = kd_list(a, sg);
-      if (a.clog) k8_take(sg, rank, a.clog);
-      if constexpr (A::kPerToken) {
-        ids += sg.blk0;
-        if (part == 0)
-          for (int x = lane; x < min(sg.nfast, kKdIds); x += 32) s_ids[buf * kKdIds + x] = ids[x];
-      }
-      if (lane == 0 && part == 0) it.seg = sg;
-      kd_item_queries<D, E>(a, sg, it, s_q + buf * Rp * D, part * (Rp / kK8Side), (part + 1) * (Rp / kK8Side));
+      if (u > u0) fetch(u, buf, part == 0, part * (Rp / kK8Side), (part + 1) * (Rp / kK8Side));
       __syncwarp();
       if (lane == 0) mbar_arrive(item_full + 8 * buf);
       u += sg.step;
     };
-    for (int buf = 0; buf < kK8Items; ++buf) fetch(buf);
-    float* keep = s_q + Rp * D;                   // (with a.clog there is one item: the other places are free)
+    for (int buf = 0; buf < kK8Items; ++buf) ahead(buf);
     int64_t done = u0;
     for (int k = 0, buf = 0; done < u1; ++k) {
-      if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(sums_full, k & 1));
       const KdSegOf<A> s = items[buf].seg;
-      k8_merge<D, MT>(a, s, nteam, team * MT * 8, s_m, s_l, s_acc, keep, part * (Rp / kK8Side), (part + 1) * (Rp / kK8Side));
+      done += s.step;
+      if (done >= u1) break;                      // the last one's sums are merged by the others
+      if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(sums_full, k & 1));
+      k8_merge<D, MT>(a, s, nteam, team * MT * 8, s_m, s_l, s_acc, nullptr, part * (Rp / kK8Side), (part + 1) * (Rp / kK8Side));
       __syncwarp();
       if (lane == 0) mbar_arrive(sums_empty);
-      done += s.step;
       bar_sync(1, kK8Side * 32);                  // both have read the item
-      fetch(buf);
+      ahead(buf);
       if (++buf == kK8Items) buf = 0;
     }
     if (dead && lane == 0) atomicOr(a.status, 4u);
-    if (a.clog && u0 < u1) {
-      cluster_sync();
-      k8_join<D>(a, items[0].seg, keep, rank, part);
-      cluster_sync();                             // (its shared memory has been read)
-    }
     return;
   }
 
@@ -737,7 +743,7 @@ __global__ void __launch_bounds__(kK8Threads<W, MT>, 1) kv8_decode_kernel(const 
   int phase = 0;                                  // parity of its slots
   bool sent = false;                              // the team's first warp has sent for that block,
   float2 step = make_float2(0.0f, 0.0f);          // and its steps are known
-  int k = 0, buf = 0, turn = 0;                   // number of the item, its place, its parity there
+  int k = 0, buf = 0, turn = 0, last = 0;         // number of the item, its place, its parity there, the last one's place
 
   for (int64_t u = u0; u < u1; ++k) {
     if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(item_full + 8 * buf, turn));
@@ -848,8 +854,9 @@ __global__ void __launch_bounds__(kK8Threads<W, MT>, 1) kv8_decode_kernel(const 
     for (int t = 0; t < MT; ++t)
       k8_store<D, MT>(f[t], s_m + (w * MT + t) * 8, s_l + (w * MT + t) * 8, s_acc + (w * MT + t) * 8 * kK8Pitch<D, MT>);
     __syncwarp();
-    if (lane == 0) mbar_arrive(sums_full);        // (and the item's place may be filled again)
+    if (u_next < u1 && lane == 0) mbar_arrive(sums_full);        // (and the item's place may be filled again)
     u = u_next;
+    last = buf;
     buf = buf1;
     turn = turn1;
   }
@@ -857,6 +864,16 @@ __global__ void __launch_bounds__(kK8Threads<W, MT>, 1) kv8_decode_kernel(const 
     // copies in flight land before the CTA can end (of whichever phase)
     for (int i = 0; i < 4; ++i) mbar_wait(full + 8 * (i & 1), i >> 1);
     if (lane == 0) atomicOr(a.status, 4u);
+  }
+  if (u0 >= u1) return;
+  bar_sync(2, W * 32);
+  const KdSegOf<A> s = items[last].seg;
+  float* keep = s_q + Rp * D;                     // (with a.clog there is one item: the other places are free)
+  for (int r = 4 * w; r < R; r += 4 * W) k8_merge<D, MT>(a, s, nteam, team * MT * 8, s_m, s_l, s_acc, keep, r, r + 4);
+  if (a.clog) {
+    cluster_sync();
+    k8_join<D>(a, s, keep, rank, w, W);
+    cluster_sync();                               // (its shared memory has been read)
   }
 }
 
