@@ -9,8 +9,9 @@
 // whatever the lengths, which are read on the device; a CTA walks its run item by
 // item, its warps take the blocks in turn, each with its own running maximum and
 // sums, and merge them in shared memory.  Items that were cut are joined by a
-// second kernel.  An item is a sequence and KV head with its T * G query rows;
-// over lists, where each token has blocks of its own, a token's G rows.
+// second kernel; few small ones are shared by clusters of CTAs instead, which join
+// their sums in shared memory (k8_clog).  An item is a sequence and KV head with its
+// T * G query rows; over lists, where each token has blocks of its own, a token's G.
 //
 // A warp handles one tile of 8 rows, or two; with more the warps of a CTA form teams
 // that share the blocks.  Codes become half-precision numbers exactly (a
@@ -32,7 +33,8 @@
 // Each warp has a slot of shared memory for a block's keys and one for its values
 // (a team shares its two).  As it is done with one it sends for the next block's
 // itself, a bulk copy that completes on an mbarrier, into the next item too.  Two
-// further warps fetch the next items' queries and merge the last one's sums.
+// further warps fetch the next items' queries and merge the sums of those done with;
+// the run's first queries and last sums are all warps' work.
 //
 // What bounds it, bf16, d = 128: with one tile of rows and long contexts memory (4 x
 // 128K tokens, 32 / 8 heads: 1.07 GB in 166 us, 6.5 TB/s); with many items also an
@@ -40,8 +42,8 @@
 // 1K to 8K tokens, 64 / 8 heads: 111 us, 5.6 TB/s; 128 of 960: 56 us); with more
 // tiles the latency of the warps, whose issue slots and tensor pipe are a third
 // busy (8 sequences of up to 20000 tokens, 24 rows: 104 us, 2.1 TB/s); short ones
-// the chain of lengths, queries, a round of blocks, the merge and the join (1000
-// tokens, 32 / 8 heads: 12 us).  A warp that sends for all (218 us for 4 x 128K),
+// the chain of lengths, queries, a round of blocks and the merges (1000
+// tokens, 32 / 8 heads: 8.4 us).  A warp that sends for all (218 us for 4 x 128K),
 // three slots a warp (188) and two blocks ahead were slower.
 #include <cmath>
 
@@ -879,22 +881,24 @@ __global__ void __launch_bounds__(kK8Threads<W, MT>, 1) kv8_decode_kernel(const 
 
 namespace {
 
-// Items stay whole, and need no second kernel, where their blocks are one round of
-// a CTA's warps at most, and up to 16 blocks where there are items for a quarter of
-// the SMs.  Whole / cut, us, bf16, d = 128:
-//                     500 tokens     1000 tokens    1500 tokens    2000 tokens
-//     8 items,  8 rows  10.0 / 11.0    12.4 / 11.7    15.0 / 12.4    18.1 / 12.6
-//              24 rows  21.5 / 17.6    27.3 / 18.2    34.4 / 19.0    40.9 / 19.3
-//              64 rows  45.9 / 34.9    60.0 / 35.5    74.9 / 34.9    89.1 / 35.6
-//    32 items,  8 rows        -        13.2 / 13.2    15.8 / 13.4    19.1 / 13.9
-//              32 rows        -        33.8 / 26.2    41.8 / 27.9    49.1 / 30.8
-//    64 items,  8 rows        -        13.3 / 16.0    16.2 / 16.7    21.2 / 19.9
-//              32 rows        -        34.0 / 33.0    44.9 / 38.5    54.5 / 46.3
-//   160 items,  8 rows        -        23.4 / 25.4    27.8 / 29.1    32.7 / 31.1
-//              32 rows        -        62.3 / 59.7    78.9 / 67.8    92.9 / 73.8
-//   512 items,  8 rows        -        40.5 / 42.3    48.0 / 50.9    55.9 / 58.0
-//              32 rows        -         115 / 127      145 / 145      176 / 168
-// (160 are one more than the SMs have in a round: the worst for whole ones.)
+// How items are dealt out: whole, one CTA each; shared by clusters of CTAs; or cut
+// wherever the CTAs' equal runs end, and joined by a second kernel.  us, bf16, d = 128,
+// lengths all the same, whole / shared / cut:
+//                    300 tokens       1000             2000             4000             8000
+//    8 items,  4 rows   8 /  -  / 11   11 /  8 / 11     17 /  8 / 12     27 / 10 / 13     47 / 12 / 13
+//             20 rows  13 / 12  / 13   22 / 12 / 14     36 / 12 / 15     65 / 16 / 16    120 / 22 / 20
+//             64 rows  27 / 23  / 23   48 / 21 / 25     77 / 23 / 25    142 / 33 / 28    265 / 45 / 34
+//   32 items,  4 rows   8 /  -  / 11   12 /  9 / 13     18 / 10 / 13     29 / 15 / 17     49 / 22 / 23
+//             16 rows  15 / 13  / 17   19 / 13 / 18     27 / 17 / 20     45 / 23 / 24     74 / 28 / 33
+//   64 items,  8 rows   9 /  -  / 13   12 / 11 / 16     19 / 14 / 18     30 / 22 / 26     49 / 32 / 35
+//             32 rows  18 /  -  / 24   28 / 22 / 28     45 / 32 / 38     79 / 49 / 54    140 / 78 / 78
+//  160 items,  8 rows  13 /  -  / 17   21 /  - / 24     31 /  - / 30     51 /  - / 43     90 /  - / 64
+//  512 items,  8 rows  27 /  -  / 31   38 /  - / 43     53 /  - / 59     94 /  - / 97    173 /  - / 168
+// Lengths that differ favour cut items: whole and shared ones take as long as the
+// longest (512 items of up to 2000 tokens: 56 us, cut 52).
+//
+// Whole: where the blocks are one round of a CTA's warps at most, and up to 16
+// blocks where there are items for a quarter of the SMs.
 constexpr int64_t kK8WholeBlocks = 16;
 int64_t k8_blocks(const csa_shape* s, int n_sel) {
   const int64_t blocks = (s->n_max + kBlock - 1) / kBlock;
@@ -902,27 +906,21 @@ int64_t k8_blocks(const csa_shape* s, int n_sel) {
 }
 int64_t k8_items(const csa_shape* s, int T, int n_sel) { return (int64_t)s->B * s->Hkv * (n_sel ? T : 1); }
 int k8_rows_of(const csa_shape* s, int T, int n_sel) { return (n_sel ? 1 : T) * (s->Hq / s->Hkv); }
-// Few items of few blocks: 2, 4 or 8 CTAs to an item, which join their sums through
-// shared memory, where that makes two rounds of their warps at most, or four with
-// CTAs for more than half of the SMs.  Eight only for half of the SMs: a card full
-// of such clusters, which lie within groups of SMs, takes two rounds.  Shared /
-// cut, us, bf16, d = 128:
-//                      1000 tokens    2000 tokens    4000 tokens    8000 tokens
-//    8 items,  4 rows   9.8 / 12.0    10.5 / 12.2    11.5 / 13.9    13.8 / 14.4
-//             20 rows  16.7 / 18.0    16.9 / 19.1    21.3 / 20.4    27.4 / 23.8
-//             64 rows  34.4 / 37.0    35.4 / 36.9    45.7 / 39.9    58.6 / 47.1
-//   32 items,  4 rows  10.6 / 13.0    11.6 / 13.9    17.0 / 18.2    24.2 / 24.3
-//             16 rows  17.3 / 20.4    20.2 / 22.9    27.4 / 27.9    33.6 / 36.4
-// As many as leave each more than 2 blocks of a tile, beside the incomplete one's
-// up to eight turns (1000 tokens, 4 rows: 9.8 us, with 10 blocks to a CTA 11.4), of
-// lists more than 10; six blocks stay together (300 tokens: 9.0 us, shared 9.7).
+// Shared by 2, 4 or 8 CTAs, as the SMs allow (eight only for half of them: a card full
+// of such clusters, which lie within groups of SMs, takes two rounds).  As many as
+// leave each more than 2 blocks of a tile, beside the incomplete one's up to eight
+// turns (1000 tokens, 4 rows: 9.8 us, with 10 blocks to a CTA 11.4), of lists more
+// than 10; up to 6 blocks stay together (300 tokens: 9.0 us, shared 9.7).  And up to
+// three rounds of their warps; with CTAs for more than half of the SMs, where cutting
+// has less to gain, six, or twelve of lists, which are mostly of one length (64 items
+// of 256 blocks: 65 us, cut 70).
 int k8_clog(const csa_shape* s, int T, int n_sel) {
   const int tiles = (k8_rows_of(s, T, n_sel) + 7) / 8, least = n_sel || 2 * tiles > kK8Warps ? kK8Warps : 2 * tiles;
   const int64_t items = k8_items(s, T, n_sel), work = k8_blocks(s, n_sel) * tiles;
   int clog = 0;
   if (work <= 6) return 0;
   while (clog < 3 && (items << (clog + 1)) <= (clog < 2 ? sm_count() : sm_count() / 2) && work > ((int64_t)least << clog)) ++clog;
-  const int rounds = 2 * (items << clog) <= sm_count() ? 2 : 4;
+  const int rounds = 2 * (items << clog) <= sm_count() ? 3 : n_sel ? 12 : 6;
   return work <= ((int64_t)rounds * kK8Warps << clog) ? clog : 0;
 }
 int k8_whole(const csa_shape* s, int T, int n_sel) {

@@ -84,7 +84,7 @@ def test_decode_refusals(lib, over, want):
     (dict(n_sel=0), INVALID), (dict(n_sel=-1), INVALID), (dict(n_sel=1025), UNSUPPORTED)])
 def test_decode_blocks_refusals(lib, over, want):
     a = dict(shape=shape(), cache=cache(), T=4, q=FAKE, qs=strides(),
-             lens_dev=FAKE, n_q=None, blocks=FAKE, count=FAKE, n_sel=100, o=FAKE,
+             lens_dev=FAKE, n_q=None, blocks=FAKE, count=FAKE, n_sel=1000, o=FAKE,
              lse=None, workspace=FAKE, workspace_bytes=1 << 40, stream=0)
     a.update(over)
     assert csa.csa_kv8_decode_blocks(**a) == want
