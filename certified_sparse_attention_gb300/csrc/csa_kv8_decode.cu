@@ -574,14 +574,21 @@ __device__ __forceinline__ void k8_merge(const A& a, const KdSegOf<A>& s, int nt
 }
 
 // The share of CTA `rank` of the 2^clog that take an item together: whole blocks in
-// turn, the incomplete one with the first share, which is the smallest.
+// order, and of the incomplete one's tokens, eight at a time, those from k8_first on
+// (from the last CTA to the first, as the first shares of blocks are the smallest);
+// with up to 16 rows, of which a CTA does eight times eight tokens at once, rank 0
+// takes it all (8 items, 500 tokens, 64 rows: 16.3 us, all to one CTA 22.3; 20 rows
+// 11.0 and 12.4; but 32 items, 1000 tokens, 4 rows 9.5 and 9.1, 16 rows 14.2 and 13.4).
+__device__ __forceinline__ int k8_first(int tokens, int rank, int clog) {
+  return kK8Few * ((tokens + kK8Few - 1) / kK8Few * ((1 << clog) - 1 - rank) >> clog);
+}
 template <typename S>
-__device__ __forceinline__ void k8_take(S& s, int rank, int clog) {
+__device__ __forceinline__ void k8_take(S& s, int rank, int clog, bool spread) {
   const int lo = (int)((int64_t)s.nfast * rank >> clog), hi = (int)((int64_t)s.nfast * (rank + 1) >> clog);
   s.blk0 += lo;
   s.nfast = hi - lo;
   s.clear = min(max(s.clear - lo, 0), s.nfast);
-  if (rank) s.left = 0;
+  if (rank) s.left = spread ? min(s.left, k8_first(s.left, rank - 1, clog)) : 0;
 }
 // The item's sums from its CTAs' (keep), by warp `part` of `parts` of CTA `rank`: rows
 // rank, rank + the CTAs, ...  First a lane to a CTA, then D / 32 channels to a lane.
@@ -673,7 +680,7 @@ __global__ void __launch_bounds__(kK8Threads<W, MT>, 1) kv8_decode_kernel(const 
     sg = u == u0 ? kd_seg(a, batch, u, u1) : kd_next(a, batch, sg, u, u1);
     const int32_t* ids = nullptr;
     if constexpr (A::kPerToken) ids = kd_list(a, sg);
-    if (a.clog) k8_take(sg, rank, a.clog);
+    if (a.clog) k8_take(sg, rank, a.clog, R > 16);
     if constexpr (A::kPerToken) {
       ids += sg.blk0;
       if (writer)
@@ -762,9 +769,10 @@ __global__ void __launch_bounds__(kK8Threads<W, MT>, 1) kv8_decode_kernel(const 
     const int64_t tail0 = it.seg.n / kBlock * kBlock;
     const E* Kt = reinterpret_cast<const E*>(a.c.Kt) + it.seg.bg * kBlock * D;
     const E* Vt = reinterpret_cast<const E*>(a.c.Vt) + it.seg.bg * kBlock * D;
-    const int turns = n + (left + kK8Few - 1) / kK8Few;
+    const int first = a.clog && R > 16 ? min(k8_first((int)(it.seg.n % kBlock), rank, a.clog), left) : 0;
+    const int turns = n + (left - first + kK8Few - 1) / kK8Few;
     const int x1 = x < turns ? x + (turns - x + nteam - 1) / nteam * nteam - turns : x - turns;   // the team's first turn in the next item
-    const int few = !works ? kBlock : kK8Few * ((x < n ? x + (n - x + nteam - 1) / nteam * nteam : x) - n);
+    const int few = !works ? kBlock : first + kK8Few * ((x < n ? x + (n - x + nteam - 1) / nteam * nteam : x) - n);
     if (few < left) k8_rows_ahead<D>(Kt, Vt, few, left);
     if (x < n && !sent && !dead) {
       const int64_t at = k8_at(a, it.seg, s_ids + buf * kKdIds, x);
@@ -886,8 +894,8 @@ namespace {
 // lengths all the same, whole / shared / cut:
 //                    300 tokens       1000             2000             4000             8000
 //    8 items,  4 rows   8 /  -  / 11   11 /  8 / 11     17 /  8 / 12     27 / 10 / 13     47 / 12 / 13
-//             20 rows  13 / 12  / 13   22 / 12 / 14     36 / 12 / 15     65 / 16 / 16    120 / 22 / 20
-//             64 rows  27 / 23  / 23   48 / 21 / 25     77 / 23 / 25    142 / 33 / 28    265 / 45 / 34
+//             20 rows  13 / 11  / 13   22 / 11 / 14     36 / 13 / 15     65 / 16 / 16    120 / 22 / 20
+//             64 rows  27 / 19  / 23   48 / 20 / 25     77 / 23 / 25    142 / 33 / 28    265 / 45 / 34
 //   32 items,  4 rows   8 /  -  / 11   12 /  9 / 13     18 / 10 / 13     29 / 15 / 17     49 / 22 / 23
 //             16 rows  15 / 13  / 17   19 / 13 / 18     27 / 17 / 20     45 / 23 / 24     74 / 28 / 33
 //   64 items,  8 rows   9 /  -  / 13   12 / 11 / 16     19 / 14 / 18     30 / 22 / 26     49 / 32 / 35
@@ -912,15 +920,15 @@ int k8_rows_of(const csa_shape* s, int T, int n_sel) { return (n_sel ? 1 : T) * 
 // turns (1000 tokens, 4 rows: 9.8 us, with 10 blocks to a CTA 11.4), of lists more
 // than 10; up to 6 blocks stay together (300 tokens: 9.0 us, shared 9.7).  And up to
 // three rounds of their warps; with CTAs for more than half of the SMs, where cutting
-// has less to gain, six, or twelve of lists, which are mostly of one length (64 items
-// of 256 blocks: 65 us, cut 70).
+// has less to gain, six, or sixteen of lists, which are mostly of one length (64
+// items of 256 blocks: 65 us, cut 70).
 int k8_clog(const csa_shape* s, int T, int n_sel) {
   const int tiles = (k8_rows_of(s, T, n_sel) + 7) / 8, least = n_sel || 2 * tiles > kK8Warps ? kK8Warps : 2 * tiles;
   const int64_t items = k8_items(s, T, n_sel), work = k8_blocks(s, n_sel) * tiles;
   int clog = 0;
   if (work <= 6) return 0;
   while (clog < 3 && (items << (clog + 1)) <= (clog < 2 ? sm_count() : sm_count() / 2) && work > ((int64_t)least << clog)) ++clog;
-  const int rounds = 2 * (items << clog) <= sm_count() ? 3 : n_sel ? 12 : 6;
+  const int rounds = 2 * (items << clog) <= sm_count() ? 3 : n_sel ? 16 : 6;
   return work <= ((int64_t)rounds * kK8Warps << clog) ? clog : 0;
 }
 int k8_whole(const csa_shape* s, int T, int n_sel) {
