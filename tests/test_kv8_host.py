@@ -1,6 +1,9 @@
 """Host side of the 8-bit cache: refusals (before any launch), the layout and
 arithmetic of its codes, the choice of blocks (no GPU work)."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -259,6 +262,18 @@ def test_choice():
     assert kv8.choose(s[:3], 2, 2, 0, 1) == [0, 2]
 
 
-def test_structure_matches_the_header(lib):
-    assert ctypes.sizeof(csa.csa_kv8) == 7 * ctypes.sizeof(ctypes.c_void_p)
-    assert [f for f, _ in csa.csa_kv8._fields_] == ["K8", "V8", "scale", "span", "Kt", "Vt", "refused"]
+def test_structure_matches_the_header(lib, tmp_path):
+    # sizes and offsets as a C compiler has them
+    cc = shutil.which("cc") or shutil.which("gcc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    fields = [f for f, _ in csa.csa_kv8._fields_]
+    lines = ["#include <stdio.h>", "#include <stddef.h>", '#include "csa.h"', "int main(void) {",
+             '  printf("%zu\\n", sizeof(csa_kv8));']
+    lines += [f'  printf("%zu\\n", offsetof(csa_kv8, {f}));' for f in fields]
+    (tmp_path / "l.c").write_text("\n".join(lines + ["  return 0;", "}"]) + "\n")
+    subprocess.run([cc, "-std=c11", "-Wall", "-Werror", "-I", os.path.join(root, "include"), str(tmp_path / "l.c"), "-o",
+                    str(tmp_path / "l")], check=True)
+    got = [int(x) for x in subprocess.run([str(tmp_path / "l")], capture_output=True, text=True, check=True).stdout.split()]
+    assert got == [ctypes.sizeof(csa.csa_kv8)] + [getattr(csa.csa_kv8, f).offset for f in fields]
