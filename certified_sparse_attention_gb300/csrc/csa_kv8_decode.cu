@@ -39,7 +39,7 @@
 // What bounds it, bf16, d = 128: with one tile of rows and long contexts memory (4 x
 // 128K tokens, 32 / 8 heads: 1.07 GB in 166 us, 6.5 TB/s); with many items also an
 // item's start and end, 1.5 to 3 us of a CTA beside 0.36 us a block (64 sequences of
-// 1K to 8K tokens, 64 / 8 heads: 111 us, 5.6 TB/s; 128 of 960: 56 us); with more
+// 1K to 8K tokens, 64 / 8 heads: 115 us, 5.5 TB/s; 128 of 960: 54 us); with more
 // tiles the latency of the warps, whose issue slots and tensor pipe are a third
 // busy (8 sequences of up to 20000 tokens, 24 rows: 104 us, 2.1 TB/s); short ones
 // the chain of lengths, queries, a round of blocks and the merges (1000
