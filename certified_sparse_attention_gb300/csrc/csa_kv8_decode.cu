@@ -45,6 +45,7 @@
 // the chain of lengths, queries, a round of blocks and the merges (1000
 // tokens, 32 / 8 heads: 8.4 us).  A warp that sends for all (218 us for 4 x 128K),
 // three slots a warp (188) and two blocks ahead were slower.
+#include <algorithm>
 #include <cmath>
 
 #include "csa_decode.cuh"
@@ -1047,7 +1048,14 @@ extern "C" {
 
 size_t csa_kv8_workspace_size(const csa_shape* shape, int T, int n_sel) {
   csa_status st;
-  return n_sel >= 0 && n_sel <= CSA_KV8_MAX_SEL && k8_args_ok(shape, T, &st) ? k8_workspace(shape, T, n_sel) : 0;
+  if (n_sel < 0 || n_sel > CSA_KV8_MAX_SEL || !k8_args_ok(shape, T, &st)) return 0;
+  // Fewer tokens may need more: their lists are fewer items, which are cut where
+  // more of them share CTAs (16 sequences and KV heads, 121 blocks: one token 0.6 MB,
+  // two 256 bytes).  With fewer blocks, the tokens the same, items are never cut
+  // that were not with more.
+  size_t most = 0;
+  for (int t = 1; t <= T; ++t) most = std::max(most, k8_workspace(shape, t, n_sel));
+  return most;
 }
 
 csa_status csa_kv8_decode(const csa_shape* shape, const csa_kv8* cache, int T, const void* q, const csa_strides* qs,

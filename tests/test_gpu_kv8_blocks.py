@@ -368,3 +368,25 @@ def test_choice_at_the_longest_context():
         own = (n - T + t) // BLOCK
         score = np.append(kv8.scores(float32(q)[0, t], span[0, 0, :own], scale[0, 0, :own]), 0)
         assert got[0, t, 0].tolist() == kv8.choose(score, own, N, 1, 2) and count[0, t, 0] == N
+
+
+@pytest.mark.parametrize("T,N", [(2, 121), (4, 300), (8, 200)])
+def test_workspace_for_more_tokens_serves_fewer(T, N):
+    # lists of T tokens are shared by CTAs, of one token cut and joined from the
+    # workspace, which was sized for T
+    torch, csa, dev = _t()
+    rng = np.random.default_rng(N)
+    B, H, G, d, n = 2, 8, 1, 64, 64 * 310 + 5
+    s, cache, model = filled(rng, "bf16", d, H, [n, n - 70], n, H * G, step=8192)
+    q = rows(rng, (B, 1, H * G, d), "bf16")
+    op = csa.KV8Sparse(s, dev, N, with_lse=True)
+    op(q, cache, i64([n, n - 70]))
+    want = op.o.clone()
+    check_listed(f64(op.o), f64(op.lse), f64(q), model, [n, n - 70], [1, 1], op.blocks.cpu().numpy(), op.count.cpu().numpy())
+    size = csa.csa_kv8_workspace_size(s, T, N)
+    assert size >= csa.csa_kv8_workspace_size(s, 1, N) and size >= csa.csa_kv8_workspace_size(s, T, N - 7)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    op.o.fill_(55.0)
+    assert csa.csa_kv8_decode_blocks(s, cache.desc, 1, q, q, i64([n, n - 70]), None, op.blocks, op.count, N,
+                                     op.o, None, ws, size) == 0
+    assert csa.csa_check(ws) == 0 and torch.equal(op.o, want)

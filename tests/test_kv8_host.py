@@ -127,6 +127,23 @@ def test_workspace_size(lib):
     assert csa.csa_kv8_workspace_size(shape(Hq=16), 9) == 0
 
 
+@pytest.mark.parametrize("BH", [(1, 1), (2, 1), (4, 4), (2, 8), (3, 3), (19, 1), (8, 5), (16, 8)])
+@pytest.mark.parametrize("G,d", [(1, 64), (2, 128), (4, 128), (8, 64)])
+def test_workspace_is_enough_for_fewer_tokens_and_shorter_lists(lib, BH, G, d):
+    # what was sized for T tokens and lists of n_sel blocks also serves a call of
+    # fewer: more tokens are more items, which share CTAs where fewer are cut
+    s = csa.make_shape(BH[0], BH[1] * G, BH[1], d, 64 * 700, "bf16")
+    tokens = [t for t in range(1, 17) if t * G <= 64]
+    by_lists = {}
+    for n in [0] + list(range(1, 45)) + [60, 61, 80, 81, 120, 121, 160, 161, 240, 241, 320, 321, 480, 640, 1024]:
+        sizes = [csa.csa_kv8_workspace_size(s, t, n) for t in tokens]
+        assert min(sizes) >= 256 and sizes == sorted(sizes), n
+        if n:
+            by_lists[n] = sizes
+    for i in range(len(tokens)):
+        assert [x[i] for x in by_lists.values()] == sorted(x[i] for x in by_lists.values())
+
+
 # ------------------------------------------------------------- the binding
 
 def kv8_cache(s=None, device=0):
