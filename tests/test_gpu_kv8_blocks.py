@@ -390,3 +390,81 @@ def test_workspace_for_more_tokens_serves_fewer(T, N):
     assert csa.csa_kv8_decode_blocks(s, cache.desc, 1, q, q, i64([n, n - 70]), None, op.blocks, op.count, N,
                                      op.o, None, ws, size) == 0
     assert csa.csa_check(ws) == 0 and torch.equal(op.o, want)
+
+
+@pytest.mark.parametrize("dtype,d,B,H,G,T,n,N", [
+    ("bf16", 128, 1, 2, 4, 1, 64 * 4096 + 5, 16), ("f32", 64, 1, 1, 2, 5, 64 * 4096 + 5, 300),
+    ("bf16", 64, 2, 1, 8, 1, 64 * 5003, 1024), ("f32", 128, 1, 1, 1, 16, 64 * 4100 + 3, 7),
+    ("bf16", 128, 1, 1, 1, 1, 64 * 16384, 256), ("f32", 128, 1, 1, 4, 2, 64 * 16384 - 1, 1024),
+    ("f32", 64, 1, 2, 8, 1, 64 * 16384 + 63, 1), ("bf16", 128, 1, 1, 4, 1, 64 * 36864, 64)])
+def test_choice_by_sixteen_warps(dtype, d, B, H, G, T, n, N):
+    # contexts of 4096 blocks and more, few enough rows for half of the SMs: chunks of
+    # 256 blocks, one token's scores to a CTA; many equal scores
+    torch, csa, dev = _t()
+    rng = np.random.default_rng(n + d)
+    s = csa.make_shape(B, H * G, H, d, n, dtype)
+    nblk = -(-n // BLOCK)
+    span = rng.integers(1, 256, (B, H, nblk, 2, d)).astype(np.uint8)
+    span[:, :, nblk // 3:nblk // 2] = span[:, :, :1]
+    scale = (0.01 * 2.0 ** rng.integers(-2, 3, (B, H, nblk))).astype(np.float32)
+    scale[:, :, nblk // 3:nblk // 2] = 0.04
+    q = rows(rng, (B, T, H * G, d), dtype)
+    lens = [n - 64 * 300 * b for b in range(B)]
+    first, last = (0, 1) if N == 1 else (1, 2)
+    got, count = spans_choice(s, with_spans(s, span, scale), q, lens, N, first, last, T)
+    qn = float32(q)
+    for b in range(B):
+        for t in range(T):
+            for g in range(H):
+                own = (lens[b] - T + t) // BLOCK
+                score = np.append(kv8.scores(qn[b, t, g * G:(g + 1) * G], span[b, g, :own], scale[b, g, :own]), 0)
+                assert got[b, t, g].tolist() == kv8.choose(score, own, N, first, last), (b, t, g)
+                assert count[b, t, g] == N
+
+
+@pytest.mark.parametrize("T,n", [(1, 3 << 20), (2, (3 << 20) - 64)])
+def test_choice_at_the_longest_context_of_wide_heads(T, n):
+    # d = 128 near CSA_KV8_MAX_SELECT_TOKENS: beside the scores there is room for one
+    # chunk of 64 blocks
+    torch, csa, dev = _t()
+    d, N = 128, 20
+    s = csa.make_shape(1, 4, 1, d, 3 << 20, "bf16")
+    rng = np.random.default_rng(T)
+    nblk = (3 << 20) // BLOCK
+    span = rng.integers(1, 256, (1, 1, nblk, 2, d)).astype(np.uint8)
+    span[:, :, 1000:9000] = span[:, :, :1]
+    scale = np.full((1, 1, nblk), 0.02, np.float32)
+    q = rows(rng, (1, T, 4, d), "bf16")
+    got, count = spans_choice(s, with_spans(s, span, scale), q, [n], N, 1, 2, T)
+    for t in range(T):
+        own = (n - T + t) // BLOCK
+        score = np.append(kv8.scores(float32(q)[0, t], span[0, 0, :own], scale[0, 0, :own]), 0)
+        assert got[0, t, 0].tolist() == kv8.choose(score, own, N, 1, 2) and count[0, t, 0] == N
+
+
+@pytest.mark.parametrize("N", [320, 400])
+def test_long_runs_of_lists(N):
+    # more listed blocks of an item to one CTA than it holds numbers of: shared by two
+    # CTAs (320), and cut into runs of about 170 (400)
+    torch, csa, dev = _t()
+    rng = np.random.default_rng(N)
+    T, H, d, n = 16, 4, 64, 64 * 420 + 17
+    s, cache, model = filled(rng, "bf16", d, H, [n], n, H, step=8192)
+    q = rows(rng, (1, T, H, d), "bf16")
+    q[0, 3] *= 0.02
+    op = csa.KV8Sparse(s, dev, N, T, with_lse=True)
+    blocks = np.full((1, T, H, N), -1)
+    count = rng.integers(N - 30, N + 1, (1, T, H))
+    count[0, 0, 0], count[0, 5, 1] = N, 129
+    for t in range(T):
+        for g in range(H):
+            m = count[0, t, g]
+            own = (n - T + t) // BLOCK
+            ids = np.sort(rng.permutation(own)[:m])
+            if (t + g) % 2:
+                ids[-1] = own
+            blocks[0, t, g, :m] = ids
+    op.ws.fill_(0xFF)
+    o = op.attend(q, cache, i64([n]), None, i32(blocks), i32(count))
+    assert csa.csa_check(op.ws) == 0
+    check_listed(f64(o), f64(op.lse), f64(q), model, [n], [T], blocks, count)
