@@ -328,9 +328,32 @@ __device__ __forceinline__ void k8_rows(K8Fast<D>& f, const uint4* qa, const E* 
         if (N > 1) mma_bf16(s, a[0][N - 1], 0u, a[1][N - 1], 0u, b[0][i], b[1][i]);
       }
     }
-  const int t0 = 2 * tid;
-  const float sa = t0 < end ? (s4[0][0] + s4[1][0] + (s4[0][2] + s4[1][2])) * f.inv : -INFINITY;
-  const float sb = t0 + 1 < end ? (s4[0][1] + s4[1][1] + (s4[0][3] + s4[1][3])) * f.inv : -INFINITY;
+  float sa = (s4[0][0] + s4[1][0] + (s4[0][2] + s4[1][2])) * f.inv, sb = (s4[0][1] + s4[1][1] + (s4[0][3] + s4[1][3])) * f.inv;
+  // An infinite key has met zeros (the rows that are not there, the other parts) and
+  // made NaNs of its token's scores: those are taken again, channel by channel
+  if (__builtin_expect(__any_sync(0xffffffffu, odd_number(sa) || odd_number(sb)), 0)) {
+#pragma unroll 1
+    for (int t = 0; t < min(left, kK8Few); ++t) {
+      float s = 0.0f;
+#pragma unroll 1
+      for (int c = 0; c < D / 16; ++c) {
+        const uint4 q = qa[c * 32];
+        const float4 k = four_of(K + t * D + 64 * (c / 4) + 16 * tid + 4 * (c % 4));
+        const float2 x0 = __half22float2(*reinterpret_cast<const __half2*>(&q.x)), y0 = __half22float2(*reinterpret_cast<const __half2*>(&q.y));
+        const float2 x1 = __half22float2(*reinterpret_cast<const __half2*>(&q.z)), y1 = __half22float2(*reinterpret_cast<const __half2*>(&q.w));
+        s = fmaf(fmaf(y0.x, kLowUnit, x0.x) * f.inv, k.x, s);
+        s = fmaf(fmaf(y0.y, kLowUnit, x0.y) * f.inv, k.y, s);
+        s = fmaf(fmaf(y1.x, kLowUnit, x1.x) * f.inv, k.z, s);
+        s = fmaf(fmaf(y1.y, kLowUnit, x1.y) * f.inv, k.w, s);
+      }
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      if (t == 2 * tid && odd_number(sa)) sa = s;
+      if (t == 2 * tid + 1 && odd_number(sb)) sb = s;
+    }
+  }
+  if (2 * tid >= end) sa = -INFINITY;
+  if (2 * tid + 1 >= end) sb = -INFINITY;
   const K8Share sh = k8_share<D>(f, fmaxf(sa, sb));
   const float pa = ex2(sa - sh.ref), pb = ex2(sb - sh.ref);
   f.l = fmaf(pa + pb, sh.share, f.l);

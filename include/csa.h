@@ -519,7 +519,9 @@ size_t csa_kv8_workspace_size(const csa_shape* shape, int T, int n_sel);
  * Hkv <= 64) as in csa_kv4_decode.  Softmax statistics and sums in float32; a
  * query element is held to 2^-22 of itself or 2^-48 of its row's largest,
  * whichever is more, a weight to 2^-22 of itself or 2^-37 of its block's
- * largest. */
+ * largest.  An infinite key of the incomplete block gives its token a score of
+ * -infinity, a weight of 0 (a row with no other score is as one with no position
+ * to attend to), or of +infinity or NaN, which make the row NaN. */
 csa_status csa_kv8_decode(const csa_shape* shape, const csa_kv8* cache, int T,
                           const void* q, const csa_strides* qs,
                           const int64_t* len, const int64_t* n_q, float* o,

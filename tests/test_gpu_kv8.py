@@ -566,6 +566,57 @@ def test_decode_unseen_values_do_not_leak(what):
     assert not torch.isfinite(o[0, T - 1]).any()
 
 
+def keys_of_the_last_block(dtype, d, G, T, n, n_max, put, seed):
+    """Attention over n tokens of which put(q, k, v) changes rows first; o, lse, q and
+    the rows the cache stands for."""
+    torch, csa, dev = _t()
+    rng = np.random.default_rng(seed)
+    s = csa.make_shape(1, G, 1, d, n_max, dtype)
+    k, v, q = [float32(rows(rng, (1, x, h, d), dtype)) for x, h in ((n, 1), (n, 1), (T, G))]
+    put(q[0], k[0, :, 0], v[0, :, 0])
+    cache, model = csa.KV8Cache(s, dev), Model(1, 1, d)
+    k, v, q = [on_gpu(x).to(tdtype(dtype)) for x in (k, v, q)]
+    cache.append(k, v, i64([n]))
+    model.add(float32(k), float32(v), [n])
+    op = csa.KV8Decode(s, dev, T, with_lse=True)
+    o = op(q, cache, i64([n]))
+    assert csa.csa_check(op.ws) == 0
+    return f64(o)[0], f64(op.lse)[0], f64(q)[0], model.stands(0, 0)
+
+
+@pytest.mark.parametrize("G,T,n,n_max", [(4, 1, 127, 128), (1, 1, 65, 9000), (4, 1, 1, 64), (8, 2, 200, 200), (4, 5, 1003, 9000),
+                                         (8, 3, 700, 700), (8, 8, 72, 9000)])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64), ("f32", 128), ("bf16", 64)])
+def test_infinite_keys_of_the_incomplete_block(G, T, n, n_max, dtype, d):
+    # a score of -infinity is a weight of 0 (nothing is attended to where there is no
+    # other), one of +infinity or a NaN makes the row NaN, and a row that does not see
+    # the token is as it would be
+    first = n // 64 * 64
+    at = sorted({first, (first + n) // 2, n - 2, n - 1} & set(range(first, n)))
+
+    def put(q, k, v):
+        for i, p in enumerate(at):
+            k[p, 7 + i % 2] = (np.inf, -np.inf)[i % 2]
+        # most rows score the tokens -infinity, a few +infinity, one both in one token
+        q[..., 7], q[..., 8] = -np.abs(q[..., 7]) - 0.1, np.abs(q[..., 8]) + 0.1
+        q[-1, G // 2, 7] = 0.25
+        if T > 1:
+            q[0, 0, 8] = -0.5
+            q[1, 0, 7] = 0.0
+
+    o, lse, q, (k, v) = keys_of_the_last_block(dtype, d, G, T, n, n_max, put, d + T)
+    for t in range(T):
+        seen = n - T + t + 1
+        for h in range(G):
+            with np.errstate(invalid="ignore"):
+                score = k[:seen].astype(np.float64) @ q[t, h]
+            if np.isnan(score).any() or (score == np.inf).any():
+                assert np.isnan(o[t, h]).all() and np.isnan(lse[t, h])
+            else:
+                there = score > -np.inf
+                check_row(o[t, h], lse[t, h], q[t, h], k[:seen][there], v[:seen][there], (t, h))
+
+
 def test_drafts_over_the_end_of_a_block_do_not_leak():
     # eight drafted tokens fill a block's end, eight more begin the next: those
     # of NaN keys and infinite values do not reach the ones before
