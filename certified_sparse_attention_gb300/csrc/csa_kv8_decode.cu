@@ -286,7 +286,8 @@ __device__ __forceinline__ float2 pair_of(const float* p) { return *reinterpret_
 // four channels
 __device__ __forceinline__ float4 four_of(const __nv_bfloat16* p) { return Elem<__nv_bfloat16>::get4(p); }
 __device__ __forceinline__ float4 four_of(const float* p) { return Elem<float>::get4(p); }
-__device__ __forceinline__ bool odd_number(float x) { return !(fabsf(x) < INFINITY); }
+// infinities, NaNs and float32 numbers that bf16 rounds to infinity
+__device__ __forceinline__ bool odd_number(float x) { return !(fabsf(x) < 0x1.FFp127f); }
 
 // Eight tokens of the incomplete block at K, V, `left` of them there, of which the
 // lane's row sees those below end; on the tensor cores too.  Keys and queries are
@@ -329,8 +330,9 @@ __device__ __forceinline__ void k8_rows(K8Fast<D>& f, const uint4* qa, const E* 
       }
     }
   float sa = (s4[0][0] + s4[1][0] + (s4[0][2] + s4[1][2])) * f.inv, sb = (s4[0][1] + s4[1][1] + (s4[0][3] + s4[1][3])) * f.inv;
-  // An infinite key has met zeros (the rows that are not there, the other parts) and
-  // made NaNs of its token's scores: those are taken again, channel by channel
+  // An infinite key (or one that bf16 rounds to infinity) has met zeros, the rows that
+  // are not there or other parts, and made NaNs of its token's scores: those are taken
+  // again, channel by channel
   if (__builtin_expect(__any_sync(0xffffffffu, odd_number(sa) || odd_number(sb)), 0)) {
 #pragma unroll 1
     for (int t = 0; t < min(left, kK8Few); ++t) {
@@ -363,7 +365,7 @@ __device__ __forceinline__ void k8_rows(K8Fast<D>& f, const uint4* qa, const E* 
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) {
     const float2 v = pair_of(reinterpret_cast<const E*>(&vraw[i]));
-    // (infinities and NaNs are left to the loop below)
+    // (what is no number of bf16 parts is left to the loop below)
     const bool ox = odd_number(v.x), oy = odd_number(v.y);
     odd = odd || ox || oy;
     unsigned b[N];

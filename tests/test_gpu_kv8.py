@@ -617,6 +617,27 @@ def test_infinite_keys_of_the_incomplete_block(G, T, n, n_max, dtype, d):
                 check_row(o[t, h], lse[t, h], q[t, h], k[:seen][there], v[:seen][there], (t, h))
 
 
+@pytest.mark.parametrize("G,T,d", [(2, 4, 64), (8, 3, 128), (8, 8, 64), (4, 4, 128)])
+@pytest.mark.parametrize("n,n_max", [(200, 200), (1001, 9000)])
+def test_largest_numbers_of_the_incomplete_block(G, T, d, n, n_max):
+    # float32 values that bf16 rounds to infinity, and a key of that size where the
+    # query is 0: rows that do not see them are as they would be, and so is the weight
+    # of the others
+    top = np.finfo(np.float32).max
+
+    def put(q, k, v):
+        k[n - 3, 11], q[..., 11] = top, 0.0
+        k[n - 2:] = 0.0
+        v[n - 2, 9], v[n - 1, 5], v[n - 1, d - 1] = np.float32(2.0 ** 127 * (2 - 2.0 ** -8)), -top, top
+
+    o, lse, q, (k, v) = keys_of_the_last_block("f32", d, G, T, n, n_max, put, d + T)
+    for t in range(T):
+        seen = n - T + t + 1
+        for h in range(G):
+            assert np.isfinite(o[t, h]).all()
+            check_row(o[t, h], lse[t, h], q[t, h], k[:seen], v[:seen], (t, h))
+
+
 def test_drafts_over_the_end_of_a_block_do_not_leak():
     # eight drafted tokens fill a block's end, eight more begin the next: those
     # of NaN keys and infinite values do not reach the ones before
