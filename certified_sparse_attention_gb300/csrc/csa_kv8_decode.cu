@@ -289,13 +289,42 @@ __device__ __forceinline__ float4 four_of(const float* p) { return Elem<float>::
 // infinities, NaNs and float32 numbers that bf16 rounds to infinity
 __device__ __forceinline__ bool odd_number(float x) { return !(fabsf(x) < 0x1.FFp127f); }
 
+constexpr int kK8Few = 8;         // tokens of the incomplete block at a time
+// Scores of up to eight tokens at K, channel by channel: the lane's row with tokens
+// 2 tid, 2 tid + 1.  (Not inline: its registers would cost float32 drafts of 20 rows 1.0
+// of 68 us, the call costs 0.4.)
+template <int D, typename E>
+__device__ __noinline__ float2 k8_scores(const uint4* qa, const E* K, int tokens, float inv) {
+  const int tid = threadIdx.x & 3;
+  float2 out = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+  for (int t = 0; t < tokens; ++t) {
+    float s = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < D / 16; ++c) {
+      const uint4 q = qa[c * 32];
+      const float4 k = four_of(K + t * D + 64 * (c / 4) + 16 * tid + 4 * (c % 4));
+      const float2 x0 = __half22float2(*reinterpret_cast<const __half2*>(&q.x)), y0 = __half22float2(*reinterpret_cast<const __half2*>(&q.y));
+      const float2 x1 = __half22float2(*reinterpret_cast<const __half2*>(&q.z)), y1 = __half22float2(*reinterpret_cast<const __half2*>(&q.w));
+      s = fmaf(fmaf(y0.x, kLowUnit, x0.x) * inv, k.x, s);
+      s = fmaf(fmaf(y0.y, kLowUnit, x0.y) * inv, k.y, s);
+      s = fmaf(fmaf(y1.x, kLowUnit, x1.x) * inv, k.z, s);
+      s = fmaf(fmaf(y1.y, kLowUnit, x1.y) * inv, k.w, s);
+    }
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    if (t == 2 * tid) out.x = s;
+    if (t == 2 * tid + 1) out.y = s;
+  }
+  return out;
+}
+
 // Eight tokens of the incomplete block at K, V, `left` of them there, of which the
 // lane's row sees those below end; on the tensor cores too.  Keys and queries are
 // split into bf16 parts (a bf16 number is one; float32 ones are three, whose
 // products are all summed), weights into three: the instruction's 16 rows are
 // the high and middle parts, and the low ones stand in its second eight tokens,
 // which are the first ones again.
-constexpr int kK8Few = 8;
 template <int D, typename E>
 __device__ __forceinline__ void k8_rows(K8Fast<D>& f, const uint4* qa, const E* K, const E* V, int left, int end) {
   constexpr int N = sizeof(E) == 2 ? 1 : 3;
@@ -334,25 +363,9 @@ __device__ __forceinline__ void k8_rows(K8Fast<D>& f, const uint4* qa, const E* 
   // are not there or other parts, and made NaNs of its token's scores: those are taken
   // again, channel by channel
   if (__builtin_expect(__any_sync(0xffffffffu, odd_number(sa) || odd_number(sb)), 0)) {
-#pragma unroll 1
-    for (int t = 0; t < min(left, kK8Few); ++t) {
-      float s = 0.0f;
-#pragma unroll 1
-      for (int c = 0; c < D / 16; ++c) {
-        const uint4 q = qa[c * 32];
-        const float4 k = four_of(K + t * D + 64 * (c / 4) + 16 * tid + 4 * (c % 4));
-        const float2 x0 = __half22float2(*reinterpret_cast<const __half2*>(&q.x)), y0 = __half22float2(*reinterpret_cast<const __half2*>(&q.y));
-        const float2 x1 = __half22float2(*reinterpret_cast<const __half2*>(&q.z)), y1 = __half22float2(*reinterpret_cast<const __half2*>(&q.w));
-        s = fmaf(fmaf(y0.x, kLowUnit, x0.x) * f.inv, k.x, s);
-        s = fmaf(fmaf(y0.y, kLowUnit, x0.y) * f.inv, k.y, s);
-        s = fmaf(fmaf(y1.x, kLowUnit, x1.x) * f.inv, k.z, s);
-        s = fmaf(fmaf(y1.y, kLowUnit, x1.y) * f.inv, k.w, s);
-      }
-      s += __shfl_xor_sync(0xffffffffu, s, 1);
-      s += __shfl_xor_sync(0xffffffffu, s, 2);
-      if (t == 2 * tid && odd_number(sa)) sa = s;
-      if (t == 2 * tid + 1 && odd_number(sb)) sb = s;
-    }
+    const float2 s = k8_scores<D, E>(qa, K, min(left, kK8Few), f.inv);
+    if (odd_number(sa)) sa = s.x;
+    if (odd_number(sb)) sb = s.y;
   }
   if (2 * tid >= end) sa = -INFINITY;
   if (2 * tid + 1 >= end) sb = -INFINITY;
