@@ -16,8 +16,8 @@
 //                                 sqrt(d) goes into what undoes a row's scale
 //   put<D>(q, r, lane, x, up)     lays channels lane D / 32 ... of query row r,
 //                                 x up, down in shared memory
-//   top<D>(c)                     what the kernel wants to know of the channel c
-//                                 of a row's largest query element
+//   kTop, top<D>(c)               whether the kernel wants to know of the channel c
+//                                 of a row's largest query element, and what
 #pragma once
 
 #include <type_traits>
@@ -292,12 +292,17 @@ __device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(
 // (kPlainQ: q) times a power of two that puts the row's largest at 2^11 .. 2^12
 // (undone by inv), laid out by A::put.
 template <typename A>
-struct KdItem {
+struct KdPlainItem {
   KdSegOf<A> seg;
   int64_t end[CSA_KV4_MAX_ROWS];    // row r sees positions below end[r]
   float inv[CSA_KV4_MAX_ROWS];      // undoes the scale of row r
+};
+template <typename A>
+struct KdTopItem : KdPlainItem<A> {
   int top[CSA_KV4_MAX_ROWS];        // of the channel of the largest of row r: A::top
 };
+template <typename A>
+using KdItem = std::conditional_t<A::kTop, KdTopItem<A>, KdPlainItem<A>>;
 
 // the rows [r0, r1) of an item, but for it.seg
 template <int D, typename E, typename A>
@@ -322,12 +327,12 @@ __device__ __forceinline__ void kd_item_queries(const A& a, const KdSegOf<A>& sg
         x[0] = v.x; x[1] = v.y;
       }
     }
-    // the row's largest in magnitude, without its last 7 bits, and its channel
+    // the row's largest in magnitude, without its last 7 bits, and (kTop) its channel
     unsigned key = 0;
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
       if constexpr (!A::kPlainQ) x[c] *= a.rs;
-      key = max(key, (__float_as_uint(x[c]) & 0x7fffff80u) + lane * CPL + c);
+      key = max(key, (__float_as_uint(x[c]) & 0x7fffff80u) + (A::kTop ? lane * CPL + c : 0));
     }
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, m));
@@ -336,8 +341,7 @@ __device__ __forceinline__ void kd_item_queries(const A& a, const KdSegOf<A>& sg
     const float up = pow2i(e);
     A::template put<D>(q, r, lane, x, up);
     if (lane == 0) {
-      const int c = key & 127;
-      it.top[r] = A::template top<D>(c);
+      if constexpr (A::kTop) it.top[r] = A::template top<D>((int)(key & 127));
       it.inv[r] = A::kPlainQ ? a.rs * pow2i(-e) : pow2i(-e);
       it.end[r] = t < sg.nq ? sg.n - sg.nq + t + 1 : 0;
     }

@@ -106,7 +106,7 @@ struct Kv4DecodeArgs : DecodeArgs {
   // item's own cost, have the same weights and would want a smaller lead.  An item
   // whose sequence has no query token (n_q = 0) is walked like any other.
   static constexpr int kLead = 16, kTailBase = 6, kTailStep = 4;
-  static constexpr bool kPerToken = false, kPlainQ = false;
+  static constexpr bool kPerToken = false, kPlainQ = false, kTop = true;
   static constexpr int kMaxCtas = 256;     // one per SM
   template <int D>
   static __device__ __forceinline__ void put(float* q, int r, int lane, const float (&x)[D / 32], float up) {

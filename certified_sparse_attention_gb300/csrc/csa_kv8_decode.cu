@@ -80,7 +80,7 @@ struct Kv8DecodeArgs : DecodeArgs {
   // and of 12 take the same time there; 128 sequences of up to 2000 tokens take 101,
   // 94 and 92 us with 5, 8 and 12, one CTA's worth of drafts 115, 116 and 118.
   static constexpr int kLead = 8, kTailBase = 4, kTailStep = 64;
-  static constexpr bool kPerToken = LIST, kPlainQ = true;
+  static constexpr bool kPerToken = LIST, kPlainQ = true, kTop = false;
   static constexpr int kMaxCtas = 256;     // one per SM
   // Query rows as the matrix instructions' operand: of each tile of 8 rows, the
   // channels 64 h + 16 tid + 4 s + (0..3) of row gid are 16 bytes, (h, s, lane) in
@@ -96,8 +96,6 @@ struct Kv8DecodeArgs : DecodeArgs {
       *reinterpret_cast<uint2*>(at + i) = make_uint2(hi, lo);
     }
   }
-  template <int D>
-  static __device__ __forceinline__ int top(int c) { return c; }
 };
 
 // ------------------------------------------------------ tensor-core blocks
