@@ -43,7 +43,7 @@
 // tiles the latency of the warps, whose issue slots and tensor pipe are a third
 // busy (8 sequences of up to 20000 tokens, 24 rows: 104 us, 2.1 TB/s); short ones
 // the chain of lengths, queries, a round of blocks and the merges (1000
-// tokens, 32 / 8 heads: 8.4 us).  A warp that sends for all (218 us for 4 x 128K),
+// tokens, 32 / 8 heads: 8.2 us).  A warp that sends for all (218 us for 4 x 128K),
 // three slots a warp (188) and two blocks ahead were slower.
 #include <algorithm>
 #include <cmath>
@@ -930,15 +930,15 @@ namespace {
 // wherever the CTAs' equal runs end, and joined by a second kernel.  us, bf16, d = 128,
 // lengths all the same, whole / shared / cut:
 //                    300 tokens       1000             2000             4000             8000
-//    8 items,  4 rows   8 /  -  / 11   11 /  8 / 11     17 /  8 / 12     27 / 10 / 13     47 / 12 / 13
-//             20 rows  13 / 11  / 13   22 / 11 / 14     36 / 13 / 15     65 / 16 / 16    120 / 22 / 20
-//             64 rows  27 / 19  / 23   48 / 20 / 25     77 / 23 / 25    142 / 33 / 28    265 / 45 / 34
-//   32 items,  4 rows   8 /  -  / 11   12 /  9 / 13     18 / 10 / 13     29 / 15 / 17     49 / 22 / 23
-//             16 rows  15 / 13  / 17   19 / 13 / 18     27 / 17 / 20     45 / 23 / 24     74 / 28 / 33
-//   64 items,  8 rows   9 /  -  / 13   12 / 11 / 16     19 / 14 / 18     30 / 22 / 26     49 / 32 / 35
-//             32 rows  18 /  -  / 24   28 / 22 / 28     45 / 32 / 38     79 / 49 / 54    140 / 78 / 78
-//  160 items,  8 rows  13 /  -  / 17   21 /  - / 24     31 /  - / 30     51 /  - / 43     90 /  - / 64
-//  512 items,  8 rows  27 /  -  / 31   38 /  - / 43     53 /  - / 59     94 /  - / 97    173 /  - / 168
+//    8 items,  4 rows   8 /  -  / 10   11 /  8 / 11     17 /  8 / 11     27 / 10 / 13     46 / 12 / 13
+//             20 rows  13 / 10  / 13   22 / 11 / 14     36 / 12 / 15     64 / 16 / 16    119 / 22 / 20
+//             64 rows  27 / 19  / 23   48 / 20 / 25     77 / 23 / 25    141 / 31 / 28    263 / 45 / 34
+//   32 items,  4 rows   8 /  -  / 11   12 /  9 / 13     17 / 10 / 13     28 / 13 / 16     48 / 19 / 19
+//             16 rows  15 / 13  / 16   19 / 13 / 18     27 / 16 / 20     43 / 20 / 22     72 / 25 / 28
+//   64 items,  8 rows   8 /  -  / 13   12 / 11 / 16     18 / 13 / 17     28 / 19 / 22     49 / 31 / 34
+//             32 rows  18 / 17  / 23   28 / 21 / 28     43 / 30 / 36     76 / 46 / 48    140 / 79 / 78
+//  160 items,  8 rows  13 /  -  / 16   19 /  - / 20     29 /  - / 25     51 /  - / 42     90 /  - / 64
+//  512 items,  8 rows  23 /  -  / 28   38 /  - / 43     54 /  - / 58     94 /  - / 96    173 /  - / 168
 // Lengths that differ favour cut items: whole and shared ones take as long as the
 // longest (512 items of up to 2000 tokens: 56 us, cut 52).
 //
@@ -952,10 +952,11 @@ int64_t k8_blocks(const csa_shape* s, int n_sel) {
 int64_t k8_items(const csa_shape* s, int T, int n_sel) { return (int64_t)s->B * s->Hkv * (n_sel ? T : 1); }
 int k8_rows_of(const csa_shape* s, int T, int n_sel) { return (n_sel ? 1 : T) * (s->Hq / s->Hkv); }
 // Shared by 2, 4 or 8 CTAs, as the SMs allow (eight only for half of them: a card full
-// of such clusters, which lie within groups of SMs, takes two rounds).  As many as
-// leave each more than 2 blocks of a tile, beside the incomplete one's up to eight
-// turns (1000 tokens, 4 rows: 9.8 us, with 10 blocks to a CTA 11.4), of lists more
-// than 10; up to 6 blocks stay together (300 tokens: 9.0 us, shared 9.7).  And up to
+// of such clusters, which lie within groups of SMs, takes two rounds).  They are doubled
+// while each still has more than 2 blocks of a tile, beside the incomplete one's up to
+// eight turns, of lists more than 10: each is left with more than 1, of lists 5 (1000
+// tokens, 4 rows: 8.2 us, doubled only from 10 blocks 9.9); up to 6 blocks stay
+// together (300 tokens: 7.7 us, shared 8.1).  And up to
 // three rounds of their warps; with CTAs for more than half of the SMs, where cutting
 // has less to gain, six, or sixteen of lists, which are mostly of one length (64
 // items of 256 blocks: 65 us, cut 70).
