@@ -521,7 +521,11 @@ size_t csa_kv8_workspace_size(const csa_shape* shape, int T, int n_sel);
  * whichever is more, a weight to 2^-22 of itself or 2^-37 of its block's
  * largest.  An infinite key of the incomplete block gives its token a score of
  * -infinity, a weight of 0 (a row with no other score is as one with no position
- * to attend to), or of +infinity or NaN, which make the row NaN. */
+ * to attend to), or of +infinity or NaN, which make the row NaN.
+ * How the work is shared out, here, in csa_kv8_select and in
+ * csa_kv8_decode_blocks, follows the sizes of the call (n_max, T, n_sel), not the
+ * lengths: short contexts are quickest in a cache with little room to spare.
+ * Over all of the cache, a sequence with n_q = 0 takes its time all the same. */
 csa_status csa_kv8_decode(const csa_shape* shape, const csa_kv8* cache, int T,
                           const void* q, const csa_strides* qs,
                           const int64_t* len, const int64_t* n_q, float* o,
